@@ -22,7 +22,10 @@
  * Around the step: the cache append of the new tokens (with INT8
  * quantise-on-write), fp32 RMSNorm + rotary embedding, both in one launch
  * (dsa_rope_append), and _paged forms of the calls for caches kept in a pool
- * of token blocks with a block table.
+ * of token blocks with a block table. Beside it, for a server built on the
+ * library: full attention of new tokens over the cache (dsa_full_attn), the
+ * life of the blocks (dsa_pages_update, dsa_pages_compact) and the selection
+ * of beam search (dsa_beam_select).
  *
  * Conventions (all calls):
  *  - Positions: a sequence's cache holds T_b = total_len[b] rows and its
@@ -469,11 +472,223 @@ int dsa_cache_append_paged(const dsa_problem* p, const dsa_kv_pages* pages, cons
                            float* k_scale, float* v_scale, void* stream);
 
 /*
+ * dsa_full_attn -- attention of every sequence's new tokens over ALL of its
+ * cached keys (no selection), for the layers beside the sparse ones and for
+ * contexts no longer than top_k. One call takes any mix of sequences: one new
+ * token (decode), a few (speculation), thousands (a prefill chunk), none.
+ *
+ * Query i of sequence b (0 <= i < q_len[b]) sits at position
+ * P = total_len[b] - q_len[b] + i and sees the keys t with
+ *     max(first_key[b], window > 0 ? P - window + 1 : 0) <= t <= P.
+ * For query head h (KV head h / (Hq / Hkv)):
+ *     z_t = scale * q.K_t;  softcap > 0: z_t = softcap * tanh(z_t / softcap);
+ *     slopes: z_t += slopes[h] * (t - P)
+ *     out = sum_t softmax(z)_t V_t;   lse = log(sum_t exp(z_t))
+ * A query that sees no key gets out = 0 and lse = -infinity.
+ *
+ * The queries are packed: sequence b's rows follow those of the sequences
+ * before it, N = sum q_len rows in all (equal q_len = S: the [B, S, Hq, 128]
+ * of the other calls). Rows of q, out and lse behind the N-th are not touched.
+ *
+ *   batch            1 .. DSA_MAX_BATCH
+ *   num_q_heads, num_kv_heads   Hq % Hkv == 0
+ *   head_dim         must be 128
+ *   cache_capacity   rows allocated per sequence (paged: blocks_per_seq *
+ *                    block_size)
+ *   window           0 (none) or the number of keys a query sees at most
+ *   q_len[b]         >= 0; total_len[b]  q_len[b] .. cache_capacity, the new
+ *                    tokens included (at most DSA_MAX_CONTEXT)
+ *   first_key[b]     0 .. total_len[b]: first key that may be read
+ *   softmax_scale    0 selects 1/sqrt(head_dim)
+ *   softcap          0: none; finite, >= 0
+ *   q_dtype          DSA_BF16 or DSA_FP16
+ *   kv_dtype         DSA_BF16 (BF16 queries only), DSA_FP16 or DSA_INT8
+ *   out_dtype        DSA_BF16, DSA_FP16 or DSA_FP32
+ *
+ *   q        [N, Hq, 128] q_dtype, 16-byte aligned
+ *   k, v     [B, cap, Hkv, 128] kv_dtype, 16-byte aligned; the rows that some
+ *            query sees must be finite, whatever the others hold
+ *   k_scale, v_scale  [B, cap, Hkv] fp32, required iff kv_dtype == DSA_INT8
+ *   slopes   [Hq] fp32 or NULL
+ *   out      [N, Hq, 128] out_dtype, 16-byte aligned
+ *   lse      [N, Hq] fp32 or NULL
+ *
+ * Arithmetic: logits, softmax statistics and sums in fp32; the weights enter
+ * the second product in 16 bits. The workspace is read and written as
+ * described at the top; the call takes its size from
+ * dsa_full_attn_workspace_size (0 and a message if `p` is invalid).
+ * N = 0 launches nothing. The pages have no counterpart of this call.
+ */
+typedef struct dsa_full_problem {
+  int32_t batch;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t cache_capacity;
+  int32_t window;
+  int32_t q_len[DSA_MAX_BATCH];
+  int32_t total_len[DSA_MAX_BATCH];
+  int32_t first_key[DSA_MAX_BATCH];
+  float softmax_scale;
+  float softcap;
+  int32_t q_dtype;
+  int32_t kv_dtype;
+  int32_t out_dtype;
+} dsa_full_problem;
+
+size_t dsa_full_attn_workspace_size(const dsa_full_problem* p);
+
+int dsa_full_attn(const dsa_full_problem* p, const void* q, const void* k, const void* v,
+                  const float* k_scale, const float* v_scale, const float* slopes, void* out,
+                  float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* dsa_full_attn on paged K / V / scale pools (dsa_kv_pages above). Blocks that
+ * hold no key between the first that some query sees and total_len[b] are
+ * never read: their table entries may be anything. */
+int dsa_full_attn_paged(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* q,
+                        const void* k, const void* v, const float* k_scale, const float* v_scale,
+                        const float* slopes, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * Page management: who holds which block of a paged pool. The state is a
+ * block table [rows, blocks_per_seq] (entry -1: no block) and a reference
+ * count per block, both on the device; a block is free when its count is 0.
+ * Every table entry counts once; a caller that holds blocks elsewhere (a
+ * prefix cache) adds its own counts.
+ *
+ *   block_size       as for dsa_kv_pages
+ *   num_blocks       blocks of the pool, 1 .. 2^24
+ *   rows             rows of the table, 1 .. 4096
+ *   blocks_per_seq   columns (rows * blocks_per_seq <= 2^26)
+ *   block_table, refs   DEVICE int32, 4-byte aligned
+ *
+ * A pool is one array whose blocks are moved when a block is: block x starts
+ * at base + x * block_bytes (kI, K, V and the INT8 scales of every layer are
+ * one pool each). base and block_bytes are multiples of 16.
+ */
+#define DSA_MAX_POOLS 256
+typedef struct dsa_page_state {
+  int32_t block_size;
+  int32_t num_blocks;
+  int32_t rows;
+  int32_t blocks_per_seq;
+  const int32_t* block_table;
+  const int32_t* refs;
+} dsa_page_state;
+
+typedef struct dsa_page_pool {
+  void* base;
+  int64_t block_bytes;
+} dsa_page_pool;
+
+size_t dsa_pages_workspace_size(const dsa_page_state* st);
+
+/*
+ * dsa_pages_update -- one step of the table's life: rows follow other rows
+ * (fork, the reordering of beam search), end, are cut back, and grow. Row r of
+ * the new table starts as the blocks of row parent[r] of the old one that hold
+ * its first keep_len[r] tokens and grows to hold new_len[r]:
+ *   - parent[r] = -1 (keep_len[r] must be 0) starts an empty row; blocks that
+ *     no row holds any more become free;
+ *   - a row that will write (new_len > keep_len) into a partly filled last
+ *     block gets a copy of it, in every pool, if anyone else holds the block;
+ *     if all its holders will write into it, the lowest row keeps it;
+ *   - new blocks are the free ones of lowest index, handed to the rows in
+ *     order (the copy first, then the new blocks); entries behind new_len are -1;
+ *   - first_key[r] > 0 drops (-1) the blocks that lie wholly below it.
+ *
+ *   parent, keep_len, new_len   DEVICE [rows] int32, -1 <= parent < rows,
+ *               0 <= keep_len <= new_len <= blocks_per_seq * block_size
+ *   first_key   DEVICE [rows] int32 (0 .. keep_len) or NULL
+ *   num_pools, pools   HOST array of 0 .. DSA_MAX_POOLS pools
+ *   table_out, refs_out  the new state: the arrays of `st` themselves (in
+ *               place) or arrays that do not overlap them
+ *   counts      DEVICE [2] int32 or NULL: blocks copied, blocks free afterwards
+ *
+ * All or nothing: when the pool has too few free blocks (status bit 3) or an
+ * argument or table entry is out of range (bit 4), the new state is the old
+ * one, nothing is copied and counts = {-1, blocks free before}; read it with
+ * dsa_read_device_status (DSA_ERR_WORKSPACE for bit 3, DSA_ERR_INVALID_ARG for
+ * bit 4). Results do not depend on the order of execution.
+ */
+int dsa_pages_update(const dsa_page_state* st, const int32_t* parent, const int32_t* keep_len,
+                     const int32_t* new_len, const int32_t* first_key, int num_pools,
+                     const dsa_page_pool* pools, int32_t* table_out, int32_t* refs_out,
+                     int32_t* counts, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dsa_pages_compact -- move the live blocks to the front of the pools: with L
+ * blocks in use, the used blocks L and above take the free places below L,
+ * both in ascending order; every other block stays. Table entries and counts
+ * follow.
+ *   remap   DEVICE [num_blocks] int32 or NULL: the new index of every used
+ *           block (-1: free), for references kept outside the table
+ *   counts  DEVICE [2] int32 or NULL: blocks moved, blocks free
+ * Entries that are out of range or name a free block set status bit 4 and
+ * leave everything as it was (counts = {-1, blocks free}).
+ */
+int dsa_pages_compact(const dsa_page_state* st, int num_pools, const dsa_page_pool* pools,
+                      int32_t* table_out, int32_t* refs_out, int32_t* remap, int32_t* counts,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * dsa_beam_select -- the selection of beam search: for every batch entry the
+ * `select` best continuations of its beams,
+ *     total(i, t) = score_i + logit[i][t] - log(sum_u exp(logit[i][u])),
+ * in descending order, ties to the lower beam, then the lower token. A
+ * finished beam has one continuation, pad_token at its own score. A
+ * continuation of total -infinity (a token masked by -infinity, a beam of
+ * score -infinity) or NaN (any NaN or +infinity among the beam's logits, or as
+ * its score) is never selected; slots left over get score -infinity, token -1
+ * and parent -1.
+ *
+ *   batch       1 .. 65535
+ *   beams       1 .. 64
+ *   vocab       1 .. 2^24
+ *   select      1 .. 64 (beams, or 2 * beams where the caller sorts out ended ones)
+ *   logits_dtype  DSA_BF16, DSA_FP16 or DSA_FP32
+ *   pad_token   0 .. vocab - 1 (used with `finished`)
+ *   row_stride  elements between two rows of logits, >= vocab (0: vocab)
+ *
+ *   logits      [batch * beams, row_stride], aligned to its elements
+ *   scores      [batch * beams] fp32
+ *   finished    [batch * beams] bytes (non-zero: finished) or NULL
+ *   out_scores  [batch, select] fp32
+ *   out_tokens  [batch, select] int32
+ *   out_parents [batch, select] int32: the row (batch entry * beams + beam)
+ *               that is continued -- what dsa_pages_update takes as `parent`
+ *
+ * Sums are taken in fp32 per thread and joined in 64 bits; totals are formed
+ * and compared in 64 bits.
+ */
+typedef struct dsa_beam_problem {
+  int32_t batch;
+  int32_t beams;
+  int32_t vocab;
+  int32_t select;
+  int32_t logits_dtype;
+  int32_t pad_token;
+  int64_t row_stride;
+} dsa_beam_problem;
+
+#define DSA_MAX_BEAMS 64
+#define DSA_MAX_SELECT 64
+
+size_t dsa_beam_workspace_size(const dsa_beam_problem* p);
+
+int dsa_beam_select(const dsa_beam_problem* p, const void* logits, const float* scores,
+                    const uint8_t* finished, float* out_scores, int32_t* out_tokens,
+                    int32_t* out_parents, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises `stream`, then copies the device status word from the
  * workspace to *status_out (0 = no device-side problem; bit 0 = a bounded
  * wait ran out; bit 1 = a gathered key's block-table entry lay outside the
- * pool). Returns DSA_ERR_TIMEOUT if bit 0 is set, else DSA_ERR_INVALID_ARG if
- * bit 1 is set.
+ * pool; bit 3 = dsa_pages_update found too few free blocks; bit 4 = a page
+ * call found an argument or table entry out of range). Returns DSA_ERR_TIMEOUT
+ * if bit 0 is set, else DSA_ERR_INVALID_ARG if bit 1 or 4 is set, else
+ * DSA_ERR_WORKSPACE if bit 3 is set.
  */
 int dsa_read_device_status(const void* workspace, size_t workspace_bytes,
                            void* stream, uint32_t* status_out);

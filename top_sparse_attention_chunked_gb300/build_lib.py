@@ -23,7 +23,7 @@ DEBUG_BUILD = os.path.join(HERE, "_build_debug")
 DEBUG_LIB = os.path.join(HERE, "libdsa_debug.so")
 SOURCES = ["dsa_api.cu", "indexer.cu", "topk.cu", "attention.cu", "prefill_attn.cu",
            "topk_noalloc.cu", "cache_append.cu", "rmsnorm_rotary.cu",
-           "rope_append.cu"]
+           "rope_append.cu", "full_attn.cu", "pages.cu", "beam.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

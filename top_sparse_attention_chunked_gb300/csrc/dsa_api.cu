@@ -174,6 +174,28 @@ int make_map_kv_rows(CUtensorMap* m, const void* base, long long rows) {
   return DSA_OK;
 }
 
+// rows tokens x heads x 128 values (16- or 8-bit): a box of 128 tokens of one
+// head, 128 bytes of each, 128-byte swizzle -- a tile of consecutive cache rows
+int make_map_kv_tiles(CUtensorMap* m, const void* base, long long rows, int heads, int elem_bytes) {
+  const int kind = elem_bytes == 2 ? 2 : 3;
+  if (map_cached(kind, base, rows, heads, m)) return DSA_OK;
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t row = static_cast<cuuint64_t>(DSA_HEAD_DIM) * elem_bytes;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(DSA_HEAD_DIM), static_cast<cuuint64_t>(heads),
+                        static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {row, row * heads};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem_bytes), 1, 128};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled (KV tiles) failed (%d)", (int)r);
+  map_remember(kind, base, rows, heads, *m);
+  return DSA_OK;
+}
+
 // ------------------------------------------------------------------ problem checks
 struct Derived {
   int rows = 0;        // B * S
@@ -840,6 +862,40 @@ int noalloc_fail(int status, const char* msg) { return fail(status, "%s", msg); 
 // Records a failure of a call implemented in another translation unit.
 int report_error(int status, const char* msg) { return fail(status, "%s", msg); }
 
+int report_errorf(int status, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  g_err = buf;
+  return status;
+}
+
+int check_call_workspace(const void* ws, size_t bytes, size_t need) {
+  Layout L;
+  L.total = need;
+  return check_ws(const_cast<void*>(ws), bytes, L);
+}
+
+int current_device(int* sms) {
+  DeviceInfo di;
+  if (int rc = device_info(&di)) return rc;
+  *sms = di.sms;
+  return DSA_OK;
+}
+
+int check_full_pages(const dsa_full_problem* p, const dsa_kv_pages* pages, Paging* pg) {
+  dsa_problem q{};   // what check_pages reads
+  q.cache_capacity = p->cache_capacity;
+  q.num_kv_heads = p->num_kv_heads;
+  return check_pages(&q, pages, pg);
+}
+
+int kv_tile_map(CUtensorMap* m, const void* base, long long rows, int heads, int elem_bytes) {
+  return make_map_kv_tiles(m, base, rows, heads, elem_bytes);
+}
+
 // Problem validation for calls that write caches (any q_len, as for prefill).
 int problem_check_for_append(const dsa_problem* p) {
   Derived d;
@@ -1089,6 +1145,9 @@ int dsa_read_device_status(const void* ws, size_t ws_bytes, void* stream, uint32
   if (v & kDevTimeout) return fail(DSA_ERR_TIMEOUT, "a kernel's bounded wait ran out");
   if (v & kDevBadPage)
     return fail(DSA_ERR_INVALID_ARG, "a gathered key's block-table entry lies outside the pool");
+  if (v & kDevBadState)
+    return fail(DSA_ERR_INVALID_ARG, "a page call found an argument or table entry out of range");
+  if (v & kDevNoPages) return fail(DSA_ERR_WORKSPACE, "the pool has too few free blocks");
   if (v & kDevBounds)
     return fail(DSA_ERR_INVALID_ARG, "a debug bounds check failed (a row outside its array)");
   return DSA_OK;

@@ -94,6 +94,8 @@ struct IndexerParams {
 };
 
 constexpr uint32_t kDevBounds = 4u;    // status bit: a debug bounds check failed
+constexpr uint32_t kDevNoPages = 8u;   // status bit: a page update found too few free blocks
+constexpr uint32_t kDevBadState = 16u; // status bit: a page call's argument or table entry out of range
 
 // Debug builds (-DDSA_DEBUG_BOUNDS) check the rows that index-driven gathers
 // compute against the extent of the array they read: a row outside it sets
@@ -248,5 +250,15 @@ struct AppendParams {
 };
 
 cudaError_t launch_cache_append(const AppendParams& p, int sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------- shared by the calls of other files
+// (defined beside the C ABI)
+int report_error(int status, const char* msg);
+int report_errorf(int status, const char* fmt, ...);
+int check_call_workspace(const void* ws, size_t bytes, size_t need);
+int current_device(int* sms);   // its SM count; an error status if it is not of this family
+int check_full_pages(const dsa_full_problem* p, const dsa_kv_pages* pages, Paging* pg);
+// tiles of 128 consecutive cache rows of one KV head (elem_bytes 2 or 1)
+int kv_tile_map(CUtensorMap* m, const void* base, long long rows, int heads, int elem_bytes);
 
 }  // namespace dsa

@@ -35,7 +35,10 @@ EXPORTED = ["dsa_workspace_size", "dsa_index_scores", "dsa_topk",
             "dsa_last_launches", "dsa_cache_append", "dsa_index_scores_paged",
             "dsa_sparse_attn_decode_paged", "dsa_sparse_attn_prefill_paged",
             "dsa_cache_append_paged", "dsa_rmsnorm_rotary", "dsa_rope_append",
-            "dsa_sparse_attn_decode_aux", "dsa_set_wait_budget"]
+            "dsa_sparse_attn_decode_aux", "dsa_set_wait_budget",
+            "dsa_full_attn", "dsa_full_attn_paged", "dsa_full_attn_workspace_size",
+            "dsa_pages_update", "dsa_pages_compact", "dsa_pages_workspace_size",
+            "dsa_beam_select", "dsa_beam_workspace_size"]
 
 _DT = {"bf16": DSA_BF16, "fp16": DSA_FP16, "int8": DSA_INT8, "fp32": DSA_FP32}
 _TORCH_DT = {DSA_BF16: torch.bfloat16, DSA_FP16: torch.float16, DSA_INT8: torch.int8,
@@ -107,6 +110,56 @@ class DsaProblem(ctypes.Structure):
     ]
 
 
+class DsaFullProblem(ctypes.Structure):
+    """dsa_full_problem (attention over all cached keys)."""
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("cache_capacity", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("q_len", ctypes.c_int32 * DSA_MAX_BATCH),
+        ("total_len", ctypes.c_int32 * DSA_MAX_BATCH),
+        ("first_key", ctypes.c_int32 * DSA_MAX_BATCH),
+        ("softmax_scale", ctypes.c_float),
+        ("softcap", ctypes.c_float),
+        ("q_dtype", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+    ]
+
+
+class DsaPageState(ctypes.Structure):
+    """dsa_page_state: a block table and the blocks' reference counts."""
+    _fields_ = [
+        ("block_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("rows", ctypes.c_int32),
+        ("blocks_per_seq", ctypes.c_int32),
+        ("block_table", ctypes.c_void_p),
+        ("refs", ctypes.c_void_p),
+    ]
+
+
+class DsaPagePool(ctypes.Structure):
+    """dsa_page_pool: an array whose blocks move with the table's."""
+    _fields_ = [("base", ctypes.c_void_p), ("block_bytes", ctypes.c_int64)]
+
+
+class DsaBeamProblem(ctypes.Structure):
+    """dsa_beam_problem (beam search's selection)."""
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("beams", ctypes.c_int32),
+        ("vocab", ctypes.c_int32),
+        ("select", ctypes.c_int32),
+        ("logits_dtype", ctypes.c_int32),
+        ("pad_token", ctypes.c_int32),
+        ("row_stride", ctypes.c_int64),
+    ]
+
+
 class DsaError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{msg} (status {status})")
@@ -130,6 +183,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
     P = ctypes.POINTER(DsaProblem)
     PG = ctypes.POINTER(DsaKvPages)
+    PF, PS = ctypes.POINTER(DsaFullProblem), ctypes.POINTER(DsaPageState)
+    PP, PB = ctypes.POINTER(DsaPagePool), ctypes.POINTER(DsaBeamProblem)
     sig = {
         "dsa_workspace_size": (sz, [P, i32]),
         "dsa_index_scores": (i32, [P, vp, vp, vp, vp, vp, sz, vp]),
@@ -153,6 +208,14 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "dsa_cache_append_paged": (i32, [P, PG] + [vp] * 9),
         "dsa_rmsnorm_rotary": (i32, [ctypes.POINTER(DsaRopeProblem)] + [vp] * 7),
         "dsa_rope_append": (i32, [P, ctypes.POINTER(DsaRopeParams)] + [vp] * 11),
+        "dsa_full_attn_workspace_size": (sz, [PF]),
+        "dsa_full_attn": (i32, [PF] + [vp] * 9 + [sz, vp]),
+        "dsa_full_attn_paged": (i32, [PF, PG] + [vp] * 9 + [sz, vp]),
+        "dsa_pages_workspace_size": (sz, [PS]),
+        "dsa_pages_update": (i32, [PS] + [vp] * 4 + [i32, PP] + [vp] * 4 + [sz, vp]),
+        "dsa_pages_compact": (i32, [PS, i32, PP] + [vp] * 5 + [sz, vp]),
+        "dsa_beam_workspace_size": (sz, [PB]),
+        "dsa_beam_select": (i32, [PB] + [vp] * 7 + [sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -461,6 +524,200 @@ def dsa_sparse_attn_prefill(p, q, qI, w, kI, k, v, k_scale, v_scale, idx_out, ou
                             stream=None, pages=None):
     _attn("dsa_sparse_attn_prefill", p, q, qI, w, kI, k, v, k_scale, v_scale, idx_out, out,
           workspace, stream, pages)
+
+
+def _here(t: Optional[torch.Tensor], name: str, dtype=None, shape=None):
+    """_ptr of a tensor that must lie on the current device (whose stream the
+    call goes to)."""
+    ptr = _ptr(t, name, dtype, shape)
+    if t is not None and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return ptr
+
+
+def _ws_here(ws: torch.Tensor):
+    return _here(ws, "workspace", torch.uint8), ws.numel()
+
+
+def make_full_attn_problem(q_len: Sequence[int], total_len: Sequence[int], num_q_heads: int,
+                           num_kv_heads: int, cache_capacity: Optional[int] = None, window: int = 0,
+                           softcap: float = 0.0, first_key: Optional[Sequence[int]] = None,
+                           q_dtype="bf16", kv_dtype="bf16", out_dtype=None,
+                           softmax_scale: float = 0.0, head_dim: int = 128) -> DsaFullProblem:
+    """Fill a DsaFullProblem: sequence b has q_len[b] new tokens (0 allowed),
+    total_len[b] tokens with them, and first readable key first_key[b] (0)."""
+    if len(q_len) != len(total_len) or (first_key is not None and len(first_key) != len(q_len)):
+        raise ValueError("q_len, total_len and first_key need one entry per sequence")
+    p = DsaFullProblem()
+    p.batch = len(q_len)
+    for b in range(min(p.batch, DSA_MAX_BATCH)):
+        p.q_len[b], p.total_len[b] = int(q_len[b]), int(total_len[b])
+        p.first_key[b] = 0 if first_key is None else int(first_key[b])
+    p.num_q_heads, p.num_kv_heads, p.head_dim = num_q_heads, num_kv_heads, head_dim
+    p.cache_capacity = cache_capacity if cache_capacity is not None else max(total_len)
+    p.window, p.softcap, p.softmax_scale = window, softcap, softmax_scale
+    p.q_dtype, p.kv_dtype = _DT[q_dtype], _DT[kv_dtype]
+    p.out_dtype = _DT[out_dtype if out_dtype is not None else q_dtype]
+    return p
+
+
+def dsa_full_attn_workspace_size(p: DsaFullProblem) -> int:
+    lib = load_library()
+    n = lib.dsa_full_attn_workspace_size(ctypes.byref(p))
+    if n == 0:
+        raise DsaError(DSA_ERR_INVALID_ARG, lib.dsa_last_error_string().decode())
+    return n
+
+
+def alloc_full_attn_workspace(p: DsaFullProblem, device="cuda") -> torch.Tensor:
+    return torch.empty(dsa_full_attn_workspace_size(p), dtype=torch.uint8, device=device)
+
+
+def dsa_full_attn(p: DsaFullProblem, q, k, v, k_scale, v_scale, out, workspace, slopes=None, lse=None,
+                  stream=None, pages=None):
+    """Attention of the packed new tokens q [N, Hq, 128] (N = sum of q_len, or
+    more: rows behind are left alone) over all cached keys; with `pages`
+    (make_pages) the caches are paged pools. lse [N, Hq] fp32 is optional."""
+    Hq, Hkv = p.num_q_heads, p.num_kv_heads
+    lib = load_library()
+    wp, wn = _ws_here(workspace)
+    kvdt = _TORCH_DT[p.kv_dtype]
+    lead = _cache_shapes(p, pages)
+    need = sum(p.q_len[:p.batch])
+    for t, name, tail in ((q, "q", (Hq, 128)), (out, "out", (Hq, 128)), (lse, "lse", (Hq,))):
+        if t is not None and (t.dim() < 1 + len(tail) or tuple(t.shape[-len(tail):]) != tail
+                              or t.numel() < need * math.prod(tail)):
+            raise ValueError(f"{name} must be [N, {', '.join(map(str, tail))}] with N >= {need}, "
+                             f"got {tuple(t.shape)}")
+    args = [_here(q, "q", _TORCH_DT[p.q_dtype]), _here(k, "k", kvdt, lead + (Hkv, 128)),
+            _here(v, "v", kvdt, lead + (Hkv, 128)), _here(k_scale, "k_scale", torch.float32, lead + (Hkv,)),
+            _here(v_scale, "v_scale", torch.float32, lead + (Hkv,)),
+            _here(slopes, "slopes", torch.float32, (Hq,)), _here(out, "out", _TORCH_DT[p.out_dtype]),
+            _here(lse, "lse", torch.float32), wp, wn, _stream(stream)]
+    if pages is None:
+        _check(lib.dsa_full_attn(ctypes.byref(p), *args))
+    else:
+        _check(lib.dsa_full_attn_paged(ctypes.byref(p), ctypes.byref(pages), *args))
+
+
+def make_page_state(block_table: torch.Tensor, refs: torch.Tensor, block_size: int) -> DsaPageState:
+    """A dsa_page_state for a device int32 block table [rows, blocks_per_seq]
+    and reference counts [num_blocks] (kept alive by the returned object)."""
+    _ptr(block_table, "block_table", torch.int32)
+    _ptr(refs, "refs", torch.int32)
+    if block_table.dim() != 2 or refs.dim() != 1:
+        raise ValueError("block_table must be [rows, blocks_per_seq] and refs [num_blocks]")
+    st = DsaPageState(block_size, refs.shape[0], block_table.shape[0], block_table.shape[1],
+                      block_table.data_ptr(), refs.data_ptr())
+    st._keep = (block_table, refs)
+    return st
+
+
+def make_page_pools(tensors: Sequence[torch.Tensor], num_blocks: int):
+    """The pools whose blocks move with the table's: contiguous tensors that
+    hold num_blocks equal blocks each (kept alive by the returned object)."""
+    arr = (DsaPagePool * max(1, len(tensors)))()
+    for i, t in enumerate(tensors):
+        n = t.numel() * t.element_size()
+        if n == 0 or t.numel() % num_blocks:
+            raise ValueError(f"pool {i} does not hold {num_blocks} equal blocks")
+        arr[i] = DsaPagePool(_ptr(t, f"pool {i}"), n // num_blocks)
+    arr._keep = tuple(tensors)
+    arr._blocks = num_blocks
+    return arr
+
+
+def dsa_pages_workspace_size(st: DsaPageState) -> int:
+    lib = load_library()
+    n = lib.dsa_pages_workspace_size(ctypes.byref(st))
+    if n == 0:
+        raise DsaError(DSA_ERR_INVALID_ARG, lib.dsa_last_error_string().decode())
+    return n
+
+
+def alloc_pages_workspace(st: DsaPageState, device="cuda") -> torch.Tensor:
+    return torch.empty(dsa_pages_workspace_size(st), dtype=torch.uint8, device=device)
+
+
+def _page_args(st: DsaPageState, pools, table_out, refs_out):
+    """Checked addresses of the new state (None: the old one's arrays) and the pools."""
+    table, refs = st._keep
+    for t, name in ((table, "block_table"), (refs, "refs")) + tuple((t, "pool") for t in (pools._keep if pools else ())):
+        _here(t, name)
+    if pools and pools._blocks != st.num_blocks:
+        raise ValueError(f"the pools hold {pools._blocks} blocks, the state {st.num_blocks}")
+    return (len(pools._keep) if pools else 0, pools if pools else None,
+            _here(table if table_out is None else table_out, "table_out", torch.int32, table.shape),
+            _here(refs if refs_out is None else refs_out, "refs_out", torch.int32, refs.shape))
+
+
+def dsa_pages_update(st: DsaPageState, parent, keep_len, new_len, pools, workspace, table_out=None,
+                     refs_out=None, first_key=None, counts=None, stream=None):
+    """Fork, reorder, end, cut back and grow the rows of a block table: row r
+    becomes the first keep_len[r] tokens of old row parent[r] (-1: empty) and
+    room for new_len[r]. Without table_out / refs_out the state is changed in
+    place; pools from make_page_pools (None: no contents move)."""
+    lib = load_library()
+    wp, wn = _ws_here(workspace)
+    n, arr, tp, rp = _page_args(st, pools, table_out, refs_out)
+    one = (st.rows,)
+    _check(lib.dsa_pages_update(
+        ctypes.byref(st), _here(parent, "parent", torch.int32, one), _here(keep_len, "keep_len", torch.int32, one),
+        _here(new_len, "new_len", torch.int32, one), _here(first_key, "first_key", torch.int32, one), n, arr,
+        tp, rp, _here(counts, "counts", torch.int32, (2,)), wp, wn, _stream(stream)))
+
+
+def dsa_pages_compact(st: DsaPageState, pools, workspace, table_out=None, refs_out=None, remap=None,
+                      counts=None, stream=None):
+    """Move the live blocks to the front of the pools (in place without
+    table_out / refs_out); remap [num_blocks] receives the new indices."""
+    lib = load_library()
+    wp, wn = _ws_here(workspace)
+    n, arr, tp, rp = _page_args(st, pools, table_out, refs_out)
+    _check(lib.dsa_pages_compact(
+        ctypes.byref(st), n, arr, tp, rp, _here(remap, "remap", torch.int32, (st.num_blocks,)),
+        _here(counts, "counts", torch.int32, (2,)), wp, wn, _stream(stream)))
+
+
+def make_beam_problem(batch: int, beams: int, vocab: int, select: int, logits_dtype="bf16",
+                      pad_token: int = 0, row_stride: int = 0) -> DsaBeamProblem:
+    return DsaBeamProblem(batch, beams, vocab, select, _DT[logits_dtype], pad_token, row_stride)
+
+
+def dsa_beam_workspace_size(p: DsaBeamProblem) -> int:
+    lib = load_library()
+    n = lib.dsa_beam_workspace_size(ctypes.byref(p))
+    if n == 0:
+        raise DsaError(DSA_ERR_INVALID_ARG, lib.dsa_last_error_string().decode())
+    return n
+
+
+def alloc_beam_workspace(p: DsaBeamProblem, device="cuda") -> torch.Tensor:
+    return torch.empty(dsa_beam_workspace_size(p), dtype=torch.uint8, device=device)
+
+
+def dsa_beam_select(p: DsaBeamProblem, logits, scores, out_scores, out_tokens, out_parents, workspace,
+                    finished=None, stream=None):
+    """The `select` best continuations of each batch entry's beams: logits
+    [batch * beams, vocab] whose rows may lie row_stride elements apart
+    (p.row_stride), scores [batch * beams]; out_* [batch, select]."""
+    lib = load_library()
+    wp, wn = _ws_here(workspace)
+    n, out = p.batch * p.beams, (p.batch, p.select)
+    stride = p.row_stride or p.vocab
+    if logits.shape != (n, p.vocab) or logits.stride(-1) != 1 or (n > 1 and logits.stride(0) != stride):
+        raise ValueError(f"logits must be [{n}, {p.vocab}] with rows {stride} elements apart, got "
+                         f"{tuple(logits.shape)} with strides {logits.stride()}")
+    if logits.dtype != _TORCH_DT[p.logits_dtype]:
+        raise ValueError(f"logits must be {_TORCH_DT[p.logits_dtype]}, got {logits.dtype}")
+    _here(logits[:1], "logits")
+    if finished is not None and finished.dtype == torch.bool:
+        finished = finished.view(torch.uint8)
+    _check(lib.dsa_beam_select(
+        ctypes.byref(p), logits.data_ptr(), _here(scores, "scores", torch.float32, (n,)),
+        _here(finished, "finished", torch.uint8, (n,)), _here(out_scores, "out_scores", torch.float32, out),
+        _here(out_tokens, "out_tokens", torch.int32, out), _here(out_parents, "out_parents", torch.int32, out),
+        wp, wn, _stream(stream)))
 
 
 def dsa_read_device_status(workspace, stream=None) -> int:
