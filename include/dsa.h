@@ -517,7 +517,7 @@ int dsa_cache_append_paged(const dsa_problem* p, const dsa_kv_pages* pages, cons
  * the second product in 16 bits. The workspace is read and written as
  * described at the top; the call takes its size from
  * dsa_full_attn_workspace_size (0 and a message if `p` is invalid).
- * N = 0 launches nothing. The pages have no counterpart of this call.
+ * N = 0 runs no kernel. The pages have no counterpart of this call.
  */
 typedef struct dsa_full_problem {
   int32_t batch;

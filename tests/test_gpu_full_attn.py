@@ -82,6 +82,10 @@ def reference(c, window=0, softcap=0.0, slopes=None, scale=None):
     n_all = sum(c["q_len"])
     out, mag = np.zeros((n_all, c["hq"], 128)), np.zeros((n_all, c["hq"], 128))
     lse, dz = np.full((n_all, c["hq"]), -np.inf), np.zeros((n_all, c["hq"]))
+    # an FP16 weight below 2^-14 is rounded to a multiple of 2^-24, off by 2^-25 at most; the weight at the
+    # maximum is taken as 2^7 or more and their sum is no less, so a key's share of the output is off by up
+    # to 2^-32 |v| beside the relative half step that `check` counts
+    tiny = 2.0 ** -32 / HALF_STEP["fp16"] if c["kvdt"] == "fp16" else 0.0
     n0 = 0
     for b, (n, t) in enumerate(zip(c["q_len"], c["total_len"])):
         k, v = (c[x][b, :t].double().numpy() for x in ("k", "v"))
@@ -112,7 +116,7 @@ def reference(c, window=0, softcap=0.0, slopes=None, scale=None):
                 p = np.exp(z - m)
                 lse[n0 + i, h] = m + math.log(p.sum())
                 p /= p.sum()
-                out[n0 + i, h], mag[n0 + i, h] = p @ vv, p @ np.abs(vv)
+                out[n0 + i, h], mag[n0 + i, h] = p @ vv, (p + tiny) @ np.abs(vv)
                 dz[n0 + i, h] = (p * err).sum() + err[p > 1e-9].max()
         n0 += n
     return out, lse, mag, dz

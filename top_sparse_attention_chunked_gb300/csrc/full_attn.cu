@@ -1,7 +1,47 @@
-// Full GQA attention of every sequence's new tokens over its cached keys.
+// Full GQA attention of every sequence's new tokens over its cached keys, on
+// tcgen05 tensor cores.
 //
-// One warp per (query token, query head): four dims a lane, one key after the
-// other, an online softmax in fp32.
+// The query rows of one KV head -- all new tokens of a sequence times the G
+// heads that share the KV head, row = token * G + head -- are cut into items of
+// up to 256 rows; the keys an item sees are cut into tiles of 128. One thread
+// block per SM walks a run of (item, tile) units of equal cost, whatever the
+// mix of sequences: where a run begins or ends inside an item, the item's
+// partial state (running maximum, sum, unnormalised output, fp32) goes to the
+// workspace and full_attn_merge_kernel joins the parts. So one token over a
+// long cache and thousands of tokens take the same path, and every SM gets the
+// same share of tiles.
+//
+// Inside a block, two slots of 128 rows alternate on the tensor core:
+//   rows mode (129 .. 256 rows): both slots take every key tile, each for its
+//     own half of the rows (a tile of K or V is loaded once for 256 rows);
+//   keys mode (up to 128 rows): the slots share the rows and take every other
+//     key tile; their two states are joined at the item's end.
+// Per slot and tile: S = Q K^T (128 x 128, fp32, in tensor memory), four warps
+// read their rows of S (one row a thread), form P = exp2(S c - m) in 16 bits
+// and put it back over S, O += P V with P read from tensor memory. While one
+// slot is in its softmax the other's two products run.
+//
+// The running maximum m is raised (and O rescaled in tensor memory) only when
+// a row's logits grow by more than 2^8 over it. P = 2^kLift exp2(S c - m): the
+// scale cancels in O / sum P, the largest weights stay below 2^15, inside
+// either 16-bit type, and FP16's smallest step (2^-24) is 2^-31 of the weight
+// at the maximum. A slot's S is only
+// complete when its previous P V is (the products run in order), so the
+// rescale needs no further synchronisation.
+//
+// K and V tiles arrive by TMA (128 consecutive cache rows of one head: a tile
+// never straddles a block of a paged cache, whose blocks hold a multiple of 128
+// tokens) in a ring of shared stages. INT8 tiles land as codes and four warps
+// widen them to 16 bits (exact); the key's scale multiplies its column of S,
+// the value's its column of P. Rows of V outside the item's keys are zeroed in
+// shared memory (a masked weight is 0, but 0 times a NaN is not); masked
+// columns of S are replaced before the maximum, whatever they hold.
+//
+// Types: the products take the cache's type (INT8: the query's for S, BF16 for
+// P V, since a value's scale may lie outside FP16's range). A BF16 query on an
+// FP16 cache is scaled by a power of two per row to at most 2^14 first, which
+// is exact for all elements within 2^-28 of the row's largest.
+#include <atomic>
 #include <cmath>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -13,6 +53,23 @@
 namespace dsa {
 namespace {
 
+constexpr int kTileKeys = 128;
+constexpr int kSlotRows = 128;
+constexpr int kItemRows = 2 * kSlotRows;
+constexpr int kMaxCtas = 192;                          // thread blocks the schedule is laid out for
+constexpr uint32_t kBlk = kTileKeys * 128;             // 64 columns of a 16-bit tile: 16 KB
+constexpr uint32_t kTile16 = 2 * kBlk;                 // 32 KB
+constexpr uint32_t kTile8 = kTileKeys * DSA_HEAD_DIM;  // 16 KB of codes
+constexpr uint32_t kTmemCols = 512;                    // S 0-127, 128-255; O 256-383, 384-511
+constexpr int kRing16 = 5, kRing8 = 3, kRaw = 3, kScaleRing = 4;
+constexpr int kThreads16 = 384, kThreads8 = 512;
+// registers per thread after the split, and what the block needs in all
+constexpr int kSoftRegs16 = 208, kMiscRegs16 = 80, kSoftRegs8 = 168, kMiscRegs8 = 72, kWidenRegs = 96;
+template <bool INT8>
+constexpr int kRegs = INT8 ? 256 * kSoftRegs8 + 128 * (kMiscRegs8 + kWidenRegs) : 256 * kSoftRegs16 + 128 * kMiscRegs16;
+constexpr float kLift = 7.0f;                          // log2 of the weight at the running maximum
+constexpr float kRaise = 8.0f;                         // log2 growth that raises the running maximum
+
 struct FullParams {
   const void* q;
   const void* k;
@@ -23,79 +80,914 @@ struct FullParams {
   void* out;
   float* lse;
   uint32_t* status;
-  int B, Hq, Hkv, cap, window;
-  int q_dtype, kv_dtype, out_dtype;
-  float scale, softcap;
+  uint32_t* errors;     // [blocks] status bits of each block, OR-ed into *status by the merge
+  float* partial;       // [2 * blocks] parts of part_rows * (128 + 2) floats
+  int part_rows;
+  int B, Hq, Hkv, G, cap, window;
+  int q_dtype, out_dtype;
+  float scale_log2, softcap;
   Paging pg;
-  int q0[DSA_MAX_BATCH + 1];     // first query row of each sequence
+  int q0[DSA_MAX_BATCH + 1];      // first query row of each sequence
+  int item0[DSA_MAX_BATCH + 1];   // first item of each sequence
   int T[DSA_MAX_BATCH], first[DSA_MAX_BATCH];
+  int cta_item[kMaxCtas + 1], cta_tile[kMaxCtas + 1];   // where each block's run begins
 };
 
-__device__ __forceinline__ void load4(const void* p, int dtype, long long i, float* x) {
-  if (dtype == DSA_INT8) {
-    const char4 c = *reinterpret_cast<const char4*>(static_cast<const int8_t*>(p) + i);
-    x[0] = c.x; x[1] = c.y; x[2] = c.z; x[3] = c.w;
-    return;
+// One item: rows [row0, row0 + nrows) of (sequence b, KV head g) and the key
+// tiles [tile0, tile0 + ntiles) that some row of it sees.
+struct Item {
+  int b, g, row0, nrows, tile0, ntiles;
+  int past;             // position of the sequence's first new token
+  int lo, hi;           // keys that some row sees
+};
+
+__host__ __device__ __forceinline__ int imax(int a, int b) { return a > b ? a : b; }
+__host__ __device__ __forceinline__ int imin(int a, int b) { return a < b ? a : b; }
+
+__host__ __device__ __forceinline__ Item make_item(const FullParams& p, int i) {
+  Item w;
+  int b = 0;
+  while (i >= p.item0[b + 1]) ++b;
+  const int S = p.q0[b + 1] - p.q0[b];
+  const int rows = S * p.G;
+  const int per_head = (rows + kItemRows - 1) / kItemRows;
+  const int k = i - p.item0[b];
+  w.b = b;
+  w.g = k / per_head;
+  w.row0 = (k - w.g * per_head) * kItemRows;
+  w.nrows = imin(kItemRows, rows - w.row0);
+  w.past = p.T[b] - S;
+  w.hi = w.past + (w.row0 + w.nrows - 1) / p.G + 1;
+  w.lo = p.first[b];
+  if (p.window > 0) w.lo = imax(w.lo, w.past + w.row0 / p.G - p.window + 1);
+  w.lo = imin(w.lo, w.hi);
+  w.tile0 = w.lo / kTileKeys;
+  w.ntiles = w.lo < w.hi ? (w.hi + kTileKeys - 1) / kTileKeys - w.tile0 : 0;
+  return w;
+}
+
+// A block's run of units, one segment (a run of tiles of one item) at a time.
+struct Segment {
+  Item w;
+  int t0, t1;           // tiles, within the item's
+  bool rows_mode, whole;
+  int part;             // where a partial state goes
+};
+
+struct Walk {
+  int item, tile, end_item, end_tile;
+  __device__ __forceinline__ explicit Walk(const FullParams& p) {
+    item = p.cta_item[blockIdx.x];
+    tile = p.cta_tile[blockIdx.x];
+    end_item = p.cta_item[blockIdx.x + 1];
+    end_tile = p.cta_tile[blockIdx.x + 1];
   }
-  const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-  if (dtype == DSA_FP16) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+  __device__ __forceinline__ bool next(const FullParams& p, Segment* s) {
+    if (item > end_item || (item == end_item && tile >= end_tile)) return false;
+    s->w = make_item(p, item);
+    s->t0 = tile;
+    s->t1 = item == end_item ? end_tile : s->w.ntiles;
+    s->rows_mode = s->w.nrows > kSlotRows;
+    s->whole = s->t0 == 0 && s->t1 == s->w.ntiles;
+    s->part = 2 * blockIdx.x + (s->t0 > 0 ? 0 : 1);
+    ++item;
+    tile = 0;
+    return true;
+  }
+};
+
+// What a slot does of a segment: its rows, its tiles (first, step, count).
+struct SlotWork {
+  int row0, nrows, first, step, n;
+};
+__device__ __forceinline__ SlotWork slot_work(const Segment& s, int slot) {
+  SlotWork x;
+  const int n = s.t1 - s.t0;
+  if (s.rows_mode) {
+    x.row0 = s.w.row0 + slot * kSlotRows;
+    x.nrows = imin(kSlotRows, s.w.nrows - slot * kSlotRows);
+    x.first = s.t0;
+    x.step = 1;
+    x.n = n;
   } else {
-    x[0] = __uint_as_float(u.x << 16); x[1] = __uint_as_float(u.x & 0xffff0000u);
-    x[2] = __uint_as_float(u.y << 16); x[3] = __uint_as_float(u.y & 0xffff0000u);
+    x.row0 = s.w.row0;
+    x.nrows = s.w.nrows;
+    x.first = s.t0 + slot;
+    x.step = 2;
+    x.n = (n + 1 - slot) >> 1;
+  }
+  return x;
+}
+
+struct FullBars {
+  uint64_t full[kRing16], empty[kRing16];       // 16-bit tiles ready / consumed
+  uint64_t raw_full[kRaw], raw_empty[kRaw];     // INT8 codes landed / widened
+  uint64_t scales[kScaleRing];                  // a tile's scales are in shared memory
+  uint64_t q_ready[2], s_full[2], p_full[2], o_full[2];
+  uint64_t fix;                                 // a tile whose rows are zeroed before use has landed
+  uint64_t ml;                                  // keys mode: slot 1's statistics are in shared memory
+  uint64_t done;
+  uint32_t tmem_base;
+  int abort_flag, bad_page;
+  float m[kSlotRows], l[kSlotRows];
+};
+
+template <bool INT8>
+constexpr size_t full_smem() {
+  return 1024 + 2 * kTile16 + (INT8 ? kRing8 * kTile16 + kRaw * kTile8 + kScaleRing * 2 * kTileKeys * 4
+                                    : kRing16 * kTile16) + sizeof(FullBars);
+}
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// 128-byte-swizzled operand: `lbo` the pitch of 64-element column blocks of an
+// MN-major operand, 8-row groups 1,024 bytes apart.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// kind::f16, fp32 accumulator, M = N = 128; B K-major or MN-major
+__host__ __device__ constexpr uint32_t idesc128(bool f16, bool b_mn) {
+  return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((b_mn ? 1u : 0u) << 16) |
+         (16u << 17) | (8u << 24);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// 32 lanes x 32 columns of 32 bits, one lane a thread
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+      "%28,%29,%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+        "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+        "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+        "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+      "%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+      "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  uint32_t r;
+  if constexpr (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// Two signed codes, bytes 2i and 2i + 1 of `x`, as two exact 16-bit floats.
+// BF16: 0x4300 | n is 128 + n for n < 128, and 0x4380 is 256, so
+// (0x4300 | (c & 0x7f)) - (0x4300 | (c & 0x80)) is c. FP16: 0x6400 | u is
+// 1,024 + u for any byte, and u = c + 128.
+template <bool F16>
+__device__ __forceinline__ uint32_t widen2(uint32_t x, int i) {
+  if constexpr (F16) {
+    const uint32_t u = __byte_perm(x ^ 0x80808080u, 0x64646464u, i ? 0x4342 : 0x4140);
+    const uint32_t bias = 0x64806480u;   // 1,152
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&bias));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const uint32_t u = __byte_perm(x, 0u, i ? 0x4342 : 0x4140);
+    const uint32_t a = (u & 0x007f007fu) | 0x43004300u, b = (u & 0x00800080u) | 0x43004300u;
+    const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
 
-__global__ void __launch_bounds__(32) full_attn_kernel(const __grid_constant__ FullParams p) {
-  const int n = blockIdx.x, h = blockIdx.y, lane = threadIdx.x;
-  int b = 0;
-  while (n >= p.q0[b + 1]) ++b;
-  const int S = p.q0[b + 1] - p.q0[b];
-  const int pos = p.T[b] - S + (n - p.q0[b]);
-  int lo = p.first[b];
-  if (p.window > 0) lo = max(lo, pos - p.window + 1);
-  const int g = h / (p.Hq / p.Hkv);
-  float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-  const long long qi = (static_cast<long long>(n) * p.Hq + h) * DSA_HEAD_DIM + lane * 4;
-  load4(p.q, p.q_dtype, qi, q);
-  const float slope = p.slopes ? p.slopes[h] : 0.f;
-  bool bad = false;
-  for (int t = lo; t <= pos; ++t) {
-    const long long row = cache_row(p.pg, b, p.cap, t, &bad) * p.Hkv + g;
-    float k[4], v[4];
-    load4(p.k, p.kv_dtype, row * DSA_HEAD_DIM + lane * 4, k);
-    load4(p.v, p.kv_dtype, row * DSA_HEAD_DIM + lane * 4, v);
-    float z = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) z = fmaf(q[i], k[i], z);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
-    z *= p.scale;
-    float vs = 1.f;
-    if (p.kv_dtype == DSA_INT8) {
-      z *= p.k_scale[row];
-      vs = p.v_scale[row];
+// A wait of a whole warp: every lane gets the same answer, and the warp is
+// converged afterwards.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag));
+}
+
+// ---------------------------------------------------------------- loader
+// Issues the tiles in the order the products consume them: rows mode K0 V0 K1
+// V1 ..., keys mode K0 K1 V0 K2 V1 K3 ...
+template <class F>
+__device__ __forceinline__ bool for_tiles(const Segment& s, F&& f) {
+  const int n = s.t1 - s.t0;
+  if (s.rows_mode) {
+    for (int j = 0; j < n; ++j)
+      if (!f(s.t0 + j, false) || !f(s.t0 + j, true)) return false;
+  } else {
+    for (int i = 0; i < n + 2; ++i) {
+      if (i >= 2 && !f(s.t0 + i - 2, true)) return false;
+      if (i < n && !f(s.t0 + i, false)) return false;
+      if (n == 1 && i == 0) {   // a single tile: K0 V0
+        return f(s.t0, true);
+      }
     }
-    if (p.softcap > 0.f) z = p.softcap * tanhf(z / p.softcap);
-    z += slope * static_cast<float>(t - pos);
-    const float mn = fmaxf(m, z);
-    const float a = expf(m - mn), w = expf(z - mn);
-    l = l * a + w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = o[i] * a + w * vs * v[i];
-    m = mn;
   }
-  if (bad && lane == 0) atomicOr(p.status, kDevBadPage);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float x = l > 0.f ? o[i] / l : 0.f;
-    if (p.out_dtype == DSA_BF16) static_cast<__nv_bfloat16*>(p.out)[qi + i] = __float2bfloat16_rn(x);
-    else if (p.out_dtype == DSA_FP16) static_cast<__half*>(p.out)[qi + i] = __float2half_rn(x);
-    else static_cast<float*>(p.out)[qi + i] = x;
+  return true;
+}
+
+template <bool INT8>
+__device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                          FullBars* bars, uint8_t* ring, volatile int* abort_flag) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kStages = INT8 ? kRaw : kRing16;
+  constexpr uint32_t kBytes = INT8 ? kTile8 : kTile16;
+  uint64_t* full = INT8 ? bars->raw_full : bars->full;
+  uint64_t* empty = INT8 ? bars->raw_empty : bars->empty;
+  if (lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
-  if (p.lse && lane == 0) p.lse[static_cast<long long>(n) * p.Hq + h] = l > 0.f ? m + logf(l) : -INFINITY;
+  uint32_t seq = 0, fixes = 0;
+  bool bad = false;
+  Walk walk(p);
+  Segment s;
+  while (walk.next(p, &s)) {
+    const bool ok = for_tiles(s, [&](int t, bool is_v) {
+      const int st = seq % kStages;
+      if (seq >= kStages && !warp_wait(&empty[st], ((seq / kStages) - 1) & 1, abort_flag)) return false;
+      const int key = (s.w.tile0 + t) * kTileKeys;
+      const int row = static_cast<int>(cache_row(p.pg, s.w.b, p.cap, key, &bad));
+      uint8_t* dst = ring + st * kBytes;
+      const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
+      // rows of V that no query of the item sees
+      const int lo = imax(0, s.w.lo - key), hi = imin(kTileKeys, s.w.hi - key);
+      const bool fix = !INT8 && is_v && (lo > 0 || hi < kTileKeys);
+      uint64_t* bar = fix ? &bars->fix : &full[st];
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, kBytes);
+        tma_load_3d(dst, tm, bar, 0, s.w.g, row);
+        if constexpr (!INT8) tma_load_3d(dst + kBlk, tm, bar, 64, s.w.g, row);
+      }
+      __syncwarp();
+      if (fix) {
+        if (!warp_wait(&bars->fix, fixes++ & 1, abort_flag)) return false;
+        for (int r = 0; r < kTileKeys; ++r) {
+          if (r >= lo && r < hi) continue;
+          if (lane < 16)
+            *reinterpret_cast<uint4*>(dst + (lane >> 3) * kBlk + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+      }
+      ++seq;
+      return true;
+    });
+    if (!ok) break;
+  }
+  if (bad) bars->bad_page = 1;
+  if (lane == 0) {
+    // a block must not end with copies in flight (the consumers may have given up)
+    for (uint32_t q = seq > kStages ? seq - kStages : 0; q < seq; ++q) {
+      const long long t0 = clock64();
+      while (!mbar_try_wait(&full[q % kStages], (q / kStages) & 1) && clock64() - t0 < kWaitBudgetCycles) {
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ INT8 widening
+template <bool QK_F16>
+__device__ __forceinline__ void widen_role(const FullParams& p, FullBars* bars, uint8_t* ring, const uint8_t* raw,
+                                           float* scales, int tid, volatile int* abort_flag) {
+  uint32_t seq = 0, tiles = 0;
+  bool bad = false;
+  Walk walk(p);
+  Segment s;
+  while (walk.next(p, &s)) {
+    // this thread's key's scales, fetched a tile ahead (two dependent loads)
+    float ks = 0.f, vs = 0.f;
+    const auto fetch = [&](int t) {
+      const int key = (s.w.tile0 + t) * kTileKeys + tid;
+      ks = vs = 0.f;
+      if (t < s.t1 && key >= s.w.lo && key < s.w.hi) {
+        const long long i = cache_row(p.pg, s.w.b, p.cap, key, &bad) * p.Hkv + s.w.g;
+        ks = __ldg(p.k_scale + i);
+        vs = __ldg(p.v_scale + i);
+      }
+    };
+    fetch(s.t0);
+    const bool ok = for_tiles(s, [&](int t, bool is_v) {
+      const int rs = seq % kRaw, st = seq % kRing8;
+      if (!warp_wait(&bars->raw_full[rs], (seq / kRaw) & 1, abort_flag)) return false;
+      if (seq >= kRing8 && !warp_wait(&bars->empty[st], ((seq / kRing8) - 1) & 1, abort_flag)) return false;
+      if (!is_v) {
+        // (scales of the tile kScaleRing before are no longer read: its V stage
+        // was consumed before this tile's K stage became free)
+        float* sc = scales + (tiles % kScaleRing) * 2 * kTileKeys;
+        sc[tid] = ks;
+        sc[kTileKeys + tid] = vs;
+        mbar_arrive(&bars->scales[tiles % kScaleRing]);
+        ++tiles;
+        fetch(t + 1);
+      }
+      const uint8_t* src = raw + rs * kTile8;
+      uint8_t* dst = ring + st * kTile16;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = i * 16 + (tid >> 3), c = tid & 7;   // 16 codes: chunk c of the row
+        const uint4 x = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          o[e] = is_v ? widen2<false>(w[e >> 1], e & 1) : widen2<QK_F16>(w[e >> 1], e & 1);
+        uint8_t* d = dst + (c >> 2) * kBlk + row * 128;
+        const int ch = (c & 3) * 2;
+        *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      fence_async_smem();
+      mbar_arrive(&bars->full[st]);
+      mbar_arrive(&bars->raw_empty[rs]);
+      ++seq;
+      return true;
+    });
+    if (!ok) break;
+  }
+  if (bad) bars->bad_page = 1;
+}
+
+// ------------------------------------------------------------ tensor core
+template <bool QK_F16, bool PV_F16, int STAGES>
+__device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint32_t q_addr,
+                                         uint32_t ring_addr, volatile int* abort_flag) {
+  constexpr uint32_t id_qk = idesc128(QK_F16, false), id_pv = idesc128(PV_F16, true);
+  uint32_t seq = 0, nseg = 0, np[2] = {0, 0};
+  const auto wait_tile = [&](uint32_t q) { return mbar_wait_bounded(&bars->full[q % STAGES], (q / STAGES) & 1, abort_flag); };
+  const auto qk = [&](int slot, uint32_t q_tile, uint32_t q) {   // S[slot] = Q K^T
+    const uint32_t a = q_addr + q_tile * kTile16, b = ring_addr + (q % STAGES) * kTile16;
+#pragma unroll
+    for (int kk = 0; kk < DSA_HEAD_DIM / 16; ++kk) {
+      const uint32_t off = (kk >> 2) * kBlk + (kk & 3) * 32;
+      tc_mma_f16(tmem + slot * 128, sw128_desc(a + off, 16), sw128_desc(b + off, 16), id_qk, kk > 0);
+    }
+    tc_commit(&bars->s_full[slot]);
+  };
+  const auto pv = [&](int slot, uint32_t q, bool first) {        // O[slot] (+)= P V
+    if (!mbar_wait_bounded(&bars->p_full[slot], np[slot] & 1, abort_flag)) return false;
+    ++np[slot];
+    tc_fence_after();
+    const uint32_t b = ring_addr + (q % STAGES) * kTile16;
+#pragma unroll
+    for (int kk = 0; kk < kTileKeys / 16; ++kk)
+      tc_mma_f16_ts(tmem + 256 + slot * 128, tmem + slot * 128 + kk * 8, sw128_desc(b + kk * 16 * 128, kBlk), id_pv,
+                    !first || kk > 0);
+    return true;
+  };
+  const auto release = [&](uint32_t q) { tc_commit(&bars->empty[q % STAGES]); };
+  Walk walk(p);
+  Segment s;
+  bool ok = true;
+  while (ok && walk.next(p, &s)) {
+    // both slots are done with the previous segment, the queries are in place
+    if (!mbar_wait_bounded(&bars->q_ready[0], nseg & 1, abort_flag)) break;
+    if (!mbar_wait_bounded(&bars->q_ready[1], nseg & 1, abort_flag)) break;
+    ++nseg;
+    tc_fence_after();
+    const int n = s.t1 - s.t0;
+    if (n == 0) continue;
+    if (s.rows_mode) {
+      // ring positions: K_j at seq + 2j, V_j at seq + 2j + 1
+      for (int j = 0; j <= n && ok; ++j) {
+        const uint32_t k = seq + 2 * j, v = k - 1;
+        if (j > 0) ok = wait_tile(v);
+        if (ok && j < n) ok = wait_tile(k);
+        if (!ok) break;
+        tc_fence_after();
+        for (int slot = 0; slot < 2 && ok; ++slot) {
+          if (j > 0) {
+            ok = pv(slot, v, j == 1);
+            if (!ok) break;
+            if (slot == 1) release(v);
+            if (j == n) tc_commit(&bars->o_full[slot]);
+          }
+          if (j < n) {
+            qk(slot, slot, k);
+            if (slot == 1) release(k);
+          }
+        }
+      }
+      seq += 2 * n;
+    } else {
+      // step i: P V of tile i - 2, then S of tile i, both in slot i & 1
+      for (int i = 0; i < n + 2 && ok; ++i) {
+        const int slot = i & 1;
+        if (i >= 2 && i - 2 < n) {
+          ok = wait_tile(seq);
+          if (!ok) break;
+          tc_fence_after();
+          ok = pv(slot, seq, i < 4);
+          if (!ok) break;
+          release(seq++);
+          if (i >= n) tc_commit(&bars->o_full[slot]);
+        }
+        if (i < n) {
+          ok = wait_tile(seq);
+          if (!ok) break;
+          tc_fence_after();
+          qk(slot, 0, seq);
+          release(seq++);
+        }
+      }
+    }
+  }
+  tc_commit(&bars->done);
+  const long long t0 = clock64();
+  while (!mbar_try_wait(&bars->done, 0) && clock64() - t0 < kWaitBudgetCycles) {
+  }
+}
+
+// ---------------------------------------------------------------- softmax
+// One slot's four warps, one row a thread. MOD: the scores are capped or get a
+// bias.
+template <bool QK_F16, bool PV_F16, bool INT8, bool MOD>
+__device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint8_t* sQ,
+                                             const float* scales, int slot, volatile int* abort_flag) {
+  const int tid = threadIdx.x & 127, lane = tid & 31;
+  const uint32_t lane_addr = static_cast<uint32_t>((tid >> 5) * 32) << 16;
+  const uint32_t tS = tmem + lane_addr + slot * 128, tO = tmem + lane_addr + 256 + slot * 128;
+  uint32_t ns = 0, no = 0, nml = 0, nseg = 0, tile_seq = 0;
+  Walk walk(p);
+  Segment s;
+  while (walk.next(p, &s)) {
+    const SlotWork x = slot_work(s, slot);
+    const int r = x.row0 + tid;
+    const bool valid = tid < x.nrows;
+    const bool warp_valid = (tid & ~31) < x.nrows;
+    const int tok = r / p.G;
+    const int pos = s.w.past + tok;
+    const int head = s.w.g * p.G + (r - tok * p.G);
+    const long long row = (static_cast<long long>(p.q0[s.w.b]) + tok) * p.Hq + head;   // query row
+    float c = p.scale_log2;   // logits in units of log2 e per unit of S
+    if (slot == 0 || s.rows_mode) {
+      uint8_t* dst = sQ + slot * kTile16;
+      uint4 u[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        u[i] = valid ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row * DSA_HEAD_DIM) + i)
+                     : make_uint4(0, 0, 0, 0);
+      if (QK_F16 && p.q_dtype == DSA_BF16) {
+        // the row's largest exponent to 14
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        }
+        const int ex = top >= 0x80u ? static_cast<int>(top >> 7) - 127 - 14 : -126 - 14;   // scaled by 2^-ex
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack2<true>(ldexpf(__uint_as_float(w[e] << 16), -ex), ldexpf(__uint_as_float(w[e] & 0xffff0000u), -ex));
+          u[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        c = ldexpf(c, ex);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        *reinterpret_cast<uint4*>(dst + (i >> 3) * kBlk + tid * 128 + (((i & 7) ^ (tid & 7)) << 4)) = u[i];
+      fence_async_smem();
+      if (!s.rows_mode) bars->m[tid] = c;   // for slot 1
+    }
+    tc_fence_before();
+    mbar_arrive(&bars->q_ready[slot]);
+    if (slot == 1 && !s.rows_mode) {
+      // slot 0 loads the shared rows; what it scaled them by
+      if (!warp_wait(&bars->q_ready[0], nseg & 1, abort_flag)) break;
+      c = bars->m[tid];
+    }
+    ++nseg;
+    const float slope = MOD && p.slopes && valid ? p.slopes[head] * 1.4426950408889634f : 0.f;
+    const int pos0 = s.w.past + x.row0 / p.G, pos1 = s.w.past + (x.row0 + x.nrows - 1) / p.G;
+    const int lo = imax(p.first[s.w.b], p.window > 0 ? pos - p.window + 1 : 0);
+    const int lo1 = imax(p.first[s.w.b], p.window > 0 ? pos1 - p.window + 1 : 0);   // the last row's
+
+    float m = -INFINITY, l = 0.f;   // running maximum (in S units, or log2 units where c = 1), sum
+    bool ok = true;
+    for (int j = 0; j < x.n; ++j) {
+      const int t = x.first + j * x.step;
+      const int key0 = (s.w.tile0 + t) * kTileKeys;
+      if (!warp_wait(&bars->s_full[slot], ns & 1, abort_flag)) {
+        ok = false;
+        break;
+      }
+      ++ns;
+      tc_fence_after();
+      if constexpr (INT8) {
+        const uint32_t q = tile_seq + (t - s.t0);
+        if (!warp_wait(&bars->scales[q % kScaleRing], (q / kScaleRing) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+      }
+      if (warp_valid) {
+        float z[kTileKeys];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(tS + i * 32, z + i * 32);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < kTileKeys; ++i) asm volatile("" : "+f"(z[i]));   // no use before the wait
+        const float* sc = scales + ((tile_seq + (t - s.t0)) % kScaleRing) * 2 * kTileKeys;
+        if constexpr (INT8) {
+#pragma unroll
+          for (int i = 0; i < kTileKeys; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(sc + i);
+            z[i] *= f.x;
+            z[i + 1] *= f.y;
+            z[i + 2] *= f.z;
+            z[i + 3] *= f.w;
+          }
+        }
+        float cz = c;
+        if constexpr (MOD) {
+          cz = 1.0f;
+          if (p.softcap > 0.f) {
+            // cap * tanh(y) = cap - 2 cap / (1 + e^2y), in log2 units
+            const float two = 2.0f * c / p.softcap;                 // c holds log2 e
+            const float cap = p.softcap * 1.4426950408889634f;
+#pragma unroll
+            for (int i = 0; i < kTileKeys; ++i)
+              z[i] = fmaf(-2.0f * cap, fast_rcp(1.0f + fast_exp2(z[i] * two)), cap);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kTileKeys; ++i) z[i] *= c;
+          }
+          if (p.slopes) {
+            const float d = static_cast<float>(key0 - pos);
+#pragma unroll
+            for (int i = 0; i < kTileKeys; ++i) z[i] = fmaf(slope, d + static_cast<float>(i), z[i]);
+          }
+        }
+        if (key0 + kTileKeys - 1 > pos0 || key0 < lo1) {
+          const int a = lo - key0, b = pos - key0;   // columns a .. b are visible
+#pragma unroll
+          for (int i = 0; i < kTileKeys; ++i)
+            if (i < a || i > b) z[i] = -INFINITY;
+        }
+        float mt[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+        for (int i = 4; i < kTileKeys; i += 4) {
+          mt[0] = fmaxf(mt[0], z[i]);
+          mt[1] = fmaxf(mt[1], z[i + 1]);
+          mt[2] = fmaxf(mt[2], z[i + 2]);
+          mt[3] = fmaxf(mt[3], z[i + 3]);
+        }
+        const float mn = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+        // (-inf stays as it is: nothing seen yet)
+        const bool raise = mn > m && (m == -INFINITY || (mn - m) * cz > kRaise);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float to = fmaxf(m, mn);
+          const float f = to == -INFINITY || m == -INFINITY ? (m == to ? 1.0f : 0.0f) : fast_exp2((m - to) * cz);
+          m = to;
+          l *= f;
+          if (j > 0) {
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              float o[32];
+              uint32_t w[32];
+              tmem_ld32(tO + i * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(o[e]));
+#pragma unroll
+              for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
+              tmem_st32(tO + i * 32, w);
+            }
+          }
+        }
+        const float mc = m == -INFINITY ? 0.f : kLift - m * cz;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 c2 = make_float2(cz, cz), m2 = make_float2(mc, mc);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int e = h * 64 + 2 * i;
+            const float2 y = fma_f32x2(make_float2(z[e], z[e + 1]), c2, m2);
+            float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            sum[i & 1] = fma_f32x2(pr, make_float2(1.f, 1.f), sum[i & 1]);
+            if constexpr (INT8) {
+              const float2 vs = *reinterpret_cast<const float2*>(sc + kTileKeys + e);
+              pr.x *= vs.x;
+              pr.y *= vs.y;
+            }
+            w[i] = pack2<PV_F16>(pr.x, pr.y);
+          }
+          tmem_st32(tS + h * 32, w);
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      mbar_arrive(&bars->p_full[slot]);
+    }
+    if (!ok) break;
+    tile_seq += s.t1 - s.t0;
+    const float cz = MOD ? 1.0f : c;
+    const float m_log2 = m == -INFINITY ? -INFINITY : m * cz;
+    if (x.n > 0) {
+      if (!warp_wait(&bars->o_full[slot], no & 1, abort_flag)) break;
+      ++no;
+      tc_fence_after();
+    }
+    if (!s.rows_mode && slot == 1) {
+      // slot 0 joins the two states; it reads this slot's O itself
+      bars->m[tid] = m_log2;
+      bars->l[tid] = l;
+      mbar_arrive(&bars->ml);
+      continue;
+    }
+    float f0 = 1.0f, f1 = 0.0f, mj = m_log2, lj = l;
+    bool other = false;
+    if (!s.rows_mode) {
+      if (!warp_wait(&bars->ml, nml & 1, abort_flag)) break;
+      ++nml;
+      tc_fence_after();
+      other = slot_work(s, 1).n > 0;
+      if (other) {
+        const float m1 = bars->m[tid], l1 = bars->l[tid];
+        mj = fmaxf(m_log2, m1);
+        f0 = m_log2 == -INFINITY ? 0.f : fast_exp2(m_log2 - mj);
+        f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - mj);
+        lj = l * f0 + l1 * f1;
+      }
+    }
+    if (!warp_valid) continue;
+    float norm = 1.0f;
+    float* part = nullptr;
+    if (s.whole) {
+      norm = lj > 0.f ? 1.0f / lj : 0.f;
+      if (valid && p.lse) p.lse[row] = lj > 0.f ? (mj - kLift + log2f(lj)) * 0.6931471805599453f : -INFINITY;
+    } else {
+      part = p.partial + static_cast<long long>(s.part) * p.part_rows * (DSA_HEAD_DIM + 2);
+      const int pr = r - s.w.row0;
+      if (valid) {
+        part[p.part_rows * DSA_HEAD_DIM + 2 * pr] = mj;
+        part[p.part_rows * DSA_HEAD_DIM + 2 * pr + 1] = lj;
+      }
+      part += pr * DSA_HEAD_DIM;
+    }
+    f0 *= norm;
+    f1 *= norm;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      float o[32];
+      if (x.n > 0) {
+        tmem_ld32(tO + i * 32, o);
+        if (other) {
+          float b[32];
+          tmem_ld32(tO + 128 + i * 32, b);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(o[e]), "+f"(b[e]));
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = f0 * o[e] + f1 * b[e];
+        } else {
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(o[e]));
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= f0;
+        }
+        // a row without a key: whatever the products hold, its output is 0
+        if (s.whole && !(lj > 0.f)) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+      }
+      if (!valid) continue;
+      if (part) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<float4*>(part + i * 32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      } else if (p.out_dtype == DSA_FP32) {
+        float* d = static_cast<float*>(p.out) + row * DSA_HEAD_DIM + i * 32;
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<float4*>(d + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      } else {
+        uint16_t* d = static_cast<uint16_t*>(p.out) + row * DSA_HEAD_DIM + i * 32;
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w[e] = p.out_dtype == DSA_FP16 ? pack2<true>(o[2 * e], o[2 * e + 1]) : pack2<false>(o[2 * e], o[2 * e + 1]);
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(d + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+      }
+    }
+  }
+}
+
+template <bool QK_F16, bool PV_F16, bool INT8, bool MOD>
+__global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
+    full_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ FullParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  constexpr int kStages = INT8 ? kRing8 : kRing16;
+  uint8_t* sQ = base;
+  uint8_t* ring = sQ + 2 * kTile16;
+  uint8_t* raw = ring + kStages * kTile16;
+  float* scales = reinterpret_cast<float*>(raw + (INT8 ? kRaw * kTile8 : 0));
+  FullBars* bars = reinterpret_cast<FullBars*>(reinterpret_cast<uint8_t*>(scales) + (INT8 ? kScaleRing * 2 * kTileKeys * 4 : 0));
+  volatile int* abort_flag = &bars->abort_flag;
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bars->full[i], INT8 ? 128 : 1);
+      mbar_init(&bars->empty[i], 1);
+    }
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(&bars->raw_full[i], 1);
+      mbar_init(&bars->raw_empty[i], 128);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->q_ready[i], 128);
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_full[i], 128);
+      mbar_init(&bars->o_full[i], 1);
+    }
+    for (int i = 0; i < kScaleRing; ++i) mbar_init(&bars->scales[i], 128);
+    mbar_init(&bars->fix, 1);
+    mbar_init(&bars->ml, 128);
+    mbar_init(&bars->done, 1);
+    bars->abort_flag = 0;
+    bars->bad_page = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) tmem_alloc(&bars->tmem_base, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  pdl_trigger();
+  // registers: the launch gives every thread the same number; the softmax
+  // threads hold a row of S (128 values) and take what the others give up
+  if (warp < 8) {
+    regs_up<INT8 ? kSoftRegs8 : kSoftRegs16>();
+    softmax_role<QK_F16, PV_F16, INT8, MOD>(p, bars, tmem, sQ, scales, warp >> 2, abort_flag);
+  } else if (warp < 12) {
+    regs_down<INT8 ? kMiscRegs8 : kMiscRegs16>();
+    if (warp == 8) {
+      if ((threadIdx.x & 31) == 0)
+        mma_role<QK_F16, PV_F16, kStages>(p, bars, tmem, smem_u32(sQ), smem_u32(ring), abort_flag);
+    } else if (warp == 9) {
+      load_role<INT8>(p, tm_k, tm_v, bars, INT8 ? raw : ring, abort_flag);
+    }
+  } else {
+    if constexpr (INT8) {
+      regs_down<kWidenRegs>();
+      widen_role<QK_F16>(p, bars, ring, raw, scales, threadIdx.x - 384, abort_flag);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, kTmemCols);
+  if (threadIdx.x == 0)
+    p.errors[blockIdx.x] = (bars->abort_flag ? kDevTimeout : 0u) | (bars->bad_page ? kDevBadPage : 0u);
+}
+
+// ------------------------------------------------------------------ merge
+// Joins the parts of the items that more than one block worked on: `wpr` warps
+// per query row take every wpr-th part, four dims a lane.
+struct MergeParams {
+  const float* partial;
+  void* out;
+  float* lse;
+  int part_rows, out_dtype, wpr, splits, blocks;
+  int first_cta[kMaxCtas], last_cta[kMaxCtas];   // blocks that hold split item i's parts
+};
+constexpr int kMergeThreads = 256;
+
+__global__ void __launch_bounds__(kMergeThreads)
+    full_attn_merge_kernel(const __grid_constant__ FullParams p, const __grid_constant__ MergeParams mp) {
+  __shared__ float s_m[kMergeThreads / 32], s_l[kMergeThreads / 32];
+  __shared__ float4 s_o[kMergeThreads];
+  __shared__ uint32_t s_err;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    if (threadIdx.x == 0) s_err = 0u;
+    __syncthreads();
+    pdl_wait();
+    uint32_t e = 0;
+    for (int c = threadIdx.x; c < mp.blocks; c += kMergeThreads) e |= __ldcg(p.errors + c);
+    if (e) atomicOr(&s_err, e);
+    __syncthreads();
+    if (threadIdx.x == 0) *p.status = s_err;
+  }
+  if (mp.splits == 0) return;
+  const int sub = warp % mp.wpr, rows_here = kMergeThreads / 32 / mp.wpr;
+  const int i = blockIdx.y;
+  const int c0 = mp.first_cta[i], c1 = mp.last_cta[i];
+  // the item is the one block c1's run begins in
+  const Item w = make_item(p, p.cta_item[c1]);
+  const int pr = blockIdx.x * rows_here + warp / mp.wpr;
+  pdl_wait();
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (pr < w.nrows) {
+    const long long pitch = static_cast<long long>(mp.part_rows) * (DSA_HEAD_DIM + 2);
+    const auto part_of = [&](int c) { return mp.partial + (2 * c + (c == c0 ? 1 : 0)) * pitch; };
+    const long long ml = static_cast<long long>(mp.part_rows) * DSA_HEAD_DIM + 2 * pr;
+    for (int c = c0 + sub; c <= c1; c += mp.wpr) m = fmaxf(m, __ldcg(part_of(c) + ml));
+#pragma unroll 4
+    for (int c = c0 + sub; c <= c1; c += mp.wpr) {
+      const float* q = part_of(c);
+      const float2 x = __ldcg(reinterpret_cast<const float2*>(q + ml));
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(q + pr * DSA_HEAD_DIM) + lane);
+      if (x.x == -INFINITY) continue;
+      const float f = fast_exp2(x.x - m);
+      l = fmaf(x.y, f, l);
+      o.x = fmaf(y.x, f, o.x);
+      o.y = fmaf(y.y, f, o.y);
+      o.z = fmaf(y.z, f, o.z);
+      o.w = fmaf(y.w, f, o.w);
+    }
+  }
+  if (mp.wpr > 1) {
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
+    s_o[threadIdx.x] = o;
+    __syncthreads();
+    if (sub != 0) return;
+    float mm = -INFINITY;
+    for (int k = 0; k < mp.wpr; ++k) mm = fmaxf(mm, s_m[warp + k]);
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < mp.wpr; ++k) {
+      if (s_m[warp + k] == -INFINITY) continue;
+      const float f = fast_exp2(s_m[warp + k] - mm);
+      const float4 y = s_o[threadIdx.x + k * 32];
+      l = fmaf(s_l[warp + k], f, l);
+      o.x = fmaf(y.x, f, o.x);
+      o.y = fmaf(y.y, f, o.y);
+      o.z = fmaf(y.z, f, o.z);
+      o.w = fmaf(y.w, f, o.w);
+    }
+    m = mm;
+  }
+  if (pr >= w.nrows) return;
+  const float norm = l > 0.f ? 1.0f / l : 0.f;
+  const int r = w.row0 + pr, tok = r / p.G;
+  const long long row = (static_cast<long long>(p.q0[w.b]) + tok) * p.Hq + w.g * p.G + (r - tok * p.G);
+  const float4 v = make_float4(o.x * norm, o.y * norm, o.z * norm, o.w * norm);
+  if (mp.out_dtype == DSA_FP32)
+    *(reinterpret_cast<float4*>(static_cast<float*>(mp.out) + row * DSA_HEAD_DIM) + lane) = v;
+  else
+    *(reinterpret_cast<uint2*>(static_cast<uint16_t*>(mp.out) + row * DSA_HEAD_DIM) + lane) =
+        mp.out_dtype == DSA_FP16 ? make_uint2(pack2<true>(v.x, v.y), pack2<true>(v.z, v.w))
+                                 : make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+  if (mp.lse && lane == 0) mp.lse[row] = l > 0.f ? (m - kLift + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // -------------------------------------------------------------------- host
@@ -139,6 +1031,105 @@ int check_full(const dsa_full_problem* p) {
   return DSA_OK;
 }
 
+// Costs of a unit, in quarters of a tile of 256 rows: a tile of up to 128 rows
+// takes the same loads and half the products; an item, its queries and output.
+constexpr int kCostRows = 4, kCostKeys = 3, kCostItem = 6;
+
+// Lays the items out over the blocks (fp: the problem and the runs, mp: the
+// items that are split) and returns the number of blocks.
+int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp) {
+  fp->B = p->batch;
+  fp->Hq = p->num_q_heads;
+  fp->Hkv = p->num_kv_heads;
+  fp->G = p->num_q_heads / p->num_kv_heads;
+  fp->cap = p->cache_capacity;
+  fp->window = p->window;
+  fp->part_rows = 0;
+  for (int b = 0; b < p->batch; ++b) {
+    const long long rows = static_cast<long long>(p->q_len[b]) * fp->G;
+    fp->q0[b + 1] = fp->q0[b] + p->q_len[b];
+    fp->item0[b + 1] = fp->item0[b] + static_cast<int>((rows + kItemRows - 1) / kItemRows) * p->num_kv_heads;
+    fp->T[b] = p->total_len[b];
+    fp->first[b] = p->first_key[b];
+    fp->part_rows = imax(fp->part_rows, static_cast<int>(rows < kItemRows ? rows : kItemRows));
+  }
+  fp->part_rows = (fp->part_rows + 3) & ~3;   // parts stay 16-byte aligned
+  const int items = fp->item0[p->batch];
+  long long cost = 0, tiles = 0;
+  for (int i = 0; i < items; ++i) {
+    const Item w = make_item(*fp, i);
+    cost += kCostItem + static_cast<long long>(w.ntiles) * (w.nrows > kSlotRows ? kCostRows : kCostKeys);
+    tiles += w.ntiles;
+  }
+  const int most = imin(sms, kMaxCtas);
+  const int want = static_cast<int>(tiles < most ? (tiles > 0 ? tiles : 1) : most);
+  // run k begins where the costs reach k / want of their sum
+  int blocks = 0;
+  long long at = 0;
+  int k = 0;
+  for (int i = 0; i < items; ++i) {
+    const Item w = make_item(*fp, i);
+    const int unit = w.nrows > kSlotRows ? kCostRows : kCostKeys;
+    const long long end = at + kCostItem + static_cast<long long>(w.ntiles) * unit;
+    for (; k < want && cost * k < end * want; ++k) {
+      const long long x = cost * k / want - at - kCostItem;
+      const int tile = x > 0 ? static_cast<int>(x / unit) : 0;
+      if (blocks > 0 && fp->cta_item[blocks - 1] == i && fp->cta_tile[blocks - 1] >= tile) continue;
+      fp->cta_item[blocks] = i;
+      fp->cta_tile[blocks++] = tile;
+    }
+    at = end;
+  }
+  fp->cta_item[blocks] = items;
+  fp->cta_tile[blocks] = 0;
+  mp->splits = 0;
+  int parts = 1;
+  for (int c = 1; c < blocks; ++c) {
+    if (fp->cta_tile[c] == 0) continue;
+    const int n = mp->splits;
+    if (n > 0 && mp->last_cta[n - 1] == c - 1 && fp->cta_item[c] == fp->cta_item[c - 1]) {
+      mp->last_cta[n - 1] = c;
+    } else {
+      mp->first_cta[n] = c - 1;
+      mp->last_cta[n] = c;
+      ++mp->splits;
+    }
+    parts = imax(parts, c - mp->first_cta[mp->splits - 1] + 1);
+  }
+  mp->wpr = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;
+  return blocks;
+}
+
+constexpr size_t kPartialAt = 256 + ((kMaxCtas * 4 + 255) / 256) * 256;
+
+size_t full_bytes(const dsa_full_problem* p) {
+  FullParams fp{};
+  MergeParams mp{};
+  // (a schedule never has more blocks than tiles, whatever the device)
+  const int blocks = schedule(p, kMaxCtas, &fp, &mp);
+  return kPartialAt + static_cast<size_t>(2) * blocks * fp.part_rows * (DSA_HEAD_DIM + 2) * 4;
+}
+
+template <bool QK_F16, bool PV_F16, bool INT8>
+cudaError_t launch_full(bool mod, int blocks, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const FullParams& fp,
+                        cudaStream_t st) {
+  const auto kern = mod ? full_attn_kernel<QK_F16, PV_F16, INT8, true> : full_attn_kernel<QK_F16, PV_F16, INT8, false>;
+  constexpr size_t smem = full_smem<INT8>();
+  cudaError_t e = set_max_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  // the warps' register counts must fit into what the block is launched with:
+  // a warp that asks for more would wait for ever
+  static std::atomic<int> regs{0};   // of either kernel of this family: their launch bounds are the same
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes a;
+    if ((e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(kern))) != cudaSuccess) return e;
+    if (a.numRegs * (INT8 ? kThreads8 : kThreads16) < kRegs<INT8>) return cudaErrorInvalidConfiguration;
+    regs.store(a.numRegs, std::memory_order_relaxed);
+  }
+  return launch_kernel("full_attn_kernel", kern, dim3(blocks), dim3(INT8 ? kThreads8 : kThreads16), smem, st, false,
+                       tm_k, tm_v, fp);
+}
+
 int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* q, const void* k, const void* v,
               const float* ks, const float* vs, const float* slopes, void* out, float* lse, void* ws,
               size_t ws_bytes, void* stream) {
@@ -161,36 +1152,52 @@ int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* 
   int sms = 0;
   if (int rc = current_device(&sms)) return rc;
   FullParams fp{};
+  MergeParams mp{};
+  const int blocks = schedule(p, sms, &fp, &mp);
+  if (fp.q0[p->batch] == 0) {
+    const cudaError_t e = cudaMemsetAsync(ws, 0, 4, static_cast<cudaStream_t>(stream));   // the status word
+    return e == cudaSuccess ? DSA_OK : report_errorf(DSA_ERR_CUDA, "status clear: %s", cudaGetErrorString(e));
+  }
+  const long long rows = pages ? static_cast<long long>(pages->num_blocks) * pages->block_size
+                               : static_cast<long long>(p->batch) * p->cache_capacity;
+  if (rows >= (1LL << 31)) return report_error(DSA_ERR_UNSUPPORTED, "the caches must hold fewer than 2^31 tokens");
+  const int elem = p->kv_dtype == DSA_INT8 ? 1 : 2;
+  CUtensorMap tm_k, tm_v;
+  if (int rc = kv_tile_map(&tm_k, k, rows, p->num_kv_heads, elem)) return rc;
+  if (int rc = kv_tile_map(&tm_v, v, rows, p->num_kv_heads, elem)) return rc;
   fp.q = q;
-  fp.k = k;
-  fp.v = v;
   fp.k_scale = ks;
   fp.v_scale = vs;
   fp.slopes = slopes;
   fp.out = out;
   fp.lse = lse;
   fp.status = static_cast<uint32_t*>(ws);
-  fp.B = p->batch;
-  fp.Hq = p->num_q_heads;
-  fp.Hkv = p->num_kv_heads;
-  fp.cap = p->cache_capacity;
-  fp.window = p->window;
+  fp.errors = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + 256);
+  fp.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kPartialAt);
   fp.q_dtype = p->q_dtype;
-  fp.kv_dtype = p->kv_dtype;
   fp.out_dtype = p->out_dtype;
-  fp.scale = p->softmax_scale > 0.0f ? p->softmax_scale : 1.0f / std::sqrt(static_cast<float>(p->head_dim));
+  const float scale = p->softmax_scale > 0.0f ? p->softmax_scale : 1.0f / std::sqrt(static_cast<float>(p->head_dim));
+  fp.scale_log2 = scale * 1.4426950408889634f;
   fp.softcap = p->softcap;
   fp.pg = pg;
-  for (int b = 0; b < p->batch; ++b) {
-    fp.q0[b + 1] = fp.q0[b] + p->q_len[b];
-    fp.T[b] = p->total_len[b];
-    fp.first[b] = p->first_key[b];
-  }
+  mp.partial = fp.partial;
+  mp.out = out;
+  mp.lse = lse;
+  mp.part_rows = fp.part_rows;
+  mp.out_dtype = p->out_dtype;
+  mp.blocks = blocks;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemsetAsync(ws, 0, 256, st);
-  const int n = fp.q0[p->batch];
-  if (e == cudaSuccess && n > 0)
-    e = launch_kernel("full_attn_kernel", full_attn_kernel, dim3(n, p->num_q_heads), dim3(32), 0, st, false, fp);
+  const bool mod = p->softcap > 0.0f || slopes != nullptr;
+  cudaError_t e;
+  if (p->kv_dtype == DSA_BF16) e = launch_full<false, false, false>(mod, blocks, tm_k, tm_v, fp, st);
+  else if (p->kv_dtype == DSA_FP16) e = launch_full<true, true, false>(mod, blocks, tm_k, tm_v, fp, st);
+  else if (p->q_dtype == DSA_FP16) e = launch_full<true, false, true>(mod, blocks, tm_k, tm_v, fp, st);
+  else e = launch_full<false, false, true>(mod, blocks, tm_k, tm_v, fp, st);
+  if (e == cudaSuccess) {
+    const int rows_here = kMergeThreads / 32 / mp.wpr;
+    const dim3 grid = mp.splits ? dim3((fp.part_rows + rows_here - 1) / rows_here, mp.splits) : dim3(1);
+    e = launch_kernel("full_attn_merge_kernel", full_attn_merge_kernel, grid, dim3(kMergeThreads), 0, st, true, fp, mp);
+  }
   if (e != cudaSuccess) return report_errorf(DSA_ERR_CUDA, "full attention launch: %s", cudaGetErrorString(e));
   return DSA_OK;
 }
@@ -202,7 +1209,7 @@ using namespace dsa;
 
 extern "C" size_t dsa_full_attn_workspace_size(const dsa_full_problem* p) {
   if (check_full(p)) return 0;
-  return 256;
+  return full_bytes(p);
 }
 
 extern "C" int dsa_full_attn(const dsa_full_problem* p, const void* q, const void* k, const void* v,
