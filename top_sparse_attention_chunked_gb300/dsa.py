@@ -526,17 +526,24 @@ def dsa_sparse_attn_prefill(p, q, qI, w, kI, k, v, k_scale, v_scale, idx_out, ou
           workspace, stream, pages)
 
 
-def _here(t: Optional[torch.Tensor], name: str, dtype=None, shape=None):
-    """_ptr of a tensor that must lie on the current device (whose stream the
-    call goes to)."""
-    ptr = _ptr(t, name, dtype, shape)
-    if t is not None and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return ptr
+def _here(dev: int, t: Optional[torch.Tensor], name: str, dtype=None, shape=None):
+    """_ptr of a tensor that must lie on device `dev`, the current one (whose
+    stream the call goes to)."""
+    if t is None:
+        return None
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _ws_here(ws: torch.Tensor):
-    return _here(ws, "workspace", torch.uint8), ws.numel()
+def _ws_here(dev: int, ws: torch.Tensor):
+    return _here(dev, ws, "workspace", torch.uint8), ws.numel()
 
 
 def make_full_attn_problem(q_len: Sequence[int], total_len: Sequence[int], num_q_heads: int,
@@ -578,25 +585,27 @@ def dsa_full_attn(p: DsaFullProblem, q, k, v, k_scale, v_scale, out, workspace, 
     """Attention of the packed new tokens q [N, Hq, 128] (N = sum of q_len, or
     more: rows behind are left alone) over all cached keys; with `pages`
     (make_pages) the caches are paged pools. lse [N, Hq] fp32 is optional."""
-    Hq, Hkv = p.num_q_heads, p.num_kv_heads
-    lib = load_library()
-    wp, wn = _ws_here(workspace)
+    Hq, Hkv, lib, dev = p.num_q_heads, p.num_kv_heads, load_library(), torch.cuda.current_device()
+    wp, wn = _ws_here(dev, workspace)
     kvdt = _TORCH_DT[p.kv_dtype]
     lead = _cache_shapes(p, pages)
     need = sum(p.q_len[:p.batch])
-    for t, name, tail in ((q, "q", (Hq, 128)), (out, "out", (Hq, 128)), (lse, "lse", (Hq,))):
-        if t is not None and (t.dim() < 1 + len(tail) or tuple(t.shape[-len(tail):]) != tail
-                              or t.numel() < need * math.prod(tail)):
-            raise ValueError(f"{name} must be [N, {', '.join(map(str, tail))}] with N >= {need}, "
-                             f"got {tuple(t.shape)}")
-    args = [_here(q, "q", _TORCH_DT[p.q_dtype]), _here(k, "k", kvdt, lead + (Hkv, 128)),
-            _here(v, "v", kvdt, lead + (Hkv, 128)), _here(k_scale, "k_scale", torch.float32, lead + (Hkv,)),
-            _here(v_scale, "v_scale", torch.float32, lead + (Hkv,)),
-            _here(slopes, "slopes", torch.float32, (Hq,)), _here(out, "out", _TORCH_DT[p.out_dtype]),
-            _here(lse, "lse", torch.float32), wp, wn, _stream(stream)]
+    if q.dim() != 3 or q.shape[1:] != (Hq, 128) or q.shape[0] < need:
+        raise ValueError(f"q must be [N, {Hq}, 128] with N >= {need}, got {tuple(q.shape)}")
+    if out.dim() != 3 or out.shape[1:] != (Hq, 128) or out.shape[0] < need:
+        raise ValueError(f"out must be [N, {Hq}, 128] with N >= {need}, got {tuple(out.shape)}")
+    if lse is not None and (lse.dim() != 2 or lse.shape[1] != Hq or lse.shape[0] < need):
+        raise ValueError(f"lse must be [N, {Hq}] with N >= {need}, got {tuple(lse.shape)}")
+    args = [_here(dev, q, "q", _TORCH_DT[p.q_dtype]), _here(dev, k, "k", kvdt, lead + (Hkv, 128)),
+            _here(dev, v, "v", kvdt, lead + (Hkv, 128)),
+            _here(dev, k_scale, "k_scale", torch.float32, lead + (Hkv,)),
+            _here(dev, v_scale, "v_scale", torch.float32, lead + (Hkv,)),
+            _here(dev, slopes, "slopes", torch.float32, (Hq,)), _here(dev, out, "out", _TORCH_DT[p.out_dtype]),
+            _here(dev, lse, "lse", torch.float32), wp, wn, _stream(stream)]
     if pages is None:
         _check(lib.dsa_full_attn(ctypes.byref(p), *args))
     else:
+        _here(dev, pages._table, "block_table")
         _check(lib.dsa_full_attn_paged(ctypes.byref(p), ctypes.byref(pages), *args))
 
 
@@ -622,8 +631,10 @@ def make_page_pools(tensors: Sequence[torch.Tensor], num_blocks: int):
         if n == 0 or t.numel() % num_blocks:
             raise ValueError(f"pool {i} does not hold {num_blocks} equal blocks")
         arr[i] = DsaPagePool(_ptr(t, f"pool {i}"), n // num_blocks)
-    arr._keep = tuple(tensors)
-    arr._blocks = num_blocks
+    devs = {t.get_device() for t in tensors}
+    if len(devs) > 1:
+        raise ValueError(f"the pools lie on different devices: {sorted(devs)}")
+    arr._keep, arr._blocks, arr._dev = tuple(tensors), num_blocks, devs.pop() if devs else None
     return arr
 
 
@@ -639,16 +650,21 @@ def alloc_pages_workspace(st: DsaPageState, device="cuda") -> torch.Tensor:
     return torch.empty(dsa_pages_workspace_size(st), dtype=torch.uint8, device=device)
 
 
-def _page_args(st: DsaPageState, pools, table_out, refs_out):
+def _page_args(dev: int, st: DsaPageState, pools, table_out, refs_out):
     """Checked addresses of the new state (None: the old one's arrays) and the pools."""
     table, refs = st._keep
-    for t, name in ((table, "block_table"), (refs, "refs")) + tuple((t, "pool") for t in (pools._keep if pools else ())):
-        _here(t, name)
-    if pools and pools._blocks != st.num_blocks:
-        raise ValueError(f"the pools hold {pools._blocks} blocks, the state {st.num_blocks}")
-    return (len(pools._keep) if pools else 0, pools if pools else None,
-            _here(table if table_out is None else table_out, "table_out", torch.int32, table.shape),
-            _here(refs if refs_out is None else refs_out, "refs_out", torch.int32, refs.shape))
+    _here(dev, table, "block_table")
+    _here(dev, refs, "refs")
+    n = 0
+    if pools is not None and len(pools._keep):
+        n = len(pools._keep)
+        if pools._blocks != st.num_blocks:
+            raise ValueError(f"the pools hold {pools._blocks} blocks, the state {st.num_blocks}")
+        if pools._dev != dev:
+            raise ValueError(f"the pools are on cuda:{pools._dev}, the current device is cuda:{dev}")
+    return (n, pools if n else None,
+            st.block_table if table_out is None else _here(dev, table_out, "table_out", torch.int32, table.shape),
+            st.refs if refs_out is None else _here(dev, refs_out, "refs_out", torch.int32, refs.shape))
 
 
 def dsa_pages_update(st: DsaPageState, parent, keep_len, new_len, pools, workspace, table_out=None,
@@ -657,26 +673,26 @@ def dsa_pages_update(st: DsaPageState, parent, keep_len, new_len, pools, workspa
     becomes the first keep_len[r] tokens of old row parent[r] (-1: empty) and
     room for new_len[r]. Without table_out / refs_out the state is changed in
     place; pools from make_page_pools (None: no contents move)."""
-    lib = load_library()
-    wp, wn = _ws_here(workspace)
-    n, arr, tp, rp = _page_args(st, pools, table_out, refs_out)
-    one = (st.rows,)
+    lib, dev = load_library(), torch.cuda.current_device()
+    wp, wn = _ws_here(dev, workspace)
+    n, arr, tp, rp = _page_args(dev, st, pools, table_out, refs_out)
+    i32, one = torch.int32, (st.rows,)
     _check(lib.dsa_pages_update(
-        ctypes.byref(st), _here(parent, "parent", torch.int32, one), _here(keep_len, "keep_len", torch.int32, one),
-        _here(new_len, "new_len", torch.int32, one), _here(first_key, "first_key", torch.int32, one), n, arr,
-        tp, rp, _here(counts, "counts", torch.int32, (2,)), wp, wn, _stream(stream)))
+        ctypes.byref(st), _here(dev, parent, "parent", i32, one), _here(dev, keep_len, "keep_len", i32, one),
+        _here(dev, new_len, "new_len", i32, one), _here(dev, first_key, "first_key", i32, one), n, arr,
+        tp, rp, _here(dev, counts, "counts", i32, (2,)), wp, wn, _stream(stream)))
 
 
 def dsa_pages_compact(st: DsaPageState, pools, workspace, table_out=None, refs_out=None, remap=None,
                       counts=None, stream=None):
     """Move the live blocks to the front of the pools (in place without
     table_out / refs_out); remap [num_blocks] receives the new indices."""
-    lib = load_library()
-    wp, wn = _ws_here(workspace)
-    n, arr, tp, rp = _page_args(st, pools, table_out, refs_out)
+    lib, dev = load_library(), torch.cuda.current_device()
+    wp, wn = _ws_here(dev, workspace)
+    n, arr, tp, rp = _page_args(dev, st, pools, table_out, refs_out)
     _check(lib.dsa_pages_compact(
-        ctypes.byref(st), n, arr, tp, rp, _here(remap, "remap", torch.int32, (st.num_blocks,)),
-        _here(counts, "counts", torch.int32, (2,)), wp, wn, _stream(stream)))
+        ctypes.byref(st), n, arr, tp, rp, _here(dev, remap, "remap", torch.int32, (st.num_blocks,)),
+        _here(dev, counts, "counts", torch.int32, (2,)), wp, wn, _stream(stream)))
 
 
 def make_beam_problem(batch: int, beams: int, vocab: int, select: int, logits_dtype="bf16",
@@ -701,8 +717,8 @@ def dsa_beam_select(p: DsaBeamProblem, logits, scores, out_scores, out_tokens, o
     """The `select` best continuations of each batch entry's beams: logits
     [batch * beams, vocab] whose rows may lie row_stride elements apart
     (p.row_stride), scores [batch * beams]; out_* [batch, select]."""
-    lib = load_library()
-    wp, wn = _ws_here(workspace)
+    lib, dev = load_library(), torch.cuda.current_device()
+    wp, wn = _ws_here(dev, workspace)
     n, out = p.batch * p.beams, (p.batch, p.select)
     stride = p.row_stride or p.vocab
     if logits.shape != (n, p.vocab) or logits.stride(-1) != 1 or (n > 1 and logits.stride(0) != stride):
@@ -710,13 +726,15 @@ def dsa_beam_select(p: DsaBeamProblem, logits, scores, out_scores, out_tokens, o
                          f"{tuple(logits.shape)} with strides {logits.stride()}")
     if logits.dtype != _TORCH_DT[p.logits_dtype]:
         raise ValueError(f"logits must be {_TORCH_DT[p.logits_dtype]}, got {logits.dtype}")
-    _here(logits[:1], "logits")
+    if logits.get_device() != dev:
+        raise ValueError(f"logits is on {logits.device}, the current device is cuda:{dev}")
     if finished is not None and finished.dtype == torch.bool:
         finished = finished.view(torch.uint8)
+    i32 = torch.int32
     _check(lib.dsa_beam_select(
-        ctypes.byref(p), logits.data_ptr(), _here(scores, "scores", torch.float32, (n,)),
-        _here(finished, "finished", torch.uint8, (n,)), _here(out_scores, "out_scores", torch.float32, out),
-        _here(out_tokens, "out_tokens", torch.int32, out), _here(out_parents, "out_parents", torch.int32, out),
+        ctypes.byref(p), logits.data_ptr(), _here(dev, scores, "scores", torch.float32, (n,)),
+        _here(dev, finished, "finished", torch.uint8, (n,)), _here(dev, out_scores, "out_scores", torch.float32, out),
+        _here(dev, out_tokens, "out_tokens", i32, out), _here(dev, out_parents, "out_parents", i32, out),
         wp, wn, _stream(stream)))
 
 
