@@ -2,26 +2,35 @@
 // over beams x vocabulary, per batch entry.
 //
 // Two launches. beam_scan_kernel reads every logit once. Its blocks, as many as
-// are resident at once, take equal runs of tiles (512 16-byte vectors of a
+// are resident at once, take equal runs of tiles (1,024 16-byte vectors of a
 // row), a run spanning the end of one row and the start of the next where it
 // must; a row's part in a block is a slice. Of each slice a block keeps, side
-// by side, the maximum and the sum of exponentials (one online state a thread,
-// joined at the end) and the `select` largest logits. The latter through a
-// lower bound: every thread holds the largest value it has seen, a warp's j-th
-// largest of those (j = select / 8 warps) is reached by j values of the warp,
-// so the smallest of the eight warps' is reached by `select` values of the
-// slice. Values that reach it -- a few times `select` in all, one comparison
-// per tile for the rest -- are appended to a list that the block sorts when
-// it fills and at the end. Within a row totals are ordered as the logits are,
-// so a row's candidates are its `select` largest logits, lower tokens first.
-// beam_merge_kernel joins the slices' sums of each row in 64 bits, forms the
-// candidates' totals in 64 bits (rows have different offsets: totals may lie
-// closer together than fp32 tells apart), bounds them in the same way and
-// sorts the few that are left.
+// by side, the sum of exponentials and the values that can be among the best.
+// The latter through a lower bound: every thread holds the largest value it
+// has seen, a warp's j-th largest of those (j = select / 8 warps) is reached by
+// j values of the warp, so the smallest of the eight warps' is reached by
+// `select` values of the slice. Values that reach it -- a few times `select`
+// in all, one comparison per thread and tile for the rest -- are appended to a
+// list, of which what the final bound leaves goes to the workspace as it is.
+// Only a list that gets long (ties, rising rows) is cut to its best `select`.
+// Within a row totals are ordered as the logits are, so that loses nothing.
+//
+// Sums: a thread's is sum 2^(x H + c) with H = log2(e) rounded to fp32 and c an
+// integer (the maximum's, negated): one paired multiply-add and one 2^ a
+// value, and sums of different c join by exact powers of two. A slice's joins
+// as 64-bit fixed point (2^-36 of a term at the maximum). H's rounding scales
+// every exponent by 1 - 1.3e-8, which the merge undoes at the maximum; what is
+// left is 1.3e-8 of a term's distance from it.
+//
+// beam_merge_kernel joins the slices' sums of each row, bounds the candidates'
+// totals in the same way, forms the totals of those that reach the bound in 64
+// bits (rows have different offsets: totals may lie closer together than fp32
+// tells apart) and ranks them by counting.
 //
 // The order of a list depends on the order of execution; its keys are distinct
-// (value, then token), so what is sorted out of it does not.
+// (value, then token), so what is picked out of it does not.
 #include <algorithm>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -34,44 +43,42 @@ namespace {
 
 constexpr int kBmThreads = 256;
 constexpr int kBmWarps = kBmThreads / 32;
-constexpr int kVecs = 2;            // 16-byte vectors a thread takes per tile
+constexpr int kVecs = 4;            // 16-byte vectors a thread takes per tile
 constexpr int kTileVecs = kBmThreads * kVecs;
-constexpr int kDrain = 184;         // list entries that trigger a sort
-constexpr int kMaxCands = 8192;     // candidates of one batch entry (all rows and slices)
-constexpr int kMergeList = 1024;    // of which the merge sorts from a list
-constexpr int kResident = 5;        // scan blocks per SM (37 KB of shared memory each)
+constexpr int kKeep = 128;          // candidates a slice may hand on
+constexpr int kDrain = 256;         // list entries that are cut to the best at once
+constexpr int kMaxLists = 512;      // slices of one batch entry
+constexpr int kMergeList = kBmWarps * kKeep + DSA_MAX_SELECT;   // the merge's list: a round's candidates and the best before
+constexpr int kResident = 3;        // scan blocks per SM (70 KB of shared memory each for 16-bit logits)
 
-struct Cand {
-  float value;
-  int32_t token;      // -1: none
-};
 struct SliceSum {
-  double sum;         // of exp(x - max); NaN if the slice holds a NaN or +infinity
+  unsigned long long sum;   // of 2^(x H + c) with the c of `max`, times 2^36; kNaN: a NaN or +infinity
   float max;
+  int count;                // candidates
 };
+constexpr unsigned long long kNaN = ~0ull;
 
 struct BeamParams {
   uint32_t* status;   // device status word: nothing can go wrong on the device
   const void* logits;
   const float* scores;
   const uint8_t* finished;
-  Cand* cands;        // [rows, slices, select]
+  unsigned long long* cands;   // [rows, slices, kKeep] keys (cand_key)
   SliceSum* sums;     // [rows, slices], slice 0 the row's first
   float* out_scores;
   int32_t* out_tokens;
   int32_t* out_parents;
   long long stride;   // elements between rows
-  long long units;    // tiles of all rows
-  int row_tiles, blocks;
+  unsigned per, extra;         // units of a block: per, one more in the first `extra`
+  int row_tiles;
   int batch, beams, vocab, select, slices, pad;
 };
 
-// Block c takes the units [run_begin(c), run_begin(c + 1)).
-__host__ __device__ __forceinline__ long long run_begin(long long units, int blocks, int c) {
-  return units * c / blocks;
-}
-__device__ __forceinline__ int run_of(long long units, int blocks, long long u) {
-  return static_cast<int>(((u + 1) * blocks - 1) / units);
+// Block c takes the units (tiles of all rows) [run_begin(c), run_begin(c + 1)).
+__device__ __forceinline__ unsigned run_begin(const BeamParams& p, unsigned c) { return c * p.per + min(c, p.extra); }
+__device__ __forceinline__ unsigned run_of(const BeamParams& p, unsigned u) {
+  const unsigned head = p.extra * (p.per + 1);
+  return u < head ? u / (p.per + 1) : p.extra + (u - head) / p.per;
 }
 
 __device__ __forceinline__ float ex2_ftz(float x) {
@@ -79,10 +86,29 @@ __device__ __forceinline__ float ex2_ftz(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// exp(x) for x <= 0: log2(e) in two parts, so that its own rounding does not
-// bias the sum (one part: 1.3e-8 of x, the same sign for every term)
-constexpr float kLog2eHi = 1.44269502e0f, kLog2eLo = 1.92596303e-8f;
-__device__ __forceinline__ float exp_neg(float x) { return ex2_ftz(fmaf(x, kLog2eHi, x * kLog2eLo)); }
+constexpr float kLog2e = 1.44269502e0f;           // H
+constexpr double kLog2eRest = 1.925963033e-8;     // log2(e) - H
+// Up to this size of a maximum its c is an exact integer that cancels it to
+// about 1; rows beyond (masked with the type's lowest value throughout) take
+// the differences from it instead.
+constexpr float kFar = 1e7f;
+__device__ __forceinline__ float exp_neg(float x) { return ex2_ftz(x * kLog2e); }
+__device__ __forceinline__ float offset_of(float m) { return -rintf(m * kLog2e); }   // c
+// 2^n for an integer n <= 0 (0 from 2^-126 down)
+__device__ __forceinline__ float pow2_int(float n) {
+  return n > -126.f ? __int_as_float((static_cast<int>(n) + 127) << 23) : 0.f;
+}
+// What joins a sum at maximum m to one at maximum `to`.
+__device__ __forceinline__ float join_factor(float m, float to) {
+  if (!(m > -INFINITY)) return 0.f;
+  if (m == to) return 1.f;
+  if (fabsf(m) <= kFar && fabsf(to) <= kFar) return pow2_int(offset_of(to) - offset_of(m));
+  // (a far sum's terms are relative to its maximum, a near one's to its c)
+  float f = exp_neg(m - to);
+  if (fabsf(m) <= kFar) f *= ex2_ftz(-fmaf(m, kLog2e, offset_of(m)));
+  if (fabsf(to) <= kFar) f *= ex2_ftz(fmaf(to, kLog2e, offset_of(to)));
+  return f;
+}
 
 // A row candidate as one key: larger value first, then the lower token.
 __device__ __forceinline__ unsigned long long cand_key(float v, int token) {
@@ -103,63 +129,47 @@ __device__ __forceinline__ bool above(const unsigned long long& a, const unsigne
 __device__ __forceinline__ bool above(const Total& a, const Total& b) {
   return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
 }
-__device__ __forceinline__ unsigned long long shfl_xor(unsigned long long k, int m) {
-  return __shfl_xor_sync(0xffffffffu, k, m);
-}
-__device__ __forceinline__ Total shfl_xor(const Total& k, int m) {
-  return Total{__shfl_xor_sync(0xffffffffu, k.hi, m), __shfl_xor_sync(0xffffffffu, k.lo, m)};
-}
-
-// Sorts keys of the block's first `size` threads (a power of two; what the
-// others hold is not looked at), largest in thread 0. Bitonic; the exchanges
-// beyond a warp go through `buf`. Up to 32 keys stay in the first warp.
+// Puts the best `k` of list[0..n) into out[0..k), largest first, by counting
+// for every key those above it; places that have no key get `none`. n is at
+// most kBmThreads, the keys are distinct. The whole block calls it after a
+// barrier that completes the list; `rank` is kBmThreads ints, out is not list.
 template <typename K>
-__device__ __forceinline__ K block_sort(K key, K* buf, int size) {
+__device__ void rank_best(K* out, const K* list, int n, int k, K none, int* rank) {
   const int t = threadIdx.x;
-#pragma unroll 1
-  for (int run = 2; run <= size; run <<= 1) {
-    const bool down = (t & run) == 0;   // this run sorts largest first
-#pragma unroll 1
-    for (int m = run >> 1; m > 0; m >>= 1) {
-      K other;
-      if (m >= 32) {
-        __syncthreads();
-        buf[t] = key;
-        __syncthreads();
-        other = buf[t ^ m];
-      } else {
-        if (t >= size && size <= 32) break;
-        other = shfl_xor(key, m);
-      }
-      const bool first = (t & m) == 0;
-      const bool take_max = first == down;
-      if (above(other, key) == take_max) key = other;
-    }
-  }
-  return key;
-}
-
-// Sorts the best `k` of top[0..k) and list[0..n) into top, largest first.
-// `none` fills places that have no key. The whole block calls it; `fresh`:
-// top holds nothing yet.
-template <typename K>
-__device__ void drain(K* top, const K* list, int n, int k, K none, K* buf, bool fresh) {
-  const int t = threadIdx.x;
+  int width = 32;                       // keys side by side; the rest of the block shares the counting
+  while (width < n) width <<= 1;
+  const int parts = kBmThreads / width, part = t / width, i = t & (width - 1);
+  rank[t] = 0;
+  if (t < k) out[t] = none;
   __syncthreads();
-  for (int at = 0; at < n || fresh;) {
-    const int have = fresh ? 0 : k;
-    const int i = at + t - have;
-    const int here = have + min(n - at, kBmThreads - have);
-    int size = 32;
-    while (size < here || size < k) size <<= 1;
-    K key = t < have ? top[t] : (i < n && t < here ? list[i] : none);
-    if (size > 32 || t < 32) key = block_sort(key, buf, size);
-    __syncthreads();
-    if (t < k) top[t] = t < size ? key : none;
-    __syncthreads();
-    at += kBmThreads - have;
-    fresh = false;
+  if (i < n) {
+    const K key = list[i];
+    int above_it = 0;
+    const int step = (n + parts - 1) / parts, end = min(n, (part + 1) * step);
+    for (int j = part * step; j < end; ++j) above_it += above(list[j], key) ? 1 : 0;
+    if (above_it) atomicAdd(&rank[i], above_it);
   }
+  __syncthreads();
+  if (t < n && rank[t] < k) out[rank[t]] = list[t];
+  __syncthreads();
+}
+
+// Cuts list[0..n) to its best `k`, in order, at its front, kBmThreads at a
+// time through `buf` (kBmThreads keys). Returns how many there are.
+template <typename K>
+__device__ int cut_list(K* list, int n, int k, K none, K* buf, int* rank) {
+  const int t = threadIdx.x;
+  int have = 0;
+  for (int at = 0; at < n;) {
+    const int here = min(n - at, kBmThreads - have);
+    if (t < have) buf[t] = list[t];
+    else if (t < have + here) buf[t] = list[at + t - have];
+    __syncthreads();
+    at += here;
+    rank_best(list, buf, have + here, k, none, rank);
+    have = min(k, have + here);
+  }
+  return have;
 }
 
 // The j-th largest of the warp's keys (0 if it has fewer than j that are not 0).
@@ -184,14 +194,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// Two exp(x) for x <= 0, as exp_neg.
-__device__ __forceinline__ float2 exp_neg2(float2 x) {
-  const float2 zero = make_float2(0.f, 0.f);
-  const float2 lo = fma_f32x2(x, make_float2(kLog2eLo, kLog2eLo), zero);
-  const float2 y = fma_f32x2(x, make_float2(kLog2eHi, kLog2eHi), lo);
-  return make_float2(ex2_ftz(y.x), ex2_ftz(y.y));
-}
-
 // The four bytes of two 16-bit values, or one fp32 value, as floats.
 template <typename T>
 __device__ __forceinline__ float2 two_of(const uint32_t* w, int i);
@@ -208,179 +210,218 @@ __device__ __forceinline__ float2 two_of<float>(const uint32_t* w, int i) {
   return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
 }
 
+// A tile's values and what the list may hold before it.
+template <typename T>
+constexpr int kListKeys = kTileVecs * (16 / static_cast<int>(sizeof(T))) + kDrain;
+
+// The largest of a thread's values (a NaN is passed over).
+template <typename T>
+__device__ __forceinline__ float top_of(const uint4* v) {
+  if constexpr (sizeof(T) == 4) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      top = fmaxf(top, fmaxf(fmaxf(__uint_as_float(v[i].x), __uint_as_float(v[i].y)),
+                             fmaxf(__uint_as_float(v[i].z), __uint_as_float(v[i].w))));
+    return top;
+  } else {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    T2 top = *reinterpret_cast<const T2*>(&v[0].x);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = __hmax2(top, *reinterpret_cast<const T2*>(w + e));
+    }
+    const float2 f = two_of<T>(reinterpret_cast<const uint32_t*>(&top), 0);
+    return fmaxf(fmaxf(f.x, f.y), -INFINITY);   // NaN: -infinity
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const BeamParams p) {
   constexpr int VE = 16 / sizeof(T);
   constexpr int kPairs = VE / 2;
-  constexpr int kList = kTileVecs * VE + kDrain;
-  __shared__ unsigned long long s_list[kList];
-  __shared__ unsigned long long s_top[DSA_MAX_SELECT];
+  extern __shared__ unsigned long long s_list[];   // kListKeys<T>
   __shared__ unsigned long long s_buf[kBmThreads];
+  __shared__ int s_rank[kBmThreads];
   __shared__ uint32_t s_bound[2][kBmWarps];
-  __shared__ int s_count;
-  __shared__ double s_sum[kBmWarps];
+  __shared__ int s_count, s_kept;
+  __shared__ unsigned long long s_sum[kBmWarps];
   __shared__ float s_max[kBmWarps];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int k = p.select, nth = (k + kBmWarps - 1) / kBmWarps;
   pdl_trigger();
-  const long long u_end = run_begin(p.units, p.blocks, blockIdx.x + 1);
-  for (long long u = run_begin(p.units, p.blocks, blockIdx.x); u < u_end;) {
-    const int row = static_cast<int>(u / p.row_tiles);
-    const int t0 = static_cast<int>(u - static_cast<long long>(row) * p.row_tiles);
-    const int t1 = static_cast<int>(min(static_cast<long long>(p.row_tiles), t0 + (u_end - u)));
+  const unsigned u_end = run_begin(p, blockIdx.x + 1);
+  for (unsigned u = run_begin(p, blockIdx.x); u < u_end;) {
+    const int row = static_cast<int>(u / static_cast<unsigned>(p.row_tiles));
+    const int t0 = static_cast<int>(u - static_cast<unsigned>(row) * p.row_tiles);
+    const int t1 = static_cast<int>(min(static_cast<unsigned>(p.row_tiles), t0 + (u_end - u)));
     u += t1 - t0;
     if (p.finished && p.finished[row]) continue;   // the merge knows its one continuation
     const T* x0 = static_cast<const T*>(p.logits) + static_cast<long long>(row) * p.stride;
     // 16-byte vectors from the aligned address at or before the row's first element
     const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(x0) & 15) / sizeof(T));
-    const int v_end = t1 * kTileVecs;              // (vectors past the row read as masked)
 
     const auto load = [&](int v) {
       const int e0 = v * VE - mis;
       uint4 r;
-      if (v < v_end && e0 >= 0 && e0 + VE <= p.vocab) {
+      if (e0 >= 0 && e0 + VE <= p.vocab) {
         r = __ldcs(reinterpret_cast<const uint4*>(x0 + e0));
       } else {
         alignas(16) T out[VE];
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const bool in = v < v_end && e0 + e >= 0 && e0 + e < p.vocab;
-          out[e] = in ? x0[e0 + e] : T(-INFINITY);
-        }
+        for (int e = 0; e < VE; ++e) out[e] = e0 + e >= 0 && e0 + e < p.vocab ? x0[e0 + e] : T(-INFINITY);
         r = *reinterpret_cast<const uint4*>(out);
       }
       return r;
     };
 
-    float m = -INFINITY;                 // this thread's maximum
-    float2 sum = make_float2(0.f, 0.f);  // and its sum of exp(x - m)
+    float m = -INFINITY, c = 0.f;        // this thread's maximum, and its offset
+    float2 sum = make_float2(0.f, 0.f);  // its sum
     float thr = -INFINITY, past = -INFINITY;   // candidates are >= thr and > past
-    bool fresh = true;
     uint4 cur[kVecs], nxt[kVecs];
+    // a warp takes every eighth run of four vectors (64 bytes) of 256, so that a
+    // tile that the row fills only in part still gives every warp its share and
+    // the warps' bounds stay alike
+    const int own_vec = (lane >> 2) * 32 + wid * 4 + (lane & 3);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) cur[i] = load(t0 * kTileVecs + i * kBmThreads + tid);
+    for (int i = 0; i < kVecs; ++i) cur[i] = load(t0 * kTileVecs + i * kBmThreads + own_vec);
     if (tid == 0) s_count = 0;
     for (int t = t0; t < t1; ++t) {
       const int v0 = t * kTileVecs;
       if (t + 1 < t1) {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) nxt[i] = load(v0 + kTileVecs + i * kBmThreads + tid);
+        for (int i = 0; i < kVecs; ++i) nxt[i] = load(v0 + kTileVecs + i * kBmThreads + own_vec);
       }
-      float2 x[kVecs][kPairs];
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
-#pragma unroll
-        for (int e = 0; e < kPairs; ++e) {
-          x[i][e] = two_of<T>(w, e);
-          top = fmaxf(top, fmaxf(x[i][e].x, x[i][e].y));
-        }
-      }
+      const float top = top_of<T>(cur);
       if (top > m) {
-        const float f = exp_neg(m - top);   // the first time: 0 * exp(-inf)
+        const float f = join_factor(m, top);   // (0 * 0 keeps a NaN)
         sum.x *= f;
         sum.y *= f;
         m = top;
+        c = offset_of(m);
       }
-      if (m > -INFINITY) {
-        const float2 neg = make_float2(-m, -m);
+      if (fabsf(m) <= kFar) {
+        const float2 h2 = make_float2(kLog2e, kLog2e), c2 = make_float2(c, c);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i)
+        for (int i = 0; i < kVecs; ++i) {
+          const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
 #pragma unroll
-          for (int e = 0; e < kPairs; ++e) sum = add2(sum, exp_neg2(add2(x[i][e], neg)));
+          for (int e = 0; e < kPairs; ++e) {
+            const float2 y = fma_f32x2(two_of<T>(w, e), h2, c2);
+            sum = add2(sum, make_float2(ex2_ftz(y.x), ex2_ftz(y.y)));
+          }
+        }
       } else {
+        // a far maximum, or nothing but -infinity (and NaN) so far
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i)
+        for (int i = 0; i < kVecs; ++i) {
+          const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
 #pragma unroll
-          for (int e = 0; e < kPairs; ++e)
-            if (x[i][e].x != x[i][e].x || x[i][e].y != x[i][e].y) sum.x = NAN;   // among masked tokens
+          for (int e = 0; e < kPairs; ++e) {
+            const float2 x = two_of<T>(w, e);
+            if (m > -INFINITY) sum = add2(sum, make_float2(exp_neg(x.x - m), exp_neg(x.y - m)));
+            else if (x.x != x.x || x.y != x.y) sum.x = NAN;
+          }
+        }
       }
-      // the bound so far; the first tile's is needed at once, later ones may lag
-      const uint32_t bound = warp_jth(float_key(m), nth);
-      if (lane == 0) s_bound[t & 1][wid] = bound;
+      // the bound so far: the first tile's is needed at once; it is renewed
+      // where it still moves, and may lag a tile
+      const int done = t - t0;
+      const bool renew = done < 4 || (done & 3) == 0;
+      if (renew) {
+        const uint32_t bound = warp_jth(float_key(m), nth);
+        if (lane == 0) s_bound[t & 1][wid] = bound;
+      }
       const auto join = [&] {
         uint32_t b = s_bound[t & 1][0];
 #pragma unroll
         for (int i = 1; i < kBmWarps; ++i) b = min(b, s_bound[t & 1][i]);
         if (b != 0u) thr = key_value(static_cast<unsigned long long>(b) << 32);
       };
-      if (t == t0) {
+      if (done == 0) {
         __syncthreads();
         join();
       }
-      // append what reaches it
-      uint32_t hits = 0;
-      if (top >= thr) {
+      // append what reaches it (few: the value is read again)
+      bool full = false;
+      if (top >= thr && top > past) {
+        uint32_t hits = 0;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i)
+        for (int i = 0; i < kVecs; ++i) {
+          const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
 #pragma unroll
           for (int e = 0; e < kPairs; ++e) {
-            if (x[i][e].x >= thr && x[i][e].x > past) hits |= 1u << (i * VE + 2 * e);
-            if (x[i][e].y >= thr && x[i][e].y > past) hits |= 2u << (i * VE + 2 * e);
+            const float2 x = two_of<T>(w, e);
+            if (x.x >= thr && x.x > past) hits |= 1u << (i * VE + 2 * e);
+            if (x.y >= thr && x.y > past) hits |= 2u << (i * VE + 2 * e);
           }
-      }
-      bool full = false;
-      if (__any_sync(0xffffffffu, hits != 0)) {
-        const int n = __popc(hits);
-        int before = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, before, o);
-          if (lane >= o) before += y;
         }
-        int at = 0;
-        if (lane == 31) at = atomicAdd(&s_count, before);
-        at = __shfl_sync(0xffffffffu, at, 31) + before - n;
-        full = at + n > kDrain;
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-#pragma unroll
-          for (int e = 0; e < VE; ++e)
-            if (hits & (1u << (i * VE + e)))
-              s_list[at++] = cand_key((e & 1) ? x[i][e >> 1].y : x[i][e >> 1].x,
-                                      (v0 + i * kBmThreads + tid) * VE - mis + e);
+        int at = atomicAdd(&s_count, __popc(hits));
+        while (hits) {
+          const int bit = __ffs(hits) - 1;
+          hits &= hits - 1;
+          const int token = (v0 + (bit / VE) * kBmThreads + own_vec) * VE - mis + (bit % VE);
+          s_list[at++] = cand_key(static_cast<float>(x0[token]), token);
+        }
+        full = at > kDrain;
       }
       if (__syncthreads_or(full)) {
-        const int n = s_count;
-        drain(s_top, s_list, n, k, 0ull, s_buf, fresh);
-        fresh = false;
-        if (tid == 0) s_count = 0;
+        const int n = cut_list(s_list, s_count, k, 0ull, s_buf, s_rank);
+        if (tid == 0) s_count = n;
         // what comes later in the row has higher tokens: equal is not enough
-        if (s_top[k - 1] != 0ull) past = key_value(s_top[k - 1]);
+        if (n == k) past = key_value(s_list[k - 1]);
         __syncthreads();
       }
-      join();
+      if (renew) join();
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) cur[i] = nxt[i];
     }
-    drain(s_top, s_list, s_count, k, 0ull, s_buf, fresh);
-    // join the threads' sums
+    // hand on what the bound has not overtaken (n <= kDrain: one key a thread)
+    const int n = s_count;
+    const unsigned long long key = tid < n ? s_list[tid] : 0ull;
+    const bool keep = tid < n && key_value(key) >= thr;
+    // the threads' sums join meanwhile
     float mm = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
     if (lane == 0) s_max[wid] = mm;
+    if (tid == 0) s_kept = 0;
     __syncthreads();
+    const uint32_t kept = __ballot_sync(0xffffffffu, keep);
+    int at = 0;
+    if (lane == 0 && kept) at = atomicAdd(&s_kept, __popc(kept));
+    at = __shfl_sync(0xffffffffu, at, 0) + __popc(kept & ((1u << lane) - 1u));
     mm = s_max[0];
 #pragma unroll
     for (int i = 1; i < kBmWarps; ++i) mm = fmaxf(mm, s_max[i]);
-    // (a thread that saw nothing but -infinity adds its 0, or its NaN)
-    const float own = sum.x + sum.y;
-    double d = static_cast<double>(m > -INFINITY ? own * exp_neg(m - mm) : own);
+    const float own = sum.x + sum.y;     // 0 (or a NaN) where nothing but -infinity was seen
+    // (a thread's maximum may be +infinity, its sum is a NaN then)
+    const bool bad = !(own < INFINITY);
+    unsigned long long fixed =
+        bad ? 0ull : static_cast<unsigned long long>(own * join_factor(m, mm) * 0x1p36f);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) s_sum[wid] = d;
-    __syncthreads();
-    const int slice = blockIdx.x - run_of(p.units, p.blocks, static_cast<long long>(row) * p.row_tiles);
-    const long long at = static_cast<long long>(row) * p.slices + slice;
-    if (tid == 0) {
-      d = 0.0;
-      for (int i = 0; i < kBmWarps; ++i) d += s_sum[i];
-      p.sums[at] = SliceSum{d, mm};
+    for (int o = 16; o > 0; o >>= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
+    if (lane == 0) s_sum[wid] = fixed;
+    const bool poison = __syncthreads_or(bad);
+    const unsigned slice = blockIdx.x - run_of(p, static_cast<unsigned>(row) * p.row_tiles);
+    const long long to = static_cast<long long>(row) * p.slices + slice;
+    unsigned long long* out = p.cands + to * kKeep;
+    int handed = s_kept;
+    if (handed <= kKeep) {
+      if (keep) out[at] = key;
+    } else {
+      if (keep) s_buf[at] = key;
+      __syncthreads();
+      rank_best(s_list, s_buf, handed, k, 0ull, s_rank);
+      handed = k;
+      if (tid < k) out[tid] = s_list[tid];
     }
-    if (tid < k) {
-      const unsigned long long key = s_top[tid];
-      p.cands[at * k + tid] = key ? Cand{key_value(key), static_cast<int32_t>(~static_cast<uint32_t>(key))} : Cand{0.0f, -1};
+    if (tid == 0) {
+      fixed = 0ull;
+      for (int i = 0; i < kBmWarps; ++i) fixed += s_sum[i];
+      p.sums[to] = SliceSum{poison ? kNaN : fixed, mm, handed};
     }
     __syncthreads();   // (the next slice's lists)
   }
@@ -395,96 +436,118 @@ __device__ __forceinline__ double key_double(unsigned long long k) {
   return __longlong_as_double(static_cast<long long>((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
 }
 
+// One thread block per batch entry; its beams' slices are the lists
+// b * slices + j.
 __global__ void __launch_bounds__(kBmThreads) beam_merge_kernel(const BeamParams p) {
   __shared__ Total s_list[kMergeList];
   __shared__ Total s_buf[kBmThreads];
-  __shared__ Total s_top[DSA_MAX_SELECT];
-  __shared__ double s_off[DSA_MAX_BEAMS];   // score - log sum exp of each beam
-  __shared__ int s_slices[DSA_MAX_BEAMS];   // its slices (0: finished)
+  __shared__ Total s_best[DSA_MAX_SELECT];
+  __shared__ int s_rank[kBmThreads];
+  __shared__ SliceSum s_sum[kMaxLists];
+  __shared__ double s_off[DSA_MAX_BEAMS];   // score - log sum exp of each beam (a finished one: its score)
   __shared__ uint32_t s_bound[kBmWarps];
   __shared__ int s_count;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int row0 = blockIdx.x * p.beams;
   const int k = p.select;
   const Total none{0ull, 0u};
+  const int lists = p.beams * p.slices;
   if (tid == 0) s_count = 0;
   pdl_wait();
   if (blockIdx.x == 0 && tid == 0) *p.status = 0u;
-  for (int b = wid; b < p.beams; b += kBmThreads / 32) {
-    const int row = row0 + b;
-    const bool over = p.finished && p.finished[row];
-    const long long u = static_cast<long long>(row) * p.row_tiles;
-    const int slices = over ? 0 : run_of(p.units, p.blocks, u + p.row_tiles - 1) - run_of(p.units, p.blocks, u) + 1;
-    if (lane == 0) s_slices[b] = slices;
-    if (over) continue;
-    const SliceSum* s = p.sums + static_cast<long long>(row) * p.slices;
-    float mm = -INFINITY;
-    for (int i = lane; i < slices; i += 32) mm = fmaxf(mm, s[i].max);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    double d = 0.0;
-    for (int i = lane; i < slices; i += 32) {
-      const double v = s[i].sum;
-      // (0 from a slice of masked tokens only: its maximum has no exponential)
-      if (v != 0.0) d += s[i].max > -INFINITY ? v * exp(static_cast<double>(s[i].max) - mm) : v;
+  // the slices there are; a finished beam's only list holds pad_token
+  for (int i = tid; i < lists; i += kBmThreads) {
+    const int b = i / p.slices, j = i - b * p.slices, row = row0 + b;
+    SliceSum s{0ull, -INFINITY, 0};
+    if (p.finished && p.finished[row]) {
+      if (j == 0) s.count = 1;
+    } else {
+      const unsigned u = static_cast<unsigned>(row) * p.row_tiles;
+      if (j <= static_cast<int>(run_of(p, u + p.row_tiles - 1) - run_of(p, u)))
+        s = p.sums[static_cast<long long>(row0) * p.slices + i];
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) s_off[b] = static_cast<double>(p.scores[row]) - (static_cast<double>(mm) + log(d));
+    s_sum[i] = s;
   }
   __syncthreads();
-  // candidate i of the entry's beams x slices x select (finished beams: one)
-  const int per_row = p.slices * k, n = p.beams * per_row;
-  const auto total = [&](int i) {
-    const int b = i / per_row, j = i - b * per_row;
+  for (int b = tid; b < p.beams; b += kBmThreads) {
     const int row = row0 + b;
-    double t;
-    int token;
-    if (s_slices[b] == 0) {
-      if (j > 0) return none;
-      t = p.scores[row];
-      token = p.pad;
-    } else {
-      if (j >= s_slices[b] * k) return none;
-      const Cand c = p.cands[static_cast<long long>(row) * per_row + j];
-      if (c.token < 0) return none;
-      t = static_cast<double>(c.value) + s_off[b];
-      token = c.token;
+    double off = p.scores[row];
+    if (!(p.finished && p.finished[row])) {
+      const SliceSum* s = s_sum + b * p.slices;
+      float mm = -INFINITY;
+      bool bad = false;
+      for (int j = 0; j < p.slices; ++j) {
+        mm = fmaxf(mm, s[j].max);
+        bad = bad || s[j].sum == kNaN;
+      }
+      unsigned long long sum = 0ull;
+      for (int j = 0; j < p.slices; ++j)
+        if (s[j].max == mm) sum += s[j].sum;
+        else if (s[j].max > -INFINITY)
+          sum += static_cast<unsigned long long>(static_cast<double>(s[j].sum) * join_factor(s[j].max, mm));
+      // log sum = max-relative sum, and H's part undone at the maximum
+      const double ln2 = 0.6931471805599453;
+      const double base = fabsf(mm) <= kFar ? ln2 * (mm * kLog2eRest - static_cast<double>(offset_of(mm))) : static_cast<double>(mm);
+      off -= bad ? NAN : base + log(static_cast<double>(sum) * 0x1p-36);
     }
-    if (!(t > -INFINITY)) return none;   // -infinity or NaN
-    return Total{double_key(t), ~static_cast<uint32_t>(b * p.vocab + token)};
-  };
-  // a bound as in the scan, in fp32 rounded down (which keeps the order)
-  const auto key32 = [&](const Total& t) { return t.hi ? float_key(__double2float_rd(key_double(t.hi))) : 0u; };
+    s_off[b] = off;
+  }
+  __syncthreads();
+  // A lane takes a list, a warp every eighth of its candidates (beams may be far
+  // apart: this way the warps' shares are alike, and so are their bounds).
+  const unsigned long long* cands = p.cands + static_cast<long long>(row0) * p.slices * kKeep;
   uint32_t best = 0u;
-  for (int i = tid; i < n; i += kBmThreads) best = max(best, key32(total(i)));
+  for (int i = lane; i < lists; i += 32) {
+    const int b = i / p.slices, n = s_sum[i].count;
+    const float off = __double2float_rd(s_off[b]);
+    const bool over = p.finished && p.finished[row0 + b];
+    float top = -INFINITY;
+#pragma unroll 4
+    for (int j = wid; j < n; j += kBmWarps) top = fmaxf(top, over ? 0.f : key_value(cands[i * kKeep + j]));
+    const float t = over ? (n > 0 && wid == 0 ? off : -INFINITY) : __fadd_rd(top, off);
+    if (t > -INFINITY) best = max(best, float_key(t));   // (not for a NaN)
+  }
   best = warp_jth(best, (k + kBmWarps - 1) / kBmWarps);
   if (lane == 0) s_bound[wid] = best;
   __syncthreads();
   best = s_bound[0];
 #pragma unroll
   for (int i = 1; i < kBmWarps; ++i) best = min(best, s_bound[i]);
-  bool fresh = true;
-  for (int i0 = 0; i0 < n; i0 += kBmThreads) {
-    const int i = i0 + tid;
-    const Total t = i < n ? total(i) : none;
-    const bool hit = t.hi != 0ull && key32(t) >= best;
-    const uint32_t hits = __ballot_sync(0xffffffffu, hit);
-    int at = 0;
-    if (lane == 0 && hits) at = atomicAdd(&s_count, __popc(hits));
-    at = __shfl_sync(0xffffffffu, at, 0) + __popc(hits & ((1u << lane) - 1u));
-    if (hit) s_list[at] = t;
-    // room for the next round's?
-    if (__syncthreads_or(hit && at >= kMergeList - kBmThreads)) {
-      drain(s_top, s_list, s_count, k, none, s_buf, fresh);
-      fresh = false;
-      if (tid == 0) s_count = 0;
+  // the totals of those that may reach it, a round of kBmWarps lists at a time
+  const int rounds = (lists + kBmWarps - 1) / kBmWarps;
+  for (int r = 0; r < rounds; ++r) {
+    const int i = r * kBmWarps + wid;
+    const int b = i < lists ? i / p.slices : 0, n = i < lists ? s_sum[i].count : 0;
+    const double off = s_off[b];
+    const float off_up = __double2float_ru(off);
+    const bool over = p.finished && p.finished[row0 + b];
+    bool full = false;
+#pragma unroll
+    for (int j0 = 0; j0 < kKeep; j0 += 32) {
+      const int j = j0 + lane;
+      if (j >= n) continue;
+      const unsigned long long key = over ? 0ull : cands[i * kKeep + j];
+      const float up = over ? off_up : __fadd_ru(key_value(key), off_up);
+      if (!(up > -INFINITY) || float_key(up) < best) continue;
+      const double t = over ? off : static_cast<double>(key_value(key)) + off;
+      if (!(t > -INFINITY)) continue;
+      const int token = over ? p.pad : static_cast<int32_t>(~static_cast<uint32_t>(key));
+      const int at = atomicAdd(&s_count, 1);
+      s_list[at] = Total{double_key(t), ~static_cast<uint32_t>(b * p.vocab + token)};
+      full = full || at >= DSA_MAX_SELECT;
+    }
+    // make room for the next round
+    if (__syncthreads_or(full) && r + 1 < rounds) {
+      const int have = cut_list(s_list, s_count, k, none, s_buf, s_rank);
+      if (tid == 0) s_count = have;
       __syncthreads();
     }
   }
-  drain(s_top, s_list, s_count, k, none, s_buf, fresh);
+  const int n = s_count;
+  if (n > kBmThreads) cut_list(s_list, n, k, none, s_buf, s_rank);
+  else rank_best(s_best, s_list, n, k, none, s_rank);
   if (tid < k) {
-    const Total t = s_top[tid];
+    const Total t = n > kBmThreads ? s_list[tid] : s_best[tid];
     const long long o = static_cast<long long>(blockIdx.x) * k + tid;
     const uint32_t place = ~t.lo;
     const bool got = t.hi != 0ull;
@@ -519,46 +582,48 @@ size_t up(size_t x) { return (x + 255) & ~size_t(255); }
 
 // How the rows are cut: tiles per row, blocks (as many as are resident at
 // once), slices a row may have.
+int most_slices(const dsa_beam_problem* p) { return std::max(2, kMaxLists / p->beams); }
 struct Cut {
   long long units;
   int row_tiles, blocks, slices;
 };
-Cut cut(const dsa_beam_problem* p, int sms) {
+Cut cut(const dsa_beam_problem* p, int sms, bool base_aligned) {
   Cut c;
   const int ve = p->logits_dtype == DSA_FP32 ? 4 : 8;
-  const long long vecs = (p->vocab + 2LL * ve - 2) / ve;   // whatever the row's alignment
+  // a row that does not begin on 16 bytes may take a vector more
+  const bool even = base_aligned && p->row_stride % ve == 0 && (p->row_stride != 0 || p->vocab % ve == 0);
+  const long long vecs = (p->vocab + ve - 1LL + (even ? 0 : ve - 1)) / ve;
   c.row_tiles = static_cast<int>((vecs + kTileVecs - 1) / kTileVecs);
   const long long rows = static_cast<long long>(p->batch) * p->beams;
   c.units = rows * c.row_tiles;
   // a run of `per` tiles cuts a row into at most (row_tiles - 2) / per + 2
-  // slices; their candidates stay within kMaxCands per batch entry
-  const long long most = std::max(2, kMaxCands / (p->beams * p->select));
-  long long blocks = std::min<long long>(c.units, static_cast<long long>(sms) * kResident);
+  // slices; a batch entry has at most kMaxLists
   const auto slices = [&](long long n) {
     const long long per = c.units / n;
     return c.row_tiles == 1 ? 1LL : (c.row_tiles - 2) / per + 2;
   };
-  while (blocks > rows && slices(blocks) > most) blocks = std::max(rows, blocks * 7 / 8);
+  long long blocks = std::min<long long>(c.units, static_cast<long long>(sms) * kResident);
+  while (blocks > rows && slices(blocks) > most_slices(p)) blocks = std::max(rows, blocks * 7 / 8);
   c.blocks = static_cast<int>(blocks);
   c.slices = static_cast<int>(slices(blocks));
   return c;
 }
 
 size_t beam_bytes(const dsa_beam_problem* p, size_t* sums_at) {
-  // the most slices any number of blocks leads to: one per tile of a row, no
-  // more than the candidates allow, two where there is a block per row
-  const int tiles = cut(p, 1).row_tiles;
-  const int slices = std::min(tiles, std::max(2, kMaxCands / (p->beams * p->select)));
+  // the most slices any number of blocks leads to
+  const int slices = std::min(cut(p, 1, false).row_tiles, most_slices(p));
   const size_t n = static_cast<size_t>(p->batch) * p->beams * slices;
-  const size_t c = 256 + up(n * p->select * sizeof(Cand));
+  const size_t c = 256 + up(n * kKeep * sizeof(unsigned long long));
   if (sums_at) *sums_at = c;
   return c + up(n * sizeof(SliceSum));
 }
 
 template <typename T>
-cudaError_t launch_scan(const BeamParams& p, cudaStream_t s) {
-  return launch_kernel("beam_scan_kernel", beam_scan_kernel<T>, dim3(p.blocks), dim3(kBmThreads),
-                       0, s, false, p);
+cudaError_t launch_scan(const BeamParams& p, int blocks, cudaStream_t s) {
+  constexpr int smem = kListKeys<T> * 8;
+  const cudaError_t e = set_max_smem(reinterpret_cast<const void*>(beam_scan_kernel<T>), smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel("beam_scan_kernel", beam_scan_kernel<T>, dim3(blocks), dim3(kBmThreads), smem, s, false, p);
 }
 
 }  // namespace
@@ -593,7 +658,7 @@ extern "C" int dsa_beam_select(const dsa_beam_problem* bp, const void* logits, c
   p.logits = logits;
   p.scores = scores;
   p.finished = finished;
-  p.cands = reinterpret_cast<Cand*>(static_cast<uint8_t*>(ws) + 256);
+  p.cands = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(ws) + 256);
   p.sums = reinterpret_cast<SliceSum*>(static_cast<uint8_t*>(ws) + sums_at);
   p.out_scores = out_scores;
   p.out_tokens = out_tokens;
@@ -604,14 +669,14 @@ extern "C" int dsa_beam_select(const dsa_beam_problem* bp, const void* logits, c
   p.select = bp->select;
   p.pad = bp->pad_token;
   p.stride = bp->row_stride ? bp->row_stride : bp->vocab;
-  const Cut c = cut(bp, sms);
-  p.units = c.units;
+  const Cut c = cut(bp, sms, (reinterpret_cast<uintptr_t>(logits) & 15) == 0);
+  p.per = static_cast<unsigned>(c.units / c.blocks);
+  p.extra = static_cast<unsigned>(c.units % c.blocks);
   p.row_tiles = c.row_tiles;
-  p.blocks = c.blocks;
   p.slices = c.slices;
-  cudaError_t e = bp->logits_dtype == DSA_FP32   ? launch_scan<float>(p, s)
-                  : bp->logits_dtype == DSA_FP16 ? launch_scan<__half>(p, s)
-                                                 : launch_scan<__nv_bfloat16>(p, s);
+  cudaError_t e = bp->logits_dtype == DSA_FP32   ? launch_scan<float>(p, c.blocks, s)
+                  : bp->logits_dtype == DSA_FP16 ? launch_scan<__half>(p, c.blocks, s)
+                                                 : launch_scan<__nv_bfloat16>(p, c.blocks, s);
   if (e == cudaSuccess)
     e = launch_kernel("beam_merge_kernel", beam_merge_kernel, dim3(bp->batch), dim3(kBmThreads), 0, s, true, p);
   if (e != cudaSuccess) return report_errorf(DSA_ERR_CUDA, "beam_select launch: %s", cudaGetErrorString(e));
