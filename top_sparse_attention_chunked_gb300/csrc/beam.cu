@@ -47,8 +47,11 @@ constexpr int kVecs = 4;            // 16-byte vectors a thread takes per tile
 constexpr int kTileVecs = kBmThreads * kVecs;
 constexpr int kKeep = 128;          // candidates a slice may hand on
 constexpr int kDrain = 256;         // list entries that are cut to the best at once
+constexpr int kGroup = 2;           // tiles between two looks at the list's length
+constexpr int kMergeThreads = 1024;
+constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMaxLists = 512;      // slices of one batch entry
-constexpr int kMergeList = kBmWarps * kKeep + DSA_MAX_SELECT;   // the merge's list: a round's candidates and the best before
+constexpr int kMergeList = kMergeWarps * kKeep;   // candidates of one round of the merge
 constexpr int kResident = 3;        // scan blocks per SM (70 KB of shared memory each for 16-bit logits)
 
 struct SliceSum {
@@ -119,6 +122,12 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
 
+// The next value above a finite one (the smallest positive one above either 0).
+__device__ __forceinline__ float next_above(float x) {
+  const uint32_t k = float_key(x);
+  return key_value(static_cast<unsigned long long>(k == 0x7ffffffeu ? 0x80000000u : k + 1u) << 32);
+}
+
 // A total with its place: larger total first, then the lower place. hi = 0:
 // none.
 struct Total {
@@ -131,15 +140,16 @@ __device__ __forceinline__ bool above(const Total& a, const Total& b) {
 }
 // Puts the best `k` of list[0..n) into out[0..k), largest first, by counting
 // for every key those above it; places that have no key get `none`. n is at
-// most kBmThreads, the keys are distinct. The whole block calls it after a
-// barrier that completes the list; `rank` is kBmThreads ints, out is not list.
-template <typename K>
+// most kBmThreads, the keys are distinct. A whole block of NT threads calls it
+// after a barrier that completes the list; `rank` is kBmThreads ints, out is
+// not list.
+template <int NT, typename K>
 __device__ void rank_best(K* out, const K* list, int n, int k, K none, int* rank) {
   const int t = threadIdx.x;
   int width = 32;                       // keys side by side; the rest of the block shares the counting
   while (width < n) width <<= 1;
-  const int parts = kBmThreads / width, part = t / width, i = t & (width - 1);
-  rank[t] = 0;
+  const int parts = NT / width, part = t / width, i = t & (width - 1);
+  if (t < kBmThreads) rank[t] = 0;
   if (t < k) out[t] = none;
   __syncthreads();
   if (i < n) {
@@ -154,19 +164,19 @@ __device__ void rank_best(K* out, const K* list, int n, int k, K none, int* rank
   __syncthreads();
 }
 
-// Cuts list[0..n) to its best `k`, in order, at its front, kBmThreads at a
-// time through `buf` (kBmThreads keys). Returns how many there are.
-template <typename K>
-__device__ int cut_list(K* list, int n, int k, K none, K* buf, int* rank) {
+// Puts the best `k` of the n keys get(0) .. get(n - 1) into best[0..k), in
+// order, kBmThreads at a time through `buf`. Returns how many there are.
+template <int NT, typename K, class F>
+__device__ int cut_to_best(K* best, F&& get, int n, int k, K none, K* buf, int* rank) {
   const int t = threadIdx.x;
   int have = 0;
   for (int at = 0; at < n;) {
     const int here = min(n - at, kBmThreads - have);
-    if (t < have) buf[t] = list[t];
-    else if (t < have + here) buf[t] = list[at + t - have];
+    if (t < have) buf[t] = best[t];
+    else if (t < have + here) buf[t] = get(at + t - have);
     __syncthreads();
     at += here;
-    rank_best(list, buf, have + here, k, none, rank);
+    rank_best<NT>(best, buf, have + here, k, none, rank);
     have = min(k, have + here);
   }
   return have;
@@ -210,9 +220,9 @@ __device__ __forceinline__ float2 two_of<float>(const uint32_t* w, int i) {
   return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
 }
 
-// A tile's values and what the list may hold before it.
+// The list (of tokens): a group's values and what it may hold before it.
 template <typename T>
-constexpr int kListKeys = kTileVecs * (16 / static_cast<int>(sizeof(T))) + kDrain;
+constexpr int kListLen = kGroup * kTileVecs * (16 / static_cast<int>(sizeof(T))) + kDrain;
 
 // The largest of a thread's values (a NaN is passed over).
 template <typename T>
@@ -242,10 +252,10 @@ template <typename T>
 __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const BeamParams p) {
   constexpr int VE = 16 / sizeof(T);
   constexpr int kPairs = VE / 2;
-  extern __shared__ unsigned long long s_list[];   // kListKeys<T>
-  __shared__ unsigned long long s_buf[kBmThreads];
+  extern __shared__ int32_t s_list[];   // kListLen<T> tokens
+  __shared__ unsigned long long s_buf[kBmThreads], s_best[DSA_MAX_SELECT];
   __shared__ int s_rank[kBmThreads];
-  __shared__ uint32_t s_bound[2][kBmWarps];
+  __shared__ volatile uint32_t s_bound[kBmWarps];
   __shared__ int s_count, s_kept;
   __shared__ unsigned long long s_sum[kBmWarps];
   __shared__ float s_max[kBmWarps];
@@ -279,21 +289,18 @@ __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const 
 
     float m = -INFINITY, c = 0.f;        // this thread's maximum, and its offset
     float2 sum = make_float2(0.f, 0.f);  // its sum
-    float thr = -INFINITY, past = -INFINITY;   // candidates are >= thr and > past
-    uint4 cur[kVecs], nxt[kVecs];
+    float lim = key_value(1ull << 55);   // candidates are at least this (the smallest finite value to begin with)
     // a warp takes every eighth run of four vectors (64 bytes) of 256, so that a
     // tile that the row fills only in part still gives every warp its share and
     // the warps' bounds stay alike
     const int own_vec = (lane >> 2) * 32 + wid * 4 + (lane & 3);
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) cur[i] = load(t0 * kTileVecs + i * kBmThreads + own_vec);
     if (tid == 0) s_count = 0;
-    for (int t = t0; t < t1; ++t) {
-      const int v0 = t * kTileVecs;
-      if (t + 1 < t1) {
+    if (lane == 0) s_bound[wid] = 0u;
+    const auto fetch = [&](int t, uint4* v) {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) nxt[i] = load(v0 + kTileVecs + i * kBmThreads + own_vec);
-      }
+      for (int i = 0; i < kVecs; ++i) v[i] = load(t * kTileVecs + i * kBmThreads + own_vec);
+    };
+    const auto tile = [&](int t, const uint4* cur) {
       const float top = top_of<T>(cur);
       if (top > m) {
         const float f = join_factor(m, top);   // (0 * 0 keeps a NaN)
@@ -326,27 +333,20 @@ __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const 
           }
         }
       }
-      // the bound so far: the first tile's is needed at once; it is renewed
-      // where it still moves, and may lag a tile
+      // the bound so far; an older one of another warp is a bound as well, so
+      // only the first tile's has to be waited for
       const int done = t - t0;
-      const bool renew = done < 4 || (done & 3) == 0;
-      if (renew) {
+      if (done < 4 || (done & 3) == 0) {
         const uint32_t bound = warp_jth(float_key(m), nth);
-        if (lane == 0) s_bound[t & 1][wid] = bound;
-      }
-      const auto join = [&] {
-        uint32_t b = s_bound[t & 1][0];
+        if (lane == 0) s_bound[wid] = bound;
+        if (done == 0) __syncthreads();
+        uint32_t b = s_bound[0];
 #pragma unroll
-        for (int i = 1; i < kBmWarps; ++i) b = min(b, s_bound[t & 1][i]);
-        if (b != 0u) thr = key_value(static_cast<unsigned long long>(b) << 32);
-      };
-      if (done == 0) {
-        __syncthreads();
-        join();
+        for (int i = 1; i < kBmWarps; ++i) b = min(b, s_bound[i]);
+        if (b != 0u) lim = fmaxf(lim, key_value(static_cast<unsigned long long>(b) << 32));
       }
-      // append what reaches it (few: the value is read again)
-      bool full = false;
-      if (top >= thr && top > past) {
+      // append the places that reach it
+      if (top >= lim) {
         uint32_t hits = 0;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
@@ -354,33 +354,54 @@ __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const 
 #pragma unroll
           for (int e = 0; e < kPairs; ++e) {
             const float2 x = two_of<T>(w, e);
-            if (x.x >= thr && x.x > past) hits |= 1u << (i * VE + 2 * e);
-            if (x.y >= thr && x.y > past) hits |= 2u << (i * VE + 2 * e);
+            if (x.x >= lim) hits |= 1u << (i * VE + 2 * e);
+            if (x.y >= lim) hits |= 2u << (i * VE + 2 * e);
           }
         }
         int at = atomicAdd(&s_count, __popc(hits));
         while (hits) {
           const int bit = __ffs(hits) - 1;
           hits &= hits - 1;
-          const int token = (v0 + (bit / VE) * kBmThreads + own_vec) * VE - mis + (bit % VE);
-          s_list[at++] = cand_key(static_cast<float>(x0[token]), token);
+          s_list[at++] = (t * kTileVecs + (bit / VE) * kBmThreads + own_vec) * VE - mis + (bit % VE);
         }
-        full = at > kDrain;
       }
-      if (__syncthreads_or(full)) {
-        const int n = cut_list(s_list, s_count, k, 0ull, s_buf, s_rank);
-        if (tid == 0) s_count = n;
+    };
+    const auto key_at = [&](int i) {
+      const int token = s_list[i];
+      return cand_key(static_cast<float>(x0[token]), token);
+    };
+    uint4 va[kVecs], vb[kVecs];
+    fetch(t0, va);
+    __syncthreads();
+    static_assert(kGroup == 2, "a group is what the two buffers hold");
+    for (int t = t0; t < t1; t += kGroup) {
+      if (t + 1 < t1) fetch(t + 1, vb);
+      tile(t, va);
+      if (t + 2 < t1) fetch(t + 2, va);
+      if (t + 1 < t1) tile(t + 1, vb);
+      __syncthreads();
+      const int n = s_count;
+      __syncthreads();
+      if (n > kDrain) {
+        const int have = cut_to_best<kBmThreads>(s_best, key_at, n, k, 0ull, s_buf, s_rank);
+        if (tid < have) s_list[tid] = static_cast<int32_t>(~static_cast<uint32_t>(s_best[tid]));
+        if (tid == 0) s_count = have;
         // what comes later in the row has higher tokens: equal is not enough
-        if (n == k) past = key_value(s_list[k - 1]);
+        if (have == k) lim = fmaxf(lim, next_above(key_value(s_best[k - 1])));
         __syncthreads();
       }
-      if (renew) join();
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) cur[i] = nxt[i];
     }
     // hand on what the bound has not overtaken (n <= kDrain: one key a thread)
     const int n = s_count;
-    const unsigned long long key = tid < n ? s_list[tid] : 0ull;
+    const unsigned long long key = tid < n ? key_at(tid) : 0ull;
+    float thr;
+    {
+      uint32_t b = s_bound[0];
+#pragma unroll
+      for (int i = 1; i < kBmWarps; ++i) b = min(b, s_bound[i]);
+      // (not `lim`, which may lie above the last of a cut list)
+      thr = b != 0u ? key_value(static_cast<unsigned long long>(b) << 32) : -INFINITY;
+    }
     const bool keep = tid < n && key_value(key) >= thr;
     // the threads' sums join meanwhile
     float mm = m;
@@ -414,9 +435,9 @@ __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const 
     } else {
       if (keep) s_buf[at] = key;
       __syncthreads();
-      rank_best(s_list, s_buf, handed, k, 0ull, s_rank);
+      rank_best<kBmThreads>(s_best, s_buf, handed, k, 0ull, s_rank);
       handed = k;
-      if (tid < k) out[tid] = s_list[tid];
+      if (tid < k) out[tid] = s_best[tid];
     }
     if (tid == 0) {
       fixed = 0ull;
@@ -438,14 +459,17 @@ __device__ __forceinline__ double key_double(unsigned long long k) {
 
 // One thread block per batch entry; its beams' slices are the lists
 // b * slices + j.
-__global__ void __launch_bounds__(kBmThreads) beam_merge_kernel(const BeamParams p) {
-  __shared__ Total s_list[kMergeList];
+__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p) {
+  extern __shared__ Total s_totals[];       // kMergeList + DSA_MAX_SELECT
+  Total* s_list = s_totals;
   __shared__ Total s_buf[kBmThreads];
   __shared__ Total s_best[DSA_MAX_SELECT];
   __shared__ int s_rank[kBmThreads];
   __shared__ SliceSum s_sum[kMaxLists];
   __shared__ double s_off[DSA_MAX_BEAMS];   // score - log sum exp of each beam (a finished one: its score)
-  __shared__ uint32_t s_bound[kBmWarps];
+  __shared__ float s_score[DSA_MAX_BEAMS];
+  __shared__ uint8_t s_over[DSA_MAX_BEAMS];
+  __shared__ uint32_t s_bound[2 * kMergeWarps];
   __shared__ int s_count;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int row0 = blockIdx.x * p.beams;
@@ -453,101 +477,139 @@ __global__ void __launch_bounds__(kBmThreads) beam_merge_kernel(const BeamParams
   const Total none{0ull, 0u};
   const int lists = p.beams * p.slices;
   if (tid == 0) s_count = 0;
-  pdl_wait();
-  if (blockIdx.x == 0 && tid == 0) *p.status = 0u;
-  // the slices there are; a finished beam's only list holds pad_token
-  for (int i = tid; i < lists; i += kBmThreads) {
-    const int b = i / p.slices, j = i - b * p.slices, row = row0 + b;
-    SliceSum s{0ull, -INFINITY, 0};
-    if (p.finished && p.finished[row]) {
-      if (j == 0) s.count = 1;
-    } else {
-      const unsigned u = static_cast<unsigned>(row) * p.row_tiles;
-      if (j <= static_cast<int>(run_of(p, u + p.row_tiles - 1) - run_of(p, u)))
-        s = p.sums[static_cast<long long>(row0) * p.slices + i];
-    }
-    s_sum[i] = s;
+  // (scores and flags are the caller's, not the scan's)
+  if (tid < p.beams) {
+    s_score[tid] = p.scores[row0 + tid];
+    s_over[tid] = p.finished && p.finished[row0 + tid];
   }
   __syncthreads();
-  for (int b = tid; b < p.beams; b += kBmThreads) {
-    const int row = row0 + b;
-    double off = p.scores[row];
-    if (!(p.finished && p.finished[row])) {
-      const SliceSum* s = s_sum + b * p.slices;
+  int b = 0;
+  bool there = false;
+  if (tid < lists) {
+    b = tid / p.slices;
+    const unsigned u = static_cast<unsigned>(row0 + b) * p.row_tiles;
+    there = !s_over[b] && tid - b * p.slices <= static_cast<int>(run_of(p, u + p.row_tiles - 1) - run_of(p, u));
+  }
+  pdl_wait();
+  if (blockIdx.x == 0 && tid == 0) *p.status = 0u;
+  if (tid < lists) {
+    SliceSum s{0ull, -INFINITY, 0};
+    if (there) s = p.sums[static_cast<long long>(row0) * p.slices + tid];
+    else if (s_over[b] && tid == b * p.slices) s.count = 1;   // a finished beam's only candidate is pad_token
+    s_sum[tid] = s;
+  }
+  __syncthreads();
+  if (tid < p.beams) {
+    double off = s_score[tid];
+    if (!s_over[tid]) {
+      const SliceSum* s = s_sum + tid * p.slices;
       float mm = -INFINITY;
+      for (int j = 0; j < p.slices; ++j) mm = fmaxf(mm, s[j].max);
+      unsigned long long sum = 0ull;
       bool bad = false;
       for (int j = 0; j < p.slices; ++j) {
-        mm = fmaxf(mm, s[j].max);
         bad = bad || s[j].sum == kNaN;
-      }
-      unsigned long long sum = 0ull;
-      for (int j = 0; j < p.slices; ++j)
-        if (s[j].max == mm) sum += s[j].sum;
-        else if (s[j].max > -INFINITY)
+        if (!(s[j].max > -INFINITY)) continue;
+        if (fabsf(mm) <= kFar && fabsf(s[j].max) <= kFar) {
+          const float d = offset_of(s[j].max) - offset_of(mm);   // >= 0
+          sum += d < 64.f ? s[j].sum >> static_cast<int>(d) : 0ull;
+        } else {
           sum += static_cast<unsigned long long>(static_cast<double>(s[j].sum) * join_factor(s[j].max, mm));
-      // log sum = max-relative sum, and H's part undone at the maximum
+        }
+      }
+      // the logarithm, and H's part undone at the maximum
       const double ln2 = 0.6931471805599453;
       const double base = fabsf(mm) <= kFar ? ln2 * (mm * kLog2eRest - static_cast<double>(offset_of(mm))) : static_cast<double>(mm);
       off -= bad ? NAN : base + log(static_cast<double>(sum) * 0x1p-36);
     }
-    s_off[b] = off;
+    s_off[tid] = off;
   }
   __syncthreads();
-  // A lane takes a list, a warp every eighth of its candidates (beams may be far
-  // apart: this way the warps' shares are alike, and so are their bounds).
+  // A bound on the totals (fp32, rounded down). A lane takes a list, a warp
+  // every 32nd of its candidates (beams may be far apart: this way the warps'
+  // shares are alike); of the warps' two largest values `select` reach the
+  // select-th largest.
   const unsigned long long* cands = p.cands + static_cast<long long>(row0) * p.slices * kKeep;
   uint32_t best = 0u;
   for (int i = lane; i < lists; i += 32) {
-    const int b = i / p.slices, n = s_sum[i].count;
-    const float off = __double2float_rd(s_off[b]);
-    const bool over = p.finished && p.finished[row0 + b];
+    const int at = i / p.slices, n = s_sum[i].count;
+    const float off = __double2float_rd(s_off[at]);
     float top = -INFINITY;
-#pragma unroll 4
-    for (int j = wid; j < n; j += kBmWarps) top = fmaxf(top, over ? 0.f : key_value(cands[i * kKeep + j]));
-    const float t = over ? (n > 0 && wid == 0 ? off : -INFINITY) : __fadd_rd(top, off);
+    if (s_over[at]) {
+      if (n > 0 && wid == 0) top = 0.f;
+    } else {
+#pragma unroll
+      for (int j0 = 0; j0 < kKeep; j0 += kMergeWarps)
+        if (j0 + wid < n) top = fmaxf(top, key_value(cands[i * kKeep + j0 + wid]));
+    }
+    const float t = __fadd_rd(top, off);
     if (t > -INFINITY) best = max(best, float_key(t));   // (not for a NaN)
   }
-  best = warp_jth(best, (k + kBmWarps - 1) / kBmWarps);
-  if (lane == 0) s_bound[wid] = best;
+  const uint32_t first = __reduce_max_sync(0xffffffffu, best);
+  const uint32_t holders = __ballot_sync(0xffffffffu, best == first);
+  if (lane == __ffs(holders) - 1) best = 0u;
+  const uint32_t second = __reduce_max_sync(0xffffffffu, best);
+  if (lane == 0) {
+    s_bound[wid] = first;
+    s_bound[kMergeWarps + wid] = second;
+  }
+  __syncthreads();
+  if (wid == 0) {
+    // the select-th largest of the 64, a bit at a time
+    const uint32_t v0 = s_bound[lane], v1 = s_bound[32 + lane];
+    uint32_t bound = 0u;
+#pragma unroll 1
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t t = bound | (1u << bit);
+      const int n = __popc(__ballot_sync(0xffffffffu, v0 >= t)) + __popc(__ballot_sync(0xffffffffu, v1 >= t));
+      if (n >= k) bound = t;
+    }
+    if (lane == 0) s_bound[0] = bound;
+  }
   __syncthreads();
   best = s_bound[0];
+  // the totals of those that may reach it, a round of kMergeWarps lists at a time
+  int have = 0;
+  for (int r = 0; r < lists; r += kMergeWarps) {
+    const int i = r + wid;
+    if (i < lists) {
+      const int at_b = i / p.slices, n = s_sum[i].count;
+      const double off = s_off[at_b];
+      const float off_up = __double2float_ru(off);
+      const bool over = s_over[at_b];
 #pragma unroll
-  for (int i = 1; i < kBmWarps; ++i) best = min(best, s_bound[i]);
-  // the totals of those that may reach it, a round of kBmWarps lists at a time
-  const int rounds = (lists + kBmWarps - 1) / kBmWarps;
-  for (int r = 0; r < rounds; ++r) {
-    const int i = r * kBmWarps + wid;
-    const int b = i < lists ? i / p.slices : 0, n = i < lists ? s_sum[i].count : 0;
-    const double off = s_off[b];
-    const float off_up = __double2float_ru(off);
-    const bool over = p.finished && p.finished[row0 + b];
-    bool full = false;
-#pragma unroll
-    for (int j0 = 0; j0 < kKeep; j0 += 32) {
-      const int j = j0 + lane;
-      if (j >= n) continue;
-      const unsigned long long key = over ? 0ull : cands[i * kKeep + j];
-      const float up = over ? off_up : __fadd_ru(key_value(key), off_up);
-      if (!(up > -INFINITY) || float_key(up) < best) continue;
-      const double t = over ? off : static_cast<double>(key_value(key)) + off;
-      if (!(t > -INFINITY)) continue;
-      const int token = over ? p.pad : static_cast<int32_t>(~static_cast<uint32_t>(key));
-      const int at = atomicAdd(&s_count, 1);
-      s_list[at] = Total{double_key(t), ~static_cast<uint32_t>(b * p.vocab + token)};
-      full = full || at >= DSA_MAX_SELECT;
+      for (int j0 = 0; j0 < kKeep; j0 += 32) {
+        const int j = j0 + lane;
+        if (j >= n) continue;
+        const unsigned long long key = over ? 0ull : cands[i * kKeep + j];
+        const float up = over ? off_up : __fadd_ru(key_value(key), off_up);
+        if (!(up > -INFINITY) || float_key(up) < best) continue;
+        const double t = over ? off : static_cast<double>(key_value(key)) + off;
+        if (!(t > -INFINITY)) continue;
+        const int token = over ? p.pad : static_cast<int32_t>(~static_cast<uint32_t>(key));
+        s_list[atomicAdd(&s_count, 1)] = Total{double_key(t), ~static_cast<uint32_t>(at_b * p.vocab + token)};
+      }
     }
-    // make room for the next round
-    if (__syncthreads_or(full) && r + 1 < rounds) {
-      const int have = cut_list(s_list, s_count, k, none, s_buf, s_rank);
-      if (tid == 0) s_count = have;
+    __syncthreads();
+    // join them with the best so far
+    const int n = s_count, old = have;
+    if (old + n <= kBmThreads) {
+      if (tid < old) s_buf[tid] = s_best[tid];
+      else if (tid < old + n) s_buf[tid] = s_list[tid - old];
       __syncthreads();
+      rank_best<kMergeThreads>(s_best, s_buf, old + n, k, none, s_rank);
+      have = min(k, old + n);
+    } else {
+      // (ties, or far more candidates than the bound leaves in general)
+      if (tid < old) s_list[n + tid] = s_best[tid];
+      __syncthreads();
+      have = cut_to_best<kMergeThreads>(s_best, [&](int x) { return s_list[x]; }, n + old, k, none, s_buf, s_rank);
     }
+    if (tid == 0) s_count = 0;
+    __syncthreads();
   }
-  const int n = s_count;
-  if (n > kBmThreads) cut_list(s_list, n, k, none, s_buf, s_rank);
-  else rank_best(s_best, s_list, n, k, none, s_rank);
   if (tid < k) {
-    const Total t = n > kBmThreads ? s_list[tid] : s_best[tid];
+    const Total t = s_best[tid];
     const long long o = static_cast<long long>(blockIdx.x) * k + tid;
     const uint32_t place = ~t.lo;
     const bool got = t.hi != 0ull;
@@ -620,7 +682,7 @@ size_t beam_bytes(const dsa_beam_problem* p, size_t* sums_at) {
 
 template <typename T>
 cudaError_t launch_scan(const BeamParams& p, int blocks, cudaStream_t s) {
-  constexpr int smem = kListKeys<T> * 8;
+  constexpr int smem = kListLen<T> * 4;
   const cudaError_t e = set_max_smem(reinterpret_cast<const void*>(beam_scan_kernel<T>), smem);
   if (e != cudaSuccess) return e;
   return launch_kernel("beam_scan_kernel", beam_scan_kernel<T>, dim3(blocks), dim3(kBmThreads), smem, s, false, p);
@@ -677,8 +739,10 @@ extern "C" int dsa_beam_select(const dsa_beam_problem* bp, const void* logits, c
   cudaError_t e = bp->logits_dtype == DSA_FP32   ? launch_scan<float>(p, c.blocks, s)
                   : bp->logits_dtype == DSA_FP16 ? launch_scan<__half>(p, c.blocks, s)
                                                  : launch_scan<__nv_bfloat16>(p, c.blocks, s);
+  constexpr int merge_smem = (kMergeList + DSA_MAX_SELECT) * static_cast<int>(sizeof(Total));
+  if (e == cudaSuccess) e = set_max_smem(reinterpret_cast<const void*>(beam_merge_kernel), merge_smem);
   if (e == cudaSuccess)
-    e = launch_kernel("beam_merge_kernel", beam_merge_kernel, dim3(bp->batch), dim3(kBmThreads), 0, s, true, p);
+    e = launch_kernel("beam_merge_kernel", beam_merge_kernel, dim3(bp->batch), dim3(kMergeThreads), merge_smem, s, true, p);
   if (e != cudaSuccess) return report_errorf(DSA_ERR_CUDA, "beam_select launch: %s", cudaGetErrorString(e));
   return DSA_OK;
 }
