@@ -61,7 +61,12 @@ constexpr uint32_t kBlk = kTileKeys * 128;             // 64 columns of a 16-bit
 constexpr uint32_t kTile16 = 2 * kBlk;                 // 32 KB
 constexpr uint32_t kTile8 = kTileKeys * DSA_HEAD_DIM;  // 16 KB of codes
 constexpr uint32_t kTmemCols = 512;                    // S 0-127, 128-255; O 256-383, 384-511
-constexpr int kRing16 = 5, kRing8 = 3, kRaw = 3, kScaleRing = 4;
+// Stages of the rings. A call without an item of more than 128 rows does not
+// need the second query tile: its 32 KB hold one stage (16-bit) or two (INT8
+// codes) more.
+constexpr int kRing16 = 5, kRing8 = 3, kRaw = 3;
+constexpr int kMaxRing = 6, kMaxRaw = 5;
+constexpr int kScaleRing = 8;                          // see load_role
 constexpr int kThreads16 = 384, kThreads8 = 512;
 // registers per thread after the split, and what the block needs in all
 constexpr int kSoftRegs16 = 208, kMiscRegs16 = 80, kSoftRegs8 = 168, kMiscRegs8 = 72, kWidenRegs = 96;
@@ -83,6 +88,7 @@ struct FullParams {
   uint32_t* errors;     // [blocks] status bits of each block, OR-ed into *status by the merge
   float* partial;       // [2 * blocks] parts of part_rows * (128 + 2) floats
   int part_rows;
+  int wide;             // some item has more than 128 rows
   int B, Hq, Hkv, G, cap, window;
   int q_dtype, out_dtype;
   float scale_log2, softcap;
@@ -180,8 +186,8 @@ __device__ __forceinline__ SlotWork slot_work(const Segment& s, int slot) {
 }
 
 struct FullBars {
-  uint64_t full[kRing16], empty[kRing16];       // 16-bit tiles ready / consumed
-  uint64_t raw_full[kRaw], raw_empty[kRaw];     // INT8 codes landed / widened
+  uint64_t full[kMaxRing], empty[kMaxRing];       // 16-bit tiles ready / consumed
+  uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];     // INT8 codes landed / widened
   uint64_t scales[kScaleRing];                  // a tile's scales are in shared memory
   uint64_t q_ready[2], s_full[2], p_full[2], o_full[2];
   uint64_t fix;                                 // a tile whose rows are zeroed before use has landed
@@ -252,6 +258,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const float* v) {
+  uint32_t w[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+  tmem_st32(addr, w);
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 template <int N>
@@ -268,6 +280,15 @@ __device__ __forceinline__ float fast_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+  unsigned long long ra, rb, rd;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(ra) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(rb) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
+  return d;
 }
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -303,6 +324,22 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag));
 }
 
+// Position in a ring whose number of stages is known at run time.
+struct RingPos {
+  int stage = 0;
+  uint32_t round = 0;       // parity: the round's `full`; of `empty`, the round before
+  __device__ __forceinline__ void step(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      ++round;
+    }
+  }
+};
+
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {   // when this thread's copies so far have landed
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // ---------------------------------------------------------------- loader
 // Issues the tiles in the order the products consume them: rows mode K0 V0 K1
 // V1 ..., keys mode K0 K1 V0 K2 V1 K3 ...
@@ -324,11 +361,18 @@ __device__ __forceinline__ bool for_tiles(const Segment& s, F&& f) {
   return true;
 }
 
+//
+// INT8: the scales of a K tile's keys, and of the same keys' values, are copied
+// beside it, four bytes a key, into a ring of their own. A slot is written
+// again eight tiles on. By then the softmax has read it: tile i + 8's K tile is
+// issued when a raw stage is free, so V of tile i + 4 at least has been widened,
+// so K of tile i + 3 has been consumed, and its product was issued after the
+// weights of tile i + 1.
 template <bool INT8>
 __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                          FullBars* bars, uint8_t* ring, volatile int* abort_flag) {
+                                          FullBars* bars, uint8_t* ring, int stages, float* scales,
+                                          volatile int* abort_flag) {
   const int lane = threadIdx.x & 31;
-  constexpr int kStages = INT8 ? kRaw : kRing16;
   constexpr uint32_t kBytes = INT8 ? kTile8 : kTile16;
   uint64_t* full = INT8 ? bars->raw_full : bars->full;
   uint64_t* empty = INT8 ? bars->raw_empty : bars->empty;
@@ -336,16 +380,30 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  uint32_t seq = 0, fixes = 0;
+  RingPos pos;
+  uint32_t fixes = 0, tiles = 0;
   bool bad = false;
   Walk walk(p);
   Segment s;
   while (walk.next(p, &s)) {
+    // cache rows of 32 tiles, one a lane, looked up together and 32 tiles ahead
+    const auto look_up = [&](int t) {
+      return t < s.t1 ? cache_row(p.pg, s.w.b, p.cap, (s.w.tile0 + t) * kTileKeys, &bad) : 0;
+    };
+    int base = s.t0;
+    long long rows = look_up(base + lane), rows_next = look_up(base + 32 + lane);
     const bool ok = for_tiles(s, [&](int t, bool is_v) {
-      const int st = seq % kStages;
-      if (seq >= kStages && !warp_wait(&empty[st], ((seq / kStages) - 1) & 1, abort_flag)) return false;
+      const int st = pos.stage;
+      if (pos.round > 0 && !warp_wait(&empty[st], (pos.round - 1) & 1, abort_flag)) return false;
       const int key = (s.w.tile0 + t) * kTileKeys;
-      const int row = static_cast<int>(cache_row(p.pg, s.w.b, p.cap, key, &bad));
+      // (K runs up to two tiles ahead of V: the window moves when V has left it)
+      if (is_v && t >= base + 32) {
+        base += 32;
+        rows = rows_next;
+        rows_next = look_up(base + 32 + lane);
+      }
+      const long long first = __shfl_sync(0xffffffffu, t < base + 32 ? rows : rows_next, (t - base) & 31);
+      const int row = static_cast<int>(first);
       uint8_t* dst = ring + st * kBytes;
       const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
       // rows of V that no query of the item sees
@@ -356,6 +414,21 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
         mbar_arrive_expect_tx(bar, kBytes);
         tma_load_3d(dst, tm, bar, 0, s.w.g, row);
         if constexpr (!INT8) tma_load_3d(dst + kBlk, tm, bar, 64, s.w.g, row);
+      }
+      if constexpr (INT8) {
+        if (!is_v) {
+          float* sc = scales + (tiles % kScaleRing) * 2 * kTileKeys;
+#pragma unroll
+          for (int i = 0; i < kTileKeys / 32; ++i) {
+            const int r = i * 32 + lane;
+            const bool in = r >= lo && r < hi;
+            const long long at = in ? (first + r) * p.Hkv + s.w.g : 0;
+            cp_async4(sc + r, p.k_scale + at, in);
+            cp_async4(sc + kTileKeys + r, p.v_scale + at, in);
+          }
+          cp_async_arrive(&bars->scales[tiles % kScaleRing]);
+          ++tiles;
+        }
       }
       __syncwarp();
       if (fix) {
@@ -369,93 +442,97 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[st]);
       }
-      ++seq;
+      pos.step(stages);
       return true;
     });
     if (!ok) break;
   }
   if (bad) bars->bad_page = 1;
+  if constexpr (INT8) {
+    cp_async_commit();
+    cp_async_wait<0>();
+  }
   if (lane == 0) {
     // a block must not end with copies in flight (the consumers may have given up)
-    for (uint32_t q = seq > kStages ? seq - kStages : 0; q < seq; ++q) {
+    for (int q = 0; q < stages; ++q) {
+      // stage q's last use: this round if the position is past it, else the one before
+      const uint32_t uses = pos.round + (q < pos.stage ? 1 : 0);
+      if (uses == 0) continue;
       const long long t0 = clock64();
-      while (!mbar_try_wait(&full[q % kStages], (q / kStages) & 1) && clock64() - t0 < kWaitBudgetCycles) {
+      while (!mbar_try_wait(&full[q], (uses - 1) & 1) && clock64() - t0 < kWaitBudgetCycles) {
       }
     }
   }
 }
 
 // ------------------------------------------------------------ INT8 widening
+// A tile of 128 x 128 codes (128-byte rows, swizzled) to a 16-bit tile, by 128
+// threads. Eight lanes take chunks 0-3 (16 codes each) of an even row and 4-7
+// of the next, then the other halves: the reads, and the two 16-byte writes a
+// chunk becomes, each touch eight different 16-byte columns. (Unrolled by four
+// chunks only: with the softmax's loop this has to stay in the instruction cache.)
+template <bool F16>
+__device__ __forceinline__ void widen_tile(const uint8_t* src, uint8_t* dst, int tid) {
+  const int half = (tid >> 2) & 1;
+#pragma unroll 1
+  for (int i = 0; i < 4; i += 2) {
+    uint4 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = ((i + (j >> 1)) * 16 + (tid >> 3)) * 2 + half;
+      x[j] = *reinterpret_cast<const uint4*>(src + row * 128 + ((((tid & 3) + 4 * (half ^ (j & 1))) ^ (row & 7)) << 4));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = ((i + (j >> 1)) * 16 + (tid >> 3)) * 2 + half;
+      const int c = (tid & 3) + 4 * (half ^ (j & 1));
+      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = widen2<F16>(w[e >> 1], e & 1);
+      uint8_t* d = dst + (c >> 2) * kBlk + row * 128;
+      const int ch = (c & 3) * 2;
+      *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
 template <bool QK_F16>
 __device__ __forceinline__ void widen_role(const FullParams& p, FullBars* bars, uint8_t* ring, const uint8_t* raw,
-                                           float* scales, int tid, volatile int* abort_flag) {
-  uint32_t seq = 0, tiles = 0;
-  bool bad = false;
+                                           int raw_stages, int tid, volatile int* abort_flag) {
+  RingPos from, to;
   Walk walk(p);
   Segment s;
   while (walk.next(p, &s)) {
-    // this thread's key's scales, fetched a tile ahead (two dependent loads)
-    float ks = 0.f, vs = 0.f;
-    const auto fetch = [&](int t) {
-      const int key = (s.w.tile0 + t) * kTileKeys + tid;
-      ks = vs = 0.f;
-      if (t < s.t1 && key >= s.w.lo && key < s.w.hi) {
-        const long long i = cache_row(p.pg, s.w.b, p.cap, key, &bad) * p.Hkv + s.w.g;
-        ks = __ldg(p.k_scale + i);
-        vs = __ldg(p.v_scale + i);
-      }
-    };
-    fetch(s.t0);
-    const bool ok = for_tiles(s, [&](int t, bool is_v) {
-      const int rs = seq % kRaw, st = seq % kRing8;
-      if (!warp_wait(&bars->raw_full[rs], (seq / kRaw) & 1, abort_flag)) return false;
-      if (seq >= kRing8 && !warp_wait(&bars->empty[st], ((seq / kRing8) - 1) & 1, abort_flag)) return false;
-      if (!is_v) {
-        // (scales of the tile kScaleRing before are no longer read: its V stage
-        // was consumed before this tile's K stage became free)
-        float* sc = scales + (tiles % kScaleRing) * 2 * kTileKeys;
-        sc[tid] = ks;
-        sc[kTileKeys + tid] = vs;
-        mbar_arrive(&bars->scales[tiles % kScaleRing]);
-        ++tiles;
-        fetch(t + 1);
-      }
-      const uint8_t* src = raw + rs * kTile8;
-      uint8_t* dst = ring + st * kTile16;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = i * 16 + (tid >> 3), c = tid & 7;   // 16 codes: chunk c of the row
-        const uint4 x = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          o[e] = is_v ? widen2<false>(w[e >> 1], e & 1) : widen2<QK_F16>(w[e >> 1], e & 1);
-        uint8_t* d = dst + (c >> 2) * kBlk + row * 128;
-        const int ch = (c & 3) * 2;
-        *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-      }
+    const bool ok = for_tiles(s, [&](int, bool is_v) {
+      if (!warp_wait(&bars->raw_full[from.stage], from.round & 1, abort_flag)) return false;
+      if (to.round > 0 && !warp_wait(&bars->empty[to.stage], (to.round - 1) & 1, abort_flag)) return false;
+      const uint8_t* src = raw + from.stage * kTile8;
+      uint8_t* dst = ring + to.stage * kTile16;
+      if (!QK_F16 || is_v) widen_tile<false>(src, dst, tid);
+      else widen_tile<QK_F16>(src, dst, tid);
       fence_async_smem();
-      mbar_arrive(&bars->full[st]);
-      mbar_arrive(&bars->raw_empty[rs]);
-      ++seq;
+      mbar_arrive(&bars->full[to.stage]);
+      mbar_arrive(&bars->raw_empty[from.stage]);
+      from.step(raw_stages);
+      to.step(kRing8);
       return true;
     });
     if (!ok) break;
   }
-  if (bad) bars->bad_page = 1;
 }
 
 // ------------------------------------------------------------ tensor core
-template <bool QK_F16, bool PV_F16, int STAGES>
+template <bool QK_F16, bool PV_F16>
 __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint32_t q_addr,
-                                         uint32_t ring_addr, volatile int* abort_flag) {
+                                         uint32_t ring_addr, int stages, volatile int* abort_flag) {
   constexpr uint32_t id_qk = idesc128(QK_F16, false), id_pv = idesc128(PV_F16, true);
-  uint32_t seq = 0, nseg = 0, np[2] = {0, 0};
-  const auto wait_tile = [&](uint32_t q) { return mbar_wait_bounded(&bars->full[q % STAGES], (q / STAGES) & 1, abort_flag); };
-  const auto qk = [&](int slot, uint32_t q_tile, uint32_t q) {   // S[slot] = Q K^T
-    const uint32_t a = q_addr + q_tile * kTile16, b = ring_addr + (q % STAGES) * kTile16;
+  uint32_t nseg = 0, np[2] = {0, 0};
+  RingPos pos;
+  const auto wait_tile = [&](const RingPos& q) { return mbar_wait_bounded(&bars->full[q.stage], q.round & 1, abort_flag); };
+  const auto qk = [&](int slot, uint32_t q_tile, const RingPos& q) {   // S[slot] = Q K^T
+    const uint32_t a = q_addr + q_tile * kTile16, b = ring_addr + q.stage * kTile16;
 #pragma unroll
     for (int kk = 0; kk < DSA_HEAD_DIM / 16; ++kk) {
       const uint32_t off = (kk >> 2) * kBlk + (kk & 3) * 32;
@@ -463,18 +540,18 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
     }
     tc_commit(&bars->s_full[slot]);
   };
-  const auto pv = [&](int slot, uint32_t q, bool first) {        // O[slot] (+)= P V
+  const auto pv = [&](int slot, const RingPos& q, bool first) {        // O[slot] (+)= P V
     if (!mbar_wait_bounded(&bars->p_full[slot], np[slot] & 1, abort_flag)) return false;
     ++np[slot];
     tc_fence_after();
-    const uint32_t b = ring_addr + (q % STAGES) * kTile16;
+    const uint32_t b = ring_addr + q.stage * kTile16;
 #pragma unroll
     for (int kk = 0; kk < kTileKeys / 16; ++kk)
       tc_mma_f16_ts(tmem + 256 + slot * 128, tmem + slot * 128 + kk * 8, sw128_desc(b + kk * 16 * 128, kBlk), id_pv,
                     !first || kk > 0);
     return true;
   };
-  const auto release = [&](uint32_t q) { tc_commit(&bars->empty[q % STAGES]); };
+  const auto release = [&](const RingPos& q) { tc_commit(&bars->empty[q.stage]); };
   Walk walk(p);
   Segment s;
   bool ok = true;
@@ -487,9 +564,10 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
     const int n = s.t1 - s.t0;
     if (n == 0) continue;
     if (s.rows_mode) {
-      // ring positions: K_j at seq + 2j, V_j at seq + 2j + 1
+      // round j: P V of tile j - 1 and S of tile j in slot 0, then in slot 1
+      RingPos v = pos;
       for (int j = 0; j <= n && ok; ++j) {
-        const uint32_t k = seq + 2 * j, v = k - 1;
+        const RingPos k = pos;
         if (j > 0) ok = wait_tile(v);
         if (ok && j < n) ok = wait_tile(k);
         if (!ok) break;
@@ -506,27 +584,33 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
             if (slot == 1) release(k);
           }
         }
+        if (j < n) {
+          pos.step(stages);
+          v = pos;
+          pos.step(stages);
+        }
       }
-      seq += 2 * n;
     } else {
       // step i: P V of tile i - 2, then S of tile i, both in slot i & 1
       for (int i = 0; i < n + 2 && ok; ++i) {
         const int slot = i & 1;
         if (i >= 2 && i - 2 < n) {
-          ok = wait_tile(seq);
+          ok = wait_tile(pos);
           if (!ok) break;
           tc_fence_after();
-          ok = pv(slot, seq, i < 4);
+          ok = pv(slot, pos, i < 4);
           if (!ok) break;
-          release(seq++);
+          release(pos);
+          pos.step(stages);
           if (i >= n) tc_commit(&bars->o_full[slot]);
         }
         if (i < n) {
-          ok = wait_tile(seq);
+          ok = wait_tile(pos);
           if (!ok) break;
           tc_fence_after();
-          qk(slot, 0, seq);
-          release(seq++);
+          qk(slot, 0, pos);
+          release(pos);
+          pos.step(stages);
         }
       }
     }
@@ -538,12 +622,57 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
 }
 
 // ---------------------------------------------------------------- softmax
+// z (units of S, c log2-units each) -> cap * tanh(z c ln2 / cap) in log2 units.
+// Up to 1 in size the argument takes an odd polynomial (least maximum error on
+// [-1, 1], fitted for this: 7e-8 in fp32, paired arithmetic), beyond it
+// tanh y = 1 - 2 / (1 + e^2y), whose two special-function calls a value the
+// kernel would otherwise wait for.
+template <int N>
+__device__ __forceinline__ void cap_scores(float* z, float c, float softcap) {
+  const float cap = softcap * 1.4426950408889634f, ys = c / cap;
+  float far = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) far = fmaxf(far, fabsf(z[i]));
+  if (__all_sync(0xffffffffu, far * ys <= 1.0f)) {
+    const float2 y2 = make_float2(ys, ys), w2 = make_float2(c, c);
+    const auto both = [](float x) { return make_float2(x, x); };
+    const float2 zero = both(0.f);
+    // eight pairs side by side: a chain of ten dependent operations each
+#pragma unroll
+    for (int i = 0; i < N; i += 16) {
+      float2 t[8], a[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 y = fma_f32x2(make_float2(z[i + 2 * e], z[i + 2 * e + 1]), y2, zero);
+        t[e] = fma_f32x2(y, y, zero);
+        a[e] = both(9.63771308e-4f);
+      }
+      constexpr float k[6] = {-5.95127745e-3f, 1.99732799e-2f, -5.32658324e-2f, 1.33195832e-1f, -3.33321303e-1f, 9.99999702e-1f};
+#pragma unroll
+      for (int d = 0; d < 6; ++d)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] = fma_f32x2(a[e], t[e], both(k[d]));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {   // cap y = z c
+        const float2 x = fma_f32x2(make_float2(z[i + 2 * e], z[i + 2 * e + 1]), w2, zero);
+        a[e] = fma_f32x2(a[e], x, zero);
+        z[i + 2 * e] = a[e].x;
+        z[i + 2 * e + 1] = a[e].y;
+      }
+    }
+  } else {
+    const float two = 2.0f * c / softcap;
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = fmaf(-2.0f * cap, fast_rcp(1.0f + fast_exp2(z[i] * two)), cap);
+  }
+}
+
 // One slot's four warps, one row a thread. MOD: the scores are capped or get a
 // bias.
 template <bool QK_F16, bool PV_F16, bool INT8, bool MOD>
 __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint8_t* sQ,
                                              const float* scales, int slot, volatile int* abort_flag) {
-  const int tid = threadIdx.x & 127, lane = tid & 31;
+  const int tid = threadIdx.x & 127;
   const uint32_t lane_addr = static_cast<uint32_t>((tid >> 5) * 32) << 16;
   const uint32_t tS = tmem + lane_addr + slot * 128, tO = tmem + lane_addr + 256 + slot * 128;
   uint32_t ns = 0, no = 0, nml = 0, nseg = 0, tile_seq = 0;
@@ -561,34 +690,33 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     float c = p.scale_log2;   // logits in units of log2 e per unit of S
     if (slot == 0 || s.rows_mode) {
       uint8_t* dst = sQ + slot * kTile16;
-      uint4 u[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        u[i] = valid ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row * DSA_HEAD_DIM) + i)
-                     : make_uint4(0, 0, 0, 0);
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row * DSA_HEAD_DIM);
+      int ex = 0;   // the row is scaled by 2^-ex
       if (QK_F16 && p.q_dtype == DSA_BF16) {
         // the row's largest exponent to 14
         uint32_t top = 0;
-#pragma unroll
+#pragma unroll 8
         for (int i = 0; i < 16; ++i) {
-          const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+          const uint4 u = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
         }
-        const int ex = top >= 0x80u ? static_cast<int>(top >> 7) - 127 - 14 : -126 - 14;   // scaled by 2^-ex
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        ex = top >= 0x80u ? static_cast<int>(top >> 7) - 127 - 14 : -126 - 14;
+        c = ldexpf(c, ex);
+      }
+#pragma unroll 8
+      for (int i = 0; i < 16; ++i) {
+        uint4 u = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        if (QK_F16 && p.q_dtype == DSA_BF16) {
+          uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             w[e] = pack2<true>(ldexpf(__uint_as_float(w[e] << 16), -ex), ldexpf(__uint_as_float(w[e] & 0xffff0000u), -ex));
-          u[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          u = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        c = ldexpf(c, ex);
+        *reinterpret_cast<uint4*>(dst + (i >> 3) * kBlk + tid * 128 + (((i & 7) ^ (tid & 7)) << 4)) = u;
       }
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        *reinterpret_cast<uint4*>(dst + (i >> 3) * kBlk + tid * 128 + (((i & 7) ^ (tid & 7)) << 4)) = u[i];
       fence_async_smem();
       if (!s.rows_mode) bars->m[tid] = c;   // for slot 1
     }
@@ -624,58 +752,68 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
         }
       }
       if (warp_valid) {
-        float z[kTileKeys];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(tS + i * 32, z + i * 32);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < kTileKeys; ++i) asm volatile("" : "+f"(z[i]));   // no use before the wait
+        // kCols values of S at a time: all 128 in registers, or (INT8, MOD) two
+        // passes over halves, the first of which leaves what it made of S in
+        // place -- half the code, which must share the instruction cache with
+        // the widening, and registers that spill nothing
+        constexpr int kCols = INT8 || MOD ? 64 : 128;
         const float* sc = scales + ((tile_seq + (t - s.t0)) % kScaleRing) * 2 * kTileKeys;
-        if constexpr (INT8) {
+        const bool masked = key0 + kTileKeys - 1 > pos0 || key0 < lo1;
+        const float cz = MOD ? 1.0f : c;
+        float z[kCols];
+        float mn = -INFINITY;
+        const auto load_s = [&](int col) {
 #pragma unroll
-          for (int i = 0; i < kTileKeys; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(sc + i);
-            z[i] *= f.x;
-            z[i + 1] *= f.y;
-            z[i + 2] *= f.z;
-            z[i + 3] *= f.w;
+          for (int i = 0; i < kCols; i += 32) tmem_ld32(tS + col + i, z + i);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) asm volatile("" : "+f"(z[i]));   // no use before the wait
+        };
+#pragma unroll 1
+        for (int col = 0; col < kTileKeys; col += kCols) {
+          load_s(col);
+          if constexpr (INT8) {
+#pragma unroll
+            for (int i = 0; i < kCols; i += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(sc + col + i);
+              z[i] *= f.x;
+              z[i + 1] *= f.y;
+              z[i + 2] *= f.z;
+              z[i + 3] *= f.w;
+            }
+          }
+          if constexpr (MOD) {
+            if (p.softcap > 0.f) cap_scores<kCols>(z, c, p.softcap);
+            else
+#pragma unroll
+              for (int i = 0; i < kCols; ++i) z[i] *= c;
+            if (p.slopes) {
+              const float d = static_cast<float>(key0 + col - pos);
+#pragma unroll
+              for (int i = 0; i < kCols; ++i) z[i] = fmaf(slope, d + static_cast<float>(i), z[i]);
+            }
+          }
+          if (masked) {
+            const int a = lo - key0 - col, b = pos - key0 - col;   // columns a .. b are visible
+#pragma unroll
+            for (int i = 0; i < kCols; ++i)
+              if (i < a || i > b) z[i] = -INFINITY;
+          }
+          float mt[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+          for (int i = 4; i < kCols; i += 4) {
+            mt[0] = fmaxf(mt[0], z[i]);
+            mt[1] = fmaxf(mt[1], z[i + 1]);
+            mt[2] = fmaxf(mt[2], z[i + 2]);
+            mt[3] = fmaxf(mt[3], z[i + 3]);
+          }
+          mn = fmaxf(mn, fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])));
+          if constexpr (kCols < kTileKeys) {
+#pragma unroll
+            for (int i = 0; i < kCols; i += 32) tmem_st32(tS + col + i, z + i);
           }
         }
-        float cz = c;
-        if constexpr (MOD) {
-          cz = 1.0f;
-          if (p.softcap > 0.f) {
-            // cap * tanh(y) = cap - 2 cap / (1 + e^2y), in log2 units
-            const float two = 2.0f * c / p.softcap;                 // c holds log2 e
-            const float cap = p.softcap * 1.4426950408889634f;
-#pragma unroll
-            for (int i = 0; i < kTileKeys; ++i)
-              z[i] = fmaf(-2.0f * cap, fast_rcp(1.0f + fast_exp2(z[i] * two)), cap);
-          } else {
-#pragma unroll
-            for (int i = 0; i < kTileKeys; ++i) z[i] *= c;
-          }
-          if (p.slopes) {
-            const float d = static_cast<float>(key0 - pos);
-#pragma unroll
-            for (int i = 0; i < kTileKeys; ++i) z[i] = fmaf(slope, d + static_cast<float>(i), z[i]);
-          }
-        }
-        if (key0 + kTileKeys - 1 > pos0 || key0 < lo1) {
-          const int a = lo - key0, b = pos - key0;   // columns a .. b are visible
-#pragma unroll
-          for (int i = 0; i < kTileKeys; ++i)
-            if (i < a || i > b) z[i] = -INFINITY;
-        }
-        float mt[4] = {z[0], z[1], z[2], z[3]};
-#pragma unroll
-        for (int i = 4; i < kTileKeys; i += 4) {
-          mt[0] = fmaxf(mt[0], z[i]);
-          mt[1] = fmaxf(mt[1], z[i + 1]);
-          mt[2] = fmaxf(mt[2], z[i + 2]);
-          mt[3] = fmaxf(mt[3], z[i + 3]);
-        }
-        const float mn = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+        if constexpr (kCols < kTileKeys) tmem_st_wait();
         // (-inf stays as it is: nothing seen yet)
         const bool raise = mn > m && (m == -INFINITY || (mn - m) * cz > kRaise);
         if (__any_sync(0xffffffffu, raise)) {
@@ -699,27 +837,35 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
           }
         }
         const float mc = m == -INFINITY ? 0.f : kLift - m * cz;
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float2 c2 = make_float2(cz, cz), m2 = make_float2(mc, mc);
+#pragma unroll 1
+        for (int col = 0; col < kTileKeys; col += kCols) {
+          if constexpr (kCols < kTileKeys) load_s(col);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+          for (int h = 0; h < kCols; h += 64) {
+            uint32_t w[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int e = h * 64 + 2 * i;
-            const float2 y = fma_f32x2(make_float2(z[e], z[e + 1]), c2, m2);
-            float2 pr = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-            sum[i & 1] = fma_f32x2(pr, make_float2(1.f, 1.f), sum[i & 1]);
-            if constexpr (INT8) {
-              const float2 vs = *reinterpret_cast<const float2*>(sc + kTileKeys + e);
-              pr.x *= vs.x;
-              pr.y *= vs.y;
+            for (int i = 0; i < 32; i += 8) {
+              float2 pr[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) pr[e] = fma_f32x2(make_float2(z[h + 2 * (i + e)], z[h + 2 * (i + e) + 1]), c2, m2);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) pr[e] = make_float2(fast_exp2(pr[e].x), fast_exp2(pr[e].y));
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                sum[e & 3] = add_f32x2(pr[e], sum[e & 3]);
+                if constexpr (INT8) {
+                  const float2 vs = *reinterpret_cast<const float2*>(sc + kTileKeys + col + h + 2 * (i + e));
+                  pr[e] = fma_f32x2(pr[e], vs, make_float2(0.f, 0.f));
+                }
+                w[i + e] = pack2<PV_F16>(pr[e].x, pr[e].y);
+              }
             }
-            w[i] = pack2<PV_F16>(pr.x, pr.y);
+            tmem_st32(tS + (col + h) / 2, w);
           }
-          tmem_st32(tS + h * 32, w);
         }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
         tmem_st_wait();
       }
       tc_fence_before();
@@ -831,20 +977,24 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
                      const __grid_constant__ FullParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  constexpr int kStages = INT8 ? kRing8 : kRing16;
+  // queries | (INT8: codes) | 16-bit tiles | (INT8: scales) | barriers; without
+  // wide items what follows the first query tile begins at the second
   uint8_t* sQ = base;
-  uint8_t* ring = sQ + 2 * kTile16;
-  uint8_t* raw = ring + kStages * kTile16;
-  float* scales = reinterpret_cast<float*>(raw + (INT8 ? kRaw * kTile8 : 0));
+  uint8_t* after_q = sQ + (p.wide ? 2 : 1) * kTile16;
+  const int raw_stages = INT8 ? (p.wide ? kRaw : kMaxRaw) : 0;
+  const int stages = INT8 ? kRing8 : (p.wide ? kRing16 : kMaxRing);
+  uint8_t* raw = after_q;
+  uint8_t* ring = after_q + raw_stages * kTile8;
+  float* scales = reinterpret_cast<float*>(base + 2 * kTile16 + (INT8 ? kRaw * kTile8 + kRing8 * kTile16 : kRing16 * kTile16));
   FullBars* bars = reinterpret_cast<FullBars*>(reinterpret_cast<uint8_t*>(scales) + (INT8 ? kScaleRing * 2 * kTileKeys * 4 : 0));
   volatile int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kMaxRing; ++i) {
       mbar_init(&bars->full[i], INT8 ? 128 : 1);
       mbar_init(&bars->empty[i], 1);
     }
-    for (int i = 0; i < kRaw; ++i) {
+    for (int i = 0; i < kMaxRaw; ++i) {
       mbar_init(&bars->raw_full[i], 1);
       mbar_init(&bars->raw_empty[i], 128);
     }
@@ -854,7 +1004,7 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
       mbar_init(&bars->p_full[i], 128);
       mbar_init(&bars->o_full[i], 1);
     }
-    for (int i = 0; i < kScaleRing; ++i) mbar_init(&bars->scales[i], 128);
+    for (int i = 0; i < kScaleRing; ++i) mbar_init(&bars->scales[i], 32);
     mbar_init(&bars->fix, 1);
     mbar_init(&bars->ml, 128);
     mbar_init(&bars->done, 1);
@@ -877,14 +1027,14 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
     regs_down<INT8 ? kMiscRegs8 : kMiscRegs16>();
     if (warp == 8) {
       if ((threadIdx.x & 31) == 0)
-        mma_role<QK_F16, PV_F16, kStages>(p, bars, tmem, smem_u32(sQ), smem_u32(ring), abort_flag);
+        mma_role<QK_F16, PV_F16>(p, bars, tmem, smem_u32(sQ), smem_u32(ring), stages, abort_flag);
     } else if (warp == 9) {
-      load_role<INT8>(p, tm_k, tm_v, bars, INT8 ? raw : ring, abort_flag);
+      load_role<INT8>(p, tm_k, tm_v, bars, INT8 ? raw : ring, INT8 ? raw_stages : stages, scales, abort_flag);
     }
   } else {
     if constexpr (INT8) {
       regs_down<kWidenRegs>();
-      widen_role<QK_F16>(p, bars, ring, raw, scales, threadIdx.x - 384, abort_flag);
+      widen_role<QK_F16>(p, bars, ring, raw, raw_stages, threadIdx.x - 384, abort_flag);
     }
   }
   tc_fence_before();
@@ -1053,6 +1203,7 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
     fp->first[b] = p->first_key[b];
     fp->part_rows = imax(fp->part_rows, static_cast<int>(rows < kItemRows ? rows : kItemRows));
   }
+  fp->wide = fp->part_rows > kSlotRows;
   fp->part_rows = (fp->part_rows + 3) & ~3;   // parts stay 16-byte aligned
   const int items = fp->item0[p->batch];
   long long cost = 0, tiles = 0;
