@@ -16,9 +16,9 @@
 //     own half of the rows (a tile of K or V is loaded once for 256 rows);
 //   keys mode (up to 128 rows): the slots share the rows and take every other
 //     key tile; their two states are joined at the item's end.
-// Per slot and tile: S = Q K^T (128 x 128, fp32, in tensor memory), four warps
-// read their rows of S (one row a thread), form P = exp2(S c - m) in 16 bits
-// and put it back over S, O += P V with P read from tensor memory. While one
+// Per slot and tile: S = Q K^T (128 x 128, fp32, in tensor memory), eight warps
+// read S (half a row a thread), form P = exp2(S c - m) in 16 bits and put it
+// back over S, O += P V with P read from tensor memory. While one
 // slot is in its softmax the other's two products run.
 //
 // The running maximum m is raised (and O rescaled in tensor memory) only when
@@ -31,7 +31,7 @@
 //
 // K and V tiles arrive by TMA (128 consecutive cache rows of one head: a tile
 // never straddles a block of a paged cache, whose blocks hold a multiple of 128
-// tokens) in a ring of shared stages. INT8 tiles land as codes and four warps
+// tokens) in a ring of shared stages. INT8 tiles land as codes and eight warps
 // widen them to 16 bits (exact); the key's scale multiplies its column of S,
 // the value's its column of P. Rows of V outside the item's keys are zeroed in
 // shared memory (a masked weight is 0, but 0 times a NaN is not); masked
@@ -67,11 +67,15 @@ constexpr uint32_t kTmemCols = 512;                    // S 0-127, 128-255; O 25
 constexpr int kRing16 = 5, kRing8 = 3, kRaw = 3;
 constexpr int kMaxRing = 6, kMaxRaw = 5;
 constexpr int kScaleRing = 8;                          // see load_role
-constexpr int kThreads16 = 384, kThreads8 = 512;
+// Warps: 16 softmax (slot, half of the columns, quarter of the rows), 4 for the
+// products and the loads, 8 that widen INT8 tiles.
+constexpr int kSoftThreads = 512, kThreads16 = 640, kWidenThreads = 256, kThreads8 = kThreads16 + kWidenThreads;
+constexpr int kHalf = kTileKeys / 2;
 // registers per thread after the split, and what the block needs in all
-constexpr int kSoftRegs16 = 208, kMiscRegs16 = 80, kSoftRegs8 = 168, kMiscRegs8 = 72, kWidenRegs = 96;
+constexpr int kSoftRegs16 = 104, kMiscRegs16 = 64, kSoftRegs8 = 80, kMiscRegs8 = 56, kWidenRegs = 64;
 template <bool INT8>
-constexpr int kRegs = INT8 ? 256 * kSoftRegs8 + 128 * (kMiscRegs8 + kWidenRegs) : 256 * kSoftRegs16 + 128 * kMiscRegs16;
+constexpr int kRegs = INT8 ? kSoftThreads * kSoftRegs8 + 128 * kMiscRegs8 + kWidenThreads * kWidenRegs
+                           : kSoftThreads * kSoftRegs16 + 128 * kMiscRegs16;
 constexpr float kLift = 7.0f;                          // log2 of the weight at the running maximum
 constexpr float kRaise = 8.0f;                         // log2 growth that raises the running maximum
 
@@ -192,15 +196,16 @@ struct FullBars {
   uint64_t q_ready[2], s_full[2], p_full[2], o_full[2];
   uint64_t fix;                                 // a tile whose rows are zeroed before use has landed
   uint64_t ml;                                  // keys mode: slot 1's statistics are in shared memory
+  uint64_t pair[2][4];                          // the two warps of a slot's quarter of the rows
   uint64_t done;
   uint32_t tmem_base;
   int abort_flag, bad_page;
-  float m[kSlotRows], l[kSlotRows];
+  float swap[2][2][kSlotRows];                  // [slot][half]: what the two threads of a row tell each other
 };
 
 template <bool INT8>
 constexpr size_t full_smem() {
-  return 1024 + 2 * kTile16 + (INT8 ? kRing8 * kTile16 + kRaw * kTile8 + kScaleRing * 2 * kTileKeys * 4
+  return 2 * kTile16 + (INT8 ? kRing8 * kTile16 + kRaw * kTile8 + kScaleRing * 2 * kTileKeys * 4
                                     : kRing16 * kTile16) + sizeof(FullBars);
 }
 
@@ -213,11 +218,12 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t
       : "memory");
 }
 
-// 128-byte-swizzled operand: `lbo` the pitch of 64-element column blocks of an
-// MN-major operand, 8-row groups 1,024 bytes apart.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo) {
-  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Descriptor of a 128-byte-swizzled operand, 8-row groups 1,024 bytes apart.
+// Low word: address / 16, and `lbo` / 16, the pitch of the 64-element column
+// blocks of an MN-major operand; an offset adds to the address field alone.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
 
 // kind::f16, fp32 accumulator, M = N = 128; B K-major or MN-major
@@ -226,12 +232,23 @@ __host__ __device__ constexpr uint32_t idesc128(bool f16, bool b_mn) {
          (16u << 17) | (8u << 24);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+// D[tmem] (+)= A * B with B, and A, in shared memory (ss), or A in tensor memory
+// (ts). Descriptors by their low words: few scalar instructions per product, for
+// the one thread that issues them is as busy as the tensor core.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(static_cast<int>(acc)), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(static_cast<int>(acc)), "r"(kDescHi)
       : "memory");
 }
 
@@ -263,6 +280,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const float* v) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
   tmem_st32(addr, w);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -466,25 +490,23 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
 }
 
 // ------------------------------------------------------------ INT8 widening
-// A tile of 128 x 128 codes (128-byte rows, swizzled) to a 16-bit tile, by 128
+// A tile of 128 x 128 codes (128-byte rows, swizzled) to a 16-bit tile, by 256
 // threads. Eight lanes take chunks 0-3 (16 codes each) of an even row and 4-7
 // of the next, then the other halves: the reads, and the two 16-byte writes a
-// chunk becomes, each touch eight different 16-byte columns. (Unrolled by four
-// chunks only: with the softmax's loop this has to stay in the instruction cache.)
+// chunk becomes, each touch eight different 16-byte columns.
 template <bool F16>
 __device__ __forceinline__ void widen_tile(const uint8_t* src, uint8_t* dst, int tid) {
   const int half = (tid >> 2) & 1;
-#pragma unroll 1
-  for (int i = 0; i < 4; i += 2) {
+  {
     uint4 x[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = ((i + (j >> 1)) * 16 + (tid >> 3)) * 2 + half;
+      const int row = ((j >> 1) * 32 + (tid >> 3)) * 2 + half;
       x[j] = *reinterpret_cast<const uint4*>(src + row * 128 + ((((tid & 3) + 4 * (half ^ (j & 1))) ^ (row & 7)) << 4));
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = ((i + (j >> 1)) * 16 + (tid >> 3)) * 2 + half;
+      const int row = ((j >> 1) * 32 + (tid >> 3)) * 2 + half;
       const int c = (tid & 3) + 4 * (half ^ (j & 1));
       const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
       uint32_t o[8];
@@ -528,15 +550,17 @@ template <bool QK_F16, bool PV_F16>
 __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint32_t q_addr,
                                          uint32_t ring_addr, int stages, volatile int* abort_flag) {
   constexpr uint32_t id_qk = idesc128(QK_F16, false), id_pv = idesc128(PV_F16, true);
+  const uint32_t qd = desc_lo(q_addr, 16), kd = desc_lo(ring_addr, 16), vd = desc_lo(ring_addr, kBlk);
   uint32_t nseg = 0, np[2] = {0, 0};
   RingPos pos;
   const auto wait_tile = [&](const RingPos& q) { return mbar_wait_bounded(&bars->full[q.stage], q.round & 1, abort_flag); };
   const auto qk = [&](int slot, uint32_t q_tile, const RingPos& q) {   // S[slot] = Q K^T
-    const uint32_t a = q_addr + q_tile * kTile16, b = ring_addr + q.stage * kTile16;
+    const uint32_t a = qd + q_tile * (kTile16 / 16), b = kd + q.stage * (kTile16 / 16);
 #pragma unroll
     for (int kk = 0; kk < DSA_HEAD_DIM / 16; ++kk) {
-      const uint32_t off = (kk >> 2) * kBlk + (kk & 3) * 32;
-      tc_mma_f16(tmem + slot * 128, sw128_desc(a + off, 16), sw128_desc(b + off, 16), id_qk, kk > 0);
+      constexpr uint32_t kStep = 32 / 16;
+      const uint32_t off = (kk >> 2) * (kBlk / 16) + (kk & 3) * kStep;
+      mma_ss(tmem + slot * 128, a + off, b + off, id_qk, kk > 0);
     }
     tc_commit(&bars->s_full[slot]);
   };
@@ -544,11 +568,11 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
     if (!mbar_wait_bounded(&bars->p_full[slot], np[slot] & 1, abort_flag)) return false;
     ++np[slot];
     tc_fence_after();
-    const uint32_t b = ring_addr + q.stage * kTile16;
+    const uint32_t b = vd + q.stage * (kTile16 / 16);
 #pragma unroll
     for (int kk = 0; kk < kTileKeys / 16; ++kk)
-      tc_mma_f16_ts(tmem + 256 + slot * 128, tmem + slot * 128 + kk * 8, sw128_desc(b + kk * 16 * 128, kBlk), id_pv,
-                    !first || kk > 0);
+      mma_ts(tmem + 256 + slot * 128, tmem + slot * 128 + (kk >> 2) * kHalf + (kk & 3) * 8, b + kk * (16 * 128 / 16), id_pv,
+             !first || kk > 0);
     return true;
   };
   const auto release = [&](const RingPos& q) { tc_commit(&bars->empty[q.stage]); };
@@ -623,39 +647,37 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
 
 // ---------------------------------------------------------------- softmax
 // z (units of S, c log2-units each) -> cap * tanh(z c ln2 / cap) in log2 units.
-// Up to 1 in size the argument takes an odd polynomial (least maximum error on
-// [-1, 1], fitted for this: 7e-8 in fp32, paired arithmetic), beyond it
-// tanh y = 1 - 2 / (1 + e^2y), whose two special-function calls a value the
-// kernel would otherwise wait for.
+// Up to 0.7 in size the argument takes an odd polynomial (least maximum error
+// on [-0.7, 0.7], fitted for this: 1.2e-7 in fp32; paired arithmetic, 7 cycles
+// of the multiply-add pipe a value), beyond it tanh y = 1 - 2 / (1 + e^2y),
+// whose two special-function calls a value would be the kernel's bound.
 template <int N>
 __device__ __forceinline__ void cap_scores(float* z, float c, float softcap) {
   const float cap = softcap * 1.4426950408889634f, ys = c / cap;
   float far = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) far = fmaxf(far, fabsf(z[i]));
-  if (__all_sync(0xffffffffu, far * ys <= 1.0f)) {
-    const float2 y2 = make_float2(ys, ys), w2 = make_float2(c, c);
+  if (__all_sync(0xffffffffu, far * ys <= 0.7f)) {
     const auto both = [](float x) { return make_float2(x, x); };
-    const float2 zero = both(0.f);
-    // eight pairs side by side: a chain of ten dependent operations each
+    const float2 y2 = both(ys), zero = both(0.f);
+    const float k[5] = {0.0131941866f * cap, -0.0501952581f * cap, 0.132574543f * cap, -0.333269745f * cap, 0.99999851f * cap};
+    // eight pairs side by side: a chain of seven dependent operations each
 #pragma unroll
     for (int i = 0; i < N; i += 16) {
-      float2 t[8], a[8];
+      float2 y[8], t[8], a[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float2 y = fma_f32x2(make_float2(z[i + 2 * e], z[i + 2 * e + 1]), y2, zero);
-        t[e] = fma_f32x2(y, y, zero);
-        a[e] = both(9.63771308e-4f);
+        y[e] = fma_f32x2(make_float2(z[i + 2 * e], z[i + 2 * e + 1]), y2, zero);
+        t[e] = fma_f32x2(y[e], y[e], zero);
+        a[e] = both(k[0]);
       }
-      constexpr float k[6] = {-5.95127745e-3f, 1.99732799e-2f, -5.32658324e-2f, 1.33195832e-1f, -3.33321303e-1f, 9.99999702e-1f};
 #pragma unroll
-      for (int d = 0; d < 6; ++d)
+      for (int d = 1; d < 5; ++d)
 #pragma unroll
         for (int e = 0; e < 8; ++e) a[e] = fma_f32x2(a[e], t[e], both(k[d]));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {   // cap y = z c
-        const float2 x = fma_f32x2(make_float2(z[i + 2 * e], z[i + 2 * e + 1]), w2, zero);
-        a[e] = fma_f32x2(a[e], x, zero);
+      for (int e = 0; e < 8; ++e) {
+        a[e] = fma_f32x2(a[e], y[e], zero);
         z[i + 2 * e] = a[e].x;
         z[i + 2 * e + 1] = a[e].y;
       }
@@ -667,15 +689,30 @@ __device__ __forceinline__ void cap_scores(float* z, float c, float softcap) {
   }
 }
 
-// One slot's four warps, one row a thread. MOD: the scores are capped or get a
-// bias.
+// One slot's eight warps: a thread has half the columns of a row (64 of S, and
+// the same half of the query's and the output's dims); the two threads of a
+// row, in the warps `quarter` and `quarter` + 4 of the slot, swap their maxima
+// through shared memory. MOD: the scores are capped or get a bias.
 template <bool QK_F16, bool PV_F16, bool INT8, bool MOD>
 __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint8_t* sQ,
-                                             const float* scales, int slot, volatile int* abort_flag) {
-  const int tid = threadIdx.x & 127;
-  const uint32_t lane_addr = static_cast<uint32_t>((tid >> 5) * 32) << 16;
-  const uint32_t tS = tmem + lane_addr + slot * 128, tO = tmem + lane_addr + 256 + slot * 128;
-  uint32_t ns = 0, no = 0, nml = 0, nseg = 0, tile_seq = 0;
+                                             const float* scales, int slot, int half, volatile int* abort_flag) {
+  const int tid = threadIdx.x & 127, quarter = tid >> 5;
+  const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+  const uint32_t tS = tmem + lane_addr + slot * 128 + half * kHalf, tO = tmem + lane_addr + 256 + slot * 128 + half * kHalf;
+  float* mine = &bars->swap[slot][half][tid];
+  const volatile float* theirs = &bars->swap[slot][half ^ 1][tid];
+  uint64_t* pair = &bars->pair[slot][quarter];
+  uint32_t ns = 0, no = 0, nml = 0, nseg = 0, npair = 0, tile_seq = 0;
+  // Swaps a value with the row's other thread. (A thread's next value is
+  // written after every thread of the slot has arrived at one of the barriers
+  // that the products wait for, so after this one was read.)
+  const auto swap = [&](float x, float* other) {
+    *mine = x;
+    mbar_arrive(pair);
+    if (!warp_wait(pair, npair++ & 1, abort_flag)) return false;
+    *other = *theirs;
+    return true;
+  };
   Walk walk(p);
   Segment s;
   while (walk.next(p, &s)) {
@@ -689,45 +726,54 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     const long long row = (static_cast<long long>(p.q0[s.w.b]) + tok) * p.Hq + head;   // query row
     float c = p.scale_log2;   // logits in units of log2 e per unit of S
     if (slot == 0 || s.rows_mode) {
-      uint8_t* dst = sQ + slot * kTile16;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row * DSA_HEAD_DIM);
-      int ex = 0;   // the row is scaled by 2^-ex
+      uint8_t* dst = sQ + slot * kTile16 + half * kBlk + tid * 128;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row * DSA_HEAD_DIM + half * kHalf);
+      uint4 u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
       if (QK_F16 && p.q_dtype == DSA_BF16) {
-        // the row's largest exponent to 14
+        // the row's largest exponent to 14: scaled by 2^-ex
         uint32_t top = 0;
-#pragma unroll 8
-        for (int i = 0; i < 16; ++i) {
-          const uint4 u = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
         }
-        ex = top >= 0x80u ? static_cast<int>(top >> 7) - 127 - 14 : -126 - 14;
-        c = ldexpf(c, ex);
-      }
-#pragma unroll 8
-      for (int i = 0; i < 16; ++i) {
-        uint4 u = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-        if (QK_F16 && p.q_dtype == DSA_BF16) {
-          uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        const uint4* rest = src + (half ? -8 : 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 v = valid ? __ldg(rest + i) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        }
+        const int ex = top >= 0x80u ? static_cast<int>(top >> 7) - 127 - 14 : -126 - 14;
+        // 2^-ex as two factors: it may lie outside fp32's normal range
+        const float f0 = __int_as_float((127 - ex / 2) << 23), f1 = __int_as_float((127 - (ex - ex / 2)) << 23);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            w[e] = pack2<true>(ldexpf(__uint_as_float(w[e] << 16), -ex), ldexpf(__uint_as_float(w[e] & 0xffff0000u), -ex));
-          u = make_uint4(w[0], w[1], w[2], w[3]);
+            w[e] = pack2<true>(__uint_as_float(w[e] << 16) * f0 * f1, __uint_as_float(w[e] & 0xffff0000u) * f0 * f1);
+          u[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *reinterpret_cast<uint4*>(dst + (i >> 3) * kBlk + tid * 128 + (((i & 7) ^ (tid & 7)) << 4)) = u;
+        c = ldexpf(c, ex);
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(dst + ((i ^ (tid & 7)) << 4)) = u[i];
       fence_async_smem();
-      if (!s.rows_mode) bars->m[tid] = c;   // for slot 1
+      if (!s.rows_mode && half == 0) bars->swap[0][1][tid] = c;   // for slot 1
     }
-    tc_fence_before();
-    mbar_arrive(&bars->q_ready[slot]);
     if (slot == 1 && !s.rows_mode) {
       // slot 0 loads the shared rows; what it scaled them by
       if (!warp_wait(&bars->q_ready[0], nseg & 1, abort_flag)) break;
-      c = bars->m[tid];
+      c = *const_cast<const volatile float*>(&bars->swap[0][1][tid]);
     }
     ++nseg;
+    tc_fence_before();
+    mbar_arrive(&bars->q_ready[slot]);
     const float slope = MOD && p.slopes && valid ? p.slopes[head] * 1.4426950408889634f : 0.f;
     const int pos0 = s.w.past + x.row0 / p.G, pos1 = s.w.past + (x.row0 + x.nrows - 1) / p.G;
     const int lo = imax(p.first[s.w.b], p.window > 0 ? pos - p.window + 1 : 0);
@@ -737,7 +783,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     bool ok = true;
     for (int j = 0; j < x.n; ++j) {
       const int t = x.first + j * x.step;
-      const int key0 = (s.w.tile0 + t) * kTileKeys;
+      const int key0 = (s.w.tile0 + t) * kTileKeys;   // (of the tile)
       if (!warp_wait(&bars->s_full[slot], ns & 1, abort_flag)) {
         ok = false;
         break;
@@ -752,13 +798,13 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
         }
       }
       if (warp_valid) {
-        // kCols values of S at a time: all 128 in registers, or (INT8, MOD) two
-        // passes over halves, the first of which leaves what it made of S in
-        // place -- half the code, which must share the instruction cache with
-        // the widening, and registers that spill nothing
-        constexpr int kCols = INT8 || MOD ? 64 : 128;
-        const float* sc = scales + ((tile_seq + (t - s.t0)) % kScaleRing) * 2 * kTileKeys;
+        // kCols values of S at a time: the half row in registers, or (INT8, MOD)
+        // two passes over quarters, the first of which leaves what it made of S
+        // in place
+        constexpr int kCols = INT8 || MOD ? 32 : kHalf;
+        const float* sc = scales + ((tile_seq + (t - s.t0)) % kScaleRing) * 2 * kTileKeys + half * kHalf;
         const bool masked = key0 + kTileKeys - 1 > pos0 || key0 < lo1;
+        const int first = key0 + half * kHalf;
         const float cz = MOD ? 1.0f : c;
         float z[kCols];
         float mn = -INFINITY;
@@ -770,7 +816,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
           for (int i = 0; i < kCols; ++i) asm volatile("" : "+f"(z[i]));   // no use before the wait
         };
 #pragma unroll 1
-        for (int col = 0; col < kTileKeys; col += kCols) {
+        for (int col = 0; col < kHalf; col += kCols) {
           load_s(col);
           if constexpr (INT8) {
 #pragma unroll
@@ -788,13 +834,13 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
 #pragma unroll
               for (int i = 0; i < kCols; ++i) z[i] *= c;
             if (p.slopes) {
-              const float d = static_cast<float>(key0 + col - pos);
+              const float d = static_cast<float>(first + col - pos);
 #pragma unroll
               for (int i = 0; i < kCols; ++i) z[i] = fmaf(slope, d + static_cast<float>(i), z[i]);
             }
           }
           if (masked) {
-            const int a = lo - key0 - col, b = pos - key0 - col;   // columns a .. b are visible
+            const int a = lo - first - col, b = pos - first - col;   // columns a .. b are visible
 #pragma unroll
             for (int i = 0; i < kCols; ++i)
               if (i < a || i > b) z[i] = -INFINITY;
@@ -808,13 +854,16 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
             mt[3] = fmaxf(mt[3], z[i + 3]);
           }
           mn = fmaxf(mn, fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])));
-          if constexpr (kCols < kTileKeys) {
-#pragma unroll
-            for (int i = 0; i < kCols; i += 32) tmem_st32(tS + col + i, z + i);
-          }
+          if constexpr (kCols < kHalf) tmem_st32(tS + col, z);
         }
-        if constexpr (kCols < kTileKeys) tmem_st_wait();
-        // (-inf stays as it is: nothing seen yet)
+        if constexpr (kCols < kHalf) tmem_st_wait();
+        float other = -INFINITY;
+        if (!swap(mn, &other)) {
+          ok = false;
+          break;
+        }
+        mn = fmaxf(mn, other);
+        // (-inf stays as it is: nothing seen yet; both halves come to the same answer)
         const bool raise = mn > m && (m == -INFINITY || (mn - m) * cz > kRaise);
         if (__any_sync(0xffffffffu, raise)) {
           const float to = fmaxf(m, mn);
@@ -823,30 +872,30 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
           l *= f;
           if (j > 0) {
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              float o[32];
-              uint32_t w[32];
-              tmem_ld32(tO + i * 32, o);
+            for (int i = 0; i < kHalf; i += 16) {
+              float o[16];
+              uint32_t w[16];
+              tmem_ld16(tO + i, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(o[e]));
+              for (int e = 0; e < 16; ++e) asm volatile("" : "+f"(o[e]));
 #pragma unroll
-              for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
-              tmem_st32(tO + i * 32, w);
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
+              tmem_st16(tO + i, w);
             }
           }
         }
         const float mc = m == -INFINITY ? 0.f : kLift - m * cz;
-        float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float2 c2 = make_float2(cz, cz), m2 = make_float2(mc, mc);
 #pragma unroll 1
-        for (int col = 0; col < kTileKeys; col += kCols) {
-          if constexpr (kCols < kTileKeys) load_s(col);
+        for (int col = 0; col < kHalf; col += kCols) {
+          if constexpr (kCols < kHalf) load_s(col);
 #pragma unroll
-          for (int h = 0; h < kCols; h += 64) {
-            uint32_t w[32];
+          for (int h = 0; h < kCols; h += 32) {
+            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
+            for (int i = 0; i < 16; i += 8) {
               float2 pr[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) pr[e] = fma_f32x2(make_float2(z[h + 2 * (i + e)], z[h + 2 * (i + e) + 1]), c2, m2);
@@ -854,7 +903,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
               for (int e = 0; e < 8; ++e) pr[e] = make_float2(fast_exp2(pr[e].x), fast_exp2(pr[e].y));
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                sum[e & 3] = add_f32x2(pr[e], sum[e & 3]);
+                sum[e & 1] = add_f32x2(pr[e], sum[e & 1]);
                 if constexpr (INT8) {
                   const float2 vs = *reinterpret_cast<const float2*>(sc + kTileKeys + col + h + 2 * (i + e));
                   pr[e] = fma_f32x2(pr[e], vs, make_float2(0.f, 0.f));
@@ -862,10 +911,10 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
                 w[i + e] = pack2<PV_F16>(pr[e].x, pr[e].y);
               }
             }
-            tmem_st32(tS + (col + h) / 2, w);
+            tmem_st16(tS + (col + h) / 2, w);   // over columns of S that have been read
           }
         }
-        l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_st_wait();
       }
       tc_fence_before();
@@ -879,11 +928,23 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
       if (!warp_wait(&bars->o_full[slot], no & 1, abort_flag)) break;
       ++no;
       tc_fence_after();
+      if (warp_valid) {
+        float other = 0.f;
+        if (!swap(l, &other)) break;
+        l = half ? other + l : l + other;   // the same sum in both
+      }
     }
     if (!s.rows_mode && slot == 1) {
-      // slot 0 joins the two states; it reads this slot's O itself
-      bars->m[tid] = m_log2;
-      bars->l[tid] = l;
+      // slot 0 joins the two states; it reads this slot's O itself. (The swap
+      // before is over in both threads before its places are used again.)
+      if (x.n > 0 && warp_valid) {
+        mbar_arrive(pair);
+        if (!warp_wait(pair, npair++ & 1, abort_flag)) break;
+      }
+      if (half == 0) {
+        bars->swap[1][0][tid] = m_log2;
+        bars->swap[1][1][tid] = l;
+      }
       mbar_arrive(&bars->ml);
       continue;
     }
@@ -895,7 +956,8 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
       tc_fence_after();
       other = slot_work(s, 1).n > 0;
       if (other) {
-        const float m1 = bars->m[tid], l1 = bars->l[tid];
+        const volatile float* v = &bars->swap[1][0][tid];
+        const float m1 = v[0], l1 = v[kSlotRows];
         mj = fmaxf(m_log2, m1);
         f0 = m_log2 == -INFINITY ? 0.f : fast_exp2(m_log2 - mj);
         f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - mj);
@@ -907,65 +969,66 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     float* part = nullptr;
     if (s.whole) {
       norm = lj > 0.f ? 1.0f / lj : 0.f;
-      if (valid && p.lse) p.lse[row] = lj > 0.f ? (mj - kLift + log2f(lj)) * 0.6931471805599453f : -INFINITY;
+      if (valid && half == 0 && p.lse)
+        p.lse[row] = lj > 0.f ? (mj - kLift + log2f(lj)) * 0.6931471805599453f : -INFINITY;
     } else {
       part = p.partial + static_cast<long long>(s.part) * p.part_rows * (DSA_HEAD_DIM + 2);
       const int pr = r - s.w.row0;
-      if (valid) {
+      if (valid && half == 0) {
         part[p.part_rows * DSA_HEAD_DIM + 2 * pr] = mj;
         part[p.part_rows * DSA_HEAD_DIM + 2 * pr + 1] = lj;
       }
-      part += pr * DSA_HEAD_DIM;
+      part += pr * DSA_HEAD_DIM + half * kHalf;
     }
     f0 *= norm;
     f1 *= norm;
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      float o[32];
+    for (int i = 0; i < kHalf; i += 16) {
+      float o[16];
       if (x.n > 0) {
-        tmem_ld32(tO + i * 32, o);
+        tmem_ld16(tO + i, o);
         if (other) {
-          float b[32];
-          tmem_ld32(tO + 128 + i * 32, b);
+          float b[16];
+          tmem_ld16(tO + 128 + i, b);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(o[e]), "+f"(b[e]));
+          for (int e = 0; e < 16; ++e) asm volatile("" : "+f"(o[e]), "+f"(b[e]));
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = f0 * o[e] + f1 * b[e];
+          for (int e = 0; e < 16; ++e) o[e] = f0 * o[e] + f1 * b[e];
         } else {
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(o[e]));
+          for (int e = 0; e < 16; ++e) asm volatile("" : "+f"(o[e]));
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= f0;
+          for (int e = 0; e < 16; ++e) o[e] *= f0;
         }
         // a row without a key: whatever the products hold, its output is 0
         if (s.whole && !(lj > 0.f)) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          for (int e = 0; e < 16; ++e) o[e] = 0.f;
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        for (int e = 0; e < 16; ++e) o[e] = 0.f;
       }
       if (!valid) continue;
       if (part) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4*>(part + i * 32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<float4*>(part + i + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       } else if (p.out_dtype == DSA_FP32) {
-        float* d = static_cast<float*>(p.out) + row * DSA_HEAD_DIM + i * 32;
+        float* d = static_cast<float*>(p.out) + row * DSA_HEAD_DIM + half * kHalf + i;
 #pragma unroll
-        for (int e = 0; e < 32; e += 4)
+        for (int e = 0; e < 16; e += 4)
           *reinterpret_cast<float4*>(d + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       } else {
-        uint16_t* d = static_cast<uint16_t*>(p.out) + row * DSA_HEAD_DIM + i * 32;
-        uint32_t w[16];
+        uint16_t* d = static_cast<uint16_t*>(p.out) + row * DSA_HEAD_DIM + half * kHalf + i;
+        uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
+        for (int e = 0; e < 8; ++e)
           w[e] = p.out_dtype == DSA_FP16 ? pack2<true>(o[2 * e], o[2 * e + 1]) : pack2<false>(o[2 * e], o[2 * e + 1]);
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(d + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+        *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(d + 8) = make_uint4(w[4], w[5], w[6], w[7]);
       }
     }
   }
@@ -975,8 +1038,14 @@ template <bool QK_F16, bool PV_F16, bool INT8, bool MOD>
 __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
     full_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ FullParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // (the kernel has no static shared memory: the dynamic part begins on the
+  // 1,024 bytes that the swizzled tiles need, of which there is none to spare)
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* base = smem_raw;
+  if (smem_u32(base) & 1023u) {
+    if (threadIdx.x == 0) p.errors[blockIdx.x] = kDevBounds;
+    return;
+  }
   // queries | (INT8: codes) | 16-bit tiles | (INT8: scales) | barriers; without
   // wide items what follows the first query tile begins at the second
   uint8_t* sQ = base;
@@ -991,56 +1060,57 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxRing; ++i) {
-      mbar_init(&bars->full[i], INT8 ? 128 : 1);
+      mbar_init(&bars->full[i], INT8 ? kWidenThreads : 1);
       mbar_init(&bars->empty[i], 1);
     }
     for (int i = 0; i < kMaxRaw; ++i) {
       mbar_init(&bars->raw_full[i], 1);
-      mbar_init(&bars->raw_empty[i], 128);
+      mbar_init(&bars->raw_empty[i], kWidenThreads);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->q_ready[i], 128);
+      mbar_init(&bars->q_ready[i], 256);
       mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_full[i], 128);
+      mbar_init(&bars->p_full[i], 256);
       mbar_init(&bars->o_full[i], 1);
+      for (int k = 0; k < 4; ++k) mbar_init(&bars->pair[i][k], 64);
     }
     for (int i = 0; i < kScaleRing; ++i) mbar_init(&bars->scales[i], 32);
     mbar_init(&bars->fix, 1);
-    mbar_init(&bars->ml, 128);
+    mbar_init(&bars->ml, 256);
     mbar_init(&bars->done, 1);
     bars->abort_flag = 0;
     bars->bad_page = 0;
     fence_mbar_init();
   }
-  if (warp == 8) tmem_alloc(&bars->tmem_base, kTmemCols);
+  if (warp == 16) tmem_alloc(&bars->tmem_base, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   pdl_trigger();
   // registers: the launch gives every thread the same number; the softmax
-  // threads hold a row of S (128 values) and take what the others give up
-  if (warp < 8) {
+  // threads hold half a row of S and take what the others give up
+  if (warp < 16) {
     regs_up<INT8 ? kSoftRegs8 : kSoftRegs16>();
-    softmax_role<QK_F16, PV_F16, INT8, MOD>(p, bars, tmem, sQ, scales, warp >> 2, abort_flag);
-  } else if (warp < 12) {
+    softmax_role<QK_F16, PV_F16, INT8, MOD>(p, bars, tmem, sQ, scales, warp >> 3, (warp >> 2) & 1, abort_flag);
+  } else if (warp < 20) {
     regs_down<INT8 ? kMiscRegs8 : kMiscRegs16>();
-    if (warp == 8) {
+    if (warp == 16) {
       if ((threadIdx.x & 31) == 0)
         mma_role<QK_F16, PV_F16>(p, bars, tmem, smem_u32(sQ), smem_u32(ring), stages, abort_flag);
-    } else if (warp == 9) {
+    } else if (warp == 17) {
       load_role<INT8>(p, tm_k, tm_v, bars, INT8 ? raw : ring, INT8 ? raw_stages : stages, scales, abort_flag);
     }
   } else {
     if constexpr (INT8) {
       regs_down<kWidenRegs>();
-      widen_role<QK_F16>(p, bars, ring, raw, raw_stages, threadIdx.x - 384, abort_flag);
+      widen_role<QK_F16>(p, bars, ring, raw, raw_stages, threadIdx.x - kThreads16, abort_flag);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 16) tmem_dealloc(tmem, kTmemCols);
   if (threadIdx.x == 0)
     p.errors[blockIdx.x] = (bars->abort_flag ? kDevTimeout : 0u) | (bars->bad_page ? kDevBadPage : 0u);
 }
