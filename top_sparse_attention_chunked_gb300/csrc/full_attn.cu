@@ -16,9 +16,9 @@
 //     own half of the rows (a tile of K or V is loaded once for 256 rows);
 //   keys mode (up to 128 rows): the slots share the rows and take every other
 //     key tile; their two states are joined at the item's end.
-// Per slot and tile: S = Q K^T (128 x 128, fp32, in tensor memory), eight warps
-// read S (half a row a thread), form P = exp2(S c - m) in 16 bits and put it
-// back over S, O += P V with P read from tensor memory. While one
+// Per slot and tile: S = Q K^T (128 x 128, fp32, in tensor memory), four warps
+// read S (a row a thread, half of it at a time), form P = exp2(S c - m) in 16
+// bits and put it back over S, O += P V with P read from tensor memory. While one
 // slot is in its softmax the other's two products run.
 //
 // The running maximum m is raised (and O rescaled in tensor memory) only when
@@ -67,15 +67,15 @@ constexpr uint32_t kTmemCols = 512;                    // S 0-127, 128-255; O 25
 constexpr int kRing16 = 5, kRing8 = 3, kRaw = 3;
 constexpr int kMaxRing = 6, kMaxRaw = 5;
 constexpr int kScaleRing = 8;                          // see load_role
-// Warps: 16 softmax (slot, half of the columns, quarter of the rows), 4 for the
-// products and the loads, 8 that widen INT8 tiles.
-constexpr int kSoftThreads = 512, kThreads16 = 640, kWidenThreads = 256, kThreads8 = kThreads16 + kWidenThreads;
+// Warps: 8 softmax (slot, quarter of the rows), 4 for the products and the
+// loads, 8 that widen INT8 tiles.
+constexpr int kSoftThreads = 256, kThreads16 = 384, kWidenThreads = 256, kThreads8 = kThreads16 + kWidenThreads;
 constexpr int kHalf = kTileKeys / 2;
-// registers per thread after the split, and what the block needs in all
-constexpr int kSoftRegs16 = 104, kMiscRegs16 = 64, kSoftRegs8 = 80, kMiscRegs8 = 56, kWidenRegs = 64;
-template <bool INT8>
-constexpr int kRegs = INT8 ? kSoftThreads * kSoftRegs8 + 128 * kMiscRegs8 + kWidenThreads * kWidenRegs
-                           : kSoftThreads * kSoftRegs16 + 128 * kMiscRegs16;
+// Registers: 16-bit blocks have enough as they are launched (168 a thread);
+// with INT8 the softmax takes what the others give up. What the block needs in
+// all must be within what it is launched with:
+constexpr int kSoftRegs8 = 128, kMiscRegs8 = 64, kWidenRegs = 80;
+constexpr int kRegs8 = kSoftThreads * kSoftRegs8 + 128 * kMiscRegs8 + kWidenThreads * kWidenRegs;
 constexpr float kLift = 7.0f;                          // log2 of the weight at the running maximum
 constexpr float kRaise = 8.0f;                         // log2 growth that raises the running maximum
 
@@ -196,11 +196,10 @@ struct FullBars {
   uint64_t q_ready[2], s_full[2], p_full[2], o_full[2];
   uint64_t fix;                                 // a tile whose rows are zeroed before use has landed
   uint64_t ml;                                  // keys mode: slot 1's statistics are in shared memory
-  uint64_t pair[2][4];                          // the two warps of a slot's quarter of the rows
   uint64_t done;
   uint32_t tmem_base;
   int abort_flag, bad_page;
-  float swap[2][2][kSlotRows];                  // [slot][half]: what the two threads of a row tell each other
+  float m[kSlotRows], l[kSlotRows];             // keys mode: slot 1's, for slot 0 (m first: slot 0's scale)
 };
 
 template <bool INT8>
@@ -274,12 +273,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
       "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const float* v) {
-  uint32_t w[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
-  tmem_st32(addr, w);
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
@@ -565,10 +558,10 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
     tc_commit(&bars->s_full[slot]);
   };
   const auto pv = [&](int slot, const RingPos& q, bool first) {        // O[slot] (+)= P V
+    const uint32_t b = vd + q.stage * (kTile16 / 16);
     if (!mbar_wait_bounded(&bars->p_full[slot], np[slot] & 1, abort_flag)) return false;
     ++np[slot];
     tc_fence_after();
-    const uint32_t b = vd + q.stage * (kTile16 / 16);
 #pragma unroll
     for (int kk = 0; kk < kTileKeys / 16; ++kk)
       mma_ts(tmem + 256 + slot * 128, tmem + slot * 128 + (kk >> 2) * kHalf + (kk & 3) * 8, b + kk * (16 * 128 / 16), id_pv,
@@ -646,42 +639,53 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
 }
 
 // ---------------------------------------------------------------- softmax
+// y P(y^2) for N values, y = z * ys, P of K coefficients (highest first): K + 2
+// cycles of the multiply-add pipe a value (paired arithmetic; eight pairs side
+// by side, a chain of K + 2 dependent operations each).
+template <int N, int K>
+__device__ __forceinline__ void odd_poly(float* z, float ys, const float (&k)[K]) {
+  const auto both = [](float x) { return make_float2(x, x); };
+  const float2 y2 = both(ys), zero = both(0.f);
+#pragma unroll
+  for (int i = 0; i < N; i += 16) {
+    float2 y[8], t[8], a[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[e] = fma_f32x2(make_float2(z[i + 2 * e], z[i + 2 * e + 1]), y2, zero);
+      t[e] = fma_f32x2(y[e], y[e], zero);
+      a[e] = both(k[0]);
+    }
+#pragma unroll
+    for (int d = 1; d < K; ++d)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a[e] = fma_f32x2(a[e], t[e], both(k[d]));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a[e] = fma_f32x2(a[e], y[e], zero);
+      z[i + 2 * e] = a[e].x;
+      z[i + 2 * e + 1] = a[e].y;
+    }
+  }
+}
+
 // z (units of S, c log2-units each) -> cap * tanh(z c ln2 / cap) in log2 units.
-// Up to 0.7 in size the argument takes an odd polynomial (least maximum error
-// on [-0.7, 0.7], fitted for this: 1.2e-7 in fp32; paired arithmetic, 7 cycles
-// of the multiply-add pipe a value), beyond it tanh y = 1 - 2 / (1 + e^2y),
-// whose two special-function calls a value would be the kernel's bound.
+// Small arguments take odd polynomials fitted for the least maximum error, in
+// fp32 5e-7 of the range up to 0.35 and 1.2e-7 up to 0.7; larger ones
+// tanh y = 1 - 2 / (1 + e^2y), whose two special-function calls a value would
+// be the kernel's bound.
 template <int N>
 __device__ __forceinline__ void cap_scores(float* z, float c, float softcap) {
   const float cap = softcap * 1.4426950408889634f, ys = c / cap;
-  float far = 0.f;
+  float far[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < N; ++i) far = fmaxf(far, fabsf(z[i]));
-  if (__all_sync(0xffffffffu, far * ys <= 0.7f)) {
-    const auto both = [](float x) { return make_float2(x, x); };
-    const float2 y2 = both(ys), zero = both(0.f);
+  for (int i = 0; i < N; ++i) far[i & 3] = fmaxf(far[i & 3], fabsf(z[i]));
+  const float y = fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3])) * ys;
+  if (__all_sync(0xffffffffu, y <= 0.35f)) {
+    const float k[3] = {0.122480378f * cap, -0.3326841f * cap, 0.999990225f * cap};
+    odd_poly<N, 3>(z, ys, k);
+  } else if (__all_sync(0xffffffffu, y <= 0.7f)) {
     const float k[5] = {0.0131941866f * cap, -0.0501952581f * cap, 0.132574543f * cap, -0.333269745f * cap, 0.99999851f * cap};
-    // eight pairs side by side: a chain of seven dependent operations each
-#pragma unroll
-    for (int i = 0; i < N; i += 16) {
-      float2 y[8], t[8], a[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = fma_f32x2(make_float2(z[i + 2 * e], z[i + 2 * e + 1]), y2, zero);
-        t[e] = fma_f32x2(y[e], y[e], zero);
-        a[e] = both(k[0]);
-      }
-#pragma unroll
-      for (int d = 1; d < 5; ++d)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] = fma_f32x2(a[e], t[e], both(k[d]));
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[e] = fma_f32x2(a[e], y[e], zero);
-        z[i + 2 * e] = a[e].x;
-        z[i + 2 * e + 1] = a[e].y;
-      }
-    }
+    odd_poly<N, 5>(z, ys, k);
   } else {
     const float two = 2.0f * c / softcap;
 #pragma unroll
@@ -689,30 +693,43 @@ __device__ __forceinline__ void cap_scores(float* z, float c, float softcap) {
   }
 }
 
-// One slot's eight warps: a thread has half the columns of a row (64 of S, and
-// the same half of the query's and the output's dims); the two threads of a
-// row, in the warps `quarter` and `quarter` + 4 of the slot, swap their maxima
-// through shared memory. MOD: the scores are capped or get a bias.
+// The 32 columns of P (64 weights a row) at `addr` times f.
+template <bool F16>
+__device__ __forceinline__ void rescale_p(uint32_t addr, float f) {
+  tmem_st_wait();   // (this warp's own store of them)
+#pragma unroll 1
+  for (int i = 0; i < 32; i += 16) {
+    float v[16];
+    uint32_t w[16];
+    tmem_ld16(addr + i, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) asm volatile("" : "+f"(v[e]));
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint32_t u = __float_as_uint(v[e]);
+      const float2 x = F16 ? __half22float2(*reinterpret_cast<const __half2*>(&u))
+                           : make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+      w[e] = pack2<F16>(x.x * f, x.y * f);
+    }
+    tmem_st16(addr + i, w);
+  }
+}
+
+// One slot's four warps, one row a thread. MOD: the scores are capped or get a
+// bias.
+//
+// A row goes in two halves of 64 columns (code and registers for one). The
+// exponentials are formed with the running maximum as it was, next to the
+// half's own maximum; only where that calls for raising the former are they
+// formed again.
 template <bool QK_F16, bool PV_F16, bool INT8, bool MOD>
 __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint8_t* sQ,
-                                             const float* scales, int slot, int half, volatile int* abort_flag) {
-  const int tid = threadIdx.x & 127, quarter = tid >> 5;
-  const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-  const uint32_t tS = tmem + lane_addr + slot * 128 + half * kHalf, tO = tmem + lane_addr + 256 + slot * 128 + half * kHalf;
-  float* mine = &bars->swap[slot][half][tid];
-  const volatile float* theirs = &bars->swap[slot][half ^ 1][tid];
-  uint64_t* pair = &bars->pair[slot][quarter];
-  uint32_t ns = 0, no = 0, nml = 0, nseg = 0, npair = 0, tile_seq = 0;
-  // Swaps a value with the row's other thread. (A thread's next value is
-  // written after every thread of the slot has arrived at one of the barriers
-  // that the products wait for, so after this one was read.)
-  const auto swap = [&](float x, float* other) {
-    *mine = x;
-    mbar_arrive(pair);
-    if (!warp_wait(pair, npair++ & 1, abort_flag)) return false;
-    *other = *theirs;
-    return true;
-  };
+                                             const float* scales, int slot, volatile int* abort_flag) {
+  const int tid = threadIdx.x & 127;
+  const uint32_t lane_addr = static_cast<uint32_t>((tid >> 5) * 32) << 16;
+  const uint32_t tS = tmem + lane_addr + slot * 128, tO = tmem + lane_addr + 256 + slot * 128;
+  uint32_t ns = 0, no = 0, nml = 0, nseg = 0, tile_seq = 0;
   Walk walk(p);
   Segment s;
   while (walk.next(p, &s)) {
@@ -726,50 +743,44 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     const long long row = (static_cast<long long>(p.q0[s.w.b]) + tok) * p.Hq + head;   // query row
     float c = p.scale_log2;   // logits in units of log2 e per unit of S
     if (slot == 0 || s.rows_mode) {
-      uint8_t* dst = sQ + slot * kTile16 + half * kBlk + tid * 128;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row * DSA_HEAD_DIM + half * kHalf);
-      uint4 u[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+      uint8_t* dst = sQ + slot * kTile16 + tid * 128;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row * DSA_HEAD_DIM);
+      float f0 = 1.0f, f1 = 1.0f;   // the row is scaled by f0 f1
       if (QK_F16 && p.q_dtype == DSA_BF16) {
         // the row's largest exponent to 14: scaled by 2^-ex
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-        }
-        const uint4* rest = src + (half ? -8 : 8);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 v = valid ? __ldg(rest + i) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < 16; ++i) {
+          const uint4 u = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
         }
         const int ex = top >= 0x80u ? static_cast<int>(top >> 7) - 127 - 14 : -126 - 14;
-        // 2^-ex as two factors: it may lie outside fp32's normal range
-        const float f0 = __int_as_float((127 - ex / 2) << 23), f1 = __int_as_float((127 - (ex - ex / 2)) << 23);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        // (two factors: 2^-ex may lie outside fp32's normal range)
+        f0 = __int_as_float((127 - ex / 2) << 23);
+        f1 = __int_as_float((127 - (ex - ex / 2)) << 23);
+        c = ldexpf(c, ex);
+      }
+#pragma unroll 8
+      for (int i = 0; i < 16; ++i) {
+        uint4 u = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        if (QK_F16 && p.q_dtype == DSA_BF16) {
+          uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             w[e] = pack2<true>(__uint_as_float(w[e] << 16) * f0 * f1, __uint_as_float(w[e] & 0xffff0000u) * f0 * f1);
-          u[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          u = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        c = ldexpf(c, ex);
+        *reinterpret_cast<uint4*>(dst + (i >> 3) * kBlk + (((i & 7) ^ (tid & 7)) << 4)) = u;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(dst + ((i ^ (tid & 7)) << 4)) = u[i];
       fence_async_smem();
-      if (!s.rows_mode && half == 0) bars->swap[0][1][tid] = c;   // for slot 1
+      if (!s.rows_mode) bars->m[tid] = c;   // for slot 1
     }
     if (slot == 1 && !s.rows_mode) {
       // slot 0 loads the shared rows; what it scaled them by
       if (!warp_wait(&bars->q_ready[0], nseg & 1, abort_flag)) break;
-      c = *const_cast<const volatile float*>(&bars->swap[0][1][tid]);
+      c = *const_cast<const volatile float*>(&bars->m[tid]);
     }
     ++nseg;
     tc_fence_before();
@@ -780,10 +791,11 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     const int lo1 = imax(p.first[s.w.b], p.window > 0 ? pos1 - p.window + 1 : 0);   // the last row's
 
     float m = -INFINITY, l = 0.f;   // running maximum (in S units, or log2 units where c = 1), sum
+    const float cz = MOD ? 1.0f : c;
     bool ok = true;
     for (int j = 0; j < x.n; ++j) {
       const int t = x.first + j * x.step;
-      const int key0 = (s.w.tile0 + t) * kTileKeys;   // (of the tile)
+      const int key0 = (s.w.tile0 + t) * kTileKeys;
       if (!warp_wait(&bars->s_full[slot], ns & 1, abort_flag)) {
         ok = false;
         break;
@@ -797,30 +809,21 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
           break;
         }
       }
-      if (warp_valid) {
-        // kCols values of S at a time: the half row in registers, or (INT8, MOD)
-        // two passes over quarters, the first of which leaves what it made of S
-        // in place
-        constexpr int kCols = INT8 || MOD ? 32 : kHalf;
-        const float* sc = scales + ((tile_seq + (t - s.t0)) % kScaleRing) * 2 * kTileKeys + half * kHalf;
-        const bool masked = key0 + kTileKeys - 1 > pos0 || key0 < lo1;
-        const int first = key0 + half * kHalf;
-        const float cz = MOD ? 1.0f : c;
-        float z[kCols];
-        float mn = -INFINITY;
-        const auto load_s = [&](int col) {
-#pragma unroll
-          for (int i = 0; i < kCols; i += 32) tmem_ld32(tS + col + i, z + i);
+      const bool masked = key0 + kTileKeys - 1 > pos0 || key0 < lo1;
+      const float* sc = scales + ((tile_seq + (t - s.t0)) % kScaleRing) * 2 * kTileKeys;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        if (warp_valid) {
+          const int col = h * kHalf, first = key0 + col;
+          float z[kHalf];
+          tmem_ld32(tS + col, z);
+          tmem_ld32(tS + col + 32, z + 32);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < kCols; ++i) asm volatile("" : "+f"(z[i]));   // no use before the wait
-        };
-#pragma unroll 1
-        for (int col = 0; col < kHalf; col += kCols) {
-          load_s(col);
+          for (int i = 0; i < kHalf; ++i) asm volatile("" : "+f"(z[i]));   // no use before the wait
           if constexpr (INT8) {
 #pragma unroll
-            for (int i = 0; i < kCols; i += 4) {
+            for (int i = 0; i < kHalf; i += 4) {
               const float4 f = *reinterpret_cast<const float4*>(sc + col + i);
               z[i] *= f.x;
               z[i + 1] *= f.y;
@@ -829,122 +832,93 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
             }
           }
           if constexpr (MOD) {
-            if (p.softcap > 0.f) cap_scores<kCols>(z, c, p.softcap);
+            if (p.softcap > 0.f) cap_scores<kHalf>(z, c, p.softcap);
             else
 #pragma unroll
-              for (int i = 0; i < kCols; ++i) z[i] *= c;
+              for (int i = 0; i < kHalf; ++i) z[i] *= c;
             if (p.slopes) {
-              const float d = static_cast<float>(first + col - pos);
+              const float d = static_cast<float>(first - pos);
 #pragma unroll
-              for (int i = 0; i < kCols; ++i) z[i] = fmaf(slope, d + static_cast<float>(i), z[i]);
+              for (int i = 0; i < kHalf; ++i) z[i] = fmaf(slope, d + static_cast<float>(i), z[i]);
             }
           }
           if (masked) {
-            const int a = lo - first - col, b = pos - first - col;   // columns a .. b are visible
+            const int a = lo - first, b = pos - first;   // columns a .. b are visible
 #pragma unroll
-            for (int i = 0; i < kCols; ++i)
+            for (int i = 0; i < kHalf; ++i)
               if (i < a || i > b) z[i] = -INFINITY;
           }
-          float mt[4] = {z[0], z[1], z[2], z[3]};
-#pragma unroll
-          for (int i = 4; i < kCols; i += 4) {
-            mt[0] = fmaxf(mt[0], z[i]);
-            mt[1] = fmaxf(mt[1], z[i + 1]);
-            mt[2] = fmaxf(mt[2], z[i + 2]);
-            mt[3] = fmaxf(mt[3], z[i + 3]);
-          }
-          mn = fmaxf(mn, fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])));
-          if constexpr (kCols < kHalf) tmem_st32(tS + col, z);
-        }
-        if constexpr (kCols < kHalf) tmem_st_wait();
-        float other = -INFINITY;
-        if (!swap(mn, &other)) {
-          ok = false;
-          break;
-        }
-        mn = fmaxf(mn, other);
-        // (-inf stays as it is: nothing seen yet; both halves come to the same answer)
-        const bool raise = mn > m && (m == -INFINITY || (mn - m) * cz > kRaise);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float to = fmaxf(m, mn);
-          const float f = to == -INFINITY || m == -INFINITY ? (m == to ? 1.0f : 0.0f) : fast_exp2((m - to) * cz);
-          m = to;
-          l *= f;
-          if (j > 0) {
+          uint32_t w[32];
+          float2 sum[2];
 #pragma unroll 1
-            for (int i = 0; i < kHalf; i += 16) {
-              float o[16];
-              uint32_t w[16];
-              tmem_ld16(tO + i, o);
-              tmem_ld_wait();
+          while (true) {
+            const float mc = m == -INFINITY ? 0.f : kLift - m * cz;
+            sum[0] = sum[1] = make_float2(0.f, 0.f);
+            const float2 c2 = make_float2(cz, cz), m2 = make_float2(mc, mc);
+            float mt[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
-              for (int e = 0; e < 16; ++e) asm volatile("" : "+f"(o[e]));
-#pragma unroll
-              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
-              tmem_st16(tO + i, w);
-            }
-          }
-        }
-        const float mc = m == -INFINITY ? 0.f : kLift - m * cz;
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float2 c2 = make_float2(cz, cz), m2 = make_float2(mc, mc);
-#pragma unroll 1
-        for (int col = 0; col < kHalf; col += kCols) {
-          if constexpr (kCols < kHalf) load_s(col);
-#pragma unroll
-          for (int h = 0; h < kCols; h += 32) {
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; i += 8) {
+            for (int i = 0; i < 32; i += 8) {
               float2 pr[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) pr[e] = fma_f32x2(make_float2(z[h + 2 * (i + e)], z[h + 2 * (i + e) + 1]), c2, m2);
+              for (int e = 0; e < 8; ++e) pr[e] = fma_f32x2(make_float2(z[2 * (i + e)], z[2 * (i + e) + 1]), c2, m2);
 #pragma unroll
               for (int e = 0; e < 8; ++e) pr[e] = make_float2(fast_exp2(pr[e].x), fast_exp2(pr[e].y));
+#pragma unroll
+              for (int e = 0; e < 16; ++e) mt[e & 3] = fmaxf(mt[e & 3], z[2 * i + e]);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 sum[e & 1] = add_f32x2(pr[e], sum[e & 1]);
                 if constexpr (INT8) {
-                  const float2 vs = *reinterpret_cast<const float2*>(sc + kTileKeys + col + h + 2 * (i + e));
+                  const float2 vs = *reinterpret_cast<const float2*>(sc + kTileKeys + col + 2 * (i + e));
                   pr[e] = fma_f32x2(pr[e], vs, make_float2(0.f, 0.f));
                 }
                 w[i + e] = pack2<PV_F16>(pr[e].x, pr[e].y);
               }
             }
-            tmem_st16(tS + (col + h) / 2, w);   // over columns of S that have been read
+            const float mn = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+            // (-inf stays as it is: nothing seen yet)
+            const bool raise = mn > m && (m == -INFINITY || (mn - m) * cz > kRaise);
+            if (!__any_sync(0xffffffffu, raise)) break;
+            const float to = fmaxf(m, mn);
+            const float f = to == -INFINITY || m == -INFINITY ? (m == to ? 1.0f : 0.0f) : fast_exp2((m - to) * cz);
+            m = to;
+            l *= f;
+            if (h == 1) rescale_p<PV_F16>(tS, f);   // the first half's, not yet in O
+            if (j > 0) {
+#pragma unroll 1
+              for (int i = 0; i < DSA_HEAD_DIM; i += 16) {
+                float o[16];
+                uint32_t v[16];
+                tmem_ld16(tO + i, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) asm volatile("" : "+f"(o[e]));
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(o[e] * f);
+                tmem_st16(tO + i, v);
+              }
+            }
           }
+          tmem_st32(tS + col, w);   // over columns of S that have been read
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        tmem_st_wait();
       }
+      if (warp_valid) tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&bars->p_full[slot]);
     }
     if (!ok) break;
     tile_seq += s.t1 - s.t0;
-    const float cz = MOD ? 1.0f : c;
     const float m_log2 = m == -INFINITY ? -INFINITY : m * cz;
     if (x.n > 0) {
       if (!warp_wait(&bars->o_full[slot], no & 1, abort_flag)) break;
       ++no;
       tc_fence_after();
-      if (warp_valid) {
-        float other = 0.f;
-        if (!swap(l, &other)) break;
-        l = half ? other + l : l + other;   // the same sum in both
-      }
     }
     if (!s.rows_mode && slot == 1) {
-      // slot 0 joins the two states; it reads this slot's O itself. (The swap
-      // before is over in both threads before its places are used again.)
-      if (x.n > 0 && warp_valid) {
-        mbar_arrive(pair);
-        if (!warp_wait(pair, npair++ & 1, abort_flag)) break;
-      }
-      if (half == 0) {
-        bars->swap[1][0][tid] = m_log2;
-        bars->swap[1][1][tid] = l;
-      }
+      // slot 0 joins the two states; it reads this slot's O itself
+      bars->m[tid] = m_log2;
+      bars->l[tid] = l;
       mbar_arrive(&bars->ml);
       continue;
     }
@@ -956,7 +930,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
       tc_fence_after();
       other = slot_work(s, 1).n > 0;
       if (other) {
-        const volatile float* v = &bars->swap[1][0][tid];
+        const volatile float* v = &bars->m[tid];
         const float m1 = v[0], l1 = v[kSlotRows];
         mj = fmaxf(m_log2, m1);
         f0 = m_log2 == -INFINITY ? 0.f : fast_exp2(m_log2 - mj);
@@ -969,66 +943,62 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     float* part = nullptr;
     if (s.whole) {
       norm = lj > 0.f ? 1.0f / lj : 0.f;
-      if (valid && half == 0 && p.lse)
-        p.lse[row] = lj > 0.f ? (mj - kLift + log2f(lj)) * 0.6931471805599453f : -INFINITY;
+      if (valid && p.lse) p.lse[row] = lj > 0.f ? (mj - kLift + log2f(lj)) * 0.6931471805599453f : -INFINITY;
     } else {
       part = p.partial + static_cast<long long>(s.part) * p.part_rows * (DSA_HEAD_DIM + 2);
       const int pr = r - s.w.row0;
-      if (valid && half == 0) {
-        part[p.part_rows * DSA_HEAD_DIM + 2 * pr] = mj;
-        part[p.part_rows * DSA_HEAD_DIM + 2 * pr + 1] = lj;
-      }
-      part += pr * DSA_HEAD_DIM + half * kHalf;
+      if (valid) *reinterpret_cast<float2*>(part + p.part_rows * DSA_HEAD_DIM + 2 * pr) = make_float2(mj, lj);
+      part += pr * DSA_HEAD_DIM;
     }
     f0 *= norm;
     f1 *= norm;
 #pragma unroll 1
-    for (int i = 0; i < kHalf; i += 16) {
-      float o[16];
+    for (int i = 0; i < DSA_HEAD_DIM; i += 32) {
+      float o[32];
       if (x.n > 0) {
-        tmem_ld16(tO + i, o);
+        tmem_ld32(tO + i, o);
         if (other) {
-          float b[16];
-          tmem_ld16(tO + 128 + i, b);
+          float b[32];
+          tmem_ld32(tO + 128 + i, b);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) asm volatile("" : "+f"(o[e]), "+f"(b[e]));
+          for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(o[e]), "+f"(b[e]));
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = f0 * o[e] + f1 * b[e];
+          for (int e = 0; e < 32; ++e) o[e] = f0 * o[e] + f1 * b[e];
         } else {
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) asm volatile("" : "+f"(o[e]));
+          for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(o[e]));
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] *= f0;
+          for (int e = 0; e < 32; ++e) o[e] *= f0;
         }
         // a row without a key: whatever the products hold, its output is 0
         if (s.whole && !(lj > 0.f)) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = 0.f;
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = 0.f;
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
       }
       if (!valid) continue;
       if (part) {
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
+        for (int e = 0; e < 32; e += 4)
           *reinterpret_cast<float4*>(part + i + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       } else if (p.out_dtype == DSA_FP32) {
-        float* d = static_cast<float*>(p.out) + row * DSA_HEAD_DIM + half * kHalf + i;
+        float* d = static_cast<float*>(p.out) + row * DSA_HEAD_DIM + i;
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
+        for (int e = 0; e < 32; e += 4)
           *reinterpret_cast<float4*>(d + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       } else {
-        uint16_t* d = static_cast<uint16_t*>(p.out) + row * DSA_HEAD_DIM + half * kHalf + i;
-        uint32_t w[8];
+        uint16_t* d = static_cast<uint16_t*>(p.out) + row * DSA_HEAD_DIM + i;
+        uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < 16; ++e)
           w[e] = p.out_dtype == DSA_FP16 ? pack2<true>(o[2 * e], o[2 * e + 1]) : pack2<false>(o[2 * e], o[2 * e + 1]);
-        *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(d + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) *reinterpret_cast<uint4*>(d + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
       }
     }
   }
@@ -1068,37 +1038,34 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
       mbar_init(&bars->raw_empty[i], kWidenThreads);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->q_ready[i], 256);
+      mbar_init(&bars->q_ready[i], 128);
       mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_full[i], 256);
+      mbar_init(&bars->p_full[i], 128);
       mbar_init(&bars->o_full[i], 1);
-      for (int k = 0; k < 4; ++k) mbar_init(&bars->pair[i][k], 64);
     }
     for (int i = 0; i < kScaleRing; ++i) mbar_init(&bars->scales[i], 32);
     mbar_init(&bars->fix, 1);
-    mbar_init(&bars->ml, 256);
+    mbar_init(&bars->ml, 128);
     mbar_init(&bars->done, 1);
     bars->abort_flag = 0;
     bars->bad_page = 0;
     fence_mbar_init();
   }
-  if (warp == 16) tmem_alloc(&bars->tmem_base, kTmemCols);
+  if (warp == 8) tmem_alloc(&bars->tmem_base, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
   pdl_trigger();
-  // registers: the launch gives every thread the same number; the softmax
-  // threads hold half a row of S and take what the others give up
-  if (warp < 16) {
-    regs_up<INT8 ? kSoftRegs8 : kSoftRegs16>();
-    softmax_role<QK_F16, PV_F16, INT8, MOD>(p, bars, tmem, sQ, scales, warp >> 3, (warp >> 2) & 1, abort_flag);
-  } else if (warp < 20) {
-    regs_down<INT8 ? kMiscRegs8 : kMiscRegs16>();
-    if (warp == 16) {
+  if (warp < 8) {
+    if constexpr (INT8) regs_up<kSoftRegs8>();
+    softmax_role<QK_F16, PV_F16, INT8, MOD>(p, bars, tmem, sQ, scales, warp >> 2, abort_flag);
+  } else if (warp < 12) {
+    if constexpr (INT8) regs_down<kMiscRegs8>();
+    if (warp == 8) {
       if ((threadIdx.x & 31) == 0)
         mma_role<QK_F16, PV_F16>(p, bars, tmem, smem_u32(sQ), smem_u32(ring), stages, abort_flag);
-    } else if (warp == 17) {
+    } else if (warp == 9) {
       load_role<INT8>(p, tm_k, tm_v, bars, INT8 ? raw : ring, INT8 ? raw_stages : stages, scales, abort_flag);
     }
   } else {
@@ -1110,7 +1077,7 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 8) tmem_dealloc(tmem, kTmemCols);
   if (threadIdx.x == 0)
     p.errors[blockIdx.x] = (bars->abort_flag ? kDevTimeout : 0u) | (bars->bad_page ? kDevBadPage : 0u);
 }
@@ -1344,7 +1311,7 @@ cudaError_t launch_full(bool mod, int blocks, const CUtensorMap& tm_k, const CUt
   if (regs.load(std::memory_order_relaxed) == 0) {
     cudaFuncAttributes a;
     if ((e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(kern))) != cudaSuccess) return e;
-    if (a.numRegs * (INT8 ? kThreads8 : kThreads16) < kRegs<INT8>) return cudaErrorInvalidConfiguration;
+    if (INT8 && a.numRegs * kThreads8 < kRegs8) return cudaErrorInvalidConfiguration;
     regs.store(a.numRegs, std::memory_order_relaxed);
   }
   return launch_kernel("full_attn_kernel", kern, dim3(blocks), dim3(INT8 ? kThreads8 : kThreads16), smem, st, false,
