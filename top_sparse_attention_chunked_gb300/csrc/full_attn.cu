@@ -745,34 +745,40 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     if (slot == 0 || s.rows_mode) {
       uint8_t* dst = sQ + slot * kTile16 + tid * 128;
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row * DSA_HEAD_DIM);
-      float f0 = 1.0f, f1 = 1.0f;   // the row is scaled by f0 f1
-      if (QK_F16 && p.q_dtype == DSA_BF16) {
-        // the row's largest exponent to 14: scaled by 2^-ex
-        uint32_t top = 0;
+      // (no INT8 call converts its query; a 16-bit call has registers for a row)
+      constexpr int kBatch = INT8 ? 8 : 16;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint4 u = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      for (int i0 = 0; i0 < 16; i0 += kBatch) {
+        uint4 u[kBatch];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        for (int i = 0; i < kBatch; ++i) u[i] = valid ? __ldg(src + i0 + i) : make_uint4(0, 0, 0, 0);
+        if constexpr (QK_F16 && !INT8) {
+          if (p.q_dtype == DSA_BF16) {
+            // the row's largest exponent to 14: scaled by 2^-ex
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+            }
+            const int ex = top >= 0x80u ? static_cast<int>(top >> 7) - 127 - 14 : -126 - 14;
+            // (two factors: 2^-ex may lie outside fp32's normal range)
+            const float f0 = __int_as_float((127 - ex / 2) << 23), f1 = __int_as_float((127 - (ex - ex / 2)) << 23);
+            c = ldexpf(c, ex);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack2<true>(__uint_as_float(w[e] << 16) * f0 * f1, __uint_as_float(w[e] & 0xffff0000u) * f0 * f1);
+              u[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
         }
-        const int ex = top >= 0x80u ? static_cast<int>(top >> 7) - 127 - 14 : -126 - 14;
-        // (two factors: 2^-ex may lie outside fp32's normal range)
-        f0 = __int_as_float((127 - ex / 2) << 23);
-        f1 = __int_as_float((127 - (ex - ex / 2)) << 23);
-        c = ldexpf(c, ex);
-      }
-#pragma unroll 8
-      for (int i = 0; i < 16; ++i) {
-        uint4 u = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-        if (QK_F16 && p.q_dtype == DSA_BF16) {
-          uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack2<true>(__uint_as_float(w[e] << 16) * f0 * f1, __uint_as_float(w[e] & 0xffff0000u) * f0 * f1);
-          u = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        *reinterpret_cast<uint4*>(dst + (i >> 3) * kBlk + (((i & 7) ^ (tid & 7)) << 4)) = u;
+        for (int i = 0; i < kBatch; ++i)
+          *reinterpret_cast<uint4*>(dst + ((i0 + i) >> 3) * kBlk + ((((i0 + i) & 7) ^ (tid & 7)) << 4)) = u[i];
       }
       fence_async_smem();
       if (!s.rows_mode) bars->m[tid] = c;   // for slot 1
@@ -1124,19 +1130,35 @@ __global__ void __launch_bounds__(kMergeThreads)
     const long long pitch = static_cast<long long>(mp.part_rows) * (DSA_HEAD_DIM + 2);
     const auto part_of = [&](int c) { return mp.partial + (2 * c + (c == c0 ? 1 : 0)) * pitch; };
     const long long ml = static_cast<long long>(mp.part_rows) * DSA_HEAD_DIM + 2 * pr;
-    for (int c = c0 + sub; c <= c1; c += mp.wpr) m = fmaxf(m, __ldcg(part_of(c) + ml));
-#pragma unroll 4
-    for (int c = c0 + sub; c <= c1; c += mp.wpr) {
-      const float* q = part_of(c);
-      const float2 x = __ldcg(reinterpret_cast<const float2*>(q + ml));
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(q + pr * DSA_HEAD_DIM) + lane);
-      if (x.x == -INFINITY) continue;
-      const float f = fast_exp2(x.x - m);
-      l = fmaf(x.y, f, l);
-      o.x = fmaf(y.x, f, o.x);
-      o.y = fmaf(y.y, f, o.y);
-      o.z = fmaf(y.z, f, o.z);
-      o.w = fmaf(y.w, f, o.w);
+    // four parts at a time: all their loads in flight together
+    for (int c = c0 + sub; c <= c1; c += 4 * mp.wpr) {
+      float2 x[4];
+      float4 y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int ck = c + k * mp.wpr;
+        x[k] = make_float2(-INFINITY, 0.f);
+        if (ck > c1) continue;
+        const float* q = part_of(ck);
+        x[k] = __ldcg(reinterpret_cast<const float2*>(q + ml));
+        y[k] = __ldcg(reinterpret_cast<const float4*>(q + pr * DSA_HEAD_DIM) + lane);
+      }
+      const float to = fmaxf(m, fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)));
+      if (to == -INFINITY) continue;
+      const float old = m == -INFINITY ? 0.f : fast_exp2(m - to);
+      l *= old;
+      o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+      m = to;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (x[k].x == -INFINITY) continue;
+        const float f = fast_exp2(x[k].x - m);
+        l = fmaf(x[k].y, f, l);
+        o.x = fmaf(y[k].x, f, o.x);
+        o.y = fmaf(y[k].y, f, o.y);
+        o.z = fmaf(y[k].z, f, o.z);
+        o.w = fmaf(y[k].w, f, o.w);
+      }
     }
   }
   if (mp.wpr > 1) {
@@ -1220,7 +1242,7 @@ int check_full(const dsa_full_problem* p) {
 
 // Costs of a unit, in quarters of a tile of 256 rows: a tile of up to 128 rows
 // takes the same loads and half the products; an item, its queries and output.
-constexpr int kCostRows = 4, kCostKeys = 3, kCostItem = 6;
+constexpr int kCostRows = 4, kCostKeys = 3, kCostItem = 12;
 
 // Lays the items out over the blocks (fp: the problem and the runs, mp: the
 // items that are split) and returns the number of blocks.
@@ -1284,7 +1306,7 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
     }
     parts = imax(parts, c - mp->first_cta[mp->splits - 1] + 1);
   }
-  mp->wpr = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;
+  mp->wpr = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;   // four loads a lane in flight, at most eight warps
   return blocks;
 }
 

@@ -7,7 +7,7 @@
 // by scanning the counts, so the new state is a function of the old one alone
 // (lowest index first), whatever the order in which the threads run.
 //
-// dsa_pages_update, four launches:
+// dsa_pages_update, four launches (steps 1 to 3 in one where one block does them):
 //   1. the scratch (count changes, writers per block, a flag) is cleared;
 //   2. pages_count_kernel, one thread per table entry: the entry's old block
 //      loses a holder, the block it takes from its parent row gains one (an
@@ -41,6 +41,9 @@ namespace {
 constexpr int kPgThreads = 256;
 constexpr int kPlanThreads = 1024;
 constexpr int kCopyUnroll = 8;
+// States that one block counts by itself, sums in shared memory: up to this many
+// table entries and blocks.
+constexpr int kSmallEntries = 8192, kSmallBlocks = 8192;
 constexpr long long kPiece = kPgThreads * 16LL * kCopyUnroll;   // bytes of one copy task
 
 struct PageDims {
@@ -104,48 +107,67 @@ __device__ __forceinline__ int ceil_shift(int n, int shift) {
 }
 
 // ------------------------------------------------------------------ update
-__global__ void __launch_bounds__(kPgThreads)
-    pages_count_kernel(const PageDims d, const PageWs w, const int32_t* __restrict__ table,
-                       const int32_t* __restrict__ parent, const int32_t* __restrict__ keep_len,
-                       const int32_t* __restrict__ new_len, const int32_t* __restrict__ first_key) {
-  pdl_wait();   // the cleared scratch
-  const long long n = static_cast<long long>(d.rows) * d.W;
-  const long long most = static_cast<long long>(d.W) << d.shift;
-  for (long long e = static_cast<long long>(blockIdx.x) * kPgThreads + threadIdx.x; e < n;
-       e += static_cast<long long>(gridDim.x) * kPgThreads) {
-    const int r = static_cast<int>(e / d.W), j = static_cast<int>(e - static_cast<long long>(r) * d.W);
-    const int old = table[e];
-    const int p = parent[r], keep = keep_len[r], grown = new_len[r];
-    const int drop = first_key ? first_key[r] : 0;
-    bool bad = old >= d.nb || p < -1 || p >= d.rows || keep < 0 || grown < keep || grown > most ||
-               (p < 0 && keep != 0) || drop < 0 || drop > keep;
-    int got = -1;
-    if (!bad) {
-      const int kept = ceil_shift(keep, d.shift);
-      if (j < kept && j >= (drop >> d.shift)) {
-        got = table[static_cast<long long>(p) * d.W + j];
-        if (got < 0) got = -1;
-        if (got >= d.nb) {
-          bad = true;
-          got = -1;
-        }
-      }
-      if (j == kept - 1 && grown > keep && (keep & ((1 << d.shift) - 1)) != 0) {
-        if (got < 0) {
-          bad = true;            // nothing there to write into
-        } else {
-          atomicAdd(w.writers + got, 1);
-          atomicMax(w.low + got, d.rows - r);
-        }
+// What the count step adds up, in the workspace or (small states) in shared
+// memory.
+struct Counts {
+  uint32_t* flag;
+  int32_t* delta;
+  int32_t* writers;
+  int32_t* low;
+};
+
+struct Rows {   // the caller's row arguments
+  const int32_t* __restrict__ parent;
+  const int32_t* __restrict__ keep_len;
+  const int32_t* __restrict__ new_len;
+  const int32_t* __restrict__ first_key;
+};
+
+// Table entry e.
+__device__ __forceinline__ void count_entry(const PageDims& d, const Counts& c, int32_t* stage, const Rows& a,
+                                            const int32_t* __restrict__ table, int e) {
+  const int most = d.W << d.shift;   // (below 2^31, checked)
+  const int r = e / d.W, j = e - r * d.W;
+  const int old = table[e];
+  const int p = a.parent[r], keep = a.keep_len[r], grown = a.new_len[r];
+  const int drop = a.first_key ? a.first_key[r] : 0;
+  bool bad = old >= d.nb || p < -1 || p >= d.rows || keep < 0 || grown < keep || grown > most ||
+             (p < 0 && keep != 0) || drop < 0 || drop > keep;
+  int got = -1;
+  if (!bad) {
+    const int kept = ceil_shift(keep, d.shift);
+    if (j < kept && j >= (drop >> d.shift)) {
+      got = p == r ? old : table[p * d.W + j];
+      if (got < 0) got = -1;
+      if (got >= d.nb) {
+        bad = true;
+        got = -1;
       }
     }
-    w.stage[e] = got;
-    if (bad) *w.flag = 1u;
-    if (old != got) {
-      if (old >= 0 && old < d.nb) atomicAdd(w.delta + old, -1);
-      if (got >= 0) atomicAdd(w.delta + got, 1);
+    if (j == kept - 1 && grown > keep && (keep & ((1 << d.shift) - 1)) != 0) {
+      if (got < 0) {
+        bad = true;            // nothing there to write into
+      } else {
+        atomicAdd(c.writers + got, 1);
+        atomicMax(c.low + got, d.rows - r);
+      }
     }
   }
+  stage[e] = got;
+  if (bad) *c.flag = 1u;
+  if (old != got) {
+    if (old >= 0 && old < d.nb) atomicAdd(c.delta + old, -1);
+    if (got >= 0) atomicAdd(c.delta + got, 1);
+  }
+}
+
+__global__ void __launch_bounds__(kPgThreads)
+    pages_count_kernel(const PageDims d, const PageWs w, const Rows a, const int32_t* __restrict__ table) {
+  pdl_wait();   // the cleared scratch
+  const Counts c{w.flag, w.delta, w.writers, w.low};
+  const int n = d.rows * d.W;
+  for (int e = blockIdx.x * kPgThreads + threadIdx.x; e < n; e += gridDim.x * kPgThreads)
+    count_entry(d, c, w.stage, a, table, e);
 }
 
 // The calling warp's slice of the blocks.
@@ -173,15 +195,14 @@ __device__ __forceinline__ int warp_prefix(int v, int* tot, int* sum) {
   return __shfl_sync(0xffffffffu, x, wid) - v;
 }
 
-__global__ void __launch_bounds__(kPlanThreads)
-    pages_plan_kernel(const PageDims d, const PageWs w, const int32_t* refs,
-                      const int32_t* __restrict__ parent, const int32_t* __restrict__ keep_len,
-                      const int32_t* __restrict__ new_len, int32_t* refs_out, int32_t* counts) {
+// One block: the rows' copies and fresh blocks, the list of free blocks, the
+// new counts.
+__device__ __forceinline__ void plan_update(const PageDims& d, const PageWs& w, const Counts& c, const Rows& a,
+                                            const int32_t* refs, int32_t* refs_out, int32_t* counts) {
   __shared__ uint32_t scan_tot[32];
   __shared__ int warp_tot[32];
-  pdl_wait();
   const int lane = threadIdx.x & 31;
-  const bool bad = *w.flag != 0;
+  const bool bad = *c.flag != 0;
   bool fail = bad;
   // rows: who copies, how many blocks each wants, where its share begins
   uint32_t wanted = 0, copies = 0;   // so far
@@ -190,12 +211,12 @@ __global__ void __launch_bounds__(kPlanThreads)
     uint32_t want = 0, copy = 0;
     int from = 0;
     if (r < d.rows && !fail) {
-      const int keep = keep_len[r], grown = new_len[r];
+      const int keep = a.keep_len[r], grown = a.new_len[r];
       const int kept = ceil_shift(keep, d.shift);
       if (grown > keep && (keep & ((1 << d.shift) - 1)) != 0) {
-        const int t = w.stage[static_cast<long long>(r) * d.W + kept - 1];
-        const int n = w.writers[t];
-        copy = !(refs[t] + w.delta[t] == n && d.rows - w.low[t] == r);
+        const int t = w.stage[r * d.W + kept - 1];
+        const int n = c.writers[t];
+        copy = !(refs[t] + c.delta[t] == n && d.rows - c.low[t] == r);
       }
       from = kept - static_cast<int>(copy);
       want = static_cast<uint32_t>(ceil_shift(grown, d.shift) - from);
@@ -218,7 +239,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 #pragma unroll 4
   for (int b = lo; b < hi; b += 32) {
     const int r = b + lane < hi ? refs[b + lane] : 1;
-    const int n = b + lane < hi ? r + w.delta[b + lane] : 1;
+    const int n = b + lane < hi ? r + c.delta[b + lane] : 1;
     mine += __popc(__ballot_sync(0xffffffffu, n == 0));
     mine_before += __popc(__ballot_sync(0xffffffffu, r == 0));
   }
@@ -230,7 +251,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   for (int b = lo; b < hi; b += 32) {
     const bool in = b + lane < hi;
     const int old = in ? refs[b + lane] : 1;
-    int n = in ? old + w.delta[b + lane] : 1;
+    int n = in ? old + c.delta[b + lane] : 1;
     const uint32_t m = __ballot_sync(0xffffffffu, n == 0);
     if (n == 0) {
       const int k = rank + __popc(m & ((1u << lane) - 1u));
@@ -238,7 +259,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       if (k < static_cast<int>(wanted)) n = 1;
     } else if (in) {
       // its writers that copy let go of it
-      const int wr = w.writers[b + lane];
+      const int wr = c.writers[b + lane];
       n -= wr - (wr > 0 && n == wr ? 1 : 0);
     }
     rank += __popc(m);
@@ -253,6 +274,29 @@ __global__ void __launch_bounds__(kPlanThreads)
       counts[1] = fail ? nbefore : nfree - static_cast<int>(wanted);
     }
   }
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+    pages_plan_kernel(const PageDims d, const PageWs w, const Rows a, const int32_t* refs, int32_t* refs_out,
+                      int32_t* counts) {
+  pdl_wait();
+  plan_update(d, w, Counts{w.flag, w.delta, w.writers, w.low}, a, refs, refs_out, counts);
+}
+
+// Small states: the count and the plan in one block, the sums in shared memory
+// (cleared here). One launch in place of three.
+__global__ void __launch_bounds__(kPlanThreads)
+    pages_small_kernel(const PageDims d, const PageWs w, const Rows a, const int32_t* __restrict__ table,
+                       const int32_t* refs, int32_t* refs_out, int32_t* counts) {
+  extern __shared__ int32_t sums[];   // 3 * nb + 1
+  const Counts c{reinterpret_cast<uint32_t*>(sums + 3 * d.nb), sums, sums + d.nb, sums + 2 * d.nb};
+  pdl_trigger();
+  for (int i = threadIdx.x; i <= 3 * d.nb; i += kPlanThreads) sums[i] = 0;
+  __syncthreads();
+  const int n = d.rows * d.W;
+  for (int e = threadIdx.x; e < n; e += kPlanThreads) count_entry(d, c, w.stage, a, table, e);
+  __syncthreads();
+  plan_update(d, w, c, a, refs, refs_out, counts);
 }
 
 // Copy task t of `src` -> `dst` in every pool: one piece of one pool's block.
@@ -286,17 +330,14 @@ __global__ void __launch_bounds__(kPgThreads)
                         const int32_t* table, const int32_t* __restrict__ new_len, int32_t* table_out) {
   pdl_wait();
   const int copies = w.head[0];
-  const long long n = static_cast<long long>(d.rows) * d.W;
+  const int n = d.rows * d.W;
   if (copies < 0) {   // refused: the new table is the old one
     if (table_out != table)
-      for (long long e = static_cast<long long>(blockIdx.x) * kPgThreads + threadIdx.x; e < n;
-           e += static_cast<long long>(gridDim.x) * kPgThreads)
-        table_out[e] = table[e];
+      for (int e = blockIdx.x * kPgThreads + threadIdx.x; e < n; e += gridDim.x * kPgThreads) table_out[e] = table[e];
     return;
   }
-  for (long long e = static_cast<long long>(blockIdx.x) * kPgThreads + threadIdx.x; e < n;
-       e += static_cast<long long>(gridDim.x) * kPgThreads) {
-    const int r = static_cast<int>(e / d.W), j = static_cast<int>(e - static_cast<long long>(r) * d.W);
+  for (int e = blockIdx.x * kPgThreads + threadIdx.x; e < n; e += gridDim.x * kPgThreads) {
+    const int r = e / d.W, j = e - r * d.W;
     const int from = w.from[r];
     int v = -1;
     if (j < from) v = w.stage[e];
@@ -308,30 +349,40 @@ __global__ void __launch_bounds__(kPgThreads)
   for (long long t = blockIdx.x; t < tasks; t += gridDim.x) {
     const int c = static_cast<int>(t / per);
     const int r = w.copy_row[c];
-    const int src = w.stage[static_cast<long long>(r) * d.W + w.from[r]];
+    const int src = w.stage[r * d.W + w.from[r]];
     copy_piece(pools, static_cast<int>(t - static_cast<long long>(c) * per), src, w.free_ids[w.off[r]]);
   }
 }
 
 // ----------------------------------------------------------------- compact
+__device__ __forceinline__ bool bad_entry(const PageDims& d, int x, const int32_t* __restrict__ refs) {
+  return x >= 0 && (x >= d.nb || refs[x] <= 0);
+}
+
 __global__ void __launch_bounds__(kPgThreads)
     pages_check_kernel(const PageDims d, const PageWs w, const int32_t* __restrict__ table,
                        const int32_t* __restrict__ refs) {
-  const long long n = static_cast<long long>(d.rows) * d.W;
-  for (long long e = static_cast<long long>(blockIdx.x) * kPgThreads + threadIdx.x; e < n;
-       e += static_cast<long long>(gridDim.x) * kPgThreads) {
-    const int x = table[e];
-    if (x >= 0 && (x >= d.nb || refs[x] <= 0)) *w.flag = 1u;
-  }
+  pdl_wait();   // the cleared flag
+  const int n = d.rows * d.W;
+  for (int e = blockIdx.x * kPgThreads + threadIdx.x; e < n; e += gridDim.x * kPgThreads)
+    if (bad_entry(d, table[e], refs)) *w.flag = 1u;
 }
 
+// `table` is given where the block checks the entries itself (small states).
 __global__ void __launch_bounds__(kPlanThreads)
-    compact_plan_kernel(const PageDims d, const PageWs w, const int32_t* refs, int32_t* refs_out,
-                        int32_t* remap_out, int32_t* counts) {
+    compact_plan_kernel(const PageDims d, const PageWs w, const int32_t* table, const int32_t* refs,
+                        int32_t* refs_out, int32_t* remap_out, int32_t* counts) {
   __shared__ int warp_tot[32];
-  pdl_wait();
+  pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const bool fail = *w.flag != 0;
+  bool fail = false;
+  if (table) {
+    for (int e = threadIdx.x; e < d.rows * d.W; e += kPlanThreads) fail = fail || bad_entry(d, table[e], refs);
+    fail = __syncthreads_or(fail);
+  } else {
+    pdl_wait();
+    fail = *w.flag != 0;
+  }
   int lo, hi;
   warp_slice(d.nb, &lo, &hi);
   int mine = 0;
@@ -398,10 +449,9 @@ __global__ void __launch_bounds__(kPgThreads)
                           const int32_t* table, int32_t* table_out) {
   pdl_wait();
   const int moves = w.head[0];
-  const long long n = static_cast<long long>(d.rows) * d.W;
+  const int n = d.rows * d.W;
   if (moves >= 0 || table_out != table)
-    for (long long e = static_cast<long long>(blockIdx.x) * kPgThreads + threadIdx.x; e < n;
-         e += static_cast<long long>(gridDim.x) * kPgThreads) {
+    for (int e = blockIdx.x * kPgThreads + threadIdx.x; e < n; e += gridDim.x * kPgThreads) {
       const int x = table[e];
       table_out[e] = moves < 0 || x < 0 ? x : w.remap[x];
     }
@@ -485,6 +535,8 @@ int check_common(const dsa_page_state* st, const PageDims& d, int num_pools, con
   return check_call_workspace(ws, ws_bytes, page_ws(nullptr, d).total);
 }
 
+bool small_state(const PageDims& d) { return d.rows * d.W <= kSmallEntries && d.nb <= kSmallBlocks; }
+
 unsigned entry_grid(const PageDims& d, int sms) {
   const long long n = (static_cast<long long>(d.rows) * d.W + kPgThreads - 1) / kPgThreads;
   return static_cast<unsigned>(std::min<long long>(n, 8LL * sms));
@@ -534,13 +586,23 @@ extern "C" int dsa_pages_update(const dsa_page_state* st, const int32_t* parent,
   if (int rc = current_device(&sms)) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const PageWs w = page_ws(ws, d);
-  cudaError_t e = launch_zero_scratch(w.flag, w.zero_bytes, s);
-  if (e == cudaSuccess)
-    e = launch_kernel("pages_count_kernel", pages_count_kernel, dim3(entry_grid(d, sms)), dim3(kPgThreads), 0, s,
-                      true, d, w, st->block_table, parent, keep_len, new_len, first_key);
-  if (e == cudaSuccess)
-    e = launch_kernel("pages_plan_kernel", pages_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, true, d, w,
-                      st->refs, parent, keep_len, new_len, refs_out, counts);
+  const Rows rows{parent, keep_len, new_len, first_key};
+  cudaError_t e;
+  if (small_state(d)) {
+    const int smem = (3 * d.nb + 1) * 4;
+    e = set_max_smem(reinterpret_cast<const void*>(pages_small_kernel), (3 * kSmallBlocks + 1) * 4);
+    if (e == cudaSuccess)
+      e = launch_kernel("pages_small_kernel", pages_small_kernel, dim3(1), dim3(kPlanThreads), smem, s, false, d, w, rows,
+                        st->block_table, st->refs, refs_out, counts);
+  } else {
+    e = launch_zero_scratch(w.flag, w.zero_bytes, s);
+    if (e == cudaSuccess)
+      e = launch_kernel("pages_count_kernel", pages_count_kernel, dim3(entry_grid(d, sms)), dim3(kPgThreads), 0, s, true,
+                        d, w, rows, st->block_table);
+    if (e == cudaSuccess)
+      e = launch_kernel("pages_plan_kernel", pages_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, true, d, w, rows,
+                        st->refs, refs_out, counts);
+  }
   if (e == cudaSuccess)
     e = launch_kernel("pages_commit_kernel", pages_commit_kernel, dim3(commit_grid(d, sms, list, d.rows)),
                       dim3(kPgThreads), 0, s, true, d, w, list, st->block_table, new_len, table_out);
@@ -560,13 +622,17 @@ extern "C" int dsa_pages_compact(const dsa_page_state* st, int num_pools, const 
   if (int rc = current_device(&sms)) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const PageWs w = page_ws(ws, d);
-  cudaError_t e = cudaMemsetAsync(w.flag, 0, 4, s);
+  cudaError_t e = cudaSuccess;
+  const bool small = small_state(d);
+  if (!small) {
+    e = launch_zero_scratch(w.flag, 256, s);
+    if (e == cudaSuccess)
+      e = launch_kernel("pages_check_kernel", pages_check_kernel, dim3(entry_grid(d, sms)), dim3(kPgThreads), 0, s, true,
+                        d, w, st->block_table, st->refs);
+  }
   if (e == cudaSuccess)
-    e = launch_kernel("pages_check_kernel", pages_check_kernel, dim3(entry_grid(d, sms)), dim3(kPgThreads), 0, s,
-                      false, d, w, st->block_table, st->refs);
-  if (e == cudaSuccess)
-    e = launch_kernel("compact_plan_kernel", compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, true, d, w,
-                      st->refs, refs_out, remap, counts);
+    e = launch_kernel("compact_plan_kernel", compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, !small, d, w,
+                      small ? st->block_table : nullptr, st->refs, refs_out, remap, counts);
   if (e == cudaSuccess)
     e = launch_kernel("compact_commit_kernel", compact_commit_kernel,
                       dim3(commit_grid(d, sms, list, (d.nb + 1) / 2)), dim3(kPgThreads), 0, s, true, d, w, list,
