@@ -90,23 +90,31 @@ struct FullParams {
   float* lse;
   uint32_t* status;
   uint32_t* errors;     // [blocks] status bits of each block, OR-ed into *status by the merge
-  float* partial;       // [2 * blocks] parts of part_rows * (128 + 2) floats
+  // [2 * blocks] parts: O as [32 groups of 4 dims][part_rows] (lanes that hold
+  // consecutive rows write consecutive 16 bytes), then [part_rows] (m, l)
+  float* partial;
   int part_rows;
   int wide;             // some item has more than 128 rows
   int B, Hq, Hkv, G, cap, window;
   int q_dtype, out_dtype;
   float scale_log2, softcap;
   Paging pg;
-  int q0[DSA_MAX_BATCH + 1];      // first query row of each sequence
-  int item0[DSA_MAX_BATCH + 1];   // first item of each sequence
-  int T[DSA_MAX_BATCH], first[DSA_MAX_BATCH];
-  int cta_item[kMaxCtas + 1], cta_tile[kMaxCtas + 1];   // where each block's run begins
+  // (what a block needs first lies together: every line of the parameters is a
+  // miss to begin with)
+  struct Seq {
+    int q0, item0;                // its first query row, its first item
+    int T, first;
+  } seq[DSA_MAX_BATCH + 1];
+  struct Run {
+    int item, tile, b, pad;       // where a block's run begins, and the item's sequence
+  } run[kMaxCtas + 1];
 };
 
 // One item: rows [row0, row0 + nrows) of (sequence b, KV head g) and the key
 // tiles [tile0, tile0 + ntiles) that some row of it sees.
 struct Item {
   int b, g, row0, nrows, tile0, ntiles;
+  int q0, first;        // the sequence's first query row, its first key
   int past;             // position of the sequence's first new token
   int lo, hi;           // keys that some row sees
 };
@@ -114,21 +122,24 @@ struct Item {
 __host__ __device__ __forceinline__ int imax(int a, int b) { return a > b ? a : b; }
 __host__ __device__ __forceinline__ int imin(int a, int b) { return a < b ? a : b; }
 
-__host__ __device__ __forceinline__ Item make_item(const FullParams& p, int i) {
+// (b: a sequence no later than the item's)
+__host__ __device__ __forceinline__ Item make_item(const FullParams& p, int i, int b) {
   Item w;
-  int b = 0;
-  while (i >= p.item0[b + 1]) ++b;
-  const int S = p.q0[b + 1] - p.q0[b];
+  while (i >= p.seq[b + 1].item0) ++b;
+  const FullParams::Seq q = p.seq[b];
+  const int S = p.seq[b + 1].q0 - q.q0;
   const int rows = S * p.G;
   const int per_head = (rows + kItemRows - 1) / kItemRows;
-  const int k = i - p.item0[b];
+  const int k = i - q.item0;
   w.b = b;
   w.g = k / per_head;
   w.row0 = (k - w.g * per_head) * kItemRows;
   w.nrows = imin(kItemRows, rows - w.row0);
-  w.past = p.T[b] - S;
+  w.q0 = q.q0;
+  w.first = q.first;
+  w.past = q.T - S;
   w.hi = w.past + (w.row0 + w.nrows - 1) / p.G + 1;
-  w.lo = p.first[b];
+  w.lo = q.first;
   if (p.window > 0) w.lo = imax(w.lo, w.past + w.row0 / p.G - p.window + 1);
   w.lo = imin(w.lo, w.hi);
   w.tile0 = w.lo / kTileKeys;
@@ -145,16 +156,19 @@ struct Segment {
 };
 
 struct Walk {
-  int item, tile, end_item, end_tile;
+  int item, tile, b, end_item, end_tile;
   __device__ __forceinline__ explicit Walk(const FullParams& p) {
-    item = p.cta_item[blockIdx.x];
-    tile = p.cta_tile[blockIdx.x];
-    end_item = p.cta_item[blockIdx.x + 1];
-    end_tile = p.cta_tile[blockIdx.x + 1];
+    const FullParams::Run at = p.run[blockIdx.x], end = p.run[blockIdx.x + 1];
+    item = at.item;
+    tile = at.tile;
+    b = at.b;
+    end_item = end.item;
+    end_tile = end.tile;
   }
   __device__ __forceinline__ bool next(const FullParams& p, Segment* s) {
     if (item > end_item || (item == end_item && tile >= end_tile)) return false;
-    s->w = make_item(p, item);
+    s->w = make_item(p, item, b);
+    b = s->w.b;
     s->t0 = tile;
     s->t1 = item == end_item ? end_tile : s->w.ntiles;
     s->rows_mode = s->w.nrows > kSlotRows;
@@ -740,7 +754,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     const int tok = r / p.G;
     const int pos = s.w.past + tok;
     const int head = s.w.g * p.G + (r - tok * p.G);
-    const long long row = (static_cast<long long>(p.q0[s.w.b]) + tok) * p.Hq + head;   // query row
+    const long long row = (static_cast<long long>(s.w.q0) + tok) * p.Hq + head;   // query row
     float c = p.scale_log2;   // logits in units of log2 e per unit of S
     if (slot == 0 || s.rows_mode) {
       uint8_t* dst = sQ + slot * kTile16 + tid * 128;
@@ -793,8 +807,8 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     mbar_arrive(&bars->q_ready[slot]);
     const float slope = MOD && p.slopes && valid ? p.slopes[head] * 1.4426950408889634f : 0.f;
     const int pos0 = s.w.past + x.row0 / p.G, pos1 = s.w.past + (x.row0 + x.nrows - 1) / p.G;
-    const int lo = imax(p.first[s.w.b], p.window > 0 ? pos - p.window + 1 : 0);
-    const int lo1 = imax(p.first[s.w.b], p.window > 0 ? pos1 - p.window + 1 : 0);   // the last row's
+    const int lo = imax(s.w.first, p.window > 0 ? pos - p.window + 1 : 0);
+    const int lo1 = imax(s.w.first, p.window > 0 ? pos1 - p.window + 1 : 0);   // the last row's
 
     float m = -INFINITY, l = 0.f;   // running maximum (in S units, or log2 units where c = 1), sum
     const float cz = MOD ? 1.0f : c;
@@ -954,7 +968,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
       part = p.partial + static_cast<long long>(s.part) * p.part_rows * (DSA_HEAD_DIM + 2);
       const int pr = r - s.w.row0;
       if (valid) *reinterpret_cast<float2*>(part + p.part_rows * DSA_HEAD_DIM + 2 * pr) = make_float2(mj, lj);
-      part += pr * DSA_HEAD_DIM;
+      part += pr * 4;
     }
     f0 *= norm;
     f1 *= norm;
@@ -991,7 +1005,8 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
       if (part) {
 #pragma unroll
         for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4*>(part + i + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          *reinterpret_cast<float4*>(part + static_cast<long long>(i + e) * p.part_rows) =
+              make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       } else if (p.out_dtype == DSA_FP32) {
         float* d = static_cast<float*>(p.out) + row * DSA_HEAD_DIM + i;
 #pragma unroll
@@ -1089,59 +1104,60 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
 }
 
 // ------------------------------------------------------------------ merge
-// Joins the parts of the items that more than one block worked on: `wpr` warps
-// per query row take every wpr-th part, four dims a lane.
+// Joins the parts of the items that more than one block worked on. A thread
+// block takes four query rows; 128 threads hold a row's four dims each, and
+// `groups` such sets take every groups-th part.
 struct MergeParams {
   const float* partial;
   void* out;
   float* lse;
-  int part_rows, out_dtype, wpr, splits, blocks;
+  int part_rows, out_dtype, groups, splits, blocks;
   int first_cta[kMaxCtas], last_cta[kMaxCtas];   // blocks that hold split item i's parts
 };
-constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = 4, kMergeSet = 32 * kMergeRows, kMaxGroups = 8;
 
-__global__ void __launch_bounds__(kMergeThreads)
+__global__ void __launch_bounds__(kMergeSet * kMaxGroups)
     full_attn_merge_kernel(const __grid_constant__ FullParams p, const __grid_constant__ MergeParams mp) {
-  __shared__ float s_m[kMergeThreads / 32], s_l[kMergeThreads / 32];
-  __shared__ float4 s_o[kMergeThreads];
+  __shared__ float4 s_o[kMergeSet * kMaxGroups];
+  __shared__ float2 s_ml[kMergeRows * kMaxGroups];
   __shared__ uint32_t s_err;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     if (threadIdx.x == 0) s_err = 0u;
     __syncthreads();
     pdl_wait();
     uint32_t e = 0;
-    for (int c = threadIdx.x; c < mp.blocks; c += kMergeThreads) e |= __ldcg(p.errors + c);
+    for (int c = threadIdx.x; c < mp.blocks; c += blockDim.x) e |= __ldcg(p.errors + c);
     if (e) atomicOr(&s_err, e);
     __syncthreads();
     if (threadIdx.x == 0) *p.status = s_err;
   }
   if (mp.splits == 0) return;
-  const int sub = warp % mp.wpr, rows_here = kMergeThreads / 32 / mp.wpr;
-  const int i = blockIdx.y;
-  const int c0 = mp.first_cta[i], c1 = mp.last_cta[i];
+  const int set = threadIdx.x / kMergeSet, t = threadIdx.x % kMergeSet;
+  const int rr = t % kMergeRows, d4 = t / kMergeRows;   // (64 consecutive bytes of a part for four lanes)
+  const int c0 = mp.first_cta[blockIdx.y], c1 = mp.last_cta[blockIdx.y];
   // the item is the one block c1's run begins in
-  const Item w = make_item(p, p.cta_item[c1]);
-  const int pr = blockIdx.x * rows_here + warp / mp.wpr;
+  const FullParams::Run run = p.run[c1];
+  const Item w = make_item(p, run.item, run.b);
+  const int pr = blockIdx.x * kMergeRows + rr;
   pdl_wait();
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   if (pr < w.nrows) {
     const long long pitch = static_cast<long long>(mp.part_rows) * (DSA_HEAD_DIM + 2);
-    const auto part_of = [&](int c) { return mp.partial + (2 * c + (c == c0 ? 1 : 0)) * pitch; };
-    const long long ml = static_cast<long long>(mp.part_rows) * DSA_HEAD_DIM + 2 * pr;
+    const long long at_o = (static_cast<long long>(d4) * mp.part_rows + pr) * 4;
+    const long long at_ml = static_cast<long long>(mp.part_rows) * DSA_HEAD_DIM + 2 * pr;
     // four parts at a time: all their loads in flight together
-    for (int c = c0 + sub; c <= c1; c += 4 * mp.wpr) {
+    for (int c = c0 + set; c <= c1; c += 4 * mp.groups) {
       float2 x[4];
       float4 y[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int ck = c + k * mp.wpr;
+        const int ck = c + k * mp.groups;
         x[k] = make_float2(-INFINITY, 0.f);
         if (ck > c1) continue;
-        const float* q = part_of(ck);
-        x[k] = __ldcg(reinterpret_cast<const float2*>(q + ml));
-        y[k] = __ldcg(reinterpret_cast<const float4*>(q + pr * DSA_HEAD_DIM) + lane);
+        const float* q = mp.partial + (2 * ck + (ck == c0 ? 1 : 0)) * pitch;
+        x[k] = __ldcg(reinterpret_cast<const float2*>(q + at_ml));
+        y[k] = __ldcg(reinterpret_cast<const float4*>(q + at_o));
       }
       const float to = fmaxf(m, fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)));
       if (to == -INFINITY) continue;
@@ -1161,23 +1177,21 @@ __global__ void __launch_bounds__(kMergeThreads)
       }
     }
   }
-  if (mp.wpr > 1) {
-    if (lane == 0) {
-      s_m[warp] = m;
-      s_l[warp] = l;
-    }
+  if (mp.groups > 1) {
+    if (d4 == 0) s_ml[set * kMergeRows + rr] = make_float2(m, l);
     s_o[threadIdx.x] = o;
     __syncthreads();
-    if (sub != 0) return;
+    if (set != 0) return;
     float mm = -INFINITY;
-    for (int k = 0; k < mp.wpr; ++k) mm = fmaxf(mm, s_m[warp + k]);
+    for (int k = 0; k < mp.groups; ++k) mm = fmaxf(mm, s_ml[k * kMergeRows + rr].x);
     l = 0.f;
     o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < mp.wpr; ++k) {
-      if (s_m[warp + k] == -INFINITY) continue;
-      const float f = fast_exp2(s_m[warp + k] - mm);
-      const float4 y = s_o[threadIdx.x + k * 32];
-      l = fmaf(s_l[warp + k], f, l);
+    for (int k = 0; k < mp.groups; ++k) {
+      const float2 x = s_ml[k * kMergeRows + rr];
+      if (x.x == -INFINITY) continue;
+      const float f = fast_exp2(x.x - mm);
+      const float4 y = s_o[k * kMergeSet + t];
+      l = fmaf(x.y, f, l);
       o.x = fmaf(y.x, f, o.x);
       o.y = fmaf(y.y, f, o.y);
       o.z = fmaf(y.z, f, o.z);
@@ -1188,15 +1202,15 @@ __global__ void __launch_bounds__(kMergeThreads)
   if (pr >= w.nrows) return;
   const float norm = l > 0.f ? 1.0f / l : 0.f;
   const int r = w.row0 + pr, tok = r / p.G;
-  const long long row = (static_cast<long long>(p.q0[w.b]) + tok) * p.Hq + w.g * p.G + (r - tok * p.G);
+  const long long row = (static_cast<long long>(w.q0) + tok) * p.Hq + w.g * p.G + (r - tok * p.G);
   const float4 v = make_float4(o.x * norm, o.y * norm, o.z * norm, o.w * norm);
   if (mp.out_dtype == DSA_FP32)
-    *(reinterpret_cast<float4*>(static_cast<float*>(mp.out) + row * DSA_HEAD_DIM) + lane) = v;
+    *(reinterpret_cast<float4*>(static_cast<float*>(mp.out) + row * DSA_HEAD_DIM) + d4) = v;
   else
-    *(reinterpret_cast<uint2*>(static_cast<uint16_t*>(mp.out) + row * DSA_HEAD_DIM) + lane) =
+    *(reinterpret_cast<uint2*>(static_cast<uint16_t*>(mp.out) + row * DSA_HEAD_DIM) + d4) =
         mp.out_dtype == DSA_FP16 ? make_uint2(pack2<true>(v.x, v.y), pack2<true>(v.z, v.w))
                                  : make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
-  if (mp.lse && lane == 0) mp.lse[row] = l > 0.f ? (m - kLift + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  if (mp.lse && d4 == 0) mp.lse[row] = l > 0.f ? (m - kLift + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // -------------------------------------------------------------------- host
@@ -1256,18 +1270,19 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
   fp->part_rows = 0;
   for (int b = 0; b < p->batch; ++b) {
     const long long rows = static_cast<long long>(p->q_len[b]) * fp->G;
-    fp->q0[b + 1] = fp->q0[b] + p->q_len[b];
-    fp->item0[b + 1] = fp->item0[b] + static_cast<int>((rows + kItemRows - 1) / kItemRows) * p->num_kv_heads;
-    fp->T[b] = p->total_len[b];
-    fp->first[b] = p->first_key[b];
+    fp->seq[b + 1].q0 = fp->seq[b].q0 + p->q_len[b];
+    fp->seq[b + 1].item0 = fp->seq[b].item0 + static_cast<int>((rows + kItemRows - 1) / kItemRows) * p->num_kv_heads;
+    fp->seq[b].T = p->total_len[b];
+    fp->seq[b].first = p->first_key[b];
     fp->part_rows = imax(fp->part_rows, static_cast<int>(rows < kItemRows ? rows : kItemRows));
   }
   fp->wide = fp->part_rows > kSlotRows;
   fp->part_rows = (fp->part_rows + 3) & ~3;   // parts stay 16-byte aligned
-  const int items = fp->item0[p->batch];
+  const int items = fp->seq[p->batch].item0;
   long long cost = 0, tiles = 0;
-  for (int i = 0; i < items; ++i) {
-    const Item w = make_item(*fp, i);
+  for (int i = 0, at = 0; i < items; ++i) {
+    const Item w = make_item(*fp, i, at);
+    at = w.b;
     cost += kCostItem + static_cast<long long>(w.ntiles) * (w.nrows > kSlotRows ? kCostRows : kCostKeys);
     tiles += w.ntiles;
   }
@@ -1277,27 +1292,26 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
   int blocks = 0;
   long long at = 0;
   int k = 0;
-  for (int i = 0; i < items; ++i) {
-    const Item w = make_item(*fp, i);
+  for (int i = 0, b = 0; i < items; ++i) {
+    const Item w = make_item(*fp, i, b);
+    b = w.b;
     const int unit = w.nrows > kSlotRows ? kCostRows : kCostKeys;
     const long long end = at + kCostItem + static_cast<long long>(w.ntiles) * unit;
     for (; k < want && cost * k < end * want; ++k) {
       const long long x = cost * k / want - at - kCostItem;
       const int tile = x > 0 ? static_cast<int>(x / unit) : 0;
-      if (blocks > 0 && fp->cta_item[blocks - 1] == i && fp->cta_tile[blocks - 1] >= tile) continue;
-      fp->cta_item[blocks] = i;
-      fp->cta_tile[blocks++] = tile;
+      if (blocks > 0 && fp->run[blocks - 1].item == i && fp->run[blocks - 1].tile >= tile) continue;
+      fp->run[blocks++] = FullParams::Run{i, tile, b, 0};
     }
     at = end;
   }
-  fp->cta_item[blocks] = items;
-  fp->cta_tile[blocks] = 0;
+  fp->run[blocks] = FullParams::Run{items, 0, p->batch, 0};
   mp->splits = 0;
   int parts = 1;
   for (int c = 1; c < blocks; ++c) {
-    if (fp->cta_tile[c] == 0) continue;
+    if (fp->run[c].tile == 0) continue;
     const int n = mp->splits;
-    if (n > 0 && mp->last_cta[n - 1] == c - 1 && fp->cta_item[c] == fp->cta_item[c - 1]) {
+    if (n > 0 && mp->last_cta[n - 1] == c - 1 && fp->run[c].item == fp->run[c - 1].item) {
       mp->last_cta[n - 1] = c;
     } else {
       mp->first_cta[n] = c - 1;
@@ -1306,7 +1320,7 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
     }
     parts = imax(parts, c - mp->first_cta[mp->splits - 1] + 1);
   }
-  mp->wpr = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;   // four loads a lane in flight, at most eight warps
+  mp->groups = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : kMaxGroups;   // four parts a thread at once
   return blocks;
 }
 
@@ -1364,7 +1378,7 @@ int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* 
   FullParams fp{};
   MergeParams mp{};
   const int blocks = schedule(p, sms, &fp, &mp);
-  if (fp.q0[p->batch] == 0) {
+  if (fp.seq[p->batch].q0 == 0) {
     const cudaError_t e = cudaMemsetAsync(ws, 0, 4, static_cast<cudaStream_t>(stream));   // the status word
     return e == cudaSuccess ? DSA_OK : report_errorf(DSA_ERR_CUDA, "status clear: %s", cudaGetErrorString(e));
   }
@@ -1404,9 +1418,8 @@ int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* 
   else if (p->q_dtype == DSA_FP16) e = launch_full<true, false, true>(mod, blocks, tm_k, tm_v, fp, st);
   else e = launch_full<false, false, true>(mod, blocks, tm_k, tm_v, fp, st);
   if (e == cudaSuccess) {
-    const int rows_here = kMergeThreads / 32 / mp.wpr;
-    const dim3 grid = mp.splits ? dim3((fp.part_rows + rows_here - 1) / rows_here, mp.splits) : dim3(1);
-    e = launch_kernel("full_attn_merge_kernel", full_attn_merge_kernel, grid, dim3(kMergeThreads), 0, st, true, fp, mp);
+    const dim3 grid = mp.splits ? dim3((fp.part_rows + kMergeRows - 1) / kMergeRows, mp.splits) : dim3(1);
+    e = launch_kernel("full_attn_merge_kernel", full_attn_merge_kernel, grid, dim3(kMergeSet * mp.groups), 0, st, true, fp, mp);
   }
   if (e != cudaSuccess) return report_errorf(DSA_ERR_CUDA, "full attention launch: %s", cudaGetErrorString(e));
   return DSA_OK;
