@@ -413,7 +413,7 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
   }
   RingPos pos;
   uint32_t fixes = 0, tiles = 0;
-  bool bad = false;
+  bool bad = false, begin = true;
   Walk walk(p);
   Segment s;
   while (walk.next(p, &s)) {
@@ -423,6 +423,16 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
     };
     int base = s.t0;
     long long rows = look_up(base + lane), rows_next = look_up(base + 32 + lane);
+    // the item's queries, which the softmax warps load when they get there
+    // (those of the first they load at the same time)
+    for (int i = lane; !begin && i < s.w.nrows; i += 32) {
+      const int r = s.w.row0 + i, tok = r / p.G;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q) +
+                          ((static_cast<long long>(s.w.q0) + tok) * p.Hq + s.w.g * p.G + (r - tok * p.G)) * DSA_HEAD_DIM;
+      prefetch_l2_line(q);
+      prefetch_l2_line(q + 64);
+    }
+    begin = false;
     const bool ok = for_tiles(s, [&](int t, bool is_v) {
       const int st = pos.stage;
       if (pos.round > 0 && !warp_wait(&empty[st], (pos.round - 1) & 1, abort_flag)) return false;
@@ -1256,7 +1266,7 @@ int check_full(const dsa_full_problem* p) {
 
 // Costs of a unit, in quarters of a tile of 256 rows: a tile of up to 128 rows
 // takes the same loads and half the products; an item, its queries and output.
-constexpr int kCostRows = 4, kCostKeys = 3, kCostItem = 12;
+constexpr int kCostRows = 4, kCostKeys = 3, kCostItem = 20;
 
 // Lays the items out over the blocks (fp: the problem and the runs, mp: the
 // items that are split) and returns the number of blocks.

@@ -526,20 +526,32 @@ def dsa_sparse_attn_prefill(p, q, qI, w, kI, k, v, k_scale, v_scale, idx_out, ou
           workspace, stream, pages)
 
 
-def _here(dev: int, t: Optional[torch.Tensor], name: str, dtype=None, shape=None):
-    """_ptr of a tensor that must lie on device `dev`, the current one (whose
-    stream the call goes to)."""
-    if t is None:
-        return None
+def _refuse(dev: int, t: torch.Tensor, name: str, dtype, shape):
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _here(dev: int, t: Optional[torch.Tensor], name: str, dtype=None, shape=None):
+    """_ptr of a tensor that must lie on device `dev`, the current one (whose
+    stream the call goes to)."""
+    if t is None:
+        return None
+    if (t.get_device() != dev or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype)
+            or (shape is not None and t.shape != shape)):
+        _refuse(dev, t, name, dtype, shape)
     return t.data_ptr()
+
+
+def _stream_here(dev: int, stream) -> int:
+    """_stream with the current device known."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 def _ws_here(dev: int, ws: torch.Tensor):
@@ -601,7 +613,7 @@ def dsa_full_attn(p: DsaFullProblem, q, k, v, k_scale, v_scale, out, workspace, 
             _here(dev, k_scale, "k_scale", torch.float32, lead + (Hkv,)),
             _here(dev, v_scale, "v_scale", torch.float32, lead + (Hkv,)),
             _here(dev, slopes, "slopes", torch.float32, (Hq,)), _here(dev, out, "out", _TORCH_DT[p.out_dtype]),
-            _here(dev, lse, "lse", torch.float32), wp, wn, _stream(stream)]
+            _here(dev, lse, "lse", torch.float32), wp, wn, _stream_here(dev, stream)]
     if pages is None:
         _check(lib.dsa_full_attn(ctypes.byref(p), *args))
     else:
@@ -680,7 +692,7 @@ def dsa_pages_update(st: DsaPageState, parent, keep_len, new_len, pools, workspa
     _check(lib.dsa_pages_update(
         ctypes.byref(st), _here(dev, parent, "parent", i32, one), _here(dev, keep_len, "keep_len", i32, one),
         _here(dev, new_len, "new_len", i32, one), _here(dev, first_key, "first_key", i32, one), n, arr,
-        tp, rp, _here(dev, counts, "counts", i32, (2,)), wp, wn, _stream(stream)))
+        tp, rp, _here(dev, counts, "counts", i32, (2,)), wp, wn, _stream_here(dev, stream)))
 
 
 def dsa_pages_compact(st: DsaPageState, pools, workspace, table_out=None, refs_out=None, remap=None,
@@ -692,7 +704,7 @@ def dsa_pages_compact(st: DsaPageState, pools, workspace, table_out=None, refs_o
     n, arr, tp, rp = _page_args(dev, st, pools, table_out, refs_out)
     _check(lib.dsa_pages_compact(
         ctypes.byref(st), n, arr, tp, rp, _here(dev, remap, "remap", torch.int32, (st.num_blocks,)),
-        _here(dev, counts, "counts", torch.int32, (2,)), wp, wn, _stream(stream)))
+        _here(dev, counts, "counts", torch.int32, (2,)), wp, wn, _stream_here(dev, stream)))
 
 
 def make_beam_problem(batch: int, beams: int, vocab: int, select: int, logits_dtype="bf16",
@@ -735,7 +747,7 @@ def dsa_beam_select(p: DsaBeamProblem, logits, scores, out_scores, out_tokens, o
         ctypes.byref(p), logits.data_ptr(), _here(dev, scores, "scores", torch.float32, (n,)),
         _here(dev, finished, "finished", torch.uint8, (n,)), _here(dev, out_scores, "out_scores", torch.float32, out),
         _here(dev, out_tokens, "out_tokens", i32, out), _here(dev, out_parents, "out_parents", i32, out),
-        wp, wn, _stream(stream)))
+        wp, wn, _stream_here(dev, stream)))
 
 
 def dsa_read_device_status(workspace, stream=None) -> int:
