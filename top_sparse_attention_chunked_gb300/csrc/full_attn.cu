@@ -31,7 +31,7 @@
 //
 // K and V tiles arrive by TMA (128 consecutive cache rows of one head: a tile
 // never straddles a block of a paged cache, whose blocks hold a multiple of 128
-// tokens) in a ring of shared stages. INT8 tiles land as codes and eight warps
+// tokens) in a ring of shared stages. INT8 tiles land as codes and four warps
 // widen them to 16 bits (exact); the key's scale multiplies its column of S,
 // the value's its column of P. Rows of V outside the item's keys are zeroed in
 // shared memory (a masked weight is 0, but 0 times a NaN is not); masked
@@ -68,13 +68,13 @@ constexpr int kRing16 = 5, kRing8 = 3, kRaw = 3;
 constexpr int kMaxRing = 6, kMaxRaw = 5;
 constexpr int kScaleRing = 8;                          // see load_role
 // Warps: 8 softmax (slot, quarter of the rows), 4 for the products and the
-// loads, 8 that widen INT8 tiles.
-constexpr int kSoftThreads = 256, kThreads16 = 384, kWidenThreads = 256, kThreads8 = kThreads16 + kWidenThreads;
+// loads, 4 that widen INT8 tiles.
+constexpr int kSoftThreads = 256, kThreads16 = 384, kWidenThreads = 128, kThreads8 = kThreads16 + kWidenThreads;
 constexpr int kHalf = kTileKeys / 2;
 // Registers: 16-bit blocks have enough as they are launched (168 a thread);
 // with INT8 the softmax takes what the others give up. What the block needs in
 // all must be within what it is launched with:
-constexpr int kSoftRegs8 = 128, kMiscRegs8 = 64, kWidenRegs = 80;
+constexpr int kSoftRegs8 = 168, kMiscRegs8 = 72, kWidenRegs = 96;
 constexpr int kRegs8 = kSoftThreads * kSoftRegs8 + 128 * kMiscRegs8 + kWidenThreads * kWidenRegs;
 constexpr float kLift = 7.0f;                          // log2 of the weight at the running maximum
 constexpr float kRaise = 8.0f;                         // log2 growth that raises the running maximum
@@ -213,7 +213,9 @@ struct FullBars {
   uint64_t done;
   uint32_t tmem_base;
   int abort_flag, bad_page;
-  float m[kSlotRows], l[kSlotRows];             // keys mode: slot 1's, for slot 0 (m first: slot 0's scale)
+  // a segment's beginning: the scales of slot 0's and slot 1's rows; its end in
+  // keys mode: slot 1's statistics, for slot 0
+  float m[kSlotRows], l[kSlotRows];
 };
 
 template <bool INT8>
@@ -507,23 +509,25 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
 }
 
 // ------------------------------------------------------------ INT8 widening
-// A tile of 128 x 128 codes (128-byte rows, swizzled) to a 16-bit tile, by 256
-// threads. Eight lanes take chunks 0-3 (16 codes each) of an even row and 4-7
+// A tile of 128 x 128 codes (128-byte rows, swizzled) to a 16-bit tile, by
+// kWidenThreads threads. Eight lanes take chunks 0-3 (16 codes each) of an even row and 4-7
 // of the next, then the other halves: the reads, and the two 16-byte writes a
 // chunk becomes, each touch eight different 16-byte columns.
 template <bool F16>
 __device__ __forceinline__ void widen_tile(const uint8_t* src, uint8_t* dst, int tid) {
   const int half = (tid >> 2) & 1;
-  {
+  constexpr int kPairs = kWidenThreads / 8;   // pairs of rows at once
+#pragma unroll 1
+  for (int r0 = tid >> 3; r0 < kTileKeys / 2; r0 += 2 * kPairs) {
     uint4 x[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = ((j >> 1) * 32 + (tid >> 3)) * 2 + half;
+      const int row = (r0 + (j >> 1) * kPairs) * 2 + half;
       x[j] = *reinterpret_cast<const uint4*>(src + row * 128 + ((((tid & 3) + 4 * (half ^ (j & 1))) ^ (row & 7)) << 4));
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = ((j >> 1) * 32 + (tid >> 3)) * 2 + half;
+      const int row = (r0 + (j >> 1) * kPairs) * 2 + half;
       const int c = (tid & 3) + 4 * (half ^ (j & 1));
       const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
       uint32_t o[8];
@@ -750,8 +754,10 @@ __device__ __forceinline__ void rescale_p(uint32_t addr, float f) {
 template <bool QK_F16, bool PV_F16, bool INT8, bool MOD>
 __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint8_t* sQ,
                                              const float* scales, int slot, volatile int* abort_flag) {
-  const int tid = threadIdx.x & 127;
-  const uint32_t lane_addr = static_cast<uint32_t>((tid >> 5) * 32) << 16;
+  const int tid = threadIdx.x & 127, lane = tid & 31, warp_row = tid & ~31;
+  const bool scaled = QK_F16 && !INT8 && p.q_dtype == DSA_BF16;
+  bool begin = true;
+  const uint32_t lane_addr = static_cast<uint32_t>(warp_row) << 16;
   const uint32_t tS = tmem + lane_addr + slot * 128, tO = tmem + lane_addr + 256 + slot * 128;
   uint32_t ns = 0, no = 0, nml = 0, nseg = 0, tile_seq = 0;
   Walk walk(p);
@@ -767,50 +773,61 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     const long long row = (static_cast<long long>(s.w.q0) + tok) * p.Hq + head;   // query row
     float c = p.scale_log2;   // logits in units of log2 e per unit of S
     if (slot == 0 || s.rows_mode) {
-      uint8_t* dst = sQ + slot * kTile16 + tid * 128;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row * DSA_HEAD_DIM);
-      // (no INT8 call converts its query; a 16-bit call has registers for a row)
-      constexpr int kBatch = INT8 ? 8 : 16;
+      // The warp's 32 rows, four at a time: eight lanes a row, lane k of them its
+      // 16-byte chunks k and k + 8 (one in each block of 64 columns).
+      volatile float* row_c = slot == 0 ? bars->m : bars->l;
+      const int sub = lane & 7;
+      uint8_t* dst = sQ + slot * kTile16;
+#pragma unroll 1
+      for (int i0 = 0; i0 < 8; i0 += 4) {
+        uint4 u[4][2];
 #pragma unroll
-      for (int i0 = 0; i0 < 16; i0 += kBatch) {
-        uint4 u[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) u[i] = valid ? __ldg(src + i0 + i) : make_uint4(0, 0, 0, 0);
-        if constexpr (QK_F16 && !INT8) {
-          if (p.q_dtype == DSA_BF16) {
-            // the row's largest exponent to 14: scaled by 2^-ex
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-            }
-            const int ex = top >= 0x80u ? static_cast<int>(top >> 7) - 127 - 14 : -126 - 14;
-            // (two factors: 2^-ex may lie outside fp32's normal range)
-            const float f0 = __int_as_float((127 - ex / 2) << 23), f1 = __int_as_float((127 - (ex - ex / 2)) << 23);
-            c = ldexpf(c, ex);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack2<true>(__uint_as_float(w[e] << 16) * f0 * f1, __uint_as_float(w[e] & 0xffff0000u) * f0 * f1);
-              u[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int t = warp_row + (i0 + i) * 4 + (lane >> 3);
+          const int rr = x.row0 + t, tk = rr / p.G;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              static_cast<const uint16_t*>(p.q) +
+              ((static_cast<long long>(s.w.q0) + tk) * p.Hq + s.w.g * p.G + (rr - tk * p.G)) * DSA_HEAD_DIM);
+          const bool in = t < x.nrows;
+          u[i][0] = in ? __ldg(src + sub) : make_uint4(0, 0, 0, 0);
+          u[i][1] = in ? __ldg(src + sub + 8) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-          *reinterpret_cast<uint4*>(dst + ((i0 + i) >> 3) * kBlk + ((((i0 + i) & 7) ^ (tid & 7)) << 4)) = u[i];
+        for (int i = 0; i < 4; ++i) {
+          const int t = warp_row + (i0 + i) * 4 + (lane >> 3);
+          if constexpr (QK_F16 && !INT8) {   // (no INT8 call converts its query)
+            if (p.q_dtype == DSA_BF16) {
+              // the row's largest exponent to 14: scaled by 2^-ex
+              uint32_t w[8] = {u[i][0].x, u[i][0].y, u[i][0].z, u[i][0].w, u[i][1].x, u[i][1].y, u[i][1].z, u[i][1].w};
+              uint32_t top = 0;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+#pragma unroll
+              for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+              const int ex = top >= 0x80u ? static_cast<int>(top >> 7) - 127 - 14 : -126 - 14;
+              // (two factors: 2^-ex may lie outside fp32's normal range)
+              const float f0 = __int_as_float((127 - ex / 2) << 23), f1 = __int_as_float((127 - (ex - ex / 2)) << 23);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                w[e] = pack2<true>(__uint_as_float(w[e] << 16) * f0 * f1, __uint_as_float(w[e] & 0xffff0000u) * f0 * f1);
+              u[i][0] = make_uint4(w[0], w[1], w[2], w[3]);
+              u[i][1] = make_uint4(w[4], w[5], w[6], w[7]);
+              if (sub == 0) row_c[t] = ldexpf(p.scale_log2, ex);
+            }
+          }
+          uint8_t* d = dst + t * 128 + ((sub ^ (t & 7)) << 4);
+          *reinterpret_cast<uint4*>(d) = u[i][0];
+          *reinterpret_cast<uint4*>(d + kBlk) = u[i][1];
+        }
       }
+      __syncwarp();
+      if (scaled) c = row_c[tid];
       fence_async_smem();
-      if (!s.rows_mode) bars->m[tid] = c;   // for slot 1
     }
     if (slot == 1 && !s.rows_mode) {
       // slot 0 loads the shared rows; what it scaled them by
       if (!warp_wait(&bars->q_ready[0], nseg & 1, abort_flag)) break;
-      c = *const_cast<const volatile float*>(&bars->m[tid]);
+      if (scaled) c = *const_cast<const volatile float*>(&bars->m[tid]);
     }
     ++nseg;
     tc_fence_before();
@@ -823,16 +840,22 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     float m = -INFINITY, l = 0.f;   // running maximum (in S units, or log2 units where c = 1), sum
     const float cz = MOD ? 1.0f : c;
     bool ok = true;
-    for (int j = 0; j < x.n; ++j) {
-      const int t = x.first + j * x.step;
+    // (round -1 of a block's first segment forms weights of whatever tensor
+    // memory holds and drops them: the loop's instructions come into the cache
+    // while the first tile is on its way -- 5,200 cycles for the first tile's
+    // softmax otherwise, 1,400 for the next; INT8's larger code gains nothing)
+    for (int j = begin && !INT8 ? -1 : 0; j < x.n; ++j) {
+      const int t = x.first + imax(j, 0) * x.step;
       const int key0 = (s.w.tile0 + t) * kTileKeys;
-      if (!warp_wait(&bars->s_full[slot], ns & 1, abort_flag)) {
-        ok = false;
-        break;
+      if (j >= 0) {
+        if (!warp_wait(&bars->s_full[slot], ns & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        ++ns;
+        tc_fence_after();
       }
-      ++ns;
-      tc_fence_after();
-      if constexpr (INT8) {
+      if (INT8 && j >= 0) {
         const uint32_t q = tile_seq + (t - s.t0);
         if (!warp_wait(&bars->scales[q % kScaleRing], (q / kScaleRing) & 1, abort_flag)) {
           ok = false;
@@ -913,6 +936,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
             const float f = to == -INFINITY || m == -INFINITY ? (m == to ? 1.0f : 0.0f) : fast_exp2((m - to) * cz);
             m = to;
             l *= f;
+            if (j < 0) break;
             if (h == 1) rescale_p<PV_F16>(tS, f);   // the first half's, not yet in O
             if (j > 0) {
 #pragma unroll 1
@@ -929,14 +953,20 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
               }
             }
           }
-          tmem_st32(tS + col, w);   // over columns of S that have been read
+          if (j >= 0) tmem_st32(tS + col, w);   // over columns of S that have been read
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
+      }
+      if (j < 0) {
+        m = -INFINITY;
+        l = 0.f;
+        continue;
       }
       if (warp_valid) tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&bars->p_full[slot]);
     }
+    begin = false;
     if (!ok) break;
     tile_seq += s.t1 - s.t0;
     const float m_log2 = m == -INFINITY ? -INFINITY : m * cz;
