@@ -124,9 +124,11 @@ def reference(c, window=0, softcap=0.0, slopes=None, scale=None):
 
 def check(c, got, lse, ref, out_dtype):
     """The weights enter the second product in 16 bits: half a step of the type it is taken in, FP16 for an
-    FP16 cache, BF16 otherwise; the statistics are off by their logits' error, 2^-21 for the exponential."""
+    FP16 cache, a BF16 pair for an FP16 query on an INT8 cache, BF16 otherwise; the statistics are off by their logits' error, 2^-21 for the exponential."""
     out, lse_ref, mag, dz = ref
     u_p = HALF_STEP["fp16"] if c["kvdt"] == "fp16" else HALF_STEP["bf16"]
+    if c["kvdt"] == "int8" and c["qdt"] == "fp16":
+        u_p = HALF_STEP["bf16"] ** 2                # a BF16 pair
     tol = HALF_STEP[out_dtype] * np.abs(out) + mag * (1.01 * u_p + 2.5 * dz[..., None] + 2.0 ** -19) + 1e-30
     if out_dtype == "fp16":
         tol = tol + 2.0 ** -25                      # its smallest step
@@ -194,6 +196,14 @@ def test_chunks(D, q_len, total, kv):
 @pytest.mark.parametrize("out_dtype", ["bf16", "fp16", "fp32"])
 def test_output_types(D, out_dtype):
     run(D, make([4, 150], [260, 150], 8, 2, "bf16", "fp16", block=256), out_dtype=out_dtype)
+
+
+@pytest.mark.parametrize("q_len,total", [([1], [700]), ([90, 3], [300, 1111])])
+@pytest.mark.parametrize("kw", [dict(), dict(window=150, softcap=5.0)])
+def test_fp16_query_on_int8_keeps_fp16_precision(D, q_len, total, kw):
+    c = make(q_len, total, 12, 2, "fp16", "int8", block=128, seed=17)
+    run(D, c, out_dtype="fp32", **kw)
+    run(D, c, **kw)
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp16", "int8"])

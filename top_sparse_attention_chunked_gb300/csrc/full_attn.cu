@@ -40,7 +40,8 @@
 // Types: the products take the cache's type (INT8: the query's for S, BF16 for
 // P V, since a value's scale may lie outside FP16's range). A BF16 query on an
 // FP16 cache is scaled by a power of two per row to at most 2^14 first, which
-// is exact for all elements within 2^-28 of the row's largest.
+// is exact for all elements within 2^-28 of the row's largest. (An FP16 query on
+// INT8: see split_p.)
 #include <atomic>
 #include <cmath>
 #include <cuda_bf16.h>
@@ -567,7 +568,13 @@ __device__ __forceinline__ void widen_role(const FullParams& p, FullBars* bars, 
 }
 
 // ------------------------------------------------------------ tensor core
-template <bool QK_F16, bool PV_F16>
+// An FP16 query on an INT8 cache: its output has three bits more than a BF16
+// weight, so P goes as a BF16 pair, high and low part, and the second product is
+// taken with both.
+template <bool QK_F16, bool INT8>
+__host__ __device__ constexpr bool split_p() { return QK_F16 && INT8; }
+
+template <bool QK_F16, bool PV_F16, bool INT8>
 __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint32_t q_addr,
                                          uint32_t ring_addr, int stages, volatile int* abort_flag) {
   constexpr uint32_t id_qk = idesc128(QK_F16, false), id_pv = idesc128(PV_F16, true);
@@ -591,9 +598,11 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
     ++np[slot];
     tc_fence_after();
 #pragma unroll
-    for (int kk = 0; kk < kTileKeys / 16; ++kk)
-      mma_ts(tmem + 256 + slot * 128, tmem + slot * 128 + (kk >> 2) * kHalf + (kk & 3) * 8, b + kk * (16 * 128 / 16), id_pv,
-             !first || kk > 0);
+    for (int kk = 0; kk < kTileKeys / 16; ++kk) {
+      const uint32_t pa = tmem + slot * 128 + (kk >> 2) * kHalf + (kk & 3) * 8;
+      mma_ts(tmem + 256 + slot * 128, pa, b + kk * (16 * 128 / 16), id_pv, !first || kk > 0);
+      if constexpr (split_p<QK_F16, INT8>()) mma_ts(tmem + 256 + slot * 128, pa + 32, b + kk * (16 * 128 / 16), id_pv, true);
+    }
     return true;
   };
   const auto release = [&](const RingPos& q) { tc_commit(&bars->empty[q.stage]); };
@@ -697,8 +706,8 @@ __device__ __forceinline__ void odd_poly(float* z, float ys, const float (&k)[K]
 }
 
 // z (units of S, c log2-units each) -> cap * tanh(z c ln2 / cap) in log2 units.
-// Small arguments take odd polynomials fitted for the least maximum error, in
-// fp32 5e-7 of the range up to 0.35 and 1.2e-7 up to 0.7; larger ones
+// Small arguments take odd polynomials fitted for the least maximum error (5e-8
+// of the range in fp32, up to 0.4 and up to 0.7); larger ones
 // tanh y = 1 - 2 / (1 + e^2y), whose two special-function calls a value would
 // be the kernel's bound.
 template <int N>
@@ -708,12 +717,13 @@ __device__ __forceinline__ void cap_scores(float* z, float c, float softcap) {
 #pragma unroll
   for (int i = 0; i < N; ++i) far[i & 3] = fmaxf(far[i & 3], fabsf(z[i]));
   const float y = fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3])) * ys;
-  if (__all_sync(0xffffffffu, y <= 0.35f)) {
-    const float k[3] = {0.122480378f * cap, -0.3326841f * cap, 0.999990225f * cap};
-    odd_poly<N, 3>(z, ys, k);
+  if (__all_sync(0xffffffffu, y <= 0.4f)) {
+    const float k[4] = {-0.0468257405f * cap, 0.13250567f * cap, -0.333297253f * cap, 0.999999583f * cap};
+    odd_poly<N, 4>(z, ys, k);
   } else if (__all_sync(0xffffffffu, y <= 0.7f)) {
-    const float k[5] = {0.0131941866f * cap, -0.0501952581f * cap, 0.132574543f * cap, -0.333269745f * cap, 0.99999851f * cap};
-    odd_poly<N, 5>(z, ys, k);
+    const float k[6] = {-0.004874242f * cap, 0.0197352078f * cap, -0.0533838086f * cap,
+                        0.13325353f * cap,   -0.333328605f * cap, 0.99999994f * cap};
+    odd_poly<N, 6>(z, ys, k);
   } else {
     const float two = 2.0f * c / softcap;
 #pragma unroll
@@ -755,6 +765,7 @@ template <bool QK_F16, bool PV_F16, bool INT8, bool MOD>
 __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint8_t* sQ,
                                              const float* scales, int slot, volatile int* abort_flag) {
   const int tid = threadIdx.x & 127, lane = tid & 31, warp_row = tid & ~31;
+  constexpr bool kSplit = split_p<QK_F16, INT8>();
   const bool scaled = QK_F16 && !INT8 && p.q_dtype == DSA_BF16;
   bool begin = true;
   const uint32_t lane_addr = static_cast<uint32_t>(warp_row) << 16;
@@ -901,7 +912,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
             for (int i = 0; i < kHalf; ++i)
               if (i < a || i > b) z[i] = -INFINITY;
           }
-          uint32_t w[32];
+          uint32_t w[32], wl[kSplit ? 32 : 1];
           float2 sum[2];
 #pragma unroll 1
           while (true) {
@@ -926,6 +937,9 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
                   pr[e] = fma_f32x2(pr[e], vs, make_float2(0.f, 0.f));
                 }
                 w[i + e] = pack2<PV_F16>(pr[e].x, pr[e].y);
+                if constexpr (kSplit)
+                  wl[i + e] = pack2<false>(pr[e].x - __uint_as_float(w[i + e] << 16),
+                                           pr[e].y - __uint_as_float(w[i + e] & 0xffff0000u));
               }
             }
             const float mn = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
@@ -937,7 +951,10 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
             m = to;
             l *= f;
             if (j < 0) break;
-            if (h == 1) rescale_p<PV_F16>(tS, f);   // the first half's, not yet in O
+            if (h == 1) {   // the first half's P, not yet in O
+              rescale_p<PV_F16>(tS, f);
+              if constexpr (kSplit) rescale_p<PV_F16>(tS + 32, f);
+            }
             if (j > 0) {
 #pragma unroll 1
               for (int i = 0; i < DSA_HEAD_DIM; i += 16) {
@@ -953,7 +970,10 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
               }
             }
           }
-          if (j >= 0) tmem_st32(tS + col, w);   // over columns of S that have been read
+          if (j >= 0) {   // over columns of S that have been read
+            tmem_st32(tS + col, w);
+            if constexpr (kSplit) tmem_st32(tS + col + 32, wl);
+          }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
       }
@@ -1125,7 +1145,7 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
     if constexpr (INT8) regs_down<kMiscRegs8>();
     if (warp == 8) {
       if ((threadIdx.x & 31) == 0)
-        mma_role<QK_F16, PV_F16>(p, bars, tmem, smem_u32(sQ), smem_u32(ring), stages, abort_flag);
+        mma_role<QK_F16, PV_F16, INT8>(p, bars, tmem, smem_u32(sQ), smem_u32(ring), stages, abort_flag);
     } else if (warp == 9) {
       load_role<INT8>(p, tm_k, tm_v, bars, INT8 ? raw : ring, INT8 ? raw_stages : stages, scales, abort_flag);
     }
