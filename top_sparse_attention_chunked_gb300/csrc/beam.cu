@@ -457,6 +457,29 @@ __device__ __forceinline__ double key_double(unsigned long long k) {
   return __longlong_as_double(static_cast<long long>((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
 }
 
+// log(x / 2^36) for x > 0. With x = 2^e q, q in [1/sqrt 2, sqrt 2), and
+// f = (q - 1) / (q + 1): log q = 2 (f + f^3 / 3 + f^5 / 5 + ...), |f| < 0.172;
+// the terms left out are below 2e-14. 64-bit arithmetic is slow here: this is
+// some twenty operations, most of them side by side, where the library's
+// logarithm took 4,000 cycles of a latency-bound kernel.
+__device__ __forceinline__ double log_fixed(unsigned long long x) {
+  int e = 63 - __clzll(static_cast<long long>(x));
+  double q = __longlong_as_double(static_cast<long long>(
+      (1023ull << 52) | (e <= 52 ? (x << (52 - e)) & 0xfffffffffffffull : (x >> (e - 52)) & 0xfffffffffffffull)));
+  if (q > 1.4142135623730951) {
+    q *= 0.5;
+    ++e;
+  }
+  const double d = q + 1.0;
+  double r = static_cast<double>(__frcp_rn(static_cast<float>(d)));   // 1 / d, by two Newton steps
+  r = r * (2.0 - d * r);
+  r = r * (2.0 - d * r);
+  const double f = (q - 1.0) * r, g = f * f, g2 = g * g, g4 = g2 * g2;
+  const double a = 1.0 + g * (1.0 / 3), b = 1.0 / 5 + g * (1.0 / 7), c = 1.0 / 9 + g * (1.0 / 11), h = 1.0 / 13 + g * (1.0 / 15);
+  const double s = (a + g2 * b) + g4 * (c + g2 * h);
+  return 2.0 * f * s + static_cast<double>(e - 36) * 0.6931471805599453;
+}
+
 // One thread block per batch entry; its beams' slices are the lists
 // b * slices + j.
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p) {
@@ -499,6 +522,25 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
     s_sum[tid] = s;
   }
   __syncthreads();
+  // A lane takes a list, a warp every 32nd of its candidates (beams may be far
+  // apart: this way the warps' shares are alike). The first 64 lists' are read
+  // while the sums are joined.
+  const unsigned long long* cands = p.cands + static_cast<long long>(row0) * p.slices * kKeep;
+  const auto share = [&](int i) {   // the warp's largest value of list i
+    float top = -INFINITY;
+    if (i < lists) {
+      const int n = s_sum[i].count;
+      if (s_over[i / p.slices]) {
+        if (n > 0 && wid == 0) top = 0.f;
+      } else {
+#pragma unroll
+        for (int j0 = 0; j0 < kKeep; j0 += kMergeWarps)
+          if (j0 + wid < n) top = fmaxf(top, key_value(cands[i * kKeep + j0 + wid]));
+      }
+    }
+    return top;
+  };
+  const float ahead[2] = {share(lane), share(lane + 32)};
   if (tid < p.beams) {
     double off = s_score[tid];
     if (!s_over[tid]) {
@@ -520,29 +562,18 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
       // the logarithm, and H's part undone at the maximum
       const double ln2 = 0.6931471805599453;
       const double base = fabsf(mm) <= kFar ? ln2 * (mm * kLog2eRest - static_cast<double>(offset_of(mm))) : static_cast<double>(mm);
-      off -= bad ? NAN : base + log(static_cast<double>(sum) * 0x1p-36);
+      off -= bad || sum == 0ull ? NAN : base + log_fixed(sum);   // (nothing but -infinity: no candidate)
     }
     s_off[tid] = off;
   }
   __syncthreads();
-  // A bound on the totals (fp32, rounded down). A lane takes a list, a warp
-  // every 32nd of its candidates (beams may be far apart: this way the warps'
-  // shares are alike); of the warps' two largest values `select` reach the
-  // select-th largest.
-  const unsigned long long* cands = p.cands + static_cast<long long>(row0) * p.slices * kKeep;
+  // A bound on the totals (fp32, rounded down): of the warps' two largest values
+  // `select` reach the select-th largest.
   uint32_t best = 0u;
+#pragma unroll 1
   for (int i = lane; i < lists; i += 32) {
-    const int at = i / p.slices, n = s_sum[i].count;
-    const float off = __double2float_rd(s_off[at]);
-    float top = -INFINITY;
-    if (s_over[at]) {
-      if (n > 0 && wid == 0) top = 0.f;
-    } else {
-#pragma unroll
-      for (int j0 = 0; j0 < kKeep; j0 += kMergeWarps)
-        if (j0 + wid < n) top = fmaxf(top, key_value(cands[i * kKeep + j0 + wid]));
-    }
-    const float t = __fadd_rd(top, off);
+    const float top = i < 32 ? ahead[0] : i < 64 ? ahead[1] : share(i);
+    const float t = __fadd_rd(top, __double2float_rd(s_off[i / p.slices]));
     if (t > -INFINITY) best = max(best, float_key(t));   // (not for a NaN)
   }
   const uint32_t first = __reduce_max_sync(0xffffffffu, best);
@@ -555,14 +586,17 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   }
   __syncthreads();
   if (wid == 0) {
-    // the select-th largest of the 64, a bit at a time
-    const uint32_t v0 = s_bound[lane], v1 = s_bound[32 + lane];
-    uint32_t bound = 0u;
+    // the select-th largest of the 64 (a lane's first is no less than its second)
+    uint32_t cur = s_bound[lane], rest = s_bound[32 + lane], bound = 0u;
 #pragma unroll 1
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t t = bound | (1u << bit);
-      const int n = __popc(__ballot_sync(0xffffffffu, v0 >= t)) + __popc(__ballot_sync(0xffffffffu, v1 >= t));
-      if (n >= k) bound = t;
+    for (int i = 0; i < k; ++i) {
+      bound = __reduce_max_sync(0xffffffffu, cur);
+      if (bound == 0u) break;
+      const uint32_t holders = __ballot_sync(0xffffffffu, cur == bound);
+      if (lane == __ffs(holders) - 1) {
+        cur = rest;
+        rest = 0u;
+      }
     }
     if (lane == 0) s_bound[0] = bound;
   }
