@@ -51,7 +51,9 @@ constexpr int kGroup = 2;           // tiles between two looks at the list's len
 constexpr int kMergeThreads = 1024;
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMaxLists = 512;      // slices of one batch entry
-constexpr int kMergeList = kMergeWarps * kKeep;   // candidates of one round of the merge
+constexpr int kRound = 2 * kMergeWarps;           // lists that the merge takes at once
+constexpr int kMergeList = kRound * kKeep;        // and their candidates
+constexpr int kShare = kKeep / kMergeWarps;
 constexpr int kResident = 3;        // scan blocks per SM (70 KB of shared memory each for 16-bit logits)
 
 struct SliceSum {
@@ -90,7 +92,7 @@ __device__ __forceinline__ float ex2_ftz(float x) {
   return y;
 }
 constexpr float kLog2e = 1.44269502e0f;           // H
-constexpr double kLog2eRest = 1.925963033e-8;     // log2(e) - H
+constexpr float kLog2eRest = 1.925963033e-8f;     // log2(e) - H
 // Up to this size of a maximum its c is an exact integer that cancels it to
 // about 1; rows beyond (masked with the type's lowest value throughout) take
 // the differences from it instead.
@@ -457,27 +459,38 @@ __device__ __forceinline__ double key_double(unsigned long long k) {
   return __longlong_as_double(static_cast<long long>((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
 }
 
-// log(x / 2^36) for x > 0. With x = 2^e q, q in [1/sqrt 2, sqrt 2), and
-// f = (q - 1) / (q + 1): log q = 2 (f + f^3 / 3 + f^5 / 5 + ...), |f| < 0.172;
-// the terms left out are below 2e-14. 64-bit arithmetic is slow here: this is
-// some twenty operations, most of them side by side, where the library's
-// logarithm took 4,000 cycles of a latency-bound kernel.
-__device__ __forceinline__ double log_fixed(unsigned long long x) {
+// log2(e) (log(x / 2^36)) of x > 0 as an integer of log2 plus hi + lo in natural
+// units: with x = 2^e q, q in [1/sqrt 2, sqrt 2), and f = (q - 1) / (q + 1),
+// log q = 2 f + 2 f (f^2 / 3 + f^4 / 5 + ...), |f| < 0.172. 2 f is taken to two
+// fp32 numbers, the rest, below 4e-3, in fp32: together good to 2e-9. (64-bit
+// arithmetic has a latency of some hundred cycles here, and this kernel's time
+// is one dependent chain.)
+__device__ __forceinline__ int log_fixed(unsigned long long x, float* hi, float* lo) {
   int e = 63 - __clzll(static_cast<long long>(x));
-  double q = __longlong_as_double(static_cast<long long>(
-      (1023ull << 52) | (e <= 52 ? (x << (52 - e)) & 0xfffffffffffffull : (x >> (e - 52)) & 0xfffffffffffffull)));
-  if (q > 1.4142135623730951) {
-    q *= 0.5;
+  // q - 1 in units of 2^-62, from the bits below the leading one
+  long long d = static_cast<long long>((e < 62 ? x << (62 - e) : x >> (e - 62)) & 0x3fffffffffffffffull);
+  if (d > 0x1A827999FCEF3243ll) {   // q > sqrt 2: halve it
+    d = (d >> 1) - 0x2000000000000000ll;
     ++e;
   }
-  const double d = q + 1.0;
-  double r = static_cast<double>(__frcp_rn(static_cast<float>(d)));   // 1 / d, by two Newton steps
-  r = r * (2.0 - d * r);
-  r = r * (2.0 - d * r);
-  const double f = (q - 1.0) * r, g = f * f, g2 = g * g, g4 = g2 * g2;
-  const double a = 1.0 + g * (1.0 / 3), b = 1.0 / 5 + g * (1.0 / 7), c = 1.0 / 9 + g * (1.0 / 11), h = 1.0 / 13 + g * (1.0 / 15);
-  const double s = (a + g2 * b) + g4 * (c + g2 * h);
-  return 2.0 * f * s + static_cast<double>(e - 36) * 0.6931471805599453;
+  const float dh = static_cast<float>(d) * 0x1p-62f;
+  const float dl = static_cast<float>(d - static_cast<long long>(static_cast<float>(d))) * 0x1p-62f;
+  // f = (dh + dl) / (2 + dh + dl)
+  const float nh = 2.0f + dh, nl = (2.0f - nh) + dh + dl;
+  const float r = __frcp_rn(nh);
+  const float fh = dh * r;
+  const float fl = (fmaf(-fh, nh, dh) + dl - fh * nl) * r;
+  const float g = fh * fh;
+  float s = 1.0f / 15;
+  s = fmaf(s, g, 1.0f / 13);
+  s = fmaf(s, g, 1.0f / 11);
+  s = fmaf(s, g, 1.0f / 9);
+  s = fmaf(s, g, 1.0f / 7);
+  s = fmaf(s, g, 1.0f / 5);
+  s = fmaf(s, g, 1.0f / 3);
+  *hi = 2.0f * fh;
+  *lo = 2.0f * fmaf(fh * g, s, fl);
+  return e - 36;
 }
 
 // One thread block per batch entry; its beams' slices are the lists
@@ -526,21 +539,17 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   // apart: this way the warps' shares are alike). The first 64 lists' are read
   // while the sums are joined.
   const unsigned long long* cands = p.cands + static_cast<long long>(row0) * p.slices * kKeep;
-  const auto share = [&](int i) {   // the warp's largest value of list i
-    float top = -INFINITY;
-    if (i < lists) {
-      const int n = s_sum[i].count;
-      if (s_over[i / p.slices]) {
-        if (n > 0 && wid == 0) top = 0.f;
-      } else {
+  const auto fetch = [&](int i, uint32_t* key) {   // the warp's share of list i: the values' keys
+    const int n = i < lists && !s_over[i / p.slices] ? s_sum[i].count : 0;
 #pragma unroll
-        for (int j0 = 0; j0 < kKeep; j0 += kMergeWarps)
-          if (j0 + wid < n) top = fmaxf(top, key_value(cands[i * kKeep + j0 + wid]));
-      }
+    for (int j = 0; j < kShare; ++j) {
+      const int at = j * kMergeWarps + wid;
+      key[j] = at < n ? reinterpret_cast<const uint32_t*>(cands + i * kKeep + at)[1] : 0u;
     }
-    return top;
   };
-  const float ahead[2] = {share(lane), share(lane + 32)};
+  uint32_t ahead[2][kShare];
+  fetch(lane, ahead[0]);
+  fetch(lane + 32, ahead[1]);
   if (tid < p.beams) {
     double off = s_score[tid];
     if (!s_over[tid]) {
@@ -559,10 +568,19 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
           sum += static_cast<unsigned long long>(static_cast<double>(s[j].sum) * join_factor(s[j].max, mm));
         }
       }
-      // the logarithm, and H's part undone at the maximum
-      const double ln2 = 0.6931471805599453;
-      const double base = fabsf(mm) <= kFar ? ln2 * (mm * kLog2eRest - static_cast<double>(offset_of(mm))) : static_cast<double>(mm);
-      off -= bad || sum == 0ull ? NAN : base + log_fixed(sum);   // (nothing but -infinity: no candidate)
+      if (bad || sum == 0ull) {
+        off = NAN;   // nothing but -infinity: no candidate
+      } else {
+        // the logarithm, and H's part undone at the maximum
+        float hi, lo;
+        const int e = log_fixed(sum, &hi, &lo);
+        const bool near = fabsf(mm) <= kFar;
+        if (near) lo = fmaf(mm, kLog2eRest * 0.693147181f, lo);
+        const float whole = static_cast<float>(e) - (near ? offset_of(mm) : 0.f);   // (below 2^24)
+        double lse = fma(static_cast<double>(whole), 0.6931471805599453, static_cast<double>(hi)) + static_cast<double>(lo);
+        if (!near) lse += static_cast<double>(mm);
+        off -= lse;
+      }
     }
     s_off[tid] = off;
   }
@@ -570,11 +588,24 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   // A bound on the totals (fp32, rounded down): of the warps' two largest values
   // `select` reach the select-th largest.
   uint32_t best = 0u;
-#pragma unroll 1
-  for (int i = lane; i < lists; i += 32) {
-    const float top = i < 32 ? ahead[0] : i < 64 ? ahead[1] : share(i);
-    const float t = __fadd_rd(top, __double2float_rd(s_off[i / p.slices]));
+  const auto join_list = [&](int i, const uint32_t* key) {
+    if (i >= lists) return;
+    const int at = i / p.slices;
+    uint32_t top = key[0];
+#pragma unroll
+    for (int j = 1; j < kShare; ++j) top = max(top, key[j]);
+    const float off = __double2float_rd(s_off[at]);
+    float t = -INFINITY;
+    if (top != 0u) t = __fadd_rd(key_value(static_cast<unsigned long long>(top) << 32), off);
+    else if (s_over[at] && wid == 0 && s_sum[i].count > 0) t = off;
     if (t > -INFINITY) best = max(best, float_key(t));   // (not for a NaN)
+  };
+  join_list(lane, ahead[0]);
+  join_list(lane + 32, ahead[1]);
+  for (int i = lane + 64; i < lists; i += 32) {
+    uint32_t key[kShare];
+    fetch(i, key);
+    join_list(i, key);
   }
   const uint32_t first = __reduce_max_sync(0xffffffffu, best);
   const uint32_t holders = __ballot_sync(0xffffffffu, best == first);
@@ -602,11 +633,10 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   }
   __syncthreads();
   best = s_bound[0];
-  // the totals of those that may reach it, a round of kMergeWarps lists at a time
+  // the totals of those that may reach it, a round of lists at a time
   int have = 0;
-  for (int r = 0; r < lists; r += kMergeWarps) {
-    const int i = r + wid;
-    if (i < lists) {
+  for (int r = 0; r < lists; r += kRound) {
+    for (int i = r + wid; i < min(lists, r + kRound); i += kMergeWarps) {
       const int at_b = i / p.slices, n = s_sum[i].count;
       const double off = s_off[at_b];
       const float off_up = __double2float_ru(off);
