@@ -68,6 +68,27 @@ def test_full_attention_pointer_checks(D):
         assert call_full(D, p, pages) == D.DSA_ERR_NO_DEVICE
 
 
+def test_full_attention_workspace_holds_every_block_s_parts(D):
+    """At most one block per tile of 128 keys, 192 at the most, two parts each:
+    a device with fewer SMs may use more blocks than one with more."""
+    import random
+    for seed in list(range(40)) + [63, 1330, 1979]:
+        r = random.Random(seed)
+        n = r.randint(1, 64)
+        q = [r.choice([1, 1, 1, 2, r.randint(0, 40)]) for _ in range(n)]
+        if sum(q) == 0:
+            continue
+        total = [x + r.choice([0, r.randint(0, 600), r.randint(0, 60)]) for x in q]
+        grp, hkv = r.choice([1, 4, 12, 20, 130]), r.choice([1, 2, 4, 8])
+        tiles = rows = 0
+        for s, t in zip(q, total):
+            rows = max(rows, min(256, s * grp))
+            for row0 in range(0, s * grp, 256):
+                tiles += hkv * -(-(t - s + (min(row0 + 256, s * grp) - 1) // grp + 1) // 128)
+        p = D.make_full_attn_problem(q, total, grp * hkv, hkv)
+        assert D.dsa_full_attn_workspace_size(p) >= 2 * min(tiles, 192) * rows * 130 * 4
+
+
 def state(D, **kw):
     a = dict(block_size=128, num_blocks=16, rows=4, blocks_per_seq=8, block_table=0x10000, refs=0x20000)
     a.update(kw)

@@ -42,6 +42,7 @@
 // FP16 cache is scaled by a power of two per row to at most 2^14 first, which
 // is exact for all elements within 2^-28 of the row's largest. (An FP16 query on
 // INT8: see split_p.)
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cuda_bf16.h>
@@ -1318,9 +1319,10 @@ int check_full(const dsa_full_problem* p) {
 // takes the same loads and half the products; an item, its queries and output.
 constexpr int kCostRows = 4, kCostKeys = 3, kCostItem = 20;
 
-// Lays the items out over the blocks (fp: the problem and the runs, mp: the
-// items that are split) and returns the number of blocks.
-int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp) {
+// Lays the items out over at most min(sms, kMaxCtas, tiles) blocks (fp: the
+// problem and the runs, mp: the items that are split) and returns their number;
+// *most gets that bound.
+int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp, int* most) {
   fp->B = p->batch;
   fp->Hq = p->num_q_heads;
   fp->Hkv = p->num_kv_heads;
@@ -1346,8 +1348,8 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
     cost += kCostItem + static_cast<long long>(w.ntiles) * (w.nrows > kSlotRows ? kCostRows : kCostKeys);
     tiles += w.ntiles;
   }
-  const int most = imin(sms, kMaxCtas);
-  const int want = static_cast<int>(tiles < most ? (tiles > 0 ? tiles : 1) : most);
+  const int want = static_cast<int>(std::min<long long>(imin(sms, kMaxCtas), std::max(tiles, 1LL)));
+  if (most) *most = want;
   // run k begins where the costs reach k / want of their sum
   int blocks = 0;
   long long at = 0;
@@ -1389,9 +1391,10 @@ constexpr size_t kPartialAt = 256 + ((kMaxCtas * 4 + 255) / 256) * 256;
 size_t full_bytes(const dsa_full_problem* p) {
   FullParams fp{};
   MergeParams mp{};
-  // (a schedule never has more blocks than tiles, whatever the device)
-  const int blocks = schedule(p, kMaxCtas, &fp, &mp);
-  return kPartialAt + static_cast<size_t>(2) * blocks * fp.part_rows * (DSA_HEAD_DIM + 2) * 4;
+  // (more SMs may lead to fewer blocks: cuts that fall into the same tile are one)
+  int most = 0;
+  schedule(p, kMaxCtas, &fp, &mp, &most);
+  return kPartialAt + static_cast<size_t>(2) * most * fp.part_rows * (DSA_HEAD_DIM + 2) * 4;
 }
 
 template <bool QK_F16, bool PV_F16, bool INT8>
@@ -1403,12 +1406,14 @@ cudaError_t launch_full(bool mod, int blocks, const CUtensorMap& tm_k, const CUt
   if (e != cudaSuccess) return e;
   // the warps' register counts must fit into what the block is launched with:
   // a warp that asks for more would wait for ever
-  static std::atomic<int> regs{0};   // of either kernel of this family: their launch bounds are the same
-  if (regs.load(std::memory_order_relaxed) == 0) {
-    cudaFuncAttributes a;
-    if ((e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(kern))) != cudaSuccess) return e;
-    if (INT8 && a.numRegs * kThreads8 < kRegs8) return cudaErrorInvalidConfiguration;
-    regs.store(a.numRegs, std::memory_order_relaxed);
+  if constexpr (INT8) {
+    static std::atomic<int> regs[2];   // of either kernel, once asked for
+    if (regs[mod].load(std::memory_order_relaxed) == 0) {
+      cudaFuncAttributes a;
+      if ((e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(kern))) != cudaSuccess) return e;
+      if (a.numRegs * kThreads8 < kRegs8) return cudaErrorInvalidConfiguration;
+      regs[mod].store(a.numRegs, std::memory_order_relaxed);
+    }
   }
   return launch_kernel("full_attn_kernel", kern, dim3(blocks), dim3(INT8 ? kThreads8 : kThreads16), smem, st, false,
                        tm_k, tm_v, fp);
@@ -1437,7 +1442,7 @@ int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* 
   if (int rc = current_device(&sms)) return rc;
   FullParams fp{};
   MergeParams mp{};
-  const int blocks = schedule(p, sms, &fp, &mp);
+  const int blocks = schedule(p, sms, &fp, &mp, nullptr);
   if (fp.seq[p->batch].q0 == 0) {
     const cudaError_t e = cudaMemsetAsync(ws, 0, 4, static_cast<cudaStream_t>(stream));   // the status word
     return e == cudaSuccess ? DSA_OK : report_errorf(DSA_ERR_CUDA, "status clear: %s", cudaGetErrorString(e));
