@@ -513,11 +513,13 @@ int dsa_cache_append_paged(const dsa_problem* p, const dsa_kv_pages* pages, cons
  *   out      [N, Hq, 128] out_dtype, 16-byte aligned
  *   lse      [N, Hq] fp32 or NULL
  *
- * Arithmetic: logits, softmax statistics and sums in fp32; the weights enter
- * the second product in 16 bits. The workspace is read and written as
- * described at the top; the call takes its size from
- * dsa_full_attn_workspace_size (0 and a message if `p` is invalid).
- * N = 0 runs no kernel. The pages have no counterpart of this call.
+ * Arithmetic: logits, softmax statistics and sums in fp32. The weights enter
+ * the second product in FP16 for an FP16 cache, as a pair of BF16 numbers for
+ * an FP16 query on an INT8 cache, and in BF16 otherwise. A BF16 query on an
+ * FP16 cache is scaled by a power of two per row. The workspace is read and
+ * written as described at the top; the call takes its size from
+ * dsa_full_attn_workspace_size (0 and a message if `p` is invalid). N = 0 runs
+ * no kernel.
  */
 typedef struct dsa_full_problem {
   int32_t batch;
@@ -658,6 +660,8 @@ int dsa_pages_compact(const dsa_page_state* st, int num_pools, const dsa_page_po
  *   out_tokens  [batch, select] int32
  *   out_parents [batch, select] int32: the row (batch entry * beams + beam)
  *               that is continued -- what dsa_pages_update takes as `parent`
+ * The results overlap neither each other nor an input, but for out_scores,
+ * which may be `scores` itself where select == beams.
  *
  * Sums are taken in fp32 per thread and joined in 64 bits; totals are formed
  * and compared in 64 bits.
@@ -720,8 +724,8 @@ int dsa_version(void);
 /*
  * dsa_last_launches -- the kernels that the last dsa_index_scores, dsa_topk,
  * dsa_topk_noalloc, dsa_cache_append, dsa_rmsnorm_rotary, dsa_rope_append,
- * dsa_sparse_attn_decode or
- * dsa_sparse_attn_prefill call (or its _paged form) on
+ * dsa_sparse_attn_decode, dsa_sparse_attn_prefill, dsa_full_attn (or its
+ * _paged form), dsa_pages_update, dsa_pages_compact or dsa_beam_select call on
  * this host thread enqueued. Returns how many (0 after a call that failed
  * before launching); when buf is not NULL, writes their names in launch order,
  * comma-separated and NUL-terminated, truncated to fit buflen bytes. No

@@ -187,3 +187,14 @@ def test_binding_refusals(D):
         D.dsa_beam_select(p, x, s[:3], *o, ws)
     with pytest.raises(D.DsaError):
         D.dsa_beam_select(p, x, s, *o, ws[:256])
+
+
+def test_scores_in_place(D):
+    x, s = rand(24, 9001, "bf16", 31)
+    want = run(D, x, s, 4, 6, 6)
+    p = D.make_beam_problem(4, 6, 9001, 6)
+    o = tuple(torch.empty_like(w) for w in want[1:])
+    D.dsa_beam_select(p, x, s, s.view(4, 6), *o, D.alloc_beam_workspace(p))
+    assert torch.equal(s.view(4, 6), want[0]) and torch.equal(o[0], want[1]) and torch.equal(o[1], want[2])
+    with pytest.raises(D.DsaError):
+        D.dsa_beam_select(p, x, s, want[0], s.view(torch.int32).view(4, 6), o[1], D.alloc_beam_workspace(p))

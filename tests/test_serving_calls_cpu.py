@@ -155,10 +155,21 @@ def test_beam_call_checks(D):
     p = D.make_beam_problem(2, 4, 100, 8, "fp32")
     need = D.dsa_beam_workspace_size(p)
 
-    def call(logits=0x1000, scores=0x2000, o=0x3000, ws=0x10000, n=need):
-        return lib.dsa_beam_select(ctypes.byref(p), logits, scores, None, o, 0x4000, 0x5000, ws, n, None)
+    def call(logits=0x1000, scores=0x2000, o=0x3000, ws=0x10000, n=need, tokens=0x4000, done=None, p=p):
+        return lib.dsa_beam_select(ctypes.byref(p), logits, scores, done, o, tokens, 0x5000, ws, n, None)
 
     assert call(logits=None) == D.DSA_ERR_INVALID_ARG
+    assert call(o=0x2000) == D.DSA_ERR_INVALID_ARG           # select != beams
+    assert call(o=0x1ffc) == D.DSA_ERR_INVALID_ARG
+    assert call(tokens=0x3010) == D.DSA_ERR_INVALID_ARG
+    assert call(o=0x1000 + 8 * 400 - 4) == D.DSA_ERR_INVALID_ARG
+    assert call(done=0x4020) == D.DSA_ERR_INVALID_ARG
+    same = D.make_beam_problem(2, 8, 100, 8, "fp32")
+    assert call(tokens=0x2000, p=same) == D.DSA_ERR_INVALID_ARG
+    import torch
+    if not torch.cuda.is_available():
+        assert call(o=0x2000, p=same, logits=0x8000, ws=0x100000, n=1 << 40) == D.DSA_ERR_NO_DEVICE
+        assert call() == D.DSA_ERR_NO_DEVICE
     assert call(logits=0x1002) == D.DSA_ERR_MISALIGNED
     assert call(o=0x3001) == D.DSA_ERR_MISALIGNED
     assert call(n=need - 1) == D.DSA_ERR_WORKSPACE

@@ -76,7 +76,7 @@ struct BeamParams {
   long long stride;   // elements between rows
   unsigned per, extra;         // units of a block: per, one more in the first `extra`
   int row_tiles;
-  int batch, beams, vocab, select, slices, pad;
+  int beams, vocab, select, slices, pad;
 };
 
 // Block c takes the units (tiles of all rows) [run_begin(c), run_begin(c + 1)).
@@ -459,8 +459,8 @@ __device__ __forceinline__ double key_double(unsigned long long k) {
   return __longlong_as_double(static_cast<long long>((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
 }
 
-// log2(e) (log(x / 2^36)) of x > 0 as an integer of log2 plus hi + lo in natural
-// units: with x = 2^e q, q in [1/sqrt 2, sqrt 2), and f = (q - 1) / (q + 1),
+// log(x / 2^36) of x > 0 is n log 2 + hi + lo with the n that is returned: with
+// x = 2^e q, q in [1/sqrt 2, sqrt 2), and f = (q - 1) / (q + 1),
 // log q = 2 f + 2 f (f^2 / 3 + f^4 / 5 + ...), |f| < 0.172. 2 f is taken to two
 // fp32 numbers, the rest, below 4e-3, in fp32: together good to 2e-9. (64-bit
 // arithmetic has a latency of some hundred cycles here, and this kernel's time
@@ -774,6 +774,20 @@ extern "C" int dsa_beam_select(const dsa_beam_problem* bp, const void* logits, c
       (reinterpret_cast<uintptr_t>(out_scores) & 3) || (reinterpret_cast<uintptr_t>(out_tokens) & 3) ||
       (reinterpret_cast<uintptr_t>(out_parents) & 3))
     return report_error(DSA_ERR_MISALIGNED, "tensors must be aligned to their elements");
+  {
+    // (a batch entry's scores are read before its results are written, no other's)
+    const long long rows = static_cast<long long>(bp->batch) * bp->beams;
+    const long long outs = static_cast<long long>(bp->batch) * bp->select * 4;
+    const void* out[3] = {out_scores, out_tokens, out_parents};
+    const bool in_place = out_scores == scores && bp->select == bp->beams;
+    const long long elem = bp->logits_dtype == DSA_FP32 ? 4 : 2;
+    const long long read = ((rows - 1) * (bp->row_stride ? bp->row_stride : bp->vocab) + bp->vocab) * elem;
+    for (int i = 0; i < 3; ++i)
+      if (overlap(out[i], outs, logits, read) || (overlap(out[i], outs, scores, rows * 4) && !(i == 0 && in_place)) ||
+          (finished && overlap(out[i], outs, finished, rows)) || overlap(out[i], outs, out[(i + 1) % 3], outs))
+        return report_error(DSA_ERR_INVALID_ARG, "the results must not overlap each other or an input (out_scores "
+                            "may be `scores` itself where select == beams)");
+  }
   size_t sums_at = 0;
   if (int rc = check_call_workspace(ws, ws_bytes, beam_bytes(bp, &sums_at))) return rc;
   int sms = 0;
@@ -789,7 +803,6 @@ extern "C" int dsa_beam_select(const dsa_beam_problem* bp, const void* logits, c
   p.out_scores = out_scores;
   p.out_tokens = out_tokens;
   p.out_parents = out_parents;
-  p.batch = bp->batch;
   p.beams = bp->beams;
   p.vocab = bp->vocab;
   p.select = bp->select;

@@ -256,6 +256,10 @@ cudaError_t launch_cache_append(const AppendParams& p, int sms, cudaStream_t str
 int report_error(int status, const char* msg);
 int report_errorf(int status, const char* fmt, ...);
 int check_call_workspace(const void* ws, size_t bytes, size_t need);
+inline bool overlap(const void* a, long long an, const void* b, long long bn) {   // of a's an bytes and b's bn
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
+}
 int current_device(int* sms);   // its SM count; an error status if it is not of this family
 int check_full_pages(const dsa_full_problem* p, const dsa_kv_pages* pages, Paging* pg);
 // tiles of 128 consecutive cache rows of one KV head (elem_bytes 2 or 1)

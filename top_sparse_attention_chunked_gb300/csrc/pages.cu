@@ -465,11 +465,6 @@ __global__ void __launch_bounds__(kPgThreads)
 }
 
 // -------------------------------------------------------------------- host
-bool overlap(const void* a, long long an, const void* b, long long bn) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
-}
-
 bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
 int check_state(const dsa_page_state* st, PageDims* d) {
