@@ -353,6 +353,15 @@ __device__ __forceinline__ uint32_t widen2(uint32_t x, int i) {
   }
 }
 
+// Byte e of x and of y, two signed codes, as two BF16 (see above).
+__device__ __forceinline__ uint32_t widen_pair(uint32_t x, uint32_t y, int e) {
+  const uint32_t u = __byte_perm(x, y, (4 + e) << 8 | e);
+  const uint32_t a = (u & 0x007f007fu) | 0x43004300u, b = (u & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // A wait of a whole warp: every lane gets the same answer, and the warp is
 // converged afterwards.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -1164,6 +1173,365 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
     p.errors[blockIdx.x] = (bars->abort_flag ? kDevTimeout : 0u) | (bars->bad_page ? kDevBadPage : 0u);
 }
 
+// --------------------------------------------------------------- few rows
+// INT8 caches, items of up to 16 rows (one token of up to 16 heads a KV head):
+// the tensor core's tiles would be empty but for a few rows, and its operands
+// have to pass through shared memory once more as 16-bit tiles. Here eight
+// warps take 16 keys of a tile each, read the codes straight into the register
+// layout of m16n8k16 products (rows of Q x 8 keys x 16 dims, rows x 8 dims x 16
+// keys) and widen them there. The two contractions may take their indices in
+// any order, and keys and output columns may be permuted, which is used so that
+// every thread reads 16 consecutive codes at a time, without bank conflicts:
+//   S: thread (g, c) = (lane / 4, lane % 4) holds, of key row 4 (g % 2) + g / 2
+//      of eight, the dims 16 c .. and 64 + 16 c .. (16 each);
+//   O: of keys c, c + 4, c + 8, c + 12 the dims 16 (4 (g % 2) + g / 2) .. (16).
+// Each warp has its own running maximum, sum and output; they are joined at the
+// segment's end. Schedule, loads, parts and merge are as above.
+constexpr int kFewRows = 16, kFewWarps = 12, kFewThreads = 32 * (kFewWarps + 4);   // (the loader's warpgroup last)
+constexpr int kFewGroup = 16, kFewGroups = kTileKeys / kFewGroup;   // keys a warp takes at once; such groups of a tile
+constexpr int kFewRing = 3;
+constexpr int kFewRegs = 152, kFewLoadRegs = 56;
+constexpr int kFewLaunchRegs = 32 * kFewWarps * kFewRegs + 128 * kFewLoadRegs;
+constexpr uint32_t kFewStage = 2 * kTile8 + 2 * kTileKeys * 4;   // K, V, their scales (1 KB)
+constexpr int kFewPitch = DSA_HEAD_DIM + 4;            // floats between rows of a warp's output
+
+struct FewBars {
+  uint64_t full[kFewRing], empty[kFewRing];
+  int abort_flag, bad_page;
+  float2 ml[kFewWarps][kFewRows];
+};
+
+constexpr size_t kFewJoin = sizeof(float) * kFewWarps * kFewRows * kFewPitch;
+constexpr size_t few_smem() {
+  return kFewRing * kFewStage + kFewJoin + sizeof(FewBars);
+}
+
+// One stage holds a tile's keys, values and scales.
+__device__ __forceinline__ void few_load(const FullParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                         FewBars* bars, uint8_t* ring, volatile int* abort_flag) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  RingPos pos;
+  bool bad = false, ok = true;
+  Walk walk(p);
+  Segment s;
+  while (ok && walk.next(p, &s)) {
+    long long rows = 0;
+    for (int t = s.t0; t < s.t1; ++t) {
+      // cache rows of 32 tiles, one a lane
+      if (((t - s.t0) & 31) == 0)
+        rows = t + lane < s.t1 ? cache_row(p.pg, s.w.b, p.cap, (s.w.tile0 + t + lane) * kTileKeys, &bad) : 0;
+      const long long first = __shfl_sync(0xffffffffu, rows, (t - s.t0) & 31);
+      if (pos.round > 0 && !warp_wait(&bars->empty[pos.stage], (pos.round - 1) & 1, abort_flag)) {
+        ok = false;
+        break;
+      }
+      uint8_t* dst = ring + pos.stage * kFewStage;
+      uint64_t* bar = &bars->full[pos.stage];
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, 2 * kTile8);
+        tma_load_3d(dst, &tm_k, bar, 0, s.w.g, static_cast<int>(first));
+        tma_load_3d(dst + kTile8, &tm_v, bar, 0, s.w.g, static_cast<int>(first));
+      }
+      float* sc = reinterpret_cast<float*>(dst + 2 * kTile8);
+      const int key = (s.w.tile0 + t) * kTileKeys;
+#pragma unroll
+      for (int i = 0; i < kTileKeys / 32; ++i) {
+        const int r = i * 32 + lane;
+        const bool in = key + r >= s.w.lo && key + r < s.w.hi;
+        const long long at = in ? (first + r) * p.Hkv + s.w.g : 0;
+        cp_async4(sc + r, p.k_scale + at, in);
+        cp_async4(sc + kTileKeys + r, p.v_scale + at, in);
+      }
+      cp_async_arrive(bar);
+      __syncwarp();
+      pos.step(kFewRing);
+    }
+  }
+  if (bad) bars->bad_page = 1;
+  cp_async_commit();
+  cp_async_wait<0>();
+  __syncwarp();
+  if (lane == 0) {
+    // (as load_role: no copy in flight at the end)
+    for (int q = 0; q < kFewRing; ++q) {
+      const uint32_t uses = pos.round + (q < pos.stage ? 1 : 0);
+      if (uses == 0) continue;
+      const long long t0 = clock64();
+      while (!mbar_try_wait(&bars->full[q], (uses - 1) & 1) && clock64() - t0 < kWaitBudgetCycles) {
+      }
+    }
+  }
+}
+
+// SPLIT: the weights go as BF16 pairs (an FP16 query, see split_p). MOD as above.
+template <bool SPLIT, bool MOD>
+__device__ __forceinline__ void few_role(const FullParams& p, FewBars* bars, const uint8_t* ring, float* join,
+                                         volatile int* abort_flag) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  const int perm = 4 * (g & 1) + (g >> 1);             // key row, and 16-byte column, of g
+  uint32_t before = 0;                                  // tiles of the segments before
+  Walk walk(p);
+  Segment s;
+  while (walk.next(p, &s)) {
+    // queries: rows g and g + 8, this thread's 32 dims
+    uint32_t q[8][4];
+    int at[2], lo[2];
+    float slope[2], unit[2];                            // unit: log2 units per unit of S, without the key's scale
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = imin(g + 8 * i, s.w.nrows - 1), tok = r / p.G, head = s.w.g * p.G + (r - tok * p.G);
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const uint16_t*>(p.q) + ((static_cast<long long>(s.w.q0) + tok) * p.Hq + head) * DSA_HEAD_DIM);
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 u = __ldg(src + (j >> 1) * 8 + 2 * c + (j & 1));
+        w[4 * j] = u.x;
+        w[4 * j + 1] = u.y;
+        w[4 * j + 2] = u.z;
+        w[4 * j + 3] = u.w;
+      }
+      unit[i] = p.scale_log2;
+      if constexpr (!SPLIT) {   // a BF16 row: to FP16, its largest exponent to 14 (see softmax_role)
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int ex = top >= 0x80u ? static_cast<int>(top >> 7) - 127 - 14 : -126 - 14;
+        const float f0 = __int_as_float((127 - ex / 2) << 23), f1 = __int_as_float((127 - (ex - ex / 2)) << 23);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w[e] = pack2<true>(__uint_as_float(w[e] << 16) * f0 * f1, __uint_as_float(w[e] & 0xffff0000u) * f0 * f1);
+        unit[i] = ldexpf(p.scale_log2, ex);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        q[j][i] = w[2 * j];
+        q[j][2 + i] = w[2 * j + 1];
+      }
+      at[i] = s.w.past + tok;
+      lo[i] = imax(s.w.first, p.window > 0 ? at[i] - p.window + 1 : 0);
+      slope[i] = MOD && p.slopes ? p.slopes[head] * 1.4426950408889634f : 0.f;
+    }
+    const int pos0 = s.w.past, lo1 = imax(s.w.first, p.window > 0 ? s.w.past + (s.w.nrows - 1) / p.G - p.window + 1 : 0);
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // (m in log2 units)
+    float o[16][4];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    const int groups = (s.t1 - s.t0) * kFewGroups;
+    for (int grp = warp; grp < groups; grp += kFewWarps) {
+      const uint32_t tile = grp / kFewGroups, use = before + tile, stage = use % kFewRing;
+      const int first = (grp % kFewGroups) * kFewGroup;   // within the tile
+      if (!warp_wait(&bars->full[stage], (use / kFewRing) & 1, abort_flag)) break;
+      const uint8_t* src = ring + stage * kFewStage + first * 128;
+      // S of 2 x 8 keys
+      uint4 u[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = (j >> 1) * 8 + perm, chunk = (j & 1) * 4 + c;
+        u[j] = *reinterpret_cast<const uint4*>(src + row * 128 + ((chunk ^ (row & 7)) << 4));
+      }
+      float z[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint4& x = u[2 * n + j];
+            const uint32_t y = w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w;
+            const uint32_t b[2] = {widen2<true>(y, 0), widen2<true>(y, 1)};
+            mma_16816<true>(z[n], q[4 * j + w], b);
+          }
+      src += kTile8;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = 4 * j + c;
+        u[j] = *reinterpret_cast<const uint4*>(src + row * 128 + ((perm ^ (row & 7)) << 4));
+      }
+      // logits: z[n][2 i + e] is row i's, key 8 n + 4 e + c
+      const float* sc = reinterpret_cast<const float*>(ring + stage * kFewStage + 2 * kTile8) + first + c;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[n][e] *= sc[8 * n + 4 * (e & 1)];
+      const int key0 = (s.w.tile0 + s.t0 + static_cast<int>(tile)) * kTileKeys;
+      if constexpr (MOD) {   // to log2 units
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            z[n][e] *= unit[e >> 1];
+            if (p.softcap > 0.f) {
+              const float two = 2.0f / p.softcap, cap = p.softcap * 1.4426950408889634f;
+              z[n][e] = fmaf(-2.0f * cap, fast_rcp(1.0f + fast_exp2(z[n][e] * two)), cap);
+            }
+            z[n][e] = fmaf(slope[e >> 1], static_cast<float>(key0 + first + 8 * n + 4 * (e & 1) + c - at[e >> 1]), z[n][e]);
+          }
+      }
+      if (key0 + kTileKeys - 1 > pos0 || key0 < lo1) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + first + 8 * n + 4 * (e & 1) + c;
+            if (key < lo[e >> 1] || key > at[e >> 1]) z[n][e] = -INFINITY;
+          }
+      }
+      float top[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        top[i] = fmaxf(fmaxf(z[0][2 * i], z[0][2 * i + 1]), fmaxf(z[1][2 * i], z[1][2 * i + 1])) * (MOD ? 1.0f : unit[i]);
+      if (__any_sync(0xffffffffu, top[0] > m[0] + kRaise || top[1] > m[1] + kRaise)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+          top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+          const float to = fmaxf(m[i], top[i]);
+          const float f = m[i] == -INFINITY ? 0.f : fast_exp2(m[i] - to);
+          m[i] = to;
+          l[i] *= f;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            o[j][2 * i] *= f;
+            o[j][2 * i + 1] *= f;
+          }
+        }
+      }
+      uint32_t a[4], al[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float mc = m[i] == -INFINITY ? 0.f : kLift - m[i], un = MOD ? 1.0f : unit[i];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float x = fast_exp2(fmaf(z[n][2 * i], un, mc)), y = fast_exp2(fmaf(z[n][2 * i + 1], un, mc));
+          l[i] += x + y;
+          x *= sc[kTileKeys + 8 * n];
+          y *= sc[kTileKeys + 8 * n + 4];
+          a[2 * n + i] = pack2<false>(x, y);
+          if constexpr (SPLIT)
+            al[2 * n + i] = pack2<false>(x - __uint_as_float(a[2 * n + i] << 16),
+                                         y - __uint_as_float(a[2 * n + i] & 0xffff0000u));
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const auto word = [&](const uint4& x) { return w == 0 ? x.x : w == 1 ? x.y : w == 2 ? x.z : x.w; };
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // byte e of two keys, side by side
+          const uint32_t b[2] = {widen_pair(word(u[0]), word(u[1]), e), widen_pair(word(u[2]), word(u[3]), e)};
+          mma_16816<false>(o[4 * w + e], a, b);
+          if constexpr (SPLIT) mma_16816<false>(o[4 * w + e], al, b);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->empty[stage]);
+    }
+    before += s.t1 - s.t0;
+    // the warps' states, joined
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if (c == 0) bars->ml[warp][g + 8 * i] = make_float2(m[i], l[i]);
+      // columns 2 c and 2 c + 1 are dims 16 c .. and 64 + 16 c ..
+      float* d = join + (warp * kFewRows + g + 8 * i) * kFewPitch + 16 * c;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+          *reinterpret_cast<float4*>(d + 64 * e + j) =
+              make_float4(o[j][2 * i + e], o[j + 1][2 * i + e], o[j + 2][2 * i + e], o[j + 3][2 * i + e]);
+    }
+    named_bar_sync(1, 32 * kFewWarps);
+    if (threadIdx.x < 16 * kFewRows) {   // 16 threads a row
+      const int r = threadIdx.x >> 4, d = (threadIdx.x & 15) * 8;
+      float mj = -INFINITY, lj = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) mj = fmaxf(mj, bars->ml[w][r].x);
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) {
+        const float2 v = bars->ml[w][r];
+        const float f = v.x == -INFINITY ? 0.f : fast_exp2(v.x - mj);
+        lj = fmaf(v.y, f, lj);
+        const float* y = join + (w * kFewRows + r) * kFewPitch + d;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fmaf(y[e], f, x[e]);
+      }
+      if (r < s.w.nrows) {
+        const int tok = r / p.G, head = s.w.g * p.G + (r - tok * p.G);
+        const long long row = (static_cast<long long>(s.w.q0) + tok) * p.Hq + head;
+        if (s.whole) {
+          const float norm = lj > 0.f ? 1.0f / lj : 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] *= norm;
+          if (p.lse && d == 0) p.lse[row] = lj > 0.f ? (mj - kLift + log2f(lj)) * 0.6931471805599453f : -INFINITY;
+          if (p.out_dtype == DSA_FP32) {
+            float4* to = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * DSA_HEAD_DIM + d);
+            to[0] = make_float4(x[0], x[1], x[2], x[3]);
+            to[1] = make_float4(x[4], x[5], x[6], x[7]);
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = p.out_dtype == DSA_FP16 ? pack2<true>(x[2 * e], x[2 * e + 1]) : pack2<false>(x[2 * e], x[2 * e + 1]);
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * DSA_HEAD_DIM + d) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          float* part = p.partial + static_cast<long long>(s.part) * p.part_rows * (DSA_HEAD_DIM + 2);
+          if (d == 0) *reinterpret_cast<float2*>(part + p.part_rows * DSA_HEAD_DIM + 2 * r) = make_float2(mj, lj);
+          part += d * p.part_rows + 4 * r;
+          *reinterpret_cast<float4*>(part) = make_float4(x[0], x[1], x[2], x[3]);
+          *reinterpret_cast<float4*>(part + 4 * p.part_rows) = make_float4(x[4], x[5], x[6], x[7]);
+        }
+      }
+    }
+    named_bar_sync(1, 32 * kFewWarps);
+  }
+}
+
+template <bool SPLIT, bool MOD>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    full_attn_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ FullParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (smem_u32(smem_raw) & 1023u) {
+    if (threadIdx.x == 0) p.errors[blockIdx.x] = kDevBounds;
+    return;
+  }
+  uint8_t* ring = smem_raw;
+  float* join = reinterpret_cast<float*>(ring + kFewRing * kFewStage);
+  FewBars* bars = reinterpret_cast<FewBars*>(reinterpret_cast<uint8_t*>(join) + kFewJoin);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kFewRing; ++i) {
+      mbar_init(&bars->full[i], 33);   // the copies' bytes, and 32 lanes' scales
+      mbar_init(&bars->empty[i], kFewGroups);
+    }
+    bars->abort_flag = 0;
+    bars->bad_page = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_trigger();
+  if (threadIdx.x < 32 * kFewWarps) {
+    regs_up<kFewRegs>();
+    few_role<SPLIT, MOD>(p, bars, ring, join, &bars->abort_flag);
+  } else {
+    regs_down<kFewLoadRegs>();
+    if (threadIdx.x < 32 * (kFewWarps + 1)) few_load(p, tm_k, tm_v, bars, ring, &bars->abort_flag);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0)
+    p.errors[blockIdx.x] = (bars->abort_flag ? kDevTimeout : 0u) | (bars->bad_page ? kDevBadPage : 0u);
+}
+
 // ------------------------------------------------------------------ merge
 // Joins the parts of the items that more than one block worked on. A thread
 // block takes four query rows; 128 threads hold a row's four dims each, and
@@ -1397,26 +1765,43 @@ size_t full_bytes(const dsa_full_problem* p) {
   return kPartialAt + static_cast<size_t>(2) * most * fp.part_rows * (DSA_HEAD_DIM + 2) * 4;
 }
 
+// Launches one of two kernels of a family (with and without MOD). Where warps
+// change their register counts, those must fit into what the block is launched
+// with: a warp that asks for more would wait for ever.
+template <typename K>
+cudaError_t launch_one(const char* name, K* const (&kernels)[2], bool mod, std::atomic<int> (&regs)[2], int need, int blocks,
+                       int threads, size_t smem, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const FullParams& fp,
+                       cudaStream_t st) {
+  K* const kern = kernels[mod];
+  cudaError_t e = set_max_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  if (need > 0 && regs[mod].load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes a;
+    if ((e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(kern))) != cudaSuccess) return e;
+    if (a.numRegs * threads < need) return cudaErrorInvalidConfiguration;
+    regs[mod].store(a.numRegs, std::memory_order_relaxed);
+  }
+  return launch_kernel(name, kern, dim3(blocks), dim3(threads), smem, st, false, tm_k, tm_v, fp);
+}
+
 template <bool QK_F16, bool PV_F16, bool INT8>
 cudaError_t launch_full(bool mod, int blocks, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const FullParams& fp,
                         cudaStream_t st) {
-  const auto kern = mod ? full_attn_kernel<QK_F16, PV_F16, INT8, true> : full_attn_kernel<QK_F16, PV_F16, INT8, false>;
-  constexpr size_t smem = full_smem<INT8>();
-  cudaError_t e = set_max_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  // the warps' register counts must fit into what the block is launched with:
-  // a warp that asks for more would wait for ever
-  if constexpr (INT8) {
-    static std::atomic<int> regs[2];   // of either kernel, once asked for
-    if (regs[mod].load(std::memory_order_relaxed) == 0) {
-      cudaFuncAttributes a;
-      if ((e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(kern))) != cudaSuccess) return e;
-      if (a.numRegs * kThreads8 < kRegs8) return cudaErrorInvalidConfiguration;
-      regs[mod].store(a.numRegs, std::memory_order_relaxed);
-    }
-  }
-  return launch_kernel("full_attn_kernel", kern, dim3(blocks), dim3(INT8 ? kThreads8 : kThreads16), smem, st, false,
-                       tm_k, tm_v, fp);
+  static std::atomic<int> regs[2];
+  using K = void(const CUtensorMap, const CUtensorMap, const FullParams);
+  K* const kernels[2] = {full_attn_kernel<QK_F16, PV_F16, INT8, false>, full_attn_kernel<QK_F16, PV_F16, INT8, true>};
+  return launch_one("full_attn_kernel", kernels, mod, regs, INT8 ? kRegs8 : 0, blocks, INT8 ? kThreads8 : kThreads16,
+                    full_smem<INT8>(), tm_k, tm_v, fp, st);
+}
+
+template <bool SPLIT>
+cudaError_t launch_few(bool mod, int blocks, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const FullParams& fp,
+                       cudaStream_t st) {
+  static std::atomic<int> regs[2];
+  using K = void(const CUtensorMap, const CUtensorMap, const FullParams);
+  K* const kernels[2] = {full_attn_few_kernel<SPLIT, false>, full_attn_few_kernel<SPLIT, true>};
+  return launch_one("full_attn_few_kernel", kernels, mod, regs, kFewLaunchRegs, blocks, kFewThreads, few_smem(), tm_k, tm_v,
+                    fp, st);
 }
 
 int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* q, const void* k, const void* v,
@@ -1478,7 +1863,10 @@ int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool mod = p->softcap > 0.0f || slopes != nullptr;
   cudaError_t e;
-  if (p->kv_dtype == DSA_BF16) e = launch_full<false, false, false>(mod, blocks, tm_k, tm_v, fp, st);
+  if (p->kv_dtype == DSA_INT8 && fp.part_rows <= kFewRows)
+    e = p->q_dtype == DSA_FP16 ? launch_few<true>(mod, blocks, tm_k, tm_v, fp, st)
+                               : launch_few<false>(mod, blocks, tm_k, tm_v, fp, st);
+  else if (p->kv_dtype == DSA_BF16) e = launch_full<false, false, false>(mod, blocks, tm_k, tm_v, fp, st);
   else if (p->kv_dtype == DSA_FP16) e = launch_full<true, true, false>(mod, blocks, tm_k, tm_v, fp, st);
   else if (p->q_dtype == DSA_FP16) e = launch_full<true, false, true>(mod, blocks, tm_k, tm_v, fp, st);
   else e = launch_full<false, false, true>(mod, blocks, tm_k, tm_v, fp, st);
