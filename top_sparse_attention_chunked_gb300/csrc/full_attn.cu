@@ -72,7 +72,10 @@ constexpr int kScaleRing = 8;                          // see load_role
 // Warps: 8 softmax (slot, quarter of the rows), 4 for the products and the
 // loads, 4 that widen INT8 tiles.
 constexpr int kSoftThreads = 256, kThreads16 = 384, kWidenThreads = 128, kThreads8 = kThreads16 + kWidenThreads;
-constexpr int kHalf = kTileKeys / 2;
+// Columns of S that a softmax thread takes at once. INT8: fewer, for its code has
+// to share the instruction cache with the widening.
+template <bool INT8>
+__host__ __device__ constexpr int part_cols() { return INT8 ? 32 : 64; }
 // Registers: 16-bit blocks have enough as they are launched (168 a thread);
 // with INT8 the softmax takes what the others give up. What the block needs in
 // all must be within what it is launched with:
@@ -609,9 +612,10 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
     tc_fence_after();
 #pragma unroll
     for (int kk = 0; kk < kTileKeys / 16; ++kk) {
-      const uint32_t pa = tmem + slot * 128 + (kk >> 2) * kHalf + (kk & 3) * 8;
+      constexpr int kCols = part_cols<INT8>(), kSteps = kCols / 16;   // (a part's weights over its own columns)
+      const uint32_t pa = tmem + slot * 128 + kk / kSteps * kCols + kk % kSteps * 8;
       mma_ts(tmem + 256 + slot * 128, pa, b + kk * (16 * 128 / 16), id_pv, !first || kk > 0);
-      if constexpr (split_p<QK_F16, INT8>()) mma_ts(tmem + 256 + slot * 128, pa + 32, b + kk * (16 * 128 / 16), id_pv, true);
+      if constexpr (split_p<QK_F16, INT8>()) mma_ts(tmem + 256 + slot * 128, pa + kCols / 2, b + kk * (16 * 128 / 16), id_pv, true);
     }
     return true;
   };
@@ -741,12 +745,12 @@ __device__ __forceinline__ void cap_scores(float* z, float c, float softcap) {
   }
 }
 
-// The 32 columns of P (64 weights a row) at `addr` times f.
-template <bool F16>
+// N columns of P (2 N weights a row) at `addr` times f.
+template <bool F16, int N>
 __device__ __forceinline__ void rescale_p(uint32_t addr, float f) {
   tmem_st_wait();   // (this warp's own store of them)
 #pragma unroll 1
-  for (int i = 0; i < 32; i += 16) {
+  for (int i = 0; i < N; i += 16) {
     float v[16];
     uint32_t w[16];
     tmem_ld16(addr + i, v);
@@ -767,15 +771,16 @@ __device__ __forceinline__ void rescale_p(uint32_t addr, float f) {
 // One slot's four warps, one row a thread. MOD: the scores are capped or get a
 // bias.
 //
-// A row goes in two halves of 64 columns (code and registers for one). The
+// A row goes in parts of 64 or 32 columns (code and registers for one). The
 // exponentials are formed with the running maximum as it was, next to the
-// half's own maximum; only where that calls for raising the former are they
+// part's own maximum; only where that calls for raising the former are they
 // formed again.
 template <bool QK_F16, bool PV_F16, bool INT8, bool MOD>
 __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint8_t* sQ,
                                              const float* scales, int slot, volatile int* abort_flag) {
   const int tid = threadIdx.x & 127, lane = tid & 31, warp_row = tid & ~31;
   constexpr bool kSplit = split_p<QK_F16, INT8>();
+  constexpr int kCols = part_cols<INT8>();
   const bool scaled = QK_F16 && !INT8 && p.q_dtype == DSA_BF16;
   bool begin = true;
   const uint32_t lane_addr = static_cast<uint32_t>(warp_row) << 16;
@@ -886,18 +891,18 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
       const bool masked = key0 + kTileKeys - 1 > pos0 || key0 < lo1;
       const float* sc = scales + ((tile_seq + (t - s.t0)) % kScaleRing) * 2 * kTileKeys;
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kTileKeys / kCols; ++h) {
         if (warp_valid) {
-          const int col = h * kHalf, first = key0 + col;
-          float z[kHalf];
+          const int col = h * kCols, first = key0 + col;
+          float z[kCols];
           tmem_ld32(tS + col, z);
-          tmem_ld32(tS + col + 32, z + 32);
+          if constexpr (kCols > 32) tmem_ld32(tS + col + 32, z + 32);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < kHalf; ++i) asm volatile("" : "+f"(z[i]));   // no use before the wait
+          for (int i = 0; i < kCols; ++i) asm volatile("" : "+f"(z[i]));   // no use before the wait
           if constexpr (INT8) {
 #pragma unroll
-            for (int i = 0; i < kHalf; i += 4) {
+            for (int i = 0; i < kCols; i += 4) {
               const float4 f = *reinterpret_cast<const float4*>(sc + col + i);
               z[i] *= f.x;
               z[i + 1] *= f.y;
@@ -906,23 +911,23 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
             }
           }
           if constexpr (MOD) {
-            if (p.softcap > 0.f) cap_scores<kHalf>(z, c, p.softcap);
+            if (p.softcap > 0.f) cap_scores<kCols>(z, c, p.softcap);
             else
 #pragma unroll
-              for (int i = 0; i < kHalf; ++i) z[i] *= c;
+              for (int i = 0; i < kCols; ++i) z[i] *= c;
             if (p.slopes) {
               const float d = static_cast<float>(first - pos);
 #pragma unroll
-              for (int i = 0; i < kHalf; ++i) z[i] = fmaf(slope, d + static_cast<float>(i), z[i]);
+              for (int i = 0; i < kCols; ++i) z[i] = fmaf(slope, d + static_cast<float>(i), z[i]);
             }
           }
           if (masked) {
             const int a = lo - first, b = pos - first;   // columns a .. b are visible
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i)
+            for (int i = 0; i < kCols; ++i)
               if (i < a || i > b) z[i] = -INFINITY;
           }
-          uint32_t w[32], wl[kSplit ? 32 : 1];
+          uint32_t w[kCols / 2], wl[kSplit ? kCols / 2 : 1];
           float2 sum[2];
 #pragma unroll 1
           while (true) {
@@ -931,7 +936,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
             const float2 c2 = make_float2(cz, cz), m2 = make_float2(mc, mc);
             float mt[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
+            for (int i = 0; i < kCols / 2; i += 8) {
               float2 pr[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) pr[e] = fma_f32x2(make_float2(z[2 * (i + e)], z[2 * (i + e) + 1]), c2, m2);
@@ -961,9 +966,10 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
             m = to;
             l *= f;
             if (j < 0) break;
-            if (h == 1) {   // the first half's P, not yet in O
-              rescale_p<PV_F16>(tS, f);
-              if constexpr (kSplit) rescale_p<PV_F16>(tS + 32, f);
+#pragma unroll 1
+            for (int e = 0; e < h; ++e) {   // the parts before, not yet in O
+              rescale_p<PV_F16, kCols / 2>(tS + e * kCols, f);
+              if constexpr (kSplit) rescale_p<PV_F16, kCols / 2>(tS + e * kCols + kCols / 2, f);
             }
             if (j > 0) {
 #pragma unroll 1
@@ -981,8 +987,12 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
             }
           }
           if (j >= 0) {   // over columns of S that have been read
-            tmem_st32(tS + col, w);
-            if constexpr (kSplit) tmem_st32(tS + col + 32, wl);
+            if constexpr (kCols > 32) {
+              tmem_st32(tS + col, w);
+            } else {
+              tmem_st16(tS + col, w);
+              if constexpr (kSplit) tmem_st16(tS + col + kCols / 2, wl);
+            }
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
