@@ -37,11 +37,11 @@
 // shared memory (a masked weight is 0, but 0 times a NaN is not); masked
 // columns of S are replaced before the maximum, whatever they hold.
 //
-// Types: the products take the cache's type (INT8: the query's for S, BF16 for
-// P V, since a value's scale may lie outside FP16's range). A BF16 query on an
-// FP16 cache is scaled by a power of two per row to at most 2^14 first, which
-// is exact for all elements within 2^-28 of the row's largest. (An FP16 query on
-// INT8: see split_p.)
+// Types: the products take the cache's type (INT8: FP16 for S, which codes are
+// widened to in the fewest instructions, and BF16 for P V, since a value's scale
+// may lie outside FP16's range). A BF16 query for a product in FP16 is scaled by
+// a power of two per row to at most 2^14 first, which is exact for all elements
+// within 2^-28 of the row's largest. (An FP16 query on INT8: see split_p.)
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -527,38 +527,42 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
 // kWidenThreads threads. Eight lanes take chunks 0-3 (16 codes each) of an even row and 4-7
 // of the next, then the other halves: the reads, and the two 16-byte writes a
 // chunk becomes, each touch eight different 16-byte columns.
+struct WidenAt {   // this thread's places in a tile of codes and in a 16-bit tile
+  int from, to;
+  __device__ __forceinline__ explicit WidenAt(int tid) {
+    const int half = (tid >> 2) & 1, row = (tid >> 3) * 2 + half;
+    from = row * 128 + ((((tid & 3) + 4 * half) ^ (row & 7)) << 4);
+    to = half * kBlk + row * 128 + ((((tid & 3) * 2) ^ (row & 7)) << 4);
+  }
+};
 template <bool F16>
-__device__ __forceinline__ void widen_tile(const uint8_t* src, uint8_t* dst, int tid) {
-  const int half = (tid >> 2) & 1;
-  constexpr int kPairs = kWidenThreads / 8;   // pairs of rows at once
+__device__ __forceinline__ void widen_tile(const uint8_t* src, uint8_t* dst, const WidenAt& at) {
+  constexpr int kStep = kWidenThreads / 4 * 128;   // bytes of the rows taken at once, a multiple of eight rows
+  static_assert(kWidenThreads % 32 == 0 && kTile8 % (2 * kStep) == 0, "rows a thread takes");
 #pragma unroll 1
-  for (int r0 = tid >> 3; r0 < kTileKeys / 2; r0 += 2 * kPairs) {
+  for (int i = 0; i < static_cast<int>(kTile8); i += 2 * kStep) {
     uint4 x[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = (r0 + (j >> 1) * kPairs) * 2 + half;
-      x[j] = *reinterpret_cast<const uint4*>(src + row * 128 + ((((tid & 3) + 4 * (half ^ (j & 1))) ^ (row & 7)) << 4));
-    }
+    for (int j = 0; j < 4; ++j)
+      x[j] = *reinterpret_cast<const uint4*>(src + i + (j >> 1) * kStep + (at.from ^ ((j & 1) << 6)));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = (r0 + (j >> 1) * kPairs) * 2 + half;
-      const int c = (tid & 3) + 4 * (half ^ (j & 1));
       const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
       uint32_t o[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = widen2<F16>(w[e >> 1], e & 1);
-      uint8_t* d = dst + (c >> 2) * kBlk + row * 128;
-      const int ch = (c & 3) * 2;
-      *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      uint8_t* d = dst + i + (j >> 1) * kStep;
+      const int to = at.to ^ ((j & 1) * kBlk);
+      *reinterpret_cast<uint4*>(d + to) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(d + (to ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
     }
   }
 }
 
-template <bool QK_F16>
 __device__ __forceinline__ void widen_role(const FullParams& p, FullBars* bars, uint8_t* ring, const uint8_t* raw,
                                            int raw_stages, int tid, volatile int* abort_flag) {
   RingPos from, to;
+  const WidenAt at(tid);
   Walk walk(p);
   Segment s;
   while (walk.next(p, &s)) {
@@ -567,8 +571,8 @@ __device__ __forceinline__ void widen_role(const FullParams& p, FullBars* bars, 
       if (to.round > 0 && !warp_wait(&bars->empty[to.stage], (to.round - 1) & 1, abort_flag)) return false;
       const uint8_t* src = raw + from.stage * kTile8;
       uint8_t* dst = ring + to.stage * kTile16;
-      if (!QK_F16 || is_v) widen_tile<false>(src, dst, tid);
-      else widen_tile<QK_F16>(src, dst, tid);
+      if (is_v) widen_tile<false>(src, dst, at);
+      else widen_tile<true>(src, dst, at);
       fence_async_smem();
       mbar_arrive(&bars->full[to.stage]);
       mbar_arrive(&bars->raw_empty[from.stage]);
@@ -590,7 +594,7 @@ __host__ __device__ constexpr bool split_p() { return QK_F16 && INT8; }
 template <bool QK_F16, bool PV_F16, bool INT8>
 __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint32_t q_addr,
                                          uint32_t ring_addr, int stages, volatile int* abort_flag) {
-  constexpr uint32_t id_qk = idesc128(QK_F16, false), id_pv = idesc128(PV_F16, true);
+  constexpr uint32_t id_qk = idesc128(QK_F16 || INT8, false), id_pv = idesc128(PV_F16, true);
   const uint32_t qd = desc_lo(q_addr, 16), kd = desc_lo(ring_addr, 16), vd = desc_lo(ring_addr, kBlk);
   uint32_t nseg = 0, np[2] = {0, 0};
   RingPos pos;
@@ -781,7 +785,8 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
   const int tid = threadIdx.x & 127, lane = tid & 31, warp_row = tid & ~31;
   constexpr bool kSplit = split_p<QK_F16, INT8>();
   constexpr int kCols = part_cols<INT8>();
-  const bool scaled = QK_F16 && !INT8 && p.q_dtype == DSA_BF16;
+  constexpr bool kMayScale = QK_F16 != INT8;   // a BF16 query for products in FP16
+  const bool scaled = kMayScale && p.q_dtype == DSA_BF16;
   bool begin = true;
   const uint32_t lane_addr = static_cast<uint32_t>(warp_row) << 16;
   const uint32_t tS = tmem + lane_addr + slot * 128, tO = tmem + lane_addr + 256 + slot * 128;
@@ -821,8 +826,8 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = warp_row + (i0 + i) * 4 + (lane >> 3);
-          if constexpr (QK_F16 && !INT8) {   // (no INT8 call converts its query)
-            if (p.q_dtype == DSA_BF16) {
+          if constexpr (kMayScale) {
+            if (scaled) {
               // the row's largest exponent to 14: scaled by 2^-ex
               uint32_t w[8] = {u[i][0].x, u[i][0].y, u[i][0].z, u[i][0].w, u[i][1].x, u[i][1].y, u[i][1].z, u[i][1].w};
               uint32_t top = 0;
@@ -1172,7 +1177,7 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
   } else {
     if constexpr (INT8) {
       regs_down<kWidenRegs>();
-      widen_role<QK_F16>(p, bars, ring, raw, raw_stages, threadIdx.x - kThreads16, abort_flag);
+      widen_role(p, bars, ring, raw, raw_stages, threadIdx.x - kThreads16, abort_flag);
     }
   }
   tc_fence_before();
