@@ -63,11 +63,10 @@ constexpr uint32_t kBlk = kTileKeys * 128;             // 64 columns of a 16-bit
 constexpr uint32_t kTile16 = 2 * kBlk;                 // 32 KB
 constexpr uint32_t kTile8 = kTileKeys * DSA_HEAD_DIM;  // 16 KB of codes
 constexpr uint32_t kTmemCols = 512;                    // S 0-127, 128-255; O 256-383, 384-511
-// Stages of the rings. A call without an item of more than 128 rows does not
-// need the second query tile: its 32 KB hold one stage (16-bit) or two (INT8
-// codes) more.
+// Stages of the rings (a sixth 16-bit stage in place of the second query tile,
+// which calls without an item of more than 128 rows do not need, gained nothing:
+// 16 ragged decodes of up to 32K 52.0 us with it, 51.2 without).
 constexpr int kRing16 = 5, kRing8 = 3, kRaw = 3;
-constexpr int kMaxRing = 6, kMaxRaw = 5;
 constexpr int kScaleRing = 8;                          // see load_role
 // Warps: 8 softmax (slot, quarter of the rows), 4 for the products and the
 // loads, 4 that widen INT8 tiles.
@@ -99,7 +98,6 @@ struct FullParams {
   // consecutive rows write consecutive 16 bytes), then [part_rows] (m, l)
   float* partial;
   int part_rows;
-  int wide;             // some item has more than 128 rows
   int B, Hq, Hkv, G, cap, window;
   int q_dtype, out_dtype;
   float scale_log2, softcap;
@@ -209,8 +207,8 @@ __device__ __forceinline__ SlotWork slot_work(const Segment& s, int slot) {
 }
 
 struct FullBars {
-  uint64_t full[kMaxRing], empty[kMaxRing];       // 16-bit tiles ready / consumed
-  uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];     // INT8 codes landed / widened
+  uint64_t full[kRing16], empty[kRing16];       // 16-bit tiles ready / consumed
+  uint64_t raw_full[kRaw], raw_empty[kRaw];     // INT8 codes landed / widened
   uint64_t scales[kScaleRing];                  // a tile's scales are in shared memory
   uint64_t q_ready[2], s_full[2], p_full[2], o_full[2];
   uint64_t fix;                                 // a tile whose rows are zeroed before use has landed
@@ -371,7 +369,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag));
 }
 
-// Position in a ring whose number of stages is known at run time.
+// Position in a ring.
 struct RingPos {
   int stage = 0;
   uint32_t round = 0;       // parity: the round's `full`; of `empty`, the round before
@@ -417,10 +415,11 @@ __device__ __forceinline__ bool for_tiles(const Segment& s, F&& f) {
 // weights of tile i + 1.
 template <bool INT8>
 __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                          FullBars* bars, uint8_t* ring, int stages, float* scales,
+                                          FullBars* bars, uint8_t* ring, float* scales,
                                           volatile int* abort_flag) {
   const int lane = threadIdx.x & 31;
   constexpr uint32_t kBytes = INT8 ? kTile8 : kTile16;
+  constexpr int stages = INT8 ? kRaw : kRing16;
   uint64_t* full = INT8 ? bars->raw_full : bars->full;
   uint64_t* empty = INT8 ? bars->raw_empty : bars->empty;
   if (lane == 0) {
@@ -560,7 +559,7 @@ __device__ __forceinline__ void widen_tile(const uint8_t* src, uint8_t* dst, con
 }
 
 __device__ __forceinline__ void widen_role(const FullParams& p, FullBars* bars, uint8_t* ring, const uint8_t* raw,
-                                           int raw_stages, int tid, volatile int* abort_flag) {
+                                           int tid, volatile int* abort_flag) {
   RingPos from, to;
   const WidenAt at(tid);
   Walk walk(p);
@@ -576,7 +575,7 @@ __device__ __forceinline__ void widen_role(const FullParams& p, FullBars* bars, 
       fence_async_smem();
       mbar_arrive(&bars->full[to.stage]);
       mbar_arrive(&bars->raw_empty[from.stage]);
-      from.step(raw_stages);
+      from.step(kRaw);
       to.step(kRing8);
       return true;
     });
@@ -593,7 +592,8 @@ __host__ __device__ constexpr bool split_p() { return QK_F16 && INT8; }
 
 template <bool QK_F16, bool PV_F16, bool INT8>
 __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint32_t q_addr,
-                                         uint32_t ring_addr, int stages, volatile int* abort_flag) {
+                                         uint32_t ring_addr, volatile int* abort_flag) {
+  constexpr int stages = INT8 ? kRing8 : kRing16;
   constexpr uint32_t id_qk = idesc128(QK_F16 || INT8, false), id_pv = idesc128(PV_F16, true);
   const uint32_t qd = desc_lo(q_addr, 16), kd = desc_lo(ring_addr, 16), vd = desc_lo(ring_addr, kBlk);
   uint32_t nseg = 0, np[2] = {0, 0};
@@ -787,7 +787,6 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
   constexpr int kCols = part_cols<INT8>();
   constexpr bool kMayScale = QK_F16 != INT8;   // a BF16 query for products in FP16
   const bool scaled = kMayScale && p.q_dtype == DSA_BF16;
-  bool begin = true;
   const uint32_t lane_addr = static_cast<uint32_t>(warp_row) << 16;
   const uint32_t tS = tmem + lane_addr + slot * 128, tO = tmem + lane_addr + 256 + slot * 128;
   uint32_t ns = 0, no = 0, nml = 0, nseg = 0, tile_seq = 0;
@@ -871,22 +870,16 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     float m = -INFINITY, l = 0.f;   // running maximum (in S units, or log2 units where c = 1), sum
     const float cz = MOD ? 1.0f : c;
     bool ok = true;
-    // (round -1 of a block's first segment forms weights of whatever tensor
-    // memory holds and drops them: the loop's instructions come into the cache
-    // while the first tile is on its way -- 5,200 cycles for the first tile's
-    // softmax otherwise, 1,400 for the next; INT8's larger code gains nothing)
-    for (int j = begin && !INT8 ? -1 : 0; j < x.n; ++j) {
-      const int t = x.first + imax(j, 0) * x.step;
+    for (int j = 0; j < x.n; ++j) {
+      const int t = x.first + j * x.step;
       const int key0 = (s.w.tile0 + t) * kTileKeys;
-      if (j >= 0) {
-        if (!warp_wait(&bars->s_full[slot], ns & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        ++ns;
-        tc_fence_after();
+      if (!warp_wait(&bars->s_full[slot], ns & 1, abort_flag)) {
+        ok = false;
+        break;
       }
-      if (INT8 && j >= 0) {
+      ++ns;
+      tc_fence_after();
+      if constexpr (INT8) {
         const uint32_t q = tile_seq + (t - s.t0);
         if (!warp_wait(&bars->scales[q % kScaleRing], (q / kScaleRing) & 1, abort_flag)) {
           ok = false;
@@ -970,7 +963,6 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
             const float f = to == -INFINITY || m == -INFINITY ? (m == to ? 1.0f : 0.0f) : fast_exp2((m - to) * cz);
             m = to;
             l *= f;
-            if (j < 0) break;
 #pragma unroll 1
             for (int e = 0; e < h; ++e) {   // the parts before, not yet in O
               rescale_p<PV_F16, kCols / 2>(tS + e * kCols, f);
@@ -991,27 +983,20 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
               }
             }
           }
-          if (j >= 0) {   // over columns of S that have been read
-            if constexpr (kCols > 32) {
-              tmem_st32(tS + col, w);
-            } else {
-              tmem_st16(tS + col, w);
-              if constexpr (kSplit) tmem_st16(tS + col + kCols / 2, wl);
-            }
+          // over columns of S that have been read
+          if constexpr (kCols > 32) {
+            tmem_st32(tS + col, w);
+          } else {
+            tmem_st16(tS + col, w);
+            if constexpr (kSplit) tmem_st16(tS + col + kCols / 2, wl);
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         }
-      }
-      if (j < 0) {
-        m = -INFINITY;
-        l = 0.f;
-        continue;
       }
       if (warp_valid) tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&bars->p_full[slot]);
     }
-    begin = false;
     if (!ok) break;
     tile_seq += s.t1 - s.t0;
     const float m_log2 = m == -INFINITY ? -INFINITY : m * cz;
@@ -1122,24 +1107,20 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
     if (threadIdx.x == 0) p.errors[blockIdx.x] = kDevBounds;
     return;
   }
-  // queries | (INT8: codes) | 16-bit tiles | (INT8: scales) | barriers; without
-  // wide items what follows the first query tile begins at the second
+  // queries | (INT8: codes) | 16-bit tiles | (INT8: scales) | barriers
   uint8_t* sQ = base;
-  uint8_t* after_q = sQ + (p.wide ? 2 : 1) * kTile16;
-  const int raw_stages = INT8 ? (p.wide ? kRaw : kMaxRaw) : 0;
-  const int stages = INT8 ? kRing8 : (p.wide ? kRing16 : kMaxRing);
-  uint8_t* raw = after_q;
-  uint8_t* ring = after_q + raw_stages * kTile8;
-  float* scales = reinterpret_cast<float*>(base + 2 * kTile16 + (INT8 ? kRaw * kTile8 + kRing8 * kTile16 : kRing16 * kTile16));
+  uint8_t* raw = sQ + 2 * kTile16;
+  uint8_t* ring = raw + (INT8 ? kRaw * kTile8 : 0);
+  float* scales = reinterpret_cast<float*>(ring + (INT8 ? kRing8 : kRing16) * kTile16);
   FullBars* bars = reinterpret_cast<FullBars*>(reinterpret_cast<uint8_t*>(scales) + (INT8 ? kScaleRing * 2 * kTileKeys * 4 : 0));
   volatile int* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kMaxRing; ++i) {
+    for (int i = 0; i < kRing16; ++i) {
       mbar_init(&bars->full[i], INT8 ? kWidenThreads : 1);
       mbar_init(&bars->empty[i], 1);
     }
-    for (int i = 0; i < kMaxRaw; ++i) {
+    for (int i = 0; i < kRaw; ++i) {
       mbar_init(&bars->raw_full[i], 1);
       mbar_init(&bars->raw_empty[i], kWidenThreads);
     }
@@ -1170,14 +1151,14 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
     if constexpr (INT8) regs_down<kMiscRegs8>();
     if (warp == 8) {
       if ((threadIdx.x & 31) == 0)
-        mma_role<QK_F16, PV_F16, INT8>(p, bars, tmem, smem_u32(sQ), smem_u32(ring), stages, abort_flag);
+        mma_role<QK_F16, PV_F16, INT8>(p, bars, tmem, smem_u32(sQ), smem_u32(ring), abort_flag);
     } else if (warp == 9) {
-      load_role<INT8>(p, tm_k, tm_v, bars, INT8 ? raw : ring, INT8 ? raw_stages : stages, scales, abort_flag);
+      load_role<INT8>(p, tm_k, tm_v, bars, INT8 ? raw : ring, scales, abort_flag);
     }
   } else {
     if constexpr (INT8) {
       regs_down<kWidenRegs>();
-      widen_role(p, bars, ring, raw, raw_stages, threadIdx.x - kThreads16, abort_flag);
+      widen_role(p, bars, ring, raw, threadIdx.x - kThreads16, abort_flag);
     }
   }
   tc_fence_before();
@@ -1721,7 +1702,6 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
     fp->seq[b].first = p->first_key[b];
     fp->part_rows = imax(fp->part_rows, static_cast<int>(rows < kItemRows ? rows : kItemRows));
   }
-  fp->wide = fp->part_rows > kSlotRows;
   fp->part_rows = (fp->part_rows + 3) & ~3;   // parts stay 16-byte aligned
   const int items = fp->seq[p->batch].item0;
   long long cost = 0, tiles = 0;
