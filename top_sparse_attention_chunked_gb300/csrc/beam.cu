@@ -51,8 +51,9 @@ constexpr int kGroup = 2;           // tiles between two looks at the list's len
 constexpr int kMergeThreads = 1024;
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kMaxLists = 512;      // slices of one batch entry
-constexpr int kRound = 2 * kMergeWarps;           // lists that the merge takes at once
-constexpr int kMergeList = kRound * kKeep;        // and their candidates
+constexpr int kRound = kMergeWarps;               // lists that the merge takes at once
+constexpr int kMergeList = 2 * kRound * kKeep;    // room for their candidates, and as many left from before
+constexpr int kBounds = 4;                        // values of a warp that go into the merge's bound
 constexpr int kShare = kKeep / kMergeWarps;
 constexpr int kResident = 3;        // scan blocks per SM (70 KB of shared memory each for 16-bit logits)
 
@@ -495,7 +496,7 @@ __device__ __forceinline__ int log_fixed(unsigned long long x, float* hi, float*
 
 // One thread block per batch entry; its beams' slices are the lists
 // b * slices + j.
-__global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamParams p) {
+__global__ void __launch_bounds__(kMergeThreads, 1) beam_merge_kernel(const BeamParams p) {
   extern __shared__ Total s_totals[];       // kMergeList + DSA_MAX_SELECT
   Total* s_list = s_totals;
   __shared__ Total s_buf[kBmThreads];
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   __shared__ double s_off[DSA_MAX_BEAMS];   // score - log sum exp of each beam (a finished one: its score)
   __shared__ float s_score[DSA_MAX_BEAMS];
   __shared__ uint8_t s_over[DSA_MAX_BEAMS];
-  __shared__ uint32_t s_bound[2 * kMergeWarps];
+  __shared__ uint32_t s_bound[kBounds * kMergeWarps];
   __shared__ int s_count;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int row0 = blockIdx.x * p.beams;
@@ -585,8 +586,8 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
     s_off[tid] = off;
   }
   __syncthreads();
-  // A bound on the totals (fp32, rounded down): of the warps' two largest values
-  // `select` reach the select-th largest.
+  // A bound on the totals (fp32, rounded down): of the warps' four largest values
+  // (one a lane) `select` reach the select-th largest.
   uint32_t best = 0u;
   const auto join_list = [&](int i, const uint32_t* key) {
     if (i >= lists) return;
@@ -607,28 +608,31 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
     fetch(i, key);
     join_list(i, key);
   }
-  const uint32_t first = __reduce_max_sync(0xffffffffu, best);
-  const uint32_t holders = __ballot_sync(0xffffffffu, best == first);
-  if (lane == __ffs(holders) - 1) best = 0u;
-  const uint32_t second = __reduce_max_sync(0xffffffffu, best);
-  if (lane == 0) {
-    s_bound[wid] = first;
-    s_bound[kMergeWarps + wid] = second;
+#pragma unroll
+  for (int i = 0; i < kBounds; ++i) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const uint32_t holders = __ballot_sync(0xffffffffu, best == top);
+    if (lane == __ffs(holders) - 1) best = 0u;
+    if (lane == 0) s_bound[i * kMergeWarps + wid] = top;
   }
   __syncthreads();
   if (wid == 0) {
-    // the select-th largest of the 64 (a lane's first is no less than its second)
-    uint32_t cur = s_bound[lane], rest = s_bound[32 + lane], bound = 0u;
+    // the select-th largest of them (a lane's are in order)
+    uint32_t cur[kBounds], bound = 0u;
+#pragma unroll
+    for (int i = 0; i < kBounds; ++i) cur[i] = s_bound[i * kMergeWarps + lane];
 #pragma unroll 1
     for (int i = 0; i < k; ++i) {
-      bound = __reduce_max_sync(0xffffffffu, cur);
+      bound = __reduce_max_sync(0xffffffffu, cur[0]);
       if (bound == 0u) break;
-      const uint32_t holders = __ballot_sync(0xffffffffu, cur == bound);
+      const uint32_t holders = __ballot_sync(0xffffffffu, cur[0] == bound);
       if (lane == __ffs(holders) - 1) {
-        cur = rest;
-        rest = 0u;
+#pragma unroll
+        for (int j = 0; j + 1 < kBounds; ++j) cur[j] = cur[j + 1];
+        cur[kBounds - 1] = 0u;
       }
     }
+    __syncwarp();
     if (lane == 0) s_bound[0] = bound;
   }
   __syncthreads();
@@ -636,7 +640,8 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
   // the totals of those that may reach it, a round of lists at a time
   int have = 0;
   for (int r = 0; r < lists; r += kRound) {
-    for (int i = r + wid; i < min(lists, r + kRound); i += kMergeWarps) {
+    const int i = r + wid;
+    if (i < lists) {
       const int at_b = i / p.slices, n = s_sum[i].count;
       const double off = s_off[at_b];
       const float off_up = __double2float_ru(off);
@@ -655,8 +660,12 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamPar
       }
     }
     __syncthreads();
-    // join them with the best so far
+    // join them with the best so far, when all are there or there may be no room for another round's
     const int n = s_count, old = have;
+    if (r + kRound < lists && n <= kMergeList - kRound * kKeep) {
+      __syncthreads();   // (the count has been read)
+      continue;
+    }
     if (old + n <= kBmThreads) {
       if (tid < old) s_buf[tid] = s_best[tid];
       else if (tid < old + n) s_buf[tid] = s_list[tid - old];
