@@ -43,7 +43,10 @@ constexpr int kPlanThreads = 1024;
 constexpr int kCopyUnroll = 8;
 // States that one block counts by itself, sums in shared memory: up to this many
 // table entries and blocks.
-constexpr int kSmallEntries = 8192, kSmallBlocks = 8192;
+constexpr int kSmallEntries = 4096, kSmallBlocks = 8192;
+// Times 32 blocks that a warp of a plan kernel looks at together: many keep loads
+// in flight, few keep the code short, which is what a small state's time goes on.
+constexpr int kWalkSmall = 2, kWalkLarge = 8;
 constexpr long long kPiece = kPgThreads * 16LL * kCopyUnroll;   // bytes of one copy task
 
 struct PageDims {
@@ -197,6 +200,7 @@ __device__ __forceinline__ int warp_prefix(int v, int* tot, int* sum) {
 
 // One block: the rows' copies and fresh blocks, the list of free blocks, the
 // new counts.
+template <int WALK>
 __device__ __forceinline__ void plan_update(const PageDims& d, const PageWs& w, const Counts& c, const Rows& a,
                                             const int32_t* refs, int32_t* refs_out, int32_t* counts) {
   __shared__ uint32_t scan_tot[32];
@@ -236,34 +240,48 @@ __device__ __forceinline__ void plan_update(const PageDims& d, const PageWs& w, 
   int lo, hi;
   warp_slice(d.nb, &lo, &hi);
   int mine = 0, mine_before = 0;   // free after / before the releases
-#pragma unroll 4
-  for (int b = lo; b < hi; b += 32) {
-    const int r = b + lane < hi ? refs[b + lane] : 1;
-    const int n = b + lane < hi ? r + c.delta[b + lane] : 1;
-    mine += __popc(__ballot_sync(0xffffffffu, n == 0));
-    mine_before += __popc(__ballot_sync(0xffffffffu, r == 0));
+  for (int b = lo; b < hi; b += 32 * WALK) {
+    int r[WALK], n[WALK];
+#pragma unroll
+    for (int i = 0; i < WALK; ++i) {
+      const int id = b + 32 * i + lane;
+      r[i] = id < hi ? refs[id] : 1;
+      n[i] = id < hi ? r[i] + c.delta[id] : 1;
+    }
+#pragma unroll
+    for (int i = 0; i < WALK; ++i) {
+      mine += __popc(__ballot_sync(0xffffffffu, n[i] == 0));
+      mine_before += __popc(__ballot_sync(0xffffffffu, r[i] == 0));
+    }
   }
   int nfree, nbefore;
   int rank = warp_prefix(mine, warp_tot, &nfree);
   warp_prefix(mine_before, warp_tot, &nbefore);
   if (wanted > static_cast<uint32_t>(nfree)) fail = true;
-#pragma unroll 4
-  for (int b = lo; b < hi; b += 32) {
-    const bool in = b + lane < hi;
-    const int old = in ? refs[b + lane] : 1;
-    int n = in ? old + c.delta[b + lane] : 1;
-    const uint32_t m = __ballot_sync(0xffffffffu, n == 0);
-    if (n == 0) {
-      const int k = rank + __popc(m & ((1u << lane) - 1u));
-      w.free_ids[k] = b + lane;
-      if (k < static_cast<int>(wanted)) n = 1;
-    } else if (in) {
-      // its writers that copy let go of it
-      const int wr = c.writers[b + lane];
-      n -= wr - (wr > 0 && n == wr ? 1 : 0);
+  for (int b = lo; b < hi; b += 32 * WALK) {
+    int old[WALK], n[WALK], wr[WALK];   // (all read first: refs_out may be refs)
+#pragma unroll
+    for (int i = 0; i < WALK; ++i) {
+      const int id = b + 32 * i + lane;
+      old[i] = id < hi ? refs[id] : 1;
+      n[i] = id < hi ? old[i] + c.delta[id] : 1;
+      wr[i] = id < hi ? c.writers[id] : 0;
     }
-    rank += __popc(m);
-    if (in) refs_out[b + lane] = fail ? old : n;
+#pragma unroll
+    for (int i = 0; i < WALK; ++i) {
+      const int id = b + 32 * i + lane;
+      const uint32_t m = __ballot_sync(0xffffffffu, n[i] == 0);
+      if (n[i] == 0) {
+        const int k = rank + __popc(m & ((1u << lane) - 1u));
+        w.free_ids[k] = id;
+        if (k < static_cast<int>(wanted)) n[i] = 1;
+      } else {
+        // its writers that copy let go of it
+        n[i] -= wr[i] - (wr[i] > 0 && n[i] == wr[i] ? 1 : 0);
+      }
+      rank += __popc(m);
+      if (id < hi) refs_out[id] = fail ? old[i] : n[i];
+    }
   }
   if (threadIdx.x == 0) {
     *w.status = bad ? kDevBadState : fail ? kDevNoPages : 0u;
@@ -276,16 +294,16 @@ __device__ __forceinline__ void plan_update(const PageDims& d, const PageWs& w, 
   }
 }
 
-__global__ void __launch_bounds__(kPlanThreads)
+__global__ void __launch_bounds__(kPlanThreads, 1)
     pages_plan_kernel(const PageDims d, const PageWs w, const Rows a, const int32_t* refs, int32_t* refs_out,
                       int32_t* counts) {
   pdl_wait();
-  plan_update(d, w, Counts{w.flag, w.delta, w.writers, w.low}, a, refs, refs_out, counts);
+  plan_update<kWalkLarge>(d, w, Counts{w.flag, w.delta, w.writers, w.low}, a, refs, refs_out, counts);
 }
 
 // Small states: the count and the plan in one block, the sums in shared memory
 // (cleared here). One launch in place of three.
-__global__ void __launch_bounds__(kPlanThreads)
+__global__ void __launch_bounds__(kPlanThreads, 1)
     pages_small_kernel(const PageDims d, const PageWs w, const Rows a, const int32_t* __restrict__ table,
                        const int32_t* refs, int32_t* refs_out, int32_t* counts) {
   extern __shared__ int32_t sums[];   // 3 * nb + 1
@@ -296,7 +314,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   const int n = d.rows * d.W;
   for (int e = threadIdx.x; e < n; e += kPlanThreads) count_entry(d, c, w.stage, a, table, e);
   __syncthreads();
-  plan_update(d, w, c, a, refs, refs_out, counts);
+  plan_update<kWalkSmall>(d, w, c, a, refs, refs_out, counts);
 }
 
 // Copy task t of `src` -> `dst` in every pool: one piece of one pool's block.
@@ -369,7 +387,8 @@ __global__ void __launch_bounds__(kPgThreads)
 }
 
 // `table` is given where the block checks the entries itself (small states).
-__global__ void __launch_bounds__(kPlanThreads)
+template <int WALK>
+__global__ void __launch_bounds__(kPlanThreads, 1)
     compact_plan_kernel(const PageDims d, const PageWs w, const int32_t* table, const int32_t* refs,
                         int32_t* refs_out, int32_t* remap_out, int32_t* counts) {
   __shared__ int warp_tot[32];
@@ -385,37 +404,52 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   int lo, hi;
   warp_slice(d.nb, &lo, &hi);
-  int mine = 0;
-#pragma unroll 4
-  for (int b = lo; b < hi; b += 32)
-    mine += __popc(__ballot_sync(0xffffffffu, b + lane < hi && refs[b + lane] > 0));
+  // live blocks of the warp's slice below `end`
+  const auto count_live = [&](int end) {
+    int n = 0;
+    for (int b = lo; b < end; b += 32 * WALK) {
+      bool used[WALK];
+#pragma unroll
+      for (int i = 0; i < WALK; ++i) {
+        const int id = b + 32 * i + lane;
+        used[i] = id < end && refs[id] > 0;
+      }
+#pragma unroll
+      for (int i = 0; i < WALK; ++i) n += __popc(__ballot_sync(0xffffffffu, used[i]));
+    }
+    return n;
+  };
+  const int mine = count_live(hi);
   int live;
   const int before = warp_prefix(mine, warp_tot, &live);
   // k-th hole below `live`, k-th live block from `live` on: there are as many
   // of either. With x live blocks before block b, b - x free ones are.
   int x = before;
-  int high = 0;            // live blocks below `live`
-#pragma unroll 4
-  for (int b = lo; b < hi; b += 32)
-    high += __popc(__ballot_sync(0xffffffffu, b + lane < min(hi, live) && refs[b + lane] > 0));
+  const int high = count_live(min(hi, live));   // live blocks below `live`
   int below;
   warp_prefix(high, warp_tot, &below);
-#pragma unroll 4
-  for (int b = lo; b < hi; b += 32) {
-    const int id = b + lane;
-    const bool in = id < hi;
-    const bool used = in && refs[id] > 0;
-    const uint32_t m = __ballot_sync(0xffffffffu, used);
-    const int rank = x + __popc(m & ((1u << lane) - 1u));   // live blocks before this one
-    x += __popc(m);
-    if (!in) continue;
-    int to = used ? id : -1;
-    if (!fail) {
-      if (!used && id < live) w.free_ids[id - rank] = id;
-      if (used && id >= live) w.movers[rank - below] = id;
+  for (int b = lo; b < hi; b += 32 * WALK) {
+    bool used[WALK];
+#pragma unroll
+    for (int i = 0; i < WALK; ++i) {
+      const int id = b + 32 * i + lane;
+      used[i] = id < hi && refs[id] > 0;
     }
-    w.remap[id] = to;
-    if (remap_out) remap_out[id] = to;
+#pragma unroll
+    for (int i = 0; i < WALK; ++i) {
+      const int id = b + 32 * i + lane;
+      const uint32_t m = __ballot_sync(0xffffffffu, used[i]);
+      const int rank = x + __popc(m & ((1u << lane) - 1u));   // live blocks before this one
+      x += __popc(m);
+      if (id >= hi) continue;
+      const int to = used[i] ? id : -1;
+      if (!fail) {
+        if (!used[i] && id < live) w.free_ids[id - rank] = id;
+        if (used[i] && id >= live) w.movers[rank - below] = id;
+      }
+      w.remap[id] = to;
+      if (remap_out) remap_out[id] = to;
+    }
   }
   const int moves = fail ? 0 : live - below;
   __syncthreads();   // the lists are complete (block-wide visibility of global writes)
@@ -626,7 +660,7 @@ extern "C" int dsa_pages_compact(const dsa_page_state* st, int num_pools, const 
                         d, w, st->block_table, st->refs);
   }
   if (e == cudaSuccess)
-    e = launch_kernel("compact_plan_kernel", compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, !small, d, w,
+    e = launch_kernel("compact_plan_kernel", small ? compact_plan_kernel<kWalkSmall> : compact_plan_kernel<kWalkLarge>, dim3(1), dim3(kPlanThreads), 0, s, !small, d, w,
                       small ? st->block_table : nullptr, st->refs, refs_out, remap, counts);
   if (e == cudaSuccess)
     e = launch_kernel("compact_commit_kernel", compact_commit_kernel,
