@@ -263,6 +263,38 @@ def test_peaked_softmax_rescales(D):
     run(D, c)
 
 
+@pytest.mark.parametrize("q_len,total", [([1], [700]), ([4, 150], [300, 411])])
+@pytest.mark.parametrize("kv", ["bf16", "fp16", "int8"])
+@pytest.mark.parametrize("scale", [0.0, 1e-6, 1e-38])
+def test_zero_queries(D, q_len, total, kv, scale):
+    """Rows of zeros, and of BF16's smallest numbers, beside ordinary ones: even weights, under masks too."""
+    c = make(q_len, total, 8, 2, "bf16", kv, block=128, seed=3)
+    c["q"][:, ::2] = 0
+    c["q"][:, 1] = 2.0 ** -133
+    run(D, c, scale=scale, window=300)
+
+
+@pytest.mark.parametrize("q", ["bf16", "fp16"])
+@pytest.mark.parametrize("hq,hkv,n", [(1, 1, 1), (8, 8, 1), (15, 1, 1), (16, 2, 2), (16, 1, 1), (17, 1, 1), (32, 2, 1), (34, 2, 1)])
+def test_few_rows_int8(D, q, hq, hkv, n):
+    """Up to 16 rows and just above, many sequences: whole items and parts in every block."""
+    g = torch.Generator().manual_seed(hq)
+    total = [n] + (torch.randint(n, 2600, (22,), generator=g)).tolist() + [2600]
+    run(D, make([n] * 24, total, hq, hkv, q, "int8", block=256, seed=hq))
+    run(D, make([n] * 24, total, hq, hkv, q, "int8", seed=n), window=300, softcap=9.0,
+        slopes=torch.tensor([2.0 ** (-0.3 * h) for h in range(hq)]))
+
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_peaked_softmax_rescales_int8(D, n):
+    c = make([n], [1500], 8, 2, "bf16", "int8", seed=3, q_std=1.0)
+    c["k"] = torch.where(c["k"] == 127, c["k"], c["k"].abs().clamp(1, 90))
+    c["k_scale"] = torch.linspace(1e-4, 3e-2, c["cap"])[None, :, None].repeat(1, 1, 2).contiguous()
+    c["v_scale"] = (c["v_scale"] * torch.exp2(torch.linspace(-9, 9, c["cap"]))[None, :, None]).contiguous()
+    c["q"] = c["q"].abs()
+    run(D, c, out_dtype="fp32")
+
+
 def test_dense_equals_paged(D):
     for kv in ("fp16", "int8"):
         c = make([5, 200], [900, 333], 24, 2, "bf16", kv, block=256, seed=9)

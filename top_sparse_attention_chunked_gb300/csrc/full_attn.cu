@@ -1,5 +1,9 @@
 // Full GQA attention of every sequence's new tokens over its cached keys, on
-// tcgen05 tensor cores.
+// tcgen05 tensor cores (INT8 caches with few rows: see "few rows" below).
+//
+// With z_t = scale q.k_t (capped, biased), m any number and l = sum 2^(z_t log2 e
+// - m): out = sum 2^(z_t log2 e - m) v_t / l, lse = (m + log2 l) ln 2. Sums over
+// parts of the keys join by powers of two of the difference of their m.
 //
 // The query rows of one KV head -- all new tokens of a sequence times the G
 // heads that share the KV head, row = token * G + head -- are cut into items of
@@ -17,16 +21,27 @@
 //   keys mode (up to 128 rows): the slots share the rows and take every other
 //     key tile; their two states are joined at the item's end.
 // Per slot and tile: S = Q K^T (128 x 128, fp32, in tensor memory), four warps
-// read S (a row a thread, half of it at a time), form P = exp2(S c - m) in 16
+// read S (a row a thread, a part of it at a time), form P = exp2(S c - m) in 16
 // bits and put it back over S, O += P V with P read from tensor memory. While one
 // slot is in its softmax the other's two products run.
 //
+// What bounds it, BF16, 24 query and 2 KV heads where not said otherwise
+// (measured rates: 6.80 TB/s, 1,884 TFLOP/s):
+//   one token each on long caches: memory. 64 on 8,192: 87 us, 6.15 TB/s; 8 on
+//     32,768 with 8/8 heads: 166 us, 6.48 TB/s;
+//   few and short: two launches and the first tile's way through a cold block.
+//     One token on 1,024: 9.6 us, on 16,384: 14.3 us (1.2 TB/s);
+//   many tokens: the hand-over between tensor core and softmax. 4,096 on 16,384:
+//     523 us, 1,381 TFLOP/s (the two products alone would take 460); 4,096 on
+//     4,096: 110 us, 939 TFLOP/s (a block's share is 4 items);
+//   capped scores: the multiply-adds of the cap. 4,096 on 4,096: 148 us.
+//
 // The running maximum m is raised (and O rescaled in tensor memory) only when
-// a row's logits grow by more than 2^8 over it. P = 2^kLift exp2(S c - m): the
-// scale cancels in O / sum P, the largest weights stay below 2^15, inside
-// either 16-bit type, and FP16's smallest step (2^-24) is 2^-31 of the weight
-// at the maximum. A slot's S is only
-// complete when its previous P V is (the products run in order), so the
+// a row's weights grow by more than 2^8 over it, and by a whole power of two, to
+// just below the maximum. P = 2^kLift exp2(S c - m): the scale cancels in O / sum
+// P, the largest weights stay below 2^15, inside either 16-bit type, and FP16's
+// smallest step (2^-24) is at most 2^-31 of the weight at the maximum. A slot's S
+// is only complete when its previous P V is (the products run in order), so the
 // rescale needs no further synchronisation.
 //
 // K and V tiles arrive by TMA (128 consecutive cache rows of one head: a tile
@@ -72,7 +87,8 @@ constexpr int kScaleRing = 8;                          // see load_role
 // loads, 4 that widen INT8 tiles.
 constexpr int kSoftThreads = 256, kThreads16 = 384, kWidenThreads = 128, kThreads8 = kThreads16 + kWidenThreads;
 // Columns of S that a softmax thread takes at once. INT8: fewer, for its code has
-// to share the instruction cache with the widening.
+// to share the instruction cache with the widening (4,096 tokens on 4,096: 183 us
+// with 64, 167 with 32).
 template <bool INT8>
 __host__ __device__ constexpr int part_cols() { return INT8 ? 32 : 64; }
 // Registers: 16-bit blocks have enough as they are launched (168 a thread);
@@ -81,6 +97,7 @@ __host__ __device__ constexpr int part_cols() { return INT8 ? 32 : 64; }
 constexpr int kSoftRegs8 = 168, kMiscRegs8 = 72, kWidenRegs = 96;
 constexpr int kRegs8 = kSoftThreads * kSoftRegs8 + 128 * kMiscRegs8 + kWidenThreads * kWidenRegs;
 constexpr float kLift = 7.0f;                          // log2 of the weight at the running maximum
+constexpr float kLeastUnit = 1.17549435e-38f;           // fp32's smallest normal number
 constexpr float kRaise = 8.0f;                         // log2 growth that raises the running maximum
 
 struct FullParams {
@@ -510,14 +527,15 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
   }
   if (lane == 0) {
     // a block must not end with copies in flight (the consumers may have given up)
-    for (int q = 0; q < stages; ++q) {
-      // stage q's last use: this round if the position is past it, else the one before
-      const uint32_t uses = pos.round + (q < pos.stage ? 1 : 0);
-      if (uses == 0) continue;
+    const auto drain = [](uint64_t* bar, uint32_t uses) {
+      if (uses == 0) return;
       const long long t0 = clock64();
-      while (!mbar_try_wait(&full[q], (uses - 1) & 1) && clock64() - t0 < kWaitBudgetCycles) {
+      while (!mbar_try_wait(bar, (uses - 1) & 1) && clock64() - t0 < kWaitBudgetCycles) {
       }
-    }
+    };
+    // (stage q's last use: this round if the position is past it, else the one before)
+    for (int q = 0; q < stages; ++q) drain(&full[q], pos.round + (q < pos.stage ? 1 : 0));
+    if constexpr (!INT8) drain(&bars->fix, fixes);
   }
 }
 
@@ -772,6 +790,15 @@ __device__ __forceinline__ void rescale_p(uint32_t addr, float f) {
   }
 }
 
+// A BF16 row whose largest element has the bits `top` (without sign) is taken as
+// FP16 times 2^ex, the largest element's exponent 14; a row of zeros as it is.
+__device__ __forceinline__ int row_exponent(uint32_t top) {
+  return top == 0u ? 0 : imax(static_cast<int>(top >> 7), 1) - 127 - 14;
+}
+// Its log2 units per unit of S. Not 0: a masked column's -infinity times it
+// would be a NaN (below fp32's normal numbers no such row's logits differ from 0).
+__device__ __forceinline__ float row_unit(float scale_log2, int ex) { return fmaxf(ldexpf(scale_log2, ex), kLeastUnit); }
+
 // One slot's four warps, one row a thread. MOD: the scores are capped or get a
 // bias.
 //
@@ -834,7 +861,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
               for (int e = 0; e < 8; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
 #pragma unroll
               for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-              const int ex = top >= 0x80u ? static_cast<int>(top >> 7) - 127 - 14 : -126 - 14;
+              const int ex = row_exponent(top);
               // (two factors: 2^-ex may lie outside fp32's normal range)
               const float f0 = __int_as_float((127 - ex / 2) << 23), f1 = __int_as_float((127 - (ex - ex / 2)) << 23);
 #pragma unroll
@@ -842,7 +869,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
                 w[e] = pack2<true>(__uint_as_float(w[e] << 16) * f0 * f1, __uint_as_float(w[e] & 0xffff0000u) * f0 * f1);
               u[i][0] = make_uint4(w[0], w[1], w[2], w[3]);
               u[i][1] = make_uint4(w[4], w[5], w[6], w[7]);
-              if (sub == 0) row_c[t] = ldexpf(p.scale_log2, ex);
+              if (sub == 0) row_c[t] = row_unit(p.scale_log2, ex);
             }
           }
           uint8_t* d = dst + t * 128 + ((sub ^ (t & 7)) << 4);
@@ -959,9 +986,14 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
             // (-inf stays as it is: nothing seen yet)
             const bool raise = mn > m && (m == -INFINITY || (mn - m) * cz > kRaise);
             if (!__any_sync(0xffffffffu, raise)) break;
-            const float to = fmaxf(m, mn);
-            const float f = to == -INFINITY || m == -INFINITY ? (m == to ? 1.0f : 0.0f) : fast_exp2((m - to) * cz);
-            m = to;
+            // by a power of two, not above it: nothing of P or O is rounded again (a second
+            // rounding of a BF16 pair's high part would be lost to the low one)
+            float f = 1.0f;
+            if (mn > m) {
+              const float up = m == -INFINITY ? 0.f : floorf((mn - m) * cz);
+              f = m == -INFINITY ? 0.f : fast_exp2(-up);
+              m = m == -INFINITY ? mn : m + up / cz;
+            }
             l *= f;
 #pragma unroll 1
             for (int e = 0; e < h; ++e) {   // the parts before, not yet in O
@@ -1182,7 +1214,14 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
 //      of eight, the dims 16 c .. and 64 + 16 c .. (16 each);
 //   O: of keys c, c + 4, c + 8, c + 12 the dims 16 (4 (g % 2) + g / 2) .. (16).
 // Each warp has its own running maximum, sum and output; they are joined at the
-// segment's end. Schedule, loads, parts and merge are as above.
+// segment's end. Schedule, parts and merge are as above.
+//
+// Bound by the integer pipe: widening a code takes 1.25 (K) and 2 (V) of its
+// instructions, 530 of some 1,000 issue slots a tile and scheduler. 16 tokens on
+// 16,384, 32/8 heads: 106 us, 5.2 TB/s, against 198 us through the tensor core's
+// path; one on 65,536, 24/2 heads: 17.5 against 26.3; 64 on 2,048, 32/8: 70
+// against 173. From 17 rows on every further 16 would widen all codes again.
+// Twelve warps of 152 registers: eight of 168 took 155 us for the first of these.
 constexpr int kFewRows = 16, kFewWarps = 12, kFewThreads = 32 * (kFewWarps + 4);   // (the loader's warpgroup last)
 constexpr int kFewGroup = 16, kFewGroups = kTileKeys / kFewGroup;   // keys a warp takes at once; such groups of a tile
 constexpr int kFewRing = 3;
@@ -1298,12 +1337,12 @@ __device__ __forceinline__ void few_role(const FullParams& p, FewBars* bars, con
         for (int e = 0; e < 16; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int ex = top >= 0x80u ? static_cast<int>(top >> 7) - 127 - 14 : -126 - 14;
+        const int ex = row_exponent(top);
         const float f0 = __int_as_float((127 - ex / 2) << 23), f1 = __int_as_float((127 - (ex - ex / 2)) << 23);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           w[e] = pack2<true>(__uint_as_float(w[e] << 16) * f0 * f1, __uint_as_float(w[e] & 0xffff0000u) * f0 * f1);
-        unit[i] = ldexpf(p.scale_log2, ex);
+        unit[i] = row_unit(p.scale_log2, ex);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -1680,7 +1719,9 @@ int check_full(const dsa_full_problem* p) {
 }
 
 // Costs of a unit, in quarters of a tile of 256 rows: a tile of up to 128 rows
-// takes the same loads and half the products; an item, its queries and output.
+// takes the same loads and half the products; an item, its queries and output
+// (8 / 20 / 40: 2,048 tokens on 2,048 48.5 / 45.4 / 45.2 us, 32 single tokens on
+// 300 .. 8,192 keys 94.4 / 93.8 / 96.4 us).
 constexpr int kCostRows = 4, kCostKeys = 3, kCostItem = 20;
 
 // Lays the items out over at most min(sms, kMaxCtas, tiles) blocks (fp: the
@@ -1846,7 +1887,7 @@ int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* 
   fp.q_dtype = p->q_dtype;
   fp.out_dtype = p->out_dtype;
   const float scale = p->softmax_scale > 0.0f ? p->softmax_scale : 1.0f / std::sqrt(static_cast<float>(p->head_dim));
-  fp.scale_log2 = scale * 1.4426950408889634f;
+  fp.scale_log2 = std::max(scale * 1.4426950408889634f, kLeastUnit);
   fp.softcap = p->softcap;
   fp.pg = pg;
   mp.partial = fp.partial;

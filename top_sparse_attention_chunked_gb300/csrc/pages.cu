@@ -28,7 +28,13 @@
 // count and the live blocks above it, both ascending, are paired), a commit.
 //
 // Copies: the bytes are read once and written once, in 32 KB pieces of one
-// block of one pool a thread block, eight 16-byte loads a thread in flight.
+// block of one pool a thread block, eight 16-byte loads a thread in flight:
+// 580 MB (290 read, 290 written) in 100 us, 5.8 TB/s of 6.8 measured.
+//
+// Without copies the time is launches and one block's walk: 16 x 32 entries of
+// 1,024 blocks 6.0 us, 256 x 256 of 8,192 9.5 us; 65,536 blocks 25 us (the walk
+// reads 1.3 MB through one SM; a plan by many blocks would need two launches
+// more, which costs what it gains below some 40,000 blocks).
 #include <algorithm>
 
 #include "dsa_common.cuh"
@@ -42,10 +48,14 @@ constexpr int kPgThreads = 256;
 constexpr int kPlanThreads = 1024;
 constexpr int kCopyUnroll = 8;
 // States that one block counts by itself, sums in shared memory: up to this many
-// table entries and blocks.
+// table entries and blocks (one block / many, of 1,024 blocks with 512 entries:
+// 5.6 / 6.8 us; 8,192 blocks with 4,096 entries 10.2 / 10.2, 8,192 entries 12.5 /
+// 10.0).
 constexpr int kSmallEntries = 4096, kSmallBlocks = 8192;
 // Times 32 blocks that a warp of a plan kernel looks at together: many keep loads
-// in flight, few keep the code short, which is what a small state's time goes on.
+// in flight, few keep the code short, which is what a small state's time goes on
+// (8 and 2 in a small state: 7.6 and 6.0 us; 65,536 blocks with 4 and 8, the loads
+// before the first store: 25.8 and 25.0, one at a time 43.8).
 constexpr int kWalkSmall = 2, kWalkLarge = 8;
 constexpr long long kPiece = kPgThreads * 16LL * kCopyUnroll;   // bytes of one copy task
 
