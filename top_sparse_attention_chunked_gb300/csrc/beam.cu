@@ -16,7 +16,7 @@
 // Within a row totals are ordered as the logits are, so that loses nothing.
 //
 // Sums: a thread's is sum 2^(x H + c) with H = log2(e) rounded to fp32 and c an
-// integer (the maximum's, negated): one paired multiply-add and one 2^ a
+// integer (a large value's, negated; it moves when a term would pass 2^30): one paired multiply-add and one 2^ a
 // value, and sums of different c join by exact powers of two. A slice's joins
 // as 64-bit fixed point (2^-36 of a term at the maximum). H's rounding scales
 // every exponent by 1 - 1.3e-8, which the merge undoes at the maximum; what is
@@ -27,10 +27,12 @@
 // bits (rows have different offsets: totals may lie closer together than fp32
 // tells apart) and ranks them by counting.
 //
-// What bounds it: large batches the scan's instructions (a bf16 value costs three
-// quarters of an issue slot a lane: widen, multiply-add, 2^, add, maximum), 32 x 8
-// beams of 128,000: 28 us, 2.3 TB/s, as fp32 36 us, 3.6 TB/s; small ones the merge's
-// chain of dependent steps: 4 beams of 50,000 9.5 us, of which the scan is 3.
+// What bounds it: large batches the scan's instructions (profiled: 12 a warp for
+// 32 bf16 values, the scheduler 54% busy), 32 x 8 beams of 128,000 27 us, 2.4 TB/s,
+// as fp32 35 us, 3.7 TB/s, of 6.8 measured; small ones the two launches and the
+// merge's chain of dependent steps, 4 beams of 32,000 8.7 us; many beams with a
+// large `select` the merge of up to 512 lists by one block, 64 beams of 200,000
+// with 64 selected 77 us.
 //
 // The order of a list depends on the order of execution; its keys are distinct
 // (value, then token), so what is picked out of it does not.
@@ -61,7 +63,7 @@ constexpr int kMergeList = 2 * kRound * kKeep;    // room for their candidates, 
 constexpr int kBounds = 4;                        // values of a warp that go into the merge's bound
 constexpr int kShare = kKeep / kMergeWarps;
 // Scan blocks per SM (70 KB of shared memory each for 16-bit logits). With two,
-// 32 x 8 beams of 128,000 take 30.3 us and not 28.9, in fp32 41.5 and not 36.9.
+// 32 x 8 beams of 128,000 took 30.3 us and not 28.9, in fp32 41.5 and not 36.9.
 constexpr int kResident = 3;
 
 struct SliceSum {
@@ -258,6 +260,36 @@ __device__ __forceinline__ float top_of(const uint4* v) {
   }
 }
 
+// A bit for each of a thread's values that is at least `lim`, and which value a
+// bit stands for. 16-bit values are compared two at a time, bits p and 16 + p for
+// the p-th pair, with the least value of their type that is not below `lim`.
+template <typename T>
+__device__ __forceinline__ uint32_t reached(const uint4* v, float lim) {
+  uint32_t hits = 0;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (sizeof(T) == 4) {
+        if (__uint_as_float(w[e]) >= lim) hits |= 1u << (4 * i + e);
+      } else {
+        uint32_t mask;
+        if constexpr (std::is_same<T, __half>::value)
+          mask = __hge2_mask(*reinterpret_cast<const __half2*>(w + e), __half2half2(__float2half_ru(lim)));
+        else
+          mask = __hge2_mask(*reinterpret_cast<const __nv_bfloat162*>(w + e), __bfloat162bfloat162(__float2bfloat16_ru(lim)));
+        hits |= mask & (0x00010001u << (4 * i + e));
+      }
+    }
+  }
+  return hits;
+}
+template <typename T>
+__device__ __forceinline__ int value_of(int bit) {
+  return sizeof(T) == 4 ? bit : 2 * (bit & 15) + (bit >> 4);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const BeamParams p) {
   constexpr int VE = 16 / sizeof(T);
@@ -297,7 +329,8 @@ __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const 
       return r;
     };
 
-    float m = -INFINITY, c = 0.f;        // this thread's maximum, and its offset
+    float m = -INFINITY;                 // this thread's maximum
+    float ref = -INFINITY, c = 0.f;      // the maximum that its sum is relative to, and that one's offset
     float2 sum = make_float2(0.f, 0.f);  // its sum
     float lim = key_value(1ull << 55);   // candidates are at least this (the smallest finite value to begin with)
     // a warp takes every eighth run of four vectors (64 bytes) of 256, so that a
@@ -312,14 +345,17 @@ __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const 
     };
     const auto tile = [&](int t, const uint4* cur) {
       const float top = top_of<T>(cur);
-      if (top > m) {
-        const float f = join_factor(m, top);   // (0 * 0 keeps a NaN)
+      m = fmaxf(m, top);
+      // the reference moves when a term would pass 2^30 (most threads' largest
+      // value rises a few times in a row)
+      if (top > ref && !(fabsf(ref) <= kFar && fabsf(top) <= kFar && fmaf(top, kLog2e, c) <= 30.f)) {
+        const float f = join_factor(ref, top);   // (0 * 0 keeps a NaN)
         sum.x *= f;
         sum.y *= f;
-        m = top;
-        c = offset_of(m);
+        ref = top;
+        c = offset_of(ref);
       }
-      if (fabsf(m) <= kFar) {
+      if (fabsf(ref) <= kFar) {
         const float2 h2 = make_float2(kLog2e, kLog2e), c2 = make_float2(c, c);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
@@ -338,7 +374,7 @@ __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const 
 #pragma unroll
           for (int e = 0; e < kPairs; ++e) {
             const float2 x = two_of<T>(w, e);
-            if (m > -INFINITY) sum = add2(sum, make_float2(exp_neg(x.x - m), exp_neg(x.y - m)));
+            if (ref > -INFINITY) sum = add2(sum, make_float2(exp_neg(x.x - ref), exp_neg(x.y - ref)));
             else if (x.x != x.x || x.y != x.y) sum.x = NAN;
           }
         }
@@ -357,22 +393,12 @@ __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const 
       }
       // append the places that reach it
       if (top >= lim) {
-        uint32_t hits = 0;
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-          const uint32_t w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
-#pragma unroll
-          for (int e = 0; e < kPairs; ++e) {
-            const float2 x = two_of<T>(w, e);
-            if (x.x >= lim) hits |= 1u << (i * VE + 2 * e);
-            if (x.y >= lim) hits |= 2u << (i * VE + 2 * e);
-          }
-        }
+        uint32_t hits = reached<T>(cur, lim);
         int at = atomicAdd(&s_count, __popc(hits));
         while (hits) {
-          const int bit = __ffs(hits) - 1;
+          const int bit = __ffs(hits) - 1, i = value_of<T>(bit);
           hits &= hits - 1;
-          s_list[at++] = (t * kTileVecs + (bit / VE) * kBmThreads + own_vec) * VE - mis + (bit % VE);
+          s_list[at++] = (t * kTileVecs + (i / VE) * kBmThreads + own_vec) * VE - mis + (i % VE);
         }
       }
     };
@@ -431,7 +457,7 @@ __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const 
     // (a thread's maximum may be +infinity, its sum is a NaN then)
     const bool bad = !(own < INFINITY);
     unsigned long long fixed =
-        bad ? 0ull : static_cast<unsigned long long>(own * join_factor(m, mm) * 0x1p36f);
+        bad ? 0ull : static_cast<unsigned long long>(own * join_factor(ref, mm) * 0x1p36f);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) fixed += __shfl_xor_sync(0xffffffffu, fixed, o);
     if (lane == 0) s_sum[wid] = fixed;
