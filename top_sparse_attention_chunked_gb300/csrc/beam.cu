@@ -16,9 +16,10 @@
 // Within a row totals are ordered as the logits are, so that loses nothing.
 //
 // Sums: a thread's is sum 2^(x H + c) with H = log2(e) rounded to fp32 and c an
-// integer (a large value's, negated; it moves when a term would pass 2^30): one paired multiply-add and one 2^ a
-// value, and sums of different c join by exact powers of two. A slice's joins
-// as 64-bit fixed point (2^-36 of a term at the maximum). H's rounding scales
+// integer (a large value's, negated; it moves when a term would pass 2^30): one
+// paired multiply-add and one 2^ a value, and sums of different c join by exact
+// powers of two. A slice's joins as 64-bit fixed point (2^-36 of a term at the
+// maximum). H's rounding scales
 // every exponent by 1 - 1.3e-8, which the merge undoes at the maximum; what is
 // left is 1.3e-8 of a term's distance from it.
 //
@@ -27,7 +28,7 @@
 // bits (rows have different offsets: totals may lie closer together than fp32
 // tells apart) and ranks them by counting.
 //
-// What bounds it: large batches the scan's instructions (profiled: 12 a warp for
+// What bounds it: large batches the scan's instructions (some 12 of a warp for
 // 32 bf16 values, the scheduler 54% busy), 32 x 8 beams of 128,000 27 us, 2.4 TB/s,
 // as fp32 35 us, 3.7 TB/s, of 6.8 measured; small ones the two launches and the
 // merge's chain of dependent steps, 4 beams of 32,000 8.7 us; many beams with a

@@ -1725,9 +1725,13 @@ int check_full(const dsa_full_problem* p) {
 constexpr int kCostRows = 4, kCostKeys = 3, kCostItem = 20;
 
 // Lays the items out over at most min(sms, kMaxCtas, tiles) blocks (fp: the
-// problem and the runs, mp: the items that are split) and returns their number;
-// *most gets that bound.
-int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp, int* most) {
+// problem and the runs, mp: the items that are split) and returns their number.
+// *bytes gets the workspace that holds two parts of as many blocks as any device
+// may use. (More SMs may lead to fewer blocks: cuts that fall into the same tile
+// are one.)
+constexpr size_t kPartialAt = 256 + ((kMaxCtas * 4 + 255) / 256) * 256;
+
+int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp, size_t* bytes) {
   fp->B = p->batch;
   fp->Hq = p->num_q_heads;
   fp->Hkv = p->num_kv_heads;
@@ -1752,8 +1756,9 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
     cost += kCostItem + static_cast<long long>(w.ntiles) * (w.nrows > kSlotRows ? kCostRows : kCostKeys);
     tiles += w.ntiles;
   }
-  const int want = static_cast<int>(std::min<long long>(imin(sms, kMaxCtas), std::max(tiles, 1LL)));
-  if (most) *most = want;
+  const int most = static_cast<int>(std::min<long long>(kMaxCtas, std::max(tiles, 1LL)));
+  const int want = imin(sms, most);
+  *bytes = kPartialAt + static_cast<size_t>(2) * most * fp->part_rows * (DSA_HEAD_DIM + 2) * 4;
   // run k begins where the costs reach k / want of their sum
   int blocks = 0;
   long long at = 0;
@@ -1788,17 +1793,6 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
   }
   mp->groups = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : kMaxGroups;   // four parts a thread at once
   return blocks;
-}
-
-constexpr size_t kPartialAt = 256 + ((kMaxCtas * 4 + 255) / 256) * 256;
-
-size_t full_bytes(const dsa_full_problem* p) {
-  FullParams fp{};
-  MergeParams mp{};
-  // (more SMs may lead to fewer blocks: cuts that fall into the same tile are one)
-  int most = 0;
-  schedule(p, kMaxCtas, &fp, &mp, &most);
-  return kPartialAt + static_cast<size_t>(2) * most * fp.part_rows * (DSA_HEAD_DIM + 2) * 4;
 }
 
 // Launches one of two kernels of a family (with and without MOD). Where warps
@@ -1858,12 +1852,14 @@ int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* 
     return report_error(DSA_ERR_MISALIGNED, "q, k, v and out must be 16-byte aligned");
   if (off(ks, 4) || off(vs, 4) || off(slopes, 4) || off(lse, 4))
     return report_error(DSA_ERR_MISALIGNED, "scales, slopes and lse must be 4-byte aligned");
-  if (int rc = check_call_workspace(ws, ws_bytes, dsa_full_attn_workspace_size(p))) return rc;
   int sms = 0;
-  if (int rc = current_device(&sms)) return rc;
+  const bool device = current_device(&sms) == DSA_OK;
   FullParams fp{};
-  MergeParams mp{};
-  const int blocks = schedule(p, sms, &fp, &mp, nullptr);
+  MergeParams mp;
+  size_t need = 0;
+  const int blocks = schedule(p, device ? sms : kMaxCtas, &fp, &mp, &need);
+  if (int rc = check_call_workspace(ws, ws_bytes, need)) return rc;
+  if (!device) return current_device(&sms);
   if (fp.seq[p->batch].q0 == 0) {
     const cudaError_t e = cudaMemsetAsync(ws, 0, 4, static_cast<cudaStream_t>(stream));   // the status word
     return e == cudaSuccess ? DSA_OK : report_errorf(DSA_ERR_CUDA, "status clear: %s", cudaGetErrorString(e));
@@ -1921,7 +1917,11 @@ using namespace dsa;
 
 extern "C" size_t dsa_full_attn_workspace_size(const dsa_full_problem* p) {
   if (check_full(p)) return 0;
-  return full_bytes(p);
+  FullParams fp{};
+  MergeParams mp;
+  size_t bytes = 0;
+  schedule(p, kMaxCtas, &fp, &mp, &bytes);
+  return bytes;
 }
 
 extern "C" int dsa_full_attn(const dsa_full_problem* p, const void* q, const void* k, const void* v,
