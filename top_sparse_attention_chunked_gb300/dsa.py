@@ -536,15 +536,32 @@ def _refuse(dev: int, t: torch.Tensor, name: str, dtype, shape):
     raise ValueError(f"{name} must be contiguous")
 
 
-def _here(dev: int, t: Optional[torch.Tensor], name: str, dtype=None, shape=None):
-    """_ptr of a tensor that must lie on device `dev`, the current one (whose
-    stream the call goes to)."""
-    if t is None:
-        return None
-    if (t.get_device() != dev or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype)
-            or (shape is not None and t.shape != shape)):
-        _refuse(dev, t, name, dtype, shape)
-    return t.data_ptr()
+def _here(dev: int, *tensors):
+    """The addresses of tensors that must lie on device `dev`, the current one
+    (whose stream the call goes to): (tensor or None, name, dtype or None, shape
+    or None) each. One loop: a call per tensor would be a tenth of a small
+    call's time on the host."""
+    ptrs = []
+    for t, name, dtype, shape in tensors:
+        if t is None:
+            ptrs.append(None)
+            continue
+        if (t.get_device() != dev or not t.is_contiguous() or (dtype is not None and t.dtype is not dtype)
+                or (shape is not None and t.shape != shape)):
+            _refuse(dev, t, name, dtype, shape)
+        ptrs.append(t.data_ptr())
+    return ptrs
+
+
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _current_device() -> int:
+    """torch.cuda.current_device() without its check that CUDA is initialised
+    (a tensor on a CUDA device is an argument of every call)."""
+    if _raw_device is not None and torch.cuda.is_initialized():
+        return _raw_device()
+    return torch.cuda.current_device()
 
 
 def _stream_here(dev: int, stream) -> int:
@@ -552,10 +569,6 @@ def _stream_here(dev: int, stream) -> int:
     if stream is None and _raw_stream is not None:
         return _raw_stream(dev)
     return _stream(stream)
-
-
-def _ws_here(dev: int, ws: torch.Tensor):
-    return _here(dev, ws, "workspace", torch.uint8), ws.numel()
 
 
 def make_full_attn_problem(q_len: Sequence[int], total_len: Sequence[int], num_q_heads: int,
@@ -597,10 +610,10 @@ def dsa_full_attn(p: DsaFullProblem, q, k, v, k_scale, v_scale, out, workspace, 
     """Attention of the packed new tokens q [N, Hq, 128] (N = sum of q_len, or
     more: rows behind are left alone) over all cached keys; with `pages`
     (make_pages) the caches are paged pools. lse [N, Hq] fp32 is optional."""
-    Hq, Hkv, lib, dev = p.num_q_heads, p.num_kv_heads, load_library(), torch.cuda.current_device()
-    wp, wn = _ws_here(dev, workspace)
+    Hq, Hkv, lib, dev = p.num_q_heads, p.num_kv_heads, load_library(), _current_device()
     kvdt = _TORCH_DT[p.kv_dtype]
-    lead = _cache_shapes(p, pages)
+    rows = _cache_shapes(p, pages) + (Hkv,)
+    cache, f32 = rows + (128,), torch.float32
     need = sum(p.q_len[:p.batch])
     if q.dim() != 3 or q.shape[1:] != (Hq, 128) or q.shape[0] < need:
         raise ValueError(f"q must be [N, {Hq}, 128] with N >= {need}, got {tuple(q.shape)}")
@@ -608,16 +621,14 @@ def dsa_full_attn(p: DsaFullProblem, q, k, v, k_scale, v_scale, out, workspace, 
         raise ValueError(f"out must be [N, {Hq}, 128] with N >= {need}, got {tuple(out.shape)}")
     if lse is not None and (lse.dim() != 2 or lse.shape[1] != Hq or lse.shape[0] < need):
         raise ValueError(f"lse must be [N, {Hq}] with N >= {need}, got {tuple(lse.shape)}")
-    args = [_here(dev, q, "q", _TORCH_DT[p.q_dtype]), _here(dev, k, "k", kvdt, lead + (Hkv, 128)),
-            _here(dev, v, "v", kvdt, lead + (Hkv, 128)),
-            _here(dev, k_scale, "k_scale", torch.float32, lead + (Hkv,)),
-            _here(dev, v_scale, "v_scale", torch.float32, lead + (Hkv,)),
-            _here(dev, slopes, "slopes", torch.float32, (Hq,)), _here(dev, out, "out", _TORCH_DT[p.out_dtype]),
-            _here(dev, lse, "lse", torch.float32), wp, wn, _stream_here(dev, stream)]
+    args = _here(dev, (q, "q", _TORCH_DT[p.q_dtype], None), (k, "k", kvdt, cache), (v, "v", kvdt, cache),
+                 (k_scale, "k_scale", f32, rows), (v_scale, "v_scale", f32, rows), (slopes, "slopes", f32, (Hq,)),
+                 (out, "out", _TORCH_DT[p.out_dtype], None), (lse, "lse", f32, None),
+                 (workspace, "workspace", torch.uint8, None), (pages and pages._table, "block_table", None, None))
+    args[9:] = workspace.numel(), _stream_here(dev, stream)
     if pages is None:
         _check(lib.dsa_full_attn(ctypes.byref(p), *args))
     else:
-        _here(dev, pages._table, "block_table")
         _check(lib.dsa_full_attn_paged(ctypes.byref(p), ctypes.byref(pages), *args))
 
 
@@ -662,21 +673,15 @@ def alloc_pages_workspace(st: DsaPageState, device="cuda") -> torch.Tensor:
     return torch.empty(dsa_pages_workspace_size(st), dtype=torch.uint8, device=device)
 
 
-def _page_args(dev: int, st: DsaPageState, pools, table_out, refs_out):
-    """Checked addresses of the new state (None: the old one's arrays) and the pools."""
-    table, refs = st._keep
-    _here(dev, table, "block_table")
-    _here(dev, refs, "refs")
-    n = 0
-    if pools is not None and len(pools._keep):
-        n = len(pools._keep)
-        if pools._blocks != st.num_blocks:
-            raise ValueError(f"the pools hold {pools._blocks} blocks, the state {st.num_blocks}")
-        if pools._dev != dev:
-            raise ValueError(f"the pools are on cuda:{pools._dev}, the current device is cuda:{dev}")
-    return (n, pools if n else None,
-            st.block_table if table_out is None else _here(dev, table_out, "table_out", torch.int32, table.shape),
-            st.refs if refs_out is None else _here(dev, refs_out, "refs_out", torch.int32, refs.shape))
+def _page_pools(dev: int, st: DsaPageState, pools):
+    """(number, array) of checked pools."""
+    if pools is None or not pools._keep:
+        return 0, None
+    if pools._blocks != st.num_blocks:
+        raise ValueError(f"the pools hold {pools._blocks} blocks, the state {st.num_blocks}")
+    if pools._dev != dev:
+        raise ValueError(f"the pools are on cuda:{pools._dev}, the current device is cuda:{dev}")
+    return len(pools._keep), pools
 
 
 def dsa_pages_update(st: DsaPageState, parent, keep_len, new_len, pools, workspace, table_out=None,
@@ -685,26 +690,33 @@ def dsa_pages_update(st: DsaPageState, parent, keep_len, new_len, pools, workspa
     becomes the first keep_len[r] tokens of old row parent[r] (-1: empty) and
     room for new_len[r]. Without table_out / refs_out the state is changed in
     place; pools from make_page_pools (None: no contents move)."""
-    lib, dev = load_library(), torch.cuda.current_device()
-    wp, wn = _ws_here(dev, workspace)
-    n, arr, tp, rp = _page_args(dev, st, pools, table_out, refs_out)
+    lib, dev = load_library(), _current_device()
+    n, arr = _page_pools(dev, st, pools)
+    table, refs = st._keep
     i32, one = torch.int32, (st.rows,)
-    _check(lib.dsa_pages_update(
-        ctypes.byref(st), _here(dev, parent, "parent", i32, one), _here(dev, keep_len, "keep_len", i32, one),
-        _here(dev, new_len, "new_len", i32, one), _here(dev, first_key, "first_key", i32, one), n, arr,
-        tp, rp, _here(dev, counts, "counts", i32, (2,)), wp, wn, _stream_here(dev, stream)))
+    a = _here(dev, (table, "block_table", None, None), (refs, "refs", None, None), (parent, "parent", i32, one),
+              (keep_len, "keep_len", i32, one), (new_len, "new_len", i32, one), (first_key, "first_key", i32, one),
+              (table if table_out is None else table_out, "table_out", i32, table.shape),
+              (refs if refs_out is None else refs_out, "refs_out", i32, refs.shape), (counts, "counts", i32, (2,)),
+              (workspace, "workspace", torch.uint8, None))
+    _check(lib.dsa_pages_update(ctypes.byref(st), a[2], a[3], a[4], a[5], n, arr, a[6], a[7], a[8], a[9],
+                                workspace.numel(), _stream_here(dev, stream)))
 
 
 def dsa_pages_compact(st: DsaPageState, pools, workspace, table_out=None, refs_out=None, remap=None,
                       counts=None, stream=None):
     """Move the live blocks to the front of the pools (in place without
     table_out / refs_out); remap [num_blocks] receives the new indices."""
-    lib, dev = load_library(), torch.cuda.current_device()
-    wp, wn = _ws_here(dev, workspace)
-    n, arr, tp, rp = _page_args(dev, st, pools, table_out, refs_out)
-    _check(lib.dsa_pages_compact(
-        ctypes.byref(st), n, arr, tp, rp, _here(dev, remap, "remap", torch.int32, (st.num_blocks,)),
-        _here(dev, counts, "counts", torch.int32, (2,)), wp, wn, _stream_here(dev, stream)))
+    lib, dev = load_library(), _current_device()
+    n, arr = _page_pools(dev, st, pools)
+    table, refs = st._keep
+    i32 = torch.int32
+    a = _here(dev, (table, "block_table", None, None), (refs, "refs", None, None),
+              (table if table_out is None else table_out, "table_out", i32, table.shape),
+              (refs if refs_out is None else refs_out, "refs_out", i32, refs.shape),
+              (remap, "remap", i32, refs.shape), (counts, "counts", i32, (2,)),
+              (workspace, "workspace", torch.uint8, None))
+    _check(lib.dsa_pages_compact(ctypes.byref(st), n, arr, *a[2:], workspace.numel(), _stream_here(dev, stream)))
 
 
 def make_beam_problem(batch: int, beams: int, vocab: int, select: int, logits_dtype="bf16",
@@ -729,8 +741,7 @@ def dsa_beam_select(p: DsaBeamProblem, logits, scores, out_scores, out_tokens, o
     """The `select` best continuations of each batch entry's beams: logits
     [batch * beams, vocab] whose rows may lie row_stride elements apart
     (p.row_stride), scores [batch * beams]; out_* [batch, select]."""
-    lib, dev = load_library(), torch.cuda.current_device()
-    wp, wn = _ws_here(dev, workspace)
+    lib, dev = load_library(), _current_device()
     n, out = p.batch * p.beams, (p.batch, p.select)
     stride = p.row_stride or p.vocab
     if logits.shape != (n, p.vocab) or logits.stride(-1) != 1 or (n > 1 and logits.stride(0) != stride):
@@ -742,12 +753,11 @@ def dsa_beam_select(p: DsaBeamProblem, logits, scores, out_scores, out_tokens, o
         raise ValueError(f"logits is on {logits.device}, the current device is cuda:{dev}")
     if finished is not None and finished.dtype == torch.bool:
         finished = finished.view(torch.uint8)
-    i32 = torch.int32
-    _check(lib.dsa_beam_select(
-        ctypes.byref(p), logits.data_ptr(), _here(dev, scores, "scores", torch.float32, (n,)),
-        _here(dev, finished, "finished", torch.uint8, (n,)), _here(dev, out_scores, "out_scores", torch.float32, out),
-        _here(dev, out_tokens, "out_tokens", i32, out), _here(dev, out_parents, "out_parents", i32, out),
-        wp, wn, _stream_here(dev, stream)))
+    i32, f32 = torch.int32, torch.float32
+    a = _here(dev, (scores, "scores", f32, (n,)), (finished, "finished", torch.uint8, (n,)),
+              (out_scores, "out_scores", f32, out), (out_tokens, "out_tokens", i32, out),
+              (out_parents, "out_parents", i32, out), (workspace, "workspace", torch.uint8, None))
+    _check(lib.dsa_beam_select(ctypes.byref(p), logits.data_ptr(), *a, workspace.numel(), _stream_here(dev, stream)))
 
 
 def dsa_read_device_status(workspace, stream=None) -> int:
