@@ -228,6 +228,13 @@ def test_first_key_and_rows_that_see_nothing(D, kv, block):
     run(D, c, window=70)
 
 
+@pytest.mark.parametrize("kv", ["fp16", "int8"])
+@pytest.mark.parametrize("q_len,total,first", [([2, 1], [5, 130], [5, 0]), ([2], [5], [5]), ([1, 3, 1], [7, 9, 300], [7, 9, 300]),
+                                               ([2, 1, 2], [5, 9000, 4], [5, 0, 4])])
+def test_leading_sequences_that_see_nothing(D, kv, q_len, total, first):
+    run(D, make(q_len, total, 8, 2, "bf16", kv, 128, first_key=first))
+
+
 def test_nothing_to_do(D):
     c = make([0, 0], [5, 0], 8, 2)
     out, lse, _ = call(D, c)

@@ -1759,22 +1759,34 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
   const int most = static_cast<int>(std::min<long long>(kMaxCtas, std::max(tiles, 1LL)));
   const int want = imin(sms, most);
   *bytes = kPartialAt + static_cast<size_t>(2) * most * fp->part_rows * (DSA_HEAD_DIM + 2) * 4;
-  // run k begins where the costs reach k / want of their sum
   int blocks = 0;
-  long long at = 0;
-  int k = 0;
-  for (int i = 0, b = 0; i < items; ++i) {
-    const Item w = make_item(*fp, i, b);
-    b = w.b;
-    const int unit = w.nrows > kSlotRows ? kCostRows : kCostKeys;
-    const long long end = at + kCostItem + static_cast<long long>(w.ntiles) * unit;
-    for (; k < want && cost * k < end * want; ++k) {
-      const long long x = cost * k / want - at - kCostItem;
-      const int tile = x > 0 ? static_cast<int>(x / unit) : 0;
-      if (blocks > 0 && fp->run[blocks - 1].item == i && fp->run[blocks - 1].tile >= tile) continue;
-      fp->run[blocks++] = FullParams::Run{i, tile, b, 0};
+  if (tiles <= want) {
+    // a tile each, for an item costs every block the same (16 tiles, 24/2 heads:
+    // 9.5 us, against 10.1 with the cuts below, of which some fall into an item's
+    // cost and leave other blocks two tiles; 4 x 600 keys 9.3 against 10.9)
+    for (int i = 0, b = 0, before = 0; i < items; ++i) {
+      const Item w = make_item(*fp, i, b);
+      b = w.b;
+      if (i == 0) fp->run[blocks++] = FullParams::Run{0, 0, b, 0};
+      for (int t = 0; t < w.ntiles; ++t)
+        if (before++ > 0) fp->run[blocks++] = FullParams::Run{i, t, b, 0};
     }
-    at = end;
+  } else {
+    // run k begins where the costs reach k / want of their sum
+    long long at = 0;
+    for (int i = 0, b = 0, k = 0; i < items; ++i) {
+      const Item w = make_item(*fp, i, b);
+      b = w.b;
+      const int unit = w.nrows > kSlotRows ? kCostRows : kCostKeys;
+      const long long end = at + kCostItem + static_cast<long long>(w.ntiles) * unit;
+      for (; k < want && cost * k < end * want; ++k) {
+        const long long x = cost * k / want - at - kCostItem;
+        const int tile = x > 0 ? static_cast<int>(x / unit) : 0;
+        if (blocks > 0 && fp->run[blocks - 1].item == i && fp->run[blocks - 1].tile >= tile) continue;
+        fp->run[blocks++] = FullParams::Run{i, tile, b, 0};
+      }
+      at = end;
+    }
   }
   fp->run[blocks] = FullParams::Run{items, 0, p->batch, 0};
   mp->splits = 0;
