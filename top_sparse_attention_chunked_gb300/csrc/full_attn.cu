@@ -34,7 +34,7 @@
 //   many tokens: the hand-over between tensor core and softmax. 4,096 on 16,384:
 //     523 us, 1,381 TFLOP/s (the two products alone would take 460); 4,096 on
 //     4,096: 110 us, 939 TFLOP/s (a block's share is 4 items);
-//   capped scores: the multiply-adds of the cap. 4,096 on 4,096: 148 us.
+//   capped scores: the multiply-adds of the cap. 4,096 on 4,096: 141 us.
 //
 // The running maximum m is raised (and O rescaled in tensor memory) only when
 // a row's weights grow by more than 2^8 over it, and by a whole power of two, to
@@ -742,8 +742,8 @@ __device__ __forceinline__ void odd_poly(float* z, float ys, const float (&k)[K]
 }
 
 // z (units of S, c log2-units each) -> cap * tanh(z c ln2 / cap) in log2 units.
-// Small arguments take odd polynomials fitted for the least maximum error (5e-8
-// of the range in fp32, up to 0.4 and up to 0.7); larger ones
+// Small arguments take odd polynomials fitted for the least maximum error (7e-8
+// of the range in fp32, up to 0.25, 0.4 and 0.7); larger ones
 // tanh y = 1 - 2 / (1 + e^2y), whose two special-function calls a value would
 // be the kernel's bound.
 template <int N>
@@ -753,7 +753,10 @@ __device__ __forceinline__ void cap_scores(float* z, float c, float softcap) {
 #pragma unroll
   for (int i = 0; i < N; ++i) far[i & 3] = fmaxf(far[i & 3], fabsf(z[i]));
   const float y = fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3])) * ys;
-  if (__all_sync(0xffffffffu, y <= 0.4f)) {
+  if (__all_sync(0xffffffffu, y <= 0.25f)) {
+    const float k[3] = {0.127622068f * cap, -0.333157003f * cap, 0.999998629f * cap};
+    odd_poly<N, 3>(z, ys, k);
+  } else if (__all_sync(0xffffffffu, y <= 0.4f)) {
     const float k[4] = {-0.0468257405f * cap, 0.13250567f * cap, -0.333297253f * cap, 0.999999583f * cap};
     odd_poly<N, 4>(z, ys, k);
   } else if (__all_sync(0xffffffffu, y <= 0.7f)) {

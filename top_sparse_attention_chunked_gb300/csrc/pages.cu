@@ -670,8 +670,8 @@ extern "C" int dsa_pages_compact(const dsa_page_state* st, int num_pools, const 
                         d, w, st->block_table, st->refs);
   }
   if (e == cudaSuccess)
-    e = launch_kernel("compact_plan_kernel", small ? compact_plan_kernel<kWalkSmall> : compact_plan_kernel<kWalkLarge>, dim3(1), dim3(kPlanThreads), 0, s, !small, d, w,
-                      small ? st->block_table : nullptr, st->refs, refs_out, remap, counts);
+    e = launch_kernel("compact_plan_kernel", small ? compact_plan_kernel<kWalkSmall> : compact_plan_kernel<kWalkLarge>,
+                      dim3(1), dim3(kPlanThreads), 0, s, !small, d, w, small ? st->block_table : nullptr, st->refs, refs_out, remap, counts);
   if (e == cudaSuccess)
     e = launch_kernel("compact_commit_kernel", compact_commit_kernel,
                       dim3(commit_grid(d, sms, list, (d.nb + 1) / 2)), dim3(kPgThreads), 0, s, true, d, w, list,
