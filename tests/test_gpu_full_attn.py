@@ -228,6 +228,14 @@ def test_first_key_and_rows_that_see_nothing(D, kv, block):
     run(D, c, window=70)
 
 
+@pytest.mark.parametrize("q,kv", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "fp16"), ("fp16", "int8")])
+@pytest.mark.parametrize("kw", [dict(softcap=200.0), dict(softcap=30.0), dict(softcap=12.0), dict(softcap=7.0), dict(softcap=1e4),
+                                dict(softcap=0.01), dict(softcap=40.0, scale=0.6), dict(softcap=0.05, scale=1e-4)])
+def test_caps_from_narrow_to_wide(D, q, kv, kw):
+    """Arguments of the cap in each range that it is formed in, and scales far below it."""
+    run(D, make([1, 150], [600, 300], 8, 2, q, kv, block=128, seed=12), out_dtype="fp32", **kw)
+
+
 @pytest.mark.parametrize("kv", ["fp16", "int8"])
 @pytest.mark.parametrize("q_len,total,first", [([2, 1], [5, 130], [5, 0]), ([2], [5], [5]), ([1, 3, 1], [7, 9, 300], [7, 9, 300]),
                                                ([2, 1, 2], [5, 9000, 4], [5, 0, 4])])

@@ -34,7 +34,7 @@
 //   many tokens: the hand-over between tensor core and softmax. 4,096 on 16,384:
 //     523 us, 1,381 TFLOP/s (the two products alone would take 460); 4,096 on
 //     4,096: 110 us, 939 TFLOP/s (a block's share is 4 items);
-//   capped scores: the multiply-adds of the cap. 4,096 on 4,096: 141 us.
+//   capped scores: the multiply-adds of the cap. 4,096 on 4,096: 137 us.
 //
 // The running maximum m is raised (and O rescaled in tensor memory) only when
 // a row's weights grow by more than 2^8 over it, and by a whole power of two, to
@@ -712,26 +712,34 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
 }
 
 // ---------------------------------------------------------------- softmax
-// y P(y^2) for N values, y = z * ys, P of K coefficients (highest first): K + 2
+// cap y P(y^2) for N values, y = z * ys, P of K coefficients (highest first): K + 2
 // cycles of the multiply-add pipe a value (paired arithmetic; eight pairs side
-// by side, a chain of K + 2 dependent operations each).
-template <int N, int K>
-__device__ __forceinline__ void odd_poly(float* z, float ys, const float (&k)[K]) {
+// by side, a chain of dependent operations each). FOLD: ys goes into the
+// coefficients, K + 1 cycles, where its powers are normal numbers.
+template <int N, bool FOLD, int K>
+__device__ __forceinline__ void odd_poly(float* z, float ys, float cap, const float (&k)[K]) {
   const auto both = [](float x) { return make_float2(x, x); };
   const float2 y2 = both(ys), zero = both(0.f);
+  float c[K], f = FOLD ? cap * ys : cap;
+#pragma unroll
+  for (int d = K - 1; d >= 0; --d) {
+    c[d] = k[d] * f;
+    if constexpr (FOLD) f *= ys * ys;
+  }
 #pragma unroll
   for (int i = 0; i < N; i += 16) {
     float2 y[8], t[8], a[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      y[e] = fma_f32x2(make_float2(z[i + 2 * e], z[i + 2 * e + 1]), y2, zero);
+      y[e] = make_float2(z[i + 2 * e], z[i + 2 * e + 1]);
+      if constexpr (!FOLD) y[e] = fma_f32x2(y[e], y2, zero);
       t[e] = fma_f32x2(y[e], y[e], zero);
-      a[e] = both(k[0]);
+      a[e] = both(c[0]);
     }
 #pragma unroll
     for (int d = 1; d < K; ++d)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] = fma_f32x2(a[e], t[e], both(k[d]));
+      for (int e = 0; e < 8; ++e) a[e] = fma_f32x2(a[e], t[e], both(c[d]));
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       a[e] = fma_f32x2(a[e], y[e], zero);
@@ -745,24 +753,25 @@ __device__ __forceinline__ void odd_poly(float* z, float ys, const float (&k)[K]
 // Small arguments take odd polynomials fitted for the least maximum error (7e-8
 // of the range in fp32, up to 0.25, 0.4 and 0.7); larger ones
 // tanh y = 1 - 2 / (1 + e^2y), whose two special-function calls a value would
-// be the kernel's bound.
-template <int N>
+// be the kernel's bound. FOLD (c is the problem's, not a row's): see odd_poly;
+// a scale below 2^-11 of the cap leaves the polynomials out (ys^11 > 2^-121).
+template <int N, bool FOLD>
 __device__ __forceinline__ void cap_scores(float* z, float c, float softcap) {
   const float cap = softcap * 1.4426950408889634f, ys = c / cap;
   float far[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < N; ++i) far[i & 3] = fmaxf(far[i & 3], fabsf(z[i]));
-  const float y = fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3])) * ys;
+  float y = fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3])) * ys;
+  if (FOLD && ys < 0x1p-11f) y = 1.0f;
   if (__all_sync(0xffffffffu, y <= 0.25f)) {
-    const float k[3] = {0.127622068f * cap, -0.333157003f * cap, 0.999998629f * cap};
-    odd_poly<N, 3>(z, ys, k);
+    const float k[3] = {0.127622068f, -0.333157003f, 0.999998629f};
+    odd_poly<N, FOLD>(z, ys, cap, k);
   } else if (__all_sync(0xffffffffu, y <= 0.4f)) {
-    const float k[4] = {-0.0468257405f * cap, 0.13250567f * cap, -0.333297253f * cap, 0.999999583f * cap};
-    odd_poly<N, 4>(z, ys, k);
+    const float k[4] = {-0.0468257405f, 0.13250567f, -0.333297253f, 0.999999583f};
+    odd_poly<N, FOLD>(z, ys, cap, k);
   } else if (__all_sync(0xffffffffu, y <= 0.7f)) {
-    const float k[6] = {-0.004874242f * cap, 0.0197352078f * cap, -0.0533838086f * cap,
-                        0.13325353f * cap,   -0.333328605f * cap, 0.99999994f * cap};
-    odd_poly<N, 6>(z, ys, k);
+    const float k[6] = {-0.004874242f, 0.0197352078f, -0.0533838086f, 0.13325353f, -0.333328605f, 0.99999994f};
+    odd_poly<N, FOLD>(z, ys, cap, k);
   } else {
     const float two = 2.0f * c / softcap;
 #pragma unroll
@@ -939,7 +948,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
             }
           }
           if constexpr (MOD) {
-            if (p.softcap > 0.f) cap_scores<kCols>(z, c, p.softcap);
+            if (p.softcap > 0.f) cap_scores<kCols, !kMayScale>(z, c, p.softcap);
             else
 #pragma unroll
               for (int i = 0; i < kCols; ++i) z[i] *= c;
