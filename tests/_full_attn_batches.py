@@ -1,0 +1,152 @@
+"""Batches for the full attention tests that give its thread blocks work of
+every kind, what the schedule makes of them, and the definition in 64 bits on
+the GPU (test_gpu_full_attn.py has it on the host, for small problems)."""
+import math
+import os
+import re
+
+import torch
+
+from tests.test_gpu_full_attn import make
+
+SMS = 152
+_SOURCE = os.path.join(os.path.dirname(__file__), "..", "top_sparse_attention_chunked_gb300", "csrc", "full_attn.cu")
+
+
+def constants():
+    """The schedule's constants, from the source."""
+    with open(_SOURCE) as f:
+        text = f.read()
+    names = ("kTileKeys", "kSlotRows", "kMaxCtas", "kCostRows", "kCostKeys", "kCostItem")
+    return {n: int(re.search(rf"\b{n} = (\d+)", text).group(1)) for n in names}
+
+
+def items(q_len, total_len, hq, hkv, first_key=None, window=0):
+    """(rows, key tiles) of every item, in order."""
+    k, out, grp = constants(), [], hq // hkv
+    for b, (n, t) in enumerate(zip(q_len, total_len)):
+        for _ in range(hkv):
+            for row0 in range(0, n * grp, 2 * k["kSlotRows"]):
+                rows = min(2 * k["kSlotRows"], n * grp - row0)
+                hi = t - n + (row0 + rows - 1) // grp + 1
+                lo = first_key[b] if first_key else 0
+                if window:
+                    lo = max(lo, t - n + row0 // grp - window + 1)
+                lo = min(lo, hi)
+                out.append((rows, -(-hi // k["kTileKeys"]) - lo // k["kTileKeys"] if lo < hi else 0))
+    return out
+
+
+def segments(*args, **kw):
+    """What each thread block works on: lists of (rows, tiles, whole item)."""
+    k, its = constants(), items(*args, **kw)
+    unit = lambda rows: k["kCostRows"] if rows > k["kSlotRows"] else k["kCostKeys"]
+    cost = sum(k["kCostItem"] + n * unit(rows) for rows, n in its)
+    tiles = sum(n for _, n in its)
+    want = min(SMS, k["kMaxCtas"], max(tiles, 1))
+    runs = []
+    if tiles <= want:
+        runs = [(i, t) for i, (_, n) in enumerate(its) for t in range(n)]
+        runs[:1] = [(0, 0)]
+    else:
+        at, c = 0, 0
+        for i, (rows, n) in enumerate(its):
+            end = at + k["kCostItem"] + n * unit(rows)
+            while c < want and cost * c < end * want:
+                t = max(0, cost * c // want - at - k["kCostItem"]) // unit(rows)
+                c += 1
+                if not runs or runs[-1] < (i, t):
+                    runs.append((i, t))
+            at = end
+    out = []
+    for (i, t), (end_i, end_t) in zip(runs, runs[1:] + [(len(its), 0)]):
+        block = []
+        while (i, t) < (end_i, end_t):
+            stop = end_t if i == end_i else its[i][1]
+            block.append((its[i][0], stop - t, t == 0 and stop == its[i][1]))
+            i, t = i + 1, 0
+        out.append(block)
+    return out
+
+
+def changes(blocks):
+    """How often a block goes from a segment of up to kSlotRows rows ("keys") to a wider one ("rows"), by
+    the first one's number of tiles, and the other way."""
+    slot = constants()["kSlotRows"]
+    to_rows, to_keys = [], []
+    for block in blocks:
+        for (r0, n0, _), (r1, n1, _) in zip(block, block[1:]):
+            if n0 and n1 and r0 <= slot < r1:
+                to_rows.append(n0)
+            if n0 and n1 and r1 <= slot < r0:
+                to_keys.append(n0)
+    return to_rows, to_keys
+
+
+# single tokens beside a chunk, and chunks whose last item of a head is a narrow one
+MIXED = {
+    "eight_tokens_and_1000": dict(q_len=[1] * 8 + [1000], total_len=[4000] * 8 + [1000], hq=24, hkv=2),
+    "twelve_tokens_and_2048": dict(q_len=[1] * 12 + [2048], total_len=[3000] * 12 + [2048], hq=24, hkv=2),
+    "two_chunks": dict(q_len=[700, 650], total_len=[2000, 1500], hq=16, hkv=4),
+}
+
+TYPES = [("bf16", "bf16"), ("bf16", "fp16"), ("fp16", "fp16"), ("bf16", "int8"), ("fp16", "int8")]
+
+
+def batch(name_or_case, q, kv, **kw):
+    case = dict(MIXED[name_or_case] if isinstance(name_or_case, str) else name_or_case)
+    case.update(kw)
+    return make(case.pop("q_len"), case.pop("total_len"), case.pop("hq"), case.pop("hkv"), q, kv, **case)
+
+
+def reference(c, window=0, softcap=0.0, slopes=None, scale=None):
+    """(out, lse, magnitude, logits' error) in 64 bits as test_gpu_full_attn.check takes them."""
+    scale = scale or 1 / math.sqrt(128)
+    grp, dev = c["hq"] // c["hkv"], "cuda"
+    n_all = sum(c["q_len"])
+    f64 = dict(dtype=torch.float64, device=dev)
+    out, mag = torch.zeros(n_all, c["hq"], 128, **f64), torch.zeros(n_all, c["hq"], 128, **f64)
+    lse, dz = torch.full((n_all, c["hq"]), -math.inf, **f64), torch.zeros(n_all, c["hq"], **f64)
+    # (an FP16 weight below its normal numbers: see the host's reference)
+    tiny = 2.0 ** -21 if c["kvdt"] == "fp16" else 0.0
+    n0 = 0
+    for b, (n, t) in enumerate(zip(c["q_len"], c["total_len"])):
+        f = c["first_key"][b]
+        for g in range(c["hkv"] if n and f < t else 0):
+            k, v = (c[x][b, f:t, g].to(dev).double() for x in ("k", "v"))
+            if c["k_scale"] is not None:
+                k = k * c["k_scale"][b, f:t, g].to(dev).double()[:, None]
+                v = v * c["v_scale"][b, f:t, g].to(dev).double()[:, None]
+            key = torch.arange(f, t, device=dev)
+            for i0 in range(0, n, 512):
+                i1 = min(n, i0 + 512)
+                heads = slice(g * grp, (g + 1) * grp)
+                q = c["q"][n0 + i0:n0 + i1, heads].to(dev).double()
+                pos = torch.arange(t - n + i0, t - n + i1, device=dev)[:, None, None]
+                z = q @ k.T * scale                                              # [tokens, G, keys]
+                err = (q.abs() @ k.abs().T) * (scale * 130 * 2.0 ** -24) + z.abs() * 2.0 ** -21
+                if softcap:
+                    z = softcap * torch.tanh(z / softcap)
+                    err += z.abs() * 2.0 ** -20      # relative: a cap much wider than the logits costs nothing
+                if slopes is not None:
+                    d = slopes.to(dev).double()[heads][None, :, None] * (key - pos)
+                    z = z + d
+                    err += d.abs() * 2.0 ** -22
+                seen = key <= pos
+                if window:
+                    seen &= key > pos - window
+                m = z.masked_fill(~seen, -math.inf).amax(-1, keepdim=True)
+                some = m > -math.inf
+                m = torch.where(some, m, torch.zeros_like(m))
+                zmax = z.abs().masked_fill(~seen, 0).amax(-1, keepdim=True)
+                err += (zmax + (z - m).abs()) * 2.0 ** -22
+                p = torch.where(seen, torch.exp(z - m), torch.zeros_like(z))
+                total = p.sum(-1, keepdim=True)
+                p = p / torch.where(some, total, torch.ones_like(total))
+                rows = slice(n0 + i0, n0 + i1)
+                out[rows, heads] = p @ v
+                mag[rows, heads] = (p + tiny * seen) @ v.abs()
+                lse[rows, heads] = (m + torch.log(total))[..., 0]
+                dz[rows, heads] = (p * err).sum(-1) + err.masked_fill(p <= 1e-9, 0).amax(-1)
+        n0 += n
+    return tuple(x.cpu().numpy() for x in (out, lse, mag, dz))

@@ -1,0 +1,32 @@
+"""dsa_full_attn on batches whose thread blocks work on several items of
+different kinds, against the definition in 64 bits."""
+import pytest
+import torch
+
+from tests._full_attn_batches import MIXED, batch, reference
+from tests.test_gpu_full_attn import D, call, check  # noqa: F401 (D is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def run(D, c, repeats=1, **kw):  # noqa: F811
+    """One checked call; `repeats` more must give the same bits."""
+    out, lse, st = call(D, c, **kw)
+    check(c, out, lse, reference(c, **{k: v for k, v in kw.items() if k in ("window", "softcap", "slopes", "scale")}),
+          kw.get("out_dtype") or c["qdt"])
+    ws, n = D.alloc_full_attn_workspace(st["p"]), sum(c["q_len"])
+    slopes = kw.get("slopes")
+    slopes = None if slopes is None else slopes.cuda()
+    for _ in range(repeats):
+        o, s = torch.empty_like(out), torch.empty_like(lse)
+        D.dsa_full_attn(st["p"], st["q"], st["dev"]["k"], st["dev"]["v"], st["dev"]["k_scale"], st["dev"]["v_scale"],
+                        o, ws, slopes=slopes, lse=s, pages=st["pages"])
+        assert torch.equal(o[:n], out[:n]) and torch.equal(s[:n], lse[:n])
+
+
+@pytest.mark.parametrize("kv", ["fp16", "int8"])
+@pytest.mark.parametrize("name", list(MIXED))
+def test_scaled_queries_of_narrow_and_wide_items(D, name, kv):  # noqa: F811
+    """BF16 queries that are scaled for products in FP16, where a block goes from an item of up to 128 rows
+    to a wider one: the second one's units must not touch the first one's statistics."""
+    run(D, batch(name, "bf16", kv, block=256, seed=21), repeats=40)

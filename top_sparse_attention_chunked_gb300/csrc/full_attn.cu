@@ -233,9 +233,10 @@ struct FullBars {
   uint64_t done;
   uint32_t tmem_base;
   int abort_flag, bad_page;
-  // a segment's beginning: the scales of slot 0's and slot 1's rows; its end in
-  // keys mode: slot 1's statistics, for slot 0
-  float m[kSlotRows], l[kSlotRows];
+  // log2 units per unit of S of the slots' rows (keys mode: slot 0's). Not in m
+  // and l: slot 1 goes on to the next segment before slot 0 has read those.
+  float unit[2][kSlotRows];
+  float m[kSlotRows], l[kSlotRows];             // a segment's end in keys mode: slot 1's statistics, for slot 0
 };
 
 template <bool INT8>
@@ -243,6 +244,7 @@ constexpr size_t full_smem() {
   return 2 * kTile16 + (INT8 ? kRing8 * kTile16 + kRaw * kTile8 + kScaleRing * 2 * kTileKeys * 4
                                     : kRing16 * kTile16) + sizeof(FullBars);
 }
+static_assert(full_smem<false>() <= 232448 && full_smem<true>() <= 232448, "shared memory of a block");
 
 // ------------------------------------------------------------------ PTX
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t* bar, int x, int y, int z) {
@@ -844,7 +846,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     if (slot == 0 || s.rows_mode) {
       // The warp's 32 rows, four at a time: eight lanes a row, lane k of them its
       // 16-byte chunks k and k + 8 (one in each block of 64 columns).
-      volatile float* row_c = slot == 0 ? bars->m : bars->l;
+      volatile float* row_c = bars->unit[slot];
       const int sub = lane & 7;
       uint8_t* dst = sQ + slot * kTile16;
 #pragma unroll 1
@@ -896,7 +898,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     if (slot == 1 && !s.rows_mode) {
       // slot 0 loads the shared rows; what it scaled them by
       if (!warp_wait(&bars->q_ready[0], nseg & 1, abort_flag)) break;
-      if (scaled) c = *const_cast<const volatile float*>(&bars->m[tid]);
+      if (scaled) c = *const_cast<const volatile float*>(&bars->unit[0][tid]);
     }
     ++nseg;
     tc_fence_before();
