@@ -90,6 +90,17 @@ MIXED = {
     "two_chunks": dict(q_len=[700, 650], total_len=[2000, 1500], hq=16, hkv=4),
 }
 
+# left-padded prompts: long runs of items without a key in one block, before and between items that see some
+NO_KEY = {
+    "prompt_of_4096": dict(q_len=[4096], total_len=[4096], hq=24, hkv=2, first_key=[4000]),
+    "prompt_of_2048_then_chunks": dict(q_len=[2048, 300, 1], total_len=[2048, 700, 500], hq=8, hkv=2, first_key=[1900, 0, 0]),
+    # slot 1 has eight rows of 136
+    "17_tokens_of_8_heads": dict(q_len=[17] * 30 + [17], total_len=[17] * 30 + [400], hq=16, hkv=2, first_key=[17] * 30 + [0]),
+    "5_tokens_then_chunk": dict(q_len=[5] * 40 + [200], total_len=[9] * 40 + [200], hq=16, hkv=2, first_key=[9] * 40 + [0]),
+    # more tiles than blocks: the items are laid out by cost
+    "padded_batch": dict(q_len=[1500] * 4, total_len=[1500] * 4, hq=16, hkv=4, first_key=[1200, 0, 1499, 700]),
+}
+
 TYPES = [("bf16", "bf16"), ("bf16", "fp16"), ("fp16", "fp16"), ("bf16", "int8"), ("fp16", "int8")]
 
 

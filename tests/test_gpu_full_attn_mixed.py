@@ -3,7 +3,7 @@ different kinds, against the definition in 64 bits."""
 import pytest
 import torch
 
-from tests._full_attn_batches import MIXED, batch, reference
+from tests._full_attn_batches import MIXED, NO_KEY, batch, reference
 from tests.test_gpu_full_attn import D, call, check  # noqa: F401 (D is a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -30,3 +30,12 @@ def test_scaled_queries_of_narrow_and_wide_items(D, name, kv):  # noqa: F811
     """BF16 queries that are scaled for products in FP16, where a block goes from an item of up to 128 rows
     to a wider one: the second one's units must not touch the first one's statistics."""
     run(D, batch(name, "bf16", kv, block=256, seed=21), repeats=40)
+
+
+@pytest.mark.parametrize("q,kv", [("bf16", "bf16"), ("bf16", "fp16"), ("bf16", "int8"), ("fp16", "int8")])
+@pytest.mark.parametrize("name", list(NO_KEY))
+def test_runs_of_items_without_a_key(D, name, q, kv):  # noqa: F811
+    """Many items of more than 128 rows that see nothing, in a row in one block: zeros, -infinity, and what
+    follows is right. (A hand-over with the tensor core that such items take part in has no bound on how far
+    one half of the rows runs ahead of the other.)"""
+    run(D, batch(NO_KEY[name], q, kv, block=128, seed=22), repeats=5, out_dtype="fp32" if q == "fp16" else None)

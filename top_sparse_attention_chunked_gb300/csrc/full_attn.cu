@@ -451,6 +451,7 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
   Walk walk(p);
   Segment s;
   while (walk.next(p, &s)) {
+    if (s.t0 == s.t1) continue;
     // cache rows of 32 tiles, one a lane, looked up together and 32 tiles ahead
     const auto look_up = [&](int t) {
       return t < s.t1 ? cache_row(p.pg, s.w.b, p.cap, (s.w.tile0 + t) * kTileKeys, &bad) : 0;
@@ -648,13 +649,13 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
   Segment s;
   bool ok = true;
   while (ok && walk.next(p, &s)) {
+    const int n = s.t1 - s.t0;
+    if (n == 0) continue;   // (the softmax warps write its zeros)
     // both slots are done with the previous segment, the queries are in place
     if (!mbar_wait_bounded(&bars->q_ready[0], nseg & 1, abort_flag)) break;
     if (!mbar_wait_bounded(&bars->q_ready[1], nseg & 1, abort_flag)) break;
     ++nseg;
     tc_fence_after();
-    const int n = s.t1 - s.t0;
-    if (n == 0) continue;
     if (s.rows_mode) {
       // round j: P V of tile j - 1 and S of tile j in slot 0, then in slot 1
       RingPos v = pos;
@@ -813,6 +814,19 @@ __device__ __forceinline__ int row_exponent(uint32_t top) {
 // would be a NaN (below fp32's normal numbers no such row's logits differ from 0).
 __device__ __forceinline__ float row_unit(float scale_log2, int ex) { return fmaxf(ldexpf(scale_log2, ex), kLeastUnit); }
 
+// The outputs of `n` rows of an item from row0 on, none of which sees a key. One
+// warp calls it.
+__device__ __forceinline__ void write_no_key(const FullParams& p, const Item& w, int row0, int n) {
+  const int lane = threadIdx.x & 31;
+  const int vecs = DSA_HEAD_DIM * (p.out_dtype == DSA_FP32 ? 4 : 2) / 16;   // a row's, 16 bytes each
+  for (int r = row0; r < row0 + n; ++r) {
+    const int tok = r / p.G;
+    const long long row = (static_cast<long long>(w.q0) + tok) * p.Hq + w.g * p.G + (r - tok * p.G);
+    if (lane < vecs) static_cast<uint4*>(p.out)[row * vecs + lane] = make_uint4(0, 0, 0, 0);
+    if (lane == 0 && p.lse) p.lse[row] = -INFINITY;
+  }
+}
+
 // One slot's four warps, one row a thread. MOD: the scores are capped or get a
 // bias.
 //
@@ -835,6 +849,13 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
   Segment s;
   while (walk.next(p, &s)) {
     const SlotWork x = slot_work(s, slot);
+    if (s.t0 == s.t1) {
+      // No row sees a key. Such an item takes no part in the hand-over with the
+      // tensor core: a slot that has nothing to wait for there would run ahead
+      // of the other and of the barriers' phases.
+      if (slot == 0 || s.rows_mode) write_no_key(p, s.w, x.row0 + warp_row, imin(32, x.nrows - warp_row));
+      continue;
+    }
     const int r = x.row0 + tid;
     const bool valid = tid < x.nrows;
     const bool warp_valid = (tid & ~31) < x.nrows;
@@ -1046,7 +1067,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     if (!ok) break;
     tile_seq += s.t1 - s.t0;
     const float m_log2 = m == -INFINITY ? -INFINITY : m * cz;
-    if (x.n > 0) {
+    if (x.n > 0) {   // (slot 1 has no tile of a segment of one in keys mode)
       if (!warp_wait(&bars->o_full[slot], no & 1, abort_flag)) break;
       ++no;
       tc_fence_after();
@@ -1091,29 +1112,24 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
 #pragma unroll 1
     for (int i = 0; i < DSA_HEAD_DIM; i += 32) {
       float o[32];
-      if (x.n > 0) {
-        tmem_ld32(tO + i, o);
-        if (other) {
-          float b[32];
-          tmem_ld32(tO + 128 + i, b);
-          tmem_ld_wait();
+      tmem_ld32(tO + i, o);
+      if (other) {
+        float b[32];
+        tmem_ld32(tO + 128 + i, b);
+        tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(o[e]), "+f"(b[e]));
+        for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(o[e]), "+f"(b[e]));
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = f0 * o[e] + f1 * b[e];
-        } else {
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(o[e]));
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= f0;
-        }
-        // a row without a key: whatever the products hold, its output is 0
-        if (s.whole && !(lj > 0.f)) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
-        }
+        for (int e = 0; e < 32; ++e) o[e] = f0 * o[e] + f1 * b[e];
       } else {
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(o[e]));
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] *= f0;
+      }
+      // a row without a key: whatever the products hold, its output is 0
+      if (s.whole && !(lj > 0.f)) {
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0.f;
       }
