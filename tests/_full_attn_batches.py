@@ -101,7 +101,34 @@ NO_KEY = {
     "padded_batch": dict(q_len=[1500] * 4, total_len=[1500] * 4, hq=16, hkv=4, first_key=[1200, 0, 1499, 700]),
 }
 
+# several tiles a segment and several segments a block, items of up to 128 rows, wider ones, and both in turn
+LOOPS = {
+    "single_tokens": dict(q_len=[1] * 6, total_len=[9000, 12001, 7777, 128, 10240, 9985], hq=8, hkv=4),
+    "eight_tokens": dict(q_len=[8, 7, 8], total_len=[13000, 12800, 12929], hq=24, hkv=2),
+    "chunk_of_300": dict(q_len=[300], total_len=[6000], hq=24, hkv=2),
+    "unequal_chunks": dict(q_len=[129, 1, 64, 300, 2, 0, 520], total_len=[3000, 8000, 1000, 2500, 5001, 9, 2049], hq=12, hkv=4),
+    "chunk_of_2000": dict(q_len=[2000], total_len=[2000], hq=16, hkv=2),
+    "many_short": dict(q_len=[(1, 30, 50, 5, 64)[i % 5] for i in range(48)], total_len=[300 + 31 * i for i in range(48)], hq=16,
+                       hkv=4),
+}
+
 TYPES = [("bf16", "bf16"), ("bf16", "fp16"), ("fp16", "fp16"), ("bf16", "int8"), ("fp16", "int8")]
+
+
+def grow(c, top):
+    """Keys whose logits grow along the cache, to about `top`: the running maximum is raised all along."""
+    ramp = torch.linspace(0, 1, c["cap"])[None, :, None]
+    seen = torch.stack([(torch.arange(c["cap"]) < t) for t in c["total_len"]])[..., None]
+    per_unit = 128 * 1.2 / math.sqrt(128)        # a logit, of keys of 1 and queries of mean 1.2
+    if c["k_scale"] is not None:
+        c["k"] = torch.where(c["k"] == 127, c["k"], c["k"].abs().clamp(1, 90))
+        scale = (1e-4 + ramp * top / per_unit / 45).expand(c["k_scale"].shape)
+        c["k_scale"] = torch.where(seen, scale, c["k_scale"]).contiguous()
+    else:
+        k = torch.sign(c["k"].float()) * 0.02 + (ramp * top / per_unit)[..., None]
+        c["k"] = torch.where(seen[..., None], k, c["k"].float()).to(c["k"].dtype)
+    c["q"] = c["q"].abs()
+    return c
 
 
 def batch(name_or_case, q, kv, **kw):

@@ -19,3 +19,23 @@ def test_padded_batches_have_runs_of_items_without_a_key(name):
     runs = [sum(n == 0 and (rows > slot or "5_tokens" in name) for rows, n, _ in b) for b in blocks]
     assert max(runs) >= (2 if name == "padded_batch" else 25)
     assert any(n for b in blocks for _, n, _ in b)
+
+
+def test_loop_batches_cover_the_main_loop():
+    """Segments of several tiles, odd and even, in items of up to 128 rows and in wider ones; blocks of
+    several segments; changes between the two kinds, after odd and even numbers of tiles; parts and whole
+    items."""
+    slot = F.constants()["kSlotRows"]
+    blocks = {name: F.segments(**c) for name, c in F.LOOPS.items()}
+    for name, b in blocks.items():
+        assert sum(n for x in b for _, n, _ in x) >= 3 * F.SMS, name
+        assert sum(n >= 3 for x in b for _, n, _ in x) >= F.SMS // 2, name
+    segs = [s for b in blocks.values() for x in b for s in x]
+    for narrow in (True, False):
+        here = [(n, whole) for rows, n, whole in segs if (rows <= slot) == narrow]
+        assert {n % 2 for n, _ in here if n >= 3} == {0, 1}
+        assert {whole for n, whole in here if n >= 3} == {True, False}
+    to_rows = [n for b in blocks.values() for n in F.changes(b)[0]]
+    to_keys = [n for b in blocks.values() for n in F.changes(b)[1]]
+    assert {n % 2 for n in to_rows} == {n % 2 for n in to_keys} == {0, 1}
+    assert any(len(x) >= 3 for x in blocks["many_short"])

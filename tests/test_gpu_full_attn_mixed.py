@@ -3,7 +3,7 @@ different kinds, against the definition in 64 bits."""
 import pytest
 import torch
 
-from tests._full_attn_batches import MIXED, NO_KEY, batch, reference
+from tests._full_attn_batches import LOOPS, MIXED, NO_KEY, TYPES, batch, grow, reference
 from tests.test_gpu_full_attn import D, call, check  # noqa: F401 (D is a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -39,3 +39,26 @@ def test_runs_of_items_without_a_key(D, name, q, kv):  # noqa: F811
     follows is right. (A hand-over with the tensor core that such items take part in has no bound on how far
     one half of the rows runs ahead of the other.)"""
     run(D, batch(NO_KEY[name], q, kv, block=128, seed=22), repeats=5, out_dtype="fp32" if q == "fp16" else None)
+
+
+@pytest.mark.parametrize("q,kv", TYPES)
+@pytest.mark.parametrize("name", list(LOOPS))
+def test_several_tiles_and_segments_a_block(D, name, q, kv):  # noqa: F811
+    """The main loop in earnest: the rings go round, slots are joined, blocks change items."""
+    run(D, batch(LOOPS[name], q, kv, block=128, seed=23), repeats=3)
+
+
+@pytest.mark.parametrize("q,kv", TYPES)
+@pytest.mark.parametrize("name", list(LOOPS))
+def test_window_cap_and_bias_over_several_tiles(D, name, q, kv):  # noqa: F811
+    c = batch(LOOPS[name], q, kv, seed=24, first_key=[min(100, t) for t in LOOPS[name]["total_len"]])
+    slopes = torch.tensor([2.0 ** (-4 - 0.25 * h) for h in range(c["hq"])])
+    run(D, c, window=2500, softcap=20.0, slopes=slopes)
+
+
+@pytest.mark.parametrize("q,kv", TYPES)
+@pytest.mark.parametrize("name", list(LOOPS))
+@pytest.mark.parametrize("top", [30.0, 400.0])
+def test_logits_that_grow_over_several_tiles(D, name, q, kv, top):  # noqa: F811
+    """O is rescaled within segments, at every tile or every few."""
+    run(D, grow(batch(LOOPS[name], q, kv, seed=25), top), out_dtype="fp32")
