@@ -62,3 +62,40 @@ def test_window_cap_and_bias_over_several_tiles(D, name, q, kv):  # noqa: F811
 def test_logits_that_grow_over_several_tiles(D, name, q, kv, top):  # noqa: F811
     """O is rescaled within segments, at every tile or every few."""
     run(D, grow(batch(LOOPS[name], q, kv, seed=25), top), out_dtype="fp32")
+
+
+CAPPED = ([40], [150, 3])
+
+
+@pytest.mark.parametrize("q,kv", TYPES)
+@pytest.mark.parametrize("kw", [dict(softcap=1e3), dict(softcap=1e4), dict(softcap=1e6), dict(softcap=3e38),
+                                dict(softcap=1e4, scale=8.0), dict(softcap=300.0, scale=2.0), dict(softcap=30.0)])
+def test_wide_caps_keep_the_logits_precision(D, q, kv, kw):  # noqa: F811
+    """A cap far above the logits leaves them as they are, to a few roundings of the logit (not of the cap)."""
+    for q_len in CAPPED:
+        c = batch(dict(q_len=q_len, total_len=[700 + 100 * n for n in q_len], hq=12, hkv=2), q, kv, block=128, seed=26)
+        run(D, c, out_dtype="fp32", **kw)
+
+
+@pytest.mark.parametrize("q,kv", TYPES)
+def test_wide_caps_beside_masked_and_large_keys(D, q, kv):  # noqa: F811
+    """What masked keys hold, or another row's large logits, do not cost a row's precision."""
+    c = batch(dict(q_len=[40, 3, 200], total_len=[450, 300, 400], hq=12, hkv=2, first_key=[70, 5, 3]), q, kv, seed=27)
+    if kv != "int8":
+        for b, f in enumerate(c["first_key"]):
+            c["k"][b, :f] = 3e4
+    c["q"][::3] *= 300
+    run(D, c, out_dtype="fp32", softcap=1e4)
+    run(D, c, out_dtype="fp32", softcap=1e6)
+
+
+@pytest.mark.parametrize("q,kv", TYPES)
+@pytest.mark.parametrize("softcap,q_mul", [(1e-4, 2.0 ** -13), (1e-4, 1.0), (1e-5, 2.0 ** -21), (1e-5, 2.0 ** -20), (1e-5, 2.0 ** -18),
+                                           (1e-9, 2.0 ** -34), (1e-9, 2.0 ** -33), (1e-30, 1.0), (1e-42, 1.0)])
+def test_narrow_caps(D, q, kv, softcap, q_mul):  # noqa: F811
+    """Caps far below the unit of the logits, arguments in each range: no overflow on the way."""
+    for q_len in CAPPED:
+        c = batch(dict(q_len=q_len, total_len=[700 + 100 * n for n in q_len], hq=12, hkv=2), q, kv, seed=28)
+        c["q"] = (c["q"].float() * q_mul).to(c["q"].dtype)
+        c["q"][:, 1] = 0
+        run(D, c, out_dtype="fp32", softcap=softcap)

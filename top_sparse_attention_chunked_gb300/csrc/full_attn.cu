@@ -718,9 +718,10 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
 // cap y P(y^2) for N values, y = z * ys, P of K coefficients (highest first): K + 2
 // cycles of the multiply-add pipe a value (paired arithmetic; eight pairs side
 // by side, a chain of dependent operations each). FOLD: ys goes into the
-// coefficients, K + 1 cycles, where its powers are normal numbers.
+// coefficients, K + 1 cycles; its powers are normal numbers.
 template <int N, bool FOLD, int K>
 __device__ __forceinline__ void odd_poly(float* z, float ys, float cap, const float (&k)[K]) {
+  constexpr int kPairs = N < 16 ? N / 2 : 8;
   const auto both = [](float x) { return make_float2(x, x); };
   const float2 y2 = both(ys), zero = both(0.f);
   float c[K], f = FOLD ? cap * ys : cap;
@@ -730,10 +731,10 @@ __device__ __forceinline__ void odd_poly(float* z, float ys, float cap, const fl
     if constexpr (FOLD) f *= ys * ys;
   }
 #pragma unroll
-  for (int i = 0; i < N; i += 16) {
-    float2 y[8], t[8], a[8];
+  for (int i = 0; i < N; i += 2 * kPairs) {
+    float2 y[kPairs], t[kPairs], a[kPairs];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < kPairs; ++e) {
       y[e] = make_float2(z[i + 2 * e], z[i + 2 * e + 1]);
       if constexpr (!FOLD) y[e] = fma_f32x2(y[e], y2, zero);
       t[e] = fma_f32x2(y[e], y[e], zero);
@@ -742,9 +743,9 @@ __device__ __forceinline__ void odd_poly(float* z, float ys, float cap, const fl
 #pragma unroll
     for (int d = 1; d < K; ++d)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] = fma_f32x2(a[e], t[e], both(c[d]));
+      for (int e = 0; e < kPairs; ++e) a[e] = fma_f32x2(a[e], t[e], both(c[d]));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < kPairs; ++e) {
       a[e] = fma_f32x2(a[e], y[e], zero);
       z[i + 2 * e] = a[e].x;
       z[i + 2 * e + 1] = a[e].y;
@@ -752,33 +753,47 @@ __device__ __forceinline__ void odd_poly(float* z, float ys, float cap, const fl
   }
 }
 
-// z (units of S, c log2-units each) -> cap * tanh(z c ln2 / cap) in log2 units.
-// Small arguments take odd polynomials fitted for the least maximum error (7e-8
-// of the range in fp32, up to 0.25, 0.4 and 0.7); larger ones
-// tanh y = 1 - 2 / (1 + e^2y), whose two special-function calls a value would
-// be the kernel's bound. FOLD (c is the problem's, not a row's): see odd_poly;
-// a scale below 2^-11 of the cap leaves the polynomials out (ys^11 > 2^-121).
+// z (units of S, c log2-units each) -> cap * tanh(z c ln2 / cap) in log2 units, to
+// a relative error of 7e-7 of the result, however far the cap lies above it (an
+// error of some part of the cap would be one of the logit of a wide cap).
+// Arguments y of up to 0.25, 0.4 and 0.7 take odd polynomials, fitted to tanh y / y
+// for the least relative error (4e-7, 1e-7, 1e-8; the first is a multiply-add a
+// value shorter). Where a part has larger ones, those beyond 0.4 take
+// tanh y = 1 - 2 / (1 + e^2y), whose error, 2.5e-7, is one of the cap, and whose two
+// special-function calls a value would be the kernel's bound.
+// FOLD (c is the problem's, not a row's): see odd_poly; the eleventh power of
+// c / cap times cap has to be a normal number, else z is scaled first. N < 32: a
+// shorter choice (the code of a few values, not their time, is what counts).
 template <int N, bool FOLD>
 __device__ __forceinline__ void cap_scores(float* z, float c, float softcap) {
-  const float cap = softcap * 1.4426950408889634f, ys = c / cap;
+  const float cap = softcap * 1.4426950408889634f;
+  float ys = fminf(c / cap, 1e38f);
+  if (FOLD && !(ys >= 0x1p-11f && ys <= 0x1p11f && c >= 0x1p-16f && c <= 0x1p16f)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] *= ys;
+    ys = 1.0f;
+  }
   float far[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < N; ++i) far[i & 3] = fmaxf(far[i & 3], fabsf(z[i]));
-  float y = fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3])) * ys;
-  if (FOLD && ys < 0x1p-11f) y = 1.0f;
-  if (__all_sync(0xffffffffu, y <= 0.25f)) {
-    const float k[3] = {0.127622068f, -0.333157003f, 0.999998629f};
+  const float y = fmaxf(fmaxf(far[0], far[1]), fmaxf(far[2], far[3])) * ys;
+  const float k4[4] = {-0.0475536026f, 0.132709771f, -0.333313614f, 0.999999881f};
+  if (N >= 32 && __all_sync(0xffffffffu, y <= 0.25f)) {
+    const float k[3] = {0.128416136f, -0.333219081f, 0.999999583f};
     odd_poly<N, FOLD>(z, ys, cap, k);
   } else if (__all_sync(0xffffffffu, y <= 0.4f)) {
-    const float k[4] = {-0.0468257405f, 0.13250567f, -0.333297253f, 0.999999583f};
-    odd_poly<N, FOLD>(z, ys, cap, k);
-  } else if (__all_sync(0xffffffffu, y <= 0.7f)) {
-    const float k[6] = {-0.004874242f, 0.0197352078f, -0.0533838086f, 0.13325353f, -0.333328605f, 0.99999994f};
+    odd_poly<N, FOLD>(z, ys, cap, k4);
+  } else if (N >= 32 && __all_sync(0xffffffffu, y <= 0.7f)) {
+    const float k[6] = {-0.0050883363f, 0.0200244579f, -0.0535260104f, 0.133284152f, -0.333331317f, 1.0f};
     odd_poly<N, FOLD>(z, ys, cap, k);
   } else {
-    const float two = 2.0f * c / softcap;
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] = fmaf(-2.0f * cap, fast_rcp(1.0f + fast_exp2(z[i] * two)), cap);
+    for (int i = 0; i < N; ++i) {
+      const float x = z[i] * ys, t = x * x;
+      const float low = fmaf(fmaf(fmaf(k4[0], t, k4[1]), t, k4[2]), t, k4[3]) * cap * x;
+      const float high = fmaf(-2.0f * cap, fast_rcp(1.0f + fast_exp2(x * 2.8853900817779268f)), cap);
+      z[i] = fabsf(x) <= 0.4f ? low : high;
+    }
   }
 }
 
@@ -1926,7 +1941,8 @@ int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* 
   fp.out_dtype = p->out_dtype;
   const float scale = p->softmax_scale > 0.0f ? p->softmax_scale : 1.0f / std::sqrt(static_cast<float>(p->head_dim));
   fp.scale_log2 = std::max(scale * 1.4426950408889634f, kLeastUnit);
-  fp.softcap = p->softcap;
+  // (beyond, the cap leaves every finite logit of sense as it is; cap * log2 e stays finite)
+  fp.softcap = std::min(p->softcap, 1e30f);
   fp.pg = pg;
   mp.partial = fp.partial;
   mp.out = out;
