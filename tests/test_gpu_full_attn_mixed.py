@@ -64,7 +64,7 @@ def test_logits_that_grow_over_several_tiles(D, name, q, kv, top):  # noqa: F811
     run(D, grow(batch(LOOPS[name], q, kv, seed=25), top), out_dtype="fp32")
 
 
-CAPPED = ([40], [150, 3])
+CAPPED = ([1, 0, 2], [40], [150, 3])
 
 
 @pytest.mark.parametrize("q,kv", TYPES)

@@ -1445,14 +1445,13 @@ __device__ __forceinline__ void few_role(const FullParams& p, FewBars* bars, con
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            z[n][e] *= unit[e >> 1];
-            if (p.softcap > 0.f) {
-              const float two = 2.0f / p.softcap, cap = p.softcap * 1.4426950408889634f;
-              z[n][e] = fmaf(-2.0f * cap, fast_rcp(1.0f + fast_exp2(z[n][e] * two)), cap);
-            }
+          for (int e = 0; e < 4; ++e) z[n][e] *= unit[e >> 1];
+        if (p.softcap > 0.f) cap_scores<8, false>(&z[0][0], 1.0f, p.softcap);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
             z[n][e] = fmaf(slope[e >> 1], static_cast<float>(key0 + first + 8 * n + 4 * (e & 1) + c - at[e >> 1]), z[n][e]);
-          }
       }
       if (key0 + kTileKeys - 1 > pos0 || key0 < lo1) {
 #pragma unroll
