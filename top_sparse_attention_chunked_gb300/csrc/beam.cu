@@ -18,8 +18,10 @@
 // Sums: a thread's is sum 2^(x H + c) with H = log2(e) rounded to fp32 and c an
 // integer (a large value's, negated; it moves when a term would pass 2^30): one
 // paired multiply-add and one 2^ a value, and sums of different c join by exact
-// powers of two. A slice's joins as 64-bit fixed point (2^-36 of a term at the
-// maximum). H's rounding scales
+// powers of two. A tile's 16 or 32 values are added in fp32, the tiles' sums with
+// what each addition rounds off kept beside (a thread may have thousands of terms,
+// and of equal ones every addition rounds the same way). A slice's joins as 64-bit
+// fixed point (2^-36 of a term at the maximum). H's rounding scales
 // every exponent by 1 - 1.3e-8, which the merge undoes at the maximum; what is
 // left is 1.3e-8 of a term's distance from it.
 //
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const 
 
     float m = -INFINITY;                 // this thread's maximum
     float ref = -INFINITY, c = 0.f;      // the maximum that its sum is relative to, and that one's offset
-    float2 sum = make_float2(0.f, 0.f);  // its sum
+    float sum_hi = 0.f, sum_lo = 0.f;    // its sum, and what rounding left out of it
     float lim = key_value(1ull << 55);   // candidates are at least this (the smallest finite value to begin with)
     // a warp takes every eighth run of four vectors (64 bytes) of 256, so that a
     // tile that the row fills only in part still gives every warp its share and
@@ -351,11 +353,12 @@ __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const 
       // value rises a few times in a row)
       if (top > ref && !(fabsf(ref) <= kFar && fabsf(top) <= kFar && fmaf(top, kLog2e, c) <= 30.f)) {
         const float f = join_factor(ref, top);   // (0 * 0 keeps a NaN)
-        sum.x *= f;
-        sum.y *= f;
+        sum_hi *= f;
+        sum_lo *= f;
         ref = top;
         c = offset_of(ref);
       }
+      float2 sum = make_float2(0.f, 0.f);   // this tile's: 16 additions at the most one after another
       if (fabsf(ref) <= kFar) {
         const float2 h2 = make_float2(kLog2e, kLog2e), c2 = make_float2(c, c);
 #pragma unroll
@@ -380,6 +383,9 @@ __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const 
           }
         }
       }
+      const float part = sum.x + sum.y, next = sum_hi + part, got = next - sum_hi;
+      sum_lo += (sum_hi - (next - got)) + (part - got);   // (an infinite sum leaves a NaN)
+      sum_hi = next;
       // the bound so far; an older one of another warp is a bound as well, so
       // only the first tile's has to be waited for
       const int done = t - t0;
@@ -454,7 +460,7 @@ __global__ void __launch_bounds__(kBmThreads, kResident) beam_scan_kernel(const 
     mm = s_max[0];
 #pragma unroll
     for (int i = 1; i < kBmWarps; ++i) mm = fmaxf(mm, s_max[i]);
-    const float own = sum.x + sum.y;     // 0 (or a NaN) where nothing but -infinity was seen
+    const float own = sum_hi + sum_lo;   // 0 (or a NaN) where nothing but -infinity was seen
     // (a thread's maximum may be +infinity, its sum is a NaN then)
     const bool bad = !(own < INFINITY);
     unsigned long long fixed =
