@@ -664,8 +664,9 @@ int dsa_pages_compact(const dsa_page_state* st, int num_pools, const dsa_page_po
  * which may be `scores` itself where select == beams.
  *
  * Sums are taken in fp32 per thread and joined in 64 bits; totals are formed
- * and compared in 64 bits. Two beams' totals that differ by less than the sums'
- * error (about 1e-7, at most 1e-6) may change places.
+ * and compared in 64 bits. Beams of the same logits and score tie exactly;
+ * totals of different ones that differ by less than the sums' error (about
+ * 1e-7, at most 1e-6) may change places.
  */
 typedef struct dsa_beam_problem {
   int32_t batch;

@@ -33,6 +33,29 @@ def test_zero_scores_of_either_sign_are_equal(D):  # noqa: F811
             run(D, x, torch.tensor(s, device="cuda"), 2, 2, select, finished=done, pad=7)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("batch,beams,V,select", [(1, 4, 131072, 8), (3, 5, 50001, 10), (1, 64, 30011, 64), (9, 8, 131073, 16),
+                                                  (40, 4, 9001, 4), (1, 2, 260000, 2)])
+def test_beams_that_are_the_same_tie(D, dtype, batch, beams, V, select):  # noqa: F811
+    """Beams of the same logits and score, though cut into other slices and aligned otherwise: their totals
+    are equal, so the lower one's come first. Beside them others of another score, or nearly the same row."""
+    x, s = rand(batch * beams, V, dtype, V + beams)
+    for b in range(batch):
+        rows = x[b * beams:(b + 1) * beams]
+        rows[:] = rows[0].clone()
+        s[b * beams:(b + 1) * beams] = s[b * beams].clone()
+        if beams >= 4:
+            s[b * beams + 1] -= 0.125          # another score (exact in fp32, as its multiples)
+            rows[3, V // 2] = -math.inf        # another row
+    run(D, x, s, batch, beams, select)
+    # the first step as it is often written: every beam but the first far behind, all rows alike
+    x = x[:beams].clone()
+    x[:] = x[0].clone()
+    s = torch.full((beams,), -1e9, device="cuda")
+    s[0] = 0
+    run(D, x, s, 1, beams, min(64, select + 2))
+
+
 @pytest.mark.parametrize("dtype,value", [("bf16", 0.30078125), ("fp16", -4.19921875), ("fp32", 0.1), ("fp32", -7.3)])
 @pytest.mark.parametrize("rows,V", [(500, 1 << 17), (460, (1 << 20) + 3)])
 def test_sums_of_long_rows_of_equal_logits(D, dtype, value, rows, V):  # noqa: F811

@@ -90,6 +90,7 @@ struct BeamParams {
   unsigned per, extra;         // units of a block: per, one more in the first `extra`
   int row_tiles;
   int beams, vocab, select, slices, pad;
+  int elem;           // bytes of a logit
 };
 
 // Block c takes the units (tiles of all rows) [run_begin(c), run_begin(c + 1)).
@@ -534,6 +535,59 @@ __device__ __forceinline__ int log_fixed(unsigned long long x, float* hi, float*
   return e - 36;
 }
 
+// Whether the n logits at x and at y are the same (-0 as +0; a NaN's row has no
+// candidate). The whole block calls it.
+__device__ __forceinline__ bool same_logits(const uint8_t* x, const uint8_t* y, int n, int elem) {
+  const uint32_t mag = elem == 4 ? 0x7fffffffu : 0x7fff7fffu;   // without the signs
+  const auto differ = [&](uint32_t u, uint32_t v) {   // a value of 32 bits, or two of 16
+    if (u == v) return false;
+    if (elem == 4) return ((u | v) & mag) != 0u;
+    const uint32_t d = u ^ v, w = (u | v) & mag;
+    return ((d & 0xffffu) && (w & 0xffffu)) || ((d >> 16) && (w >> 16));
+  };
+  const auto one = [&](int e) {
+    return elem == 4 ? differ(reinterpret_cast<const uint32_t*>(x)[e], reinterpret_cast<const uint32_t*>(y)[e])
+                     : differ(reinterpret_cast<const uint16_t*>(x)[e], reinterpret_cast<const uint16_t*>(y)[e]);
+  };
+  // 16 bytes of x at a time, from its first such boundary; of y the five words
+  // (within it) that hold the same values
+  const int per = 16 / elem;
+  const int head = min(n, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / elem);
+  const uint8_t* xv = x + head * elem;
+  const uint8_t* yv = y + head * elem;
+  const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(yv) & 3);   // 0, or 2 for 16-bit values
+  const int vecs = max(0, (n - head - (odd ? 1 : 0)) / per), tail = head + vecs * per;
+  const uint32_t* yw = reinterpret_cast<const uint32_t*>(yv - odd);
+  bool diff = false;
+  constexpr int kAhead = 4;
+  for (int v0 = 0; v0 < vecs; v0 += kAhead * kMergeThreads) {
+    uint4 u[kAhead];
+    uint32_t w[kAhead][5];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int v = min(v0 + i * kMergeThreads + static_cast<int>(threadIdx.x), vecs - 1);
+      u[i] = reinterpret_cast<const uint4*>(xv)[v];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[i][k] = yw[4 * v + k];
+      w[i][4] = odd ? yw[4 * v + 4] : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const uint32_t c[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) diff = diff || differ(c[k], __funnelshift_r(w[i][k], w[i][k + 1], 8 * odd));
+    }
+    if (__syncthreads_or(diff)) return false;
+  }
+  // before the first vector and behind the last
+  const int rest = head + n - tail;   // (fewer than 32)
+  if (static_cast<int>(threadIdx.x) < rest) {
+    const int e = threadIdx.x;
+    diff = one(e < head ? e : tail + e - head) || diff;
+  }
+  return !__syncthreads_or(diff);
+}
+
 // One thread block per batch entry; its beams' slices are the lists
 // b * slices + j.
 __global__ void __launch_bounds__(kMergeThreads, 1) beam_merge_kernel(const BeamParams p) {
@@ -546,6 +600,8 @@ __global__ void __launch_bounds__(kMergeThreads, 1) beam_merge_kernel(const Beam
   __shared__ double s_off[DSA_MAX_BEAMS];   // score - log sum exp of each beam (a finished one: its score)
   __shared__ float s_score[DSA_MAX_BEAMS];
   __shared__ uint8_t s_over[DSA_MAX_BEAMS];
+  __shared__ unsigned long long s_alike[DSA_MAX_BEAMS];   // lower beams of the same score
+  __shared__ int s_first[DSA_MAX_BEAMS];    // the lowest beam of the same score and logits
   __shared__ uint32_t s_bound[kBounds * kMergeWarps];
   __shared__ int s_count;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -558,8 +614,36 @@ __global__ void __launch_bounds__(kMergeThreads, 1) beam_merge_kernel(const Beam
   if (tid < p.beams) {
     s_score[tid] = p.scores[row0 + tid];
     s_over[tid] = p.finished && p.finished[row0 + tid];
+    s_alike[tid] = 0ull;
+    s_first[tid] = tid;
   }
   __syncthreads();
+  // Beams of the same score and logits tie, but their rows are cut and aligned
+  // differently, and so their sums rounded: rows of equal scores are compared, while
+  // the scan runs, and a beam takes the sum of the lowest one that is the same. (Rows
+  // that differ do so early as a rule. Four equal beams of 32,000 take 22 us and not
+  // 9.3, 64 x 8 of 131,072 132 and not 41; compared by the scan's blocks these were
+  // 13 and 204, but every call of 64 x 8 took 2.3 us more.)
+  bool tied = false;
+  for (int x = tid; x < p.beams * p.beams; x += kMergeThreads) {
+    const int i = x / p.beams, j = x - i * p.beams;
+    if (j < i && !s_over[i] && !s_over[j] && s_score[i] == s_score[j] && s_score[i] > -INFINITY) {
+      atomicOr(&s_alike[i], 1ull << j);
+      tied = true;
+    }
+  }
+  if (__syncthreads_or(tied)) {
+    const long long pitch = p.stride * p.elem;
+    const uint8_t* rows = static_cast<const uint8_t*>(p.logits) + row0 * pitch;
+    for (int i = 1; i < p.beams; ++i)
+      for (unsigned long long left = s_alike[i]; left != 0ull; left &= left - 1) {
+        const int j = __ffsll(static_cast<long long>(left)) - 1;
+        if (s_first[j] != j || !same_logits(rows + i * pitch, rows + j * pitch, p.vocab, p.elem)) continue;
+        if (tid == 0) s_first[i] = j;
+        __syncthreads();
+        break;
+      }
+  }
   int b = 0;
   bool there = false;
   if (tid < lists) {
@@ -594,7 +678,7 @@ __global__ void __launch_bounds__(kMergeThreads, 1) beam_merge_kernel(const Beam
   if (tid < p.beams) {
     double off = s_score[tid];
     if (!s_over[tid]) {
-      const SliceSum* s = s_sum + tid * p.slices;
+      const SliceSum* s = s_sum + s_first[tid] * p.slices;
       float mm = -INFINITY;
       for (int j = 0; j < p.slices; ++j) mm = fmaxf(mm, s[j].max);
       unsigned long long sum = 0ull;
@@ -856,6 +940,7 @@ extern "C" int dsa_beam_select(const dsa_beam_problem* bp, const void* logits, c
   p.vocab = bp->vocab;
   p.select = bp->select;
   p.pad = bp->pad_token;
+  p.elem = bp->logits_dtype == DSA_FP32 ? 4 : 2;
   p.stride = bp->row_stride ? bp->row_stride : bp->vocab;
   const Cut c = cut(bp, sms, (reinterpret_cast<uintptr_t>(logits) & 15) == 0);
   p.per = static_cast<unsigned>(c.units / c.blocks);
