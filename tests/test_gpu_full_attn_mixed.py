@@ -99,3 +99,17 @@ def test_narrow_caps(D, q, kv, softcap, q_mul):  # noqa: F811
         c["q"] = (c["q"].float() * q_mul).to(c["q"].dtype)
         c["q"][:, 1] = 0
         run(D, c, out_dtype="fp32", softcap=softcap)
+
+
+def test_a_short_block_table_is_refused(D):  # noqa: F811
+    c = batch(dict(q_len=[1, 2], total_len=[300, 200], hq=8, hkv=2), "bf16", "bf16", block=128)
+    p = D.make_full_attn_problem(c["q_len"], c["total_len"], 8, 2, cache_capacity=c["cap"])
+    q, k, v = c["q"].cuda(), c["pools"]["k"].cuda(), c["pools"]["v"].cuda()
+    with pytest.raises(ValueError, match="rows for 2 sequences"):
+        D.dsa_full_attn(p, q, k, v, None, None, torch.empty_like(q), D.alloc_full_attn_workspace(p),
+                        pages=D.make_pages(c["table"][:1].contiguous().cuda(), 128, c["nb"]))
+    # (rows behind the call's sequences are another call's)
+    more = torch.cat([c["table"], torch.full_like(c["table"], 1 << 30)])
+    D.dsa_full_attn(p, q, k, v, None, None, torch.empty_like(q), ws := D.alloc_full_attn_workspace(p),
+                    pages=D.make_pages(more.cuda(), 128, c["nb"]))
+    assert D.dsa_read_device_status(ws) == 0

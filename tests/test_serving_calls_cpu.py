@@ -181,3 +181,16 @@ def test_struct_layouts_match_the_header(D):
     assert ctypes.sizeof(D.DsaPageState) == 32 and D.DsaPageState.block_table.offset == 16
     assert ctypes.sizeof(D.DsaPagePool) == 16
     assert ctypes.sizeof(D.DsaBeamProblem) == 32 and D.DsaBeamProblem.row_stride.offset == 24
+
+
+def test_a_block_table_needs_a_row_for_every_sequence(D):
+    import torch
+    pages = D.DsaKvPages(128, 10, 4, 0x7000)
+    assert D._cache_shapes(full(D), pages) == (1280,)
+    for rows in (1, 2, 3):
+        pages._table = torch.zeros(rows, 4, dtype=torch.int32)
+        if rows < 2:
+            with pytest.raises(ValueError, match="rows for 2 sequences"):
+                D._cache_shapes(full(D), pages)
+        else:
+            assert D._cache_shapes(full(D), pages) == (1280,)

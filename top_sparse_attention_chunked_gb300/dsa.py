@@ -343,9 +343,14 @@ def _kv_ptr(p: DsaProblem, t, name, dtype, shape):
 
 
 def _cache_shapes(p: DsaProblem, pages: Optional[DsaKvPages]):
-    """Leading dims of the kI / K / V / scale arrays: [B, cap] or the pool."""
+    """Leading dims of the kI / K / V / scale arrays: [B, cap] or the pool
+    (whose block table must have a row for every sequence: the kernels read
+    that many)."""
     if pages is None:
         return (p.batch, p.cache_capacity)
+    table = getattr(pages, "_table", None)
+    if table is not None and table.shape[0] < p.batch:
+        raise ValueError(f"block_table has {table.shape[0]} rows for {p.batch} sequences")
     return (pages.num_blocks * pages.block_size,)
 
 
