@@ -612,7 +612,9 @@ size_t dsa_pages_workspace_size(const dsa_page_state* st);
  * argument or table entry is out of range (bit 4), the new state is the old
  * one, nothing is copied and counts = {-1, blocks free before}; read it with
  * dsa_read_device_status (DSA_ERR_WORKSPACE for bit 3, DSA_ERR_INVALID_ARG for
- * bit 4). Results do not depend on the order of execution.
+ * bit 4). Results do not depend on the order of execution. parent and the
+ * lengths must not overlap the new state, a pool or counts, nor counts the old
+ * or new state or a pool.
  */
 int dsa_pages_update(const dsa_page_state* st, const int32_t* parent, const int32_t* keep_len,
                      const int32_t* new_len, const int32_t* first_key, int num_pools,
@@ -627,6 +629,7 @@ int dsa_pages_update(const dsa_page_state* st, const int32_t* parent, const int3
  *   remap   DEVICE [num_blocks] int32 or NULL: the new index of every used
  *           block (-1: free), for references kept outside the table
  *   counts  DEVICE [2] int32 or NULL: blocks moved, blocks free
+ *   (neither may overlap the other, the state or a pool)
  * Entries that are out of range or name a free block set status bit 4 and
  * leave everything as it was (counts = {-1, blocks free}).
  */

@@ -574,6 +574,22 @@ int check_common(const dsa_page_state* st, const PageDims& d, int num_pools, con
   return check_call_workspace(ws, ws_bytes, page_ws(nullptr, d).total);
 }
 
+// Whether a call's further array overlaps what the call writes: the new page
+// state and the pools.
+bool over_written(const void* x, long long bytes, const PageDims& d, const int32_t* table_out, const int32_t* refs_out,
+                  const PoolList& pools) {
+  if (!x) return false;
+  bool over = overlap(x, bytes, table_out, 4LL * d.rows * d.W) || overlap(x, bytes, refs_out, 4LL * d.nb);
+  for (int i = 0; i < pools.n; ++i) over = over || overlap(x, bytes, pools.base[i], pools.bytes[i] * d.nb);
+  return over;
+}
+// The same for an array that the call writes: nor may it lie over the old state.
+bool over_state(const void* x, long long bytes, const dsa_page_state* st, const PageDims& d, const int32_t* table_out,
+                const int32_t* refs_out, const PoolList& pools) {
+  return over_written(x, bytes, d, table_out, refs_out, pools) ||
+         (x && (overlap(x, bytes, st->block_table, 4LL * d.rows * d.W) || overlap(x, bytes, st->refs, 4LL * d.nb)));
+}
+
 bool small_state(const PageDims& d) { return d.rows * d.W <= kSmallEntries && d.nb <= kSmallBlocks; }
 
 unsigned entry_grid(const PageDims& d, int sms) {
@@ -617,10 +633,12 @@ extern "C" int dsa_pages_update(const dsa_page_state* st, const int32_t* parent,
   if (!al4(parent) || !al4(keep_len) || !al4(new_len) || !al4(first_key) || !al4(counts))
     return report_error(DSA_ERR_MISALIGNED, "parent, lengths and counts must be 4-byte aligned");
   if (int rc = check_common(st, d, num_pools, pools, table_out, refs_out, ws, ws_bytes, &list)) return rc;
-  for (const int32_t* in : {parent, keep_len, new_len, first_key, static_cast<const int32_t*>(counts)})
-    if (in && (overlap(in, in == counts ? 8 : 4LL * d.rows, table_out, 4LL * d.rows * d.W) ||
-               overlap(in, in == counts ? 8 : 4LL * d.rows, refs_out, 4LL * d.nb)))
-      return report_error(DSA_ERR_INVALID_ARG, "parent, lengths and counts must not overlap the page state");
+  for (const int32_t* in : {parent, keep_len, new_len, first_key})
+    if (over_written(in, 4LL * d.rows, d, table_out, refs_out, list) ||
+        (in && counts && overlap(in, 4LL * d.rows, counts, 8)))
+      return report_error(DSA_ERR_INVALID_ARG, "parent and lengths must not overlap the new page state, a pool or counts");
+  if (over_state(counts, 8, st, d, table_out, refs_out, list))
+    return report_error(DSA_ERR_INVALID_ARG, "counts must not overlap the page state or a pool");
   int sms = 0;
   if (int rc = current_device(&sms)) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -657,6 +675,9 @@ extern "C" int dsa_pages_compact(const dsa_page_state* st, int num_pools, const 
   if (int rc = check_state(st, &d)) return rc;
   if (!al4(remap) || !al4(counts)) return report_error(DSA_ERR_MISALIGNED, "remap and counts must be 4-byte aligned");
   if (int rc = check_common(st, d, num_pools, pools, table_out, refs_out, ws, ws_bytes, &list)) return rc;
+  if (over_state(remap, 4LL * d.nb, st, d, table_out, refs_out, list) || over_state(counts, 8, st, d, table_out, refs_out, list) ||
+      (remap && counts && overlap(remap, 4LL * d.nb, counts, 8)))
+    return report_error(DSA_ERR_INVALID_ARG, "remap and counts must not overlap each other, the page state or a pool");
   int sms = 0;
   if (int rc = current_device(&sms)) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
