@@ -17,7 +17,7 @@ def constants():
     """The schedule's constants, from the source."""
     with open(_SOURCE) as f:
         text = f.read()
-    names = ("kTileKeys", "kSlotRows", "kMaxCtas", "kCostRows", "kCostKeys", "kCostItem")
+    names = ("kTileKeys", "kSlotRows", "kMaxCtas", "kCostRows", "kCostKeys", "kCostItem", "kCostEmpty")
     return {n: int(re.search(rf"\b{n} = (\d+)", text).group(1)) for n in names}
 
 
@@ -41,19 +41,19 @@ def segments(*args, **kw):
     """What each thread block works on: lists of (rows, tiles, whole item)."""
     k, its = constants(), items(*args, **kw)
     unit = lambda rows: k["kCostRows"] if rows > k["kSlotRows"] else k["kCostKeys"]
-    cost = sum(k["kCostItem"] + n * unit(rows) for rows, n in its)
-    tiles = sum(n for _, n in its)
-    want = min(SMS, k["kMaxCtas"], max(tiles, 1))
+    base = lambda n: k["kCostItem"] if n else k["kCostEmpty"]
+    cost = sum(base(n) + n * unit(rows) for rows, n in its)
+    units = sum(max(n, 1) for _, n in its)
+    want = min(SMS, k["kMaxCtas"], units)
     runs = []
-    if tiles <= want:
-        runs = [(i, t) for i, (_, n) in enumerate(its) for t in range(n)]
-        runs[:1] = [(0, 0)]
+    if units <= want:
+        runs = [(i, t) for i, (_, n) in enumerate(its) for t in range(max(n, 1))]
     else:
         at, c = 0, 0
         for i, (rows, n) in enumerate(its):
-            end = at + k["kCostItem"] + n * unit(rows)
+            end = at + base(n) + n * unit(rows)
             while c < want and cost * c < end * want:
-                t = max(0, cost * c // want - at - k["kCostItem"]) // unit(rows)
+                t = max(0, cost * c // want - at - base(n)) // unit(rows)
                 c += 1
                 if not runs or runs[-1] < (i, t):
                     runs.append((i, t))
@@ -90,13 +90,14 @@ MIXED = {
     "two_chunks": dict(q_len=[700, 650], total_len=[2000, 1500], hq=16, hkv=4),
 }
 
-# left-padded prompts: long runs of items without a key in one block, before and between items that see some
+# left-padded prompts: runs of items without a key in one block, before and between items that see some
 NO_KEY = {
     "prompt_of_4096": dict(q_len=[4096], total_len=[4096], hq=24, hkv=2, first_key=[4000]),
     "prompt_of_2048_then_chunks": dict(q_len=[2048, 300, 1], total_len=[2048, 700, 500], hq=8, hkv=2, first_key=[1900, 0, 0]),
     # slot 1 has eight rows of 136
     "17_tokens_of_8_heads": dict(q_len=[17] * 30 + [17], total_len=[17] * 30 + [400], hq=16, hkv=2, first_key=[17] * 30 + [0]),
     "5_tokens_then_chunk": dict(q_len=[5] * 40 + [200], total_len=[9] * 40 + [200], hq=16, hkv=2, first_key=[9] * 40 + [0]),
+    "64_prompts_of_300": dict(q_len=[300] * 64, total_len=[300] * 64, hq=16, hkv=4, first_key=[299] * 20 + [300] * 40 + [0] * 4),
     # more tiles than blocks: the items are laid out by cost
     "padded_batch": dict(q_len=[1500] * 4, total_len=[1500] * 4, hq=16, hkv=4, first_key=[1200, 0, 1499, 700]),
 }

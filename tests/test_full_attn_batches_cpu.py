@@ -12,13 +12,24 @@ def test_mixed_batches_go_from_narrow_to_wide_items(name):
     assert any(n >= 3 and n % 2 for n in to_rows)
 
 
-@pytest.mark.parametrize("name", list(F.NO_KEY))
-def test_padded_batches_have_runs_of_items_without_a_key(name):
+def test_padded_batches_have_runs_of_items_without_a_key():
+    """Several in one block, of more than 128 rows, before items with keys and behind them; spread over
+    the blocks, however many there are."""
     slot = F.constants()["kSlotRows"]
-    blocks = F.segments(**F.NO_KEY[name])
-    runs = [sum(n == 0 and (rows > slot or "5_tokens" in name) for rows, n, _ in b) for b in blocks]
-    assert max(runs) >= (2 if name == "padded_batch" else 25)
-    assert any(n for b in blocks for _, n, _ in b)
+    before = after = longest = 0
+    for name, c in F.NO_KEY.items():
+        blocks = F.segments(**c)
+        empty = [sum(n == 0 for _, n, _ in b) for b in blocks]
+        assert any(n for b in blocks for _, n, _ in b) and any(empty)
+        assert max(empty) <= 20, name
+        for b in blocks:
+            run = 0
+            for (r0, n0, _), (r1, n1, _) in zip(b, b[1:]):
+                run = run + 1 if n0 == n1 == 0 and r0 > slot and r1 > slot else 0
+                longest = max(longest, run + 1)
+                before += n0 == 0 and n1 > 0 and r0 > slot
+                after += n0 > 0 and n1 == 0 and r1 > slot
+    assert longest >= 5 and before and after
 
 
 def test_loop_batches_cover_the_main_loop():

@@ -829,16 +829,19 @@ __device__ __forceinline__ int row_exponent(uint32_t top) {
 // would be a NaN (below fp32's normal numbers no such row's logits differ from 0).
 __device__ __forceinline__ float row_unit(float scale_log2, int ex) { return fmaxf(ldexpf(scale_log2, ex), kLeastUnit); }
 
-// The outputs of `n` rows of an item from row0 on, none of which sees a key. One
-// warp calls it.
+// The outputs of `n` rows (32 at the most) of an item from row0 on, none of which
+// sees a key. One warp calls it; a lane finds a row's place.
 __device__ __forceinline__ void write_no_key(const FullParams& p, const Item& w, int row0, int n) {
-  const int lane = threadIdx.x & 31;
-  const int vecs = DSA_HEAD_DIM * (p.out_dtype == DSA_FP32 ? 4 : 2) / 16;   // a row's, 16 bytes each
-  for (int r = row0; r < row0 + n; ++r) {
-    const int tok = r / p.G;
-    const long long row = (static_cast<long long>(w.q0) + tok) * p.Hq + w.g * p.G + (r - tok * p.G);
-    if (lane < vecs) static_cast<uint4*>(p.out)[row * vecs + lane] = make_uint4(0, 0, 0, 0);
-    if (lane == 0 && p.lse) p.lse[row] = -INFINITY;
+  if (n <= 0) return;
+  const int lane = threadIdx.x & 31, r = row0 + imin(lane, n - 1), tok = r / p.G;
+  const long long row = (static_cast<long long>(w.q0) + tok) * p.Hq + w.g * p.G + (r - tok * p.G);
+  if (p.lse && lane < n) p.lse[row] = -INFINITY;
+  const int vecs = p.out_dtype == DSA_FP32 ? 32 : 16;   // a row's, 16 bytes each
+#pragma unroll 4
+  for (int i = 0; i < n; i += 32 / vecs) {
+    const int k = i + lane / vecs;
+    const long long to = __shfl_sync(0xffffffffu, row, imin(k, n - 1));
+    if (k < n) static_cast<uint4*>(p.out)[to * vecs + lane % vecs] = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -1765,11 +1768,15 @@ int check_full(const dsa_full_problem* p) {
 // Costs of a unit, in quarters of a tile of 256 rows: a tile of up to 128 rows
 // takes the same loads and half the products; an item, its queries and output
 // (8 / 20 / 40: 2,048 tokens on 2,048 48.5 / 45.4 / 45.2 us, 32 single tokens on
-// 300 .. 8,192 keys 94.4 / 93.8 / 96.4 us).
-constexpr int kCostRows = 4, kCostKeys = 3, kCostItem = 20;
+// 300 .. 8,192 keys 94.4 / 93.8 / 96.4 us); an item without a key, its zeros
+// (2 / 4 / 8: 4 prompts of 2,048, left-padded by 0 .. 2,000, 101 / 77 / 79 us, 8 of
+// 1,000 65 / 61 / 65 us).
+constexpr int kCostRows = 4, kCostKeys = 3, kCostItem = 20, kCostEmpty = 4;
 
-// Lays the items out over at most min(sms, kMaxCtas, tiles) blocks (fp: the
+// Lays the items out over at most min(sms, kMaxCtas, units) blocks (fp: the
 // problem and the runs, mp: the items that are split) and returns their number.
+// A unit is a tile, or an item without one: a left-padded prompt has hundreds of
+// those, which would take longer than its tiles if they fell to one block.
 // *bytes gets the workspace that holds two parts of as many blocks as any device
 // may use. (More SMs may lead to fewer blocks: cuts that fall into the same tile
 // are one.)
@@ -1793,27 +1800,26 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
   }
   fp->part_rows = (fp->part_rows + 3) & ~3;   // parts stay 16-byte aligned
   const int items = fp->seq[p->batch].item0;
-  long long cost = 0, tiles = 0;
+  const auto item_cost = [](const Item& w) { return w.ntiles > 0 ? kCostItem : kCostEmpty; };
+  long long cost = 0, units = 0;
   for (int i = 0, at = 0; i < items; ++i) {
     const Item w = make_item(*fp, i, at);
     at = w.b;
-    cost += kCostItem + static_cast<long long>(w.ntiles) * (w.nrows > kSlotRows ? kCostRows : kCostKeys);
-    tiles += w.ntiles;
+    cost += item_cost(w) + static_cast<long long>(w.ntiles) * (w.nrows > kSlotRows ? kCostRows : kCostKeys);
+    units += imax(w.ntiles, 1);
   }
-  const int most = static_cast<int>(std::min<long long>(kMaxCtas, std::max(tiles, 1LL)));
+  const int most = static_cast<int>(std::min<long long>(kMaxCtas, std::max(units, 1LL)));
   const int want = imin(sms, most);
   *bytes = kPartialAt + static_cast<size_t>(2) * most * fp->part_rows * (DSA_HEAD_DIM + 2) * 4;
   int blocks = 0;
-  if (tiles <= want) {
-    // a tile each, for an item costs every block the same (16 tiles, 24/2 heads:
+  if (units <= want) {
+    // one each, for an item costs every block the same (16 tiles, 24/2 heads:
     // 9.5 us, against 10.1 with the cuts below, of which some fall into an item's
     // cost and leave other blocks two tiles; 4 x 600 keys 9.3 against 10.9)
-    for (int i = 0, b = 0, before = 0; i < items; ++i) {
+    for (int i = 0, b = 0; i < items; ++i) {
       const Item w = make_item(*fp, i, b);
       b = w.b;
-      if (i == 0) fp->run[blocks++] = FullParams::Run{0, 0, b, 0};
-      for (int t = 0; t < w.ntiles; ++t)
-        if (before++ > 0) fp->run[blocks++] = FullParams::Run{i, t, b, 0};
+      for (int t = 0; t < imax(w.ntiles, 1); ++t) fp->run[blocks++] = FullParams::Run{i, t, b, 0};
     }
   } else {
     // run k begins where the costs reach k / want of their sum
@@ -1822,9 +1828,9 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
       const Item w = make_item(*fp, i, b);
       b = w.b;
       const int unit = w.nrows > kSlotRows ? kCostRows : kCostKeys;
-      const long long end = at + kCostItem + static_cast<long long>(w.ntiles) * unit;
+      const long long end = at + item_cost(w) + static_cast<long long>(w.ntiles) * unit;
       for (; k < want && cost * k < end * want; ++k) {
-        const long long x = cost * k / want - at - kCostItem;
+        const long long x = cost * k / want - at - item_cost(w);
         const int tile = x > 0 ? static_cast<int>(x / unit) : 0;
         if (blocks > 0 && fp->run[blocks - 1].item == i && fp->run[blocks - 1].tile >= tile) continue;
         fp->run[blocks++] = FullParams::Run{i, tile, b, 0};
