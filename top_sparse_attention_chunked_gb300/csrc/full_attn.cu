@@ -118,6 +118,8 @@ struct FullParams {
   int B, Hq, Hkv, G, cap, window;
   int q_dtype, out_dtype;
   float scale_log2, softcap;
+  float cap_log2, cap_inv;      // of softcap > 0: softcap * log2 e, and 1 over it
+  float cap_pre, cap_ys;        // for FOLD: what z is scaled by first (1: nothing), the units of cap then
   Paging pg;
   // (what a block needs first lies together: every line of the parameters is a
   // miss to begin with)
@@ -754,24 +756,26 @@ __device__ __forceinline__ void odd_poly(float* z, float ys, float cap, const fl
 }
 
 // z (units of S, c log2-units each) -> cap * tanh(z c ln2 / cap) in log2 units, to
-// a relative error of 7e-7 of the result, however far the cap lies above it (an
-// error of some part of the cap would be one of the logit of a wide cap).
+// a relative error of 7e-7 of the result or 1.6e-5 of a logit, however far the cap
+// lies above it (an error of some part of a wide cap would be one of the logits).
 // Arguments y of up to 0.25, 0.4 and 0.7 take odd polynomials, fitted to tanh y / y
 // for the least relative error (4e-7, 1e-7, 1e-8; the first is a multiply-add a
-// value shorter). Where a part has larger ones, those beyond 0.4 take
-// tanh y = 1 - 2 / (1 + e^2y), whose error, 2.5e-7, is one of the cap, and whose two
-// special-function calls a value would be the kernel's bound.
+// value shorter). Parts with larger ones take tanh y = 1 - 2 / (1 + e^2y), whose two
+// special-function calls a value would be the kernel's bound, and whose error is
+// 2.5e-7 of the cap: with caps above 64, arguments of up to 0.4 take the second
+// polynomial there too (4,096 tokens on 4,096 with a cap of 3: 207 us, 275 if small
+// caps did that).
 // FOLD (c is the problem's, not a row's): see odd_poly; the eleventh power of
-// c / cap times cap has to be a normal number, else z is scaled first. N < 32: a
-// shorter choice (the code of a few values, not their time, is what counts).
+// c / cap times cap has to be a normal number, else z is scaled first (cap_fold).
+// N < 32: a shorter choice (the code of a few values, not their time, is what
+// counts).
+constexpr float kNearCap = 64.0f;
 template <int N, bool FOLD>
-__device__ __forceinline__ void cap_scores(float* z, float c, float softcap) {
-  const float cap = softcap * 1.4426950408889634f;
-  float ys = fminf(c / cap, 1e38f);
-  if (FOLD && !(ys >= 0x1p-11f && ys <= 0x1p11f && c >= 0x1p-16f && c <= 0x1p16f)) {
+__device__ __forceinline__ void cap_scores(float* z, float c, const FullParams& p) {
+  const float cap = p.cap_log2, ys = FOLD ? p.cap_ys : c * p.cap_inv;
+  if (FOLD && p.cap_pre != 1.0f) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] *= ys;
-    ys = 1.0f;
+    for (int i = 0; i < N; ++i) z[i] *= p.cap_pre;
   }
   float far[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -786,6 +790,10 @@ __device__ __forceinline__ void cap_scores(float* z, float c, float softcap) {
   } else if (N >= 32 && __all_sync(0xffffffffu, y <= 0.7f)) {
     const float k[6] = {-0.0050883363f, 0.0200244579f, -0.0535260104f, 0.133284152f, -0.333331317f, 1.0f};
     odd_poly<N, FOLD>(z, ys, cap, k);
+  } else if (p.softcap <= kNearCap) {
+    const float two = ys * 2.8853900817779268f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = fmaf(-2.0f * cap, fast_rcp(1.0f + fast_exp2(z[i] * two)), cap);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -989,7 +997,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
             }
           }
           if constexpr (MOD) {
-            if (p.softcap > 0.f) cap_scores<kCols, !kMayScale>(z, c, p.softcap);
+            if (p.softcap > 0.f) cap_scores<kCols, !kMayScale>(z, c, p);
             else
 #pragma unroll
               for (int i = 0; i < kCols; ++i) z[i] *= c;
@@ -1449,7 +1457,7 @@ __device__ __forceinline__ void few_role(const FullParams& p, FewBars* bars, con
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) z[n][e] *= unit[e >> 1];
-        if (p.softcap > 0.f) cap_scores<8, false>(&z[0][0], 1.0f, p.softcap);
+        if (p.softcap > 0.f) cap_scores<8, false>(&z[0][0], 1.0f, p);
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -1896,6 +1904,20 @@ cudaError_t launch_few(bool mod, int blocks, const CUtensorMap& tm_k, const CUte
                     fp, st);
 }
 
+// What cap_scores takes of a cap. A cap beyond 1e30 leaves every logit as it is and
+// is taken as that; 1 / cap stays below 1e38, a cap that small makes all logits 0.
+void cap_fold(float softcap, FullParams* fp) {
+  fp->softcap = std::min(softcap, 1e30f);
+  if (!(softcap > 0.0f)) return;
+  const float c = fp->scale_log2;
+  fp->cap_log2 = fp->softcap * 1.4426950408889634f;
+  fp->cap_inv = std::min(1.0f / fp->cap_log2, 1e38f);
+  const float ys = std::min(c * fp->cap_inv, 1e38f);
+  const bool fold = ys >= 0x1p-11f && ys <= 0x1p11f && c >= 0x1p-16f && c <= 0x1p16f;
+  fp->cap_pre = fold ? 1.0f : ys;
+  fp->cap_ys = fold ? ys : 1.0f;
+}
+
 int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* q, const void* k, const void* v,
               const float* ks, const float* vs, const float* slopes, void* out, float* lse, void* ws,
               size_t ws_bytes, void* stream) {
@@ -1946,8 +1968,7 @@ int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* 
   fp.out_dtype = p->out_dtype;
   const float scale = p->softmax_scale > 0.0f ? p->softmax_scale : 1.0f / std::sqrt(static_cast<float>(p->head_dim));
   fp.scale_log2 = std::max(scale * 1.4426950408889634f, kLeastUnit);
-  // (beyond, the cap leaves every finite logit of sense as it is; cap * log2 e stays finite)
-  fp.softcap = std::min(p->softcap, 1e30f);
+  cap_fold(p->softcap, &fp);
   fp.pg = pg;
   mp.partial = fp.partial;
   mp.out = out;
