@@ -101,6 +101,15 @@ def test_narrow_caps(D, q, kv, softcap, q_mul):  # noqa: F811
         run(D, c, out_dtype="fp32", softcap=softcap)
 
 
+@pytest.mark.parametrize("kv", ["fp16", "int8"])
+def test_a_narrow_cap_on_large_queries(D, kv):  # noqa: F811
+    """Units of a scaled row over a cap that leave fp32, beside keys of zeros."""
+    c = batch(dict(q_len=[2, 40, 150], total_len=[300, 300, 300], hq=12, hkv=2), "bf16", kv, seed=29)
+    c["q"] = (c["q"].float() * 2.0 ** 100).to(torch.bfloat16)
+    c["k"][:, ::3] = 0
+    run(D, c, out_dtype="fp32", softcap=1e-30)
+
+
 def test_a_short_block_table_is_refused(D):  # noqa: F811
     c = batch(dict(q_len=[1, 2], total_len=[300, 200], hq=8, hkv=2), "bf16", "bf16", block=128)
     p = D.make_full_attn_problem(c["q_len"], c["total_len"], 8, 2, cache_capacity=c["cap"])

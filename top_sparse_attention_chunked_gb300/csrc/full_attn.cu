@@ -772,7 +772,7 @@ __device__ __forceinline__ void odd_poly(float* z, float ys, float cap, const fl
 constexpr float kNearCap = 64.0f;
 template <int N, bool FOLD>
 __device__ __forceinline__ void cap_scores(float* z, float c, const FullParams& p) {
-  const float cap = p.cap_log2, ys = FOLD ? p.cap_ys : c * p.cap_inv;
+  const float cap = p.cap_log2, ys = FOLD ? p.cap_ys : fminf(c * p.cap_inv, 1e38f);
   if (FOLD && p.cap_pre != 1.0f) {
 #pragma unroll
     for (int i = 0; i < N; ++i) z[i] *= p.cap_pre;
