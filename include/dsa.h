@@ -516,7 +516,8 @@ int dsa_cache_append_paged(const dsa_problem* p, const dsa_kv_pages* pages, cons
  * Arithmetic: logits, softmax statistics and sums in fp32. The weights enter
  * the second product in FP16 for an FP16 cache, as a pair of BF16 numbers for
  * an FP16 query on an INT8 cache, and in BF16 otherwise. A BF16 query on an
- * FP16 cache is scaled by a power of two per row. The workspace is read and
+ * FP16 cache is scaled by a power of two per row. Logits of visible keys must
+ * stay below 2^30 in size (before a cap, of which there may be any). The workspace is read and
  * written as described at the top; the call takes its size from
  * dsa_full_attn_workspace_size (0 and a message if `p` is invalid). N = 0 runs
  * no kernel.
@@ -648,7 +649,7 @@ int dsa_pages_compact(const dsa_page_state* st, int num_pools, const dsa_page_po
  * its score) is never selected; slots left over get score -infinity, token -1
  * and parent -1.
  *
- *   batch       1 .. 65535
+ *   batch       1 .. 65535, batch * beams at most 65535
  *   beams       1 .. 64
  *   vocab       1 .. 2^24
  *   select      1 .. 64 (beams, or 2 * beams where the caller sorts out ended ones)
@@ -669,7 +670,11 @@ int dsa_pages_compact(const dsa_page_state* st, int num_pools, const dsa_page_po
  * Sums are taken in fp32 per thread and joined in 64 bits; totals are formed
  * and compared in 64 bits. Beams of the same logits and score tie exactly;
  * totals of different ones that differ by less than the sums' error (about
- * 1e-7, at most 1e-6) may change places.
+ * 1e-7, at most 1e-6) may change places. A total is logit + (score - log sum)
+ * in 64 bits, so a row whose largest logit is far beyond 1e9 in size keeps of
+ * its scores what 64 bits leave at that size: mask with -infinity (a row of
+ * nothing else has no continuation) rather than with the type's lowest value
+ * throughout, of which every total is 0.
  */
 typedef struct dsa_beam_problem {
   int32_t batch;

@@ -30,12 +30,14 @@
 // bits (rows have different offsets: totals may lie closer together than fp32
 // tells apart) and ranks them by counting.
 //
-// What bounds it: large batches the scan's instructions (11 of a warp for 32
-// bf16 values, the scheduler 50% busy), 32 x 8 beams of 128,000 27 us, 2.4 TB/s,
-// as fp32 35 us, 3.7 TB/s, of 6.8 measured; small ones the two launches and the
-// merge's chain of dependent steps, 4 beams of 32,000 8.7 us; many beams with a
-// large `select` the merge of up to 512 lists by one block, 64 beams of 200,000
-// with 64 selected 77 us.
+// What bounds it: large batches the scan's latency (11 instructions of a warp for
+// 32 bf16 values keep the scheduler 50% busy, the memory is 45% busy: one tile is
+// in flight while one is worked on, with two barriers every second tile), 32 x 8
+// beams of 128,000 27 us, 2.4 TB/s, as fp32 35 us, 3.7 TB/s, of 6.8 measured; small
+// ones the two launches and the merge's chain of dependent steps, 4 beams of 32,000
+// 9.3 us; many beams with a large `select` the merge of up to 512 lists by one
+// block, 64 beams of 200,000 with 64 selected 78 us. Beams of equal scores, as of a
+// first step, are compared besides (see the merge).
 //
 // The order of a list depends on the order of execution; its keys are distinct
 // (value, then token), so what is picked out of it does not.

@@ -33,8 +33,10 @@
 //     One token on 1,024: 9.6 us, on 16,384: 14.3 us (1.2 TB/s);
 //   many tokens: the hand-over between tensor core and softmax. 4,096 on 16,384:
 //     523 us, 1,381 TFLOP/s (the two products alone would take 460); 4,096 on
-//     4,096: 110 us, 939 TFLOP/s (a block's share is 4 items);
-//   capped scores: the multiply-adds of the cap. 4,096 on 4,096: 137 us.
+//     4,096: 110 us, 939 TFLOP/s (a block's share is 2.5 items in 3.2 segments, and
+//     at each the output, the next queries and the first product follow one another);
+//   capped scores: the multiply-adds of the cap. 4,096 on 4,096: 139 us, with
+//     arguments beyond the polynomials (a cap of 3) 207.
 //
 // The running maximum m is raised (and O rescaled in tensor memory) only when
 // a row's weights grow by more than 2^8 over it, and by a whole power of two, to
@@ -1260,8 +1262,8 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
 // --------------------------------------------------------------- few rows
 // INT8 caches, items of up to 16 rows (one token of up to 16 heads a KV head):
 // the tensor core's tiles would be empty but for a few rows, and its operands
-// have to pass through shared memory once more as 16-bit tiles. Here eight
-// warps take 16 keys of a tile each, read the codes straight into the register
+// have to pass through shared memory once more as 16-bit tiles. Here twelve
+// warps take groups of 16 keys in turn, read the codes straight into the register
 // layout of m16n8k16 products (rows of Q x 8 keys x 16 dims, rows x 8 dims x 16
 // keys) and widen them there. The two contractions may take their indices in
 // any order, and keys and output columns may be permuted, which is used so that
