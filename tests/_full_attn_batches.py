@@ -113,6 +113,12 @@ LOOPS = {
                        hkv=4),
 }
 
+# narrow items of one tile, which only one slot works on, before wider ones
+ONE_TILE = {
+    "token_then_300": dict(q_len=[1, 300] * 20, total_len=[100, 900] * 20, hq=24, hkv=2),
+    "small_and_wide": dict(q_len=[3, 200, 1, 130] * 16, total_len=[90, 700, 128, 400] * 16, hq=8, hkv=4),
+}
+
 TYPES = [("bf16", "bf16"), ("bf16", "fp16"), ("fp16", "fp16"), ("bf16", "int8"), ("fp16", "int8")]
 
 

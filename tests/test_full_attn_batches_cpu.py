@@ -12,6 +12,12 @@ def test_mixed_batches_go_from_narrow_to_wide_items(name):
     assert any(n >= 3 and n % 2 for n in to_rows)
 
 
+@pytest.mark.parametrize("name", list(F.ONE_TILE))
+def test_one_tile_batches_go_from_narrow_items_of_one_tile_to_wide_ones(name):
+    to_rows, _ = F.changes(F.segments(**F.ONE_TILE[name]))
+    assert to_rows.count(1) >= 10
+
+
 def test_padded_batches_have_runs_of_items_without_a_key():
     """Several in one block, of more than 128 rows, before items with keys and behind them; spread over
     the blocks, however many there are."""

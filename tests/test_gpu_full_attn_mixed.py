@@ -3,7 +3,7 @@ different kinds, against the definition in 64 bits."""
 import pytest
 import torch
 
-from tests._full_attn_batches import LOOPS, MIXED, NO_KEY, TYPES, batch, grow, reference
+from tests._full_attn_batches import LOOPS, MIXED, NO_KEY, ONE_TILE, TYPES, batch, grow, reference
 from tests.test_gpu_full_attn import D, call, check  # noqa: F401 (D is a fixture)
 
 pytestmark = pytest.mark.gpu
@@ -62,6 +62,13 @@ def test_window_cap_and_bias_over_several_tiles(D, name, q, kv):  # noqa: F811
 def test_logits_that_grow_over_several_tiles(D, name, q, kv, top):  # noqa: F811
     """O is rescaled within segments, at every tile or every few."""
     run(D, grow(batch(LOOPS[name], q, kv, seed=25), top), out_dtype="fp32")
+
+
+@pytest.mark.parametrize("q,kv", TYPES)
+@pytest.mark.parametrize("name", list(ONE_TILE))
+def test_narrow_items_of_one_tile_before_wide_ones(D, name, q, kv):  # noqa: F811
+    """The slot without a tile of such an item must not run ahead of the product thread."""
+    run(D, batch(ONE_TILE[name], q, kv, block=128, seed=30), repeats=20)
 
 
 CAPPED = ([1, 0, 2], [40], [150, 3])

@@ -700,6 +700,9 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
           release(pos);
           pos.step(stages);
           if (i >= n) tc_commit(&bars->o_full[slot]);
+          // (slot 1 has no tile of a segment of one; it must not go on to the next one's
+          // queries before this thread has seen that it was ready for this one)
+          if (n == 1) tc_commit(&bars->o_full[1]);
         }
         if (i < n) {
           ok = wait_tile(pos);
@@ -1095,16 +1098,19 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     if (!ok) break;
     tile_seq += s.t1 - s.t0;
     const float m_log2 = m == -INFINITY ? -INFINITY : m * cz;
-    if (x.n > 0) {   // (slot 1 has no tile of a segment of one in keys mode)
-      if (!warp_wait(&bars->o_full[slot], no & 1, abort_flag)) break;
-      ++no;
-      tc_fence_after();
-    }
-    if (!s.rows_mode && slot == 1) {
-      // slot 0 joins the two states; it reads this slot's O itself
+    // in keys mode slot 0 joins the two states; it reads slot 1's O itself
+    const auto leave = [&]() {
       bars->m[tid] = m_log2;
       bars->l[tid] = l;
       mbar_arrive(&bars->ml);
+    };
+    const bool left = !s.rows_mode && slot == 1;
+    if (left && x.n == 0) leave();   // (slot 1 has no tile of a segment of one: slot 0 need not wait for it)
+    if (!warp_wait(&bars->o_full[slot], no & 1, abort_flag)) break;
+    ++no;
+    tc_fence_after();
+    if (left) {
+      if (x.n > 0) leave();
       continue;
     }
     float f0 = 1.0f, f1 = 0.0f, mj = m_log2, lj = l;
