@@ -23,9 +23,13 @@
  * quantise-on-write), fp32 RMSNorm + rotary embedding, both in one launch
  * (dsa_rope_append), and _paged forms of the calls for caches kept in a pool
  * of token blocks with a block table. Beside it, for a server built on the
- * library: full attention of new tokens over the cache (dsa_full_attn), the
- * life of the blocks (dsa_pages_update, dsa_pages_compact) and the selection
- * of beam search (dsa_beam_select).
+ * library: full attention of new tokens over the cache (dsa_full_attn; with a
+ * window and first keys that stay visible, dsa_full_attn_sinks), the life of
+ * the blocks (dsa_pages_update, dsa_pages_compact), the selection of beam
+ * search (dsa_beam_select) and sampling (dsa_sample); and for packed steps of
+ * unequal requests the slot map (dsa_slot_map), rotary positions with several
+ * axes and the append (dsa_rope_axes_append), and the norm between two layers
+ * (dsa_add_rmsnorm).
  *
  * Conventions (all calls):
  *  - Positions: a sequence's cache holds T_b = total_len[b] rows and its
@@ -73,7 +77,8 @@ typedef enum dsa_dtype {
   DSA_BF16 = 0,
   DSA_FP16 = 1,
   DSA_INT8 = 2,              /* KV cache only: codes + fp32 scale per token/head */
-  DSA_FP32 = 3               /* output only */
+  DSA_FP32 = 3,              /* output only (dsa_add_rmsnorm: input too) */
+  DSA_FP8_E4M3 = 4           /* output of dsa_add_rmsnorm only */
 } dsa_dtype;
 
 /* Which call a workspace is sized for. */
@@ -554,6 +559,25 @@ int dsa_full_attn_paged(const dsa_full_problem* p, const dsa_kv_pages* pages, co
                         size_t workspace_bytes, void* stream);
 
 /*
+ * dsa_full_attn_sinks -- dsa_full_attn for rolling caches: beside the window,
+ * the first `sinks` keys of every sequence stay visible. A query at position P
+ * sees the keys t with first_key[b] <= t <= P and
+ *     t < first_key[b] + sinks   or   t > P - window.
+ * Each is seen once where the two overlap; without a window (0) sinks changes
+ * nothing. Whatever lies between the first keys and the window is not read:
+ * those rows may hold anything, and so may the table entries of blocks that no
+ * query sees a key of. slopes, softcap and lse are as above.
+ *   sinks     >= 0
+ *   pages     the paged pools' description, or NULL for dense caches
+ * The workspace is dsa_full_attn's: dsa_full_attn_workspace_size(p) is enough
+ * for any number of sinks.
+ */
+int dsa_full_attn_sinks(const dsa_full_problem* p, int sinks, const dsa_kv_pages* pages, const void* q,
+                        const void* k, const void* v, const float* k_scale, const float* v_scale,
+                        const float* slopes, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
  * Page management: who holds which block of a paged pool. The state is a
  * block table [rows, blocks_per_seq] (entry -1: no block) and a reference
  * count per block, both on the device; a block is free when its count is 0.
@@ -696,6 +720,149 @@ int dsa_beam_select(const dsa_beam_problem* p, const void* logits, const float* 
                     int32_t* out_parents, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * dsa_slot_map -- where the tokens of a packed step belong, from the requests'
+ * lengths on the device: token n of the step is token i = n - first[b] of row b
+ * (first: the running sum of q_len), sits at position total_len[b] - q_len[b] +
+ * i, and its K and V belong in cache row
+ *     block_table[b][position / block_size] * block_size + position % block_size
+ * of a paged pool, or b * cache_capacity + position of a dense cache.
+ *
+ *   rows       requests, 1 .. 4096: rows of the block table (at least)
+ *   tokens     N, 0 .. 2^30: entries of slots, positions and row_of. Entries behind
+ *              the sum of q_len get slot -1, position 0 and row -1; tokens behind
+ *              the N-th are left out
+ *   pages      the paged pool, or NULL: a dense cache of cache_capacity tokens a
+ *              row (rows * cache_capacity < 2^31; not used with pages)
+ *   q_len, total_len   DEVICE [rows] int32; the new tokens count in total_len. A
+ *              q_len below 0 is taken as 0
+ *   slots      [N] int32: the row, or -1 where the position lies outside the
+ *              table or cache, or the table's entry outside the pool
+ *   positions, row_of  [N] int32, or NULL (a position below 0 is given as 0)
+ *   first      [rows + 1] int32, or NULL: the running sums, at most N each
+ * No result overlaps an input or another result. One kernel; no workspace.
+ */
+int dsa_slot_map(int rows, int64_t tokens, const dsa_kv_pages* pages, int32_t cache_capacity,
+                 const int32_t* q_len, const int32_t* total_len, int32_t* slots, int32_t* positions,
+                 int32_t* row_of, int32_t* first, void* stream);
+
+/*
+ * dsa_rope_axes_append -- what dsa_rmsnorm_rotary and the append do, for a
+ * packed step of unequal requests and positions with several axes (time, height
+ * and width of an image's or video's patches; the same number on every axis for
+ * text). With r = 2 * (the sum of sections), a(i) the axis of rotary pair i, and
+ * x a head vector of token n, first normalised where gamma is given:
+ *     x           = x * gamma / sqrt(mean(x^2) + eps)
+ *     y_i         = x_i * cos[p, i] - x_{i+r/2} * sin[p, i]     (i < r/2)
+ *     y_{i+r/2}   = x_{i+r/2} * cos[p, i] + x_i * sin[p, i]
+ *     y_i         = x_i                                        (i >= r)
+ * with p = positions of token n on axis a(i), clamped to 0 .. max_pos - 1. The
+ * queries go to q_out; the keys, rounded to q_dtype, and the values go to row
+ * slots[n] of the caches, converted or quantised as dsa_cache_append does it
+ * (INT8: absmax / 127 per token and head). A token whose slot is negative, or
+ * cache_rows or above, changes no cache; its queries are still turned. Of two
+ * tokens of the same slot either may be the one that is kept.
+ *
+ *   tokens        N >= 0 (0: nothing is launched)
+ *   num_q_heads, num_kv_heads   >= 0, not both 0
+ *   head_dim      must be 128
+ *   axes          1 .. DSA_MAX_AXES; sections[a]: the pairs that turn by axis
+ *                 a's position, 1 .. 64 in all
+ *   in_turn       0: sections[0] pairs of axis 0 come first, then those of axis
+ *                 1 ...; else pairs are dealt out to the axes in turn while they
+ *                 have some left
+ *   max_pos       rows of the cos / sin caches
+ *   eps           finite, >= 0
+ *   q_dtype       DSA_BF16 or DSA_FP16 (q, k, v and q_out)
+ *   kv_dtype      DSA_BF16 (BF16 vectors only), DSA_FP16 or DSA_INT8
+ *   cos_dtype     DSA_FP32 or DSA_BF16
+ *   q_stride, k_stride, v_stride, out_stride   elements between two tokens'
+ *                 vectors: a multiple of 8 that holds them, or 0 (they lie
+ *                 together). So q, k and v may be columns of one projection
+ *   pos_stride    elements between two axes' positions; 0: one for all axes
+ *   cache_rows    token rows of the caches, below 2^31
+ *
+ *   q [N, Hq, 128], k, v [N, Hkv, 128]   q_dtype, 16-byte aligned
+ *   gamma_q, gamma_k   [128] fp32, or NULL: no norm
+ *   cos_cache, sin_cache   [max_pos, r/2] cos_dtype
+ *   positions     [axes, N] int32 (see pos_stride)
+ *   slots         [N] int32 (dsa_slot_map)
+ *   q_out         [N, Hq, 128]: may be q itself, in place
+ *   k_cache, v_cache   [cache_rows, Hkv, 128] kv_dtype, 16-byte aligned
+ *   k_scale, v_scale   [cache_rows, Hkv] fp32 iff kv_dtype is INT8
+ * All arithmetic in fp32, rounded once. Nothing else may overlap what is
+ * written. Values must be finite. One kernel; no workspace.
+ */
+#define DSA_MAX_AXES 4
+typedef struct dsa_axes_problem {
+  int64_t tokens;
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  int64_t pos_stride;
+  int64_t cache_rows;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t axes;
+  int32_t sections[DSA_MAX_AXES];
+  int32_t in_turn;
+  int32_t max_pos;
+  float eps;
+  int32_t q_dtype;
+  int32_t kv_dtype;
+  int32_t cos_dtype;
+} dsa_axes_problem;
+
+int dsa_rope_axes_append(const dsa_axes_problem* p, const void* q, const void* k, const void* v,
+                         const float* gamma_q, const float* gamma_k, const void* cos_cache,
+                         const void* sin_cache, const int32_t* positions, const int32_t* slots,
+                         void* q_out, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                         void* stream);
+
+/*
+ * dsa_add_rmsnorm -- the work between two layers in one pass over the rows:
+ *     h = x + residual            (rounded to x_dtype; residual NULL: h = x)
+ *     y = h * gamma / sqrt(mean(h^2) + eps)
+ * h is what is stored and what is normalised. y is rounded to 16 bits, or, with
+ * top = 448 for FP8_E4M3 and 127 for INT8, given as codes and scales:
+ *     scale = absmax(y) / top     of a row, or of every 128 elements of it
+ *     code  = y / scale           rounded to the nearest (zeros: scale 0, codes 0)
+ *
+ *   rows          0 .. 2^31 - 1 (0: nothing is launched)
+ *   hidden        1 .. 32768
+ *   scale_group   0: a scale per row; 128: one per 128 elements (the last group
+ *                 may be shorter). 0 for a 16-bit y
+ *   x_dtype       DSA_BF16, DSA_FP16 or DSA_FP32 (x, residual and h)
+ *   y_dtype       DSA_BF16, DSA_FP16, DSA_FP8_E4M3 or DSA_INT8
+ *   x_stride, residual_stride, h_stride, y_stride   elements between two rows,
+ *                 at least hidden (0: hidden)
+ *   eps           finite, >= 0
+ *
+ *   x, residual, h   [rows, hidden]; residual NULL: no addition; h NULL: the sum
+ *                 is not stored
+ *   gamma         [hidden] fp32
+ *   y             [rows, hidden] y_dtype
+ *   scale         [rows, 1 or ceil(hidden / 128)] fp32, iff y is of 8 bits
+ * h may be x or the residual, and y either of them (of its element size), in
+ * place; other overlaps of their extents are refused. All arithmetic in fp32,
+ * whatever the size of the values (a row's squares neither overflow nor
+ * vanish); sums must stay finite in x_dtype. With eps = 0 a row of zeros gives
+ * NaN, as the formula does (8 bits: unspecified). Rows whose bases and strides
+ * allow vectors of 8 elements, with hidden a multiple of 8, are moved in such.
+ * One kernel; no workspace.
+ */
+typedef struct dsa_norm_problem {
+  int64_t rows;
+  int64_t x_stride, residual_stride, h_stride, y_stride;
+  int32_t hidden;
+  int32_t scale_group;
+  int32_t x_dtype;
+  int32_t y_dtype;
+  float eps;
+} dsa_norm_problem;
+
+int dsa_add_rmsnorm(const dsa_norm_problem* p, const void* x, const void* residual, const float* gamma,
+                    void* h, void* y, float* scale, void* stream);
+
+/*
  * Synchronises `stream`, then copies the device status word from the
  * workspace to *status_out (0 = no device-side problem; bit 0 = a bounded
  * wait ran out; bit 1 = a gathered key's block-table entry lay outside the
@@ -735,7 +902,8 @@ int dsa_version(void);
  * dsa_last_launches -- the kernels that the last dsa_index_scores, dsa_topk,
  * dsa_topk_noalloc, dsa_cache_append, dsa_rmsnorm_rotary, dsa_rope_append,
  * dsa_sparse_attn_decode, dsa_sparse_attn_prefill, dsa_full_attn (or its
- * _paged form), dsa_pages_update, dsa_pages_compact or dsa_beam_select call on
+ * _paged or _sinks form), dsa_pages_update, dsa_pages_compact, dsa_beam_select,
+ * dsa_slot_map, dsa_rope_axes_append, dsa_add_rmsnorm or dsa_sample call on
  * this host thread enqueued. Returns how many (0 after a call that failed
  * before launching); when buf is not NULL, writes their names in launch order,
  * comma-separated and NUL-terminated, truncated to fit buflen bytes. No

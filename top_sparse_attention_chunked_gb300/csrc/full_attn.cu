@@ -118,6 +118,7 @@ struct FullParams {
   float* partial;
   int part_rows;
   int B, Hq, Hkv, G, cap, window;
+  int sinks;            // keys from a sequence's first on that stay visible beside the window
   int q_dtype, out_dtype;
   float scale_log2, softcap;
   float cap_log2, cap_inv;      // of softcap > 0: softcap * log2 e, and 1 over it
@@ -135,18 +136,36 @@ struct FullParams {
 };
 
 // One item: rows [row0, row0 + nrows) of (sequence b, KV head g) and the key
-// tiles [tile0, tile0 + ntiles) that some row of it sees.
+// tiles that some row of it sees: ntiles from tile0 on, without the `jump` tiles
+// that lie between its first `head` ones (of keys that stay visible) and its window.
 struct Item {
   int b, g, row0, nrows, tile0, ntiles;
   int q0, first;        // the sequence's first query row, its first key
   int past;             // position of the sequence's first new token
-  int lo, hi;           // keys that some row sees
+  int lo, hi;           // keys that some row sees: lo .. hi - 1 and first .. send - 1
+  int send, head, jump;
+  template <bool SINKS>
+  __device__ __forceinline__ int key(int t) const {            // first key of the item's tile t
+    return (tile0 + t + (SINKS && t >= head ? jump : 0)) * kTileKeys;
+  }
+  // whether some row of it sees a key, or all keys of a tile
+  template <bool SINKS>
+  __device__ __forceinline__ bool sees(int k) const {
+    return (k >= lo && k < hi) || (SINKS && k >= first && k < send);
+  }
+  template <bool SINKS>
+  __device__ __forceinline__ bool sees_tile(int k) const {
+    return (k >= lo && k + kTileKeys <= hi) || (SINKS && k >= first && k + kTileKeys <= send);
+  }
 };
 
 __host__ __device__ __forceinline__ int imax(int a, int b) { return a > b ? a : b; }
 __host__ __device__ __forceinline__ int imin(int a, int b) { return a < b ? a : b; }
 
-// (b: a sequence no later than the item's)
+// (b: a sequence no later than the item's. SINKS, here and below: calls with keys
+// that stay visible have kernels of their own, for the others would pay for them:
+// 4 x 8 tokens on 32,768, 24/2 heads: 41.0 instead of 37.5 us.)
+template <bool SINKS>
 __host__ __device__ __forceinline__ Item make_item(const FullParams& p, int i, int b) {
   Item w;
   while (i >= p.seq[b + 1].item0) ++b;
@@ -166,8 +185,20 @@ __host__ __device__ __forceinline__ Item make_item(const FullParams& p, int i, i
   w.lo = q.first;
   if (p.window > 0) w.lo = imax(w.lo, w.past + w.row0 / p.G - p.window + 1);
   w.lo = imin(w.lo, w.hi);
+  w.send = w.head = w.jump = 0;
+  if (SINKS && p.sinks > 0) {
+    w.send = imin(w.first + p.sinks, w.hi);
+    if (w.send >= w.lo) w.lo = imin(w.lo, w.first);
+  }
   w.tile0 = w.lo / kTileKeys;
   w.ntiles = w.lo < w.hi ? (w.hi + kTileKeys - 1) / kTileKeys - w.tile0 : 0;
+  if (SINKS && w.send > w.first && w.first < w.lo) {   // tiles before the window's
+    const int t = w.first / kTileKeys, end = imin((w.send + kTileKeys - 1) / kTileKeys, w.tile0);
+    w.head = end - t;
+    w.jump = w.tile0 - end;
+    w.ntiles += w.head;
+    w.tile0 = t;
+  }
   return w;
 }
 
@@ -179,6 +210,7 @@ struct Segment {
   int part;             // where a partial state goes
 };
 
+template <bool SINKS>
 struct Walk {
   int item, tile, b, end_item, end_tile;
   __device__ __forceinline__ explicit Walk(const FullParams& p) {
@@ -191,7 +223,7 @@ struct Walk {
   }
   __device__ __forceinline__ bool next(const FullParams& p, Segment* s) {
     if (item > end_item || (item == end_item && tile >= end_tile)) return false;
-    s->w = make_item(p, item, b);
+    s->w = make_item<SINKS>(p, item, b);
     b = s->w.b;
     s->t0 = tile;
     s->t1 = item == end_item ? end_tile : s->w.ntiles;
@@ -436,7 +468,7 @@ __device__ __forceinline__ bool for_tiles(const Segment& s, F&& f) {
 // issued when a raw stage is free, so V of tile i + 4 at least has been widened,
 // so K of tile i + 3 has been consumed, and its product was issued after the
 // weights of tile i + 1.
-template <bool INT8>
+template <bool INT8, bool SINKS>
 __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                           FullBars* bars, uint8_t* ring, float* scales,
                                           volatile int* abort_flag) {
@@ -452,13 +484,13 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
   RingPos pos;
   uint32_t fixes = 0, tiles = 0;
   bool bad = false, begin = true;
-  Walk walk(p);
+  Walk<SINKS> walk(p);
   Segment s;
   while (walk.next(p, &s)) {
     if (s.t0 == s.t1) continue;
     // cache rows of 32 tiles, one a lane, looked up together and 32 tiles ahead
     const auto look_up = [&](int t) {
-      return t < s.t1 ? cache_row(p.pg, s.w.b, p.cap, (s.w.tile0 + t) * kTileKeys, &bad) : 0;
+      return t < s.t1 ? cache_row(p.pg, s.w.b, p.cap, s.w.key<SINKS>(t), &bad) : 0;
     };
     int base = s.t0;
     long long rows = look_up(base + lane), rows_next = look_up(base + 32 + lane);
@@ -475,7 +507,7 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
     const bool ok = for_tiles(s, [&](int t, bool is_v) {
       const int st = pos.stage;
       if (pos.round > 0 && !warp_wait(&empty[st], (pos.round - 1) & 1, abort_flag)) return false;
-      const int key = (s.w.tile0 + t) * kTileKeys;
+      const int key = s.w.key<SINKS>(t);
       // (K runs up to two tiles ahead of V: the window moves when V has left it)
       if (is_v && t >= base + 32) {
         base += 32;
@@ -487,8 +519,7 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
       uint8_t* dst = ring + st * kBytes;
       const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
       // rows of V that no query of the item sees
-      const int lo = imax(0, s.w.lo - key), hi = imin(kTileKeys, s.w.hi - key);
-      const bool fix = !INT8 && is_v && (lo > 0 || hi < kTileKeys);
+      const bool fix = !INT8 && is_v && !s.w.sees_tile<SINKS>(key);
       uint64_t* bar = fix ? &bars->fix : &full[st];
       if (lane == 0) {
         mbar_arrive_expect_tx(bar, kBytes);
@@ -501,7 +532,7 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
 #pragma unroll
           for (int i = 0; i < kTileKeys / 32; ++i) {
             const int r = i * 32 + lane;
-            const bool in = r >= lo && r < hi;
+            const bool in = s.w.sees<SINKS>(key + r);
             const long long at = in ? (first + r) * p.Hkv + s.w.g : 0;
             cp_async4(sc + r, p.k_scale + at, in);
             cp_async4(sc + kTileKeys + r, p.v_scale + at, in);
@@ -514,7 +545,7 @@ __device__ __forceinline__ void load_role(const FullParams& p, const CUtensorMap
       if (fix) {
         if (!warp_wait(&bars->fix, fixes++ & 1, abort_flag)) return false;
         for (int r = 0; r < kTileKeys; ++r) {
-          if (r >= lo && r < hi) continue;
+          if (s.w.sees<SINKS>(key + r)) continue;
           if (lane < 16)
             *reinterpret_cast<uint4*>(dst + (lane >> 3) * kBlk + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
@@ -583,11 +614,12 @@ __device__ __forceinline__ void widen_tile(const uint8_t* src, uint8_t* dst, con
   }
 }
 
+template <bool SINKS>
 __device__ __forceinline__ void widen_role(const FullParams& p, FullBars* bars, uint8_t* ring, const uint8_t* raw,
                                            int tid, volatile int* abort_flag) {
   RingPos from, to;
   const WidenAt at(tid);
-  Walk walk(p);
+  Walk<SINKS> walk(p);
   Segment s;
   while (walk.next(p, &s)) {
     const bool ok = for_tiles(s, [&](int, bool is_v) {
@@ -615,7 +647,7 @@ __device__ __forceinline__ void widen_role(const FullParams& p, FullBars* bars, 
 template <bool QK_F16, bool INT8>
 __host__ __device__ constexpr bool split_p() { return QK_F16 && INT8; }
 
-template <bool QK_F16, bool PV_F16, bool INT8>
+template <bool QK_F16, bool PV_F16, bool INT8, bool SINKS>
 __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint32_t q_addr,
                                          uint32_t ring_addr, volatile int* abort_flag) {
   constexpr int stages = INT8 ? kRing8 : kRing16;
@@ -649,7 +681,7 @@ __device__ __forceinline__ void mma_role(const FullParams& p, FullBars* bars, ui
     return true;
   };
   const auto release = [&](const RingPos& q) { tc_commit(&bars->empty[q.stage]); };
-  Walk walk(p);
+  Walk<SINKS> walk(p);
   Segment s;
   bool ok = true;
   while (ok && walk.next(p, &s)) {
@@ -865,7 +897,7 @@ __device__ __forceinline__ void write_no_key(const FullParams& p, const Item& w,
 // exponentials are formed with the running maximum as it was, next to the
 // part's own maximum; only where that calls for raising the former are they
 // formed again.
-template <bool QK_F16, bool PV_F16, bool INT8, bool MOD>
+template <bool QK_F16, bool PV_F16, bool INT8, bool MOD, bool SINKS>
 __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars, uint32_t tmem, uint8_t* sQ,
                                              const float* scales, int slot, volatile int* abort_flag) {
   const int tid = threadIdx.x & 127, lane = tid & 31, warp_row = tid & ~31;
@@ -876,7 +908,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
   const uint32_t lane_addr = static_cast<uint32_t>(warp_row) << 16;
   const uint32_t tS = tmem + lane_addr + slot * 128, tO = tmem + lane_addr + 256 + slot * 128;
   uint32_t ns = 0, no = 0, nml = 0, nseg = 0, tile_seq = 0;
-  Walk walk(p);
+  Walk<SINKS> walk(p);
   Segment s;
   while (walk.next(p, &s)) {
     const SlotWork x = slot_work(s, slot);
@@ -965,7 +997,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
     bool ok = true;
     for (int j = 0; j < x.n; ++j) {
       const int t = x.first + j * x.step;
-      const int key0 = (s.w.tile0 + t) * kTileKeys;
+      const int key0 = s.w.key<SINKS>(t);
       if (!warp_wait(&bars->s_full[slot], ns & 1, abort_flag)) {
         ok = false;
         break;
@@ -979,7 +1011,10 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
           break;
         }
       }
-      const bool masked = key0 + kTileKeys - 1 > pos0 || key0 < lo1;
+      // (first and sinks from the parameters, not from registers that would have to spill)
+      const bool head = SINKS && key0 < p.seq[s.w.b].first + p.sinks;   // keys that stay visible among the tile's
+      const bool masked = key0 + kTileKeys - 1 > pos0 ||
+                          (key0 < lo1 && !(head && key0 >= p.seq[s.w.b].first && key0 + kTileKeys <= p.seq[s.w.b].first + p.sinks));
       const float* sc = scales + ((tile_seq + (t - s.t0)) % kScaleRing) * 2 * kTileKeys;
 #pragma unroll 1
       for (int h = 0; h < kTileKeys / kCols; ++h) {
@@ -1014,9 +1049,16 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
           }
           if (masked) {
             const int a = lo - first, b = pos - first;   // columns a .. b are visible
+            if (head) {                                  // and those of the first keys up to b
+              const int c0 = p.seq[s.w.b].first - first, n = imin(p.sinks, b + 1 - c0);
 #pragma unroll
-            for (int i = 0; i < kCols; ++i)
-              if (i < a || i > b) z[i] = -INFINITY;
+              for (int i = 0; i < kCols; ++i)
+                if ((i < a || i > b) && static_cast<unsigned>(i - c0) >= static_cast<unsigned>(imax(n, 0))) z[i] = -INFINITY;
+            } else {
+#pragma unroll
+              for (int i = 0; i < kCols; ++i)
+                if (i < a || i > b) z[i] = -INFINITY;
+            }
           }
           uint32_t w[kCols / 2], wl[kSplit ? kCols / 2 : 1];
           float2 sum[2];
@@ -1191,7 +1233,7 @@ __device__ __forceinline__ void softmax_role(const FullParams& p, FullBars* bars
   }
 }
 
-template <bool QK_F16, bool PV_F16, bool INT8, bool MOD>
+template <bool QK_F16, bool PV_F16, bool INT8, bool MOD, bool SINKS>
 __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
     full_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ FullParams p) {
@@ -1242,19 +1284,19 @@ __global__ void __launch_bounds__(INT8 ? kThreads8 : kThreads16, 1)
   pdl_trigger();
   if (warp < 8) {
     if constexpr (INT8) regs_up<kSoftRegs8>();
-    softmax_role<QK_F16, PV_F16, INT8, MOD>(p, bars, tmem, sQ, scales, warp >> 2, abort_flag);
+    softmax_role<QK_F16, PV_F16, INT8, MOD, SINKS>(p, bars, tmem, sQ, scales, warp >> 2, abort_flag);
   } else if (warp < 12) {
     if constexpr (INT8) regs_down<kMiscRegs8>();
     if (warp == 8) {
       if ((threadIdx.x & 31) == 0)
-        mma_role<QK_F16, PV_F16, INT8>(p, bars, tmem, smem_u32(sQ), smem_u32(ring), abort_flag);
+        mma_role<QK_F16, PV_F16, INT8, SINKS>(p, bars, tmem, smem_u32(sQ), smem_u32(ring), abort_flag);
     } else if (warp == 9) {
-      load_role<INT8>(p, tm_k, tm_v, bars, INT8 ? raw : ring, scales, abort_flag);
+      load_role<INT8, SINKS>(p, tm_k, tm_v, bars, INT8 ? raw : ring, scales, abort_flag);
     }
   } else {
     if constexpr (INT8) {
       regs_down<kWidenRegs>();
-      widen_role(p, bars, ring, raw, threadIdx.x - kThreads16, abort_flag);
+      widen_role<SINKS>(p, bars, ring, raw, threadIdx.x - kThreads16, abort_flag);
     }
   }
   tc_fence_before();
@@ -1306,6 +1348,7 @@ constexpr size_t few_smem() {
 }
 
 // One stage holds a tile's keys, values and scales.
+template <bool SINKS>
 __device__ __forceinline__ void few_load(const FullParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                          FewBars* bars, uint8_t* ring, volatile int* abort_flag) {
   const int lane = threadIdx.x & 31;
@@ -1315,14 +1358,14 @@ __device__ __forceinline__ void few_load(const FullParams& p, const CUtensorMap&
   }
   RingPos pos;
   bool bad = false, ok = true;
-  Walk walk(p);
+  Walk<SINKS> walk(p);
   Segment s;
   while (ok && walk.next(p, &s)) {
     long long rows = 0;
     for (int t = s.t0; t < s.t1; ++t) {
       // cache rows of 32 tiles, one a lane
       if (((t - s.t0) & 31) == 0)
-        rows = t + lane < s.t1 ? cache_row(p.pg, s.w.b, p.cap, (s.w.tile0 + t + lane) * kTileKeys, &bad) : 0;
+        rows = t + lane < s.t1 ? cache_row(p.pg, s.w.b, p.cap, s.w.key<SINKS>(t + lane), &bad) : 0;
       const long long first = __shfl_sync(0xffffffffu, rows, (t - s.t0) & 31);
       if (pos.round > 0 && !warp_wait(&bars->empty[pos.stage], (pos.round - 1) & 1, abort_flag)) {
         ok = false;
@@ -1336,11 +1379,11 @@ __device__ __forceinline__ void few_load(const FullParams& p, const CUtensorMap&
         tma_load_3d(dst + kTile8, &tm_v, bar, 0, s.w.g, static_cast<int>(first));
       }
       float* sc = reinterpret_cast<float*>(dst + 2 * kTile8);
-      const int key = (s.w.tile0 + t) * kTileKeys;
+      const int key = s.w.key<SINKS>(t);
 #pragma unroll
       for (int i = 0; i < kTileKeys / 32; ++i) {
         const int r = i * 32 + lane;
-        const bool in = key + r >= s.w.lo && key + r < s.w.hi;
+        const bool in = s.w.sees<SINKS>(key + r);
         const long long at = in ? (first + r) * p.Hkv + s.w.g : 0;
         cp_async4(sc + r, p.k_scale + at, in);
         cp_async4(sc + kTileKeys + r, p.v_scale + at, in);
@@ -1367,13 +1410,13 @@ __device__ __forceinline__ void few_load(const FullParams& p, const CUtensorMap&
 }
 
 // SPLIT: the weights go as BF16 pairs (an FP16 query, see split_p). MOD as above.
-template <bool SPLIT, bool MOD>
+template <bool SPLIT, bool MOD, bool SINKS>
 __device__ __forceinline__ void few_role(const FullParams& p, FewBars* bars, const uint8_t* ring, float* join,
                                          volatile int* abort_flag) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const int perm = 4 * (g & 1) + (g >> 1);             // key row, and 16-byte column, of g
   uint32_t before = 0;                                  // tiles of the segments before
-  Walk walk(p);
+  Walk<SINKS> walk(p);
   Segment s;
   while (walk.next(p, &s)) {
     // queries: rows g and g + 8, this thread's 32 dims
@@ -1459,7 +1502,7 @@ __device__ __forceinline__ void few_role(const FullParams& p, FewBars* bars, con
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) z[n][e] *= sc[8 * n + 4 * (e & 1)];
-      const int key0 = (s.w.tile0 + s.t0 + static_cast<int>(tile)) * kTileKeys;
+      const int key0 = s.w.key<SINKS>(s.t0 + static_cast<int>(tile));
       if constexpr (MOD) {   // to log2 units
 #pragma unroll
         for (int n = 0; n < 2; ++n)
@@ -1478,7 +1521,8 @@ __device__ __forceinline__ void few_role(const FullParams& p, FewBars* bars, con
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = key0 + first + 8 * n + 4 * (e & 1) + c;
-            if (key < lo[e >> 1] || key > at[e >> 1]) z[n][e] = -INFINITY;
+            const bool stays = SINKS && key >= s.w.first && key < s.w.send;
+            if ((key < lo[e >> 1] && !stays) || key > at[e >> 1]) z[n][e] = -INFINITY;
           }
       }
       float top[2];
@@ -1595,7 +1639,7 @@ __device__ __forceinline__ void few_role(const FullParams& p, FewBars* bars, con
   }
 }
 
-template <bool SPLIT, bool MOD>
+template <bool SPLIT, bool MOD, bool SINKS>
 __global__ void __launch_bounds__(kFewThreads, 1)
     full_attn_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ FullParams p) {
@@ -1620,10 +1664,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   pdl_trigger();
   if (threadIdx.x < 32 * kFewWarps) {
     regs_up<kFewRegs>();
-    few_role<SPLIT, MOD>(p, bars, ring, join, &bars->abort_flag);
+    few_role<SPLIT, MOD, SINKS>(p, bars, ring, join, &bars->abort_flag);
   } else {
     regs_down<kFewLoadRegs>();
-    if (threadIdx.x < 32 * (kFewWarps + 1)) few_load(p, tm_k, tm_v, bars, ring, &bars->abort_flag);
+    if (threadIdx.x < 32 * (kFewWarps + 1)) few_load<SINKS>(p, tm_k, tm_v, bars, ring, &bars->abort_flag);
   }
   __syncthreads();
   if (threadIdx.x == 0)
@@ -1664,7 +1708,7 @@ __global__ void __launch_bounds__(kMergeSet * kMaxGroups)
   const int c0 = mp.first_cta[blockIdx.y], c1 = mp.last_cta[blockIdx.y];
   // the item is the one block c1's run begins in
   const FullParams::Run run = p.run[c1];
-  const Item w = make_item(p, run.item, run.b);
+  const Item w = make_item<false>(p, run.item, run.b);
   const int pr = blockIdx.x * kMergeRows + rr;
   pdl_wait();
   float m = -INFINITY, l = 0.f;
@@ -1798,13 +1842,14 @@ constexpr int kCostRows = 4, kCostKeys = 3, kCostItem = 20, kCostEmpty = 4;
 // are one.)
 constexpr size_t kPartialAt = 256 + ((kMaxCtas * 4 + 255) / 256) * 256;
 
-int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp, size_t* bytes) {
+int schedule(const dsa_full_problem* p, int sinks, int sms, FullParams* fp, MergeParams* mp, size_t* bytes) {
   fp->B = p->batch;
   fp->Hq = p->num_q_heads;
   fp->Hkv = p->num_kv_heads;
   fp->G = p->num_q_heads / p->num_kv_heads;
   fp->cap = p->cache_capacity;
   fp->window = p->window;
+  fp->sinks = p->window > 0 ? imin(sinks, DSA_MAX_CONTEXT) : 0;
   fp->part_rows = 0;
   for (int b = 0; b < p->batch; ++b) {
     const long long rows = static_cast<long long>(p->q_len[b]) * fp->G;
@@ -1819,7 +1864,7 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
   const auto item_cost = [](const Item& w) { return w.ntiles > 0 ? kCostItem : kCostEmpty; };
   long long cost = 0, units = 0;
   for (int i = 0, at = 0; i < items; ++i) {
-    const Item w = make_item(*fp, i, at);
+    const Item w = make_item<true>(*fp, i, at);
     at = w.b;
     cost += item_cost(w) + static_cast<long long>(w.ntiles) * (w.nrows > kSlotRows ? kCostRows : kCostKeys);
     units += imax(w.ntiles, 1);
@@ -1833,7 +1878,7 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
     // 9.5 us, against 10.1 with the cuts below, of which some fall into an item's
     // cost and leave other blocks two tiles; 4 x 600 keys 9.3 against 10.9)
     for (int i = 0, b = 0; i < items; ++i) {
-      const Item w = make_item(*fp, i, b);
+      const Item w = make_item<true>(*fp, i, b);
       b = w.b;
       for (int t = 0; t < imax(w.ntiles, 1); ++t) fp->run[blocks++] = FullParams::Run{i, t, b, 0};
     }
@@ -1841,7 +1886,7 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
     // run k begins where the costs reach k / want of their sum
     long long at = 0;
     for (int i = 0, b = 0, k = 0; i < items; ++i) {
-      const Item w = make_item(*fp, i, b);
+      const Item w = make_item<true>(*fp, i, b);
       b = w.b;
       const int unit = w.nrows > kSlotRows ? kCostRows : kCostKeys;
       const long long end = at + item_cost(w) + static_cast<long long>(w.ntiles) * unit;
@@ -1873,42 +1918,44 @@ int schedule(const dsa_full_problem* p, int sms, FullParams* fp, MergeParams* mp
   return blocks;
 }
 
-// Launches one of two kernels of a family (with and without MOD). Where warps
+// Launches one of the four kernels of a family (with and without MOD and SINKS). Where warps
 // change their register counts, those must fit into what the block is launched
 // with: a warp that asks for more would wait for ever.
 template <typename K>
-cudaError_t launch_one(const char* name, K* const (&kernels)[2], bool mod, std::atomic<int> (&regs)[2], int need, int blocks,
+cudaError_t launch_one(const char* name, K* const (&kernels)[4], int which, std::atomic<int> (&regs)[4], int need, int blocks,
                        int threads, size_t smem, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const FullParams& fp,
                        cudaStream_t st) {
-  K* const kern = kernels[mod];
+  K* const kern = kernels[which];
   cudaError_t e = set_max_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  if (need > 0 && regs[mod].load(std::memory_order_relaxed) == 0) {
+  if (need > 0 && regs[which].load(std::memory_order_relaxed) == 0) {
     cudaFuncAttributes a;
     if ((e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(kern))) != cudaSuccess) return e;
     if (a.numRegs * threads < need) return cudaErrorInvalidConfiguration;
-    regs[mod].store(a.numRegs, std::memory_order_relaxed);
+    regs[which].store(a.numRegs, std::memory_order_relaxed);
   }
   return launch_kernel(name, kern, dim3(blocks), dim3(threads), smem, st, false, tm_k, tm_v, fp);
 }
 
 template <bool QK_F16, bool PV_F16, bool INT8>
-cudaError_t launch_full(bool mod, int blocks, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const FullParams& fp,
+cudaError_t launch_full(int which, int blocks, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const FullParams& fp,
                         cudaStream_t st) {
-  static std::atomic<int> regs[2];
+  static std::atomic<int> regs[4];
   using K = void(const CUtensorMap, const CUtensorMap, const FullParams);
-  K* const kernels[2] = {full_attn_kernel<QK_F16, PV_F16, INT8, false>, full_attn_kernel<QK_F16, PV_F16, INT8, true>};
-  return launch_one("full_attn_kernel", kernels, mod, regs, INT8 ? kRegs8 : 0, blocks, INT8 ? kThreads8 : kThreads16,
+  K* const kernels[4] = {full_attn_kernel<QK_F16, PV_F16, INT8, false, false>, full_attn_kernel<QK_F16, PV_F16, INT8, true, false>,
+                         full_attn_kernel<QK_F16, PV_F16, INT8, false, true>, full_attn_kernel<QK_F16, PV_F16, INT8, true, true>};
+  return launch_one("full_attn_kernel", kernels, which, regs, INT8 ? kRegs8 : 0, blocks, INT8 ? kThreads8 : kThreads16,
                     full_smem<INT8>(), tm_k, tm_v, fp, st);
 }
 
 template <bool SPLIT>
-cudaError_t launch_few(bool mod, int blocks, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const FullParams& fp,
+cudaError_t launch_few(int which, int blocks, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const FullParams& fp,
                        cudaStream_t st) {
-  static std::atomic<int> regs[2];
+  static std::atomic<int> regs[4];
   using K = void(const CUtensorMap, const CUtensorMap, const FullParams);
-  K* const kernels[2] = {full_attn_few_kernel<SPLIT, false>, full_attn_few_kernel<SPLIT, true>};
-  return launch_one("full_attn_few_kernel", kernels, mod, regs, kFewLaunchRegs, blocks, kFewThreads, few_smem(), tm_k, tm_v,
+  K* const kernels[4] = {full_attn_few_kernel<SPLIT, false, false>, full_attn_few_kernel<SPLIT, true, false>,
+                         full_attn_few_kernel<SPLIT, false, true>, full_attn_few_kernel<SPLIT, true, true>};
+  return launch_one("full_attn_few_kernel", kernels, which, regs, kFewLaunchRegs, blocks, kFewThreads, few_smem(), tm_k, tm_v,
                     fp, st);
 }
 
@@ -1926,10 +1973,11 @@ void cap_fold(float softcap, FullParams* fp) {
   fp->cap_ys = fold ? ys : 1.0f;
 }
 
-int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* q, const void* k, const void* v,
+int full_call(const dsa_full_problem* p, int sinks, const dsa_kv_pages* pages, const void* q, const void* k, const void* v,
               const float* ks, const float* vs, const float* slopes, void* out, float* lse, void* ws,
               size_t ws_bytes, void* stream) {
   if (int rc = check_full(p)) return rc;
+  if (sinks < 0) return report_errorf(DSA_ERR_INVALID_ARG, "sinks %d < 0", sinks);
   Paging pg{};
   if (pages)
     if (int rc = check_full_pages(p, pages, &pg)) return rc;
@@ -1949,7 +1997,7 @@ int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* 
   FullParams fp{};
   MergeParams mp;
   size_t need = 0;
-  const int blocks = schedule(p, device ? sms : kMaxCtas, &fp, &mp, &need);
+  const int blocks = schedule(p, sinks, device ? sms : kMaxCtas, &fp, &mp, &need);
   if (int rc = check_call_workspace(ws, ws_bytes, need)) return rc;
   if (!device) return current_device(&sms);
   if (fp.seq[p->batch].q0 == 0) {
@@ -1985,15 +2033,15 @@ int full_call(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* 
   mp.out_dtype = p->out_dtype;
   mp.blocks = blocks;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool mod = p->softcap > 0.0f || slopes != nullptr;
+  const int which = (p->softcap > 0.0f || slopes != nullptr ? 1 : 0) + (fp.sinks > 0 ? 2 : 0);
   cudaError_t e;
   if (p->kv_dtype == DSA_INT8 && fp.part_rows <= kFewRows)
-    e = p->q_dtype == DSA_FP16 ? launch_few<true>(mod, blocks, tm_k, tm_v, fp, st)
-                               : launch_few<false>(mod, blocks, tm_k, tm_v, fp, st);
-  else if (p->kv_dtype == DSA_BF16) e = launch_full<false, false, false>(mod, blocks, tm_k, tm_v, fp, st);
-  else if (p->kv_dtype == DSA_FP16) e = launch_full<true, true, false>(mod, blocks, tm_k, tm_v, fp, st);
-  else if (p->q_dtype == DSA_FP16) e = launch_full<true, false, true>(mod, blocks, tm_k, tm_v, fp, st);
-  else e = launch_full<false, false, true>(mod, blocks, tm_k, tm_v, fp, st);
+    e = p->q_dtype == DSA_FP16 ? launch_few<true>(which, blocks, tm_k, tm_v, fp, st)
+                               : launch_few<false>(which, blocks, tm_k, tm_v, fp, st);
+  else if (p->kv_dtype == DSA_BF16) e = launch_full<false, false, false>(which, blocks, tm_k, tm_v, fp, st);
+  else if (p->kv_dtype == DSA_FP16) e = launch_full<true, true, false>(which, blocks, tm_k, tm_v, fp, st);
+  else if (p->q_dtype == DSA_FP16) e = launch_full<true, false, true>(which, blocks, tm_k, tm_v, fp, st);
+  else e = launch_full<false, false, true>(which, blocks, tm_k, tm_v, fp, st);
   if (e == cudaSuccess) {
     const dim3 grid = mp.splits ? dim3((fp.part_rows + kMergeRows - 1) / kMergeRows, mp.splits) : dim3(1);
     e = launch_kernel("full_attn_merge_kernel", full_attn_merge_kernel, grid, dim3(kMergeSet * mp.groups), 0, st, true, fp, mp);
@@ -2012,7 +2060,9 @@ extern "C" size_t dsa_full_attn_workspace_size(const dsa_full_problem* p) {
   FullParams fp{};
   MergeParams mp;
   size_t bytes = 0;
-  schedule(p, kMaxCtas, &fp, &mp, &bytes);
+  dsa_full_problem all = *p;   // (whatever number of first keys stays visible)
+  all.window = 0;
+  schedule(&all, 0, kMaxCtas, &fp, &mp, &bytes);
   return bytes;
 }
 
@@ -2020,7 +2070,7 @@ extern "C" int dsa_full_attn(const dsa_full_problem* p, const void* q, const voi
                              const float* k_scale, const float* v_scale, const float* slopes, void* out,
                              float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   reset_launches();
-  return full_call(p, nullptr, q, k, v, k_scale, v_scale, slopes, out, lse, workspace, workspace_bytes, stream);
+  return full_call(p, 0, nullptr, q, k, v, k_scale, v_scale, slopes, out, lse, workspace, workspace_bytes, stream);
 }
 
 extern "C" int dsa_full_attn_paged(const dsa_full_problem* p, const dsa_kv_pages* pages, const void* q,
@@ -2029,5 +2079,13 @@ extern "C" int dsa_full_attn_paged(const dsa_full_problem* p, const dsa_kv_pages
                                    size_t workspace_bytes, void* stream) {
   reset_launches();
   if (!pages) return report_error(DSA_ERR_INVALID_ARG, "pages is NULL");
-  return full_call(p, pages, q, k, v, k_scale, v_scale, slopes, out, lse, workspace, workspace_bytes, stream);
+  return full_call(p, 0, pages, q, k, v, k_scale, v_scale, slopes, out, lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" int dsa_full_attn_sinks(const dsa_full_problem* p, int sinks, const dsa_kv_pages* pages, const void* q,
+                                   const void* k, const void* v, const float* k_scale, const float* v_scale,
+                                   const float* slopes, void* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  reset_launches();
+  return full_call(p, sinks, pages, q, k, v, k_scale, v_scale, slopes, out, lse, workspace, workspace_bytes, stream);
 }

@@ -22,9 +22,10 @@ LIB_PATH = os.path.join(_HERE, "libdsa.so")
 # mirrors include/dsa.h
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE = 0, 1, 2, 3
 DSA_ERR_MISALIGNED, DSA_ERR_CUDA, DSA_ERR_TIMEOUT, DSA_ERR_NO_DEVICE = 4, 5, 6, 7
-DSA_BF16, DSA_FP16, DSA_INT8, DSA_FP32 = 0, 1, 2, 3
+DSA_BF16, DSA_FP16, DSA_INT8, DSA_FP32, DSA_FP8_E4M3 = 0, 1, 2, 3, 4
 DSA_OP_INDEX_SCORES, DSA_OP_TOPK, DSA_OP_DECODE, DSA_OP_PREFILL = 0, 1, 2, 3
 DSA_MAX_BATCH = 64
+DSA_MAX_AXES = 4
 DSA_KERNEL_INDEXER, DSA_KERNEL_TOPK_HIST, DSA_KERNEL_TOPK_SELECT = 0, 1, 2
 DSA_KERNEL_TOPK_ROW, DSA_KERNEL_ATTENTION, DSA_KERNEL_APPEND = 3, 4, 5
 
@@ -38,11 +39,12 @@ EXPORTED = ["dsa_workspace_size", "dsa_index_scores", "dsa_topk",
             "dsa_sparse_attn_decode_aux", "dsa_set_wait_budget",
             "dsa_full_attn", "dsa_full_attn_paged", "dsa_full_attn_workspace_size",
             "dsa_pages_update", "dsa_pages_compact", "dsa_pages_workspace_size",
-            "dsa_beam_select", "dsa_beam_workspace_size"]
+            "dsa_beam_select", "dsa_beam_workspace_size", "dsa_full_attn_sinks", "dsa_slot_map",
+            "dsa_rope_axes_append", "dsa_add_rmsnorm"]
 
-_DT = {"bf16": DSA_BF16, "fp16": DSA_FP16, "int8": DSA_INT8, "fp32": DSA_FP32}
+_DT = {"bf16": DSA_BF16, "fp16": DSA_FP16, "int8": DSA_INT8, "fp32": DSA_FP32, "e4m3": DSA_FP8_E4M3}
 _TORCH_DT = {DSA_BF16: torch.bfloat16, DSA_FP16: torch.float16, DSA_INT8: torch.int8,
-             DSA_FP32: torch.float32}
+             DSA_FP32: torch.float32, DSA_FP8_E4M3: torch.float8_e4m3fn}
 
 
 class DsaKvPages(ctypes.Structure):
@@ -160,6 +162,46 @@ class DsaBeamProblem(ctypes.Structure):
     ]
 
 
+class DsaAxesProblem(ctypes.Structure):
+    """dsa_axes_problem (rotary positions with several axes, and the append)."""
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+        ("pos_stride", ctypes.c_int64),
+        ("cache_rows", ctypes.c_int64),
+        ("num_q_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("axes", ctypes.c_int32),
+        ("sections", ctypes.c_int32 * DSA_MAX_AXES),
+        ("in_turn", ctypes.c_int32),
+        ("max_pos", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("q_dtype", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("cos_dtype", ctypes.c_int32),
+    ]
+
+
+class DsaNormProblem(ctypes.Structure):
+    """dsa_norm_problem (residual addition and RMS norm)."""
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("x_stride", ctypes.c_int64),
+        ("residual_stride", ctypes.c_int64),
+        ("h_stride", ctypes.c_int64),
+        ("y_stride", ctypes.c_int64),
+        ("hidden", ctypes.c_int32),
+        ("scale_group", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
 class DsaError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{msg} (status {status})")
@@ -211,6 +253,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "dsa_full_attn_workspace_size": (sz, [PF]),
         "dsa_full_attn": (i32, [PF] + [vp] * 9 + [sz, vp]),
         "dsa_full_attn_paged": (i32, [PF, PG] + [vp] * 9 + [sz, vp]),
+        "dsa_full_attn_sinks": (i32, [PF, i32, PG] + [vp] * 9 + [sz, vp]),
+        "dsa_slot_map": (i32, [i32, ctypes.c_int64, PG, i32] + [vp] * 7),
+        "dsa_rope_axes_append": (i32, [ctypes.POINTER(DsaAxesProblem)] + [vp] * 15),
+        "dsa_add_rmsnorm": (i32, [ctypes.POINTER(DsaNormProblem)] + [vp] * 7),
         "dsa_pages_workspace_size": (sz, [PS]),
         "dsa_pages_update": (i32, [PS] + [vp] * 4 + [i32, PP] + [vp] * 4 + [sz, vp]),
         "dsa_pages_compact": (i32, [PS, i32, PP] + [vp] * 5 + [sz, vp]),
@@ -611,10 +657,11 @@ def alloc_full_attn_workspace(p: DsaFullProblem, device="cuda") -> torch.Tensor:
 
 
 def dsa_full_attn(p: DsaFullProblem, q, k, v, k_scale, v_scale, out, workspace, slopes=None, lse=None,
-                  stream=None, pages=None):
+                  stream=None, pages=None, sinks: int = 0):
     """Attention of the packed new tokens q [N, Hq, 128] (N = sum of q_len, or
     more: rows behind are left alone) over all cached keys; with `pages`
-    (make_pages) the caches are paged pools. lse [N, Hq] fp32 is optional."""
+    (make_pages) the caches are paged pools. lse [N, Hq] fp32 is optional. With a
+    window, the first `sinks` keys of every sequence stay visible beside it."""
     Hq, Hkv, lib, dev = p.num_q_heads, p.num_kv_heads, load_library(), _current_device()
     kvdt = _TORCH_DT[p.kv_dtype]
     rows = _cache_shapes(p, pages) + (Hkv,)
@@ -631,7 +678,9 @@ def dsa_full_attn(p: DsaFullProblem, q, k, v, k_scale, v_scale, out, workspace, 
                  (out, "out", _TORCH_DT[p.out_dtype], None), (lse, "lse", f32, None),
                  (workspace, "workspace", torch.uint8, None), (pages and pages._table, "block_table", None, None))
     args[9:] = workspace.numel(), _stream_here(dev, stream)
-    if pages is None:
+    if sinks:
+        _check(lib.dsa_full_attn_sinks(ctypes.byref(p), sinks, None if pages is None else ctypes.byref(pages), *args))
+    elif pages is None:
         _check(lib.dsa_full_attn(ctypes.byref(p), *args))
     else:
         _check(lib.dsa_full_attn_paged(ctypes.byref(p), ctypes.byref(pages), *args))
@@ -763,6 +812,114 @@ def dsa_beam_select(p: DsaBeamProblem, logits, scores, out_scores, out_tokens, o
               (out_scores, "out_scores", f32, out), (out_tokens, "out_tokens", i32, out),
               (out_parents, "out_parents", i32, out), (workspace, "workspace", torch.uint8, None))
     _check(lib.dsa_beam_select(ctypes.byref(p), logits.data_ptr(), *a, workspace.numel(), _stream_here(dev, stream)))
+
+
+def dsa_slot_map(q_len, total_len, slots, pages: Optional[DsaKvPages] = None, capacity: int = 0, positions=None,
+                 rows=None, first=None, stream=None):
+    """Cache rows (slots [N] int32, -1 behind the last token), positions, requests
+    (rows) and running sums (first [B + 1]) of a packed step's tokens from the
+    requests' lengths q_len, total_len [B] on the device. pages: make_pages, of at
+    least B rows; else a dense cache of `capacity` tokens a request."""
+    lib, dev, i32 = load_library(), _current_device(), torch.int32
+    n, tokens = q_len.numel(), slots.numel()
+    table = None if pages is None else pages._table
+    if table is not None and table.shape[0] < n:
+        raise ValueError(f"the block table has {table.shape[0]} rows for {n} requests")
+    a = _here(dev, (q_len, "q_len", i32, (n,)), (total_len, "total_len", i32, (n,)), (slots, "slots", i32, (tokens,)),
+              (positions, "positions", i32, (tokens,)), (rows, "rows", i32, (tokens,)), (first, "first", i32, (n + 1,)),
+              (table, "block_table", None, None))
+    _check(lib.dsa_slot_map(n, tokens, None if pages is None else ctypes.byref(pages), capacity, *a[:6],
+                            _stream_here(dev, stream)))
+
+
+def make_rope_axes_problem(tokens: int, num_q_heads: int, num_kv_heads: int, cache_rows: int, sections: Sequence[int],
+                           max_pos: int, in_turn: bool = False, eps: float = 1e-6, q_dtype="bf16", kv_dtype="bf16",
+                           cos_dtype="fp32", head_dim: int = 128) -> DsaAxesProblem:
+    """Fill a DsaAxesProblem: sections[a] rotary pairs turn by the position on axis
+    a, first all of axis 0's or (in_turn) dealt out in turn. The strides are taken
+    from the tensors of the call."""
+    p = DsaAxesProblem(tokens, 0, 0, 0, 0, 0, cache_rows, num_q_heads, num_kv_heads, head_dim, len(sections))
+    for a, n in enumerate(sections[:DSA_MAX_AXES]):
+        p.sections[a] = int(n)
+    p.in_turn, p.max_pos, p.eps = int(in_turn), max_pos, eps
+    p.q_dtype, p.kv_dtype, p.cos_dtype = _DT[q_dtype], _DT[kv_dtype], _DT[cos_dtype]
+    return p
+
+
+def _token_rows(dev: int, t, name: str, dtype, tokens: int, heads: int):
+    """(address, elements from token to token) of a tensor [tokens, heads * 128] or
+    [tokens, heads, 128] whose tokens' vectors lie together each."""
+    if t is None:
+        return None, 0
+    width = heads * 128
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(dev, t, name, dtype, None)
+    st = t.stride()
+    if t.dim() == 2:
+        ok = t.shape[0] == tokens and t.shape[1] == width and (width <= 1 or st[1] == 1)
+    else:
+        ok = (t.dim() == 3 and t.shape[0] == tokens and t.shape[1] == heads and t.shape[2] == 128
+              and (width == 0 or st[2] == 1) and (heads <= 1 or st[1] == 128))
+    if not ok:
+        raise ValueError(f"{name} must be [{tokens}, {width}] or [{tokens}, {heads}, 128], each token's vectors "
+                         f"contiguous, got {tuple(t.shape)} with strides {st}")
+    return t.data_ptr(), st[0] if tokens > 1 and width else 0
+
+
+def dsa_rope_axes_append(p: DsaAxesProblem, q, k, v, gamma_q, gamma_k, cos, sin, positions, slots, q_out, k_cache, v_cache,
+                         k_scale=None, v_scale=None, stream=None):
+    """RMSNorm (gamma_q, gamma_k; None: none) and rotary positions with several axes:
+    q to q_out (or q itself), k and v into the caches [cache_rows, Hkv, 128] at
+    slots [N]. q, k and v may be columns of one projection. positions [axes, N], or
+    [N] where all axes have the same."""
+    lib, dev, n, hkv = load_library(), _current_device(), p.tokens, p.num_kv_heads
+    qdt, kvdt, f32, i32 = _TORCH_DT[p.q_dtype], _TORCH_DT[p.kv_dtype], torch.float32, torch.int32
+    qp, p.q_stride = _token_rows(dev, q, "q", qdt, n, p.num_q_heads)
+    kp, p.k_stride = _token_rows(dev, k, "k", qdt, n, hkv)
+    vp, p.v_stride = _token_rows(dev, v, "v", qdt, n, hkv)
+    op, p.out_stride = _token_rows(dev, q_out, "q_out", qdt, n, p.num_q_heads)
+    if positions.dim() == 1:
+        p.pos_stride, shape = 0, (n,)
+    else:
+        p.pos_stride, shape = n, (p.axes, n)
+    half = sum(p.sections[:p.axes])
+    cache, angles, cdt = (p.cache_rows, hkv, 128), (p.max_pos, half), _TORCH_DT[p.cos_dtype]
+    a = _here(dev, (gamma_q, "gamma_q", f32, (128,)), (gamma_k, "gamma_k", f32, (128,)), (cos, "cos", cdt, angles),
+              (sin, "sin", cdt, angles), (positions, "positions", i32, shape), (slots, "slots", i32, (n,)),
+              (k_cache, "k_cache", kvdt, cache), (v_cache, "v_cache", kvdt, cache),
+              (k_scale, "k_scale", f32, cache[:2]), (v_scale, "v_scale", f32, cache[:2]))
+    _check(lib.dsa_rope_axes_append(ctypes.byref(p), qp, kp, vp, *a[:6], op, *a[6:], _stream_here(dev, stream)))
+
+
+def make_norm_problem(rows: int, hidden: int, x_dtype="bf16", y_dtype="bf16", eps: float = 1e-6,
+                      scale_group: int = 0) -> DsaNormProblem:
+    """Fill a DsaNormProblem; scale_group: elements that share a scale of an 8-bit
+    y (0: a row's). The strides are taken from the tensors of the call."""
+    return DsaNormProblem(rows, 0, 0, 0, 0, hidden, scale_group, _DT[x_dtype], _DT[y_dtype], eps)
+
+
+def dsa_add_rmsnorm(p: DsaNormProblem, x, residual, gamma, h, y, scale=None, stream=None):
+    """h = x + residual (None: x alone, and h None), y = the RMS norm of h times
+    gamma, in 16 bits or as codes with scale [rows, 1 or ceil(hidden / 128)]. The
+    rows of x, residual, h and y [rows, hidden] may lie any stride apart."""
+    lib, dev, shape = load_library(), _current_device(), (p.rows, p.hidden)
+    ptrs, strides = [], []
+    for t, name, dt in ((x, "x", p.x_dtype), (residual, "residual", p.x_dtype), (h, "h", p.x_dtype), (y, "y", p.y_dtype)):
+        if t is None:
+            ptrs.append(None)
+            strides.append(0)
+            continue
+        if t.dtype is not _TORCH_DT[dt] or t.shape != shape or t.get_device() != dev:
+            _refuse(dev, t, name, _TORCH_DT[dt], shape)
+        st = t.stride()
+        if p.hidden > 1 and st[1] != 1:
+            raise ValueError(f"{name}'s rows must be contiguous, got strides {st}")
+        ptrs.append(t.data_ptr())
+        strides.append(st[0] if p.rows > 1 else 0)
+    p.x_stride, p.residual_stride, p.h_stride, p.y_stride = strides
+    groups = -(-p.hidden // p.scale_group) if p.scale_group else 1
+    g, s = _here(dev, (gamma, "gamma", torch.float32, (p.hidden,)), (scale, "scale", torch.float32, (p.rows, groups)))
+    _check(lib.dsa_add_rmsnorm(ctypes.byref(p), ptrs[0], ptrs[1], g, ptrs[2], ptrs[3], s, _stream_here(dev, stream)))
 
 
 def dsa_read_device_status(workspace, stream=None) -> int:
