@@ -34,12 +34,19 @@ def inputs(rows, hidden, x, seed=0, mul=1.0):
 def check(h, gamma, y, scale, out, group, eps):
     """h: what is normalised, as stored."""
     h64 = h.double().numpy()
-    ref = h64 * gamma.double().numpy() / np.sqrt((h64 ** 2).mean(1, keepdims=True) + eps)
+    with np.errstate(invalid="ignore"):
+        ref = h64 * gamma.double().numpy() / np.sqrt((h64 ** 2).mean(1, keepdims=True) + eps)
+    # sums that overflow their type are infinite, as the addition says: NaN there, 0 beside them
+    over = np.isinf(h64)
     if out in HALF:
         got = y.double().cpu().numpy()
+        assert np.isnan(got[over]).all()
+        got, ref = got[~over], ref[~over]
         tol = HALF[out] * np.abs(ref) * (1 + E) + np.abs(ref) * E + (2.0 ** -25 if out == "fp16" else 1e-39)
         assert (np.abs(got - ref) <= tol).all()
         return
+    finite = ~over.any(1)                         # (rows of codes are unspecified then)
+    y, scale, ref = y[torch.from_numpy(finite).to(y.device)], scale[torch.from_numpy(finite).to(y.device)], ref[finite]
     top = 448.0 if out == "e4m3" else 127.0
     width = group or h.shape[1]
     got, s = y.double().cpu().numpy(), scale.double().cpu().numpy()

@@ -189,8 +189,7 @@ def test_text_positions_agree_with_the_fused_prologue(D):
     gam = [1 + 0.2 * torch.randn(n, device="cuda", generator=g) for n in (128, 128, 64, 64)]
     ang = torch.arange(64, device="cuda")[:, None] * 1e4 ** (-torch.arange(64, device="cuda") / 64)
     cos, sin = ang.cos().contiguous(), ang.sin().contiguous()
-    K, V, KI = (torch.zeros(B, T, hkv, 128, device="cuda", dtype=torch.bfloat16) for _ in range(2)), None, None
-    K, V = K
+    K, V = (torch.zeros(B, T, hkv, 128, device="cuda", dtype=torch.bfloat16) for _ in range(2))
     KI = torch.zeros(B, T, 64, device="cuda", dtype=torch.bfloat16)
     K2, V2 = torch.zeros_like(K), torch.zeros_like(V)
     q2 = torch.empty(B * S, hq, 128, device="cuda", dtype=torch.bfloat16)
@@ -201,8 +200,8 @@ def test_text_positions_agree_with_the_fused_prologue(D):
     D.dsa_rope_axes_append(p2, q.view(B * S, hq, 128), k.view(B * S, hkv, 128), v.view(B * S, hkv, 128), gam[0], gam[1], cos, sin, pos,
                            slots, q2, K2.view(B * T, hkv, 128), V2.view(B * T, hkv, 128))
     p = D.make_problem(batch=B, q_len=S, total_len=[20, 33], top_k=8, num_q_heads=hq, num_kv_heads=hkv, cache_capacity=T)
-    D.dsa_rope_append(p, q, qI, k, kI, v, KI, K, V, None, None, 1e-6, *gam, cos_cache=cos, sin_cache=sin,
-                      cos_cache_index=cos[:, ::2].contiguous(), sin_cache_index=sin[:, ::2].contiguous())
+    D.dsa_rope_append(p, q, qI, k, kI, v, KI, K, V, None, None, *gam, cos=cos, sin=sin, cos_index=cos[:, ::2].contiguous(),
+                      sin_index=sin[:, ::2].contiguous())
     assert torch.equal(V, V2)
     for a, b in ((q.view_as(q2), q2), (K, K2)):
         a, b = a.double(), b.double()

@@ -305,6 +305,7 @@ extern "C" int dsa_add_rmsnorm(const dsa_norm_problem* np, const void* x, const 
   const long long stride[4] = {np->x_stride, np->residual_stride, np->h_stride, np->y_stride};
   for (long long s : stride)
     if (s != 0 && (s < np->hidden || s > (1LL << 40))) return report_error(DSA_ERR_INVALID_ARG, "a row stride must be 0 or at least hidden");
+  if (np->rows == 0) return DSA_OK;
   if (!x || !gamma || !y) return report_error(DSA_ERR_INVALID_ARG, "x, gamma and y are required");
   if (h && !residual) return report_error(DSA_ERR_INVALID_ARG, "h is the sum with a residual: there is none");
   if (q8 != (scale != nullptr)) return report_error(DSA_ERR_INVALID_ARG, "scale is required iff y is of 8 bits");
@@ -320,7 +321,6 @@ extern "C" int dsa_add_rmsnorm(const dsa_norm_problem* np, const void* x, const 
   const auto off = [](const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) != 0; };
   if (off(x, xb) || off(residual, xb) || off(h, xb) || off(y, yb) || off(gamma, 4) || off(scale, 4))
     return report_error(DSA_ERR_MISALIGNED, "tensors must be aligned to their elements");
-  if (p.rows == 0) return DSA_OK;
   // A row is read before it is written, so h may be x or the residual, and y x, the
   // residual or h's row in the same place; any other overlap is refused.
   struct Span {

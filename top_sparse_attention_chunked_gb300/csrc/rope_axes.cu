@@ -369,6 +369,8 @@ extern "C" int dsa_rope_axes_append(const dsa_axes_problem* ap, const void* q, c
   }
   const long long ps = ap->pos_stride;
   if (ps < 0 || ps > (1LL << 40)) return report_error(DSA_ERR_INVALID_ARG, "pos_stride must be >= 0");
+  const long long N = ap->tokens;
+  if (N == 0) return DSA_OK;
   if (!cos_cache || !sin_cache || !positions) return report_error(DSA_ERR_INVALID_ARG, "positions and the cos / sin caches are required");
   if ((hq > 0 && (!q || !q_out)) || (hkv > 0 && (!k || !v || !k_cache || !v_cache || !slots)))
     return report_error(DSA_ERR_INVALID_ARG, "a required tensor pointer is NULL");
@@ -381,8 +383,6 @@ extern "C" int dsa_rope_axes_append(const dsa_axes_problem* ap, const void* q, c
   if (off(gamma_q, 4) || off(gamma_k, 4) || off(positions, 4) || off(slots, 4) || off(k_scale, 4) || off(v_scale, 4) ||
       off(cos_cache, cb) || off(sin_cache, cb))
     return report_error(DSA_ERR_MISALIGNED, "gamma, positions, slots, scales, cos and sin must be aligned to their elements");
-  const long long N = ap->tokens;
-  if (N == 0) return DSA_OK;
   // what is read and what is written: q_out may be q itself
   struct Span {
     const void* at;
