@@ -863,6 +863,52 @@ int dsa_add_rmsnorm(const dsa_norm_problem* p, const void* x, const void* residu
                     void* h, void* y, float* scale, void* stream);
 
 /*
+ * dsa_sample -- a token per row from its logits and one given random number.
+ * With T the row's temperature, w_t = exp((logit_t - the row's largest) / T), and
+ * the tokens ranked by logit (ties: the lower index first), each of these keeps
+ * the first tokens of the ranking:
+ *   top_k > 0     top_k of them
+ *   top_p < 1     as few as have at least top_p of the weight that top_k leaves
+ *                 (one at least)
+ *   min_p > 0     those of weight min_p or more (min_p above 1 is taken as 1)
+ * The token is the first, in the order of their indices, at which the running
+ * sum of the kept weights exceeds uniform times their whole sum. Its log
+ * probability is log(w / the kept weights' sum).
+ *
+ * T <= 0 or NaN takes the largest logit (the lowest index of it), and so does a
+ * row with a +infinity. A token of -infinity or NaN is never taken; a row of
+ * nothing else gives token -1 and log probability -infinity.
+ *
+ *   rows          1 .. 65535
+ *   vocab         1 .. 2^19
+ *   logits_dtype  DSA_BF16, DSA_FP16 or DSA_FP32
+ *   row_stride    elements between two rows of logits, >= vocab (0: vocab)
+ *
+ *   logits        [rows, row_stride], aligned to its elements
+ *   uniform       [rows] fp32 in [0, 1) (others are taken as the nearest)
+ *   temperature, top_p, min_p   [rows] fp32; top_k [rows] int32; each or NULL: 1,
+ *                 1, 0 and 0 for all rows
+ *   tokens        [rows] int32
+ *   logprobs      [rows] fp32, or NULL
+ * No result overlaps an input or the other result.
+ *
+ * The cut and the draw are those of exact arithmetic on weights that are right
+ * to about 2^-31 of themselves and are 0 below 2^-44 of the largest; sums are
+ * of whole numbers, so the result does not depend on the order of execution.
+ * One kernel; no workspace.
+ */
+typedef struct dsa_sample_problem {
+  int32_t rows;
+  int32_t vocab;
+  int32_t logits_dtype;
+  int64_t row_stride;
+} dsa_sample_problem;
+
+int dsa_sample(const dsa_sample_problem* p, const void* logits, const float* uniform, const float* temperature,
+               const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,
+               float* logprobs, void* stream);
+
+/*
  * Synchronises `stream`, then copies the device status word from the
  * workspace to *status_out (0 = no device-side problem; bit 0 = a bounded
  * wait ran out; bit 1 = a gathered key's block-table entry lay outside the

@@ -24,7 +24,7 @@ DEBUG_LIB = os.path.join(HERE, "libdsa_debug.so")
 SOURCES = ["dsa_api.cu", "indexer.cu", "topk.cu", "attention.cu", "prefill_attn.cu",
            "topk_noalloc.cu", "cache_append.cu", "rmsnorm_rotary.cu",
            "rope_append.cu", "full_attn.cu", "pages.cu", "beam.cu", "slot_map.cu",
-           "rope_axes.cu", "add_rmsnorm.cu"]
+           "rope_axes.cu", "add_rmsnorm.cu", "sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -40,7 +40,7 @@ EXPORTED = ["dsa_workspace_size", "dsa_index_scores", "dsa_topk",
             "dsa_full_attn", "dsa_full_attn_paged", "dsa_full_attn_workspace_size",
             "dsa_pages_update", "dsa_pages_compact", "dsa_pages_workspace_size",
             "dsa_beam_select", "dsa_beam_workspace_size", "dsa_full_attn_sinks", "dsa_slot_map",
-            "dsa_rope_axes_append", "dsa_add_rmsnorm"]
+            "dsa_rope_axes_append", "dsa_add_rmsnorm", "dsa_sample"]
 
 _DT = {"bf16": DSA_BF16, "fp16": DSA_FP16, "int8": DSA_INT8, "fp32": DSA_FP32, "e4m3": DSA_FP8_E4M3}
 _TORCH_DT = {DSA_BF16: torch.bfloat16, DSA_FP16: torch.float16, DSA_INT8: torch.int8,
@@ -202,6 +202,16 @@ class DsaNormProblem(ctypes.Structure):
     ]
 
 
+class DsaSampleProblem(ctypes.Structure):
+    """dsa_sample_problem (a token per row)."""
+    _fields_ = [
+        ("rows", ctypes.c_int32),
+        ("vocab", ctypes.c_int32),
+        ("logits_dtype", ctypes.c_int32),
+        ("row_stride", ctypes.c_int64),
+    ]
+
+
 class DsaError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{msg} (status {status})")
@@ -257,6 +267,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "dsa_slot_map": (i32, [i32, ctypes.c_int64, PG, i32] + [vp] * 7),
         "dsa_rope_axes_append": (i32, [ctypes.POINTER(DsaAxesProblem)] + [vp] * 15),
         "dsa_add_rmsnorm": (i32, [ctypes.POINTER(DsaNormProblem)] + [vp] * 7),
+        "dsa_sample": (i32, [ctypes.POINTER(DsaSampleProblem)] + [vp] * 9),
         "dsa_pages_workspace_size": (sz, [PS]),
         "dsa_pages_update": (i32, [PS] + [vp] * 4 + [i32, PP] + [vp] * 4 + [sz, vp]),
         "dsa_pages_compact": (i32, [PS, i32, PP] + [vp] * 5 + [sz, vp]),
@@ -920,6 +931,32 @@ def dsa_add_rmsnorm(p: DsaNormProblem, x, residual, gamma, h, y, scale=None, str
     groups = -(-p.hidden // p.scale_group) if p.scale_group else 1
     g, s = _here(dev, (gamma, "gamma", torch.float32, (p.hidden,)), (scale, "scale", torch.float32, (p.rows, groups)))
     _check(lib.dsa_add_rmsnorm(ctypes.byref(p), ptrs[0], ptrs[1], g, ptrs[2], ptrs[3], s, _stream_here(dev, stream)))
+
+
+def make_sample_problem(rows: int, vocab: int, logits_dtype="bf16", row_stride: int = 0) -> DsaSampleProblem:
+    return DsaSampleProblem(rows, vocab, _DT[logits_dtype], row_stride)
+
+
+def dsa_sample(p: DsaSampleProblem, logits, uniform, tokens, temperature=None, top_k=None, top_p=None, min_p=None,
+               logprobs=None, stream=None):
+    """A token per row of logits [rows, vocab] (rows p.row_stride elements apart) from
+    one random number each, uniform [rows] in [0, 1): after the row's temperature,
+    top_k (int32), top_p and min_p [rows]; logprobs [rows] receives the log
+    probabilities that the tokens were drawn with."""
+    lib, dev, one = load_library(), _current_device(), (p.rows,)
+    stride = p.row_stride or p.vocab
+    if logits.shape != (p.rows, p.vocab) or logits.stride(-1) != 1 or (p.rows > 1 and logits.stride(0) != stride):
+        raise ValueError(f"logits must be [{p.rows}, {p.vocab}] with rows {stride} elements apart, got "
+                         f"{tuple(logits.shape)} with strides {logits.stride()}")
+    if logits.dtype != _TORCH_DT[p.logits_dtype]:
+        raise ValueError(f"logits must be {_TORCH_DT[p.logits_dtype]}, got {logits.dtype}")
+    if logits.get_device() != dev:
+        raise ValueError(f"logits is on {logits.device}, the current device is cuda:{dev}")
+    f32, i32 = torch.float32, torch.int32
+    a = _here(dev, (uniform, "uniform", f32, one), (temperature, "temperature", f32, one), (top_k, "top_k", i32, one),
+              (top_p, "top_p", f32, one), (min_p, "min_p", f32, one), (tokens, "tokens", i32, one),
+              (logprobs, "logprobs", f32, one))
+    _check(lib.dsa_sample(ctypes.byref(p), logits.data_ptr(), *a, _stream_here(dev, stream)))
 
 
 def dsa_read_device_status(workspace, stream=None) -> int:
