@@ -13,11 +13,13 @@
 // in fp32 pairs to 2^-31 of itself, and all sums are of 64-bit integers.
 //
 // A cluster of blocks holds a row in shared memory (read once); everything else is
-// passes over it and exchanges between the blocks. The cut is found by counts of the
-// weights' logarithms in 1,024 bins, of which the one or few that can hold the cut are
-// counted again (by the bits of x) until at most kSmList tokens are left; those are
-// ranked against each other. Top-p takes bounds from the bins' edges, exact sums of
-// what lies above them.
+// passes over it and exchanges between the blocks. A list of the tokens that reach a
+// value, which enough of the threads' largest ones do, settles most rows: sorted, it
+// has the cut of top-k, and of top-p where the list weighs enough. Otherwise the cut is
+// looked for in counts of all tokens by the logarithm of the weight, 1,024 bins with the
+// sum of what the tokens lie below their bin's edge: these bound the running sum to a
+// part in 1,000, exact sums and a list of the tokens between the bounds do the rest (if
+// they are too many for a list, they are counted again, by smaller bins).
 #include <algorithm>
 #include <cmath>
 #include <cuda_bf16.h>
@@ -30,33 +32,27 @@
 namespace dsa {
 namespace {
 
-constexpr int kSmThreads = 512, kSmWarps = kSmThreads / 32;
-constexpr int kSmBins = 1024;
-constexpr int kSmList = 512;                    // candidates that are ranked against each other
+constexpr int kSmThreads = 1024, kSmWarps = kSmThreads / 32;
+constexpr int kSmBins = kSmThreads;             // one a thread
+constexpr int kSmList = kSmThreads;             // candidates that are sorted, one a thread
+constexpr int kSmFewK = 640, kSmFewP = 256;     // tokens that a list is expected to hold, of top-k and of top-p alone
 constexpr int kSmMaxVocab = 1 << 19;
 constexpr int kSmMaxCluster = 16;
-constexpr int kSmMaxData = 196608;              // bytes of a row that a block holds
+constexpr int kSmMaxData = 172032;              // bytes of a row that a block holds
 
-// 2^(j / 512), j = 0 .. 511, times 2^30: as a float and rounded to an integer.
+// 2^(j / 512), j = 0 .. 511, times 2^30.
 struct Pow2Table {
-  uint32_t f[512], i[512];
+  uint32_t v[512];
 };
 constexpr double series_exp(double x) {         // |x| < 0.7: 1 + x (1 + x / 2 (1 + x / 3 (...)))
   double s = 1.0;
   for (int k = 24; k >= 1; --k) s = 1.0 + x * s / k;
   return s;
 }
-constexpr uint32_t bits_of_30(double v) {       // the fp32 nearest v in [2^30, 2^31)
-  const uint32_t m = static_cast<uint32_t>(v / 128.0 + 0.5);      // 24 bits: v's last place is 2^7
-  return m >= (1u << 24) ? (127u + 31u) << 23 : ((127u + 30u) << 23) | (m - (1u << 23));
-}
 constexpr Pow2Table make_table() {
   Pow2Table t{};
-  for (int j = 0; j < 512; ++j) {
-    const double v = series_exp(0.693147180559945309417 * j / 512.0) * 1073741824.0;
-    t.f[j] = bits_of_30(v);
-    t.i[j] = static_cast<uint32_t>(v + 0.5);
-  }
+  for (int j = 0; j < 512; ++j)
+    t.v[j] = static_cast<uint32_t>(series_exp(0.693147180559945309417 * j / 512.0) * 1073741824.0 + 0.5);
   return t;
 }
 __device__ const Pow2Table g_pow2 = make_table();
@@ -76,23 +72,23 @@ struct SampleParams {
 };
 
 struct SampleShared {
-  uint2 tab[512];
-  uint32_t hist[2][kSmBins];
-  uint2 list[2][kSmList];     // this block's candidates: (bits of x, index)
-  uint2 all[kSmList];         // the cluster's
-  unsigned long long weight[kSmList];
-  // what the blocks exchange (two sets: a block may be one exchange ahead)
+  uint32_t tab[512];
+  unsigned long long sort[2][kSmList];
+  // what the blocks exchange, in two sets: a block may be one exchange ahead
+  uint32_t hist[2][kSmBins], below[2][kSmBins];   // tokens of a bin; the sum of what they lie below its edge
+  unsigned long long list[2][kSmList];            // this block's candidates: (key of x, ~index)
   unsigned long long sum[2];
   uint32_t cnt[2], fill[2];
-  float top[2];
-  unsigned long long warp_sum[kSmWarps];
+  float top[2], low[2];
+  // scratch of the block
+  unsigned long long warp_sum[kSmWarps], cand_sum[kSmWarps];
   uint32_t warp_cnt[kSmWarps];
-  float2 warp_bound[kSmWarps];
+  float warp_bound[kSmWarps];
   // found by one thread, read by all
   int lo_bin, hi_bin, at_index;
   float at_x;
   unsigned long long at_sum;
-  double row_c, row_low;      // log2 e / T; T ln min_p
+  float2 row_c, row_low;      // log2 e / T and T ln min_p, as pairs of floats
 };
 
 // --------------------------------------------------------------- clusters
@@ -127,34 +123,40 @@ constexpr int kZero = -44 * 512;                // weights from 2^-44 of the lar
 
 // x -> log2 of the weight, in units of 1 / 512 and a rest. (x - b) log2 e / T is formed
 // as a pair of floats; b is 0, or the largest x where that is too large to be a
-// multiple of 1 / 512 in fp32 (then x - b is exact for all that have a weight).
+// multiple of 1 / 512 in fp32 (then x - b is exact for all that have a weight). All is
+// relative to the grid point next to the largest x, `rest` below it.
 struct Scale {
-  float b, ch, cl, rest, floor, top;            // rest: what the largest x's exponent has beyond its grid point
+  float b, ch, cl, floor, top, rest;
   int base, lg;
 };
 __device__ __forceinline__ int grid_of(const Scale& s, float x, float* frac) {
   const float d = x - s.b, p = d * s.ch;
   const float c = fmaxf(p, s.floor);            // (NaN, -infinity: the floor)
   const float t = c + kGrid;
-  const float lo = fmaf(d, s.cl, fmaf(d, s.ch, -p));
-  *frac = (c - (t - kGrid)) + (lo - s.rest);
+  *frac = (c - (t - kGrid)) + fmaf(d, s.cl, fmaf(d, s.ch, -p));
   return __float_as_int(t) - s.base;            // <= 0
 }
-__device__ __forceinline__ int bin_of(const Scale& s, float x) {   // 1 / 16 wide, 0 the largest weight's
-  const float t = fmaxf((x - s.b) * s.ch, s.floor) + kGrid;
-  return min((s.base - __float_as_int(t)) >> 5, kSmBins - 1);
+__device__ __forceinline__ int grid_of(const Scale& s, float x) {
+  return __float_as_int(fmaxf((x - s.b) * s.ch, s.floor) + kGrid) - s.base;
 }
-// 2^r - 1 = r ln 2 + (r ln 2)^2 / 2 + (r ln 2)^3 / 6 (|r| <= 2^-9: off by 2^-38)
-__device__ __forceinline__ unsigned long long weight_of(const Scale& s, const uint2* tab, float x) {
+// 2^r - 1 = r ln 2 + (r ln 2)^2 / 2 + (r ln 2)^3 / 6 (|r| <= 2^-10: off by 2^-42)
+__device__ __forceinline__ unsigned long long weight_of(const Scale& s, const uint32_t* tab, float x, int* grid) {
   float r;
   const int it = grid_of(s, x, &r);
-  const uint2 t = tab[it & 511];
+  *grid = it;
+  const uint32_t t = tab[it & 511];
   const float q = r * fmaf(r, fmaf(r, 0.05550411f, 0.24022651f), 0.69314718f);
-  const uint32_t w = t.y + (__float_as_uint(fmaf(q, __uint_as_float(t.x), kInt)) - __float_as_uint(kInt));
+  // (t as a float: its upper 24 bits)
+  const float w = fmaf(q, __uint_as_float((t >> 7) + ((127u + 29u) << 23)), kInt);
   // w 2^32 >> (lg - exponent), its last place set: the middle of what was cut off
   unsigned long long y;
-  asm("shr.u64 %0, %1, %2;" : "=l"(y) : "l"(static_cast<unsigned long long>(w) << 32), "r"(s.lg - (it >> 9)));
+  asm("shr.u64 %0, %1, %2;" : "=l"(y)
+      : "l"(static_cast<unsigned long long>(t + (__float_as_uint(w) - __float_as_uint(kInt))) << 32), "r"(s.lg - (it >> 9)));
   return it > kZero ? y | 1ull : 0ull;
+}
+__device__ __forceinline__ unsigned long long weight_of(const Scale& s, const uint32_t* tab, float x) {
+  int it;
+  return weight_of(s, tab, x, &it);
 }
 
 // ------------------------------------------------------------------ row
@@ -165,6 +167,7 @@ template <bool F32>
 struct Slice {
   const uint4* img;
   int first, count;     // the warp's vectors
+  int vecs, per;        // the block's, and a warp's
   int index0;           // index of element 0 of vector 0
   static constexpr int kVec = F32 ? 4 : 8;
   bool f16;
@@ -186,24 +189,29 @@ struct Slice {
   template <class F>
   __device__ __forceinline__ void each(F&& f) const {
     const int lane = threadIdx.x & 31;
-    for (int i = 0; i < count; i += 32) one(i, lane, f);
+    for (int i = 0; i < count; i += 32) one(first + i + lane, i + lane < count, f);
   }
   template <class F>
-  __device__ __forceinline__ void one(int i, int lane, F&& f) const {
+  __device__ __forceinline__ void one(int v, bool in, F&& f) const {
     float x[kVec];
-    if (i + lane < count) {
-      unpack(img[first + i + lane], x);
+    if (in) {
+      unpack(img[v], x);
     } else {
 #pragma unroll
       for (int e = 0; e < kVec; ++e) x[e] = -INFINITY;
     }
-    f(x, index0 + (first + i + lane) * kVec);
+    f(x, index0 + v * kVec);
   }
 };
 
 __device__ __forceinline__ unsigned long long warp_add(unsigned long long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 __device__ __forceinline__ float key_float(uint32_t k) {      // float_key's inverse
@@ -225,8 +233,17 @@ struct Sampler {
   uint32_t rank, blocks;
   uint32_t phase = 0;
   int warp, lane;
+  // the list that the last cut was found in: this thread's candidate (0: none), its sum of
+  // what lies above list_top, that of all threads
+  bool listed = false;
+  unsigned long long cand = 0, list_above = 0;
+  Sums list_sums;
+  float list_top;
 
   __device__ __forceinline__ Sampler(const SampleParams& pp, SampleShared& s) : p(pp), sh(s) {}
+
+  // What weights are multiples of 2^-32 of (the largest is 2^rest times it).
+  __device__ __forceinline__ float unit() const { return __int_as_float((127 + 62 - sc.lg) << 23); }
 
   // Adds up every thread's sum and count over the cluster.
   __device__ __forceinline__ Sums exchange(unsigned long long sum, uint32_t cnt) {
@@ -238,16 +255,13 @@ struct Sampler {
       sh.warp_cnt[warp] = cnt;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-      unsigned long long s = 0;
-      uint32_t c = 0;
-#pragma unroll
-      for (int w = 0; w < kSmWarps; ++w) {
-        s += sh.warp_sum[w];
-        c += sh.warp_cnt[w];
+    if (warp == 0) {
+      const unsigned long long s = warp_add(sh.warp_sum[lane]);
+      const uint32_t c = __reduce_add_sync(0xffffffffu, sh.warp_cnt[lane]);
+      if (lane == 0) {
+        sh.sum[ph] = s;
+        sh.cnt[ph] = c;
       }
-      sh.sum[ph] = s;
-      sh.cnt[ph] = c;
     }
     blocks_sync(blocks);
     Sums r;
@@ -262,18 +276,13 @@ struct Sampler {
     return r;
   }
 
-  // Two bins a thread, the first thread's the top ones, with the cluster's counts.
-  // (This block's are complete after a barrier that exchange() has.)
-  __device__ __forceinline__ uint2 bins(const uint32_t* hist) {
-    uint2 n = make_uint2(0, 0);
-    for (uint32_t r = 0; r < blocks; ++r) {
-      uint32_t a;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(hist + 2 * threadIdx.x)), "r"(r));
-      uint2 v;
-      asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-      n.x += v.x;
-      n.y += v.y;
-    }
+  // The cluster's counts, a bin a thread. (This block's are complete after a barrier
+  // that exchange() has.)
+  __device__ __forceinline__ uint32_t bins(const uint32_t* hist) {
+    uint32_t n = 0;
+#pragma unroll
+    for (uint32_t r = 0; r < kSmMaxCluster; ++r)
+      if (r < blocks) n += peer_load(hist + threadIdx.x, r);
     return n;
   }
   __device__ __forceinline__ uint32_t* clear_hist() {          // the set that the next exchange belongs to
@@ -282,15 +291,33 @@ struct Sampler {
     __syncthreads();
     return h;
   }
-  __device__ __forceinline__ void count(uint32_t* hist, int bin, bool in) {
-    // (rows of equal logits: one addition a warp)
-    const uint32_t who = __ballot_sync(0xffffffffu, in);
-    if (who == 0) return;
-    const int lead = __ffs(who) - 1;
-    const int first = __shfl_sync(0xffffffffu, bin, lead);
-    const uint32_t same = __ballot_sync(0xffffffffu, in && bin == first);
-    if (lane == lead) atomicAdd(hist + first, __popc(same));
-    else if (in && bin != first) atomicAdd(hist + bin, 1u);
+  // Counts a thread's tokens, those that follow one another in the same bin (-1: none)
+  // at once: rows of equal logits would otherwise meet in one place.
+  __device__ __forceinline__ void count(uint32_t* hist, const int (&bin)[Slice<F32>::kVec]) {
+    uint32_t run = 0;
+#pragma unroll
+    for (int e = 0; e < Slice<F32>::kVec; ++e) {
+      ++run;
+      if (e + 1 < Slice<F32>::kVec && bin[e + 1] == bin[e]) continue;
+      if (bin[e] >= 0) atomicAdd(hist + bin[e], run);
+      run = 0;
+    }
+  }
+  // The same for tokens at grid points g below 0: bins of 32 points, and by how much.
+  __device__ __forceinline__ void count_grid(uint32_t* hist, uint32_t* below, const int (&g)[Slice<F32>::kVec]) {
+    uint32_t run = 0, sum = 0;
+#pragma unroll
+    for (int e = 0; e < Slice<F32>::kVec; ++e) {
+      ++run;
+      sum += static_cast<uint32_t>(-g[e]) & 31u;
+      if (e + 1 < Slice<F32>::kVec && -g[e + 1] >> 5 == -g[e] >> 5) continue;
+      const int b = -g[e] >> 5;
+      if (b < kSmBins - 1) {
+        atomicAdd(hist + b, run);
+        if (sum) atomicAdd(below + b, sum);
+      }
+      run = sum = 0;
+    }
   }
 
   // Exclusive sum over the threads before this one.
@@ -304,42 +331,55 @@ struct Sampler {
     }
     if (lane == 31) part[warp] = x;
     __syncthreads();
-    T before = 0;
-    for (int w = 0; w < warp; ++w) before += part[w];
+    T before = lane < warp ? part[lane] : T(0);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
     __syncthreads();
-    return before + x - v;
+    T own = __shfl_up_sync(0xffffffffu, x, 1);
+    if (lane == 0) own = 0;
+    return before + own;
   }
 
-  // The bin (of two a thread) in which a running count passes `need`.
-  __device__ __forceinline__ void find_count(const uint2& n, uint32_t need) {
-    const uint32_t a = scan<uint32_t>(n.x + n.y, sh.warp_cnt);
-    if (a < need && need <= a + n.x + n.y) sh.lo_bin = sh.hi_bin = 2 * threadIdx.x + (a + n.x < need ? 1 : 0);
+  // The bin in which a running count passes `need`.
+  __device__ __forceinline__ void find_count(uint32_t n, uint32_t need) {
+    const uint32_t a = scan<uint32_t>(n, sh.warp_cnt);
+    if (a < need && need <= a + n) sh.lo_bin = sh.hi_bin = threadIdx.x;
     __syncthreads();
   }
-  // The bins in which a running sum may pass `need`: every token of bin i weighs
-  // between lower and upper (two a thread each), all relative to the largest weight.
-  __device__ __forceinline__ void find_bounds(const uint2& n, const float2& lower, const float2& upper, float need) {
-    const float l0 = n.x * lower.x, l1 = n.y * lower.y, u0 = n.x * upper.x, u1 = n.y * upper.y;
-    if (threadIdx.x == 0) {
-      sh.lo_bin = kSmBins - 1;
-      sh.hi_bin = kSmBins - 1;
-    }
-    __syncthreads();
-    const float l = scan<float>(l0 + l1, reinterpret_cast<float*>(sh.warp_bound));
-    const float u = scan<float>(u0 + u1, reinterpret_cast<float*>(sh.warp_bound));
+  // The bins in which a running sum may pass `need`: what the thread's bin holds weighs
+  // between l0 and u0.
+  __device__ __forceinline__ void find_bounds(float l0, float u0, float need) {
+    if (threadIdx.x == 0) sh.lo_bin = sh.hi_bin = kSmBins - 1;
+    const float l = scan<float>(l0, sh.warp_bound) + l0;
+    const float u = scan<float>(u0, sh.warp_bound) + u0;
     // (1e-4: far beyond what these sums of positive terms are off by)
-    const float most = need * 1.0001f, least = need * 0.9999f;
-    if (u + u0 >= least) atomicMin(&sh.lo_bin, 2 * static_cast<int>(threadIdx.x));
-    else if (u + u0 + u1 >= least) atomicMin(&sh.lo_bin, 2 * static_cast<int>(threadIdx.x) + 1);
-    if (l + l0 >= most) atomicMin(&sh.hi_bin, 2 * static_cast<int>(threadIdx.x));
-    else if (l + l0 + l1 >= most) atomicMin(&sh.hi_bin, 2 * static_cast<int>(threadIdx.x) + 1);
+    if (u >= need * 0.9999f) atomicMin(&sh.lo_bin, static_cast<int>(threadIdx.x));
+    if (l >= need * 1.0001f) atomicMin(&sh.hi_bin, static_cast<int>(threadIdx.x));
     __syncthreads();
   }
-  __device__ __forceinline__ void find_sum(const uint2& n, unsigned long long w0, unsigned long long w1, unsigned long long need) {
-    const unsigned long long s0 = n.x * w0, s1 = n.y * w1;
-    const unsigned long long a = scan<unsigned long long>(s0 + s1, sh.warp_sum);
-    if (a < need && need <= a + s0 + s1) sh.lo_bin = sh.hi_bin = 2 * threadIdx.x + (a + s0 < need ? 1 : 0);
+  __device__ __forceinline__ void find_sum(uint32_t n, unsigned long long w, unsigned long long need) {
+    const unsigned long long s = n * w, a = scan<unsigned long long>(s, sh.warp_sum);
+    if (a < need && need <= a + s) sh.lo_bin = sh.hi_bin = threadIdx.x;
     __syncthreads();
+  }
+  // Tokens in bins b0 .. b1.
+  __device__ __forceinline__ uint32_t held(uint32_t n, int b0, int b1) {
+    const int b = threadIdx.x;
+    const uint32_t here = __reduce_add_sync(0xffffffffu, b >= b0 && b <= b1 ? n : 0u);
+    if (lane == 0) sh.warp_cnt[warp] = here;
+    __syncthreads();
+    const uint32_t all = __reduce_add_sync(0xffffffffu, sh.warp_cnt[lane]);
+    __syncthreads();
+    return all;
+  }
+  // A sum over the block's threads.
+  __device__ __forceinline__ unsigned long long block_add(unsigned long long v) {
+    v = warp_add(v);
+    if (lane == 0) sh.warp_sum[warp] = v;
+    __syncthreads();
+    v = warp_add(sh.warp_sum[lane]);
+    __syncthreads();
+    return v;
   }
 
   // Where a running sum over the row in index order first reaches `need` (of counts of
@@ -349,45 +389,111 @@ struct Sampler {
   __device__ __forceinline__ void locate(unsigned long long mine, unsigned long long before, unsigned long long need, F&& f) {
     if (lane == 0) sh.warp_sum[warp] = mine;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
-    if (before < need && need <= before + mine) {
-      for (int i = 0; i < row.count; i += 32) {
-        unsigned long long t[Slice<F32>::kVec], own = 0;
-        float xs[Slice<F32>::kVec];
-        int at = 0;
-        row.one(i, lane, [&](const float (&x)[Slice<F32>::kVec], int idx) {
-          at = idx;
+    // the warp that has it, then its rounds of 32 vectors, one a warp (13 at most)
+    unsigned long long x = sh.warp_sum[lane], own = x;
 #pragma unroll
-          for (int e = 0; e < Slice<F32>::kVec; ++e) {
-            xs[e] = x[e];
-            t[e] = f(x[e], idx + e);
-            own += t[e];
-          }
-        });
-        unsigned long long s = own;
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const uint32_t who = __ballot_sync(0xffffffffu, before + x - own < need && need <= before + x);
+    __syncthreads();
+    if (who == 0) return;
+    const int w = __ffs(who) - 1;
+    before += __shfl_sync(0xffffffffu, x - own, w);
+    const int v0 = min(w * row.per, row.vecs), n = min(row.per, row.vecs - v0);
+    constexpr int kVec = Slice<F32>::kVec;
+    unsigned long long t[kVec];
+    float xs[kVec];
+    int at = 0;
+    own = 0;
+    if (warp * 32 < n)
+      row.one(v0 + warp * 32 + lane, warp * 32 + lane < n, [&](const float (&y)[kVec], int idx) {
+        at = idx;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned long long y = __shfl_up_sync(0xffffffffu, s, o);
-          if (lane >= o) s += y;
+        for (int e = 0; e < kVec; ++e) {
+          xs[e] = y[e];
+          t[e] = f(y[e], idx + e);
+          own += t[e];
         }
-        const unsigned long long total = __shfl_sync(0xffffffffu, s, 31);
-        unsigned long long a = before + s - own;
-        if (a < need && need <= a + own) {
+      });
+    const unsigned long long round = warp_add(own);
+    if (lane == 0) sh.warp_sum[warp] = round;
+    __syncthreads();
+    before += warp_add(lane < warp ? sh.warp_sum[lane] : 0ull);
+    if (before < need && need <= before + round) {
+      unsigned long long s = own;
 #pragma unroll
-          for (int e = 0; e < Slice<F32>::kVec; ++e) {
-            if (a < need && need <= a + t[e]) {
-              sh.at_index = at + e;
-              sh.at_x = xs[e];
-              sh.at_sum = t[e];
-            }
-            a += t[e];
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+      }
+      unsigned long long a = before + s - own;
+      if (a < need && need <= a + own) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          if (a < need && need <= a + t[e]) {
+            sh.at_index = at + e;
+            sh.at_x = xs[e];
+            sh.at_sum = t[e];
           }
+          a += t[e];
         }
-        before += total;
-        if (before >= need) break;
       }
     }
   }
+
+  // All blocks' candidates (of the exchange of parity ph): one a thread, 0 where there is
+  // none; returns how many there are (more than kSmList: not all of them).
+  __device__ __forceinline__ uint32_t collect(uint32_t ph, unsigned long long* mine) {
+    const uint32_t m = static_cast<uint32_t>(lane) < blocks ? peer_load(&sh.fill[ph], lane) : 0u;
+    uint32_t end = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += y;
+    }
+    const uint32_t n = __shfl_sync(0xffffffffu, end, 31);
+    *mine = 0;
+    if (n > kSmList) return n;
+    // the block whose range the thread is in: as many ends as are at most its number
+    uint32_t r = 0, first = 0;
+    for (uint32_t k = 0; k + 1 < blocks; ++k) {
+      const uint32_t e = __shfl_sync(0xffffffffu, end, k);
+      if (threadIdx.x >= e) {
+        r = k + 1;
+        first = e;
+      }
+    }
+    if (threadIdx.x < n) *mine = peer_load(&sh.list[ph][threadIdx.x - first], r);
+    return n;
+  }
+  __device__ __forceinline__ void offer(uint32_t ph, float x, int idx) {
+    const uint32_t at = atomicAdd(&sh.fill[ph], 1u);
+    if (at < kSmList) sh.list[ph][at] = static_cast<unsigned long long>(float_key(x)) << 32 | static_cast<uint32_t>(~idx);
+  }
+  // Bitonic sort of the threads' first n candidates, the largest first.
+  __device__ __forceinline__ unsigned long long sorted(unsigned long long v, uint32_t n) {
+    uint32_t set = 0;
+    for (uint32_t k = 2; k == 2 || k < 2 * n; k <<= 1)
+      for (uint32_t j = k >> 1; j > 0; j >>= 1) {
+        unsigned long long o;
+        if (j < 32) {
+          o = __shfl_xor_sync(0xffffffffu, v, j);
+        } else {
+          sh.sort[set][threadIdx.x] = v;
+          __syncthreads();
+          o = sh.sort[set][threadIdx.x ^ j];
+          set ^= 1;
+        }
+        const bool first = (threadIdx.x & j) == 0, down = (threadIdx.x & k) == 0;
+        v = first == down ? max(v, o) : min(v, o);
+      }
+    return v;
+  }
+  // A candidate's value and index.
+  __device__ __forceinline__ static float value_of(unsigned long long c) { return key_float(static_cast<uint32_t>(c >> 32)); }
+  __device__ __forceinline__ static int index_of(unsigned long long c) { return static_cast<int>(~static_cast<uint32_t>(c)); }
 
   // The cut: the last of the first `need` tokens of the ranking, or the token with which
   // the weights' running sum reaches `need` (of the tokens up to the cut (cx, ci) that is
@@ -403,13 +509,13 @@ struct Sampler {
     const float ox = *cx;
     const int oi = *ci;
     const auto kept = [&](float x, int idx) { return x > ox || (x == ox && idx <= oi); };
+    listed = false;
     // (four rounds from all values, seldom more. The bound is for what should not be.)
     for (int round = 0; round < 20; ++round) {
       const uint32_t klo = float_key(lo), khi = float_key(hi);
       const uint32_t ph = phase & 1;
       if (lo == hi && !few) break;
-      float unused;
-      const int ghi = grid_of(sc, hi, &unused), span = ghi - grid_of(sc, lo, &unused);
+      const int ghi = grid_of(sc, hi), span = ghi - grid_of(sc, lo);
       const bool by_grid = SUM && span >= kGridSpan && round < 10;
       int shift = 0;
       while ((by_grid ? static_cast<uint32_t>(span) : khi - klo) >> shift >= kSmBins) ++shift;
@@ -420,25 +526,32 @@ struct Sampler {
       unsigned long long above = 0;
       uint32_t n = 0;
       row.each([&](const float (&x)[Slice<F32>::kVec], int idx) {
+        float most = x[0];
 #pragma unroll
-        for (int e = 0; e < Slice<F32>::kVec; ++e) {
-          if (x[e] > hi) {
-            ++n;
-            if (kept(x[e], idx + e)) above += weight_of(sc, sh.tab, x[e]);
-          }
-          const bool in = x[e] >= lo && x[e] <= hi && (!SUM || kept(x[e], idx + e));
-          if (few) {
-            if (in) {
-              const uint32_t at = atomicAdd(&sh.fill[ph], 1u);
-              if (at < kSmList) sh.list[ph][at] = make_uint2(__float_as_uint(x[e]), idx + e);
-            }
-          } else {
-            int bin;
-            if (by_grid) bin = in ? (ghi - grid_of(sc, x[e], &unused)) >> shift : 0;
-            else bin = static_cast<int>((khi - float_key(x[e])) >> shift);
-            count(hist, bin, in);
+        for (int e = 1; e < Slice<F32>::kVec; ++e) most = fmaxf(most, x[e]);
+        if (!__any_sync(0xffffffffu, most >= lo)) return;
+        if (__any_sync(0xffffffffu, most > hi)) {
+#pragma unroll
+          for (int e = 0; e < Slice<F32>::kVec; ++e) {
+            const unsigned long long w = weight_of(sc, sh.tab, x[e]);
+            const bool over = x[e] > hi;
+            n += over ? 1u : 0u;
+            above += over && kept(x[e], idx + e) ? w : 0ull;
           }
         }
+        int bin[Slice<F32>::kVec];
+#pragma unroll
+        for (int e = 0; e < Slice<F32>::kVec; ++e) {
+          const bool in = x[e] >= lo && x[e] <= hi && (!SUM || kept(x[e], idx + e));
+          if (few) {
+            if (in) offer(ph, x[e], idx + e);
+          } else {
+            if (by_grid) bin[e] = (ghi - grid_of(sc, x[e])) >> shift;
+            else bin[e] = static_cast<int>((khi - float_key(x[e])) >> shift);
+            if (!in) bin[e] = -1;
+          }
+        }
+        if (!few) count(hist, bin);
       });
       const Sums s = exchange(above, n);
       if (SUM ? s.sum >= need : s.cnt >= need) {   // (the range does not hold it: from all values)
@@ -448,39 +561,17 @@ struct Sampler {
         continue;
       }
       if (few) {
-        // all candidates in every block; each is ranked against the others
-        uint32_t at = 0;
-        for (uint32_t r = 0; r < blocks; ++r) {
-          const uint32_t m = min(peer_load(&sh.fill[ph], r), static_cast<uint32_t>(kSmList));
-          for (uint32_t i = threadIdx.x; i < m && at + i < kSmList; i += kSmThreads) {
-            const unsigned long long v = peer_load(reinterpret_cast<const unsigned long long*>(&sh.list[ph][i]), r);
-            sh.all[at + i] = make_uint2(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
-          }
-          at = min(at + m, static_cast<uint32_t>(kSmList));
-        }
-        __syncthreads();
-        for (uint32_t i = threadIdx.x; i < at; i += kSmThreads) sh.weight[i] = weight_of(sc, sh.tab, __uint_as_float(sh.all[i].x));
         if (threadIdx.x == 0) sh.at_index = -1;
-        __syncthreads();
-        for (uint32_t i = threadIdx.x; i < at; i += kSmThreads) {
-          const float x = __uint_as_float(sh.all[i].x);
-          const uint32_t idx = sh.all[i].y;
-          unsigned long long w = 0;
-          uint32_t r = 0;
-          for (uint32_t k = 0; k < at; ++k) {
-            const uint2 o = sh.all[k];
-            const float ox2 = __uint_as_float(o.x);
-            if (ox2 > x || (ox2 == x && o.y < idx)) {
-              ++r;
-              w += sh.weight[k];
-            }
-          }
-          const unsigned long long a = SUM ? s.sum + w : static_cast<unsigned long long>(s.cnt + r);
-          if (a < need && need <= a + (SUM ? sh.weight[i] : 1ull)) {
-            sh.at_index = static_cast<int>(idx);
-            sh.at_x = x;
-            sh.at_sum = s.sum + w + sh.weight[i];
-          }
+        const uint32_t all = collect(ph, &cand);
+        cand = sorted(cand, min(all, static_cast<uint32_t>(kSmList)));
+        const bool in = threadIdx.x < all && all <= kSmList;
+        const unsigned long long own = in ? weight_of(sc, sh.tab, value_of(cand)) : 0ull;
+        const unsigned long long before = s.sum + scan<unsigned long long>(own, sh.warp_sum);
+        const unsigned long long a = SUM ? before : static_cast<unsigned long long>(s.cnt + threadIdx.x);
+        if (in && a < need && need <= a + (SUM ? own : 1ull)) {
+          sh.at_index = index_of(cand);
+          sh.at_x = value_of(cand);
+          sh.at_sum = before + own;
         }
         __syncthreads();
         const int found = sh.at_index;
@@ -489,6 +580,11 @@ struct Sampler {
           *ci = found;
           const unsigned long long sum = sh.at_sum;
           __syncthreads();
+          listed = true;
+          list_above = above;
+          list_sums = s;
+          list_top = hi;
+          if (!in) cand = 0;
           return sum;
         }
         // (not among them: from all values, by counts alone)
@@ -498,40 +594,28 @@ struct Sampler {
         hi = sc.top;
         continue;
       }
-      const uint2 m = bins(hist);
-      const uint32_t k0 = khi - ((2 * threadIdx.x) << shift), k1 = khi - ((2 * threadIdx.x + 1) << shift);   // the bins' top keys
+      const uint32_t m = bins(hist);
+      const uint32_t top_key = khi - (threadIdx.x << shift);   // of the thread's bin
       if constexpr (SUM) {
         const unsigned long long rest = need - s.sum;
         if (by_grid) {
           // (a grid point to spare on either side)
-          const float unit = static_cast<float>(0x1p62 / static_cast<double>(1ull << sc.lg));
-          const auto w = [&](int g) { return exp2f(static_cast<float>(min(g, 0)) * (1.0f / 512.0f)) * unit; };
-          const int g = ghi - ((2 * static_cast<int>(threadIdx.x)) << shift), step = 1 << shift;
-          find_bounds(m, make_float2(w(g - step), w(g - 2 * step)), make_float2(w(g + 1), w(g - step + 1)), static_cast<float>(rest));
+          const auto w = [&](int g) { return exp2f(static_cast<float>(min(g, 1)) * (1.0f / 512.0f)) * unit(); };
+          const int g = ghi - (static_cast<int>(threadIdx.x) << shift), step = 1 << shift;
+          find_bounds(m * w(g - step), m * w(g + 1), static_cast<float>(rest));
         } else if (shift == 0) {
-          const unsigned long long w0 = m.x ? weight_of(sc, sh.tab, key_float(k0)) : 0ull;
-          const unsigned long long w1 = m.y ? weight_of(sc, sh.tab, key_float(k1)) : 0ull;
-          find_sum(m, w0, w1, rest);
+          find_sum(m, m ? weight_of(sc, sh.tab, key_float(top_key)) : 0ull, rest);
         } else {
-          const uint32_t step = (1u << shift) - 1;
-          const auto w = [&](uint32_t k) { return static_cast<float>(weight_of(sc, sh.tab, key_float(k))); };
-          const float2 upper = make_float2(m.x ? w(k0) : 0.f, m.y ? w(k1) : 0.f);
-          const float2 lower = make_float2(m.x ? w(max(klo, k0 - step)) : 0.f, m.y ? w(max(klo, k1 - step)) : 0.f);
-          find_bounds(m, lower, upper, static_cast<float>(rest));
+          const auto w = [&](uint32_t k) { return m ? static_cast<float>(weight_of(sc, sh.tab, key_float(k))) : 0.f; };
+          find_bounds(m * w(max(klo, top_key - ((1u << shift) - 1))), m * w(top_key), static_cast<float>(rest));
         }
       } else {
         find_count(m, static_cast<uint32_t>(need) - s.cnt);
       }
       const int b0 = sh.lo_bin, b1 = sh.hi_bin;
       // how many tokens those bins hold (and, of the grid's, those whose tokens the new range may hold)
-      const int more = by_grid ? (3 >> shift) + 1 : 0, bin = 2 * static_cast<int>(threadIdx.x);
-      const bool in0 = bin >= b0 - more && bin <= b1 + more, in1 = bin + 1 >= b0 - more && bin + 1 <= b1 + more;
-      const uint32_t here = __reduce_add_sync(0xffffffffu, (in0 ? m.x : 0u) + (in1 ? m.y : 0u));
-      if (lane == 0) sh.warp_cnt[warp] = here;
-      __syncthreads();
-      uint32_t left = 0;
-      for (int w = 0; w < kSmWarps; ++w) left += sh.warp_cnt[w];
-      __syncthreads();
+      const int more = by_grid ? (3 >> shift) + 1 : 0;
+      const uint32_t left = held(m, b0 - more, b1 + more);
       if (by_grid) {
         const float inv = 1.0f / (512.0f * sc.ch);
         const int g0 = ghi - (b0 << shift) + 2, g1 = ghi - ((b1 + 1) << shift) - 2;
@@ -601,6 +685,8 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / kBytes;
   const int vecs = (off + len + kVec - 1) / kVec, per = (vecs + kSmWarps - 1) / kSmWarps;
   s.row.img = reinterpret_cast<const uint4*>(img);
+  s.row.vecs = vecs;
+  s.row.per = per;
   s.row.first = min(s.warp * per, vecs);
   s.row.count = min(per, vecs - s.row.first);
   s.row.index0 = t0 - off;
@@ -622,38 +708,56 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     }
   }
   cp_async_commit();
-  for (int i = threadIdx.x; i < 512; i += kSmThreads) sh.tab[i] = make_uint2(g_pow2.f[i], g_pow2.i[i]);
+  for (int i = threadIdx.x; i < 512; i += kSmThreads) sh.tab[i] = g_pow2.v[i];
   // the row's settings
   const float heat = p.heat ? __ldg(p.heat + r) : 1.0f;
   const int k = p.top_k ? __ldg(p.top_k + r) : 0;
   const float tp = p.top_p ? __ldg(p.top_p + r) : 1.0f;
   const float mp = p.min_p ? __ldg(p.min_p + r) : 0.0f;
-  if (threadIdx.x == 0) sh.row_c = fmin(1.4426950408889634074 / static_cast<double>(heat), 0x1p100);
-  if (threadIdx.x == 32) {
-    // (x >= max + T ln min_p: added to the maximum in 64 bits below)
-    sh.row_low = mp > 0.f ? static_cast<double>(heat) * log(static_cast<double>(fminf(mp, 1.0f))) : -INFINITY;
-  }
+  // (64-bit arithmetic is slow here: one thread's, beside the load)
+  const auto pair = [](double v) {
+    const float hi = static_cast<float>(v);
+    return make_float2(hi, static_cast<float>(v - static_cast<double>(hi)));
+  };
+  if (threadIdx.x == 0) sh.row_c = pair(fmin(1.4426950408889634074 / static_cast<double>(heat), 0x1p100));
+  if (threadIdx.x == 32 && mp > 0.f) sh.row_low = pair(static_cast<double>(heat) * log(static_cast<double>(fminf(mp, 1.0f))));
+  const bool by_k = heat > 0.f && k > 0 && k < p.vocab, by_p = heat > 0.f && tp < 1.0f;
+  const bool list_k = by_k && k <= kSmFewK, list_p = by_p && !by_k;
+  sh.hist[0][threadIdx.x] = sh.hist[1][threadIdx.x] = sh.below[1][threadIdx.x] = 0;
+  if (threadIdx.x == 64) sh.lo_bin = -1;
   cp_async_wait<0>();
   // the largest logit
-  float top = -INFINITY;
+  float own = -INFINITY;
   s.row.each([&](const float (&x)[kVec], int) {
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) top = fmaxf(top, x[e]);        // (NaN: passed over)
+    for (int e = 0; e < kVec; ++e) own = fmaxf(own, x[e]);        // (NaN: passed over)
   });
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (s.lane == 0) sh.warp_bound[s.warp].x = top;
+  float top = warp_max(own);
+  if (s.lane == 0) sh.warp_bound[s.warp] = top;
   __syncthreads();
+  top = warp_max(sh.warp_bound[s.lane]);
+  // and a value that enough tokens reach for a list: the threads' largest ones, counted
+  // in bins 1 / 16 of log2 of the weight wide below the block's
+  float low = -INFINITY;
+  if (list_k || list_p) {
+    const float ch = 16.0f * sh.row_c.x;
+    const float b = fminf((top - own) * ch, static_cast<float>(kSmBins - 1));       // (NaN: no bin)
+    if (b < kSmBins - 1) atomicAdd(&sh.hist[0][static_cast<int>(b)], 1u);
+    __syncthreads();
+    const uint32_t want = ((list_k ? k : kSmFewP) + blocks - 1) / blocks;
+    s.find_count(sh.hist[0][threadIdx.x], want);
+    if (sh.lo_bin >= 0) low = __fsub_rd(top, __fmul_ru(static_cast<float>(sh.lo_bin) + 1.01f, 1.0f / ch));
+  }
   const uint32_t ph = s.phase++ & 1;
   if (threadIdx.x == 0) {
-#pragma unroll
-    for (int w = 0; w < kSmWarps; ++w) top = fmaxf(top, sh.warp_bound[w].x);
     sh.top[ph] = top;
+    sh.low[ph] = low;
   }
+  if (threadIdx.x == 32) sh.fill[1] = 0;
   blocks_sync(blocks);
-  top = s.lane < blocks ? peer_load(&sh.top[ph], s.lane) : -INFINITY;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool peer = static_cast<uint32_t>(s.lane) < s.blocks;
+  top = warp_max(peer ? peer_load(&sh.top[ph], s.lane) : -INFINITY);
+  low = -warp_max(peer ? -peer_load(&sh.low[ph], s.lane) : -INFINITY);
 
   if (!(top > -INFINITY)) {                                       // nothing to take
     if (s.rank == 0 && threadIdx.x == 0) {
@@ -665,52 +769,146 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   }
   const bool greedy = !(heat > 0.f) || top == INFINITY;
   Scale& sc = s.sc;
-  const double c = sh.row_c;
   sc.top = top;
-  sc.ch = static_cast<float>(c);
-  sc.cl = static_cast<float>(c - static_cast<double>(sc.ch));
+  sc.ch = sh.row_c.x;
+  sc.cl = sh.row_c.y;
   sc.b = fabsf(top) * sc.ch < 4096.0f ? 0.f : top;
-  const float t_top = (top - sc.b) * sc.ch + kGrid;
+  const float d_top = top - sc.b, p_top = __fmul_rn(d_top, sc.ch), t_top = __fadd_rn(p_top, kGrid);
   sc.base = __float_as_int(t_top);
-  sc.rest = static_cast<float>(static_cast<double>(top - sc.b) * c - static_cast<double>(t_top - kGrid));
+  sc.rest = (p_top - (t_top - kGrid)) + fmaf(d_top, sc.cl, fmaf(d_top, sc.ch, -p_top));   // within 2^-10 of 0
   sc.floor = (t_top - kGrid) - 80.0f;
   sc.lg = p.lg;
+  // a cutoff that does not depend on the others: the least x >= max + T ln min_p
+  float least = -INFINITY;
+  if (!greedy && mp > 0.f) {
+    const float2 v = sh.row_low;
+    const float a = __fadd_rn(top, v.x), b = __fsub_rn(a, top);
+    const float e = __fadd_rn(__fadd_rn(__fsub_rn(top, __fsub_rn(a, b)), __fsub_rn(v.x, b)), v.y);   // what a is short of
+    least = e > 0.f ? __fadd_ru(a, 1.17549435e-38f) : a;
+  }
+  float u = __ldg(p.u + r);
+  u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
+  const auto fraction = [](float v) {                              // v 2^64, 0 <= v < 1
+    const uint32_t bits = __float_as_uint(v);
+    const int e = static_cast<int>(bits >> 23) - 86;               // v = mantissa 2^(e + 86 - 150)
+    const unsigned long long m = (bits & 0x7fffffu) | 0x800000u;
+    return e <= -24 ? 0ull : e < 0 ? m >> -e : m << e;
+  };
+  const auto drawn = [&](unsigned long long sum) { return __umul64hi(fraction(u), sum) + 1; };   // the running sum that the token reaches
+  const auto answer = [&](int token, float x, unsigned long long w, unsigned long long sum) {
+    p.tokens[r] = token;
+    if (!p.logprobs) return;
+    float lp = 0.f;
+    if (!greedy) {
+      const unsigned long long rest = sum - w;
+      if (rest < w) {
+        lp = log1pf(-(static_cast<float>(rest) / static_cast<float>(sum)));
+      } else {
+        lp = (x - top) / heat + sc.rest * 0.69314718f - logf(static_cast<float>(sum) * (1.0f / s.unit()));
+      }
+    }
+    p.logprobs[r] = lp;
+  };
+  // the least sum that is top-p's share of `sum`, rounded up
+  const auto share = [&](unsigned long long sum) {
+    const unsigned long long f = tp > 0.f ? fraction(tp) : 0ull;
+    return max(__umul64hi(f, sum) + (f * sum != 0 ? 1 : 0), 1ull);
+  };
 
   float cx = -INFINITY;                                           // the cut: nothing yet
   int ci = 0x7fffffff;
   unsigned long long total = 0;
-  const bool by_k = !greedy && k > 0 && k < p.vocab, by_p = !greedy && tp < 1.0f;
-  if (greedy) {
-    cx = top;                                                     // (the lowest index of it, found below)
-  } else if (by_k || by_p) {
-    // counts by the weights' logarithm, and the sum of all weights where top-p is of all
-    uint32_t* hist = s.clear_hist();
-    unsigned long long all = 0;
-    s.row.each([&](const float (&x)[kVec], int) {
+  bool counted = false;
+  if (greedy || list_k || list_p) {
+    // what reaches `low` (greedy: the largest), in a list; with top-p alone, the sum of all
+    // weights and the counts too
+    if (greedy) low = top;
+    const uint32_t lp = s.phase & 1;
+    counted = list_p && !greedy;
+    unsigned long long sum = 0;
+    s.row.each([&](const float (&x)[kVec], int idx) {
+      if (counted) {
+        int g[kVec];
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const int b = bin_of(sc, x[e]);
-        s.count(hist, b, b < kSmBins - 1);
-        if (by_p && !by_k) all += weight_of(sc, sh.tab, x[e]);
+        for (int e = 0; e < kVec; ++e) sum += weight_of(sc, sh.tab, x[e], &g[e]);
+        s.count_grid(sh.hist[lp], sh.below[lp], g);
       }
+      float most = x[0];
+#pragma unroll
+      for (int e = 1; e < kVec; ++e) most = fmaxf(most, x[e]);
+      if (!(most >= low) || most == -INFINITY) return;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e)
+        if (x[e] >= low && x[e] > -INFINITY) s.offer(lp, x[e], idx + e);
     });
-    const Sums sums = s.exchange(all, 0);
-    total = sums.sum;
-    const uint2 n = s.bins(hist);
+    total = s.exchange(sum, 0).sum;
+    const uint32_t n = s.collect(lp, &s.cand);
+    bool fits = n <= kSmList;
+    if (greedy && fits) {
+      if (threadIdx.x == 0) sh.at_index = 0x7fffffff;
+      __syncthreads();
+      if (s.cand) atomicMin(&sh.at_index, s.index_of(s.cand));
+      __syncthreads();
+      if (s.rank == 0 && threadIdx.x == 0) answer(sh.at_index, top, 1, 1);
+      blocks_sync(blocks);
+      return;
+    }
+    fits = fits && !greedy && (!list_k || n >= k || low == -INFINITY);
+    if (fits) {
+      s.cand = s.sorted(s.cand, n);
+      const bool in = threadIdx.x < n;
+      if (!in) s.cand = 0;
+      const unsigned long long w = in ? weight_of(sc, sh.tab, s.value_of(s.cand)) : 0ull;
+      const unsigned long long before = s.template scan<unsigned long long>(w, sh.warp_sum);
+      // the last token that is kept: of the first k, the one that reaches top-p's share
+      const uint32_t last = list_k ? min(static_cast<uint32_t>(k), n) - 1 : n - 1;
+      if (threadIdx.x == last) sh.at_sum = before + w;
+      if (threadIdx.x == 0) sh.at_index = -1;
+      __syncthreads();
+      const unsigned long long of = list_k ? sh.at_sum : total, need = by_p ? share(of) : of;
+      if (by_p ? in && before < need && need <= before + w : threadIdx.x == last) {
+        sh.at_index = s.index_of(s.cand);
+        sh.at_x = s.value_of(s.cand);
+      }
+      __syncthreads();
+      if (sh.at_index >= 0) {
+        cx = sh.at_x;
+        ci = sh.at_index;
+        s.listed = true;
+        s.list_above = 0;
+        s.list_sums = Sums{0, 0, 0, 0};
+        s.list_top = INFINITY;
+      }
+      __syncthreads();
+    }
+  }
+  if (s.listed) {
+  } else if (greedy) {
+    s.template cut<false>(1, top, top, false, &cx, &ci);          // (more of the largest than a list holds)
+  } else if (by_k || by_p) {
+    // counts by the weights' logarithm, bins of 32 grid points
+    uint32_t ph2 = 1;
+    if (!counted) {
+      ph2 = s.phase & 1;
+      sh.below[ph2][threadIdx.x] = 0;
+      uint32_t* hist = s.clear_hist();
+      s.row.each([&](const float (&x)[kVec], int) {
+        int g[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) g[e] = grid_of(sc, x[e]);
+        s.count_grid(hist, sh.below[ph2], g);
+      });
+      s.exchange(0, 0);
+    }
+    const uint32_t n = s.bins(sh.hist[ph2]);
     const float inv_c = 1.0f / sc.ch;
-    // values that surely hold all of bins b0 .. b1 (a bin more on either side), and
-    // whether a list holds those bins' tokens
+    // values that surely hold all of bins b0 .. b1 (two grid points more on either side), and
+    // whether a list holds these bins' tokens and their neighbours'
     const auto range = [&](int b0, int b1, float* lo, float* hi) {
-      const int a0 = b0 - 1, a1 = b1 + 1, mine = 2 * static_cast<int>(threadIdx.x);
-      const uint32_t here = __reduce_add_sync(0xffffffffu, (mine >= a0 && mine <= a1 ? n.x : 0u) + (mine + 1 >= a0 && mine + 1 <= a1 ? n.y : 0u));
-      if (s.lane == 0) sh.warp_cnt[s.warp] = here;
-      __syncthreads();
-      uint32_t left = 0;
-      for (int w = 0; w < kSmWarps; ++w) left += sh.warp_cnt[w];
-      __syncthreads();
-      *hi = b0 <= 1 ? top : fminf(top, __fsub_ru(top, __fmul_rd(static_cast<float>(b0) / 16.0f - 1.0f / 32.0f, inv_c)));
-      *lo = __fsub_rd(top, __fmul_ru(static_cast<float>(b1 + 1) / 16.0f + 1.0f / 32.0f, inv_c));
-      return left <= kSmList && a1 < kSmBins - 1;
+      const uint32_t left = s.held(n, b0 - 1, b1 + 1);
+      *hi = b0 <= 0 ? top : fminf(top, __fsub_ru(top, __fmul_rd(static_cast<float>(32 * b0 - 2) * (1.0f / 512.0f), inv_c)));
+      *lo = __fsub_rd(top, __fmul_ru(static_cast<float>(32 * (b1 + 1) + 2) * (1.0f / 512.0f), inv_c));
+      return left <= kSmList && b1 + 1 < kSmBins - 1;
     };
     float lo, hi;
     bool cut_k = false;
@@ -734,15 +932,14 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       }
     }
     if (by_p) {
-      // the least sum that is p of the total, rounded up
-      const unsigned long long pf = tp > 0.f ? static_cast<unsigned long long>(static_cast<double>(tp) * 0x1p64) : 0ull;
-      unsigned long long need = __umul64hi(pf, total) + (pf * total != 0 ? 1 : 0);
-      need = max(need, 1ull);
-      const float unit = static_cast<float>(0x1p62 / static_cast<double>(1ull << p.lg));   // the largest weight
-      const auto edge = [&](int b) { return exp2f(-static_cast<float>(b) / 16.0f) * unit; };
-      const int b = 2 * threadIdx.x;
-      s.find_bounds(n, make_float2(edge(b + 1) * 0.997f, edge(b + 2) * 0.997f), make_float2(edge(b) * 1.003f, edge(b + 1) * 1.003f),
-                    static_cast<float>(need));
+      // A bin's n tokens lie `m` grid points below its edge, between 0 and 31 each (rounded:
+      // half a point more or less). 2^-x is convex: they weigh at least n times the weight
+      // at their mean, at most what the chord from 0 to 31 gives.
+      const unsigned long long need = share(total);
+      const float m = s.bins(sh.below[ph2]), edge = -32.0f * threadIdx.x;
+      const auto w = [&](float g) { return exp2f(g * (1.0f / 512.0f)) * s.unit(); };
+      const float l = n && threadIdx.x < 700 ? n * w(edge - m / n - 0.52f) : 0.f, w0 = w(edge + 0.52f), w1 = w(edge - 30.48f);
+      s.find_bounds(l, n * w0 + m * (1.0f / 31.0f) * (w1 - w0), static_cast<float>(need));
       const int b0 = sh.lo_bin, b1 = sh.hi_bin;
       __syncthreads();
       const bool few = range(b0, b1, &lo, &hi);
@@ -753,54 +950,50 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       total = s.template cut<true>(need, lo, hi, few, &cx, &ci);
     }
   }
-  if (!greedy && mp > 0.f) {
-    const float f = __double2float_ru(static_cast<double>(top) + sh.row_low);
-    if (f > cx) {
-      cx = f;
-      ci = 0x7fffffff;
-    }
+  if (least > cx) {
+    cx = least;
+    ci = 0x7fffffff;
   }
   // the draw: the first token in index order at which the kept weights' sum exceeds u of all
   const auto term = [&](float x, int idx) -> unsigned long long {
-    if (!(x > cx || (x == cx && idx <= ci))) return 0ull;
-    return greedy ? 1ull : weight_of(sc, sh.tab, x);
+    const unsigned long long w = greedy ? 1ull : weight_of(sc, sh.tab, x);
+    return x > cx || (x == cx && idx <= ci) ? w : 0ull;
   };
-  unsigned long long sum = 0;
-  s.row.each([&](const float (&x)[kVec], int idx) {
+  unsigned long long mine, before, sum;
+  if (s.listed && least <= s.list_top) {
+    // all that is kept lies above the list, or in it
+    const bool in = s.cand != 0;
+    const float x = s.value_of(s.cand);
+    const int idx = s.index_of(s.cand), owner = in ? idx / p.slice : 0;
+    const unsigned long long w = in ? term(x, idx) : 0ull;
+    if (threadIdx.x < kSmWarps) sh.cand_sum[threadIdx.x] = 0;
+    __syncthreads();
+    if (w && owner == static_cast<int>(s.rank)) atomicAdd(&sh.cand_sum[(idx - s.row.index0) / kVec / per], w);
+    before = s.list_sums.sum_before + s.block_add(owner < static_cast<int>(s.rank) ? w : 0ull);
+    sum = s.list_sums.sum + s.block_add(w);
+    mine = warp_add(s.list_above) + sh.cand_sum[s.warp];
+  } else {
+    unsigned long long own_sum = 0;
+    s.row.each([&](const float (&x)[kVec], int idx) {
+      float most = x[0];
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) sum += term(x[e], idx + e);
-  });
-  const Sums all = s.exchange(sum, 0);
-  unsigned long long need = 1;
-  if (!greedy) {
-    float u = __ldg(p.u + r);
-    u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
-    need = __umul64hi(static_cast<unsigned long long>(static_cast<double>(u) * 0x1p64), all.sum) + 1;
+      for (int e = 1; e < kVec; ++e) most = fmaxf(most, x[e]);
+      if (!__any_sync(0xffffffffu, most >= cx)) return;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) own_sum += term(x[e], idx + e);
+    });
+    const Sums all = s.exchange(own_sum, 0);
+    mine = warp_add(own_sum);
+    before = all.sum_before;
+    sum = all.sum;
   }
-  const unsigned long long mine = warp_add(sum);
   if (threadIdx.x == 0) sh.at_index = -1;
   __syncthreads();
-  s.locate(mine, all.sum_before, need, term);
+  s.locate(mine, before, greedy ? 1ull : drawn(sum), term);
   __syncthreads();
-  if (threadIdx.x == 0 && sh.at_index >= 0) {                     // one block has it
-    p.tokens[r] = sh.at_index;
-    if (p.logprobs) {
-      float lp = 0.f;
-      if (!greedy) {
-        const unsigned long long rest = all.sum - sh.at_sum;
-        if (rest < sh.at_sum) {
-          lp = log1pf(-static_cast<float>(static_cast<double>(rest) / static_cast<double>(all.sum)));
-        } else {
-          const double unit = 0x1p62 / static_cast<double>(1ull << p.lg);
-          lp = (sh.at_x - top) / heat - logf(static_cast<float>(static_cast<double>(all.sum) / unit));
-        }
-      }
-      p.logprobs[r] = lp;
-    }
-  }
+  if (threadIdx.x == 0 && sh.at_index >= 0) answer(sh.at_index, sh.at_x, sh.at_sum, sum);   // (one block has it)
   blocks_sync(blocks);                                            // (nobody reads a block that has gone)
 }
-
 
 template <bool F32>
 cudaError_t launch_sample(SampleParams p, int f16, int sms, cudaStream_t st) {
