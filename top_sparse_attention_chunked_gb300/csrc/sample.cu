@@ -9,7 +9,7 @@
 //
 // A draw between 100,000 tokens is next to a border nearly always, so weights and
 // sums have to be the same whatever the order: a weight is a multiple of a fixed unit
-// (2^-62 times the row's length, rounded up to a power of two, of the largest), formed
+// (of the largest, 2^-62 times the row's length rounded up to a power of two), formed
 // in fp32 pairs to 2^-31 of itself, and all sums are of 64-bit integers.
 //
 // A cluster of blocks holds a row in shared memory (read once); everything else is
@@ -114,6 +114,14 @@ __device__ __forceinline__ void blocks_sync(uint32_t blocks) {
   }
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// A block must not end while another may read it: it arrives once it has read the
+// others, and waits before it ends.
+__device__ __forceinline__ void blocks_leave(uint32_t blocks) {
+  if (blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void blocks_left(uint32_t blocks) {
+  if (blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // ---------------------------------------------------------------- weights
 constexpr float kGrid = 24576.0f;               // 1.5 * 2^14: adding it rounds to multiples of 1 / 512
@@ -127,7 +135,7 @@ constexpr int kZero = -44 * 512;                // weights from 2^-44 of the lar
 // relative to the grid point next to the largest x, `rest` below it.
 struct Scale {
   float b, ch, cl, floor, top, rest;
-  int base, lg;
+  int base, up;                                 // up: the exponent of the largest weight, over w's 30 bits
 };
 __device__ __forceinline__ int grid_of(const Scale& s, float x, float* frac) {
   const float d = x - s.b, p = d * s.ch;
@@ -148,11 +156,11 @@ __device__ __forceinline__ unsigned long long weight_of(const Scale& s, const ui
   const float q = r * fmaf(r, fmaf(r, 0.05550411f, 0.24022651f), 0.69314718f);
   // (t as a float: its upper 24 bits)
   const float w = fmaf(q, __uint_as_float((t >> 7) + ((127u + 29u) << 23)), kInt);
-  // w 2^32 >> (lg - exponent), its last place set: the middle of what was cut off
-  unsigned long long y;
-  asm("shr.u64 %0, %1, %2;" : "=l"(y)
-      : "l"(static_cast<unsigned long long>(t + (__float_as_uint(w) - __float_as_uint(kInt))) << 32), "r"(s.lg - (it >> 9)));
-  return it > kZero ? y | 1ull : 0ull;
+  // times 2^(up + exponent), a shift to the left as a product (one instruction with the
+  // sum's addition), the last place of one to the right set: the middle of what is cut off
+  const int e = (it >> 9) + s.up;
+  const uint32_t v = ((t + (__float_as_uint(w) - __float_as_uint(kInt))) >> max(-e, 0)) | 1u;
+  return it > kZero ? static_cast<unsigned long long>(v) * (1u << max(e, 0)) : 0ull;
 }
 __device__ __forceinline__ unsigned long long weight_of(const Scale& s, const uint32_t* tab, float x) {
   int it;
@@ -242,8 +250,8 @@ struct Sampler {
 
   __device__ __forceinline__ Sampler(const SampleParams& pp, SampleShared& s) : p(pp), sh(s) {}
 
-  // What weights are multiples of 2^-32 of (the largest is 2^rest times it).
-  __device__ __forceinline__ float unit() const { return __int_as_float((127 + 62 - sc.lg) << 23); }
+  // The weight of grid point 0 (the largest one is 2^rest times it).
+  __device__ __forceinline__ float unit() const { return __int_as_float((127 + 30 + sc.up) << 23); }
 
   // Adds up every thread's sum and count over the cluster.
   __device__ __forceinline__ Sums exchange(unsigned long long sum, uint32_t cnt) {
@@ -472,17 +480,20 @@ struct Sampler {
     const uint32_t at = atomicAdd(&sh.fill[ph], 1u);
     if (at < kSmList) sh.list[ph][at] = static_cast<unsigned long long>(float_key(x)) << 32 | static_cast<uint32_t>(~idx);
   }
-  // Bitonic sort of the threads' first n candidates, the largest first.
+  // Bitonic sort of the threads' first n candidates, the largest first. Only the warps
+  // that have some take part.
   __device__ __forceinline__ unsigned long long sorted(unsigned long long v, uint32_t n) {
-    uint32_t set = 0;
-    for (uint32_t k = 2; k == 2 || k < 2 * n; k <<= 1)
+    uint32_t size = 32, set = 0;
+    while (size < n) size <<= 1;
+    if (threadIdx.x >= size) return v;
+    for (uint32_t k = 2; k <= size; k <<= 1)
       for (uint32_t j = k >> 1; j > 0; j >>= 1) {
         unsigned long long o;
         if (j < 32) {
           o = __shfl_xor_sync(0xffffffffu, v, j);
         } else {
           sh.sort[set][threadIdx.x] = v;
-          __syncthreads();
+          named_bar_sync(1, size);
           o = sh.sort[set][threadIdx.x ^ j];
           set ^= 1;
         }
@@ -495,9 +506,78 @@ struct Sampler {
   __device__ __forceinline__ static float value_of(unsigned long long c) { return key_float(static_cast<uint32_t>(c >> 32)); }
   __device__ __forceinline__ static int index_of(unsigned long long c) { return static_cast<int>(~static_cast<uint32_t>(c)); }
 
+  // The cut among the candidates of the list of parity ph, which `above` tokens of weight
+  // `sum` rank before: the need-th token of the ranking, or the one with which the running
+  // sum reaches `need`. Whether it is there; *upto: the sum of weights up to it.
+  template <bool SUM>
+  __device__ __forceinline__ bool settle(uint32_t ph, unsigned long long sum, uint32_t above, unsigned long long need, float* cx,
+                                         int* ci, unsigned long long* upto) {
+    if (threadIdx.x == 0) sh.at_index = -1;
+    const uint32_t all = collect(ph, &cand);
+    cand = sorted(cand, min(all, static_cast<uint32_t>(kSmList)));
+    const bool in = threadIdx.x < all && all <= kSmList;
+    const unsigned long long own = in ? weight_of(sc, sh.tab, value_of(cand)) : 0ull;
+    const unsigned long long before = sum + scan<unsigned long long>(own, sh.warp_sum);
+    const unsigned long long a = SUM ? before : static_cast<unsigned long long>(above) + threadIdx.x;
+    if (in && a < need && need <= a + (SUM ? own : 1ull)) {
+      sh.at_index = index_of(cand);
+      sh.at_x = value_of(cand);
+      sh.at_sum = before + own;
+    }
+    __syncthreads();
+    listed = sh.at_index >= 0;
+    if (listed) {
+      *cx = sh.at_x;
+      *ci = sh.at_index;
+      *upto = sh.at_sum;
+    }
+    if (!in) cand = 0;
+    __syncthreads();
+    return listed;
+  }
+  // The same of the tokens of bins b0 .. b1 (kSmList at most) of the counts by 32 grid
+  // points, `above` tokens in those before.
+  template <bool SUM>
+  __device__ __forceinline__ bool cut_bins(int b0, int b1, uint32_t above, unsigned long long need, float* cx, int* ci,
+                                           unsigned long long* upto) {
+    const uint32_t ph = phase & 1;
+    const int g0 = -32 * b0, g1 = -32 * b1 - 31;
+    if (threadIdx.x == 0) sh.fill[ph] = 0;
+    __syncthreads();
+    unsigned long long sum = 0;
+    row.each([&](const float (&x)[Slice<F32>::kVec], int idx) {
+      float most = x[0];
+#pragma unroll
+      for (int e = 1; e < Slice<F32>::kVec; ++e) most = fmaxf(most, x[e]);
+      if (!__any_sync(0xffffffffu, grid_of(sc, most) >= g1)) return;
+      uint32_t hits = 0;
+#pragma unroll
+      for (int e = 0; e < Slice<F32>::kVec; ++e) {
+        int g;
+        const unsigned long long w = weight_of(sc, sh.tab, x[e], &g);
+        if (g > g0) sum += w;
+        hits |= g <= g0 && g >= g1 ? 1u << e : 0u;
+      }
+      while (hits) {
+        const int e = __ffs(hits) - 1;
+        hits &= hits - 1;
+        float v = x[0];
+#pragma unroll
+        for (int k = 1; k < Slice<F32>::kVec; ++k)
+          if (k == e) v = x[k];
+        offer(ph, v, idx + e);
+      }
+    });
+    const Sums s = exchange(sum, 0);
+    if (!settle<SUM>(ph, s.sum, above, need, cx, ci, upto)) return false;
+    list_above = sum;
+    list_sums = s;
+    list_top = b0 > 0 ? __fsub_rd(sc.top, __fmul_ru(static_cast<float>(-g0 + 1), 1.0f / (512.0f * sc.ch))) : INFINITY;
+    return true;
+  }
+
   // The cut: the last of the first `need` tokens of the ranking, or the token with which
-  // the weights' running sum reaches `need` (of the tokens up to the cut (cx, ci) that is
-  // already there). Returns the sum of weights up to it.
+  // the weights' running sum reaches `need`. Returns the sum of weights up to it.
   //
   // From [lo, hi], values that hold the cut (`few`: at most kSmList of them): exact counts
   // and sums of what lies above hi, and either the tokens themselves or counts of them in
@@ -506,9 +586,6 @@ struct Sampler {
   // as the weights within a bin, so every round leaves that part of what the range weighs.
   template <bool SUM>
   __device__ __forceinline__ unsigned long long cut(unsigned long long need, float lo, float hi, bool few, float* cx, int* ci) {
-    const float ox = *cx;
-    const int oi = *ci;
-    const auto kept = [&](float x, int idx) { return x > ox || (x == ox && idx <= oi); };
     listed = false;
     // (four rounds from all values, seldom more. The bound is for what should not be.)
     for (int round = 0; round < 20; ++round) {
@@ -536,13 +613,13 @@ struct Sampler {
             const unsigned long long w = weight_of(sc, sh.tab, x[e]);
             const bool over = x[e] > hi;
             n += over ? 1u : 0u;
-            above += over && kept(x[e], idx + e) ? w : 0ull;
+            above += over ? w : 0ull;
           }
         }
         int bin[Slice<F32>::kVec];
 #pragma unroll
         for (int e = 0; e < Slice<F32>::kVec; ++e) {
-          const bool in = x[e] >= lo && x[e] <= hi && (!SUM || kept(x[e], idx + e));
+          const bool in = x[e] >= lo && x[e] <= hi;
           if (few) {
             if (in) offer(ph, x[e], idx + e);
           } else {
@@ -561,34 +638,14 @@ struct Sampler {
         continue;
       }
       if (few) {
-        if (threadIdx.x == 0) sh.at_index = -1;
-        const uint32_t all = collect(ph, &cand);
-        cand = sorted(cand, min(all, static_cast<uint32_t>(kSmList)));
-        const bool in = threadIdx.x < all && all <= kSmList;
-        const unsigned long long own = in ? weight_of(sc, sh.tab, value_of(cand)) : 0ull;
-        const unsigned long long before = s.sum + scan<unsigned long long>(own, sh.warp_sum);
-        const unsigned long long a = SUM ? before : static_cast<unsigned long long>(s.cnt + threadIdx.x);
-        if (in && a < need && need <= a + (SUM ? own : 1ull)) {
-          sh.at_index = index_of(cand);
-          sh.at_x = value_of(cand);
-          sh.at_sum = before + own;
-        }
-        __syncthreads();
-        const int found = sh.at_index;
-        if (found >= 0) {
-          *cx = sh.at_x;
-          *ci = found;
-          const unsigned long long sum = sh.at_sum;
-          __syncthreads();
-          listed = true;
+        unsigned long long sum;
+        if (settle<SUM>(ph, s.sum, s.cnt, need, cx, ci, &sum)) {
           list_above = above;
           list_sums = s;
           list_top = hi;
-          if (!in) cand = 0;
           return sum;
         }
         // (not among them: from all values, by counts alone)
-        __syncthreads();
         few = false;
         lo = -INFINITY;
         hi = sc.top;
@@ -632,14 +689,14 @@ struct Sampler {
     const float v = lo;
     unsigned long long above = 0;
     uint32_t n = 0, ties = 0;
-    row.each([&](const float (&x)[Slice<F32>::kVec], int idx) {
+    row.each([&](const float (&x)[Slice<F32>::kVec], int) {
 #pragma unroll
       for (int e = 0; e < Slice<F32>::kVec; ++e) {
         if (x[e] > v) {
           ++n;
-          if (kept(x[e], idx + e)) above += weight_of(sc, sh.tab, x[e]);
+          above += weight_of(sc, sh.tab, x[e]);
         }
-        ties += x[e] == v && (!SUM || kept(x[e], idx + e)) ? 1u : 0u;
+        ties += x[e] == v ? 1u : 0u;
       }
     });
     const Sums s = exchange(above, n);
@@ -650,7 +707,7 @@ struct Sampler {
     if (threadIdx.x == 0) sh.at_index = -1;
     const unsigned long long mine = __reduce_add_sync(0xffffffffu, ties);
     __syncthreads();
-    locate(mine, t.cnt_before, take, [&](float x, int idx) { return x == v && (!SUM || kept(x, idx)) ? 1ull : 0ull; });
+    locate(mine, t.cnt_before, take, [&](float x, int) { return x == v ? 1ull : 0ull; });
     __syncthreads();
     const uint32_t found = share_index();
     *cx = v;
@@ -777,7 +834,7 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   sc.base = __float_as_int(t_top);
   sc.rest = (p_top - (t_top - kGrid)) + fmaf(d_top, sc.cl, fmaf(d_top, sc.ch, -p_top));   // within 2^-10 of 0
   sc.floor = (t_top - kGrid) - 80.0f;
-  sc.lg = p.lg;
+  sc.up = min(32 - p.lg, 31);                                     // (sums stay below 2^63)
   // a cutoff that does not depend on the others: the least x >= max + T ln min_p
   float least = -INFINITY;
   if (!greedy && mp > 0.f) {
@@ -854,6 +911,8 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       return;
     }
     fits = fits && !greedy && (!list_k || n >= k || low == -INFINITY);
+    if (fits && list_p)                                           // (the list has to weigh enough)
+      fits = s.block_add(s.cand ? weight_of(sc, sh.tab, s.value_of(s.cand)) : 0ull) >= share(total);
     if (fits) {
       s.cand = s.sorted(s.cand, n);
       const bool in = threadIdx.x < n;
@@ -919,8 +978,10 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       const int b = sh.lo_bin;
       __syncthreads();
       if (b >= 0) {                                               // (else: more tokens than have a weight)
-        const bool few = range(b, b, &lo, &hi);
-        total = s.template cut<false>(k, lo, hi, few, &cx, &ci);
+        if (s.held(n, b, b) > kSmList || !s.template cut_bins<false>(b, b, s.held(n, 0, b - 1), k, &cx, &ci, &total)) {
+          const bool few = range(b, b, &lo, &hi);
+          total = s.template cut<false>(k, lo, hi, few, &cx, &ci);
+        }
         cut_k = true;
       } else if (by_p) {
         unsigned long long sum = 0;
@@ -942,12 +1003,14 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       s.find_bounds(l, n * w0 + m * (1.0f / 31.0f) * (w1 - w0), static_cast<float>(need));
       const int b0 = sh.lo_bin, b1 = sh.hi_bin;
       __syncthreads();
-      const bool few = range(b0, b1, &lo, &hi);
-      if (cut_k) {                                                // (the cut there is ends the range)
-        lo = fmaxf(lo, cx);
-        hi = fmaxf(hi, cx);
+      if (b1 == kSmBins - 1 || s.held(n, b0, b1) > kSmList || !s.template cut_bins<true>(b0, b1, 0, need, &cx, &ci, &total)) {
+        const bool few = range(b0, b1, &lo, &hi);
+        if (cut_k) {                                              // (the cut there is ends the range)
+          lo = fmaxf(lo, cx);
+          hi = fmaxf(hi, cx);
+        }
+        total = s.template cut<true>(need, lo, hi, few, &cx, &ci);
       }
-      total = s.template cut<true>(need, lo, hi, few, &cx, &ci);
     }
   }
   if (least > cx) {
@@ -987,12 +1050,15 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     before = all.sum_before;
     sum = all.sum;
   }
+  __syncwarp();
+  blocks_leave(blocks);
   if (threadIdx.x == 0) sh.at_index = -1;
   __syncthreads();
   s.locate(mine, before, greedy ? 1ull : drawn(sum), term);
   __syncthreads();
   if (threadIdx.x == 0 && sh.at_index >= 0) answer(sh.at_index, sh.at_x, sh.at_sum, sum);   // (one block has it)
-  blocks_sync(blocks);                                            // (nobody reads a block that has gone)
+  __syncwarp();
+  blocks_left(blocks);
 }
 
 template <bool F32>
