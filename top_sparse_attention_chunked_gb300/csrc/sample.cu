@@ -40,9 +40,9 @@ constexpr int kSmMaxVocab = 1 << 19;
 constexpr int kSmMaxCluster = 16;
 constexpr int kSmMaxData = 172032;              // bytes of a row that a block holds
 
-// 2^(j / 512), j = 0 .. 511, times 2^30.
+// 2^(j / 512), j = 0 .. 511, as pairs of floats.
 struct Pow2Table {
-  uint32_t v[512];
+  float2 v[512];
 };
 constexpr double series_exp(double x) {         // |x| < 0.7: 1 + x (1 + x / 2 (1 + x / 3 (...)))
   double s = 1.0;
@@ -51,8 +51,11 @@ constexpr double series_exp(double x) {         // |x| < 0.7: 1 + x (1 + x / 2 (
 }
 constexpr Pow2Table make_table() {
   Pow2Table t{};
-  for (int j = 0; j < 512; ++j)
-    t.v[j] = static_cast<uint32_t>(series_exp(0.693147180559945309417 * j / 512.0) * 1073741824.0 + 0.5);
+  for (int j = 0; j < 512; ++j) {
+    const double v = series_exp(0.693147180559945309417 * j / 512.0);
+    t.v[j].x = static_cast<float>(v);
+    t.v[j].y = static_cast<float>(v - static_cast<double>(t.v[j].x));
+  }
   return t;
 }
 __device__ const Pow2Table g_pow2 = make_table();
@@ -72,7 +75,7 @@ struct SampleParams {
 };
 
 struct SampleShared {
-  uint32_t tab[512];
+  float2 tab[512];
   unsigned long long sort[2][kSmList];
   // what the blocks exchange, in two sets: a block may be one exchange ahead
   uint32_t hist[2][kSmBins], below[2][kSmBins];   // tokens of a bin; the sum of what they lie below its edge
@@ -126,89 +129,129 @@ __device__ __forceinline__ void blocks_left(uint32_t blocks) {
 // ---------------------------------------------------------------- weights
 constexpr float kGrid = 24576.0f;               // 1.5 * 2^14: adding it rounds to multiples of 1 / 512
 constexpr float kInt = 12582912.0f;             // 1.5 * 2^23: to whole numbers
+constexpr float kHigh = 3.0f;                   // 1.5 * 2^1: to multiples of 2^-22
+constexpr float kLow = 0x1.8p-22f;              // 1.5 * 2^-22: to multiples of 2^-45
 constexpr int kGridSpan = 64;
-constexpr int kZero = -44 * 512;                // weights from 2^-44 of the largest down are 0
-
-// x -> log2 of the weight, in units of 1 / 512 and a rest. (x - b) log2 e / T is formed
-// as a pair of floats; b is 0, or the largest x where that is too large to be a
-// multiple of 1 / 512 in fp32 (then x - b is exact for all that have a weight). All is
-// relative to the grid point next to the largest x, `rest` below it.
+constexpr int kZero = 60 * 512;                 // weights from 2^-60 of the largest down are none at all
+// x -> log2 of the weight, in units of 1 / 512 and a rest: (x - b) (ch + cl), ch + cl =
+// log2 e / T as a pair of floats. b is 0, or the largest x where that is too large to be a
+// multiple of 1 / 512 in fp32 (x - b then is exact for all that have a weight).
 struct Scale {
-  float b, ch, cl, floor, top, rest;
-  int base, up;                                 // up: the exponent of the largest weight, over w's 30 bits
+  float b, ch, cl, floor, top;                  // floor: exponents below it are taken as it
+  int base, zero;                               // the largest x's grid point; the last one without a weight
+  uint32_t power;                               // what turns a whole exponent's bits into its power of two's
+  float rest;                                   // of the largest x, beside its grid point
 };
-__device__ __forceinline__ int grid_of(const Scale& s, float x, float* frac) {
-  const float d = x - s.b, p = d * s.ch;
-  const float c = fmaxf(p, s.floor);            // (NaN, -infinity: the floor)
-  const float t = c + kGrid;
-  *frac = (c - (t - kGrid)) + fmaf(d, s.cl, fmaf(d, s.ch, -p));
-  return __float_as_int(t) - s.base;            // <= 0
+__device__ __forceinline__ int point_of(const Scale& s, float x) {   // the grid point, as the bits of a float
+  return __float_as_int(__fadd_rn(fmaxf(__fmul_rn(__fadd_rn(x, -s.b), s.ch), s.floor), kGrid));   // (NaN, -infinity: the floor's)
 }
-__device__ __forceinline__ int grid_of(const Scale& s, float x) {
-  return __float_as_int(fmaxf((x - s.b) * s.ch, s.floor) + kGrid) - s.base;
+__device__ __forceinline__ int grid_of(const Scale& s, float x) { return point_of(s, x) - s.base; }   // <= 0
+
+// A weight, the largest in [1/2, 1), as the bits of kHigh + h and kLow + l, h a multiple
+// of 2^-22 and l the rest, of 2^-45 (rounded to the nearest). Nearly all in fp32 additions
+// and multiply-adds with immediate operands: the integer pipe has half their rate, and
+// pairs of fp32 operations need their constants in registers, which are not there.
+struct Weight {
+  uint32_t h, l;
+  int point;                                    // the token's grid point
+  __device__ __forceinline__ unsigned long long value() const {   // in units of 2^-45
+    return (static_cast<unsigned long long>(h - __float_as_uint(kHigh)) << 23) +
+           static_cast<long long>(static_cast<int>(l - __float_as_uint(kLow)));
+  }
+};
+// (in(point): whether it counts, else 0.) 2^r - 1 = r ln 2 + (r ln 2)^2 / 2 + (r ln 2)^3 / 6
+// with |r| <= 2^-10: off by 2^-42.
+template <class F>
+__device__ __forceinline__ Weight weight_if(const Scale& s, const float2* tab, float x, F&& in) {
+  const float d = __fadd_rn(x, -s.b), n = __fmul_rn(d, s.ch), c = fmaxf(n, s.floor);
+  const float t = __fadd_rn(c, kGrid), k = __fadd_rn(t, -kGrid);
+  float r = __fadd_rn(__fadd_rn(c, -k), __fmaf_rn(d, s.cl, __fmaf_rn(d, s.ch, -n)));
+  Weight y;
+  y.point = __float_as_int(t);
+  if (y.point <= s.zero) r = 0.f;               // (it may be infinite or NaN; the power leaves nothing)
+  const float2 a = tab[y.point & 511];
+  const float q = __fmul_rn(r, __fmaf_rn(r, __fmaf_rn(r, 0.05550411f, 0.24022651f), 0.69314718f));
+  const float b = __fmaf_rn(a.x, q, a.y), w = __fadd_rn(a.x, b), e = __fadd_rn(__fadd_rn(a.x, -w), b);   // w + e = a (1 + q)
+  float p = __uint_as_float(__float_as_uint(__fadd_rd(k, kInt)) * 0x800000u + s.power);
+  if (!in(y.point)) p = 0.f;
+  const float h = __fmaf_rn(w, p, kHigh);
+  y.h = __float_as_uint(h);
+  y.l = __float_as_uint(__fadd_rn(__fmaf_rn(e, p, __fmaf_rn(w, p, __fadd_rn(kHigh, -h))), kLow));
+  return y;
 }
-// 2^r - 1 = r ln 2 + (r ln 2)^2 / 2 + (r ln 2)^3 / 6 (|r| <= 2^-10: off by 2^-42)
-__device__ __forceinline__ unsigned long long weight_of(const Scale& s, const uint32_t* tab, float x, int* grid) {
-  float r;
-  const int it = grid_of(s, x, &r);
-  *grid = it;
-  const uint32_t t = tab[it & 511];
-  const float q = r * fmaf(r, fmaf(r, 0.05550411f, 0.24022651f), 0.69314718f);
-  // (t as a float: its upper 24 bits)
-  const float w = fmaf(q, __uint_as_float((t >> 7) + ((127u + 29u) << 23)), kInt);
-  // times 2^(up + exponent), a shift to the left as a product (one instruction with the
-  // sum's addition), the last place of one to the right set: the middle of what is cut off
-  const int e = (it >> 9) + s.up;
-  const uint32_t v = ((t + (__float_as_uint(w) - __float_as_uint(kInt))) >> max(-e, 0)) | 1u;
-  return it > kZero ? static_cast<unsigned long long>(v) * (1u << max(e, 0)) : 0ull;
+__device__ __forceinline__ unsigned long long weight_of(const Scale& s, const float2* tab, float x) {
+  return weight_if(s, tab, x, [](int) { return true; }).value();
 }
-__device__ __forceinline__ unsigned long long weight_of(const Scale& s, const uint32_t* tab, float x) {
-  int it;
-  return weight_of(s, tab, x, &it);
-}
+// A thread's sum (of 512 weights at most: 32 bits each hold h and l).
+struct WeightSum {
+  uint32_t h = 0, l = 0, pairs = 0;             // of the bits: kHigh's and kLow's are taken off at the end
+  __device__ __forceinline__ void add(const Weight& a, const Weight& b) {
+    h += a.h + b.h;
+    l += a.l + b.l;
+    ++pairs;
+  }
+  __device__ __forceinline__ unsigned long long value() const {
+    return (static_cast<unsigned long long>(h - pairs * (2 * __float_as_uint(kHigh))) << 23) +
+           static_cast<long long>(static_cast<int>(l - pairs * (2 * __float_as_uint(kLow))));
+  }
+};
 
 // ------------------------------------------------------------------ row
-// A block's tokens in shared memory as 16-byte vectors, aligned as in global
-// memory; what is not the block's in the first and the last one is -infinity. A warp
-// has consecutive vectors.
-template <bool F32>
+// A block's tokens in shared memory as 16-byte vectors, aligned as in global memory;
+// what is not the block's in the first and the last one is -infinity, and so are the
+// vectors up to a multiple of 32. A warp has consecutive ones.
+template <int TYPE>
 struct Slice {
+  static constexpr bool kF32 = TYPE == DSA_FP32;
+  static constexpr int kVec = kF32 ? 4 : 8;
   const uint4* img;
-  int first, count;     // the warp's vectors
+  int first, count;     // the warp's vectors: a multiple of 32
   int vecs, per;        // the block's, and a warp's
   int index0;           // index of element 0 of vector 0
-  static constexpr int kVec = F32 ? 4 : 8;
-  bool f16;
-  __device__ __forceinline__ void unpack(const uint4& u, float (&x)[kVec]) const {
+  __device__ __forceinline__ static void unpack(const uint4& u, float (&x)[kVec]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    if constexpr (F32) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(w[e]);
-    } else if (f16) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = __half2float(__ushort_as_half(static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)))));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+    for (int e = 0; e < kVec; ++e) {
+      if constexpr (kF32) x[e] = __uint_as_float(w[e]);
+      else if constexpr (TYPE == DSA_FP16) x[e] = __half2float(__ushort_as_half(static_cast<unsigned short>(w[e >> 1] >> (16 * (e & 1)))));
+      else x[e] = __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
     }
   }
-  // f(x[kVec], index of x[0]) for every vector of the warp; lanes beyond its end get
-  // -infinity, and all lanes come along
+  // f(x[kVec], index of x[0]) for every vector of the warp; all lanes come along
   template <class F>
   __device__ __forceinline__ void each(F&& f) const {
     const int lane = threadIdx.x & 31;
-    for (int i = 0; i < count; i += 32) one(first + i + lane, i + lane < count, f);
+#pragma unroll 1
+    for (int i = 0; i < count; i += 32) one(first + i + lane, f);
   }
   template <class F>
-  __device__ __forceinline__ void one(int v, bool in, F&& f) const {
+  __device__ __forceinline__ void one(int v, F&& f) const {
     float x[kVec];
-    if (in) {
-      unpack(img[v], x);
-    } else {
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) x[e] = -INFINITY;
-    }
+    unpack(img[v], x);
     f(x, index0 + v * kVec);
+  }
+  // f(x0, x1, index of x0) for every two tokens of n vectors from `from` on (a multiple of
+  // 32): what passes that form weights take, for eight at once in each of them would be
+  // more code than the instruction cache holds (top-p of 64 x 131,072: 83 and not 89 us).
+  template <class F>
+  __device__ __forceinline__ void pairs(int from, int n, F&& f) const {
+#pragma unroll 1
+    for (int i = threadIdx.x & 31; i < n * (kVec / 2); i += 32) pair(from * (kVec / 2) + i, f);
+  }
+  template <class F>
+  __device__ __forceinline__ void pair(int i, F&& f) const {
+    if constexpr (kF32) {
+      const float2 x = reinterpret_cast<const float2*>(img)[i];
+      f(x.x, x.y, index0 + 2 * i);
+    } else {
+      const uint32_t w = reinterpret_cast<const uint32_t*>(img)[i];
+      if constexpr (TYPE == DSA_FP16) {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        f(x.x, x.y, index0 + 2 * i);
+      } else {
+        f(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u), index0 + 2 * i);
+      }
+    }
   }
 };
 
@@ -232,11 +275,11 @@ struct Sums {
   uint32_t cnt, cnt_before;
 };
 
-template <bool F32>
+template <int TYPE>
 struct Sampler {
   const SampleParams& p;
   SampleShared& sh;
-  Slice<F32> row;
+  Slice<TYPE> row;
   Scale sc;
   uint32_t rank, blocks;
   uint32_t phase = 0;
@@ -250,8 +293,10 @@ struct Sampler {
 
   __device__ __forceinline__ Sampler(const SampleParams& pp, SampleShared& s) : p(pp), sh(s) {}
 
-  // The weight of grid point 0 (the largest one is 2^rest times it).
-  __device__ __forceinline__ float unit() const { return __int_as_float((127 + 30 + sc.up) << 23); }
+  // The weight of the largest x's grid point (its own is 2^rest times it).
+  __device__ __forceinline__ float unit() const {
+    return sh.tab[sc.base & 511].x * 0x1p44f;
+  }
 
   // Adds up every thread's sum and count over the cluster.
   __device__ __forceinline__ Sums exchange(unsigned long long sum, uint32_t cnt) {
@@ -299,32 +344,28 @@ struct Sampler {
     __syncthreads();
     return h;
   }
-  // Counts a thread's tokens, those that follow one another in the same bin (-1: none)
-  // at once: rows of equal logits would otherwise meet in one place.
-  __device__ __forceinline__ void count(uint32_t* hist, const int (&bin)[Slice<F32>::kVec]) {
-    uint32_t run = 0;
-#pragma unroll
-    for (int e = 0; e < Slice<F32>::kVec; ++e) {
-      ++run;
-      if (e + 1 < Slice<F32>::kVec && bin[e + 1] == bin[e]) continue;
-      if (bin[e] >= 0) atomicAdd(hist + bin[e], run);
-      run = 0;
-    }
+  // Counts two tokens in their bins (-1: none), at once where it is the same: rows of equal
+  // logits would otherwise meet in one place.
+  __device__ __forceinline__ void count(uint32_t* hist, int b0, int b1) {
+    if (b0 >= 0) atomicAdd(hist + b0, b0 == b1 ? 2u : 1u);
+    if (b1 >= 0 && b0 != b1) atomicAdd(hist + b1, 1u);
   }
   // The same for tokens at grid points g below 0: bins of 32 points, and by how much.
-  __device__ __forceinline__ void count_grid(uint32_t* hist, uint32_t* below, const int (&g)[Slice<F32>::kVec]) {
-    uint32_t run = 0, sum = 0;
-#pragma unroll
-    for (int e = 0; e < Slice<F32>::kVec; ++e) {
-      ++run;
-      sum += static_cast<uint32_t>(-g[e]) & 31u;
-      if (e + 1 < Slice<F32>::kVec && -g[e + 1] >> 5 == -g[e] >> 5) continue;
-      const int b = -g[e] >> 5;
-      if (b < kSmBins - 1) {
-        atomicAdd(hist + b, run);
-        if (sum) atomicAdd(below + b, sum);
-      }
-      run = sum = 0;
+  __device__ __forceinline__ void count_grid(uint32_t* hist, uint32_t* below, int g0, int g1) {
+    const int b0 = -g0 >> 5, b1 = -g1 >> 5;
+    uint32_t n = 1, s0 = static_cast<uint32_t>(-g0) & 31u;
+    const uint32_t s1 = static_cast<uint32_t>(-g1) & 31u;
+    if (b0 == b1) {
+      n = 2;
+      s0 += s1;
+    }
+    if (b0 < kSmBins - 1) {
+      atomicAdd(hist + b0, n);
+      if (s0) atomicAdd(below + b0, s0);
+    }
+    if (b1 < kSmBins - 1 && b0 != b1) {
+      atomicAdd(hist + b1, 1u);
+      if (s1) atomicAdd(below + b1, s1);
     }
   }
 
@@ -397,7 +438,7 @@ struct Sampler {
   __device__ __forceinline__ void locate(unsigned long long mine, unsigned long long before, unsigned long long need, F&& f) {
     if (lane == 0) sh.warp_sum[warp] = mine;
     __syncthreads();
-    // the warp that has it, then its rounds of 32 vectors, one a warp (13 at most)
+    // the warp that has it, then its rounds of 32 vectors, one a warp (11 at most)
     unsigned long long x = sh.warp_sum[lane], own = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -410,21 +451,13 @@ struct Sampler {
     const int w = __ffs(who) - 1;
     before += __shfl_sync(0xffffffffu, x - own, w);
     const int v0 = min(w * row.per, row.vecs), n = min(row.per, row.vecs - v0);
-    constexpr int kVec = Slice<F32>::kVec;
-    unsigned long long t[kVec];
-    float xs[kVec];
-    int at = 0;
+    constexpr int kPairs = Slice<TYPE>::kVec / 2;
+    const int v = (v0 + warp * 32 + lane) * kPairs;               // the lane's first pair, of kPairs
     own = 0;
-    if (warp * 32 < n)
-      row.one(v0 + warp * 32 + lane, warp * 32 + lane < n, [&](const float (&y)[kVec], int idx) {
-        at = idx;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          xs[e] = y[e];
-          t[e] = f(y[e], idx + e);
-          own += t[e];
-        }
-      });
+    if (warp * 32 < n) {
+#pragma unroll 1
+      for (int i = 0; i < kPairs; ++i) row.pair(v + i, [&](float x0, float x1, int idx) { own += f(x0, idx) + f(x1, idx + 1); });
+    }
     const unsigned long long round = warp_add(own);
     if (lane == 0) sh.warp_sum[warp] = round;
     __syncthreads();
@@ -438,15 +471,18 @@ struct Sampler {
       }
       unsigned long long a = before + s - own;
       if (a < need && need <= a + own) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          if (a < need && need <= a + t[e]) {
-            sh.at_index = at + e;
-            sh.at_x = xs[e];
-            sh.at_sum = t[e];
-          }
-          a += t[e];
-        }
+#pragma unroll 1
+        for (int i = 0; i < kPairs; ++i)
+          row.pair(v + i, [&](float x0, float x1, int idx) {
+            const unsigned long long t0 = f(x0, idx), t1 = f(x1, idx + 1);
+            const bool first = a < need && need <= a + t0, second = a + t0 < need && need <= a + t0 + t1;
+            if (first || second) {
+              sh.at_index = first ? idx : idx + 1;
+              sh.at_x = first ? x0 : x1;
+              sh.at_sum = first ? t0 : t1;
+            }
+            a += t0 + t1;
+          });
       }
     }
   }
@@ -480,26 +516,42 @@ struct Sampler {
     const uint32_t at = atomicAdd(&sh.fill[ph], 1u);
     if (at < kSmList) sh.list[ph][at] = static_cast<unsigned long long>(float_key(x)) << 32 | static_cast<uint32_t>(~idx);
   }
-  // Bitonic sort of the threads' first n candidates, the largest first. Only the warps
-  // that have some take part.
+  // Sorts the threads' first n candidates, the largest first: 32 by a bitonic sort within
+  // a warp, then runs of 32, 64 .. merged: a candidate's place is its own in its run and
+  // that of as many of the other's as are larger, by bisection. (A bitonic sort of 1,024
+  // across the block takes 8.5 us, this 2.) Only the warps that have some take part.
   __device__ __forceinline__ unsigned long long sorted(unsigned long long v, uint32_t n) {
-    uint32_t size = 32, set = 0;
+    uint32_t size = 32;
     while (size < n) size <<= 1;
-    if (threadIdx.x >= size) return v;
-    for (uint32_t k = 2; k <= size; k <<= 1)
-      for (uint32_t j = k >> 1; j > 0; j >>= 1) {
-        unsigned long long o;
-        if (j < 32) {
-          o = __shfl_xor_sync(0xffffffffu, v, j);
-        } else {
-          sh.sort[set][threadIdx.x] = v;
-          named_bar_sync(1, size);
-          o = sh.sort[set][threadIdx.x ^ j];
-          set ^= 1;
-        }
-        const bool first = (threadIdx.x & j) == 0, down = (threadIdx.x & k) == 0;
+    if (threadIdx.x >= size) return 0;
+#pragma unroll
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+      for (int j = k >> 1; j > 0; j >>= 1) {
+        const unsigned long long o = __shfl_xor_sync(0xffffffffu, v, j);
+        const bool first = (lane & j) == 0, down = (lane & k) == 0 || k == 32;
         v = first == down ? max(v, o) : min(v, o);
       }
+    const uint32_t t = threadIdx.x;
+    unsigned long long *a = sh.sort[0], *b = sh.sort[1];
+    for (uint32_t run = 32; run < size; run <<= 1) {
+      a[t] = v;
+      named_bar_sync(1, size);
+      // (empty places are zeros: of equal ones the first run's come first)
+      const bool second = (t & run) != 0;
+      const uint32_t other = (t & ~(2 * run - 1)) + (second ? 0 : run);
+      uint32_t lo = 0, hi = run;
+      while (lo < hi) {
+        const uint32_t mid = (lo + hi) >> 1;
+        const unsigned long long o = a[other + mid];
+        if (o > v || (second && o == v)) lo = mid + 1;
+        else hi = mid;
+      }
+      const uint32_t to = (t & ~(2 * run - 1)) + (t & (run - 1)) + lo;
+      b[to] = v;
+      named_bar_sync(1, size);
+      v = b[t];
+    }
     return v;
   }
   // A candidate's value and index.
@@ -541,38 +593,23 @@ struct Sampler {
   __device__ __forceinline__ bool cut_bins(int b0, int b1, uint32_t above, unsigned long long need, float* cx, int* ci,
                                            unsigned long long* upto) {
     const uint32_t ph = phase & 1;
-    const int g0 = -32 * b0, g1 = -32 * b1 - 31;
+    const int p0 = sc.base - 32 * b0, p1 = sc.base - 32 * b1 - 31;
     if (threadIdx.x == 0) sh.fill[ph] = 0;
     __syncthreads();
-    unsigned long long sum = 0;
-    row.each([&](const float (&x)[Slice<F32>::kVec], int idx) {
-      float most = x[0];
-#pragma unroll
-      for (int e = 1; e < Slice<F32>::kVec; ++e) most = fmaxf(most, x[e]);
-      if (!__any_sync(0xffffffffu, grid_of(sc, most) >= g1)) return;
-      uint32_t hits = 0;
-#pragma unroll
-      for (int e = 0; e < Slice<F32>::kVec; ++e) {
-        int g;
-        const unsigned long long w = weight_of(sc, sh.tab, x[e], &g);
-        if (g > g0) sum += w;
-        hits |= g <= g0 && g >= g1 ? 1u << e : 0u;
-      }
-      while (hits) {
-        const int e = __ffs(hits) - 1;
-        hits &= hits - 1;
-        float v = x[0];
-#pragma unroll
-        for (int k = 1; k < Slice<F32>::kVec; ++k)
-          if (k == e) v = x[k];
-        offer(ph, v, idx + e);
-      }
+    WeightSum sum;
+    row.pairs(row.first, row.count, [&](float x0, float x1, int idx) {
+      if (!__any_sync(0xffffffffu, point_of(sc, fmaxf(x0, x1)) >= p1)) return;
+      const auto over = [&](int point) { return point > p0; };
+      const Weight a = weight_if(sc, sh.tab, x0, over), b = weight_if(sc, sh.tab, x1, over);
+      sum.add(a, b);
+      if (a.point <= p0 && a.point >= p1) offer(ph, x0, idx);
+      if (b.point <= p0 && b.point >= p1) offer(ph, x1, idx + 1);
     });
-    const Sums s = exchange(sum, 0);
+    const Sums s = exchange(sum.value(), 0);
     if (!settle<SUM>(ph, s.sum, above, need, cx, ci, upto)) return false;
-    list_above = sum;
+    list_above = sum.value();
     list_sums = s;
-    list_top = b0 > 0 ? __fsub_rd(sc.top, __fmul_ru(static_cast<float>(-g0 + 1), 1.0f / (512.0f * sc.ch))) : INFINITY;
+    list_top = b0 > 0 ? __fsub_rd(sc.top, __fmul_ru(static_cast<float>(32 * b0 + 1), 1.0f / (512.0f * sc.ch))) : INFINITY;
     return true;
   }
 
@@ -600,37 +637,26 @@ struct Sampler {
       if (!few) hist = clear_hist();
       if (threadIdx.x == 0) sh.fill[ph] = 0;
       __syncthreads();
-      unsigned long long above = 0;
+      WeightSum above;
       uint32_t n = 0;
-      row.each([&](const float (&x)[Slice<F32>::kVec], int idx) {
-        float most = x[0];
-#pragma unroll
-        for (int e = 1; e < Slice<F32>::kVec; ++e) most = fmaxf(most, x[e]);
+      row.pairs(row.first, row.count, [&](float x0, float x1, int idx) {
+        const float most = fmaxf(x0, x1);
         if (!__any_sync(0xffffffffu, most >= lo)) return;
         if (__any_sync(0xffffffffu, most > hi)) {
-#pragma unroll
-          for (int e = 0; e < Slice<F32>::kVec; ++e) {
-            const unsigned long long w = weight_of(sc, sh.tab, x[e]);
-            const bool over = x[e] > hi;
-            n += over ? 1u : 0u;
-            above += over ? w : 0ull;
-          }
+          n += (x0 > hi ? 1u : 0u) + (x1 > hi ? 1u : 0u);
+          above.add(weight_if(sc, sh.tab, x0, [&](int) { return x0 > hi; }), weight_if(sc, sh.tab, x1, [&](int) { return x1 > hi; }));
         }
-        int bin[Slice<F32>::kVec];
-#pragma unroll
-        for (int e = 0; e < Slice<F32>::kVec; ++e) {
-          const bool in = x[e] >= lo && x[e] <= hi;
-          if (few) {
-            if (in) offer(ph, x[e], idx + e);
-          } else {
-            if (by_grid) bin[e] = (ghi - grid_of(sc, x[e])) >> shift;
-            else bin[e] = static_cast<int>((khi - float_key(x[e])) >> shift);
-            if (!in) bin[e] = -1;
-          }
+        const bool in0 = x0 >= lo && x0 <= hi, in1 = x1 >= lo && x1 <= hi;
+        if (few) {
+          if (in0) offer(ph, x0, idx);
+          if (in1) offer(ph, x1, idx + 1);
+        } else if (by_grid) {
+          count(hist, in0 ? (ghi - grid_of(sc, x0)) >> shift : -1, in1 ? (ghi - grid_of(sc, x1)) >> shift : -1);
+        } else {
+          count(hist, in0 ? static_cast<int>((khi - float_key(x0)) >> shift) : -1, in1 ? static_cast<int>((khi - float_key(x1)) >> shift) : -1);
         }
-        if (!few) count(hist, bin);
       });
-      const Sums s = exchange(above, n);
+      const Sums s = exchange(above.value(), n);
       if (SUM ? s.sum >= need : s.cnt >= need) {   // (the range does not hold it: from all values)
         few = false;
         lo = -INFINITY;
@@ -640,7 +666,7 @@ struct Sampler {
       if (few) {
         unsigned long long sum;
         if (settle<SUM>(ph, s.sum, s.cnt, need, cx, ci, &sum)) {
-          list_above = above;
+          list_above = above.value();
           list_sums = s;
           list_top = hi;
           return sum;
@@ -689,15 +715,12 @@ struct Sampler {
     const float v = lo;
     unsigned long long above = 0;
     uint32_t n = 0, ties = 0;
-    row.each([&](const float (&x)[Slice<F32>::kVec], int) {
-#pragma unroll
-      for (int e = 0; e < Slice<F32>::kVec; ++e) {
-        if (x[e] > v) {
-          ++n;
-          above += weight_of(sc, sh.tab, x[e]);
-        }
-        ties += x[e] == v ? 1u : 0u;
+    row.pairs(row.first, row.count, [&](float x0, float x1, int) {
+      if (__any_sync(0xffffffffu, fmaxf(x0, x1) > v)) {
+        n += (x0 > v ? 1u : 0u) + (x1 > v ? 1u : 0u);
+        above += (x0 > v ? weight_of(sc, sh.tab, x0) : 0ull) + (x1 > v ? weight_of(sc, sh.tab, x1) : 0ull);
       }
+      ties += (x0 == v ? 1u : 0u) + (x1 == v ? 1u : 0u);
     });
     const Sums s = exchange(above, n);
     const Sums t = exchange(0, ties);
@@ -724,13 +747,14 @@ struct Sampler {
   }
 };
 
-template <bool F32>
-__global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constant__ SampleParams p, int blocks, int f16) {
+template <int TYPE>
+__global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constant__ SampleParams p, int blocks) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SampleShared& sh = *reinterpret_cast<SampleShared*>(smem_raw);
   uint8_t* img = smem_raw + ((sizeof(SampleShared) + 15) & ~15);
-  constexpr int kBytes = F32 ? 4 : 2, kVec = 16 / kBytes;
-  Sampler<F32> s(p, sh);
+  constexpr bool kF32 = TYPE == DSA_FP32;
+  constexpr int kBytes = kF32 ? 4 : 2, kVec = 16 / kBytes;
+  Sampler<TYPE> s(p, sh);
   s.blocks = blocks;
   s.rank = blockIdx.x % blocks;
   s.warp = threadIdx.x >> 5;
@@ -740,14 +764,13 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   const int t0 = s.rank * p.slice, len = max(0, min(p.slice, p.vocab - t0));
   const uint8_t* src = static_cast<const uint8_t*>(p.logits) + (r * p.stride + t0) * kBytes;
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / kBytes;
-  const int vecs = (off + len + kVec - 1) / kVec, per = (vecs + kSmWarps - 1) / kSmWarps;
+  const int vecs = ((off + len + kVec - 1) / kVec + 31) & ~31, per = (vecs + kSmThreads - 1) / kSmThreads * 32;
   s.row.img = reinterpret_cast<const uint4*>(img);
   s.row.vecs = vecs;
   s.row.per = per;
   s.row.first = min(s.warp * per, vecs);
   s.row.count = min(per, vecs - s.row.first);
   s.row.index0 = t0 - off;
-  s.row.f16 = f16 != 0;
   for (int i = s.lane; i < s.row.count; i += 32) {
     const int v = s.row.first + i, e0 = v * kVec - off;          // the vector's first token, of the block's
     uint8_t* d = img + v * 16;
@@ -757,10 +780,10 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         const bool in = e0 + e >= 0 && e0 + e < len;
-        if constexpr (F32)
+        if constexpr (kF32)
           reinterpret_cast<float*>(d)[e] = in ? reinterpret_cast<const float*>(src)[e0 + e] : -INFINITY;
         else
-          reinterpret_cast<uint16_t*>(d)[e] = in ? reinterpret_cast<const uint16_t*>(src)[e0 + e] : f16 ? 0xfc00u : 0xff80u;
+          reinterpret_cast<uint16_t*>(d)[e] = in ? reinterpret_cast<const uint16_t*>(src)[e0 + e] : TYPE == DSA_FP16 ? 0xfc00u : 0xff80u;
       }
     }
   }
@@ -834,7 +857,9 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   sc.base = __float_as_int(t_top);
   sc.rest = (p_top - (t_top - kGrid)) + fmaf(d_top, sc.cl, fmaf(d_top, sc.ch, -p_top));   // within 2^-10 of 0
   sc.floor = (t_top - kGrid) - 80.0f;
-  sc.up = min(32 - p.lg, 31);                                     // (sums stay below 2^63)
+  sc.zero = sc.base - kZero;
+  // (the largest's power is 2^-1: sums of 2^19 weights below 2^45 stay below 2^64)
+  sc.power = (126u << 23) - __float_as_uint(__fadd_rd(t_top - kGrid, kInt)) * 0x800000u;
   // a cutoff that does not depend on the others: the least x >= max + T ln min_p
   float least = -INFINITY;
   if (!greedy && mp > 0.f) {
@@ -861,7 +886,7 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       if (rest < w) {
         lp = log1pf(-(static_cast<float>(rest) / static_cast<float>(sum)));
       } else {
-        lp = (x - top) / heat + sc.rest * 0.69314718f - logf(static_cast<float>(sum) * (1.0f / s.unit()));
+        lp = (x - top) / heat + sc.rest * 0.69314718f - logf(static_cast<float>(sum) / s.unit());
       }
     }
     p.logprobs[r] = lp;
@@ -882,14 +907,15 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     if (greedy) low = top;
     const uint32_t lp = s.phase & 1;
     counted = list_p && !greedy;
-    unsigned long long sum = 0;
+    WeightSum sum;
+    if (counted)
+      s.row.pairs(s.row.first, s.row.count, [&](float x0, float x1, int) {
+        const auto all = [](int) { return true; };
+        const Weight a = weight_if(sc, sh.tab, x0, all), b = weight_if(sc, sh.tab, x1, all);
+        sum.add(a, b);
+        s.count_grid(sh.hist[lp], sh.below[lp], a.point - sc.base, b.point - sc.base);
+      });
     s.row.each([&](const float (&x)[kVec], int idx) {
-      if (counted) {
-        int g[kVec];
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) sum += weight_of(sc, sh.tab, x[e], &g[e]);
-        s.count_grid(sh.hist[lp], sh.below[lp], g);
-      }
       float most = x[0];
 #pragma unroll
       for (int e = 1; e < kVec; ++e) most = fmaxf(most, x[e]);
@@ -898,7 +924,7 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       for (int e = 0; e < kVec; ++e)
         if (x[e] >= low && x[e] > -INFINITY) s.offer(lp, x[e], idx + e);
     });
-    total = s.exchange(sum, 0).sum;
+    total = s.exchange(sum.value(), 0).sum;
     const uint32_t n = s.collect(lp, &s.cand);
     bool fits = n <= kSmList;
     if (greedy && fits) {
@@ -951,11 +977,8 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       ph2 = s.phase & 1;
       sh.below[ph2][threadIdx.x] = 0;
       uint32_t* hist = s.clear_hist();
-      s.row.each([&](const float (&x)[kVec], int) {
-        int g[kVec];
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) g[e] = grid_of(sc, x[e]);
-        s.count_grid(hist, sh.below[ph2], g);
+      s.row.pairs(s.row.first, s.row.count, [&](float x0, float x1, int) {
+        s.count_grid(hist, sh.below[ph2], grid_of(sc, x0), grid_of(sc, x1));
       });
       s.exchange(0, 0);
     }
@@ -984,12 +1007,12 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
         }
         cut_k = true;
       } else if (by_p) {
-        unsigned long long sum = 0;
-        s.row.each([&](const float (&x)[kVec], int) {
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) sum += weight_of(sc, sh.tab, x[e]);
+        WeightSum sum;
+        s.row.pairs(s.row.first, s.row.count, [&](float x0, float x1, int) {
+          const auto all = [](int) { return true; };
+          sum.add(weight_if(sc, sh.tab, x0, all), weight_if(sc, sh.tab, x1, all));
         });
-        total = s.exchange(sum, 0).sum;
+        total = s.exchange(sum.value(), 0).sum;
       }
     }
     if (by_p) {
@@ -1018,9 +1041,9 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     ci = 0x7fffffff;
   }
   // the draw: the first token in index order at which the kept weights' sum exceeds u of all
+  const auto kept = [&](float x, int idx) { return x > cx || (x == cx && idx <= ci); };
   const auto term = [&](float x, int idx) -> unsigned long long {
-    const unsigned long long w = greedy ? 1ull : weight_of(sc, sh.tab, x);
-    return x > cx || (x == cx && idx <= ci) ? w : 0ull;
+    return !kept(x, idx) ? 0ull : greedy ? 1ull : weight_of(sc, sh.tab, x);
   };
   unsigned long long mine, before, sum;
   if (s.listed && least <= s.list_top) {
@@ -1037,14 +1060,30 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     mine = warp_add(s.list_above) + sh.cand_sum[s.warp];
   } else {
     unsigned long long own_sum = 0;
-    s.row.each([&](const float (&x)[kVec], int idx) {
-      float most = x[0];
+    if (greedy) {
+      s.row.pairs(s.row.first, s.row.count, [&](float x0, float x1, int idx) { own_sum += (kept(x0, idx) ? 1ull : 0ull) + (kept(x1, idx + 1) ? 1ull : 0ull); });
+    } else if (cx == -INFINITY) {                                 // (a temperature alone: one pass)
+      WeightSum w;
+      s.row.each([&](const float (&x)[kVec], int) {
+        const auto all = [](int) { return true; };
 #pragma unroll
-      for (int e = 1; e < kVec; ++e) most = fmaxf(most, x[e]);
-      if (!__any_sync(0xffffffffu, most >= cx)) return;
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) own_sum += term(x[e], idx + e);
-    });
+        for (int e = 0; e < kVec; e += 2) w.add(weight_if(sc, sh.tab, x[e], all), weight_if(sc, sh.tab, x[e + 1], all));
+      });
+      own_sum = w.value();
+    } else {
+      WeightSum w;
+      const bool whole = ci == 0x7fffffff;                        // (no tie is cut)
+      s.row.pairs(s.row.first, s.row.count, [&](float x0, float x1, int idx) {
+        if (!__any_sync(0xffffffffu, fmaxf(x0, x1) >= cx)) return;
+        bool in0 = x0 >= cx, in1 = x1 >= cx;
+        if (!whole) {
+          in0 = kept(x0, idx);
+          in1 = kept(x1, idx + 1);
+        }
+        w.add(weight_if(sc, sh.tab, x0, [&](int) { return in0; }), weight_if(sc, sh.tab, x1, [&](int) { return in1; }));
+      });
+      own_sum = w.value();
+    }
     const Sums all = s.exchange(own_sum, 0);
     mine = warp_add(own_sum);
     before = all.sum_before;
@@ -1061,9 +1100,9 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   blocks_left(blocks);
 }
 
-template <bool F32>
-cudaError_t launch_sample(SampleParams p, int f16, int sms, cudaStream_t st) {
-  constexpr int kBytes = F32 ? 4 : 2;
+template <int TYPE>
+cudaError_t launch_sample(SampleParams p, int sms, cudaStream_t st) {
+  constexpr int kBytes = TYPE == DSA_FP32 ? 4 : 2;
   // Blocks of a row: as few as hold it, and more where SMs would be idle and a block
   // would still have 4,096 tokens.
   int blocks = 1;
@@ -1071,8 +1110,8 @@ cudaError_t launch_sample(SampleParams p, int f16, int sms, cudaStream_t st) {
   while (blocks < kSmMaxCluster && slice_of(blocks) * kBytes > kSmMaxData) blocks *= 2;
   while (blocks < 8 && 2LL * p.rows * blocks <= sms && slice_of(2 * blocks) >= 4096) blocks *= 2;
   p.slice = slice_of(blocks);
-  const size_t smem = ((sizeof(SampleShared) + 15) & ~size_t{15}) + static_cast<size_t>(p.slice) * kBytes + 32;
-  const void* fn = reinterpret_cast<const void*>(&sample_kernel<F32>);
+  const size_t smem = ((sizeof(SampleShared) + 15) & ~size_t{15}) + static_cast<size_t>(p.slice) * kBytes + 16 + 512;
+  const void* fn = reinterpret_cast<const void*>(&sample_kernel<TYPE>);
   cudaError_t e = set_max_smem(fn, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   if (blocks > 8 && (e = set_nonportable_cluster(fn)) != cudaSuccess) return e;
@@ -1088,7 +1127,7 @@ cudaError_t launch_sample(SampleParams p, int f16, int sms, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, sample_kernel<F32>, p, blocks, f16);
+  e = cudaLaunchKernelEx(&cfg, sample_kernel<TYPE>, p, blocks);
   if (e == cudaSuccess) note_launch("sample_kernel");
   return e;
 }
@@ -1134,8 +1173,9 @@ extern "C" int dsa_sample(const dsa_sample_problem* sp, const void* logits, cons
   p.tokens = tokens, p.logprobs = logprobs, p.vocab = sp->vocab, p.rows = sp->rows;
   while ((1 << p.lg) < sp->vocab) ++p.lg;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = sp->logits_dtype == DSA_FP32 ? launch_sample<true>(p, 0, sms, st)
-                                                     : launch_sample<false>(p, sp->logits_dtype == DSA_FP16, sms, st);
+  const cudaError_t e = sp->logits_dtype == DSA_FP32   ? launch_sample<DSA_FP32>(p, sms, st)
+                        : sp->logits_dtype == DSA_FP16 ? launch_sample<DSA_FP16>(p, sms, st)
+                                                       : launch_sample<DSA_BF16>(p, sms, st);
   if (e != cudaSuccess) return report_errorf(DSA_ERR_CUDA, "sample launch: %s", cudaGetErrorString(e));
   return DSA_OK;
 }
