@@ -39,36 +39,46 @@ __device__ __forceinline__ uint32_t to16(float v, bool f16) {
   return f16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// Eight consecutive elements (VEC), or single ones, as fp32. F32: the type of x is
-// fp32, else BF16 or FP16.
-template <bool F32>
-__device__ __forceinline__ void load8(const void* base, long long i, bool f16, float* v) {
-  if constexpr (F32) {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-    const float4 a = __ldcs(s), b = __ldcs(s + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// A step's elements as they lie in memory, all loads of a row before the first use (the
+// stores of h may alias what is still to be read, as far as the compiler knows): eight
+// consecutive ones (VEC), or four single ones.
+template <bool F32, bool VEC>
+struct Raw {
+  uint32_t w[VEC ? (F32 ? 8 : 4) : (F32 ? 4 : 2)];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = from16((w[e >> 1] >> (16 * (e & 1))) & 0xffffu, f16);
+    for (uint32_t& x : w) x = 0;
   }
-}
-template <bool F32>
-__device__ __forceinline__ float load1(const void* base, long long i, bool f16) {
-  if constexpr (F32) return static_cast<const float*>(base)[i];
-  return from16(static_cast<const uint16_t*>(base)[i], f16);
-}
+  __device__ __forceinline__ void load8(const void* base, long long i) {
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + i * (F32 ? 4 : 2));
+    const uint4 a = __ldcs(s);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    if constexpr (F32) {
+      const uint4 b = __ldcs(s + 1);
+      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    }
+  }
+  __device__ __forceinline__ void load1(const void* base, long long i, int e) {
+    if constexpr (F32) w[e] = static_cast<const uint32_t*>(base)[i];
+    else w[e >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t*>(base)[i]) << (16 * (e & 1));
+  }
+  __device__ __forceinline__ float get(int e, bool f16) const {
+    if constexpr (F32) return __uint_as_float(w[e]);
+    return from16((w[e >> 1] >> (16 * (e & 1))) & 0xffffu, f16);
+  }
+};
 __device__ __forceinline__ uint4 pack8(const float* v, bool f16) {
   uint32_t w[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) w[e] = to16(v[2 * e], f16) | to16(v[2 * e + 1], f16) << 16;
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ uint32_t code8(float q, bool int8) {
-  if (int8) return static_cast<uint32_t>(__float2int_rn(fminf(fmaxf(q, -127.0f), 127.0f))) & 0xffu;
-  return __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t code_pair(float a, float b, bool int8) {   // two codes, in 16 bits
+  if (int8) {
+    return (static_cast<uint32_t>(__float2int_rn(fminf(fmaxf(a, -127.0f), 127.0f))) & 0xffu) |
+           (static_cast<uint32_t>(__float2int_rn(fminf(fmaxf(b, -127.0f), 127.0f))) & 0xffu) << 8;
+  }
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
 // Sum, or maximum, over the threads of a row: a warp's lanes, or a block's
@@ -95,8 +105,8 @@ __device__ __forceinline__ float row_reduce(float v, int warps, float (*part)[kN
 
 // VEC: rows of aligned 8-element vectors; a thread's step is one of them. Else a
 // warp's step is 128 elements, a lane's every 32nd of these.
-template <bool F32, bool VEC, int STEPS>
-__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const __grid_constant__ NormParams p, int warps) {
+template <bool F32, bool VEC, int STEPS, int THREADS>
+__global__ void __launch_bounds__(THREADS) add_rmsnorm_kernel(const __grid_constant__ NormParams p, int warps) {
   constexpr int E = VEC ? 8 : 4;
   __shared__ float s_part[2][kNormMaxWarps];
   const int lane = threadIdx.x & 31;
@@ -109,40 +119,43 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const __grid_constant
     return VEC ? ((s * warps + warp) * 32 + lane) * 8 + e : (s * warps + warp) * 128 + e * 32 + lane;
   };
   float v[STEPS][E];
+  {
+    Raw<F32, VEC> x[STEPS], r[STEPS];
+    const auto load = [&](const void* base, long long first, Raw<F32, VEC> (&to)[STEPS]) {
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    const long long i = at(s, 0);
-    if constexpr (VEC) {
-      if (i < p.hidden) {
-        load8<F32>(p.x, row * p.xs + i, f16, v[s]);
-      } else {
+      for (int s = 0; s < STEPS; ++s) {
+        if constexpr (VEC) {
+          if (at(s, 0) < p.hidden) to[s].load8(base, first + at(s, 0));
+          else to[s].zero();
+        } else {
+          to[s].zero();
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[s][e] = 0.f;
+          for (int e = 0; e < E; ++e)
+            if (at(s, e) < p.hidden) to[s].load1(base, first + at(s, e), e);
+        }
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[s][e] = at(s, e) < p.hidden ? load1<F32>(p.x, row * p.xs + at(s, e), f16) : 0.f;
-    }
-  }
-  if (p.r) {
+    };
+    load(p.x, row * p.xs, x);
+    if (p.r) load(p.r, row * p.rs, r);
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-      const long long i = at(s, 0);
-      if constexpr (VEC) {
-        if (i >= p.hidden) continue;
-        float w[E];
-        load8<F32>(p.r, row * p.rs + i, f16, w);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[s][e] += w[e];
+      for (int e = 0; e < E; ++e) v[s][e] = x[s].get(e, f16);
+      if (!p.r) continue;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[s][e] += r[s].get(e, f16);
+      if constexpr (VEC) {
+        const long long i = row * p.hs + at(s, 0);
+        const bool store = p.h && at(s, 0) < p.hidden;
         if constexpr (F32) {
-          if (p.h) {
-            float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.h) + row * p.hs + i);
+          if (store) {
+            float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.h) + i);
             d[0] = make_float4(v[s][0], v[s][1], v[s][2], v[s][3]);
             d[1] = make_float4(v[s][4], v[s][5], v[s][6], v[s][7]);
           }
         } else {
           const uint4 u = pack8(v[s], f16);
-          if (p.h) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.h) + row * p.hs + i) = u;
+          if (store) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.h) + i) = u;
           const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int e = 0; e < E; ++e) v[s][e] = from16((w4[e >> 1] >> (16 * (e & 1))) & 0xffffu, f16);
@@ -150,13 +163,12 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const __grid_constant
       } else {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          if (at(s, e) >= p.hidden) continue;
-          v[s][e] += load1<F32>(p.r, row * p.rs + at(s, e), f16);
+          const bool store = p.h && at(s, e) < p.hidden;
           if constexpr (F32) {
-            if (p.h) static_cast<float*>(p.h)[row * p.hs + at(s, e)] = v[s][e];
+            if (store) static_cast<float*>(p.h)[row * p.hs + at(s, e)] = v[s][e];
           } else {
             const uint32_t u = to16(v[s][e], f16);
-            if (p.h) static_cast<uint16_t*>(p.h)[row * p.hs + at(s, e)] = static_cast<uint16_t>(u);
+            if (store) static_cast<uint16_t*>(p.h)[row * p.hs + at(s, e)] = static_cast<uint16_t>(u);
             v[s][e] = from16(u, f16);
           }
         }
@@ -250,12 +262,12 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const __grid_constant
     if constexpr (VEC) {
       uint32_t w[2] = {0, 0};
 #pragma unroll
-      for (int e = 0; e < E; ++e) w[e >> 2] |= code8(v[s][e] * lift * by, int8) << (8 * (e & 3));
+      for (int e = 0; e < E; e += 2) w[e >> 2] |= code_pair(v[s][e] * lift * by, v[s][e + 1] * lift * by, int8) << (8 * (e & 3));
       if (i < p.hidden) __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + row * p.ys + i), make_uint2(w[0], w[1]));
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (at(s, e) < p.hidden) static_cast<uint8_t*>(p.y)[row * p.ys + at(s, e)] = static_cast<uint8_t>(code8(v[s][e] * lift * by, int8));
+        if (at(s, e) < p.hidden) static_cast<uint8_t*>(p.y)[row * p.ys + at(s, e)] = static_cast<uint8_t>(code_pair(v[s][e] * lift * by, 0.f, int8));
     }
   }
 }
@@ -277,9 +289,11 @@ cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t st) {
   const long long blocks = warps == 1 ? (p.rows + 7) / 8 : p.rows;
   const dim3 grid(static_cast<unsigned>(blocks));
   const char* name = "add_rmsnorm_kernel";
-  if (steps == S0) return launch_kernel(name, add_rmsnorm_kernel<F32, VEC, S0>, grid, dim3(threads), 0, st, false, p, warps);
-  if (steps == S1) return launch_kernel(name, add_rmsnorm_kernel<F32, VEC, S1>, grid, dim3(threads), 0, st, false, p, warps);
-  return launch_kernel(name, add_rmsnorm_kernel<F32, VEC, S2>, grid, dim3(threads), 0, st, false, p, warps);
+  if (steps == S0) return launch_kernel(name, add_rmsnorm_kernel<F32, VEC, S0, 1024>, grid, dim3(threads), 0, st, false, p, warps);
+  if (steps == S1) return launch_kernel(name, add_rmsnorm_kernel<F32, VEC, S1, 1024>, grid, dim3(threads), 0, st, false, p, warps);
+  // (32 elements a thread in 64 registers spill)
+  if (threads <= 512) return launch_kernel(name, add_rmsnorm_kernel<F32, VEC, S2, 512>, grid, dim3(threads), 0, st, false, p, warps);
+  return launch_kernel(name, add_rmsnorm_kernel<F32, VEC, S2, 1024>, grid, dim3(threads), 0, st, false, p, warps);
 }
 
 }  // namespace

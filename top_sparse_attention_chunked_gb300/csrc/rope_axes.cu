@@ -9,7 +9,8 @@
 // Eight lanes hold a head vector, a lane eight pairs of it (its elements
 // 8 l .. and r / 2 + 8 l ..): both partners of a rotation are in one thread, the
 // norm is a sum over eight lanes, and the angles, read once, serve all of the
-// vectors that the lanes go through.
+// vectors that the lanes go through. They are kept multiplied by gamma: with c, s the
+// angle's and g, h the partners' weights, y = (x g c - x' h s) / rms, y' = (x' h c + x g s) / rms.
 #include <cmath>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -42,9 +43,10 @@ struct AxesParams {
   long long tokens, qs, kst, vst, os, pos_stride, cache_rows;
   int hq, hkv, half, max_pos, q_dtype, kv_dtype;  // half: r / 2
   int per_unit, q_units, kv_units;                // vectors of a unit; units of a token's q, and of its k (and v)
-  int cos_f32, whole8;   // whole8: every eight pairs of a lane have one axis, and aligned angles
+  int q_blocks, kv_blocks;                        // thread blocks of the queries, of the keys (and values)
+  int cos_f32, whole8, axes;   // whole8: a lane's eight pairs have one axis, and their angles may be read as vectors
+  uint16_t axis[kRxLanes];     // the axes of a lane's pairs, two bits each
   float eps;
-  uint8_t axis[kRxPairs];
 };
 
 __device__ __forceinline__ float rx_from16(uint32_t u, bool f16) {
@@ -53,11 +55,6 @@ __device__ __forceinline__ float rx_from16(uint32_t u, bool f16) {
 __device__ __forceinline__ uint32_t rx_to16(float v, bool f16) {
   return f16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
-__device__ __forceinline__ uint32_t rx_bits(const uint4& u, int e) {
-  const uint32_t w = (e >> 1) == 0 ? u.x : (e >> 1) == 1 ? u.y : (e >> 1) == 2 ? u.z : u.w;
-  return (w >> (16 * (e & 1))) & 0xffffu;
-}
-
 // Where the lane's eight first and eight second elements of a vector lie. Pairs
 // from r / 2 on are not rotated: elements r + j and r + j + (128 - r) / 2.
 struct LaneAt {
@@ -119,10 +116,10 @@ __device__ __forceinline__ float max8(float v) {
   return v;
 }
 
-// x[0..7]: the lane's first elements, x[8..15]: their partners. x times gamma over
-// the root mean square; all lanes of the warp call it. Sums of squares outside
-// [2^-100, 2^100] are taken of the vector scaled by 2^-+96.
-__device__ __forceinline__ void rx_norm(float (&x)[16], const float (&g)[16], float eps) {
+// 1 over the root mean square of a vector (x[0..7]: the lane's first elements, x[8..15]:
+// their partners); all lanes of the warp call it. Where a sum of squares lies outside
+// [2^-100, 2^100] it is taken of the vector scaled by 2^-+96, which x becomes.
+__device__ __forceinline__ float rx_rms(float (&x)[16], float eps) {
   float ss = 0.f;
 #pragma unroll
   for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
@@ -142,9 +139,7 @@ __device__ __forceinline__ void rx_norm(float (&x)[16], const float (&g)[16], fl
     }
     ss = sum8(ss);
   }
-  const float inv = rsqrtf(fmaf(ss, 1.0f / DSA_HEAD_DIM, eps));
-#pragma unroll
-  for (int e = 0; e < 16; ++e) x[e] = x[e] * inv * g[e];
+  return rsqrtf(fmaf(ss, 1.0f / DSA_HEAD_DIM, eps));
 }
 
 // One 16-bit vector (the lane's packed elements u) into row `to` of a cache.
@@ -162,11 +157,18 @@ __device__ __forceinline__ void rx_append(const AxesParams& p, void* cache, floa
     top = max8(top);
     if (!live) return;
     const float scale = __fdiv_rn(top, 127.0f);
+    // rint(x / scale) from x times the reciprocal: both are within 2^-15 of the quotient, so
+    // they round alike but where it is that near a half; there, and for scales whose
+    // reciprocal may overflow, the quotient itself is rounded
     uint32_t w[4] = {0, 0, 0, 0};
     if (scale != 0.f) {
+      const bool normal = scale >= 1.17549435e-38f;
+      const float by = normal ? __fdiv_rn(1.0f, scale) : 0.f;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float c = fminf(fmaxf(rintf(__fdiv_rn(x[e], scale)), -127.0f), 127.0f);
+        const float q = x[e] * by;
+        float c = rintf(q);
+        if (!normal || fabsf(fabsf(q - c) - 0.5f) < 0x1p-12f) c = fminf(fmaxf(rintf(__fdiv_rn(x[e], scale)), -127.0f), 127.0f);
         w[e >> 2] |= (static_cast<uint32_t>(static_cast<int>(c)) & 0xffu) << (8 * (e & 3));
       }
     }
@@ -195,23 +197,70 @@ __device__ __forceinline__ void rx_append(const AxesParams& p, void* cache, floa
   rx_store<VEC>(static_cast<uint16_t*>(cache) + to * DSA_HEAD_DIM, l, p.half, u);
 }
 
-// A unit is a run of up to per_unit vectors of one token: of its queries, keys or
-// values. Eight lanes take one; the four units of a warp are neighbours, so they run
-// the same code nearly always.
+// The angles of the lane's eight pairs (1 and 0 where they are not rotated).
 template <bool VEC>
-__global__ void __launch_bounds__(kRxThreads) rope_axes_append_kernel(const __grid_constant__ AxesParams p) {
+__device__ __forceinline__ void rx_angles(const AxesParams& p, int l, long long n, float (&cs)[8], float (&sn)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    cs[e] = 1.f;
+    sn[e] = 0.f;
+  }
+  if (8 * l >= p.half) return;
+  const uint32_t axes = p.axis[l];
+  const auto row_of = [&](int a) {
+    int at = __ldg(p.pos + a * p.pos_stride + n);
+    at = at < 0 ? 0 : at >= p.max_pos ? p.max_pos - 1 : at;                    // clamped to the caches
+    return static_cast<long long>(at) * p.half + 8 * l;
+  };
+  if (VEC && p.whole8) {
+    const long long row = row_of(axes & 3u);
+    if (p.cos_f32) {
+      const float4* x = reinterpret_cast<const float4*>(static_cast<const float*>(p.cos) + row);
+      const float4* y = reinterpret_cast<const float4*>(static_cast<const float*>(p.sin) + row);
+      const float4 a0 = __ldg(x), a1 = __ldg(x + 1), b0 = __ldg(y), b1 = __ldg(y + 1);
+      cs[0] = a0.x; cs[1] = a0.y; cs[2] = a0.z; cs[3] = a0.w; cs[4] = a1.x; cs[5] = a1.y; cs[6] = a1.z; cs[7] = a1.w;
+      sn[0] = b0.x; sn[1] = b0.y; sn[2] = b0.z; sn[3] = b0.w; sn[4] = b1.x; sn[5] = b1.y; sn[6] = b1.z; sn[7] = b1.w;
+    } else {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.cos) + row));
+      const uint4 y = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.sin) + row));
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        cs[e] = rx_from16((u[e >> 1] >> (16 * (e & 1))) & 0xffffu, false);
+        sn[e] = rx_from16((v[e >> 1] >> (16 * (e & 1))) & 0xffffu, false);
+      }
+    }
+    return;
+  }
+  // all positions, then all angles: two latencies, whatever the number of axes
+  long long row[DSA_MAX_AXES];
+#pragma unroll
+  for (int a = 0; a < DSA_MAX_AXES; ++a) row[a] = a < p.axes ? row_of(a) : 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (8 * l + e >= p.half) continue;
+    const uint32_t a = (axes >> (2 * e)) & 3u;
+    const long long at = (a == 0 ? row[0] : a == 1 ? row[1] : a == 2 ? row[2] : row[3]) + e;
+    cs[e] = p.cos_f32 ? __ldg(static_cast<const float*>(p.cos) + at) : rx_from16(__ldg(static_cast<const uint16_t*>(p.cos) + at), false);
+    sn[e] = p.cos_f32 ? __ldg(static_cast<const float*>(p.sin) + at) : rx_from16(__ldg(static_cast<const uint16_t*>(p.sin) + at), false);
+  }
+}
+
+// A unit is a run of up to per_unit vectors of one token: of its queries, keys or
+// values. Eight lanes take one; a thread block's are all of the same kind.
+template <bool VEC>
+__global__ void __launch_bounds__(kRxThreads, 2) rope_axes_append_kernel(const __grid_constant__ AxesParams p) {
   const int l = threadIdx.x & (kRxLanes - 1);
-  const int units = p.q_units + 2 * p.kv_units;
-  const long long all = p.tokens * units;
-  const long long unit0 = (static_cast<long long>(blockIdx.x) * kRxThreads + threadIdx.x) / kRxLanes;
+  const int block = blockIdx.x;
+  const int kind = block < p.q_blocks ? 0 : block < p.q_blocks + p.kv_blocks ? 1 : 2;   // q, k, v
+  const int per_token = kind == 0 ? p.q_units : p.kv_units, heads = kind == 0 ? p.hq : p.hkv;
+  const long long all = p.tokens * per_token;
+  const long long unit0 = static_cast<long long>(block - (kind == 0 ? 0 : kind == 1 ? p.q_blocks : p.q_blocks + p.kv_blocks)) *
+                              (kRxThreads / kRxLanes) + threadIdx.x / kRxLanes;
   const bool in = unit0 < all;
   if (!__any_sync(0xffffffffu, in)) return;
-  const long long unit = in ? unit0 : all - 1;
-  const long long n = unit / units;
-  int c = static_cast<int>(unit - n * units);
-  const int kind = c < p.q_units ? 0 : c < p.q_units + p.kv_units ? 1 : 2;     // q, k, v
-  c -= kind == 0 ? 0 : kind == 1 ? p.q_units : p.q_units + p.kv_units;
-  const int h0 = c * p.per_unit, heads = kind == 0 ? p.hq : p.hkv;
+  const long long unit = in ? unit0 : all - 1, n = unit / per_token;
+  const int h0 = static_cast<int>(unit - n * per_token) * p.per_unit;
   const int nv = in ? min(p.per_unit, heads - h0) : 0;
   const uint16_t* src = static_cast<const uint16_t*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
                         n * (kind == 0 ? p.qs : kind == 1 ? p.kst : p.vst) + h0 * DSA_HEAD_DIM;
@@ -221,106 +270,72 @@ __global__ void __launch_bounds__(kRxThreads) rope_axes_append_kernel(const __gr
     if (slot >= p.cache_rows) slot = -1;
   }
   const bool qf = p.q_dtype == DSA_FP16;
-  // this lane's angles, and its share of gamma
-  float cs[8], sn[8], g[16];
-  const float* gamma = kind == 0 ? p.gq : p.gk;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    cs[e] = 1.f;
-    sn[e] = 0.f;
-  }
-  const auto angle_row = [&](int pair) {
-    int at = __ldg(p.pos + p.axis[pair] * p.pos_stride + n);
-    at = at < 0 ? 0 : at >= p.max_pos ? p.max_pos - 1 : at;                    // clamped to the caches
-    return static_cast<long long>(at) * p.half + pair;
-  };
-  if (kind != 2 && 8 * l < p.half) {
-    if (VEC && p.whole8) {
-      const long long at = angle_row(8 * l);
-      if (p.cos_f32) {
-        const float4* a = reinterpret_cast<const float4*>(static_cast<const float*>(p.cos) + at);
-        const float4* b = reinterpret_cast<const float4*>(static_cast<const float*>(p.sin) + at);
-        const float4 a0 = __ldg(a), a1 = __ldg(a + 1), b0 = __ldg(b), b1 = __ldg(b + 1);
-        cs[0] = a0.x; cs[1] = a0.y; cs[2] = a0.z; cs[3] = a0.w; cs[4] = a1.x; cs[5] = a1.y; cs[6] = a1.z; cs[7] = a1.w;
-        sn[0] = b0.x; sn[1] = b0.y; sn[2] = b0.z; sn[3] = b0.w; sn[4] = b1.x; sn[5] = b1.y; sn[6] = b1.z; sn[7] = b1.w;
-      } else {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.cos) + at));
-        const uint4 b = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.sin) + at));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          cs[e] = rx_from16(rx_bits(a, e), false);
-          sn[e] = rx_from16(rx_bits(b, e), false);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (8 * l + e >= p.half) continue;
-        const long long at = angle_row(8 * l + e);
-        cs[e] = p.cos_f32 ? __ldg(static_cast<const float*>(p.cos) + at)
-                          : rx_from16(__ldg(static_cast<const uint16_t*>(p.cos) + at), false);
-        sn[e] = p.cos_f32 ? __ldg(static_cast<const float*>(p.sin) + at)
-                          : rx_from16(__ldg(static_cast<const uint16_t*>(p.sin) + at), false);
-      }
-    }
-  }
-  const bool norm = kind != 2 && gamma != nullptr;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    g[e] = norm ? __ldg(gamma + pair_a(8 * l + e, p.half)) : 1.f;
-    g[8 + e] = norm ? __ldg(gamma + pair_b(8 * l + e, p.half)) : 1.f;
-  }
-  const bool any_norm = __any_sync(0xffffffffu, norm);
   int most = nv;                                                                // (the warp's lanes stay together)
   most = max(most, __shfl_xor_sync(0xffffffffu, most, 8));
   most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
+  const auto load = [&](int i, uint32_t (&u)[8]) {
+    if (i < nv) {
+      rx_load<VEC>(src + i * DSA_HEAD_DIM, l, p.half, u);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = 0;
+    }
+  };
+  if (kind == 2) {
+    for (int i0 = 0; i0 < most; i0 += kRxBatch) {
+      uint32_t u[kRxBatch][8];
+#pragma unroll
+      for (int i = 0; i < kRxBatch; ++i) load(i0 + i, u[i]);
+#pragma unroll
+      for (int i = 0; i < kRxBatch; ++i)
+        rx_append<VEC>(p, p.vc, p.vs, slot * p.hkv + h0 + i0 + i, i0 + i < nv && slot >= 0, l, u[i]);
+    }
+    return;
+  }
+  uint32_t u[kRxBatch][8];
+#pragma unroll
+  for (int i = 0; i < kRxBatch; ++i) load(i, u[i]);                             // (in flight beside the angles)
+  const float* gamma = kind == 0 ? p.gq : p.gk;
+  // the factors of the lane's pairs: first elements gc, hs, partners hc, gs
+  float gc[8], hs[8], hc[8], gs[8];
+  {
+    float cs[8], sn[8];
+    rx_angles<VEC>(p, l, n, cs, sn);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float g = gamma ? __ldg(gamma + pair_a(8 * l + e, p.half)) : 1.f, h = gamma ? __ldg(gamma + pair_b(8 * l + e, p.half)) : 1.f;
+      gc[e] = g * cs[e];
+      gs[e] = g * sn[e];
+      hc[e] = h * cs[e];
+      hs[e] = h * sn[e];
+    }
+  }
   for (int i0 = 0; i0 < most; i0 += kRxBatch) {
-    uint32_t u[kRxBatch][8];
+    if (i0 > 0) {
 #pragma unroll
-    for (int i = 0; i < kRxBatch; ++i) {
-      if (i0 + i < nv) {
-        rx_load<VEC>(src + (i0 + i) * DSA_HEAD_DIM, l, p.half, u[i]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[i][e] = 0;
-      }
+      for (int i = 0; i < kRxBatch; ++i) load(i0 + i, u[i]);
     }
 #pragma unroll
     for (int i = 0; i < kRxBatch; ++i) {
       if (i0 + i >= most) break;
       const bool live = i0 + i < nv;
-      if (__any_sync(0xffffffffu, kind != 2)) {
-        float x[16];
+      float x[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = rx_from16((u[i][e >> 1] >> (16 * (e & 1))) & 0xffffu, qf);
-        if (any_norm) {
-          float y[16];
+      for (int e = 0; e < 16; ++e) x[e] = rx_from16((u[i][e >> 1] >> (16 * (e & 1))) & 0xffffu, qf);
+      const float inv = gamma ? rx_rms(x, p.eps) : 1.0f;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = x[e];
-          rx_norm(y, g, p.eps);
-          if (norm) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = y[e];
-          }
-        }
-        if (kind != 2) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if ((VEC ? 8 * l : 8 * l + e) >= p.half) continue;
-            const float a = x[e], b = x[8 + e];
-            x[e] = a * cs[e] - b * sn[e];
-            x[8 + e] = b * cs[e] + a * sn[e];
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u[i][e] = rx_to16(x[2 * e], qf) | rx_to16(x[2 * e + 1], qf) << 16;
-        }
+      for (int e = 0; e < 8; ++e) {
+        const float a = x[e], b = x[8 + e];
+        x[e] = (a * gc[e] - b * hs[e]) * inv;
+        x[8 + e] = (b * hc[e] + a * gs[e]) * inv;
       }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[i][e] = rx_to16(x[2 * e], qf) | rx_to16(x[2 * e + 1], qf) << 16;
       if (kind == 0) {
         if (live) rx_store<VEC>(static_cast<uint16_t*>(p.out) + n * p.os + (h0 + i0 + i) * DSA_HEAD_DIM, l, p.half, u[i]);
+      } else {
+        rx_append<VEC>(p, p.kc, p.ks, slot * p.hkv + h0 + i0 + i, live && slot >= 0, l, u[i]);
       }
-      if (__any_sync(0xffffffffu, kind != 0))
-        rx_append<VEC>(p, kind == 1 ? p.kc : p.vc, kind == 1 ? p.ks : p.vs, slot * p.hkv + h0 + i0 + i,
-                       live && kind != 0 && slot >= 0, l, u[i]);
     }
   }
 }
@@ -419,6 +434,8 @@ extern "C" int dsa_rope_axes_append(const dsa_axes_problem* ap, const void* q, c
   p.tokens = N, p.qs = st4[0], p.kst = st4[1], p.vst = st4[2], p.os = st4[3], p.pos_stride = ps, p.cache_rows = ap->cache_rows;
   p.hq = hq, p.hkv = hkv, p.half = half, p.max_pos = ap->max_pos, p.q_dtype = ap->q_dtype, p.kv_dtype = ap->kv_dtype;
   p.cos_f32 = ap->cos_dtype == DSA_FP32, p.eps = ap->eps;
+  p.axes = ap->axes;
+  int axis[kRxPairs] = {};
   if (ap->in_turn) {
     int left[DSA_MAX_AXES], n = 0;
     for (int a = 0; a < ap->axes; ++a) left[a] = ap->sections[a];
@@ -426,23 +443,28 @@ extern "C" int dsa_rope_axes_append(const dsa_axes_problem* ap, const void* q, c
       for (int a = 0; a < ap->axes; ++a)
         if (left[a] > 0) {
           --left[a];
-          p.axis[n++] = static_cast<uint8_t>(a);
+          axis[n++] = a;
         }
   } else {
     for (int a = 0, n = 0; a < ap->axes; ++a)
-      for (int i = 0; i < ap->sections[a]; ++i) p.axis[n++] = static_cast<uint8_t>(a);
+      for (int i = 0; i < ap->sections[a]; ++i) axis[n++] = a;
   }
   bool whole8 = half % 8 == 0 && !off(cos_cache, 16) && !off(sin_cache, 16);
-  for (int i = 0; i < half && whole8; ++i) whole8 = p.axis[i] == p.axis[i & ~7];
+  for (int i = 0; i < half; ++i) {
+    whole8 = whole8 && axis[i] == axis[i & ~7];
+    p.axis[i / 8] |= static_cast<uint16_t>(axis[i] << (2 * (i % 8)));
+  }
   p.whole8 = whole8;
-  // a unit's vectors share their angles: as many as leave every SM enough of them
-  p.per_unit = N * (hq + 2 * hkv) >= 64LL * 1024 * 4 ? 8 : kRxBatch;
-  if (N * (hq + 2 * hkv) < 16LL * sms * 32) p.per_unit = 1;
+  // a unit's vectors share their angles: as many as leave every SM a few hundred units
+  const long long vectors = N * (hq + 2 * hkv);
+  p.per_unit = vectors >= 2048LL * sms ? 8 : vectors >= 512LL * sms ? 4 : vectors >= 128LL * sms ? 2 : 1;
   p.q_units = (hq + p.per_unit - 1) / p.per_unit;
   p.kv_units = (hkv + p.per_unit - 1) / p.per_unit;
-  const long long units = N * (p.q_units + 2 * p.kv_units);
-  const long long blocks = (units * kRxLanes + kRxThreads - 1) / kRxThreads;
+  constexpr int kUnits = kRxThreads / kRxLanes;
+  const long long qb = (N * p.q_units + kUnits - 1) / kUnits, kb = (N * p.kv_units + kUnits - 1) / kUnits, blocks = qb + 2 * kb;
   if (blocks > 0x7fffffffLL) return report_error(DSA_ERR_UNSUPPORTED, "too many tokens and heads for one call");
+  p.q_blocks = static_cast<int>(qb);
+  p.kv_blocks = static_cast<int>(kb);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>(blocks));
   const cudaError_t e =
