@@ -11,6 +11,7 @@
 // norm is a sum over eight lanes, and the angles, read once, serve all of the
 // vectors that the lanes go through. They are kept multiplied by gamma: with c, s the
 // angle's and g, h the partners' weights, y = (x g c - x' h s) / rms, y' = (x' h c + x g s) / rms.
+#include <algorithm>
 #include <cmath>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -52,8 +53,21 @@ struct AxesParams {
 __device__ __forceinline__ float rx_from16(uint32_t u, bool f16) {
   return f16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(u))) : __uint_as_float(u << 16);
 }
-__device__ __forceinline__ uint32_t rx_to16(float v, bool f16) {
-  return f16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+// Two 16-bit values in a word, and the other way.
+template <bool F16>
+__device__ __forceinline__ uint32_t rx_pack(float a, float b) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+template <bool F16>
+__device__ __forceinline__ float2 rx_unpack(uint32_t u) {
+  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&u));
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 // Where the lane's eight first and eight second elements of a vector lie. Pairs
 // from r / 2 on are not rotated: elements r + j and r + j + (128 - r) / 2.
@@ -143,16 +157,17 @@ __device__ __forceinline__ float rx_rms(float (&x)[16], float eps) {
 }
 
 // One 16-bit vector (the lane's packed elements u) into row `to` of a cache.
-template <bool VEC>
+template <bool VEC, bool F16>
 __device__ __forceinline__ void rx_append(const AxesParams& p, void* cache, float* scales, long long to, bool live, int l,
                                           uint32_t (&u)[8]) {
-  const bool qf = p.q_dtype == DSA_FP16;
   if (p.kv_dtype == DSA_INT8) {
     float x[16], top = 0.f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      x[e] = rx_from16((u[e >> 1] >> (16 * (e & 1))) & 0xffffu, qf);
-      top = fmaxf(top, fabsf(x[e]));
+    for (int e = 0; e < 8; ++e) {
+      const float2 v = rx_unpack<F16>(u[e]);
+      x[2 * e] = v.x;
+      x[2 * e + 1] = v.y;
+      top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
     }
     top = max8(top);
     if (!live) return;
@@ -188,11 +203,14 @@ __device__ __forceinline__ void rx_append(const AxesParams& p, void* cache, floa
     return;
   }
   if (!live) return;
-  if (p.kv_dtype != p.q_dtype) {
-    const bool cf = p.kv_dtype == DSA_FP16;
+  if constexpr (!F16) {
+    if (p.kv_dtype == DSA_FP16) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      u[e] = rx_to16(rx_from16(u[e] & 0xffffu, qf), cf) | rx_to16(rx_from16(u[e] >> 16, qf), cf) << 16;
+      for (int e = 0; e < 8; ++e) {
+        const float2 v = rx_unpack<false>(u[e]);
+        u[e] = rx_pack<true>(v.x, v.y);
+      }
+    }
   }
   rx_store<VEC>(static_cast<uint16_t*>(cache) + to * DSA_HEAD_DIM, l, p.half, u);
 }
@@ -248,7 +266,7 @@ __device__ __forceinline__ void rx_angles(const AxesParams& p, int l, long long 
 
 // A unit is a run of up to per_unit vectors of one token: of its queries, keys or
 // values. Eight lanes take one; a thread block's are all of the same kind.
-template <bool VEC>
+template <bool VEC, bool F16>
 __global__ void __launch_bounds__(kRxThreads, 2) rope_axes_append_kernel(const __grid_constant__ AxesParams p) {
   const int l = threadIdx.x & (kRxLanes - 1);
   const int block = blockIdx.x;
@@ -269,7 +287,6 @@ __global__ void __launch_bounds__(kRxThreads, 2) rope_axes_append_kernel(const _
     slot = __ldg(p.slots + n);
     if (slot >= p.cache_rows) slot = -1;
   }
-  const bool qf = p.q_dtype == DSA_FP16;
   int most = nv;                                                                // (the warp's lanes stay together)
   most = max(most, __shfl_xor_sync(0xffffffffu, most, 8));
   most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
@@ -288,7 +305,7 @@ __global__ void __launch_bounds__(kRxThreads, 2) rope_axes_append_kernel(const _
       for (int i = 0; i < kRxBatch; ++i) load(i0 + i, u[i]);
 #pragma unroll
       for (int i = 0; i < kRxBatch; ++i)
-        rx_append<VEC>(p, p.vc, p.vs, slot * p.hkv + h0 + i0 + i, i0 + i < nv && slot >= 0, l, u[i]);
+        rx_append<VEC, F16>(p, p.vc, p.vs, slot * p.hkv + h0 + i0 + i, i0 + i < nv && slot >= 0, l, u[i]);
     }
     return;
   }
@@ -321,7 +338,11 @@ __global__ void __launch_bounds__(kRxThreads, 2) rope_axes_append_kernel(const _
       const bool live = i0 + i < nv;
       float x[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = rx_from16((u[i][e >> 1] >> (16 * (e & 1))) & 0xffffu, qf);
+      for (int e = 0; e < 8; ++e) {
+        const float2 v = rx_unpack<F16>(u[i][e]);
+        x[2 * e] = v.x;
+        x[2 * e + 1] = v.y;
+      }
       const float inv = gamma ? rx_rms(x, p.eps) : 1.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -330,11 +351,11 @@ __global__ void __launch_bounds__(kRxThreads, 2) rope_axes_append_kernel(const _
         x[8 + e] = (b * hc[e] + a * gs[e]) * inv;
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) u[i][e] = rx_to16(x[2 * e], qf) | rx_to16(x[2 * e + 1], qf) << 16;
+      for (int e = 0; e < 8; ++e) u[i][e] = rx_pack<F16>(x[2 * e], x[2 * e + 1]);
       if (kind == 0) {
         if (live) rx_store<VEC>(static_cast<uint16_t*>(p.out) + n * p.os + (h0 + i0 + i) * DSA_HEAD_DIM, l, p.half, u[i]);
       } else {
-        rx_append<VEC>(p, p.kc, p.ks, slot * p.hkv + h0 + i0 + i, live && slot >= 0, l, u[i]);
+        rx_append<VEC, F16>(p, p.kc, p.ks, slot * p.hkv + h0 + i0 + i, live && slot >= 0, l, u[i]);
       }
     }
   }
@@ -455,9 +476,11 @@ extern "C" int dsa_rope_axes_append(const dsa_axes_problem* ap, const void* q, c
     p.axis[i / 8] |= static_cast<uint16_t>(axis[i] << (2 * (i % 8)));
   }
   p.whole8 = whole8;
-  // a unit's vectors share their angles: as many as leave every SM a few hundred units
-  const long long vectors = N * (hq + 2 * hkv);
-  p.per_unit = vectors >= 2048LL * sms ? 8 : vectors >= 512LL * sms ? 4 : vectors >= 128LL * sms ? 2 : 1;
+  // A unit's vectors share their angles: as many (of 1, 2 .. 32) as leave every SM some 40
+  // units, of the 64 that it takes at once. (8,192 tokens of 32 / 8 heads: units of 2, 4, 8,
+  // 16, 32 take 79, 55, 47, 42, 40 us.)
+  p.per_unit = 32;
+  while (p.per_unit > 1 && N * ((std::max(hq, hkv) + p.per_unit - 1) / p.per_unit) < 40LL * sms) p.per_unit /= 2;
   p.q_units = (hq + p.per_unit - 1) / p.per_unit;
   p.kv_units = (hkv + p.per_unit - 1) / p.per_unit;
   constexpr int kUnits = kRxThreads / kRxLanes;
@@ -467,9 +490,11 @@ extern "C" int dsa_rope_axes_append(const dsa_axes_problem* ap, const void* q, c
   p.kv_blocks = static_cast<int>(kb);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>(blocks));
-  const cudaError_t e =
-      half % 8 == 0 ? launch_kernel("rope_axes_append_kernel", rope_axes_append_kernel<true>, grid, dim3(kRxThreads), 0, st, false, p)
-                    : launch_kernel("rope_axes_append_kernel", rope_axes_append_kernel<false>, grid, dim3(kRxThreads), 0, st, false, p);
+  const bool vec = half % 8 == 0, f16 = ap->q_dtype == DSA_FP16;
+  using K = void(const AxesParams);
+  K* const kernels[2][2] = {{rope_axes_append_kernel<false, false>, rope_axes_append_kernel<false, true>},
+                            {rope_axes_append_kernel<true, false>, rope_axes_append_kernel<true, true>}};
+  const cudaError_t e = launch_kernel("rope_axes_append_kernel", kernels[vec][f16], grid, dim3(kRxThreads), 0, st, false, p);
   if (e != cudaSuccess) return report_errorf(DSA_ERR_CUDA, "rope_axes_append launch: %s", cudaGetErrorString(e));
   return DSA_OK;
 }
