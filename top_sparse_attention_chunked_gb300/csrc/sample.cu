@@ -132,6 +132,7 @@ constexpr float kInt = 12582912.0f;             // 1.5 * 2^23: to whole numbers
 constexpr float kHigh = 3.0f;                   // 1.5 * 2^1: to multiples of 2^-22
 constexpr float kLow = 0x1.8p-22f;              // 1.5 * 2^-22: to multiples of 2^-45
 constexpr int kGridSpan = 64;
+constexpr int kBinPoints = 16;                  // grid points of a bin
 constexpr int kZero = 60 * 512;                 // weights from 2^-60 of the largest down are none at all
 // x -> log2 of the weight, in units of 1 / 512 and a rest: (x - b) (ch + cl), ch + cl =
 // log2 e / T as a pair of floats. b is 0, or the largest x where that is too large to be a
@@ -153,7 +154,8 @@ __device__ __forceinline__ int grid_of(const Scale& s, float x) { return point_o
 // pairs of fp32 operations need their constants in registers, which are not there.
 struct Weight {
   uint32_t h, l;
-  int point;                                    // the token's grid point
+  int point;                                    // the token's grid point,
+  float r;                                      // and what its exponent has beyond it
   __device__ __forceinline__ unsigned long long value() const {   // in units of 2^-45
     return (static_cast<unsigned long long>(h - __float_as_uint(kHigh)) << 23) +
            static_cast<long long>(static_cast<int>(l - __float_as_uint(kLow)));
@@ -169,6 +171,7 @@ __device__ __forceinline__ Weight weight_if(const Scale& s, const float2* tab, f
   Weight y;
   y.point = __float_as_int(t);
   if (y.point <= s.zero) r = 0.f;               // (it may be infinite or NaN; the power leaves nothing)
+  y.r = r;
   const float2 a = tab[y.point & 511];
   const float q = __fmul_rn(r, __fmaf_rn(r, __fmaf_rn(r, 0.05550411f, 0.24022651f), 0.69314718f));
   const float b = __fmaf_rn(a.x, q, a.y), w = __fadd_rn(a.x, b), e = __fadd_rn(__fadd_rn(a.x, -w), b);   // w + e = a (1 + q)
@@ -350,22 +353,27 @@ struct Sampler {
     if (b0 >= 0) atomicAdd(hist + b0, b0 == b1 ? 2u : 1u);
     if (b1 >= 0 && b0 != b1) atomicAdd(hist + b1, 1u);
   }
-  // The same for tokens at grid points g below 0: bins of 32 points, and by how much.
-  __device__ __forceinline__ void count_grid(uint32_t* hist, uint32_t* below, int g0, int g1) {
-    const int b0 = -g0 >> 5, b1 = -g1 >> 5;
-    uint32_t n = 1, s0 = static_cast<uint32_t>(-g0) & 31u;
-    const uint32_t s1 = static_cast<uint32_t>(-g1) & 31u;
+  // The same by the weights: bins of kBinPoints grid points, and how far below its bin's
+  // edge a token lies, in 64ths of a point (and kBelow of them more, so that it is positive).
+  static constexpr int kBelow = 40;
+  __device__ __forceinline__ void count_weights(uint32_t* hist, uint32_t* below, const Weight& a, const Weight& b) {
+    const int g0 = sc.base - a.point, g1 = sc.base - b.point, b0 = g0 / kBinPoints, b1 = g1 / kBinPoints;   // (both >= 0)
+    const auto under = [](int g, float r) {
+      return static_cast<uint32_t>((g & (kBinPoints - 1)) * 64 + kBelow + __float_as_int(fmaf(r, -32768.0f, kInt)) - __float_as_int(kInt));
+    };
+    uint32_t n = 1, s0 = under(g0, a.r);
+    const uint32_t s1 = under(g1, b.r);
     if (b0 == b1) {
       n = 2;
       s0 += s1;
     }
     if (b0 < kSmBins - 1) {
       atomicAdd(hist + b0, n);
-      if (s0) atomicAdd(below + b0, s0);
+      atomicAdd(below + b0, s0);
     }
     if (b1 < kSmBins - 1 && b0 != b1) {
       atomicAdd(hist + b1, 1u);
-      if (s1) atomicAdd(below + b1, s1);
+      atomicAdd(below + b1, s1);
     }
   }
 
@@ -401,9 +409,9 @@ struct Sampler {
     if (threadIdx.x == 0) sh.lo_bin = sh.hi_bin = kSmBins - 1;
     const float l = scan<float>(l0, sh.warp_bound) + l0;
     const float u = scan<float>(u0, sh.warp_bound) + u0;
-    // (1e-4: far beyond what these sums of positive terms are off by)
-    if (u >= need * 0.9999f) atomicMin(&sh.lo_bin, static_cast<int>(threadIdx.x));
-    if (l >= need * 1.0001f) atomicMin(&sh.hi_bin, static_cast<int>(threadIdx.x));
+    // (2e-5: far beyond what these sums of positive terms are off by)
+    if (u >= need * 0.99998f) atomicMin(&sh.lo_bin, static_cast<int>(threadIdx.x));
+    if (l >= need * 1.00002f) atomicMin(&sh.hi_bin, static_cast<int>(threadIdx.x));
     __syncthreads();
   }
   __device__ __forceinline__ void find_sum(uint32_t n, unsigned long long w, unsigned long long need) {
@@ -587,13 +595,13 @@ struct Sampler {
     __syncthreads();
     return listed;
   }
-  // The same of the tokens of bins b0 .. b1 (kSmList at most) of the counts by 32 grid
-  // points, `above` tokens in those before.
+  // The same of the tokens of bins b0 .. b1 (kSmList at most) of the counts by the weights,
+  // `above` tokens in those before.
   template <bool SUM>
   __device__ __forceinline__ bool cut_bins(int b0, int b1, uint32_t above, unsigned long long need, float* cx, int* ci,
                                            unsigned long long* upto) {
     const uint32_t ph = phase & 1;
-    const int p0 = sc.base - 32 * b0, p1 = sc.base - 32 * b1 - 31;
+    const int p0 = sc.base - kBinPoints * b0, p1 = sc.base - kBinPoints * (b1 + 1) + 1;
     if (threadIdx.x == 0) sh.fill[ph] = 0;
     __syncthreads();
     WeightSum sum;
@@ -609,7 +617,7 @@ struct Sampler {
     if (!settle<SUM>(ph, s.sum, above, need, cx, ci, upto)) return false;
     list_above = sum.value();
     list_sums = s;
-    list_top = b0 > 0 ? __fsub_rd(sc.top, __fmul_ru(static_cast<float>(32 * b0 + 1), 1.0f / (512.0f * sc.ch))) : INFINITY;
+    list_top = b0 > 0 ? __fsub_rd(sc.top, __fmul_ru(static_cast<float>(kBinPoints * b0 + 1), 1.0f / (512.0f * sc.ch))) : INFINITY;
     return true;
   }
 
@@ -913,7 +921,7 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
         const auto all = [](int) { return true; };
         const Weight a = weight_if(sc, sh.tab, x0, all), b = weight_if(sc, sh.tab, x1, all);
         sum.add(a, b);
-        s.count_grid(sh.hist[lp], sh.below[lp], a.point - sc.base, b.point - sc.base);
+        s.count_weights(sh.hist[lp], sh.below[lp], a, b);
       });
     s.row.each([&](const float (&x)[kVec], int idx) {
       float most = x[0];
@@ -971,16 +979,18 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   } else if (greedy) {
     s.template cut<false>(1, top, top, false, &cx, &ci);          // (more of the largest than a list holds)
   } else if (by_k || by_p) {
-    // counts by the weights' logarithm, bins of 32 grid points
-    uint32_t ph2 = 1;
+    // counts by the weights (and of all tokens that may be taken)
+    uint32_t ph2 = 1, finite = 0;
     if (!counted) {
       ph2 = s.phase & 1;
       sh.below[ph2][threadIdx.x] = 0;
       uint32_t* hist = s.clear_hist();
       s.row.pairs(s.row.first, s.row.count, [&](float x0, float x1, int) {
-        s.count_grid(hist, sh.below[ph2], grid_of(sc, x0), grid_of(sc, x1));
+        const auto all = [](int) { return true; };
+        s.count_weights(hist, sh.below[ph2], weight_if(sc, sh.tab, x0, all), weight_if(sc, sh.tab, x1, all));
+        finite += (x0 > -INFINITY ? 1u : 0u) + (x1 > -INFINITY ? 1u : 0u);
       });
-      s.exchange(0, 0);
+      finite = s.exchange(0, finite).cnt;
     }
     const uint32_t n = s.bins(sh.hist[ph2]);
     const float inv_c = 1.0f / sc.ch;
@@ -988,45 +998,54 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     // whether a list holds these bins' tokens and their neighbours'
     const auto range = [&](int b0, int b1, float* lo, float* hi) {
       const uint32_t left = s.held(n, b0 - 1, b1 + 1);
-      *hi = b0 <= 0 ? top : fminf(top, __fsub_ru(top, __fmul_rd(static_cast<float>(32 * b0 - 2) * (1.0f / 512.0f), inv_c)));
-      *lo = __fsub_rd(top, __fmul_ru(static_cast<float>(32 * (b1 + 1) + 2) * (1.0f / 512.0f), inv_c));
+      *hi = b0 <= 0 ? top : fminf(top, __fsub_ru(top, __fmul_rd(static_cast<float>(kBinPoints * b0 - 2) * (1.0f / 512.0f), inv_c)));
+      *lo = __fsub_rd(top, __fmul_ru(static_cast<float>(kBinPoints * (b1 + 1) + 2) * (1.0f / 512.0f), inv_c));
       return left <= kSmList && b1 + 1 < kSmBins - 1;
     };
     float lo, hi;
     bool cut_k = false;
-    if (by_k) {
+    if (by_k && static_cast<uint32_t>(k) < finite) {
       if (threadIdx.x == 0) sh.lo_bin = -1;
       __syncthreads();
       s.find_count(n, k);
       const int b = sh.lo_bin;
       __syncthreads();
-      if (b >= 0) {                                               // (else: more tokens than have a weight)
-        if (s.held(n, b, b) > kSmList || !s.template cut_bins<false>(b, b, s.held(n, 0, b - 1), k, &cx, &ci, &total)) {
-          const bool few = range(b, b, &lo, &hi);
-          total = s.template cut<false>(k, lo, hi, few, &cx, &ci);
-        }
-        cut_k = true;
-      } else if (by_p) {
-        WeightSum sum;
-        s.row.pairs(s.row.first, s.row.count, [&](float x0, float x1, int) {
-          const auto all = [](int) { return true; };
-          sum.add(weight_if(sc, sh.tab, x0, all), weight_if(sc, sh.tab, x1, all));
-        });
-        total = s.exchange(sum.value(), 0).sum;
+      if (b < 0) {                                                // (below the last bin)
+        total = s.template cut<false>(k, -3.402823466e38f, top, false, &cx, &ci);
+      } else if (s.held(n, b, b) > kSmList || !s.template cut_bins<false>(b, b, s.held(n, 0, b - 1), k, &cx, &ci, &total)) {
+        const bool few = range(b, b, &lo, &hi);
+        total = s.template cut<false>(k, lo, hi, few, &cx, &ci);
       }
+      cut_k = true;
+    } else if (by_k && by_p) {                                    // (k leaves everything)
+      WeightSum sum;
+      s.row.pairs(s.row.first, s.row.count, [&](float x0, float x1, int) {
+        const auto all = [](int) { return true; };
+        sum.add(weight_if(sc, sh.tab, x0, all), weight_if(sc, sh.tab, x1, all));
+      });
+      total = s.exchange(sum.value(), 0).sum;
     }
     if (by_p) {
-      // A bin's n tokens lie `m` grid points below its edge, between 0 and 31 each (rounded:
-      // half a point more or less). 2^-x is convex: they weigh at least n times the weight
-      // at their mean, at most what the chord from 0 to 31 gives.
+      // A bin's n tokens lie m grid points below its edge on average, each between -0.7 and
+      // 15.7 (a point's rounding is half of one, a sum's a 128th a token). 2^-x is convex:
+      // they weigh at least n times the weight at their mean, at most what the chord
+      // between the ends gives.
       const unsigned long long need = share(total);
-      const float m = s.bins(sh.below[ph2]), edge = -32.0f * threadIdx.x;
+      const float m = n ? (static_cast<float>(s.bins(sh.below[ph2])) / static_cast<float>(n) - s.kBelow) * (1.0f / 64.0f) : 0.f;
+      const float edge = -static_cast<float>(kBinPoints * static_cast<int>(threadIdx.x));
       const auto w = [&](float g) { return exp2f(g * (1.0f / 512.0f)) * s.unit(); };
-      const float l = n && threadIdx.x < 700 ? n * w(edge - m / n - 0.52f) : 0.f, w0 = w(edge + 0.52f), w1 = w(edge - 30.48f);
-      s.find_bounds(l, n * w0 + m * (1.0f / 31.0f) * (w1 - w0), static_cast<float>(need));
+      const float w0 = w(edge + 0.7f), w1 = w(edge - (kBinPoints - 0.3f));
+      s.find_bounds(n * w(edge - m - 0.02f), n * (w0 + (m + 0.68f) * (1.0f / (kBinPoints + 0.4f)) * (w1 - w0)), static_cast<float>(need));
       const int b0 = sh.lo_bin, b1 = sh.hi_bin;
       __syncthreads();
-      if (b1 == kSmBins - 1 || s.held(n, b0, b1) > kSmList || !s.template cut_bins<true>(b0, b1, 0, need, &cx, &ci, &total)) {
+      // both bins at once where a list holds them, else one after the other
+      bool found = false;
+      if (b1 < kSmBins - 1 && b1 - b0 < 4) {
+        const bool all = s.held(n, b0, b1) <= kSmList;
+        for (int b = b0; b <= b1 && !found; b = all ? b1 + 1 : b + 1)
+          if (all || s.held(n, b, b) <= kSmList) found = s.template cut_bins<true>(b, all ? b1 : b, 0, need, &cx, &ci, &total);
+      }
+      if (!found) {
         const bool few = range(b0, b1, &lo, &hi);
         if (cut_k) {                                              // (the cut there is ends the range)
           lo = fmaxf(lo, cx);

@@ -862,19 +862,17 @@ def _token_rows(dev: int, t, name: str, dtype, tokens: int, heads: int):
     [tokens, heads, 128] whose tokens' vectors lie together each."""
     if t is None:
         return None, 0
-    width = heads * 128
     if t.dtype is not dtype or t.get_device() != dev:
         _refuse(dev, t, name, dtype, None)
-    st = t.stride()
-    if t.dim() == 2:
-        ok = t.shape[0] == tokens and t.shape[1] == width and (width <= 1 or st[1] == 1)
+    st, shape = t.stride(), t.shape
+    if shape == (tokens, heads * 128):
+        ok = st[1] == 1 or heads == 0
     else:
-        ok = (t.dim() == 3 and t.shape[0] == tokens and t.shape[1] == heads and t.shape[2] == 128
-              and (width == 0 or st[2] == 1) and (heads <= 1 or st[1] == 128))
+        ok = shape == (tokens, heads, 128) and (heads == 0 or (st[2] == 1 and (heads == 1 or st[1] == 128)))
     if not ok:
-        raise ValueError(f"{name} must be [{tokens}, {width}] or [{tokens}, {heads}, 128], each token's vectors "
-                         f"contiguous, got {tuple(t.shape)} with strides {st}")
-    return t.data_ptr(), st[0] if tokens > 1 and width else 0
+        raise ValueError(f"{name} must be [{tokens}, {heads * 128}] or [{tokens}, {heads}, 128], each token's vectors "
+                         f"contiguous, got {tuple(shape)} with strides {st}")
+    return t.data_ptr(), st[0] if tokens > 1 and heads else 0
 
 
 def dsa_rope_axes_append(p: DsaAxesProblem, q, k, v, gamma_q, gamma_k, cos, sin, positions, slots, q_out, k_cache, v_cache,
@@ -893,7 +891,7 @@ def dsa_rope_axes_append(p: DsaAxesProblem, q, k, v, gamma_q, gamma_k, cos, sin,
         p.pos_stride, shape = 0, (n,)
     else:
         p.pos_stride, shape = n, (p.axes, n)
-    half = sum(p.sections[:p.axes])
+    half = sum(p.sections)             # (those behind the last axis are 0)
     cache, angles, cdt = (p.cache_rows, hkv, 128), (p.max_pos, half), _TORCH_DT[p.cos_dtype]
     a = _here(dev, (gamma_q, "gamma_q", f32, (128,)), (gamma_k, "gamma_k", f32, (128,)), (cos, "cos", cdt, angles),
               (sin, "sin", cdt, angles), (positions, "positions", i32, shape), (slots, "slots", i32, (n,)),
