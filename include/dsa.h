@@ -893,8 +893,9 @@ int dsa_add_rmsnorm(const dsa_norm_problem* p, const void* x, const void* residu
  * No result overlaps an input or the other result.
  *
  * The cut and the draw are those of exact arithmetic on weights that are right
- * to about 2^-31 of themselves and are 0 below 2^-44 of the largest; sums are
- * of whole numbers, so the result does not depend on the order of execution.
+ * to 2^-31 of themselves or to 2^-45 of the largest, whichever is more (so some
+ * below that are 0); sums are of whole numbers, so the result does not depend
+ * on the order of execution.
  * One kernel; no workspace.
  */
 typedef struct dsa_sample_problem {

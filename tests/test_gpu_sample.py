@@ -141,6 +141,16 @@ def test_flat_and_steep_rows(D, dtype, std, heat):
         run(D, x, uniform(8, i), heat=heat, **s)
 
 
+@pytest.mark.parametrize("rows,vocab,dtype,std", [(48, 131072, "bf16", 1.6), (48, 131072, "fp32", 1.3), (24, 262144, "fp16", 2.5), (60, 65536, "bf16", 0.8)])
+def test_cuts_among_many_tokens_of_like_weight(D, rows, vocab, dtype, std):
+    """Nuclei that end where a 32nd of a factor of two holds some 500 to 2,000 tokens, at every place within one."""
+    x = logits_of(rows, vocab, dtype, std=std, seed=vocab + rows, peaks=5)
+    for i, (a, b) in enumerate(((0.2, 0.95), (0.6, 0.7))):
+        p = a + (b - a) * uniform(rows, 40 + i)
+        run(D, x, uniform(rows, i), p=p)
+        run(D, x, uniform(rows, 9 + i), p=p, k=torch.where(torch.arange(rows) % 2 == 0, vocab, vocab // 3), low=1e-4)
+
+
 def test_rows_of_equal_logits(D):
     """Ties go to the lower index, in top-k, in top-p and with the cut inside a tie."""
     for vocab in (10, 1000, 70000, 300000):

@@ -8,18 +8,26 @@
 // kept, and two sums over the row.
 //
 // A draw between 100,000 tokens is next to a border nearly always, so weights and
-// sums have to be the same whatever the order: a weight is a multiple of a fixed unit
-// (of the largest, 2^-62 times the row's length rounded up to a power of two), formed
-// in fp32 pairs to 2^-31 of itself, and all sums are of 64-bit integers.
+// sums have to be the same whatever the order: a weight is a multiple of 2^-45 with the
+// largest in [1/2, 1), formed in fp32 pairs to about 2^-33 of itself, and all sums are of
+// 64-bit integers.
 //
 // A cluster of blocks holds a row in shared memory (read once); everything else is
 // passes over it and exchanges between the blocks. A list of the tokens that reach a
 // value, which enough of the threads' largest ones do, settles most rows: sorted, it
 // has the cut of top-k, and of top-p where the list weighs enough. Otherwise the cut is
-// looked for in counts of all tokens by the logarithm of the weight, 1,024 bins with the
-// sum of what the tokens lie below their bin's edge: these bound the running sum to a
-// part in 1,000, exact sums and a list of the tokens between the bounds do the rest (if
-// they are too many for a list, they are counted again, by smaller bins).
+// looked for in counts of all tokens by the logarithm of the weight, 1,024 bins of 1/32 of
+// its base-2 logarithm with the sum of what the tokens lie below their bin's edge: these
+// bound the running sum to a part in 10,000, so that one or two bins hold the cut, and a
+// pass that forms the exact sum of what lies before them and lists their tokens does the
+// rest (if they are too many for a list, they are counted again, by smaller bins).
+//
+// What bounds it: not memory (64 rows of 131,072 in bf16 are 2.5 us of reads), but the
+// instructions of the passes that form weights, about 30 a token and half of them on the
+// half-rate integer pipe, and for single rows the exchanges, each a microsecond. Measured
+// (64 x 131,072 bf16): temperature alone 21.6 us, min-p 22.7, top-k 24.8, top-p 61.8 (two
+// passes that form weights and one that counts in shared memory), a mix of them 60.0;
+// 256 x 32,000 mixed 49; 1 x 131,072 12.3 / 14.7 / 26.8 (temperature, top-k, top-p).
 #include <algorithm>
 #include <cmath>
 #include <cuda_bf16.h>
@@ -71,17 +79,16 @@ struct SampleParams {
   float* logprobs;      // or nullptr
   long long stride;
   int vocab, rows, slice;   // slice: tokens of a block
-  int lg;                   // log2 of vocab, rounded up
 };
 
 struct SampleShared {
   float2 tab[512];
-  unsigned long long sort[2][kSmList];
+  unsigned long long sort[2][kSmList];            // (or two lists of candidates at once)
   // what the blocks exchange, in two sets: a block may be one exchange ahead
   uint32_t hist[2][kSmBins], below[2][kSmBins];   // tokens of a bin; the sum of what they lie below its edge
   unsigned long long list[2][kSmList];            // this block's candidates: (key of x, ~index)
   unsigned long long sum[2];
-  uint32_t cnt[2], fill[2];
+  uint32_t cnt[2], fill[2], fill_two[2];
   float top[2], low[2];
   // scratch of the block
   unsigned long long warp_sum[kSmWarps], cand_sum[kSmWarps];
@@ -495,10 +502,10 @@ struct Sampler {
     }
   }
 
-  // All blocks' candidates (of the exchange of parity ph): one a thread, 0 where there is
-  // none; returns how many there are (more than kSmList: not all of them).
-  __device__ __forceinline__ uint32_t collect(uint32_t ph, unsigned long long* mine) {
-    const uint32_t m = static_cast<uint32_t>(lane) < blocks ? peer_load(&sh.fill[ph], lane) : 0u;
+  // All blocks' candidates of a list: one a thread, 0 where there is none; returns how many
+  // there are (more than kSmList: not all of them).
+  __device__ __forceinline__ uint32_t collect(const unsigned long long* list, const uint32_t* fill, unsigned long long* mine) {
+    const uint32_t m = static_cast<uint32_t>(lane) < blocks ? peer_load(fill, lane) : 0u;
     uint32_t end = m;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -517,17 +524,18 @@ struct Sampler {
         first = e;
       }
     }
-    if (threadIdx.x < n) *mine = peer_load(&sh.list[ph][threadIdx.x - first], r);
+    if (threadIdx.x < n) *mine = peer_load(list + (threadIdx.x - first), r);
     return n;
   }
-  __device__ __forceinline__ void offer(uint32_t ph, float x, int idx) {
-    const uint32_t at = atomicAdd(&sh.fill[ph], 1u);
-    if (at < kSmList) sh.list[ph][at] = static_cast<unsigned long long>(float_key(x)) << 32 | static_cast<uint32_t>(~idx);
+  __device__ __forceinline__ static void offer(unsigned long long* list, uint32_t* fill, float x, int idx) {
+    const uint32_t at = atomicAdd(fill, 1u);
+    if (at < kSmList) list[at] = static_cast<unsigned long long>(float_key(x)) << 32 | static_cast<uint32_t>(~idx);
   }
+  __device__ __forceinline__ void offer(uint32_t ph, float x, int idx) { offer(sh.list[ph], &sh.fill[ph], x, idx); }
   // Sorts the threads' first n candidates, the largest first: 32 by a bitonic sort within
   // a warp, then runs of 32, 64 .. merged: a candidate's place is its own in its run and
-  // that of as many of the other's as are larger, by bisection. (A bitonic sort of 1,024
-  // across the block takes 8.5 us, this 2.) Only the warps that have some take part.
+  // that of as many of the other's as are larger, by bisection. (Of 600 candidates: 5.4 us,
+  // a bitonic sort across the block 8.5.) Only the warps that have some take part.
   __device__ __forceinline__ unsigned long long sorted(unsigned long long v, uint32_t n) {
     uint32_t size = 32;
     while (size < n) size <<= 1;
@@ -566,14 +574,14 @@ struct Sampler {
   __device__ __forceinline__ static float value_of(unsigned long long c) { return key_float(static_cast<uint32_t>(c >> 32)); }
   __device__ __forceinline__ static int index_of(unsigned long long c) { return static_cast<int>(~static_cast<uint32_t>(c)); }
 
-  // The cut among the candidates of the list of parity ph, which `above` tokens of weight
-  // `sum` rank before: the need-th token of the ranking, or the one with which the running
-  // sum reaches `need`. Whether it is there; *upto: the sum of weights up to it.
+  // The cut among the candidates of a list (`all` in number, this thread's in cand), which
+  // `above` tokens of weight `sum` rank before: the need-th token of the ranking, or the one
+  // with which the running sum reaches `need`. Whether it is there; *upto: the sum of
+  // weights up to it.
   template <bool SUM>
-  __device__ __forceinline__ bool settle(uint32_t ph, unsigned long long sum, uint32_t above, unsigned long long need, float* cx,
+  __device__ __forceinline__ bool settle(uint32_t all, unsigned long long sum, uint32_t above, unsigned long long need, float* cx,
                                          int* ci, unsigned long long* upto) {
     if (threadIdx.x == 0) sh.at_index = -1;
-    const uint32_t all = collect(ph, &cand);
     cand = sorted(cand, min(all, static_cast<uint32_t>(kSmList)));
     const bool in = threadIdx.x < all && all <= kSmList;
     const unsigned long long own = in ? weight_of(sc, sh.tab, value_of(cand)) : 0ull;
@@ -614,11 +622,55 @@ struct Sampler {
       if (b.point <= p0 && b.point >= p1) offer(ph, x1, idx + 1);
     });
     const Sums s = exchange(sum.value(), 0);
-    if (!settle<SUM>(ph, s.sum, above, need, cx, ci, upto)) return false;
+    const uint32_t all = collect(sh.list[ph], &sh.fill[ph], &cand);
+    if (!settle<SUM>(all, s.sum, above, need, cx, ci, upto)) return false;
     list_above = sum.value();
     list_sums = s;
-    list_top = b0 > 0 ? __fsub_rd(sc.top, __fmul_ru(static_cast<float>(kBinPoints * b0 + 1), 1.0f / (512.0f * sc.ch))) : INFINITY;
+    list_top = below_bin(b0);
     return true;
+  }
+  // The token with which the running sum reaches `need`, in bin b0 or in bins b0 + 1 .. b1
+  // (kSmList tokens at most each): a list of either in one pass, and only the one that the
+  // sums say is sorted.
+  __device__ __forceinline__ bool cut_either(int b0, int b1, unsigned long long need, float* cx, int* ci, unsigned long long* upto) {
+    const int p0 = sc.base - kBinPoints * b0, mid = p0 - kBinPoints, p1 = sc.base - kBinPoints * (b1 + 1) + 1;
+    if (threadIdx.x < 2) sh.fill_two[threadIdx.x] = 0;
+    __syncthreads();
+    WeightSum sum;
+    unsigned long long first = 0;                 // what bin b0 weighs
+    row.pairs(row.first, row.count, [&](float x0, float x1, int idx) {
+      if (!__any_sync(0xffffffffu, point_of(sc, fmaxf(x0, x1)) >= p1)) return;
+      const auto over = [&](int point) { return point > mid; };
+      const Weight a = weight_if(sc, sh.tab, x0, over), b = weight_if(sc, sh.tab, x1, over);
+      sum.add(a, b);
+      const auto take = [&](const Weight& w, float x, int i) {
+        if (w.point > p0 || w.point < p1) return;
+        const bool second = w.point <= mid;
+        offer(sh.sort[second], &sh.fill_two[second], x, i);
+        if (!second) first += w.value();
+      };
+      take(a, x0, idx);
+      take(b, x1, idx + 1);
+    });
+    const Sums in = exchange(first, 0);
+    Sums s = exchange(sum.value(), 0);            // of bin b0 and what lies before
+    const bool second = need > s.sum;
+    list_above = sum.value();
+    if (!second) {
+      list_above -= first;
+      s.sum -= in.sum;
+      s.sum_before -= in.sum_before;
+    }
+    const uint32_t all = collect(sh.sort[second], &sh.fill_two[second], &cand);
+    blocks_sync(blocks);                          // (what is sorted overwrites the lists)
+    if (!settle<true>(all, s.sum, 0, need, cx, ci, upto)) return false;
+    list_sums = s;
+    list_top = below_bin(b0 + second);
+    return true;
+  }
+  // A value that all tokens before bin b exceed.
+  __device__ __forceinline__ float below_bin(int b) const {
+    return b > 0 ? __fsub_rd(sc.top, __fmul_ru(static_cast<float>(kBinPoints * b + 1), 1.0f / (512.0f * sc.ch))) : INFINITY;
   }
 
   // The cut: the last of the first `need` tokens of the ranking, or the token with which
@@ -673,7 +725,8 @@ struct Sampler {
       }
       if (few) {
         unsigned long long sum;
-        if (settle<SUM>(ph, s.sum, s.cnt, need, cx, ci, &sum)) {
+        const uint32_t all = collect(sh.list[ph], &sh.fill[ph], &cand);
+        if (settle<SUM>(all, s.sum, s.cnt, need, cx, ci, &sum)) {
           list_above = above.value();
           list_sums = s;
           list_top = hi;
@@ -933,7 +986,7 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
         if (x[e] >= low && x[e] > -INFINITY) s.offer(lp, x[e], idx + e);
     });
     total = s.exchange(sum.value(), 0).sum;
-    const uint32_t n = s.collect(lp, &s.cand);
+    const uint32_t n = s.collect(sh.list[lp], &sh.fill[lp], &s.cand);
     bool fits = n <= kSmList;
     if (greedy && fits) {
       if (threadIdx.x == 0) sh.at_index = 0x7fffffff;
@@ -1038,12 +1091,12 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       s.find_bounds(n * w(edge - m - 0.02f), n * (w0 + (m + 0.68f) * (1.0f / (kBinPoints + 0.4f)) * (w1 - w0)), static_cast<float>(need));
       const int b0 = sh.lo_bin, b1 = sh.hi_bin;
       __syncthreads();
-      // both bins at once where a list holds them, else one after the other
+      // one list of these bins, or (they are two, seldom more) one of the first and one of the rest
       bool found = false;
-      if (b1 < kSmBins - 1 && b1 - b0 < 4) {
-        const bool all = s.held(n, b0, b1) <= kSmList;
-        for (int b = b0; b <= b1 && !found; b = all ? b1 + 1 : b + 1)
-          if (all || s.held(n, b, b) <= kSmList) found = s.template cut_bins<true>(b, all ? b1 : b, 0, need, &cx, &ci, &total);
+      if (b1 < kSmBins - 1) {
+        const uint32_t all = s.held(n, b0, b1), one = s.held(n, b0, b0);
+        if (all <= kSmList) found = s.template cut_bins<true>(b0, b1, 0, need, &cx, &ci, &total);
+        else if (one <= kSmList && all - one <= kSmList) found = s.cut_either(b0, b1, need, &cx, &ci, &total);
       }
       if (!found) {
         const bool few = range(b0, b1, &lo, &hi);
@@ -1122,12 +1175,14 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
 template <int TYPE>
 cudaError_t launch_sample(SampleParams p, int sms, cudaStream_t st) {
   constexpr int kBytes = TYPE == DSA_FP32 ? 4 : 2;
-  // Blocks of a row: as few as hold it, and more where SMs would be idle and a block
-  // would still have 4,096 tokens.
+  // Blocks of a row: as few as hold it, and more where SMs would be idle (all but an eighth:
+  // clusters do not fill every corner of the chip) and a block would still have 4,096
+  // tokens. (One row of 131,072, top-p: 47 / 33 / 28 / 32 us with 2 / 4 / 8 / 16; of 5,000,
+  // 17 / 17 / 17 / 19 / 25 with 1 to 16; 37 of 50,257 37 / 40 / 67 with 2 / 4 / 8.)
   int blocks = 1;
   const auto slice_of = [&](int n) { return ((p.vocab + n - 1) / n + 63) / 64 * 64; };
   while (blocks < kSmMaxCluster && slice_of(blocks) * kBytes > kSmMaxData) blocks *= 2;
-  while (blocks < 8 && 2LL * p.rows * blocks <= sms && slice_of(2 * blocks) >= 4096) blocks *= 2;
+  while (blocks < 8 && 16LL * p.rows * blocks <= 7LL * sms && slice_of(2 * blocks) >= 4096) blocks *= 2;
   p.slice = slice_of(blocks);
   const size_t smem = ((sizeof(SampleShared) + 15) & ~size_t{15}) + static_cast<size_t>(p.slice) * kBytes + 16 + 512;
   const void* fn = reinterpret_cast<const void*>(&sample_kernel<TYPE>);
@@ -1190,7 +1245,6 @@ extern "C" int dsa_sample(const dsa_sample_problem* sp, const void* logits, cons
   if (int rc = current_device(&sms)) return rc;
   p.logits = logits, p.u = uniform, p.heat = temperature, p.top_k = top_k, p.top_p = top_p, p.min_p = min_p;
   p.tokens = tokens, p.logprobs = logprobs, p.vocab = sp->vocab, p.rows = sp->rows;
-  while ((1 << p.lg) < sp->vocab) ++p.lg;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = sp->logits_dtype == DSA_FP32   ? launch_sample<DSA_FP32>(p, sms, st)
                         : sp->logits_dtype == DSA_FP16 ? launch_sample<DSA_FP16>(p, sms, st)
