@@ -759,8 +759,8 @@ int dsa_slot_map(int rows, int64_t tokens, const dsa_kv_pages* pages, int32_t ca
  * queries go to q_out; the keys, rounded to q_dtype, and the values go to row
  * slots[n] of the caches, converted or quantised as dsa_cache_append does it
  * (INT8: absmax / 127 per token and head). A token whose slot is negative, or
- * cache_rows or above, changes no cache; its queries are still turned. Of two
- * tokens of the same slot either may be the one that is kept.
+ * cache_rows or above, changes no cache; its queries are still turned. No two
+ * tokens may have the same slot (of a row that has two, parts of both are kept).
  *
  *   tokens        N >= 0 (0: nothing is launched)
  *   num_q_heads, num_kv_heads   >= 0, not both 0

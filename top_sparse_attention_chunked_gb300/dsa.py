@@ -872,7 +872,11 @@ def _token_rows(dev: int, t, name: str, dtype, tokens: int, heads: int):
     if not ok:
         raise ValueError(f"{name} must be [{tokens}, {heads * 128}] or [{tokens}, {heads}, 128], each token's vectors "
                          f"contiguous, got {tuple(shape)} with strides {st}")
-    return t.data_ptr(), st[0] if tokens > 1 and heads else 0
+    if tokens <= 1 or heads == 0:
+        return t.data_ptr(), 0
+    if st[0] == 0:                     # (0 would say that the tokens lie together)
+        raise ValueError(f"{name}'s tokens are one and the same (stride 0)")
+    return t.data_ptr(), st[0]
 
 
 def dsa_rope_axes_append(p: DsaAxesProblem, q, k, v, gamma_q, gamma_k, cos, sin, positions, slots, q_out, k_cache, v_cache,
@@ -882,6 +886,7 @@ def dsa_rope_axes_append(p: DsaAxesProblem, q, k, v, gamma_q, gamma_k, cos, sin,
     slots [N]. q, k and v may be columns of one projection. positions [axes, N], or
     [N] where all axes have the same."""
     lib, dev, n, hkv = load_library(), _current_device(), p.tokens, p.num_kv_heads
+    p = DsaAxesProblem.from_buffer_copy(p)             # (the strides are this call's)
     qdt, kvdt, f32, i32 = _TORCH_DT[p.q_dtype], _TORCH_DT[p.kv_dtype], torch.float32, torch.int32
     qp, p.q_stride = _token_rows(dev, q, "q", qdt, n, p.num_q_heads)
     kp, p.k_stride = _token_rows(dev, k, "k", qdt, n, hkv)
@@ -921,10 +926,11 @@ def dsa_add_rmsnorm(p: DsaNormProblem, x, residual, gamma, h, y, scale=None, str
         if t.dtype is not _TORCH_DT[dt] or t.shape != shape or t.get_device() != dev:
             _refuse(dev, t, name, _TORCH_DT[dt], shape)
         st = t.stride()
-        if p.hidden > 1 and st[1] != 1:
-            raise ValueError(f"{name}'s rows must be contiguous, got strides {st}")
+        if (p.hidden > 1 and st[1] != 1) or (p.rows > 1 and st[0] == 0):   # (0 would say that the rows lie together)
+            raise ValueError(f"{name}'s rows must be contiguous and apart, got strides {st}")
         ptrs.append(t.data_ptr())
         strides.append(st[0] if p.rows > 1 else 0)
+    p = DsaNormProblem.from_buffer_copy(p)             # (the strides are this call's)
     p.x_stride, p.residual_stride, p.h_stride, p.y_stride = strides
     groups = -(-p.hidden // p.scale_group) if p.scale_group else 1
     g, s = _here(dev, (gamma, "gamma", torch.float32, (p.hidden,)), (scale, "scale", torch.float32, (p.rows, groups)))
