@@ -209,6 +209,32 @@ def test_text_positions_agree_with_the_fused_prologue(D):
         assert (a != b).double().mean() < 0.01
 
 
+@pytest.mark.parametrize("q", ["bf16", "fp16"])
+def test_codes_are_the_appends(D, q):
+    """Values and unturned keys as codes: dsa_cache_append's, bit for bit, at scales of every size."""
+    B, S, hkv = 1, 20000, 3
+    dt = torch.bfloat16 if q == "bf16" else torch.float16
+    g = torch.Generator(device="cuda").manual_seed(17)
+    k, v = (torch.randn(B, S, hkv, 128, device="cuda", generator=g) for _ in range(2))
+    low, high = (-130, 100) if q == "bf16" else (-20, 10)
+    v *= torch.exp2(torch.randint(low, high, (B, S, hkv, 1), device="cuda", generator=g).float())
+    k[:, ::5] = torch.randint(-200, 200, (B, S // 5, hkv, 128), device="cuda", generator=g).float() / 2     # many ties
+    v[:, 7] = 0
+    k, v = k.to(dt), v.to(dt)
+    new = lambda *s, t: torch.full(s, 9, device="cuda", dtype=t)
+    K, V, K2, V2 = (new(B, S, hkv, 128, t=torch.int8) for _ in range(4))
+    ks, vs, ks2, vs2 = (new(B, S, hkv, t=torch.float32) for _ in range(4))
+    p = D.make_problem(batch=B, q_len=S, total_len=[S], top_k=8, num_q_heads=hkv, num_kv_heads=hkv, cache_capacity=S, q_dtype=q, kv_dtype="int8")
+    D.dsa_cache_append(p, new(B, S, 64, t=torch.bfloat16), k, v, new(B, S, 64, t=torch.bfloat16), K, V, ks, vs)
+    p2 = D.make_rope_axes_problem(S, 0, hkv, S, [64], 4, q_dtype=q, kv_dtype="int8")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    D.dsa_rope_axes_append(p2, None, k.view(S, hkv, 128), v.view(S, hkv, 128), None, None, torch.ones(4, 64, device="cuda"),
+                           torch.zeros(4, 64, device="cuda"), torch.zeros(S, **i32), torch.arange(S, **i32), None, K2.view(S, hkv, 128),
+                           V2.view(S, hkv, 128), ks2.view(S, hkv), vs2.view(S, hkv))
+    assert torch.equal(vs, vs2) and torch.equal(ks, ks2)
+    assert torch.equal(V, V2) and torch.equal(K, K2)
+
+
 def test_captured_and_replayed_on_new_inputs(D):
     c, c2 = make(64, 8, 2, (16, 24, 24), seed=1), make(64, 8, 2, (16, 24, 24), seed=2)
     want = call(D, c2, "fp16", False, 1e-6)

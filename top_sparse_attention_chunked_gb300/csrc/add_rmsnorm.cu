@@ -6,6 +6,14 @@
 //
 // A row stays in registers from its load to its store, so every byte passes
 // once; rows are spread over thread blocks, or over warps where they are short.
+// The mean needs the whole row before the first element can leave: the loads of one
+// block run under the arithmetic of the others on its SM.
+//
+// What bounds it: memory. 8,192 x 8,192 BF16, of the copy rate: BF16 out 83 us (96%), e4m3
+// with a scale a row 79 us (88%), a scale per 128 elements 83 us (84%; the maxima's
+// exchanges and the conversions keep the schedulers 72% busy); 4,096 x 4,096 25 us. Rows
+// that cannot be moved as vectors (4,000 x 4,001): 56 us, issue-bound. Small calls: a
+// launch and a row's way, 2.4 us for 8 x 5,120.
 #include <cmath>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -11,6 +11,11 @@
 // norm is a sum over eight lanes, and the angles, read once, serve all of the
 // vectors that the lanes go through. They are kept multiplied by gamma: with c, s the
 // angle's and g, h the partners' weights, y = (x g c - x' h s) / rms, y' = (x' h c + x g s) / rms.
+//
+// What bounds it: memory, and just below it the instructions of a vector (conversions,
+// squares, four products a pair). 8,192 tokens of 32 / 8 heads, BF16: 37 us, 81% of the
+// copy rate; 24 / 2 heads 24.2 us (74%); INT8 caches 41 us (68%). 16 tokens: 2.5 us, a
+// launch and three dependent loads (position, angle, gamma beside the vector).
 #include <algorithm>
 #include <cmath>
 #include <cuda_bf16.h>
@@ -23,7 +28,7 @@ namespace {
 
 constexpr int kRxPairs = DSA_HEAD_DIM / 2;
 constexpr int kRxLanes = 8;                       // lanes of a head vector
-constexpr int kRxThreads = 256;
+constexpr int kRxThreads = 128;
 constexpr int kRxBatch = 4;                       // vectors whose loads are in flight together
 
 struct AxesParams {
@@ -172,21 +177,31 @@ __device__ __forceinline__ void rx_append(const AxesParams& p, void* cache, floa
     top = max8(top);
     if (!live) return;
     const float scale = __fdiv_rn(top, 127.0f);
-    // rint(x / scale) from x times the reciprocal: both are within 2^-15 of the quotient, so
-    // they round alike but where it is that near a half; there, and for scales whose
-    // reciprocal may overflow, the quotient itself is rounded
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (scale != 0.f) {
-      const bool normal = scale >= 1.17549435e-38f;
-      const float by = normal ? __fdiv_rn(1.0f, scale) : 0.f;
+    // x / scale, correctly rounded, from the scale's reciprocal (Markstein, 1990: if y is 1 / b
+    // rounded to the nearest and q within a unit in the last place of a / b, then so is
+    // q + (a - b q) y rounded once; x y is within two, the first step within one). What
+    // 16-bit values hold is next to a half too often for a branch (one in 300: the largest
+    // value's half is 63.5). Scales whose remainders would be subnormal are divided by.
+    constexpr float kWhole = 12582912.0f;         // 1.5 * 2^23: adding it rounds, the low byte is the code
+    const bool large = scale >= 0x1p-90f;
+    const float by = large ? __fdiv_rn(1.0f, scale) : 0.f;
+    uint32_t c[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float q = x[e] * by;
-        float c = rintf(q);
-        if (!normal || fabsf(fabsf(q - c) - 0.5f) < 0x1p-12f) c = fminf(fmaxf(rintf(__fdiv_rn(x[e], scale)), -127.0f), 127.0f);
-        w[e >> 2] |= (static_cast<uint32_t>(static_cast<int>(c)) & 0xffu) << (8 * (e & 3));
-      }
+    for (int e = 0; e < 16; ++e) {
+      float q = __fmul_rn(x[e], by);
+      q = __fmaf_rn(__fmaf_rn(-q, scale, x[e]), by, q);
+      q = __fmaf_rn(__fmaf_rn(-q, scale, x[e]), by, q);
+      c[e] = __float_as_uint(__fadd_rn(q, kWhole));
     }
+    if (!large && scale != 0.f) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        c[e] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fdiv_rn(x[e], scale), -127.0f), 127.0f), kWhole));
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
     uint8_t* d = static_cast<uint8_t*>(cache) + to * DSA_HEAD_DIM;
     if constexpr (VEC) {
       const LaneAt at(l, p.half);
@@ -267,7 +282,7 @@ __device__ __forceinline__ void rx_angles(const AxesParams& p, int l, long long 
 // A unit is a run of up to per_unit vectors of one token: of its queries, keys or
 // values. Eight lanes take one; a thread block's are all of the same kind.
 template <bool VEC, bool F16>
-__global__ void __launch_bounds__(kRxThreads, 2) rope_axes_append_kernel(const __grid_constant__ AxesParams p) {
+__global__ void __launch_bounds__(kRxThreads, 4) rope_axes_append_kernel(const __grid_constant__ AxesParams p) {
   const int l = threadIdx.x & (kRxLanes - 1);
   const int block = blockIdx.x;
   const int kind = block < p.q_blocks ? 0 : block < p.q_blocks + p.kv_blocks ? 1 : 2;   // q, k, v
@@ -476,11 +491,12 @@ extern "C" int dsa_rope_axes_append(const dsa_axes_problem* ap, const void* q, c
     p.axis[i / 8] |= static_cast<uint16_t>(axis[i] << (2 * (i % 8)));
   }
   p.whole8 = whole8;
-  // A unit's vectors share their angles: as many (of 1, 2 .. 32) as leave every SM some 40
-  // units, of the 64 that it takes at once. (8,192 tokens of 32 / 8 heads: units of 2, 4, 8,
-  // 16, 32 take 79, 55, 47, 42, 40 us.)
+  // A unit's vectors share their angles: as many (of 1, 2 .. 32) as leave every SM some 24
+  // units, of the 64 that it takes at once. (8,192 tokens of 32 / 8 heads: units of 4, 8, 16,
+  // 32 take 50, 41, 39, 37 us; 2,000: 16.6, 16.1, 14.3 with 4, 8, 16; 300 of 24 / 2 heads:
+  // 5.0, 6.6, 11.3 with 1, 8, 16.)
   p.per_unit = 32;
-  while (p.per_unit > 1 && N * ((std::max(hq, hkv) + p.per_unit - 1) / p.per_unit) < 40LL * sms) p.per_unit /= 2;
+  while (p.per_unit > 1 && N * ((std::max(hq, hkv) + p.per_unit - 1) / p.per_unit) < 24LL * sms) p.per_unit /= 2;
   p.q_units = (hq + p.per_unit - 1) / p.per_unit;
   p.kv_units = (hkv + p.per_unit - 1) / p.per_unit;
   constexpr int kUnits = kRxThreads / kRxLanes;
