@@ -25,9 +25,9 @@
 // What bounds it: not memory (64 rows of 131,072 in bf16 are 2.5 us of reads), but the
 // instructions of the passes that form weights, about 30 a token and half of them on the
 // half-rate integer pipe, and for single rows the exchanges, each a microsecond. Measured
-// (64 x 131,072 bf16): temperature alone 21.6 us, min-p 22.7, top-k 24.8, top-p 61.8 (two
-// passes that form weights and one that counts in shared memory), a mix of them 60.0;
-// 256 x 32,000 mixed 49; 1 x 131,072 12.3 / 14.7 / 26.8 (temperature, top-k, top-p).
+// (64 x 131,072 bf16): temperature alone 21.6 us, min-p 22.7, top-k 24.6, top-p 60.4 (two
+// passes that form weights and one that counts in shared memory), a mix of them 57.9;
+// 256 x 32,000 mixed 48; 1 x 131,072 12.3 / 14.7 / 26.6 (temperature, top-k, top-p).
 #include <algorithm>
 #include <cmath>
 #include <cuda_bf16.h>
@@ -139,7 +139,7 @@ constexpr float kInt = 12582912.0f;             // 1.5 * 2^23: to whole numbers
 constexpr float kHigh = 3.0f;                   // 1.5 * 2^1: to multiples of 2^-22
 constexpr float kLow = 0x1.8p-22f;              // 1.5 * 2^-22: to multiples of 2^-45
 constexpr int kGridSpan = 64;
-constexpr int kBinPoints = 16;                  // grid points of a bin
+constexpr int kBinShift = 4, kBinPoints = 1 << kBinShift;   // grid points of a bin
 constexpr int kZero = 60 * 512;                 // weights from 2^-60 of the largest down are none at all
 // x -> log2 of the weight, in units of 1 / 512 and a rest: (x - b) (ch + cl), ch + cl =
 // log2 e / T as a pair of floats. b is 0, or the largest x where that is too large to be a
@@ -247,6 +247,29 @@ struct Slice {
   __device__ __forceinline__ void pairs(int from, int n, F&& f) const {
 #pragma unroll 1
     for (int i = threadIdx.x & 31; i < n * (kVec / 2); i += 32) pair(from * (kVec / 2) + i, f);
+  }
+  // The same for every four, in the two passes of most nuclei (64 x 131,072 mixed: 58 and not 60 us).
+  template <class F>
+  __device__ __forceinline__ void quads(int from, int n, F&& f) const {
+#pragma unroll 1
+    for (int i = threadIdx.x & 31; i < n * (kVec / 4); i += 32) {
+      const int j = from * (kVec / 4) + i;
+      float x[4];
+      if constexpr (kF32) {
+        const float4 v = reinterpret_cast<const float4*>(img)[j];
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+      } else {
+        const uint2 w = reinterpret_cast<const uint2*>(img)[j];
+        if constexpr (TYPE == DSA_FP16) {
+          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+          x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+        } else {
+          x[0] = __uint_as_float(w.x << 16); x[1] = __uint_as_float(w.x & 0xffff0000u);
+          x[2] = __uint_as_float(w.y << 16); x[3] = __uint_as_float(w.y & 0xffff0000u);
+        }
+      }
+      f(x, index0 + 4 * j);
+    }
   }
   template <class F>
   __device__ __forceinline__ void pair(int i, F&& f) const {
@@ -364,7 +387,7 @@ struct Sampler {
   // edge a token lies, in 64ths of a point (and kBelow of them more, so that it is positive).
   static constexpr int kBelow = 40;
   __device__ __forceinline__ void count_weights(uint32_t* hist, uint32_t* below, const Weight& a, const Weight& b) {
-    const int g0 = sc.base - a.point, g1 = sc.base - b.point, b0 = g0 / kBinPoints, b1 = g1 / kBinPoints;   // (both >= 0)
+    const int g0 = sc.base - a.point, g1 = sc.base - b.point, b0 = g0 >> kBinShift, b1 = g1 >> kBinShift;   // (both >= 0)
     const auto under = [](int g, float r) {
       return static_cast<uint32_t>((g & (kBinPoints - 1)) * 64 + kBelow + __float_as_int(fmaf(r, -32768.0f, kInt)) - __float_as_int(kInt));
     };
@@ -613,13 +636,21 @@ struct Sampler {
     if (threadIdx.x == 0) sh.fill[ph] = 0;
     __syncthreads();
     WeightSum sum;
-    row.pairs(row.first, row.count, [&](float x0, float x1, int idx) {
-      if (!__any_sync(0xffffffffu, point_of(sc, fmaxf(x0, x1)) >= p1)) return;
+    const float low = below_bin(b1 + 1);          // (what lies in these bins does not lie below it)
+    row.quads(row.first, row.count, [&](const float (&x)[4], int idx) {
+      if (!__any_sync(0xffffffffu, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= low)) return;
       const auto over = [&](int point) { return point > p0; };
-      const Weight a = weight_if(sc, sh.tab, x0, over), b = weight_if(sc, sh.tab, x1, over);
+      const Weight a = weight_if(sc, sh.tab, x[0], over), b = weight_if(sc, sh.tab, x[1], over);
+      const Weight c = weight_if(sc, sh.tab, x[2], over), d = weight_if(sc, sh.tab, x[3], over);
       sum.add(a, b);
-      if (a.point <= p0 && a.point >= p1) offer(ph, x0, idx);
-      if (b.point <= p0 && b.point >= p1) offer(ph, x1, idx + 1);
+      sum.add(c, d);
+      const auto take = [&](const Weight& w, float x, int i) {
+        if (static_cast<uint32_t>(w.point - p1) <= static_cast<uint32_t>(p0 - p1)) offer(ph, x, i);
+      };
+      take(a, x[0], idx);
+      take(b, x[1], idx + 1);
+      take(c, x[2], idx + 2);
+      take(d, x[3], idx + 3);
     });
     const Sums s = exchange(sum.value(), 0);
     const uint32_t all = collect(sh.list[ph], &sh.fill[ph], &cand);
@@ -634,23 +665,28 @@ struct Sampler {
   // sums say is sorted.
   __device__ __forceinline__ bool cut_either(int b0, int b1, unsigned long long need, float* cx, int* ci, unsigned long long* upto) {
     const int p0 = sc.base - kBinPoints * b0, mid = p0 - kBinPoints, p1 = sc.base - kBinPoints * (b1 + 1) + 1;
+    const float low = below_bin(b1 + 1);          // (what lies in these bins does not lie below it)
     if (threadIdx.x < 2) sh.fill_two[threadIdx.x] = 0;
     __syncthreads();
     WeightSum sum;
     unsigned long long first = 0;                 // what bin b0 weighs
-    row.pairs(row.first, row.count, [&](float x0, float x1, int idx) {
-      if (!__any_sync(0xffffffffu, point_of(sc, fmaxf(x0, x1)) >= p1)) return;
+    row.quads(row.first, row.count, [&](const float (&x)[4], int idx) {
+      if (!__any_sync(0xffffffffu, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= low)) return;
       const auto over = [&](int point) { return point > mid; };
-      const Weight a = weight_if(sc, sh.tab, x0, over), b = weight_if(sc, sh.tab, x1, over);
+      const Weight a = weight_if(sc, sh.tab, x[0], over), b = weight_if(sc, sh.tab, x[1], over);
+      const Weight c = weight_if(sc, sh.tab, x[2], over), d = weight_if(sc, sh.tab, x[3], over);
       sum.add(a, b);
+      sum.add(c, d);
       const auto take = [&](const Weight& w, float x, int i) {
-        if (w.point > p0 || w.point < p1) return;
+        if (static_cast<uint32_t>(w.point - p1) > static_cast<uint32_t>(p0 - p1)) return;
         const bool second = w.point <= mid;
         offer(sh.sort[second], &sh.fill_two[second], x, i);
         if (!second) first += w.value();
       };
-      take(a, x0, idx);
-      take(b, x1, idx + 1);
+      take(a, x[0], idx);
+      take(b, x[1], idx + 1);
+      take(c, x[2], idx + 2);
+      take(d, x[3], idx + 3);
     });
     const Sums in = exchange(first, 0);
     Sums s = exchange(sum.value(), 0);            // of bin b0 and what lies before
@@ -970,11 +1006,14 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     counted = list_p && !greedy;
     WeightSum sum;
     if (counted)
-      s.row.pairs(s.row.first, s.row.count, [&](float x0, float x1, int) {
+      s.row.quads(s.row.first, s.row.count, [&](const float (&x)[4], int) {
         const auto all = [](int) { return true; };
-        const Weight a = weight_if(sc, sh.tab, x0, all), b = weight_if(sc, sh.tab, x1, all);
+        const Weight a = weight_if(sc, sh.tab, x[0], all), b = weight_if(sc, sh.tab, x[1], all);
+        const Weight c = weight_if(sc, sh.tab, x[2], all), d = weight_if(sc, sh.tab, x[3], all);
         sum.add(a, b);
+        sum.add(c, d);
         s.count_weights(sh.hist[lp], sh.below[lp], a, b);
+        s.count_weights(sh.hist[lp], sh.below[lp], c, d);
       });
     s.row.each([&](const float (&x)[kVec], int idx) {
       float most = x[0];
