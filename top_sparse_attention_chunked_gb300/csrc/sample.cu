@@ -32,6 +32,7 @@
 #include <cmath>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <mutex>
 
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
@@ -1211,36 +1212,65 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   blocks_left(blocks);
 }
 
+constexpr size_t sample_smem(size_t data) { return ((sizeof(SampleShared) + 15) & ~size_t{15}) + data + 16 + 512; }
+static_assert(sample_smem(kSmMaxData) <= 232448, "");
+
+struct SampleConfig {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  SampleConfig(int rows, int blocks, size_t data, cudaStream_t st) {
+    cfg.gridDim = dim3(static_cast<unsigned>(rows) * blocks);
+    cfg.blockDim = dim3(kSmThreads);
+    cfg.dynamicSmemBytes = sample_smem(data);
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+};
+
+// Clusters of `blocks` (8 at most) that the current device holds at once: not as many as
+// its SMs would be enough for, since a cluster lies within one of their groups. (A block
+// takes an SM, whatever the shared memory.)
 template <int TYPE>
-cudaError_t launch_sample(SampleParams p, int sms, cudaStream_t st) {
+int sample_clusters(int blocks) {
+  static std::mutex mu;
+  static int cached[64][9] = {};                  // and 1; 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (cached[dev][blocks]) return cached[dev][blocks] - 1;
+  const SampleConfig c(1, blocks, kSmMaxData, nullptr);
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, sample_kernel<TYPE>, &c.cfg) != cudaSuccess) n = 0;
+  cudaGetLastError();
+  cached[dev][blocks] = n + 1;
+  return n;
+}
+
+template <int TYPE>
+cudaError_t launch_sample(SampleParams p, cudaStream_t st) {
   constexpr int kBytes = TYPE == DSA_FP32 ? 4 : 2;
-  // Blocks of a row: as few as hold it, and more where SMs would be idle (all but an eighth:
-  // clusters do not fill every corner of the chip) and a block would still have 4,096
-  // tokens. (One row of 131,072, top-p: 47 / 33 / 28 / 32 us with 2 / 4 / 8 / 16; of 5,000,
-  // 17 / 17 / 17 / 19 / 25 with 1 to 16; 37 of 50,257 37 / 40 / 67 with 2 / 4 / 8.)
+  // (the largest size whatever the call's: another thread may be between this and its launch)
+  const void* fn = reinterpret_cast<const void*>(&sample_kernel<TYPE>);
+  cudaError_t e = set_max_smem(fn, static_cast<int>(sample_smem(kSmMaxData)));
+  if (e != cudaSuccess) return e;
+  // Blocks of a row: as few as hold it, and up to 8 while the rows' clusters all fit on the
+  // chip at once and a block has 6,500 tokens. (Top-p: one row of 128,000 52 / 42 / 37 / 33 /
+  // 32 us with 2, 3, 4, 6, 8; 32,000 in top-k 13.2 / 12.8 / 13.7 with 1, 4, 7; 37 of 50,257
+  // 46 / 36 / 32 and, in turns, 40 / 66 with 1, 2, 3 and 4, 8; 20 of 131,072 57 / 41 / 38 and
+  // 59 with 2, 4, 6 and 7.)
   int blocks = 1;
   const auto slice_of = [&](int n) { return ((p.vocab + n - 1) / n + 63) / 64 * 64; };
-  while (blocks < kSmMaxCluster && slice_of(blocks) * kBytes > kSmMaxData) blocks *= 2;
-  while (blocks < 8 && 16LL * p.rows * blocks <= 7LL * sms && slice_of(2 * blocks) >= 4096) blocks *= 2;
+  while (blocks < kSmMaxCluster && slice_of(blocks) * kBytes > kSmMaxData) ++blocks;
+  while (blocks < 8 && slice_of(blocks + 1) >= 6500 && p.rows <= sample_clusters<TYPE>(blocks + 1)) ++blocks;
   p.slice = slice_of(blocks);
-  const size_t smem = ((sizeof(SampleShared) + 15) & ~size_t{15}) + static_cast<size_t>(p.slice) * kBytes + 16 + 512;
-  const void* fn = reinterpret_cast<const void*>(&sample_kernel<TYPE>);
-  cudaError_t e = set_max_smem(fn, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
   if (blocks > 8 && (e = set_nonportable_cluster(fn)) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.rows) * blocks);
-  cfg.blockDim = dim3(kSmThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = blocks;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, sample_kernel<TYPE>, p, blocks);
+  const SampleConfig c(p.rows, blocks, static_cast<size_t>(p.slice) * kBytes, st);
+  e = cudaLaunchKernelEx(&c.cfg, sample_kernel<TYPE>, p, blocks);
   if (e == cudaSuccess) note_launch("sample_kernel");
   return e;
 }
@@ -1285,9 +1315,9 @@ extern "C" int dsa_sample(const dsa_sample_problem* sp, const void* logits, cons
   p.logits = logits, p.u = uniform, p.heat = temperature, p.top_k = top_k, p.top_p = top_p, p.min_p = min_p;
   p.tokens = tokens, p.logprobs = logprobs, p.vocab = sp->vocab, p.rows = sp->rows;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = sp->logits_dtype == DSA_FP32   ? launch_sample<DSA_FP32>(p, sms, st)
-                        : sp->logits_dtype == DSA_FP16 ? launch_sample<DSA_FP16>(p, sms, st)
-                                                       : launch_sample<DSA_BF16>(p, sms, st);
+  const cudaError_t e = sp->logits_dtype == DSA_FP32   ? launch_sample<DSA_FP32>(p, st)
+                        : sp->logits_dtype == DSA_FP16 ? launch_sample<DSA_FP16>(p, st)
+                                                       : launch_sample<DSA_BF16>(p, st);
   if (e != cudaSuccess) return report_errorf(DSA_ERR_CUDA, "sample launch: %s", cudaGetErrorString(e));
   return DSA_OK;
 }
