@@ -678,12 +678,14 @@ def dsa_full_attn(p: DsaFullProblem, q, k, v, k_scale, v_scale, out, workspace, 
     rows = _cache_shapes(p, pages) + (Hkv,)
     cache, f32 = rows + (128,), torch.float32
     need = sum(p.q_len[:p.batch])
-    if q.dim() != 3 or q.shape[1:] != (Hq, 128) or q.shape[0] < need:
-        raise ValueError(f"q must be [N, {Hq}, 128] with N >= {need}, got {tuple(q.shape)}")
-    if out.dim() != 3 or out.shape[1:] != (Hq, 128) or out.shape[0] < need:
-        raise ValueError(f"out must be [N, {Hq}, 128] with N >= {need}, got {tuple(out.shape)}")
-    if lse is not None and (lse.dim() != 2 or lse.shape[1] != Hq or lse.shape[0] < need):
-        raise ValueError(f"lse must be [N, {Hq}] with N >= {need}, got {tuple(lse.shape)}")
+    for t, name in ((q, "q"), (out, "out")):
+        n = t.shape
+        if len(n) != 3 or n[1] != Hq or n[2] != 128 or n[0] < need:
+            raise ValueError(f"{name} must be [N, {Hq}, 128] with N >= {need}, got {tuple(n)}")
+    if lse is not None:
+        n = lse.shape
+        if len(n) != 2 or n[1] != Hq or n[0] < need:
+            raise ValueError(f"lse must be [N, {Hq}] with N >= {need}, got {tuple(n)}")
     args = _here(dev, (q, "q", _TORCH_DT[p.q_dtype], None), (k, "k", kvdt, cache), (v, "v", kvdt, cache),
                  (k_scale, "k_scale", f32, rows), (v_scale, "v_scale", f32, rows), (slopes, "slopes", f32, (Hq,)),
                  (out, "out", _TORCH_DT[p.out_dtype], None), (lse, "lse", f32, None),
@@ -896,7 +898,7 @@ def dsa_rope_axes_append(p: DsaAxesProblem, q, k, v, gamma_q, gamma_k, cos, sin,
         p.pos_stride, shape = 0, (n,)
     else:
         p.pos_stride, shape = n, (p.axes, n)
-    half = sum(p.sections)             # (those behind the last axis are 0)
+    half = sum(p.sections[:])          # (those behind the last axis are 0)
     cache, angles, cdt = (p.cache_rows, hkv, 128), (p.max_pos, half), _TORCH_DT[p.cos_dtype]
     a = _here(dev, (gamma_q, "gamma_q", f32, (128,)), (gamma_k, "gamma_k", f32, (128,)), (cos, "cos", cdt, angles),
               (sin, "sin", cdt, angles), (positions, "positions", i32, shape), (slots, "slots", i32, (n,)),
