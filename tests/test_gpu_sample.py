@@ -151,6 +151,22 @@ def test_cuts_among_many_tokens_of_like_weight(D, rows, vocab, dtype, std):
         run(D, x, uniform(rows, 9 + i), p=p, k=torch.where(torch.arange(rows) % 2 == 0, vocab, vocab // 3), low=1e-4)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("vocab,offset,step,heat", [(60000, 500.0, 2.0, 0.7), (233039, 0.0, 1.5, 1.0), (30000, -300.0, 4.0, 1.3), (90000, 8.0, 0.25, 0.2)])
+def test_cuts_next_to_the_border_of_a_heavy_value(D, dtype, vocab, offset, step, heat):
+    """A few values that thousands of tokens share, far apart, and cuts a little above and below where one's tokens end."""
+    g = torch.Generator().manual_seed(vocab)
+    x = ((torch.randn(vocab, generator=g) * 1.2).round() * step + offset).to(DT[dtype])
+    x[:: 10] = torch.finfo(DT[dtype]).min
+    v, n = x.double().unique(return_counts=True)
+    w = ((v - v[-1]) / heat).exp() * n
+    ends = (w.flip(0).cumsum(0) / w.sum())[1:5]
+    p = torch.tensor([float(e) + d for e in ends for d in (1e-3, 1e-4, 1.5e-5, 2e-6, 3e-7, -3e-7, -2e-6, -1.5e-5, -1e-4, -1e-3)]).clamp(max=0.99999)
+    x = x.expand(len(p), vocab).contiguous()
+    run(D, x, uniform(len(p), 3), heat=heat, p=p, least=0.3)
+    run(D, x, uniform(len(p), 4), heat=heat, p=p, k=vocab - 5, least=0.3)
+
+
 def test_rows_of_equal_logits(D):
     """Ties go to the lower index, in top-k, in top-p and with the cut inside a tie."""
     for vocab in (10, 1000, 70000, 300000):

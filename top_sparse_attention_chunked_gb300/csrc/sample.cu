@@ -710,22 +710,35 @@ struct Sampler {
     return b > 0 ? __fsub_rd(sc.top, __fmul_ru(static_cast<float>(kBinPoints * b + 1), 1.0f / (512.0f * sc.ch))) : INFINITY;
   }
 
+  // The bits of x in its own type, ordered as x is, and values from such: that value, and
+  // bounds of it that no other value of the type lies within.
+  static constexpr int kUnit = TYPE == DSA_FP32 ? 0 : TYPE == DSA_FP16 ? 13 : 16;
+  __device__ __forceinline__ static uint32_t unit_key(float x) { return float_key(x) >> kUnit; }
+  __device__ __forceinline__ static float unit_low(uint32_t k) { return key_float(k << kUnit); }
+  __device__ __forceinline__ static float unit_high(uint32_t k) { return key_float((k << kUnit) | ((1u << kUnit) - 1)); }
+  __device__ __forceinline__ static float unit_value(uint32_t k) { return (k << kUnit) & 0x80000000u ? unit_low(k) : unit_high(k); }
+
   // The cut: the last of the first `need` tokens of the ranking, or the token with which
   // the weights' running sum reaches `need`. Returns the sum of weights up to it.
   //
   // From [lo, hi], values that hold the cut (`few`: at most kSmList of them): exact counts
   // and sums of what lies above hi, and either the tokens themselves or counts of them in
-  // bins. The bins are of the bits of x, or, for sums while the weights' logarithms are
-  // kGridSpan grid points or more apart, of those: the bounds of the sums are as far apart
-  // as the weights within a bin, so every round leaves that part of what the range weighs.
+  // bins. The bins are of the bits of x (of those that its type has: with a value a bin, the
+  // sums are exact), or, for sums while the weights' logarithms are kGridSpan grid points or
+  // more apart, of those: the bounds of the sums are as far apart as the weights within a
+  // bin, so every round leaves that part of what the range weighs. Where the cut may still lie
+  // at either end (two heavy values with nothing between), the next round's exact sum is
+  // that of the upper half: every round leaves half of the bits' range or less.
   template <bool SUM>
   __device__ __forceinline__ unsigned long long cut(unsigned long long need, float lo, float hi, bool few, float* cx, int* ci) {
     listed = false;
-    // (four rounds from all values, seldom more. The bound is for what should not be.)
-    for (int round = 0; round < 20; ++round) {
-      const uint32_t klo = float_key(lo), khi = float_key(hi);
+    float next_lo = lo, next_hi = hi;             // of a probe: the range if its upper half holds the cut
+    bool probe = false;
+    // (four rounds from all values, seldom more: 32 halves of 32 bits, and a probe each, at most)
+    for (int round = 0; round < 80; ++round) {
+      const uint32_t klo = unit_key(lo), khi = unit_key(hi);
       const uint32_t ph = phase & 1;
-      if (lo == hi && !few) break;
+      if (klo == khi && !few && !probe) break;
       const int ghi = grid_of(sc, hi), span = ghi - grid_of(sc, lo);
       const bool by_grid = SUM && span >= kGridSpan && round < 10;
       int shift = 0;
@@ -750,11 +763,17 @@ struct Sampler {
         } else if (by_grid) {
           count(hist, in0 ? (ghi - grid_of(sc, x0)) >> shift : -1, in1 ? (ghi - grid_of(sc, x1)) >> shift : -1);
         } else {
-          count(hist, in0 ? static_cast<int>((khi - float_key(x0)) >> shift) : -1, in1 ? static_cast<int>((khi - float_key(x1)) >> shift) : -1);
+          count(hist, in0 ? static_cast<int>((khi - unit_key(x0)) >> shift) : -1, in1 ? static_cast<int>((khi - unit_key(x1)) >> shift) : -1);
         }
       });
       const Sums s = exchange(above.value(), n);
-      if (SUM ? s.sum >= need : s.cnt >= need) {   // (the range does not hold it: from all values)
+      if (SUM ? s.sum >= need : s.cnt >= need) {   // (the range does not hold it: the upper half, or from all values)
+        if (probe) {
+          probe = false;
+          lo = next_lo;
+          hi = next_hi;
+          continue;
+        }
         few = false;
         lo = -INFINITY;
         hi = sc.top;
@@ -775,6 +794,7 @@ struct Sampler {
         hi = sc.top;
         continue;
       }
+      probe = false;
       const uint32_t m = bins(hist);
       const uint32_t top_key = khi - (threadIdx.x << shift);   // of the thread's bin
       if constexpr (SUM) {
@@ -785,9 +805,9 @@ struct Sampler {
           const int g = ghi - (static_cast<int>(threadIdx.x) << shift), step = 1 << shift;
           find_bounds(m * w(g - step), m * w(g + 1), static_cast<float>(rest));
         } else if (shift == 0) {
-          find_sum(m, m ? weight_of(sc, sh.tab, key_float(top_key)) : 0ull, rest);
+          find_sum(m, m ? weight_of(sc, sh.tab, unit_value(top_key)) : 0ull, rest);
         } else {
-          const auto w = [&](uint32_t k) { return m ? static_cast<float>(weight_of(sc, sh.tab, key_float(k))) : 0.f; };
+          const auto w = [&](uint32_t k) { return m ? static_cast<float>(weight_of(sc, sh.tab, unit_value(k))) : 0.f; };
           find_bounds(m * w(max(klo, top_key - ((1u << shift) - 1))), m * w(top_key), static_cast<float>(rest));
         }
       } else {
@@ -804,13 +824,21 @@ struct Sampler {
         lo = fmaxf(lo, __fsub_rd(sc.top, __fmul_ru(static_cast<float>(-g1), inv)));
       } else {
         const uint32_t down = ((static_cast<uint32_t>(b1) + 1) << shift) - 1;
-        hi = key_float(khi - (static_cast<uint32_t>(b0) << shift));
-        lo = key_float(down >= khi - klo ? klo : khi - down);
+        if (b0 > 0) hi = unit_high(khi - (static_cast<uint32_t>(b0) << shift));
+        if (down < khi - klo) lo = unit_low(khi - down);
       }
       few = left <= kSmList;
+      const uint32_t k0 = unit_key(lo), k1 = unit_key(hi);
+      if (SUM && !few && k0 < k1 && k1 - k0 > (khi - klo) / 2) {
+        const uint32_t mid = k0 + (k1 - k0) / 2;
+        next_lo = unit_low(mid + 1);
+        next_hi = hi;
+        hi = unit_high(mid);
+        probe = true;
+      }
     }
     // more tokens of one value than a list holds: the first of them, in index order
-    const float v = lo;
+    const float v = unit_value(unit_key(lo));
     unsigned long long above = 0;
     uint32_t n = 0, ties = 0;
     row.pairs(row.first, row.count, [&](float x0, float x1, int) {
