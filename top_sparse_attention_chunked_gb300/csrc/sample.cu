@@ -1116,11 +1116,12 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     const uint32_t n = s.bins(sh.hist[ph2]);
     const float inv_c = 1.0f / sc.ch;
     // values that surely hold all of bins b0 .. b1 (two grid points more on either side), and
-    // whether a list holds these bins' tokens and their neighbours'
+    // whether a list holds these bins' tokens and their neighbours'. The last bin stands for all
+    // that weighs less than the others' tokens, down to nothing: it has no lower end.
     const auto range = [&](int b0, int b1, float* lo, float* hi) {
       const uint32_t left = s.held(n, b0 - 1, b1 + 1);
       *hi = b0 <= 0 ? top : fminf(top, __fsub_ru(top, __fmul_rd(static_cast<float>(kBinPoints * b0 - 2) * (1.0f / 512.0f), inv_c)));
-      *lo = __fsub_rd(top, __fmul_ru(static_cast<float>(kBinPoints * (b1 + 1) + 2) * (1.0f / 512.0f), inv_c));
+      *lo = b1 >= kSmBins - 1 ? -INFINITY : __fsub_rd(top, __fmul_ru(static_cast<float>(kBinPoints * (b1 + 1) + 2) * (1.0f / 512.0f), inv_c));
       return left <= kSmList && b1 + 1 < kSmBins - 1;
     };
     float lo, hi;
