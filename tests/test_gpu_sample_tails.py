@@ -6,10 +6,12 @@ the cut is where it belongs, and another token if it is not. Weights are right t
 the cut lies further from every border than all of that together."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_sample import D, DT  # noqa: F401 (D is a fixture)
+from tests.test_gpu_sample import D, DT, run, uniform  # noqa: F401 (D is a fixture)
+from tests.test_sampling_bounds_cpu import residual
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +46,19 @@ def test_cut_below_the_last_bin(D, dtype, heat, top, shared, many, third, few): 
         assert int(tok) == 0, f"the third value's first token is kept, token {int(tok)} came"
         want = math.log(w2 / (1 + many * w1 + math.ceil(last) * w2))
         assert abs(float(lp) - want) <= 2.0 ** -20 * abs(want) + 2.0 ** -28
+
+
+@pytest.mark.parametrize("heat", [0.005, 0.01, 0.72])
+def test_heavy_logit_far_beyond_its_grid_point(D, heat):  # noqa: F811
+    """The largest logit alone in its bin, and above the bin's edge by as much as fp32 steps leave it."""
+    most = 4096 * heat / 1.4426950408889634
+    x0 = np.random.default_rng(5).uniform(most * 0.5, most, 300000).astype(np.float32)
+    r = residual(x0, heat)
+    tops = torch.from_numpy(x0[np.argsort(-r)[:6]].copy())
+    assert r.max() > 0.626
+    g = torch.Generator().manual_seed(9)
+    z = (torch.randn(6, 60000, generator=g) * 0.8).clamp(max=3)
+    x = tops[:, None] + (z - 6) * heat
+    x[:, 777] = tops
+    for i, s in enumerate((dict(p=0.9), dict(p=0.3), dict(p=torch.linspace(0.02, 0.999, 6)), dict(k=20000, p=0.7), dict(k=50, p=0.9))):
+        run(D, x, uniform(6, i), heat=heat, **s)

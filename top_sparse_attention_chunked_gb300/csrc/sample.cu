@@ -142,6 +142,10 @@ constexpr float kLow = 0x1.8p-22f;              // 1.5 * 2^-22: to multiples of 
 constexpr int kGridSpan = 64;
 constexpr int kBinShift = 4, kBinPoints = 1 << kBinShift;   // grid points of a bin
 constexpr int kZero = 60 * 512;                 // weights from 2^-60 of the largest down are none at all
+// What an exponent has beyond its grid point, in points: half of one by the rounding; an eighth that
+// the product (x - b) ch is rounded by (of up to 4,096 + 80: half a unit in its last place is 2^-12);
+// and another that cl adds (4,176 x 2^-24). In all 0.753.
+constexpr float kRest = 0.76f;
 // x -> log2 of the weight, in units of 1 / 512 and a rest: (x - b) (ch + cl), ch + cl =
 // log2 e / T as a pair of floats. b is 0, or the largest x where that is too large to be a
 // multiple of 1 / 512 in fp32 (x - b then is exact for all that have a weight).
@@ -170,7 +174,7 @@ struct Weight {
   }
 };
 // (in(point): whether it counts, else 0.) 2^r - 1 = r ln 2 + (r ln 2)^2 / 2 + (r ln 2)^3 / 6
-// with |r| <= 2^-10: off by 2^-42.
+// with |r| <= kRest / 512: off by 2^-44.
 template <class F>
 __device__ __forceinline__ Weight weight_if(const Scale& s, const float2* tab, float x, F&& in) {
   const float d = __fadd_rn(x, -s.b), n = __fmul_rn(d, s.ch), c = fmaxf(n, s.floor);
@@ -385,8 +389,10 @@ struct Sampler {
     if (b1 >= 0 && b0 != b1) atomicAdd(hist + b1, 1u);
   }
   // The same by the weights: bins of kBinPoints grid points, and how far below its bin's
-  // edge a token lies, in 64ths of a point (and kBelow of them more, so that it is positive).
-  static constexpr int kBelow = 40;
+  // edge a token lies, in 64ths of a point (and kBelow of them more, so that it is positive: a sum
+  // of a bin that is not would wrap around, and its bounds with it).
+  static constexpr int kBelow = 50;
+  static_assert(kBelow >= 64 * kRest + 0.5f, "");
   __device__ __forceinline__ void count_weights(uint32_t* hist, uint32_t* below, const Weight& a, const Weight& b) {
     const int g0 = sc.base - a.point, g1 = sc.base - b.point, b0 = g0 >> kBinShift, b1 = g1 >> kBinShift;   // (both >= 0)
     const auto under = [](int g, float r) {
@@ -981,7 +987,7 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   sc.b = fabsf(top) * sc.ch < 4096.0f ? 0.f : top;
   const float d_top = top - sc.b, p_top = __fmul_rn(d_top, sc.ch), t_top = __fadd_rn(p_top, kGrid);
   sc.base = __float_as_int(t_top);
-  sc.rest = (p_top - (t_top - kGrid)) + fmaf(d_top, sc.cl, fmaf(d_top, sc.ch, -p_top));   // within 2^-10 of 0
+  sc.rest = (p_top - (t_top - kGrid)) + fmaf(d_top, sc.cl, fmaf(d_top, sc.ch, -p_top));   // within kRest / 512 of 0
   sc.floor = (t_top - kGrid) - 80.0f;
   sc.zero = sc.base - kZero;
   // (the largest's power is 2^-1: sums of 2^19 weights below 2^45 stay below 2^64)
@@ -1148,16 +1154,17 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       total = s.exchange(sum.value(), 0).sum;
     }
     if (by_p) {
-      // A bin's n tokens lie m grid points below its edge on average, each between -0.7 and
-      // 15.7 (a point's rounding is half of one, a sum's a 128th a token). 2^-x is convex:
+      // A bin's n tokens lie m grid points below its edge on average, each between -kRest and
+      // 15 + kRest (a sum's rounding is a 128th of a point a token). 2^-x is convex:
       // they weigh at least n times the weight at their mean, at most what the chord
       // between the ends gives.
       const unsigned long long need = share(total);
       const float m = n ? (static_cast<float>(s.bins(sh.below[ph2])) / static_cast<float>(n) - s.kBelow) * (1.0f / 64.0f) : 0.f;
       const float edge = -static_cast<float>(kBinPoints * static_cast<int>(threadIdx.x));
       const auto w = [&](float g) { return exp2f(g * (1.0f / 512.0f)) * s.unit(); };
-      const float w0 = w(edge + 0.7f), w1 = w(edge - (kBinPoints - 0.3f));
-      s.find_bounds(n * w(edge - m - 0.02f), n * (w0 + (m + 0.68f) * (1.0f / (kBinPoints + 0.4f)) * (w1 - w0)), static_cast<float>(need));
+      constexpr float kEnd = kBinPoints - 1 + kRest;
+      const float w0 = w(edge + kRest), w1 = w(edge - kEnd);
+      s.find_bounds(n * w(edge - m - 0.02f), n * (w0 + (m - 0.02f + kRest) * (1.0f / (kEnd + kRest)) * (w1 - w0)), static_cast<float>(need));
       const int b0 = sh.lo_bin, b1 = sh.hi_bin;
       __syncthreads();
       // one list of these bins, or (they are two, seldom more) one of the first and one of the rest
