@@ -434,12 +434,14 @@ struct Sampler {
     return before + own;
   }
 
-  // The bin in which a running count passes `need`.
-  __device__ __forceinline__ void find_count(uint32_t n, uint32_t need) {
+  // The bins in which a running count passes `need`, and `more`.
+  __device__ __forceinline__ void find_count(uint32_t n, uint32_t need, uint32_t more) {
     const uint32_t a = scan<uint32_t>(n, sh.warp_cnt);
-    if (a < need && need <= a + n) sh.lo_bin = sh.hi_bin = threadIdx.x;
+    if (a < need && need <= a + n) sh.lo_bin = threadIdx.x;
+    if (a < more && more <= a + n) sh.hi_bin = threadIdx.x;
     __syncthreads();
   }
+  __device__ __forceinline__ void find_count(uint32_t n, uint32_t need) { find_count(n, need, need); }
   // The bins in which a running sum may pass `need`: what the thread's bin holds weighs
   // between l0 and u0.
   __device__ __forceinline__ void find_bounds(float l0, float u0, float need) {
@@ -936,7 +938,7 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   const bool by_k = heat > 0.f && k > 0 && k < p.vocab, by_p = heat > 0.f && tp < 1.0f;
   const bool list_k = by_k && k <= kSmFewK, list_p = by_p && !by_k;
   sh.hist[0][threadIdx.x] = sh.hist[1][threadIdx.x] = sh.below[1][threadIdx.x] = 0;
-  if (threadIdx.x == 64) sh.lo_bin = -1;
+  if (threadIdx.x == 64) sh.lo_bin = sh.hi_bin = -1;
   cp_async_wait<0>();
   // the largest logit
   float own = -INFINITY;
@@ -949,27 +951,44 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   __syncthreads();
   top = warp_max(sh.warp_bound[s.lane]);
   // and a value that enough tokens reach for a list: the threads' largest ones, counted
-  // in bins 1 / 16 of log2 of the weight wide below the block's
-  float low = -INFINITY;
+  // in bins 1 / 16 of log2 of the weight wide below the block's. Enough is the block's share
+  // (low; infinity: it is short of it, as where it is masked), or all, where others are short.
+  const uint32_t enough = list_k ? k : kSmFewP;
+  const auto edge = [&](float t, int bin) { return __fsub_rd(t, __fmul_ru(static_cast<float>(bin) + 1.01f, 1.0f / (16.0f * sh.row_c.x))); };
+  float low = INFINITY;
   if (list_k || list_p) {
     const float ch = 16.0f * sh.row_c.x;
     const float b = fminf((top - own) * ch, static_cast<float>(kSmBins - 1));       // (NaN: no bin)
     if (b < kSmBins - 1) atomicAdd(&sh.hist[0][static_cast<int>(b)], 1u);
     __syncthreads();
-    const uint32_t want = ((list_k ? k : kSmFewP) + blocks - 1) / blocks;
-    s.find_count(sh.hist[0][threadIdx.x], want);
-    if (sh.lo_bin >= 0) low = __fsub_rd(top, __fmul_ru(static_cast<float>(sh.lo_bin) + 1.01f, 1.0f / ch));
+    s.find_count(sh.hist[0][threadIdx.x], (enough + blocks - 1) / blocks, enough);
+    if (sh.lo_bin >= 0) low = edge(top, sh.lo_bin);
   }
   const uint32_t ph = s.phase++ & 1;
   if (threadIdx.x == 0) {
     sh.top[ph] = top;
     sh.low[ph] = low;
+    sh.cnt[ph] = sh.hi_bin;                                       // (a word that this exchange has no other use for)
   }
   if (threadIdx.x == 32) sh.fill[1] = 0;
   blocks_sync(blocks);
   const bool peer = static_cast<uint32_t>(s.lane) < s.blocks;
-  top = warp_max(peer ? peer_load(&sh.top[ph], s.lane) : -INFINITY);
-  low = -warp_max(peer ? -peer_load(&sh.low[ph], s.lane) : -INFINITY);
+  const float top_there = peer ? peer_load(&sh.top[ph], s.lane) : -INFINITY;
+  top = warp_max(top_there);
+  if (list_k || list_p) {
+    low = peer ? peer_load(&sh.low[ph], s.lane) : INFINITY;
+    const uint32_t able = __popc(__ballot_sync(0xffffffffu, low < INFINITY));
+    low = -warp_max(-low);
+    // With blocks that are short of their share the others' are too few together: then what one of
+    // them has enough of by itself, where the list holds as many of each. (64 x 131,072 with half of
+    // every row masked, top-k 50 and top-p: 17 us, and 46 with all tokens offered to the list.)
+    if (able < s.blocks) {
+      const int bin = peer ? static_cast<int>(peer_load(&sh.cnt[ph], s.lane)) : -1;
+      const float alone = warp_max(bin >= 0 ? edge(top_there, bin) : -INFINITY);
+      low = able * enough <= kSmList && alone > -INFINITY ? alone : list_k ? INFINITY : low;
+    }
+    if (low == INFINITY) low = -INFINITY;                         // (no block has its share: all tokens)
+  }
 
   if (!(top > -INFINITY)) {                                       // nothing to take
     if (s.rank == 0 && threadIdx.x == 0) {
@@ -1055,6 +1074,8 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
 #pragma unroll
       for (int e = 1; e < kVec; ++e) most = fmaxf(most, x[e]);
       if (!(most >= low) || most == -INFINITY) return;
+      // (all tokens: once they are too many for the list, no more of them queue up to be counted)
+      if (low == -INFINITY && *reinterpret_cast<const volatile uint32_t*>(&sh.fill[lp]) > kSmList) return;
 #pragma unroll
       for (int e = 0; e < kVec; ++e)
         if (x[e] >= low && x[e] > -INFINITY) s.offer(lp, x[e], idx + e);
