@@ -103,6 +103,8 @@ struct SampleShared {
 };
 
 // --------------------------------------------------------------- clusters
+// The aligned barriers here and in sorted() want a warp's lanes together, and single lanes' work
+// often comes just before them: __syncwarp says so to the compiler.
 template <typename T>
 __device__ __forceinline__ T peer_load(const T* local, uint32_t rank) {
   static_assert(sizeof(T) == 4 || sizeof(T) == 8, "");
@@ -123,14 +125,17 @@ __device__ __forceinline__ void blocks_sync(uint32_t blocks) {
     __syncthreads();
     return;
   }
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // A block must not end while another may read it: it arrives once it has read the
 // others, and waits before it ends.
 __device__ __forceinline__ void blocks_leave(uint32_t blocks) {
+  __syncwarp();
   if (blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void blocks_left(uint32_t blocks) {
+  __syncwarp();
   if (blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
@@ -584,6 +589,7 @@ struct Sampler {
     unsigned long long *a = sh.sort[0], *b = sh.sort[1];
     for (uint32_t run = 32; run < size; run <<= 1) {
       a[t] = v;
+      __syncwarp();
       named_bar_sync(1, size);
       // (empty places are zeros: of equal ones the first run's come first)
       const bool second = (t & run) != 0;
@@ -597,6 +603,7 @@ struct Sampler {
       }
       const uint32_t to = (t & ~(2 * run - 1)) + (t & (run - 1)) + lo;
       b[to] = v;
+      __syncwarp();
       named_bar_sync(1, size);
       v = b[t];
     }
@@ -1258,14 +1265,12 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     before = all.sum_before;
     sum = all.sum;
   }
-  __syncwarp();
   blocks_leave(blocks);
   if (threadIdx.x == 0) sh.at_index = -1;
   __syncthreads();
   s.locate(mine, before, greedy ? 1ull : drawn(sum), term);
   __syncthreads();
   if (threadIdx.x == 0 && sh.at_index >= 0) answer(sh.at_index, sh.at_x, sh.at_sum, sum);   // (one block has it)
-  __syncwarp();
   blocks_left(blocks);
 }
 
