@@ -32,10 +32,10 @@
 #include <cmath>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <mutex>
 
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
+#include "kept_answers.h"
 #include "sm100_ptx.cuh"
 
 namespace dsa {
@@ -1299,18 +1299,15 @@ struct SampleConfig {
 // takes an SM, whatever the shared memory.)
 template <int TYPE>
 int sample_clusters(int blocks) {
-  static std::mutex mu;
-  static int cached[64][9] = {};                  // and 1; 0: not asked yet
+  static KeptAnswers<64 * 9> kept;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  if (cached[dev][blocks]) return cached[dev][blocks] - 1;
-  const SampleConfig c(1, blocks, kSmMaxData, nullptr);
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, sample_kernel<TYPE>, &c.cfg) != cudaSuccess) n = 0;
-  cudaGetLastError();
-  cached[dev][blocks] = n + 1;
-  return n;
+  return kept.get(dev * 9 + blocks, [&](int* n) {
+    const SampleConfig c(1, blocks, kSmMaxData, nullptr);
+    if (cudaOccupancyMaxActiveClusters(n, sample_kernel<TYPE>, &c.cfg) == cudaSuccess) return true;
+    cudaGetLastError();                           // (this query's own)
+    return false;
+  });
 }
 
 template <int TYPE>
