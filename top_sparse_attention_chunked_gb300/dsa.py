@@ -881,12 +881,26 @@ def _token_rows(dev: int, t, name: str, dtype, tokens: int, heads: int):
     return t.data_ptr(), st[0]
 
 
+def _positions(dev: int, t, axes: int, tokens: int):
+    """(address, elements from axis to axis) of positions [axes, tokens], the axes
+    any stride apart (0: one row for all), or [tokens] for all axes."""
+    if t is None:
+        return None, 0
+    shape, st = t.shape, t.stride()
+    one = len(shape) == 1
+    if t.dtype is not torch.int32 or t.get_device() != dev or shape != ((tokens,) if one else (axes, tokens)):
+        _refuse(dev, t, "positions", torch.int32, (tokens,) if one else (axes, tokens))
+    if st[-1] != 1 and tokens > 1:
+        raise ValueError(f"positions of an axis must be contiguous, got strides {st}")
+    return t.data_ptr(), 0 if one or axes == 1 else st[0]
+
+
 def dsa_rope_axes_append(p: DsaAxesProblem, q, k, v, gamma_q, gamma_k, cos, sin, positions, slots, q_out, k_cache, v_cache,
                          k_scale=None, v_scale=None, stream=None):
     """RMSNorm (gamma_q, gamma_k; None: none) and rotary positions with several axes:
     q to q_out (or q itself), k and v into the caches [cache_rows, Hkv, 128] at
-    slots [N]. q, k and v may be columns of one projection. positions [axes, N], or
-    [N] where all axes have the same."""
+    slots [N]. q, k and v may be columns of one projection. positions [axes, N], the
+    axes any stride apart, or [N] where all axes have the same."""
     lib, dev, n, hkv = load_library(), _current_device(), p.tokens, p.num_kv_heads
     p = DsaAxesProblem.from_buffer_copy(p)             # (the strides are this call's)
     qdt, kvdt, f32, i32 = _TORCH_DT[p.q_dtype], _TORCH_DT[p.kv_dtype], torch.float32, torch.int32
@@ -894,17 +908,14 @@ def dsa_rope_axes_append(p: DsaAxesProblem, q, k, v, gamma_q, gamma_k, cos, sin,
     kp, p.k_stride = _token_rows(dev, k, "k", qdt, n, hkv)
     vp, p.v_stride = _token_rows(dev, v, "v", qdt, n, hkv)
     op, p.out_stride = _token_rows(dev, q_out, "q_out", qdt, n, p.num_q_heads)
-    if positions.dim() == 1:
-        p.pos_stride, shape = 0, (n,)
-    else:
-        p.pos_stride, shape = n, (p.axes, n)
+    pp, p.pos_stride = _positions(dev, positions, p.axes, n)
     half = sum(p.sections[:])          # (those behind the last axis are 0)
     cache, angles, cdt = (p.cache_rows, hkv, 128), (p.max_pos, half), _TORCH_DT[p.cos_dtype]
     a = _here(dev, (gamma_q, "gamma_q", f32, (128,)), (gamma_k, "gamma_k", f32, (128,)), (cos, "cos", cdt, angles),
-              (sin, "sin", cdt, angles), (positions, "positions", i32, shape), (slots, "slots", i32, (n,)),
+              (sin, "sin", cdt, angles), (slots, "slots", i32, (n,)),
               (k_cache, "k_cache", kvdt, cache), (v_cache, "v_cache", kvdt, cache),
               (k_scale, "k_scale", f32, cache[:2]), (v_scale, "v_scale", f32, cache[:2]))
-    _check(lib.dsa_rope_axes_append(ctypes.byref(p), qp, kp, vp, *a[:6], op, *a[6:], _stream_here(dev, stream)))
+    _check(lib.dsa_rope_axes_append(ctypes.byref(p), qp, kp, vp, *a[:4], pp, a[4], op, *a[5:], _stream_here(dev, stream)))
 
 
 def make_norm_problem(rows: int, hidden: int, x_dtype="bf16", y_dtype="bf16", eps: float = 1e-6,
