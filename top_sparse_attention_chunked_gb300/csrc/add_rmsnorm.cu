@@ -111,10 +111,16 @@ __device__ __forceinline__ float row_reduce(float v, int warps, float (*part)[kN
   return v;
 }
 
+// Blocks an SM that the compiler is held to (0: it chooses). FP32 rows by single elements in blocks
+// of 1,024 hold 32 elements of x, the residual and the sum each: left to itself it takes 32
+// registers a thread, for two blocks an SM, and 1,360 bytes of the stack; with the 64 that one
+// block may have 424 (4,000 x 32,767 1,061 -> 689 us, 4,000 x 20,001 636 -> 524).
+constexpr int norm_blocks(bool f32, bool vec, int steps, int threads) { return f32 && !vec && steps == 8 && threads == 1024; }
+
 // VEC: rows of aligned 8-element vectors; a thread's step is one of them. Else a
 // warp's step is 128 elements, a lane's every 32nd of these.
 template <bool F32, bool VEC, int STEPS, int THREADS>
-__global__ void __launch_bounds__(THREADS) add_rmsnorm_kernel(const __grid_constant__ NormParams p, int warps) {
+__global__ void __launch_bounds__(THREADS, norm_blocks(F32, VEC, STEPS, THREADS)) add_rmsnorm_kernel(const __grid_constant__ NormParams p, int warps) {
   constexpr int E = VEC ? 8 : 4;
   __shared__ float s_part[2][kNormMaxWarps];
   const int lane = threadIdx.x & 31;
@@ -300,7 +306,8 @@ cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t st) {
   const char* name = "add_rmsnorm_kernel";
   if (steps == S0) return launch_kernel(name, add_rmsnorm_kernel<F32, VEC, S0, 1024>, grid, dim3(threads), 0, st, false, p, warps);
   if (steps == S1) return launch_kernel(name, add_rmsnorm_kernel<F32, VEC, S1, 1024>, grid, dim3(threads), 0, st, false, p, warps);
-  // (32 elements a thread in 64 registers spill)
+  // (32 elements a thread: up to 128 registers, which 512 threads may have; 1,024 have 64, which spill
+  // 4 bytes of 16-bit rows of vectors, 68 of FP32, and 44 and 424 of rows by single elements)
   if (threads <= 512) return launch_kernel(name, add_rmsnorm_kernel<F32, VEC, S2, 512>, grid, dim3(threads), 0, st, false, p, warps);
   return launch_kernel(name, add_rmsnorm_kernel<F32, VEC, S2, 1024>, grid, dim3(threads), 0, st, false, p, warps);
 }
