@@ -28,3 +28,9 @@ def test_positions_that_are_refused(lib):  # noqa: F811
                 torch.zeros(1, 2, 3, dtype=torch.int32)):
         with pytest.raises(ValueError, match="positions"):
             D.dsa_rope_axes_append(p, *axes_args(pos=pos))
+
+
+def test_the_package_offers_the_serving_calls():
+    import top_sparse_attention_chunked_gb300 as pkg
+    for name in ("dsa_full_attn", "dsa_slot_map", "dsa_rope_axes_append", "dsa_add_rmsnorm", "dsa_sample", "dsa_beam_select", "dsa_pages_update"):
+        assert getattr(pkg, name) is getattr(D, name)
