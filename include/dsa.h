@@ -570,7 +570,8 @@ int dsa_full_attn_paged(const dsa_full_problem* p, const dsa_kv_pages* pages, co
  *   sinks     >= 0
  *   pages     the paged pools' description, or NULL for dense caches
  * The workspace is dsa_full_attn's: dsa_full_attn_workspace_size(p) is enough
- * for any number of sinks.
+ * for any number of sinks (it is that of p without its window; a call takes
+ * any workspace that holds its own parts).
  */
 int dsa_full_attn_sinks(const dsa_full_problem* p, int sinks, const dsa_kv_pages* pages, const void* q,
                         const void* k, const void* v, const float* k_scale, const float* v_scale,

@@ -351,8 +351,8 @@ extern "C" int dsa_add_rmsnorm(const dsa_norm_problem* np, const void* x, const 
   const auto off = [](const void* q, uintptr_t a) { return (reinterpret_cast<uintptr_t>(q) & (a - 1)) != 0; };
   if (off(x, xb) || off(residual, xb) || off(h, xb) || off(y, yb) || off(gamma, 4) || off(scale, 4))
     return report_error(DSA_ERR_MISALIGNED, "tensors must be aligned to their elements");
-  // A row is read before it is written, so h may be x or the residual, and y x, the
-  // residual or h's row in the same place; any other overlap is refused.
+  // A row is read before it is written, so h may be x or the residual, and y the one or the
+  // other, in the same place; any other overlap is refused, y's with h too.
   struct Span {
     const void* at;
     long long pitch, bytes;

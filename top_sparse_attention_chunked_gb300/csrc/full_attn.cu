@@ -41,10 +41,11 @@
 // First keys that stay visible beside a window (SINKS): an item's tiles are those of the
 // first keys and those of its window, and the axis that is cut into runs has no others, so
 // a call costs what it reads. Measured: 16 sequences of one token on up to 32,768 keys, a
-// window of 4,096 and 4 first keys, 24/2 heads FP16: 24.4 us (66 MB, 2.7 TB/s: 8 tiles a
+// window of 4,096 and 4 first keys, 24/2 heads FP16: 24.4 us (66 MB, 2.7 TB/s: 7 tiles a
 // block after some 8 us of launches and first tile, and the merge); chunks of 4,096 and
 // 3,395 tokens, window 2,048 and 64 first keys, 16/4 heads: 159 us (820 TFLOP/s of what is
-// visible; tiles at both edges of the window are half masked); 8 tokens on 262,144 INT8
+// visible: a window's edges leave one or two of an item's 18 or 19 tiles half masked, and an item's
+// beginning takes as long as five, kCostItem); 8 tokens on 262,144 INT8
 // keys, window 32,768 and 1,000 first keys: 25.5 us.
 //
 // The running maximum m is raised (and O rescaled in tensor memory) only when

@@ -22,12 +22,15 @@
 // pass that forms the exact sum of what lies before them and lists their tokens does the
 // rest (if they are too many for a list, they are counted again, by smaller bins).
 //
-// What bounds it: not memory (64 rows of 131,072 in bf16 are 2.5 us of reads), but the
-// instructions of the passes that form weights, about 30 a token and half of them on the
-// half-rate integer pipe, and for single rows the exchanges, each a microsecond. Measured
-// (64 x 131,072 bf16): temperature alone 21.6 us, min-p 22.7, top-k 24.6, top-p 60.4 (two
-// passes that form weights and one that counts in shared memory), a mix of them 57.9;
-// 256 x 32,000 mixed 48; 1 x 131,072 12.3 / 14.7 / 26.6 (temperature, top-k, top-p).
+// What bounds it: not memory (64 rows of 131,072 in bf16 are 2.5 us of reads). About half is issue
+// slots (top-p: 34 million warp instructions on 128 SMs, 32 us of 60 at 2.07 GHz; 30 a token in
+// the passes that form weights), the rest waiting: one block of 1,024 threads an SM, whose
+// barriers between passes nothing else runs under, atomics in shared memory, exchanges in the
+// cluster, a microsecond each, and 24 of the 152 SMs idle with two blocks for each of 64 rows.
+// Schedulers are busy 42 to 67% of the time, the half-rate integer pipe 23 to 37%. Measured
+// (64 x 131,072 bf16, replayed, L2 flushed): temperature alone 22.5 us, min-p 23.3, top-k 26.2,
+// top-p 63.5 (two passes that form weights and one that counts in shared memory), a mix of them
+// 58; 256 x 32,000 mixed 48; 1 x 131,072 12.3 / 15.7 / 38 (temperature, top-k, top-p).
 #include <algorithm>
 #include <cmath>
 #include <cuda_bf16.h>
