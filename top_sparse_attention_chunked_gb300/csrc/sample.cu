@@ -1027,7 +1027,8 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     const float2 v = sh.row_low;
     const float a = __fadd_rn(top, v.x), b = __fsub_rn(a, top);
     const float e = __fadd_rn(__fadd_rn(__fsub_rn(top, __fsub_rn(a, b)), __fsub_rn(v.x, b)), v.y);   // what a is short of
-    least = e > 0.f ? __fadd_ru(a, 1.17549435e-38f) : a;
+    // (where max and T ln min_p nearly cancel, e is many steps of a. NaN: T ln min_p is infinite)
+    least = e == e ? __fadd_ru(a, e) : a;
   }
   float u = __ldg(p.u + r);
   u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
